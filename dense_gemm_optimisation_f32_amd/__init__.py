@@ -9,25 +9,42 @@ that a wrong buffer is refused on the host instead of faulting the GPU) or raw
 integer device addresses (passed as they are).  ``stream`` may be None (torch's
 current stream), a ``torch.cuda.Stream`` or a raw ``hipStream_t`` integer.
 
+The functions at the end (routing, grouped products, combining, adapters) run on
+the device their tensors are on, refuse tensors of more than one device, and
+where they need a workspace take ``workspace=`` or let torch allocate it.
+
 If the library is not built, importing works but every call raises
 ``GemmLibraryMissing``: there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
 __all__ = ["gemm_f32", "gemm_f16_f32acc", "gemm_batched_f16_f32acc",
            "gemm_f32_ex", "gemm_f16_f32acc_ex", "gemm_batched_f16_f32acc_ex",
            "gemm_bf16_f32acc", "gemm_batched_bf16_f32acc", "gemm_bf16_f32acc_ex", "gemm_batched_bf16_f32acc_ex",
-           "gemm_f16_f32acc_noalloc", "status_string",
+           "gemm_f16_f32acc_noalloc",
+           "moe_route_f32", "moe_route_workspace", "moe_route_f32_grad",
+           "gemm_grouped_f16_f32acc_ex", "gemm_grouped_bf16_f32acc_ex",
+           "gemm_grouped_wgrad_f16_f32acc", "gemm_grouped_wgrad_bf16_f32acc",
+           "moe_combine_f32", "moe_combine_grad_f16", "moe_combine_grad_bf16",
+           "gemm_lora_f16_f32acc_ex", "gemm_lora_bf16_f32acc_ex", "gemm_lora_workspace",
+           "status_string",
            "GemmError", "GemmLibraryMissing", "LIB_PATH", "load_library", "EXPORTS"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmi355gemm.so")
 EXPORTS = ("gemm_f32", "gemm_f16_f32acc", "gemm_batched_f16_f32acc",
            "gemm_f32_ex", "gemm_f16_f32acc_ex", "gemm_batched_f16_f32acc_ex",
            "gemm_bf16_f32acc", "gemm_batched_bf16_f32acc", "gemm_bf16_f32acc_ex", "gemm_batched_bf16_f32acc_ex",
-           "gemm_f16_f32acc_noalloc", "gemm_status_string")
+           "gemm_f16_f32acc_noalloc",
+           "moe_route_f32", "moe_route_workspace", "moe_route_f32_grad",
+           "gemm_grouped_f16_f32acc_ex", "gemm_grouped_bf16_f32acc_ex",
+           "gemm_grouped_wgrad_f16_f32acc", "gemm_grouped_wgrad_bf16_f32acc",
+           "moe_combine_f32", "moe_combine_grad_f16", "moe_combine_grad_bf16",
+           "gemm_lora_f16_f32acc_ex", "gemm_lora_bf16_f32acc_ex", "gemm_lora_workspace",
+           "gemm_status_string")
 
 _lib = None
 
@@ -75,6 +92,24 @@ def load_library(path: str = LIB_PATH):
         fn.restype = i
     lib.gemm_f16_f32acc_noalloc.argtypes = lib.gemm_f16_f32acc.argtypes
     lib.gemm_f16_f32acc_noalloc.restype = i
+    lib.moe_route_f32.argtypes = [i, i, vp, i, vp, i, i, i, i, i, i, f, vp, vp, vp, vp, vp, vp, ll, vp]
+    lib.moe_route_f32_grad.argtypes = [i, i, vp, i, i, i, i, f, vp, vp, vp, i, vp]
+    lib.moe_combine_f32.argtypes = [i, i, i, vp, i, i, vp, vp, f, vp, i, vp]
+    for t in ("f16", "bf16"):
+        getattr(lib, f"gemm_grouped_{t}_f32acc_ex").argtypes = [i, i, i, i, i, f, vp, i, i, vp, vp, i, ll, vp, f, vp, i, vp]
+        getattr(lib, f"gemm_grouped_wgrad_{t}_f32acc").argtypes = [i, i, i, i, f, vp, i, i, vp, vp, i, i, vp, vp, f, vp, i,
+                                                                   ll, vp]
+        getattr(lib, f"moe_combine_grad_{t}").argtypes = [i, i, i, vp, i, vp, i, i, vp, vp, vp, i, vp, vp]
+        getattr(lib, f"gemm_lora_{t}_f32acc_ex").argtypes = [i, i, i, i, i, i, f, vp, i, vp, i, vp, i, ll, vp, i, ll, vp, vp,
+                                                             vp, f, vp, i, vp, ll, vp]
+    for name in ("moe_route_f32", "moe_route_f32_grad", "moe_combine_f32", "gemm_grouped_f16_f32acc_ex",
+                 "gemm_grouped_bf16_f32acc_ex", "gemm_grouped_wgrad_f16_f32acc", "gemm_grouped_wgrad_bf16_f32acc",
+                 "moe_combine_grad_f16", "moe_combine_grad_bf16", "gemm_lora_f16_f32acc_ex", "gemm_lora_bf16_f32acc_ex"):
+        getattr(lib, name).restype = i
+    lib.moe_route_workspace.argtypes = [i, i, i]
+    lib.moe_route_workspace.restype = ll
+    lib.gemm_lora_workspace.argtypes = [i, i, i, i]
+    lib.gemm_lora_workspace.restype = ll
     lib.gemm_status_string.argtypes = [i]
     lib.gemm_status_string.restype = ctypes.c_char_p
     if path == LIB_PATH:
@@ -267,3 +302,189 @@ def gemm_batched_bf16_f32acc_ex(transA, transB, M, N, K, alpha, A, lda, strideA,
                                          _stream(stream))
     if rc != 0:
         raise GemmError(rc, "gemm_batched_bf16_f32acc_ex")
+
+
+# ------------------------------------------------------------------ products whose right operand is chosen per row
+def _packed(x, name: str, dtype_name: str, need: int):
+    """Device address of an array the kernels read or write without strides."""
+    if _is_tensor(x) and x.device.type == "cuda" and not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return _ptr(x, name, dtype_name, need)
+
+
+def _call(name: str, args, operands, stream, workspace=None, workspace_bytes=None) -> None:
+    """Run library function ``name`` on the device that holds ``operands`` (one for all of them): on ``stream``, or on
+    that device's current stream.  With ``workspace_bytes`` the call takes a workspace: the caller's, or one that torch's
+    allocator hands out for that stream (graph capture included) and takes back in its order."""
+    fn = getattr(load_library(), name)
+    devices = {x.device for x in operands if _is_tensor(x)}
+    if len(devices) > 1:
+        raise ValueError(f"{name}: operands on more than one device: {sorted(map(str, devices))}")
+    if not devices and stream is not None and not workspace_bytes:
+        rc = fn(*args, *(() if workspace_bytes is None else (None, 0)), _stream(stream))
+    else:
+        import torch
+
+        here = torch.cuda.current_device()
+        dev = devices.pop().index if devices else here
+        with contextlib.nullcontext() if dev == here else torch.cuda.device(dev):
+            h = _stream(stream)
+            if workspace_bytes is None:
+                rc = fn(*args, h)
+            else:
+                if workspace is None and workspace_bytes > 0:
+                    with contextlib.nullcontext() if stream is None else torch.cuda.stream(torch.cuda.ExternalStream(h)):
+                        workspace = torch.empty(workspace_bytes, dtype=torch.uint8, device="cuda")
+                rc = fn(*args, _ptr(workspace, "workspace", None, 0), _room(workspace, workspace_bytes), h)
+    if rc != 0:
+        raise GemmError(rc, name)
+
+
+def _room(workspace, need: int) -> int:
+    """Bytes the library may use: what a tensor's storage holds from its start, or for a raw address what the call needs."""
+    if not _is_tensor(workspace):
+        return need
+    st = workspace.untyped_storage()
+    return st.nbytes() - (workspace.data_ptr() - st.data_ptr())
+
+
+def moe_route_workspace(T, E, k) -> int:
+    """Bytes of workspace moe_route_f32 needs for its sorted choices (0: none)."""
+    return load_library().moe_route_workspace(T, E, k)
+
+
+def moe_route_f32(T, E, logits, ldl, bias, score, groups, group_k, group_top, k, renorm, scale, ids, weights, offsets=None,
+                  rows=None, slots=None, workspace=None, stream=None) -> None:
+    """Each of T tokens chooses k of E experts (ids, weights), and the choices sorted by expert (offsets, rows, slots)."""
+    n = max(T, 0) * max(k, 0)
+    args = (T, E, _ptr(logits, "logits", "torch.float32", _extent(T, E, ldl)), ldl, _packed(bias, "bias", "torch.float32", E),
+            int(score), groups, group_k, group_top, k, int(renorm), scale, _packed(ids, "ids", "torch.int32", n),
+            _packed(weights, "weights", "torch.float32", n), _packed(offsets, "offsets", "torch.int32", E + 1),
+            _packed(rows, "rows", "torch.int32", n), _packed(slots, "slots", "torch.int32", n))
+    need = moe_route_workspace(T, E, k) if offsets is not None else 0
+    _call("moe_route_f32", args, (logits, bias, ids, weights, offsets, rows, slots, workspace), stream, workspace, need)
+
+
+def moe_route_f32_grad(T, E, logits, ldl, score, k, renorm, scale, ids, dweights, dlogits, lddl, stream=None) -> None:
+    """dlogits from dweights: the gradient of moe_route_f32's weights in its logits."""
+    n = max(T, 0) * max(k, 0)
+    args = (T, E, _ptr(logits, "logits", "torch.float32", _extent(T, E, ldl)), ldl, int(score), k, int(renorm), scale,
+            _packed(ids, "ids", "torch.int32", n), _packed(dweights, "dweights", "torch.float32", n),
+            _ptr(dlogits, "dlogits", "torch.float32", _extent(T, E, lddl)), lddl)
+    _call("moe_route_f32_grad", args, (logits, ids, dweights, dlogits), stream)
+
+
+def _grouped(t, dtype_name, transB, groups, R, N, K, alpha, A, M, lda, rows, B, ldb, strideB, offsets, beta, C, ldc, stream):
+    tB = int(transB)
+    work = groups > 0 and R > 0 and N > 0
+    reads = work and K > 0 and alpha != 0 and M > 0
+    b = _extent(*((N, K) if tB else (K, N)), ldb) + max(groups - 1, 0) * strideB
+    args = (tB, groups, R, N, K, alpha, _ptr(A, "A", dtype_name, _extent(M, K, lda) if reads else 0), M, lda,
+            _packed(rows, "rows", "torch.int32", R if reads else 0), _ptr(B, "B", dtype_name, b if reads else 0), ldb, strideB,
+            _packed(offsets, "offsets", "torch.int32", groups + 1 if work else 0), beta,
+            _ptr(C, "C", "torch.float32", _extent(R, N, ldc)), ldc)
+    _call(f"gemm_grouped_{t}_f32acc_ex", args, (A, rows, B, offsets, C), stream)
+
+
+def gemm_grouped_f16_f32acc_ex(transB, groups, R, N, K, alpha, A, M, lda, rows, B, ldb, strideB, offsets, beta, C, ldc,
+                               stream=None) -> None:
+    """C[r,:] <- alpha*A[rows[r],:]*op(B_g) + beta*C[r,:] for the rows r of every group g; fp16 A and B, fp32 C."""
+    _grouped("f16", "torch.float16", transB, groups, R, N, K, alpha, A, M, lda, rows, B, ldb, strideB, offsets, beta, C, ldc,
+             stream)
+
+
+def gemm_grouped_bf16_f32acc_ex(transB, groups, R, N, K, alpha, A, M, lda, rows, B, ldb, strideB, offsets, beta, C, ldc,
+                                stream=None) -> None:
+    """gemm_grouped_f16_f32acc_ex with bf16 A and B."""
+    _grouped("bf16", "torch.bfloat16", transB, groups, R, N, K, alpha, A, M, lda, rows, B, ldb, strideB, offsets, beta, C, ldc,
+             stream)
+
+
+def _wgrad(t, dtype_name, groups, R, M, N, alpha, A, a_rows, lda, rowsA, B, b_rows, ldb, rowsB, offsets, beta, C, ldc, strideC,
+           stream):
+    work = groups > 0 and M > 0 and N > 0
+    reads = work and R > 0 and alpha != 0 and a_rows > 0 and b_rows > 0
+    args = (groups, R, M, N, alpha, _ptr(A, "A", dtype_name, _extent(a_rows, M, lda) if reads else 0), a_rows, lda,
+            _packed(rowsA, "rowsA", "torch.int32", R if reads else 0),
+            _ptr(B, "B", dtype_name, _extent(b_rows, N, ldb) if reads else 0), b_rows, ldb,
+            _packed(rowsB, "rowsB", "torch.int32", R if reads else 0),
+            _packed(offsets, "offsets", "torch.int32", groups + 1 if reads else 0), beta,
+            _ptr(C, "C", "torch.float32", _extent(M, N, ldc) + (groups - 1) * strideC if work else 0), ldc, strideC)
+    _call(f"gemm_grouped_wgrad_{t}_f32acc", args, (A, rowsA, B, rowsB, offsets, C), stream)
+
+
+def gemm_grouped_wgrad_f16_f32acc(groups, R, M, N, alpha, A, a_rows, lda, rowsA, B, b_rows, ldb, rowsB, offsets, beta, C, ldc,
+                                  strideC, stream=None) -> None:
+    """C_g <- alpha * sum over group g's rows r of A[rowsA[r],:]^T B[rowsB[r],:] + beta*C_g; fp16 A and B, fp32 C."""
+    _wgrad("f16", "torch.float16", groups, R, M, N, alpha, A, a_rows, lda, rowsA, B, b_rows, ldb, rowsB, offsets, beta, C, ldc,
+           strideC, stream)
+
+
+def gemm_grouped_wgrad_bf16_f32acc(groups, R, M, N, alpha, A, a_rows, lda, rowsA, B, b_rows, ldb, rowsB, offsets, beta, C, ldc,
+                                   strideC, stream=None) -> None:
+    """gemm_grouped_wgrad_f16_f32acc with bf16 A and B."""
+    _wgrad("bf16", "torch.bfloat16", groups, R, M, N, alpha, A, a_rows, lda, rowsA, B, b_rows, ldb, rowsB, offsets, beta, C, ldc,
+           strideC, stream)
+
+
+def moe_combine_f32(T, k, N, Y, R, ldy, slots, weights, beta, C, ldc, stream=None) -> None:
+    """C[t,:] <- sum_j weights[t,j]*Y[slots[t,j],:] + beta*C[t,:] (weights None: ones)."""
+    n = max(T, 0) * max(k, 0) if N > 0 else 0
+    args = (T, k, N, _ptr(Y, "Y", "torch.float32", _extent(R, N, ldy) if n else 0), R, ldy,
+            _packed(slots, "slots", "torch.int32", n), _packed(weights, "weights", "torch.float32", n), beta,
+            _ptr(C, "C", "torch.float32", _extent(T, N, ldc)), ldc)
+    _call("moe_combine_f32", args, (Y, slots, weights, C), stream)
+
+
+def _combine_grad(t, dtype_name, T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream):
+    n = max(T, 0) * max(k, 0)
+    args = (T, k, N, _ptr(dC, "dC", "torch.float32", _extent(T, N, lddc)), lddc,
+            _ptr(Y, "Y", "torch.float32", _extent(R, N, ldy) if n else 0), R, ldy, _packed(slots, "slots", "torch.int32", n),
+            _packed(weights, "weights", "torch.float32", n), _ptr(dY, "dY", dtype_name, _extent(R, N, lddy) if n else 0), lddy,
+            _packed(dweights, "dweights", "torch.float32", n))
+    _call(f"moe_combine_grad_{t}", args, (dC, Y, slots, weights, dY, dweights), stream)
+
+
+def moe_combine_grad_f16(T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream=None) -> None:
+    """The gradient of moe_combine_f32: dY in fp16 (what the grouped products take) and dweights in fp32."""
+    _combine_grad("f16", "torch.float16", T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream)
+
+
+def moe_combine_grad_bf16(T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream=None) -> None:
+    """moe_combine_grad_f16 with dY in bf16."""
+    _combine_grad("bf16", "torch.bfloat16", T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream)
+
+
+def gemm_lora_workspace(M, N, K, rank) -> int:
+    """Bytes of workspace gemm_lora_f16_f32acc_ex and its bf16 form need."""
+    return load_library().gemm_lora_workspace(M, N, K, rank)
+
+
+def _lora(t, dtype_name, transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb, LA, ldla, strideLA, LB, ldlb, strideLB, scales,
+          ranks, ids, beta, C, ldc, workspace, stream):
+    tB = int(transB)
+    na, nb, nc = _needs(M, N, K, alpha, lda, ldb, ldc, transB=tB)
+    thin = na > 0 and adapters > 0
+    last = max(adapters - 1, 0)
+    args = (tB, M, N, K, rank, adapters, alpha, _ptr(A, "A", dtype_name, na), lda, _ptr(B, "B", dtype_name, nb), ldb,
+            _ptr(LA, "LA", dtype_name, _extent(rank, K, ldla) + last * strideLA if thin else 0), ldla, strideLA,
+            _ptr(LB, "LB", dtype_name, _extent(N, rank, ldlb) + last * strideLB if thin else 0), ldlb, strideLB,
+            _packed(scales, "scales", "torch.float32", adapters if thin else 0),
+            _packed(ranks, "ranks", "torch.int32", adapters if thin else 0),
+            _packed(ids, "ids", "torch.int32", M if thin else 0), beta, _ptr(C, "C", "torch.float32", nc), ldc)
+    need = gemm_lora_workspace(M, N, K, rank) if thin else 0
+    _call(f"gemm_lora_{t}_f32acc_ex", args, (A, B, LA, LB, scales, ranks, ids, C, workspace), stream, workspace, need)
+
+
+def gemm_lora_f16_f32acc_ex(transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb, LA, ldla, strideLA, LB, ldlb, strideLB, scales,
+                            ranks, ids, beta, C, ldc, workspace=None, stream=None) -> None:
+    """C[i,:] <- alpha*(A[i,:]*op(B) + scales[a]*(A[i,:]*LA_a^T)*LB_a^T) + beta*C[i,:], a = ids[i]; fp16 inputs, fp32 C."""
+    _lora("f16", "torch.float16", transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb, LA, ldla, strideLA, LB, ldlb, strideLB,
+          scales, ranks, ids, beta, C, ldc, workspace, stream)
+
+
+def gemm_lora_bf16_f32acc_ex(transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb, LA, ldla, strideLA, LB, ldlb, strideLB,
+                             scales, ranks, ids, beta, C, ldc, workspace=None, stream=None) -> None:
+    """gemm_lora_f16_f32acc_ex with bf16 inputs."""
+    _lora("bf16", "torch.bfloat16", transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb, LA, ldla, strideLA, LB, ldlb, strideLB,
+          scales, ranks, ids, beta, C, ldc, workspace, stream)

@@ -294,13 +294,13 @@ const char *gemm_status_string(int status)
 {
     switch (status) {
     case GEMM_OK: return "success";
-    case GEMM_ERR_SIZE: return "invalid size: M, N, K or batch_count negative, or an extent overflows";
+    case GEMM_ERR_SIZE: return "invalid size: negative, outside the range the call documents, or an extent overflows";
     case GEMM_ERR_LD: return "invalid leading dimension or batch stride";
     case GEMM_ERR_NULL: return "NULL pointer for an operand the call reads or writes";
     case GEMM_ERR_ALIGN: return "pointer not aligned to its element size";
     case GEMM_ERR_LAUNCH: return "the HIP runtime refused a kernel launch";
-    case GEMM_ERR_OP: return "transpose flag is neither 0 nor 1";
-    case GEMM_ERR_SCRATCH: return "the call needs more scratch than the static buffer of the no-allocation entry point holds";
+    case GEMM_ERR_OP: return "a flag is neither 0 nor 1";
+    case GEMM_ERR_SCRATCH: return "the call needs more scratch than its workspace, or the static buffer of the no-allocation entry point, holds";
     default: return "unknown status";
     }
 }

@@ -1,7 +1,9 @@
 /*
  * mi355gemm.h -- row-major GEMM on one AMD Instinct MI355X (gfx950), C ABI.
  *
- * Every entry point computes, for row-major matrices,
+ * Every gemm_f32*, gemm_f16*, gemm_bf16* and gemm_batched_* entry point computes,
+ * for row-major matrices (the calls whose right operand is chosen per row stand
+ * at the end, with their own formulas),
  *
  *     C <- alpha * A * B + beta * C,      A: M x K,  B: K x N,  C: M x N
  *
@@ -53,7 +55,8 @@ typedef struct ihipStream_t *hipStream_t; /* the HIP runtime's stream handle */
 enum {
     GEMM_OK = 0,
     GEMM_ERR_SIZE = -1,      /* M, N, K or batch_count negative, an extent overflows 64 bits, or
-                                ceil(M/32)*ceil(N/32) exceeds INT_MAX (one launch's grid) */
+                                ceil(M/32)*ceil(N/32) exceeds INT_MAX (one launch's grid); for the
+                                calls by row, also a size outside the range the call documents */
     GEMM_ERR_LD = -2,        /* lda < max(1,K), ldb < max(1,N) (with transA: lda < max(1,M); with
                                 transB: ldb < max(1,K)), ldc < max(1,N), negative stride, or
                                 strideC smaller than one C member when batch_count > 1 */
@@ -61,8 +64,9 @@ enum {
     GEMM_ERR_LAUNCH = -4,    /* the HIP runtime refused a kernel launch (hipGetLastError) */
     GEMM_ERR_ALIGN = -5,     /* pointer not aligned to its element size */
     GEMM_ERR_OP = -6,        /* transA or transB is neither 0 nor 1 */
-    GEMM_ERR_SCRATCH = -7    /* gemm_f16_f32acc_noalloc only: the call needs more scratch than
-                                the library's static buffer holds */
+    GEMM_ERR_SCRATCH = -7    /* gemm_f16_f32acc_noalloc: the call needs more scratch than the
+                                library's static buffer holds; calls that take a workspace: it is
+                                smaller than the call needs */
 };
 
 /*
@@ -178,6 +182,156 @@ int gemm_batched_bf16_f32acc_ex(int transA, int transB, int M, int N, int K, flo
 int gemm_f16_f32acc_noalloc(int M, int N, int K, float alpha,
                             const uint16_t *A, int lda, const uint16_t *B, int ldb,
                             float beta, float *C, int ldc, hipStream_t stream);
+
+/*
+ * Products whose right operand is chosen per row: routing tokens to experts,
+ * the experts' products over the sorted rows, the weighted sum back to tokens,
+ * and low-rank adapters beside a shared projection.
+ *
+ * Index arrays (int32) and offsets are device memory and are read by the
+ * kernels only; a value that would lead outside an operand is never followed
+ * (what happens instead stands with each call), so that they can come straight
+ * from other kernels and be captured into a graph.  All matrices are row-major
+ * with caller-chosen leading dimensions; C does not overlap another operand.
+ * Calls that need scratch take it from the caller (`workspace`, at least
+ * `workspace_bytes` = what the *_workspace function returns for the same sizes,
+ * 16-byte aligned; contents before and after are of no account).  Two calls that
+ * can overlap, replays of two captured graphs among them, need two workspaces.
+ * Results are bit-identical from call to call for the same arguments.
+ */
+
+/*
+ * moe_route_f32 -- each of T tokens chooses k of E experts.
+ *   logits         : fp32, T x E, ldl >= E.
+ *   score          : 0: s = softmax over the token's E logits; 1: s = sigmoid(logit).
+ *   bias           : E fp32 values or NULL.  c = s + bias ranks the experts; the
+ *                    weights are made of s.
+ *   groups, group_k, group_top: experts g*E/groups .. form group g.  A group's score
+ *                    is the sum of its best group_top (1 or 2) available c; only the
+ *                    group_k best groups' experts can be chosen.  groups = 1: no groups.
+ *   renorm, scale  : weight_j = scale * s_j, or with renorm = 1
+ *                    scale * s_j / (sum of the token's chosen s); 0 where that sum is 0.
+ *   ids, weights   : T x k, contiguous: the choices in descending c, of equal ones
+ *                    (and groups) the lowest index first; NaN ranks below every number.
+ * An expert is unavailable to a token whose logit for it is -inf, and to all if its
+ * bias is -inf.  Choices that find no available expert have id -1 and weight 0, so a
+ * padded token is a row of -inf.  c is formed and compared in 64 bits (with softmax
+ * or sigmoid scores, no bias and group_top 1 the logits order the experts alike).
+ * The choices sorted by expert (offsets, rows and slots; all three or all NULL):
+ *   offsets        : E + 1 values; expert e's rows are offsets[e] .. offsets[e+1]-1, in
+ *                    the order of their tokens.
+ *   rows           : T*k values: the token of each row; -1 from offsets[E] on.
+ *   slots          : T x k: the row of each choice; -1 for an unfilled one.
+ * Sizes: T <= 2^23, E <= 1024, k <= min(E, 32), groups <= 64 and a divisor of E.
+ * The workspace is used for the sorted choices only.
+ */
+int moe_route_f32(int T, int E, const float *logits, int ldl, const float *bias, int score,
+                  int groups, int group_k, int group_top, int k, int renorm, float scale,
+                  int32_t *ids, float *weights, int32_t *offsets, int32_t *rows, int32_t *slots,
+                  void *workspace, long long workspace_bytes, hipStream_t stream);
+long long moe_route_workspace(int T, int E, int k);
+
+/*
+ * moe_route_f32_grad -- the gradient of moe_route_f32's weights in the logits:
+ * dlogits (T x E, lddl >= E, every entry written) from dweights (T x k) and the ids
+ * that were chosen (ids outside 0 .. E-1 get no gradient).  The choice itself and
+ * the bias have none.  logits, score, renorm and scale as for moe_route_f32.
+ */
+int moe_route_f32_grad(int T, int E, const float *logits, int ldl, int score, int k, int renorm, float scale,
+                       const int32_t *ids, const float *dweights, float *dlogits, int lddl, hipStream_t stream);
+
+/*
+ * gemm_grouped_*_f32acc_ex -- rows in groups, each group with its own right operand:
+ *     C[r,:] <- alpha * A[rows[r],:] * op(B_g) + beta * C[r,:]   for offsets[g] <= r < offsets[g+1]
+ *   R, N, K : C is R x N, op(B_g) is K x N.
+ *   A, M    : M x K, lda >= max(1,K).
+ *   rows    : R int32 indices of rows of A, or NULL for r itself; outside 0 .. M-1: a row
+ *             of zeros.
+ *   B       : groups members strideB elements apart (0: one shared), each stored K x N
+ *             (transB = 0, ldb >= max(1,N)) or N x K (transB = 1, ldb >= max(1,K)).
+ *   offsets : groups + 1 ascending int32 values; they are clamped to 0 .. R.  Rows of C in no
+ *             group are left as they are.
+ * With transB flipped this is also the gradient in A's rows.  groups <= 65535.
+ */
+int gemm_grouped_f16_f32acc_ex(int transB, int groups, int R, int N, int K, float alpha,
+                               const uint16_t *A, int M, int lda, const int32_t *rows,
+                               const uint16_t *B, int ldb, long long strideB, const int32_t *offsets,
+                               float beta, float *C, int ldc, hipStream_t stream);
+int gemm_grouped_bf16_f32acc_ex(int transB, int groups, int R, int N, int K, float alpha,
+                                const uint16_t *A, int M, int lda, const int32_t *rows,
+                                const uint16_t *B, int ldb, long long strideB, const int32_t *offsets,
+                                float beta, float *C, int ldc, hipStream_t stream);
+
+/*
+ * gemm_grouped_wgrad_*_f32acc -- the gradient in the groups' right operands:
+ *     C_g <- alpha * sum over offsets[g] <= r < offsets[g+1] of A[rowsA[r],:]^T B[rowsB[r],:] + beta * C_g
+ *   A : a_rows x M, lda >= max(1,M); B : b_rows x N, ldb >= max(1,N); rowsA, rowsB: R indices or
+ *       NULL for r; a row outside its operand adds nothing.
+ *   C : groups members M x N, strideC apart (at least (M-1)*ldc + N); an empty group's is
+ *       beta * C_g.
+ * For weights stored N x K swap the two operands.  groups <= 65535.
+ */
+int gemm_grouped_wgrad_f16_f32acc(int groups, int R, int M, int N, float alpha,
+                                  const uint16_t *A, int a_rows, int lda, const int32_t *rowsA,
+                                  const uint16_t *B, int b_rows, int ldb, const int32_t *rowsB,
+                                  const int32_t *offsets, float beta, float *C, int ldc, long long strideC,
+                                  hipStream_t stream);
+int gemm_grouped_wgrad_bf16_f32acc(int groups, int R, int M, int N, float alpha,
+                                   const uint16_t *A, int a_rows, int lda, const int32_t *rowsA,
+                                   const uint16_t *B, int b_rows, int ldb, const int32_t *rowsB,
+                                   const int32_t *offsets, float beta, float *C, int ldc, long long strideC,
+                                   hipStream_t stream);
+
+/*
+ * moe_combine_f32 -- the experts' rows back in token order:
+ *     C[t,:] <- sum_j weights[t,j] * Y[slots[t,j],:] + beta * C[t,:]
+ * in the order of j.  Y is R x N, C is T x N; slots T x k (outside 0 .. R-1: skipped, the
+ * weight is then of no account); weights T x k or NULL for ones.  T <= 2^23, k <= 32,
+ * N <= 2^25.  With NULL weights this is the gradient of a gathering grouped product's rows.
+ */
+int moe_combine_f32(int T, int k, int N, const float *Y, int R, int ldy, const int32_t *slots,
+                    const float *weights, float beta, float *C, int ldc, hipStream_t stream);
+
+/*
+ * moe_combine_grad_* -- its gradient: dY[slots[t,j],:] = weights[t,j] * dC[t,:], rounded once
+ * to the 16-bit type that the grouped products take, and dweights[t,j] = <dC[t,:], Y[slots[t,j],:]>
+ * (0 for a skipped slot).  Rows of dY that no slot names are left as they are; slots of
+ * one call are distinct (as moe_route_f32 makes them).
+ */
+int moe_combine_grad_f16(int T, int k, int N, const float *dC, int lddc, const float *Y, int R, int ldy,
+                         const int32_t *slots, const float *weights, uint16_t *dY, int lddy, float *dweights,
+                         hipStream_t stream);
+int moe_combine_grad_bf16(int T, int k, int N, const float *dC, int lddc, const float *Y, int R, int ldy,
+                          const int32_t *slots, const float *weights, uint16_t *dY, int lddy, float *dweights,
+                          hipStream_t stream);
+
+/*
+ * gemm_lora_*_f32acc_ex -- one projection for all rows and a low-rank adapter per row:
+ *     C[i,:] <- alpha * (A[i,:] op(B) + scales[a] * (A[i,:] LA_a^T) LB_a^T) + beta * C[i,:],  a = ids[i]
+ *   A, B, C, transB : as for gemm_*_f32acc_ex with transA = 0.
+ *   LA      : adapters members rank x K (ldla >= max(1,K)), strideLA apart.
+ *   LB      : adapters members N x rank (ldlb >= rank), strideLB apart.
+ *   scales  : a value per adapter, or NULL for ones.
+ *   ranks   : a rank per adapter (clamped to 0 .. rank), or NULL for rank; what LA and LB hold
+ *             past an adapter's rank is not used.
+ *   ids     : M int32 values; outside 0 .. adapters-1: no adapter for that row.
+ * The narrow product A LA^T stays in fp32 precision.  M <= 2^23, N <= 2^25, 1 <= rank <= 128.
+ */
+int gemm_lora_f16_f32acc_ex(int transB, int M, int N, int K, int rank, int adapters, float alpha,
+                            const uint16_t *A, int lda, const uint16_t *B, int ldb,
+                            const uint16_t *LA, int ldla, long long strideLA,
+                            const uint16_t *LB, int ldlb, long long strideLB,
+                            const float *scales, const int32_t *ranks, const int32_t *ids,
+                            float beta, float *C, int ldc,
+                            void *workspace, long long workspace_bytes, hipStream_t stream);
+int gemm_lora_bf16_f32acc_ex(int transB, int M, int N, int K, int rank, int adapters, float alpha,
+                             const uint16_t *A, int lda, const uint16_t *B, int ldb,
+                             const uint16_t *LA, int ldla, long long strideLA,
+                             const uint16_t *LB, int ldlb, long long strideLB,
+                             const float *scales, const int32_t *ranks, const int32_t *ids,
+                             float beta, float *C, int ldc,
+                             void *workspace, long long workspace_bytes, hipStream_t stream);
+long long gemm_lora_workspace(int M, int N, int K, int rank);
 
 /* gemm_status_string -- a static, NUL-terminated description of a status code. */
 const char *gemm_status_string(int status);

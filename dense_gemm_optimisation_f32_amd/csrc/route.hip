@@ -4,178 +4,355 @@
 #include "routed_internal.h"
 #include "epilogue.h"
 
-#include <float.h>
+#include <type_traits>
 
 namespace mi355gemm {
 namespace {
 
 // ---------------------------------------------------------------- wave helpers
-template <class T>
-__device__ __forceinline__ T wave_max(T v)
+//
+// Reductions over the 64 lanes by DPP moves (no LDS traffic): within rows of 16
+// lanes, then across rows; the whole result arrives in lane 63.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ unsigned dpp(unsigned old, unsigned v)
 {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-        const T o = __shfl_xor(v, d);
-        v = o > v ? o : v;
-    }
-    return v;
+    return (unsigned)__builtin_amdgcn_update_dpp((int)old, (int)v, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float old, float v)
+{
+    return __builtin_bit_cast(float, dpp<CTRL, ROWS>(__builtin_bit_cast(unsigned, old), __builtin_bit_cast(unsigned, v)));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double old, double v)
+{
+    const uint64_t o = __builtin_bit_cast(uint64_t, old), b = __builtin_bit_cast(uint64_t, v);
+    const uint64_t lo = dpp<CTRL, ROWS>((unsigned)o, (unsigned)b);
+    const uint64_t hi = dpp<CTRL, ROWS>((unsigned)(o >> 32), (unsigned)(b >> 32));
+    return __builtin_bit_cast(double, (hi << 32) | lo);
+}
+__device__ __forceinline__ unsigned lane_value(unsigned v, int lane)
+{
+    return (unsigned)__builtin_amdgcn_readlane((int)v, lane);
+}
+__device__ __forceinline__ float lane_value(float v, int lane)
+{
+    return __builtin_bit_cast(float, lane_value(__builtin_bit_cast(unsigned, v), lane));
+}
+__device__ __forceinline__ double lane_value(double v, int lane)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint64_t lo = lane_value((unsigned)b, lane), hi = lane_value((unsigned)(b >> 32), lane);
+    return __builtin_bit_cast(double, (hi << 32) | lo);
+}
+// op(all lanes), `none` being op's neutral value; the same in every lane.
+template <class T, class Op>
+__device__ __forceinline__ T wave_reduce(T v, T none, Op op)
+{
+    v = op(v, dpp<0x111, 0xF>(none, v));   // one lane down the row, then 2, 4, 8
+    v = op(v, dpp<0x112, 0xF>(none, v));
+    v = op(v, dpp<0x114, 0xF>(none, v));
+    v = op(v, dpp<0x118, 0xF>(none, v));
+    v = op(v, dpp<0x142, 0xA>(none, v));   // each odd row takes the row before it
+    v = op(v, dpp<0x143, 0xC>(none, v));   // the upper half takes the lower
+    return lane_value(v, 63);
+}
+__device__ __forceinline__ unsigned wave_max(unsigned v)
+{
+    return wave_reduce(v, 0u, [](unsigned a, unsigned b) { return a > b ? a : b; });
+}
+__device__ __forceinline__ float wave_max(float v)   // NaN only if every lane is
+{
+    return wave_reduce(v, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
 }
 template <class T>
 __device__ __forceinline__ T wave_sum(T v)
 {
+    return wave_reduce(v, T(0), [](T a, T b) { return a + b; });
+}
+// Sums over the lanes up to and including one's own.
+__device__ __forceinline__ int wave_scan(int v, int lane)
+{
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(v, d);
+        if (lane >= d) v += o;
+    }
     return v;
 }
 
 // A choice score as an unsigned key that orders like it: larger scores larger
-// keys, NaN below every number (key 1), an expert that cannot be chosen last
-// (key 0).  -inf is never an available expert's score, so no key clashes.
+// keys, NaN below every number; 0 is left for an expert that cannot be chosen.
+constexpr uint64_t kNanKey = 1ull << 32;
 __device__ __forceinline__ uint64_t score_key(double c)
 {
-    if (c != c) return 1;
-    const uint64_t b = (uint64_t)__double_as_longlong(c);
+    if (c != c) return kNanKey;
+    const uint64_t b = __builtin_bit_cast(uint64_t, c);
     return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+}
+__device__ __forceinline__ uint64_t logit_key(float c)
+{
+    if (c != c) return kNanKey;
+    const unsigned b = __builtin_bit_cast(unsigned, c + 0.f);   // (-0 counts as 0)
+    return (uint64_t)((b >> 31) ? ~b : (b | 0x80000000u)) << 32;
+}
+
+// v[i] = row[lane*NE + i], `none` from E on: 16-byte loads where all four are inside.
+template <int NE>
+__device__ __forceinline__ void load_experts(const float *row, int lane, int E, float none, float *v)
+{
+    const int e0 = lane * NE;
+    if constexpr (NE % 4 == 0) {
+        if (e0 + NE <= E) {
+#pragma unroll
+            for (int i = 0; i < NE; i += 4) {
+                const f32x4_t q = *reinterpret_cast<const f32x4_g *>(row + e0 + i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[i + j] = q[j];
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NE; ++i) v[i] = e0 + i < E ? row[e0 + i] : none;
 }
 
 // ---------------------------------------------------------------- routing
 //
-// A block takes `chunk` consecutive tokens, a wave one token at a time.
-//   choose: every lane holds the scores of experts lane, lane + 64, ...; the k
-//     choices are k rounds of a maximum over the wave (ties to the lowest
-//     index).  Choice scores are formed and compared in 64 bits: neighbouring
-//     scores of one token are often nearer than 32 bits can tell, and the
-//     choice is a whole number that either is right or is not.
-//   layout: the block counts its choices by expert (expert E: the unfilled
-//     choices) and numbers them in token order; one thread per expert walks
-//     the chunk's ids, so the order never depends on timing.  With one block
-//     the counts are scanned here; otherwise they go to `hist` and
-//     place_kernel turns local numbers into rows.
-template <int NE, int NT>
-__global__ __launch_bounds__(NT) void route_kernel(RouteProblem p, int chunk)
+// A block takes `chunk` consecutive tokens, a wave one token at a time; lane l
+// holds experts l*NE .. l*NE + NE-1.
+//   choose: choice scores are formed and compared in 64 bits, since neighbouring
+//     scores of a token are often nearer than 32 bits can tell and the choice is
+//     a whole number that is either right or not.  A score becomes a 64-bit key
+//     whose lowest log2(NE) bits hold the place within the lane (4 bits at most:
+//     scores are told apart to 2^-48), so a lane sorts its NE keys without a
+//     payload and equal scores come in the order of the experts.  A round of the
+//     choice is a maximum of the lanes' upper words; the lower words are looked at
+//     only where two lanes tie.  Where the logits order the experts like the
+//     scores (BY_LOGIT: no bias, a group's best score alone) no score is formed.
+//   layout: choices are numbered by expert in token order: within 64 choices by
+//     comparing ids over the wave, across the block's (at most kSegments) runs of
+//     64 by a prefix over their counts, so the order never depends on timing.
+//     With one block the counts are scanned here; otherwise they go to `counts`
+//     and place_kernel turns local numbers into rows.
+constexpr int kSegments = 16;                  // runs of 64 choices in a block
+constexpr int kChunkIds = 64 * kSegments;
+
+template <int NE, int NT, bool BY_LOGIT>
+__global__ __launch_bounds__(NT) void route_kernel(RouteProblem p, int chunk, int lanes_per_group)
 {
     constexpr int NW = NT / 64;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const int T = p.T, E = p.E, k = p.k;
     const int t0 = blockIdx.x * chunk, t1 = t0 + chunk < T ? t0 + chunk : T;
+    // group scores of odd sizes (64-bit, one row per wave), later the counts of
+    // the runs (16-bit, kSegments rows)
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    double *sc = reinterpret_cast<double *>(smem) + (size_t)wave * (p.groups > 1 ? E : 0);
-    int *cid = reinterpret_cast<int *>(smem + (p.groups > 1 ? (size_t)NW * E * sizeof(double) : 0));   // chunk x k ids
+    __shared__ int cid[kChunkIds];
+    __shared__ int total[kMaxExperts + 2];
+    double *sc = reinterpret_cast<double *>(smem) + (size_t)wave * E;
 
     for (int t = t0 + wave; t < t1; t += NW) {
         const float *row = p.logits + (long long)t * p.ldl;
         float x[NE];
+        load_experts<NE>(row, lane, E, -INFINITY, x);
+        float b[NE];
+        if (p.bias)
+            load_experts<NE>(p.bias, lane, E, -INFINITY, b);
+        else
+#pragma unroll
+            for (int i = 0; i < NE; ++i) b[i] = 0.f;
         float mx = -INFINITY;
-        bool nan = false;
-#pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const int e = lane + 64 * i;
-            x[i] = e < E ? row[e] : -INFINITY;
-            mx = x[i] > mx ? x[i] : mx;
-            nan |= x[i] != x[i];
-        }
-        mx = wave_max(mx);
-        double sum = 0.0;
-        double c[NE];
-        if (p.score == 0) {
-            // (a row of -inf alone has no available expert; its scores are not used)
-#pragma unroll
-            for (int i = 0; i < NE; ++i) {
-                c[i] = x[i] == -INFINITY ? 0.0 : exp((double)x[i] - (double)mx);
-                sum += c[i];
-            }
-            sum = wave_sum(sum);
-#pragma unroll
-            for (int i = 0; i < NE; ++i) c[i] /= sum;
-        } else {
-#pragma unroll
-            for (int i = 0; i < NE; ++i) c[i] = 1.0 / (1.0 + exp(-(double)x[i]));
-        }
+        bool bad = false;   // a softmax whose scores are NaN: the row holds NaN or +inf
+        double sum = 1.0;
         uint64_t key[NE];
-#pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const int e = lane + 64 * i;
-            const float b = p.bias && e < E ? p.bias[e] : 0.f;
-            c[i] += (double)b;
-            key[i] = x[i] == -INFINITY || b == -INFINITY ? 0 : score_key(c[i]);
-        }
-        if (p.groups > 1) {
-            // lane g sums the best group_top available scores of group g; the
-            // group_k best groups stay (ties to the lowest group)
+        if (BY_LOGIT || p.score == 0) {
 #pragma unroll
             for (int i = 0; i < NE; ++i) {
-                const int e = lane + 64 * i;
-                if (e < E) sc[e] = key[i] == 0 ? -INFINITY : c[i];
+                mx = fmaxf(mx, x[i]);
+                bad |= x[i] != x[i] || x[i] == INFINITY;
             }
-            __builtin_amdgcn_wave_barrier();
-            const int size = E / p.groups;
-            uint64_t gkey = 0;
-            if (lane < p.groups) {
-                uint64_t k1 = 0, k2 = 0;
-                double b1 = 0.0, b2 = 0.0;
-                for (int m = 0; m < size; ++m) {
-                    const double v = sc[lane * size + m];
-                    const uint64_t kv = v == -INFINITY ? 0 : score_key(v);
-                    if (kv > k1) {
-                        k2 = k1; b2 = b1; k1 = kv; b1 = v;
-                    } else if (kv > k2) {
-                        k2 = kv; b2 = v;
+            bad = __ballot(bad) != 0;
+            mx = wave_max(mx);
+        }
+        if constexpr (BY_LOGIT) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i)
+                key[i] = x[i] == -INFINITY ? 0
+                         : p.score == 0 && bad ? kNanKey | (NE - 1 - i)
+                                               : logit_key(x[i]) | (NE - 1 - i);
+            if (p.score == 0 && !p.renorm) {
+                // (32 bits: this sum only scales weights)
+                float s = 0.f;
+#pragma unroll
+                for (int i = 0; i < NE; ++i) s += x[i] == -INFINITY ? 0.f : expf(x[i] - mx);
+                sum = (double)wave_sum(s);
+            }
+        }
+        if constexpr (!BY_LOGIT) {
+            double c[NE];
+            if (p.score == 0) {
+                sum = 0.0;
+#pragma unroll
+                for (int i = 0; i < NE; ++i) {
+                    c[i] = x[i] == -INFINITY ? 0.0 : exp((double)x[i] - (double)mx);
+                    sum += c[i];
+                }
+                sum = wave_sum(sum);
+#pragma unroll
+                for (int i = 0; i < NE; ++i) c[i] /= sum;
+            } else {
+#pragma unroll
+                for (int i = 0; i < NE; ++i) c[i] = 1.0 / (1.0 + exp(-(double)x[i]));
+            }
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+                c[i] += (double)b[i];
+                const bool gone = x[i] == -INFINITY || b[i] == -INFINITY;
+                key[i] = gone ? 0 : (score_key(c[i]) & ~(uint64_t)(NE - 1)) | (NE - 1 - i);
+                if (gone) c[i] = -INFINITY;
+                nan |= c[i] != c[i];
+            }
+            if (p.groups > 1) {
+                bool kept;
+                if (lanes_per_group > 0 && __ballot(nan) == 0) {
+                    // a group is 1, 2, 4, 8 or 16 whole lanes: its two best scores by
+                    // exchanges between them (-inf: no available expert)
+                    double b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < NE; ++i) {
+                        b2 = fmax(b2, fmin(b1, c[i]));
+                        b1 = fmax(b1, c[i]);
+                    }
+                    auto merge = [&](double o1, double o2) {
+                        b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+                        b1 = fmax(b1, o1);
+                    };
+                    if (lanes_per_group > 1) merge(dpp<0xB1, 0xF>(b1, b1), dpp<0xB1, 0xF>(b2, b2));     // lane ^ 1
+                    if (lanes_per_group > 2) merge(dpp<0x4E, 0xF>(b1, b1), dpp<0x4E, 0xF>(b2, b2));     // lane ^ 2
+                    if (lanes_per_group > 4) merge(dpp<0x141, 0xF>(b1, b1), dpp<0x141, 0xF>(b2, b2));   // mirrored in 8
+                    if (lanes_per_group > 8) merge(dpp<0x140, 0xF>(b1, b1), dpp<0x140, 0xF>(b2, b2));   // mirrored in 16
+                    const double mine = p.group_top == 2 && b2 != -INFINITY ? b1 + b2 : b1;
+                    const int group = lane / lanes_per_group;
+                    int before = 0;   // groups that come before this lane's
+                    for (int g = 0; g < p.groups; ++g) {
+                        const double o = lane_value(mine, g * lanes_per_group);
+                        before += o > mine || (o == mine && g < group);
+                    }
+                    kept = before < p.group_k;
+#pragma unroll
+                    for (int i = 0; i < NE; ++i)
+                        if (!kept) key[i] = 0;
+                } else {
+                    // lane g walks group g
+#pragma unroll
+                    for (int i = 0; i < NE; ++i)
+                        if (lane * NE + i < E) sc[lane * NE + i] = c[i];
+                    __builtin_amdgcn_wave_barrier();
+                    const int size = E / p.groups;
+                    uint64_t k1 = 0, k2 = 0;
+                    double b1 = 0.0, b2 = 0.0;
+                    if (lane < p.groups)
+                        for (int m = 0; m < size; ++m) {
+                            const double v = sc[lane * size + m];
+                            const uint64_t kv = v == -INFINITY ? 0 : score_key(v);
+                            if (kv > k1) {
+                                k2 = k1; b2 = b1; k1 = kv; b1 = v;
+                            } else if (kv > k2) {
+                                k2 = kv; b2 = v;
+                            }
+                        }
+                    const uint64_t mine = k1 == 0 ? 0 : score_key(p.group_top == 2 && k2 ? b1 + b2 : b1);
+                    int before = 0;
+                    for (int g = 0; g < p.groups; ++g) {
+                        const uint64_t o = ((uint64_t)lane_value((unsigned)(mine >> 32), g) << 32) | lane_value((unsigned)mine, g);
+                        before += o > mine || (o == mine && g < lane);
+                    }
+                    const uint64_t keep = __ballot(lane < p.groups && before < p.group_k);
+#pragma unroll
+                    for (int i = 0; i < NE; ++i) {
+                        const int e = lane * NE + i;
+                        if (e < E && !((keep >> (e / size)) & 1)) key[i] = 0;
+                    }
+                    __builtin_amdgcn_wave_barrier();
+                }
+            }
+        }
+        if constexpr (BY_LOGIT) {
+            if (p.groups > 1) {
+                // a group's score is its best logit's key; groups by lanes as above, or lane by lane
+                const int size = E / p.groups;
+                uint64_t *sk = reinterpret_cast<uint64_t *>(sc);
+#pragma unroll
+                for (int i = 0; i < NE; ++i)
+                    if (lane * NE + i < E) sk[lane * NE + i] = key[i] & ~(uint64_t)(NE - 1);
+                __builtin_amdgcn_wave_barrier();
+                uint64_t mine = 0;
+                if (lane < p.groups)
+                    for (int m = 0; m < size; ++m) {
+                        const uint64_t v = sk[lane * size + m];
+                        mine = v > mine ? v : mine;
+                    }
+                int before = 0;
+                for (int g = 0; g < p.groups; ++g) {
+                    const uint64_t o = ((uint64_t)lane_value((unsigned)(mine >> 32), g) << 32) | lane_value((unsigned)mine, g);
+                    before += o > mine || (o == mine && g < lane);
+                }
+                const uint64_t keep = __ballot(lane < p.groups && before < p.group_k);
+#pragma unroll
+                for (int i = 0; i < NE; ++i) {
+                    const int e = lane * NE + i;
+                    if (e < E && !((keep >> (e / size)) & 1)) key[i] = 0;
+                }
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
+        // the lane's keys in descending order (odd-even transposition for NE <= 2, merging networks beyond)
+#pragma unroll
+        for (int w = 1; w < NE; w <<= 1)
+#pragma unroll
+            for (int d = w; d > 0; d >>= 1)
+#pragma unroll
+                for (int i = 0; i < NE; ++i) {
+                    // bitonic merges of runs of w into runs of 2w, the second run read backwards
+                    const int o = d == w ? (i / (2 * w)) * 2 * w + (2 * w - 1 - i % (2 * w)) : i ^ d;
+                    if (o > i) {
+                        const uint64_t hi = key[i] > key[o] ? key[i] : key[o], lo = key[i] > key[o] ? key[o] : key[i];
+                        key[i] = hi;
+                        key[o] = lo;
                     }
                 }
-                if (k1) gkey = score_key(p.group_top == 2 && k2 ? b1 + b2 : b1);
-            }
-            bool kept = false;
-            for (int j = 0; j < p.group_k; ++j) {
-                const uint64_t best = wave_max(kept || lane >= p.groups ? (uint64_t)0 : gkey + 1);
-                if (best == 0) break;
-                const uint64_t m = __ballot(!kept && lane < p.groups && gkey + 1 == best);
-                if (lane == __builtin_ctzll(m)) kept = true;
-            }
-            const uint64_t keep = __ballot(kept);
-#pragma unroll
-            for (int i = 0; i < NE; ++i) {
-                const int e = lane + 64 * i;
-                if (e < E && !((keep >> (e / size)) & 1)) key[i] = 0;
-            }
-            __builtin_amdgcn_wave_barrier();
-        }
-        // k rounds: the largest key, of equal ones the lowest expert
         int mine = -1;   // lane j: choice j
         for (int j = 0; j < k; ++j) {
-            uint64_t b = 0;
-            int at = 0;
-#pragma unroll
-            for (int i = 0; i < NE; ++i)
-                if (key[i] > b) {
-                    b = key[i];
-                    at = i;
-                }
-            const uint64_t best = wave_max(b);
-            if (best == 0) break;
-            int e = b == best ? lane + 64 * at : INT_MAX;
-#pragma unroll
-            for (int d = 32; d > 0; d >>= 1) {
-                const int o = __shfl_xor(e, d);
-                e = o < e ? o : e;
+            const unsigned top = wave_max((unsigned)(key[0] >> 32));
+            if (top == 0) break;
+            uint64_t at = __ballot((unsigned)(key[0] >> 32) == top);
+            if (at & (at - 1)) {   // lanes whose upper words are equal: the larger lower word, then the lower lane
+                const bool in = (at >> lane) & 1;
+                const unsigned low = in ? (unsigned)(key[0] & 0xFFFFFFFFu & ~(uint64_t)(NE - 1)) : 0u;
+                const unsigned most = wave_max(low);   // (every lane takes part)
+                at = __ballot(in && low == most);
             }
+            const int win = __builtin_ctzll(at);
+            const int e = win * NE + (NE - 1 - (int)(lane_value((unsigned)key[0], win) & (NE - 1)));
             if (lane == j) mine = e;
+            if (lane == win) {
 #pragma unroll
-            for (int i = 0; i < NE; ++i)
-                if (lane + 64 * i == e) key[i] = 0;
+                for (int i = 0; i + 1 < NE; ++i) key[i] = key[i + 1];
+                key[NE - 1] = 0;
+            }
         }
-        // weights, from the chosen logits alone where they are renormalised
+        // weights, from the chosen logits alone where they are renormalised; in 64
+        // bits, where scores that 32 bits lose still have a quotient
         const bool has = lane < k && mine >= 0;
         const float xl = has ? row[mine] : -INFINITY;
         double w = 0.0;
-        if (p.score == 1)
+        if (p.score == 1) {
             w = has ? 1.0 / (1.0 + exp(-(double)xl)) : 0.0;
-        else if (p.renorm) {
-            // (of a row that holds NaN or +inf every softmax score is NaN)
-            const bool bad = __ballot(nan) != 0 || mx == INFINITY;
-            const float cm = wave_max(xl);
-            w = has ? (bad ? (double)NAN : exp((double)xl - (double)cm)) : 0.0;
         } else {
-            w = has ? exp((double)xl - (double)mx) / sum : 0.0;
+            const float ref = p.renorm ? wave_max(xl) : mx;
+            w = !has ? 0.0 : bad ? (double)NAN : exp((double)xl - (double)ref) / sum;
         }
         if (p.renorm) {
             const double s = wave_sum(w);
@@ -188,86 +365,140 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteProblem p, int chunk)
         }
     }
     if (p.offsets == nullptr) return;
+
+    const int n = (t1 - t0) * k;   // at most kChunkIds
+    const int first = t0 * k;      // T*k fits an int
+    const int per = E + 1;
+    uint16_t *seg = reinterpret_cast<uint16_t *>(smem);
     __syncthreads();
-    const int n = (t1 - t0) * k;
-    const int first = t0 * k;   // T*k fits an int
-    if (gridDim.x > 1) {
-        int32_t *hist = p.hist + (long long)blockIdx.x * (E + 1);
-        for (int e = tid; e <= E; e += NT) {
-            int cnt = 0;
-            for (int i = 0; i < n; ++i)
-                if (cid[i] == e) p.slots[first + i] = cnt++;
-            hist[e] = cnt;
+    for (int i = tid; i < kSegments * per; i += NT) seg[i] = 0;
+    __syncthreads();
+    constexpr int IT = (kChunkIds + NT - 1) / NT;
+    int mine[IT], rank[IT];
+    const int bits = 32 - __builtin_clz((unsigned)E);   // E itself is an id
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+        const int i = it * NT + tid;
+        const int e = i < n ? cid[i] : 0;
+        uint64_t same = __ballot(i < n);
+        for (int bit = 0; bit < bits; ++bit) {
+            const bool one = (e >> bit) & 1;
+            const uint64_t m = __ballot(one);
+            same &= one ? m : ~m;
         }
-        return;
+        mine[it] = e;
+        rank[it] = __popcll(same & ((1ull << lane) - 1));
+        if (i < n && rank[it] == 0) seg[(i >> 6) * per + e] = (uint16_t)__popcll(same);
     }
-    // one block: scan the counts here.  Thread e holds expert e's, then E's.
-    __shared__ int total[kMaxExperts + 2];
-    for (int e = tid; e <= E; e += NT) {
-        int cnt = 0;
-        for (int i = 0; i < n; ++i) cnt += cid[i] == e;
-        total[e] = cnt;
+    __syncthreads();
+    for (int e = tid; e < per; e += NT) {
+        int run = 0;
+#pragma unroll
+        for (int g = 0; g < kSegments; ++g) {
+            const int v = seg[g * per + e];
+            seg[g * per + e] = (uint16_t)run;
+            run += v;
+        }
+        total[e] = run;
+        if (gridDim.x > 1) p.counts[(long long)blockIdx.x * per + e] = run;
+    }
+    __syncthreads();
+    const bool alone = gridDim.x == 1;
+    if (alone && wave == 0) {
+        int carry = 0;
+        for (int e0 = 0; e0 < per; e0 += 64) {
+            const int e = e0 + lane;
+            const int v = e < per ? total[e] : 0;
+            const int s = wave_scan(v, lane);
+            if (e < per) {
+                total[e] = carry + s - v;
+                p.offsets[e] = carry + s - v;
+            }
+            carry += __shfl(s, 63);
+        }
+    }
+    if (alone) __syncthreads();
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+        const int i = it * NT + tid;
+        if (i >= n) continue;
+        const int e = mine[it], local = seg[(i >> 6) * per + e] + rank[it];
+        if (!alone) {
+            p.slots[first + i] = local;
+        } else {
+            const int at = total[e] + local;
+            p.slots[i] = e < E ? at : -1;
+            p.rows[at] = e < E ? i / k : -1;
+        }
+    }
+}
+
+// The chunks' counts (chunks rows of E + 1) to the counts before each chunk, in
+// place, and their totals as one more row.  A block takes 64 experts, one per
+// lane; its waves share the chunks.
+__global__ __launch_bounds__(1024) void prefix_kernel(RouteProblem p, int chunks)
+{
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int per = p.E + 1, e = blockIdx.x * 64 + lane;
+    __shared__ int part[16][64];
+    const int each = (chunks + 15) / 16;
+    const int b0 = wave * each, b1 = b0 + each < chunks ? b0 + each : chunks;
+    int sum = 0;
+    if (e < per)
+#pragma unroll 8
+        for (int b = b0; b < b1; ++b) sum += p.counts[(long long)b * per + e];
+    part[wave][lane] = sum;
+    __syncthreads();
+    if (e >= per) return;
+    int run = 0;
+    for (int w = 0; w < wave; ++w) run += part[w][lane];
+#pragma unroll 8
+    for (int b = b0; b < b1; ++b) {
+        int32_t *at = p.counts + (long long)b * per + e;
+        const int v = *at;
+        *at = run;
+        run += v;
+    }
+    if (wave == 15) p.counts[(long long)chunks * per + e] = run;
+}
+
+// Local numbers to rows.  PREFIXED: prefix_kernel has run; otherwise each block
+// adds up the counts of the chunks before its own, and of all of them.
+template <bool PREFIXED>
+__global__ __launch_bounds__(1024) void place_kernel(RouteProblem p, int chunk, int chunks)
+{
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, k = p.k, E = p.E, per = E + 1;
+    __shared__ int base[kMaxExperts + 2], total[kMaxExperts + 2];
+    if constexpr (PREFIXED) {
+        for (int e = tid; e < per; e += 1024) {
+            base[e] = p.counts[(long long)blockIdx.x * per + e];
+            total[e] = p.counts[(long long)chunks * per + e];
+        }
+    } else {
+        for (int e = tid; e < per; e += 1024) base[e] = total[e] = 0;
+        __syncthreads();
+        const int runs = (per + 63) / 64;   // (64 experts) x (an eighth of the chunks) per wave and turn
+        for (int it = wave; it < 8 * runs; it += 16) {
+            const int e = it / 8 * 64 + lane;
+            if (e >= per) continue;
+            int before = 0, all = 0;
+#pragma unroll 4
+            for (int b = it % 8; b < chunks; b += 8) {
+                const int v = p.counts[(long long)b * per + e];
+                all += v;
+                before += b < (int)blockIdx.x ? v : 0;
+            }
+            atomicAdd(&base[e], before);   // whole numbers in LDS: the order does not matter
+            atomicAdd(&total[e], all);
+        }
     }
     __syncthreads();
     if (wave == 0) {
         int carry = 0;
-        for (int b = 0; b <= E; b += 64) {
-            const int e = b + lane;
-            const int v = e <= E ? total[e] : 0;
-            int s = v;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int o = __shfl_up(s, d);
-                if (lane >= d) s += o;
-            }
-            if (e <= E) total[e] = carry + s - v;
-            carry += __shfl(s, 63);
-        }
-    }
-    __syncthreads();
-    for (int e = tid; e <= E; e += NT) {
-        int at = total[e];
-        p.offsets[e] = at;
-        for (int i = 0; i < n; ++i)
-            if (cid[i] == e) {
-                p.slots[i] = e < E ? at : -1;
-                p.rows[at++] = e < E ? i / k : -1;
-            }
-    }
-}
-
-// Local numbers to rows: block b adds up the counts of the chunks before its
-// own (and of all, for the experts' starts) and places its chunk's choices.
-__global__ __launch_bounds__(1024) void place_kernel(RouteProblem p, int chunk, int chunks)
-{
-    const int tid = threadIdx.x, E = p.E, k = p.k;
-    __shared__ int base[kMaxExperts + 2], total[kMaxExperts + 2];
-    for (int e = tid; e <= E; e += 1024) base[e] = total[e] = 0;
-    __syncthreads();
-    // threads share the (chunk, expert) counts by rows of chunks
-    const int per = E + 1;
-    for (int e = tid % 512; e < per; e += 512) {
-        int before = 0, all = 0;
-        for (int b = tid / 512; b < chunks; b += 2) {
-            const int v = p.hist[(long long)b * per + e];
-            all += v;
-            if (b < (int)blockIdx.x) before += v;
-        }
-        atomicAdd(&base[e], before);   // whole numbers: the order does not matter
-        atomicAdd(&total[e], all);
-    }
-    __syncthreads();
-    if (tid < 64) {
-        int carry = 0;
-        for (int b = 0; b < per; b += 64) {
-            const int e = b + tid;
+        for (int e0 = 0; e0 < per; e0 += 64) {
+            const int e = e0 + lane;
             const int v = e < per ? total[e] : 0;
-            int s = v;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int o = __shfl_up(s, d);
-                if (tid >= d) s += o;
-            }
+            const int s = wave_scan(v, lane);
             if (e < per) {
                 base[e] += carry + s - v;
                 if (blockIdx.x == 0) p.offsets[e] = carry + s - v;
@@ -285,29 +516,40 @@ __global__ __launch_bounds__(1024) void place_kernel(RouteProblem p, int chunk, 
     }
 }
 
-// Tokens per block: one block for up to 64 tokens, else 32 or more tokens such
-// that place_kernel reads the counts of at most 256 chunks while a chunk's ids
-// fit 16 KB of LDS.
+// Tokens per block.  One block for a few tokens (one launch); else 16 tokens or
+// more, such that 256 blocks hold all of them while a block's choices fit
+// kChunkIds.
 int route_chunk(int T, int k)
 {
-    if (T <= 64) return 64;
-    const int c = (T + 255) / 256, most = 4096 / k;
-    return c < 32 ? 32 : c < most ? c : most;
+    const int most = kChunkIds / k;
+    if (T <= 64 && T <= most) return T < 1 ? 1 : T;
+    const int c = (T + 255) / 256;
+    const int least = most < 16 ? most : 16;
+    return c < least ? least : c < most ? c : most;
 }
 
-template <int NE>
+constexpr int kDirectChunks = 64;   // up to these many chunks place_kernel adds the counts up itself
+
+template <int NE, bool BY_LOGIT>
 hipError_t route_ne(const RouteProblem &p, hipStream_t stream)
 {
+    constexpr int NT = NE <= 4 ? 1024 : 512;
     const int chunk = route_chunk(p.T, p.k), chunks = p.T > 0 ? (p.T + chunk - 1) / chunk : 1;
-    constexpr int NT1 = NE <= 4 ? 1024 : 256;   // threads of a single block (32 KB of group scores either way)
-    const int nt = chunks == 1 ? NT1 : 256;
-    const size_t lds = (p.groups > 1 ? (size_t)(nt / 64) * p.E * sizeof(double) : 0) + (size_t)chunk * p.k * sizeof(int);
-    if (chunks == 1)
-        hipLaunchKernelGGL((route_kernel<NE, NT1>), dim3(1), dim3(NT1), lds, stream, p, chunk);
-    else
-        hipLaunchKernelGGL((route_kernel<NE, 256>), dim3(chunks), dim3(256), lds, stream, p, chunk);
-    if (chunks > 1 && p.offsets)
-        hipLaunchKernelGGL(place_kernel, dim3(chunks), dim3(1024), 0, stream, p, chunk, chunks);
+    // lanes that hold a group: whole ones, a power of two up to a row of 16
+    const int size = p.E / p.groups, lanes = size % NE == 0 ? size / NE : 0;
+    const int fast = lanes > 0 && lanes <= 16 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+    const size_t scores = p.groups > 1 ? (size_t)(NT / 64) * p.E * sizeof(double) : 0;
+    const size_t counts = p.offsets ? (size_t)kSegments * (p.E + 1) * sizeof(uint16_t) : 0;
+    hipLaunchKernelGGL((route_kernel<NE, NT, BY_LOGIT>), dim3(chunks), dim3(NT), scores > counts ? scores : counts, stream, p,
+                       chunk, fast);
+    if (chunks > 1 && p.offsets) {
+        if (chunks <= kDirectChunks) {
+            hipLaunchKernelGGL(place_kernel<false>, dim3(chunks), dim3(1024), 0, stream, p, chunk, chunks);
+        } else {
+            hipLaunchKernelGGL(prefix_kernel, dim3((p.E + 64) / 64), dim3(1024), 0, stream, p, chunks);
+            hipLaunchKernelGGL(place_kernel<true>, dim3(chunks), dim3(1024), 0, stream, p, chunk, chunks);
+        }
+    }
     return hipGetLastError();
 }
 
@@ -341,12 +583,9 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradProblem p)
     float dot = 0.f;
     if (whole) {
         float mx = -INFINITY;
+        load_experts<NE>(row, lane, E, -INFINITY, s);
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const int e = lane + 64 * i;
-            s[i] = e < E ? row[e] : -INFINITY;
-            mx = s[i] > mx ? s[i] : mx;
-        }
+        for (int i = 0; i < NE; ++i) mx = s[i] > mx ? s[i] : mx;
         mx = wave_max(mx);
         float sum = 0.f;
 #pragma unroll
@@ -381,17 +620,27 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradProblem p)
 #pragma unroll
     for (int i = 0; i < NE; ++i) acc[i] = 0.f;
     for (int j = 0; j < k; ++j) {
-        const int e = __shfl(id, j);
-        const float d = __shfl(v, j);
+        const int e = (int)lane_value((unsigned)id, j);
+        const float d = lane_value(v, j);
 #pragma unroll
         for (int i = 0; i < NE; ++i)
-            if (lane + 64 * i == e) acc[i] += d;
+            if (lane * NE + i == e) acc[i] += d;
     }
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        const int e = lane + 64 * i;
-        if (e < E) out[e] = whole ? s[i] * (acc[i] - dot) : acc[i];
+    for (int i = 0; i < NE; ++i)
+        if (whole) acc[i] = s[i] * (acc[i] - dot);
+    const int e0 = lane * NE;
+    if constexpr (NE % 4 == 0) {
+        if (e0 + NE <= E) {
+#pragma unroll
+            for (int i = 0; i < NE; i += 4)
+                *reinterpret_cast<f32x4_g *>(out + e0 + i) = f32x4_t{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
+            return;
+        }
     }
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+        if (e0 + i < E) out[e0 + i] = acc[i];
 }
 
 // ---------------------------------------------------------------- combining
@@ -517,16 +766,21 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(CombineGradProblem p)
 size_t route_workspace(int T, int E, int k)
 {
     const int chunk = route_chunk(T, k), chunks = (T + chunk - 1) / chunk;
-    return chunks > 1 ? (size_t)chunks * (E + 1) * sizeof(int32_t) : 0;
+    return chunks > 1 ? (size_t)(chunks + 1) * (E + 1) * sizeof(int32_t) : 0;
 }
 
 hipError_t launch_route(const RouteProblem &p, hipStream_t stream)
 {
-    if (p.E <= 64) return route_ne<1>(p, stream);
-    if (p.E <= 128) return route_ne<2>(p, stream);
-    if (p.E <= 256) return route_ne<4>(p, stream);
-    if (p.E <= 512) return route_ne<8>(p, stream);
-    return route_ne<16>(p, stream);
+    const bool by_logit = p.bias == nullptr && (p.groups == 1 || p.group_top == 1);
+    auto run = [&](auto ne) {
+        constexpr int NE = decltype(ne)::value;
+        return by_logit ? route_ne<NE, true>(p, stream) : route_ne<NE, false>(p, stream);
+    };
+    if (p.E <= 64) return run(std::integral_constant<int, 1>{});
+    if (p.E <= 128) return run(std::integral_constant<int, 2>{});
+    if (p.E <= 256) return run(std::integral_constant<int, 4>{});
+    if (p.E <= 512) return run(std::integral_constant<int, 8>{});
+    return run(std::integral_constant<int, 16>{});
 }
 
 hipError_t launch_route_grad(const RouteGradProblem &p, hipStream_t stream)

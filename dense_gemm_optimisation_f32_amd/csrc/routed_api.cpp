@@ -228,7 +228,7 @@ int moe_route_f32(int T, int E, const float *logits, int ldl, const float *bias,
     p.renorm = renorm; p.scale = scale;
     p.ids = ids; p.weights = weights;
     p.offsets = offsets; p.rows = rows; p.slots = slots;
-    p.hist = static_cast<int32_t *>(workspace);
+    p.counts = static_cast<int32_t *>(workspace);
     return launched(mi355gemm::launch_route(p, stream));   // T = 0: the offsets are zeros
 }
 

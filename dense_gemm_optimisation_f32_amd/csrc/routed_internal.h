@@ -27,7 +27,7 @@ struct RouteProblem {
     int32_t *ids;                   // T x k
     float *weights;                 // T x k
     int32_t *offsets, *rows, *slots;   // E + 1, T*k, T x k; all three or none
-    int32_t *hist;                  // workspace: chunks x (E + 1) counts
+    int32_t *counts;                // workspace: (chunks + 1) x (E + 1)
 };
 // Workspace bytes launch_route needs (0: none).
 size_t route_workspace(int T, int E, int k);

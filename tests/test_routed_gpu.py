@@ -71,6 +71,8 @@ def route_oracle(x, bias, score, groups, group_k, group_top, k, renorm, scale):
                 e = np.exp(x[t] - np.max(x[t])) if np.any(x[t] != -np.inf) else np.zeros(E)
                 s = e / e.sum()
             c = s + b
+            if bias is None and (groups == 1 or group_top == 1):   # the logits order the experts, also where 64 bits saturate
+                c = np.where(np.isnan(s), np.nan, x[t])
             if groups > 1:
                 size, best = E // groups, np.full(groups, -np.inf)
                 some = np.zeros(groups, dtype=bool)

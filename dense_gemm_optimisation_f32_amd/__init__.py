@@ -18,8 +18,8 @@ If the library is not built, importing works but every call raises
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 
 __all__ = ["gemm_f32", "gemm_f16_f32acc", "gemm_batched_f16_f32acc",
@@ -305,49 +305,86 @@ def gemm_batched_bf16_f32acc_ex(transA, transB, M, N, K, alpha, A, lda, strideA,
 
 
 # ------------------------------------------------------------------ products whose right operand is chosen per row
+#
+# These calls serve single tokens, whose kernels take a few microseconds, so their
+# marshalling is kept short: one pass over an operand's properties, sizes of
+# workspaces remembered by the sizes they belong to.
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+
+    _torch = torch
+    return torch
+
+
+def _strided(x, name: str, dtype_name: str, need: int):
+    """_ptr with a short way for a contiguous tensor that holds ``need`` elements."""
+    if x is None or type(x) is int:
+        return x
+    torch = _torch or _load_torch()
+    if isinstance(x, torch.Tensor) and x.is_cuda and x.dtype is getattr(torch, dtype_name) and x.is_contiguous() and x.numel() >= need:
+        return x.data_ptr()
+    return _ptr(x, name, "torch." + dtype_name, need)
+
+
 def _packed(x, name: str, dtype_name: str, need: int):
     """Device address of an array the kernels read or write without strides."""
-    if _is_tensor(x) and x.device.type == "cuda" and not x.is_contiguous():
+    if x is None or type(x) is int:
+        return x
+    torch = _torch or _load_torch()
+    if isinstance(x, torch.Tensor) and x.is_cuda and not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return _ptr(x, name, dtype_name, need)
+    return _strided(x, name, dtype_name, need)
 
 
-def _call(name: str, args, operands, stream, workspace=None, workspace_bytes=None) -> None:
-    """Run library function ``name`` on the device that holds ``operands`` (one for all of them): on ``stream``, or on
+def _call(fn, args, operands, stream, workspace=None, workspace_bytes=None) -> None:
+    """Run library function ``fn`` on the device that holds ``operands`` (one for all of them): on ``stream``, or on
     that device's current stream.  With ``workspace_bytes`` the call takes a workspace: the caller's, or one that torch's
     allocator hands out for that stream (graph capture included) and takes back in its order."""
-    fn = getattr(load_library(), name)
-    devices = {x.device for x in operands if _is_tensor(x)}
-    if len(devices) > 1:
-        raise ValueError(f"{name}: operands on more than one device: {sorted(map(str, devices))}")
-    if not devices and stream is not None and not workspace_bytes:
-        rc = fn(*args, *(() if workspace_bytes is None else (None, 0)), _stream(stream))
+    dev = -1
+    for x in operands:
+        if x is not None and type(x) is not int:
+            d = x.get_device()
+            if dev < 0:
+                dev = d
+            elif d != dev:
+                raise ValueError(f"{fn.__name__}: operands on more than one device: cuda:{dev} and cuda:{d}")
+    if dev < 0 and stream is not None and not (workspace_bytes and workspace is None):
+        rc = fn(*args, *(() if workspace_bytes is None else (workspace, workspace_bytes)), _stream(stream))   # addresses alone
     else:
-        import torch
-
+        torch = _torch or _load_torch()
         here = torch.cuda.current_device()
-        dev = devices.pop().index if devices else here
-        with contextlib.nullcontext() if dev == here else torch.cuda.device(dev):
-            h = _stream(stream)
-            if workspace_bytes is None:
-                rc = fn(*args, h)
-            else:
-                if workspace is None and workspace_bytes > 0:
-                    with contextlib.nullcontext() if stream is None else torch.cuda.stream(torch.cuda.ExternalStream(h)):
+        if dev >= 0 and dev != here:
+            with torch.cuda.device(dev):
+                return _call(fn, args, operands, stream, workspace, workspace_bytes)
+        h = torch.cuda.current_stream(here).cuda_stream if stream is None else _stream(stream)
+        if workspace_bytes is None:
+            rc = fn(*args, h)
+        else:
+            if workspace is None and workspace_bytes > 0:
+                if stream is None:
+                    workspace = torch.empty(workspace_bytes, dtype=torch.uint8, device="cuda")
+                else:
+                    with torch.cuda.stream(torch.cuda.ExternalStream(h)):
                         workspace = torch.empty(workspace_bytes, dtype=torch.uint8, device="cuda")
-                rc = fn(*args, _ptr(workspace, "workspace", None, 0), _room(workspace, workspace_bytes), h)
+            rc = fn(*args, *_room(workspace, workspace_bytes), h)
     if rc != 0:
-        raise GemmError(rc, name)
+        raise GemmError(rc, fn.__name__)
 
 
-def _room(workspace, need: int) -> int:
-    """Bytes the library may use: what a tensor's storage holds from its start, or for a raw address what the call needs."""
-    if not _is_tensor(workspace):
-        return need
+def _room(workspace, need: int):
+    """Address and bytes the library may use: what a tensor's storage holds from its start, or for a raw address what the call needs."""
+    if workspace is None or type(workspace) is int:
+        return workspace, need
+    at = _ptr(workspace, "workspace", None, 0)
     st = workspace.untyped_storage()
-    return st.nbytes() - (workspace.data_ptr() - st.data_ptr())
+    return at, st.nbytes() - (at - st.data_ptr())
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_route_workspace(T, E, k) -> int:
     """Bytes of workspace moe_route_f32 needs for its sorted choices (0: none)."""
     return load_library().moe_route_workspace(T, E, k)
@@ -357,21 +394,21 @@ def moe_route_f32(T, E, logits, ldl, bias, score, groups, group_k, group_top, k,
                   rows=None, slots=None, workspace=None, stream=None) -> None:
     """Each of T tokens chooses k of E experts (ids, weights), and the choices sorted by expert (offsets, rows, slots)."""
     n = max(T, 0) * max(k, 0)
-    args = (T, E, _ptr(logits, "logits", "torch.float32", _extent(T, E, ldl)), ldl, _packed(bias, "bias", "torch.float32", E),
-            int(score), groups, group_k, group_top, k, int(renorm), scale, _packed(ids, "ids", "torch.int32", n),
-            _packed(weights, "weights", "torch.float32", n), _packed(offsets, "offsets", "torch.int32", E + 1),
-            _packed(rows, "rows", "torch.int32", n), _packed(slots, "slots", "torch.int32", n))
+    args = (T, E, _strided(logits, "logits", "float32", _extent(T, E, ldl)), ldl, _packed(bias, "bias", "float32", E),
+            int(score), groups, group_k, group_top, k, int(renorm), scale, _packed(ids, "ids", "int32", n),
+            _packed(weights, "weights", "float32", n), _packed(offsets, "offsets", "int32", E + 1),
+            _packed(rows, "rows", "int32", n), _packed(slots, "slots", "int32", n))
     need = moe_route_workspace(T, E, k) if offsets is not None else 0
-    _call("moe_route_f32", args, (logits, bias, ids, weights, offsets, rows, slots, workspace), stream, workspace, need)
+    _call(load_library().moe_route_f32, args, (logits, bias, ids, weights, offsets, rows, slots, workspace), stream, workspace, need)
 
 
 def moe_route_f32_grad(T, E, logits, ldl, score, k, renorm, scale, ids, dweights, dlogits, lddl, stream=None) -> None:
     """dlogits from dweights: the gradient of moe_route_f32's weights in its logits."""
     n = max(T, 0) * max(k, 0)
-    args = (T, E, _ptr(logits, "logits", "torch.float32", _extent(T, E, ldl)), ldl, int(score), k, int(renorm), scale,
-            _packed(ids, "ids", "torch.int32", n), _packed(dweights, "dweights", "torch.float32", n),
-            _ptr(dlogits, "dlogits", "torch.float32", _extent(T, E, lddl)), lddl)
-    _call("moe_route_f32_grad", args, (logits, ids, dweights, dlogits), stream)
+    args = (T, E, _strided(logits, "logits", "float32", _extent(T, E, ldl)), ldl, int(score), k, int(renorm), scale,
+            _packed(ids, "ids", "int32", n), _packed(dweights, "dweights", "float32", n),
+            _strided(dlogits, "dlogits", "float32", _extent(T, E, lddl)), lddl)
+    _call(load_library().moe_route_f32_grad, args, (logits, ids, dweights, dlogits), stream)
 
 
 def _grouped(t, dtype_name, transB, groups, R, N, K, alpha, A, M, lda, rows, B, ldb, strideB, offsets, beta, C, ldc, stream):
@@ -379,24 +416,24 @@ def _grouped(t, dtype_name, transB, groups, R, N, K, alpha, A, M, lda, rows, B, 
     work = groups > 0 and R > 0 and N > 0
     reads = work and K > 0 and alpha != 0 and M > 0
     b = _extent(*((N, K) if tB else (K, N)), ldb) + max(groups - 1, 0) * strideB
-    args = (tB, groups, R, N, K, alpha, _ptr(A, "A", dtype_name, _extent(M, K, lda) if reads else 0), M, lda,
-            _packed(rows, "rows", "torch.int32", R if reads else 0), _ptr(B, "B", dtype_name, b if reads else 0), ldb, strideB,
-            _packed(offsets, "offsets", "torch.int32", groups + 1 if work else 0), beta,
-            _ptr(C, "C", "torch.float32", _extent(R, N, ldc)), ldc)
-    _call(f"gemm_grouped_{t}_f32acc_ex", args, (A, rows, B, offsets, C), stream)
+    args = (tB, groups, R, N, K, alpha, _strided(A, "A", dtype_name, _extent(M, K, lda) if reads else 0), M, lda,
+            _packed(rows, "rows", "int32", R if reads else 0), _strided(B, "B", dtype_name, b if reads else 0), ldb, strideB,
+            _packed(offsets, "offsets", "int32", groups + 1 if work else 0), beta,
+            _strided(C, "C", "float32", _extent(R, N, ldc)), ldc)
+    _call(getattr(load_library(), f"gemm_grouped_{t}_f32acc_ex"), args, (A, rows, B, offsets, C), stream)
 
 
 def gemm_grouped_f16_f32acc_ex(transB, groups, R, N, K, alpha, A, M, lda, rows, B, ldb, strideB, offsets, beta, C, ldc,
                                stream=None) -> None:
     """C[r,:] <- alpha*A[rows[r],:]*op(B_g) + beta*C[r,:] for the rows r of every group g; fp16 A and B, fp32 C."""
-    _grouped("f16", "torch.float16", transB, groups, R, N, K, alpha, A, M, lda, rows, B, ldb, strideB, offsets, beta, C, ldc,
+    _grouped("f16", "float16", transB, groups, R, N, K, alpha, A, M, lda, rows, B, ldb, strideB, offsets, beta, C, ldc,
              stream)
 
 
 def gemm_grouped_bf16_f32acc_ex(transB, groups, R, N, K, alpha, A, M, lda, rows, B, ldb, strideB, offsets, beta, C, ldc,
                                 stream=None) -> None:
     """gemm_grouped_f16_f32acc_ex with bf16 A and B."""
-    _grouped("bf16", "torch.bfloat16", transB, groups, R, N, K, alpha, A, M, lda, rows, B, ldb, strideB, offsets, beta, C, ldc,
+    _grouped("bf16", "bfloat16", transB, groups, R, N, K, alpha, A, M, lda, rows, B, ldb, strideB, offsets, beta, C, ldc,
              stream)
 
 
@@ -404,57 +441,58 @@ def _wgrad(t, dtype_name, groups, R, M, N, alpha, A, a_rows, lda, rowsA, B, b_ro
            stream):
     work = groups > 0 and M > 0 and N > 0
     reads = work and R > 0 and alpha != 0 and a_rows > 0 and b_rows > 0
-    args = (groups, R, M, N, alpha, _ptr(A, "A", dtype_name, _extent(a_rows, M, lda) if reads else 0), a_rows, lda,
-            _packed(rowsA, "rowsA", "torch.int32", R if reads else 0),
-            _ptr(B, "B", dtype_name, _extent(b_rows, N, ldb) if reads else 0), b_rows, ldb,
-            _packed(rowsB, "rowsB", "torch.int32", R if reads else 0),
-            _packed(offsets, "offsets", "torch.int32", groups + 1 if reads else 0), beta,
-            _ptr(C, "C", "torch.float32", _extent(M, N, ldc) + (groups - 1) * strideC if work else 0), ldc, strideC)
-    _call(f"gemm_grouped_wgrad_{t}_f32acc", args, (A, rowsA, B, rowsB, offsets, C), stream)
+    args = (groups, R, M, N, alpha, _strided(A, "A", dtype_name, _extent(a_rows, M, lda) if reads else 0), a_rows, lda,
+            _packed(rowsA, "rowsA", "int32", R if reads else 0),
+            _strided(B, "B", dtype_name, _extent(b_rows, N, ldb) if reads else 0), b_rows, ldb,
+            _packed(rowsB, "rowsB", "int32", R if reads else 0),
+            _packed(offsets, "offsets", "int32", groups + 1 if reads else 0), beta,
+            _strided(C, "C", "float32", _extent(M, N, ldc) + (groups - 1) * strideC if work else 0), ldc, strideC)
+    _call(getattr(load_library(), f"gemm_grouped_wgrad_{t}_f32acc"), args, (A, rowsA, B, rowsB, offsets, C), stream)
 
 
 def gemm_grouped_wgrad_f16_f32acc(groups, R, M, N, alpha, A, a_rows, lda, rowsA, B, b_rows, ldb, rowsB, offsets, beta, C, ldc,
                                   strideC, stream=None) -> None:
     """C_g <- alpha * sum over group g's rows r of A[rowsA[r],:]^T B[rowsB[r],:] + beta*C_g; fp16 A and B, fp32 C."""
-    _wgrad("f16", "torch.float16", groups, R, M, N, alpha, A, a_rows, lda, rowsA, B, b_rows, ldb, rowsB, offsets, beta, C, ldc,
+    _wgrad("f16", "float16", groups, R, M, N, alpha, A, a_rows, lda, rowsA, B, b_rows, ldb, rowsB, offsets, beta, C, ldc,
            strideC, stream)
 
 
 def gemm_grouped_wgrad_bf16_f32acc(groups, R, M, N, alpha, A, a_rows, lda, rowsA, B, b_rows, ldb, rowsB, offsets, beta, C, ldc,
                                    strideC, stream=None) -> None:
     """gemm_grouped_wgrad_f16_f32acc with bf16 A and B."""
-    _wgrad("bf16", "torch.bfloat16", groups, R, M, N, alpha, A, a_rows, lda, rowsA, B, b_rows, ldb, rowsB, offsets, beta, C, ldc,
+    _wgrad("bf16", "bfloat16", groups, R, M, N, alpha, A, a_rows, lda, rowsA, B, b_rows, ldb, rowsB, offsets, beta, C, ldc,
            strideC, stream)
 
 
 def moe_combine_f32(T, k, N, Y, R, ldy, slots, weights, beta, C, ldc, stream=None) -> None:
     """C[t,:] <- sum_j weights[t,j]*Y[slots[t,j],:] + beta*C[t,:] (weights None: ones)."""
     n = max(T, 0) * max(k, 0) if N > 0 else 0
-    args = (T, k, N, _ptr(Y, "Y", "torch.float32", _extent(R, N, ldy) if n else 0), R, ldy,
-            _packed(slots, "slots", "torch.int32", n), _packed(weights, "weights", "torch.float32", n), beta,
-            _ptr(C, "C", "torch.float32", _extent(T, N, ldc)), ldc)
-    _call("moe_combine_f32", args, (Y, slots, weights, C), stream)
+    args = (T, k, N, _strided(Y, "Y", "float32", _extent(R, N, ldy) if n else 0), R, ldy,
+            _packed(slots, "slots", "int32", n), _packed(weights, "weights", "float32", n), beta,
+            _strided(C, "C", "float32", _extent(T, N, ldc)), ldc)
+    _call(load_library().moe_combine_f32, args, (Y, slots, weights, C), stream)
 
 
 def _combine_grad(t, dtype_name, T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream):
     n = max(T, 0) * max(k, 0)
-    args = (T, k, N, _ptr(dC, "dC", "torch.float32", _extent(T, N, lddc)), lddc,
-            _ptr(Y, "Y", "torch.float32", _extent(R, N, ldy) if n else 0), R, ldy, _packed(slots, "slots", "torch.int32", n),
-            _packed(weights, "weights", "torch.float32", n), _ptr(dY, "dY", dtype_name, _extent(R, N, lddy) if n else 0), lddy,
-            _packed(dweights, "dweights", "torch.float32", n))
-    _call(f"moe_combine_grad_{t}", args, (dC, Y, slots, weights, dY, dweights), stream)
+    args = (T, k, N, _strided(dC, "dC", "float32", _extent(T, N, lddc)), lddc,
+            _strided(Y, "Y", "float32", _extent(R, N, ldy) if n else 0), R, ldy, _packed(slots, "slots", "int32", n),
+            _packed(weights, "weights", "float32", n), _strided(dY, "dY", dtype_name, _extent(R, N, lddy) if n else 0), lddy,
+            _packed(dweights, "dweights", "float32", n))
+    _call(getattr(load_library(), f"moe_combine_grad_{t}"), args, (dC, Y, slots, weights, dY, dweights), stream)
 
 
 def moe_combine_grad_f16(T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream=None) -> None:
     """The gradient of moe_combine_f32: dY in fp16 (what the grouped products take) and dweights in fp32."""
-    _combine_grad("f16", "torch.float16", T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream)
+    _combine_grad("f16", "float16", T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream)
 
 
 def moe_combine_grad_bf16(T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream=None) -> None:
     """moe_combine_grad_f16 with dY in bf16."""
-    _combine_grad("bf16", "torch.bfloat16", T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream)
+    _combine_grad("bf16", "bfloat16", T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream)
 
 
+@functools.lru_cache(maxsize=1024)
 def gemm_lora_workspace(M, N, K, rank) -> int:
     """Bytes of workspace gemm_lora_f16_f32acc_ex and its bf16 form need."""
     return load_library().gemm_lora_workspace(M, N, K, rank)
@@ -466,25 +504,25 @@ def _lora(t, dtype_name, transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb,
     na, nb, nc = _needs(M, N, K, alpha, lda, ldb, ldc, transB=tB)
     thin = na > 0 and adapters > 0
     last = max(adapters - 1, 0)
-    args = (tB, M, N, K, rank, adapters, alpha, _ptr(A, "A", dtype_name, na), lda, _ptr(B, "B", dtype_name, nb), ldb,
-            _ptr(LA, "LA", dtype_name, _extent(rank, K, ldla) + last * strideLA if thin else 0), ldla, strideLA,
-            _ptr(LB, "LB", dtype_name, _extent(N, rank, ldlb) + last * strideLB if thin else 0), ldlb, strideLB,
-            _packed(scales, "scales", "torch.float32", adapters if thin else 0),
-            _packed(ranks, "ranks", "torch.int32", adapters if thin else 0),
-            _packed(ids, "ids", "torch.int32", M if thin else 0), beta, _ptr(C, "C", "torch.float32", nc), ldc)
+    args = (tB, M, N, K, rank, adapters, alpha, _strided(A, "A", dtype_name, na), lda, _strided(B, "B", dtype_name, nb), ldb,
+            _strided(LA, "LA", dtype_name, _extent(rank, K, ldla) + last * strideLA if thin else 0), ldla, strideLA,
+            _strided(LB, "LB", dtype_name, _extent(N, rank, ldlb) + last * strideLB if thin else 0), ldlb, strideLB,
+            _packed(scales, "scales", "float32", adapters if thin else 0),
+            _packed(ranks, "ranks", "int32", adapters if thin else 0),
+            _packed(ids, "ids", "int32", M if thin else 0), beta, _strided(C, "C", "float32", nc), ldc)
     need = gemm_lora_workspace(M, N, K, rank) if thin else 0
-    _call(f"gemm_lora_{t}_f32acc_ex", args, (A, B, LA, LB, scales, ranks, ids, C, workspace), stream, workspace, need)
+    _call(getattr(load_library(), f"gemm_lora_{t}_f32acc_ex"), args, (A, B, LA, LB, scales, ranks, ids, C, workspace), stream, workspace, need)
 
 
 def gemm_lora_f16_f32acc_ex(transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb, LA, ldla, strideLA, LB, ldlb, strideLB, scales,
                             ranks, ids, beta, C, ldc, workspace=None, stream=None) -> None:
     """C[i,:] <- alpha*(A[i,:]*op(B) + scales[a]*(A[i,:]*LA_a^T)*LB_a^T) + beta*C[i,:], a = ids[i]; fp16 inputs, fp32 C."""
-    _lora("f16", "torch.float16", transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb, LA, ldla, strideLA, LB, ldlb, strideLB,
+    _lora("f16", "float16", transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb, LA, ldla, strideLA, LB, ldlb, strideLB,
           scales, ranks, ids, beta, C, ldc, workspace, stream)
 
 
 def gemm_lora_bf16_f32acc_ex(transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb, LA, ldla, strideLA, LB, ldlb, strideLB,
                              scales, ranks, ids, beta, C, ldc, workspace=None, stream=None) -> None:
     """gemm_lora_f16_f32acc_ex with bf16 inputs."""
-    _lora("bf16", "torch.bfloat16", transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb, LA, ldla, strideLA, LB, ldlb, strideLB,
+    _lora("bf16", "bfloat16", transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb, LA, ldla, strideLA, LB, ldlb, strideLB,
           scales, ranks, ids, beta, C, ldc, workspace, stream)

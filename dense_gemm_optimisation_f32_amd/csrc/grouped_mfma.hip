@@ -6,71 +6,12 @@
 // any split of R rows over the groups can need, and each workgroup finds its
 // group and tile from the offsets; surplus workgroups return at once.
 #include "routed_internal.h"
-#include "stage16.h"
-#include "tile_order.h"
+#include "ragged_dma.h"
 
 #include <limits.h>
 
 namespace mi355gemm {
 namespace {
-
-// Group g's rows, clamped to [0, R] so that no offset leads outside C.
-__device__ __forceinline__ void group_rows(const int32_t *offsets, int g, int R, int *lo, int *hi)
-{
-    const int a = offsets[g], b = offsets[g + 1];
-    *lo = a < 0 ? 0 : a > R ? R : a;
-    *hi = b < *lo ? *lo : b > R ? R : b;
-}
-
-// The row tiles (of BM rows, per group) of all groups, counted in order:
-// `total` of them, and of tile `want` its group, first row and the group's end.
-// Every wave does this by itself, 64 groups at a time, one per lane.
-struct RowTile {
-    int group, first, end;
-};
-__device__ __forceinline__ int count_row_tiles(const int32_t *offsets, int groups, int R, int bm)
-{
-    const int lane = threadIdx.x & 63;
-    int total = 0;
-    for (int g0 = 0; g0 < groups; g0 += 64) {
-        int n = 0;
-        if (g0 + lane < groups) {
-            int lo, hi;
-            group_rows(offsets, g0 + lane, R, &lo, &hi);
-            n = (hi - lo + bm - 1) / bm;
-        }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) n += __shfl_xor(n, d);
-        total += n;
-    }
-    return __builtin_amdgcn_readfirstlane(total);
-}
-__device__ __forceinline__ RowTile find_row_tile(const int32_t *offsets, int groups, int R, int bm, int want)
-{
-    const int lane = threadIdx.x & 63;
-    for (int g0 = 0; g0 < groups; g0 += 64) {
-        int lo = 0, hi = 0, n = 0;
-        if (g0 + lane < groups) {
-            group_rows(offsets, g0 + lane, R, &lo, &hi);
-            n = (hi - lo + bm - 1) / bm;
-        }
-        int s = n;   // inclusive sum
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(s, d);
-            if (lane >= d) s += o;
-        }
-        const uint64_t hit = __ballot(want >= s - n && want < s);
-        if (hit) {
-            const int at = __builtin_ctzll(hit);
-            const int first = __shfl(lo + (want - (s - n)) * bm, at);
-            return {__builtin_amdgcn_readfirstlane(g0 + at), __builtin_amdgcn_readfirstlane(first),
-                    __builtin_amdgcn_readfirstlane(__shfl(hi, at))};
-        }
-        want -= __builtin_amdgcn_readfirstlane(__shfl(s, 63));
-    }
-    return {-1, 0, 0};
-}
 
 // Eight consecutive values from column c of a row of `cols` (nullptr: zeros),
 // wherever the row starts; columns at or past the end read as zero.
@@ -81,24 +22,6 @@ __device__ __forceinline__ u32x4 load8_row(const uint16_t *row, long long c, lon
     if (c + 8 > cols) return load8_masked(p, (int)(cols - c));
     return (reinterpret_cast<uintptr_t>(p) & 3) == 0 ? *reinterpret_cast<const u32x4_g *>(p) : load8_words(p);
 }
-
-struct RaggedArgs {
-    int groups, R, M, N, K;   // grouped: K columns of A; wgrad: M columns of A
-    float alpha, beta;
-    const uint16_t *A;
-    int a_rows;
-    long long lda;
-    const int32_t *rowsA;
-    const uint16_t *B;
-    int b_rows;               // wgrad
-    long long ldb, strideB;
-    const int32_t *rowsB;     // wgrad
-    const int32_t *offsets;
-    float *C;
-    long long ldc, strideC;
-    int tiles_m, tiles_n;
-    bool product;             // false: C is only scaled
-};
 
 // ---------------------------------------------------------------------------
 // The kernel for every shape, stride and alignment: 64x64 tiles of four waves,
@@ -282,38 +205,104 @@ long long most_row_tiles(int R, int groups, int bm)
     return R / bm + (groups < R ? groups : R);
 }
 
-}  // namespace
+bool dwords(const void *p, long long ld, long long stride)
+{
+    return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld % 2 == 0 && stride % 2 == 0;
+}
 
-hipError_t launch_grouped(const GroupedProblem &q, bool bf, hipStream_t stream)
+// The direct-to-LDS kernel takes these operands (see ragged_dma.h).
+bool grouped_dma_ok(const GroupedProblem &q)
+{
+    return q.K > 0 && q.K % 8 == 0 && (q.transB || q.N % 8 == 0) && dwords(q.A, q.lda, 0) && dwords(q.B, q.ldb, q.strideB) &&
+           256 * q.ldb * 2 < (1LL << 31);
+}
+bool wgrad_dma_ok(const WgradProblem &q)
+{
+    return q.R > 0 && q.M % 8 == 0 && q.N % 8 == 0 && dwords(q.A, q.lda, 0) && dwords(q.B, q.ldb, 0) &&
+           64 * q.lda * 2 < (1LL << 31) && 64 * q.ldb * 2 < (1LL << 31);
+}
+
+// Rounds of 256 workgroups that the tiles take, in the time of a 256x256 tile:
+// a 128x128 tile takes 0.4 of that, a 64x128 tile 0.25.
+double tile_rounds(double tiles, double each)
+{
+    return (double)(long long)((tiles + 255) / 256) * each;
+}
+
+template <class Cfg, bool BF, int KIND, bool TB, bool GA = false, bool GB = false>
+hipError_t launch_tiles(RaggedArgs a, long long row_tiles, int batch, hipStream_t stream)
+{
+    a.tiles_m = (int)row_tiles;
+    a.tiles_n = (a.N + Cfg::BN - 1) / Cfg::BN;
+    const long long tiles = row_tiles * a.tiles_n;
+    if (tiles > INT_MAX / Cfg::NT) return hipErrorInvalidValue;   // a grid holds fewer than 2^32 threads
+    hipLaunchKernelGGL((ragged_dma_kernel<Cfg, BF, KIND, TB, GA, GB>), dim3((unsigned)tiles, 1, batch), dim3(Cfg::NT), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <bool BF, bool TB>
+hipError_t grouped_tiles(const GroupedProblem &q, hipStream_t stream)
+{
+    const RaggedArgs a = grouped_args(q);
+    // tiles to expect: half of the part-filled ones
+    const double part = 0.5 * (q.groups < q.R ? q.groups : q.R);
+    const double n256 = (q.N + 255) / 256, n128 = (q.N + 127) / 128;
+    const double c256 = tile_rounds((q.R / 256.0 + part) * n256, 1.0);
+    const double c128 = tile_rounds((q.R / 128.0 + part) * n128, 0.4);
+    const double c64 = tile_rounds((q.R / 64.0 + part) * n128, 0.25);
+    if (c256 <= c128 && c256 <= c64) return launch_tiles<Ragged256, BF, kGrouped, TB>(a, most_row_tiles(q.R, q.groups, 256), 1, stream);
+    if (c128 <= c64) return launch_tiles<Ragged128, BF, kGrouped, TB>(a, most_row_tiles(q.R, q.groups, 128), 1, stream);
+    return launch_tiles<Ragged64, BF, kGrouped, TB>(a, most_row_tiles(q.R, q.groups, 64), 1, stream);
+}
+
+template <bool BF, bool TB>
+hipError_t grouped_any(const GroupedProblem &q, hipStream_t stream)
 {
     RaggedArgs a = grouped_args(q);
     a.tiles_n = (q.N + 63) / 64;
     const long long tiles = most_row_tiles(q.R, q.groups, 64) * a.tiles_n;
-    if (tiles > INT_MAX / 256) return hipErrorInvalidValue;   // a grid holds fewer than 2^32 threads
-    const dim3 grid((unsigned)tiles), block(256);
-    if (bf && q.transB)
-        hipLaunchKernelGGL((ragged_any_kernel<true, false, true>), grid, block, 0, stream, a);
-    else if (bf)
-        hipLaunchKernelGGL((ragged_any_kernel<true, false, false>), grid, block, 0, stream, a);
-    else if (q.transB)
-        hipLaunchKernelGGL((ragged_any_kernel<false, false, true>), grid, block, 0, stream, a);
-    else
-        hipLaunchKernelGGL((ragged_any_kernel<false, false, false>), grid, block, 0, stream, a);
+    if (tiles > INT_MAX / 256) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((ragged_any_kernel<BF, false, TB>), dim3((unsigned)tiles), dim3(256), 0, stream, a);
     return hipGetLastError();
+}
+
+template <bool BF>
+hipError_t wgrad(const WgradProblem &q, hipStream_t stream)
+{
+    RaggedArgs a = wgrad_args(q);
+    if (wgrad_dma_ok(q)) {
+        const double c256 = tile_rounds((double)((q.M + 255) / 256) * ((q.N + 255) / 256) * q.groups, 1.0);
+        const double c128 = tile_rounds((double)((q.M + 127) / 128) * ((q.N + 127) / 128) * q.groups, 0.4);
+        auto tiles = [&](auto ga, auto gb) {
+            constexpr bool GA = decltype(ga)::value, GB = decltype(gb)::value;
+            if (c256 <= c128) return launch_tiles<Ragged256, BF, kWgrad, false, GA, GB>(a, (q.M + 255) / 256, q.groups, stream);
+            return launch_tiles<Ragged128, BF, kWgrad, false, GA, GB>(a, (q.M + 127) / 128, q.groups, stream);
+        };
+        if (q.rowsA) return q.rowsB ? tiles(std::true_type{}, std::true_type{}) : tiles(std::true_type{}, std::false_type{});
+        return q.rowsB ? tiles(std::false_type{}, std::true_type{}) : tiles(std::false_type{}, std::false_type{});
+    }
+    a.tiles_m = (q.M + 63) / 64;
+    a.tiles_n = (q.N + 63) / 64;
+    if ((long long)a.tiles_m * a.tiles_n > INT_MAX / 256) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((ragged_any_kernel<BF, true, false>), dim3(a.tiles_m * a.tiles_n, 1, q.groups), dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_grouped(const GroupedProblem &q, bool bf, hipStream_t stream)
+{
+    if (grouped_dma_ok(q)) {
+        if (bf) return q.transB ? grouped_tiles<true, true>(q, stream) : grouped_tiles<true, false>(q, stream);
+        return q.transB ? grouped_tiles<false, true>(q, stream) : grouped_tiles<false, false>(q, stream);
+    }
+    if (bf) return q.transB ? grouped_any<true, true>(q, stream) : grouped_any<true, false>(q, stream);
+    return q.transB ? grouped_any<false, true>(q, stream) : grouped_any<false, false>(q, stream);
 }
 
 hipError_t launch_wgrad(const WgradProblem &q, bool bf, hipStream_t stream)
 {
-    RaggedArgs a = wgrad_args(q);
-    a.tiles_m = (q.M + 63) / 64;
-    a.tiles_n = (q.N + 63) / 64;
-    if ((long long)a.tiles_m * a.tiles_n > INT_MAX / 256 || q.groups > 65535) return hipErrorInvalidValue;
-    const dim3 grid(a.tiles_m * a.tiles_n, 1, q.groups), block(256);
-    if (bf)
-        hipLaunchKernelGGL((ragged_any_kernel<true, true, false>), grid, block, 0, stream, a);
-    else
-        hipLaunchKernelGGL((ragged_any_kernel<false, true, false>), grid, block, 0, stream, a);
-    return hipGetLastError();
+    return bf ? wgrad<true>(q, stream) : wgrad<false>(q, stream);
 }
 
 }  // namespace mi355gemm

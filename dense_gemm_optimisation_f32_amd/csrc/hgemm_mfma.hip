@@ -273,34 +273,6 @@ __global__ __launch_bounds__(256) void hgemm_mfma_kernel(HgemmArgs p)
 // one wave's MFMAs cover the other's LDS latency.
 // Requires M % BM == 0, N % BN == 0, K % BK == 0, K >= STAGES*BK, 16-byte
 // aligned rows and byte offsets within a slice below 2^31.
-template <int BM_, int BN_, int STAGES_, int WM_, int WN_, int BK_, bool SPLITS_ = false>
-struct HgDmaCfg {
-    static constexpr int BM = BM_, BN = BN_, BK = BK_, STAGES = STAGES_, WM = WM_, WN = WN_;
-    static constexpr bool SPLITS = SPLITS_;   // also built with a K split over workgroups
-    static constexpr int NW = WM * WN, NT = 64 * NW;
-    static constexpr int A_CPR = BK / 8;                        // 16-byte chunks per A row
-    static constexpr int TM = BM / WM, TN = BN / WN;
-    static constexpr int FM = TM / 32, FN = TN / 32;
-    static constexpr int A_BYTES = BM * BK * 2;                 // one A slice
-    static constexpr int B_BYTES = BK * BN * 2;                 // one B slice
-    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    // A 1 KB direct-to-LDS load occupies the CU's vector-memory path for about
-    // 16 cycles, and a wave blocked on issuing loads cannot issue MFMAs.  With
-    // a two-slot ring the upper half of the waves (one per SIMD) issues every
-    // load, right after the barrier that frees a slot, and the other wave on
-    // each SIMD keeps the matrix core busy meanwhile.  With three or more
-    // slots (STAGGER) every wave loads a share: the lower half right after the
-    // barrier, the upper half two substeps before the next one, into the slot
-    // that the previous barrier freed, so the two waves of a SIMD block on
-    // their loads at different times.
-    static constexpr bool STAGGER = STAGES >= 3;
-    static constexpr int LW = STAGGER ? NW : NW / 2;            // loading waves
-    static constexpr int A_LOADS = A_BYTES / 1024 / LW;         // per loading wave per slice
-    static constexpr int B_LOADS = B_BYTES / 1024 / LW;
-    static_assert(A_BYTES % (1024 * LW) == 0 && B_BYTES % (1024 * LW) == 0, "slices must split over the loaders");
-    static_assert(A_CPR == 4 || A_CPR == 8, "K-contiguous rows of 64 or 128 bytes");
-    static_assert(STAGES * STAGE_BYTES <= 160 * 1024, "LDS ring too large");
-};
 
 // TA: A stored K x M; TB: B stored N x K.  MASK: M and N need not be
 // multiples of the tile, nor K of BK (the loads clamp to valid rows and

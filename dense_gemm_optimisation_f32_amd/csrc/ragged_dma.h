@@ -1,0 +1,571 @@
+// ragged_dma.h -- tiles of products whose right operand is chosen per row, fed by
+// direct-to-LDS loads: ragged groups of rows (grouped_mfma.hip) and rows with
+// low-rank adapters (lora_mfma.hip).
+#pragma once
+
+#include "routed_internal.h"
+#include "stage16.h"
+#include "tile_order.h"
+
+#include <type_traits>
+#include <utility>
+
+namespace mi355gemm {
+namespace {
+
+// Group g's rows, clamped to [0, R] so that no offset leads outside C.
+__device__ __forceinline__ void group_rows(const int32_t *offsets, int g, int R, int *lo, int *hi)
+{
+    const int a = offsets[g], b = offsets[g + 1];
+    *lo = a < 0 ? 0 : a > R ? R : a;
+    *hi = b < *lo ? *lo : b > R ? R : b;
+}
+
+// The row tiles (of BM rows, per group) of all groups, counted in order:
+// `total` of them, and of tile `want` its group, first row and the group's end.
+// Every wave does this by itself, 64 groups at a time, one per lane.
+struct RowTile {
+    int group, first, end;
+};
+__device__ __forceinline__ int count_row_tiles(const int32_t *offsets, int groups, int R, int bm)
+{
+    const int lane = threadIdx.x & 63;
+    int total = 0;
+    for (int g0 = 0; g0 < groups; g0 += 64) {
+        int n = 0;
+        if (g0 + lane < groups) {
+            int lo, hi;
+            group_rows(offsets, g0 + lane, R, &lo, &hi);
+            n = (hi - lo + bm - 1) / bm;
+        }
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) n += __shfl_xor(n, d);
+        total += n;
+    }
+    return __builtin_amdgcn_readfirstlane(total);
+}
+__device__ __forceinline__ RowTile find_row_tile(const int32_t *offsets, int groups, int R, int bm, int want)
+{
+    const int lane = threadIdx.x & 63;
+    for (int g0 = 0; g0 < groups; g0 += 64) {
+        int lo = 0, hi = 0, n = 0;
+        if (g0 + lane < groups) {
+            group_rows(offsets, g0 + lane, R, &lo, &hi);
+            n = (hi - lo + bm - 1) / bm;
+        }
+        int s = n;   // inclusive sum
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(s, d);
+            if (lane >= d) s += o;
+        }
+        const uint64_t hit = __ballot(want >= s - n && want < s);
+        if (hit) {
+            const int at = __builtin_ctzll(hit);
+            const int first = __shfl(lo + (want - (s - n)) * bm, at);
+            return {__builtin_amdgcn_readfirstlane(g0 + at), __builtin_amdgcn_readfirstlane(first),
+                    __builtin_amdgcn_readfirstlane(__shfl(hi, at))};
+        }
+        want -= __builtin_amdgcn_readfirstlane(__shfl(s, 63));
+    }
+    return {-1, 0, 0};
+}
+
+// The adapters of the rows (lora): the narrow product t of each row as kParts<BF>
+// 16-bit parts whose sum is t / 2^e, and the row's factor scale * 2^e.
+struct AdapterArgs {
+    const int32_t *ids, *ranks;
+    int adapters, rank;
+    const uint16_t *LB;
+    long long ldlb, strideLB;
+    const uint16_t *parts;    // kParts x M x pitch
+    int pitch;                // halves per row: rank rounded up to 16
+    const float *factor;      // M
+};
+// Parts of a 32-bit value: 24 bits as 11-bit (fp16) or 8-bit (bf16) pieces.
+template <bool BF>
+constexpr int kParts = BF ? 3 : 2;
+
+__device__ __forceinline__ int adapter_of(const int32_t *ids, int adapters, int row, int M)
+{
+    const int a = row < M ? ids[row] : -1;
+    return a >= 0 && a < adapters ? a : -1;
+}
+__device__ __forceinline__ int rank_of(const int32_t *ranks, int rank, int a)
+{
+    const int r = ranks ? ranks[a] : rank;
+    return r < 0 ? 0 : r > rank ? rank : r;
+}
+
+// Eight values at p of which the first `valid` may be read; the others are zero.
+__device__ __forceinline__ half8 load8_any(const uint16_t *p, int valid)
+{
+    u32x4 v;
+    if (valid <= 0)
+        v = u32x4{0u, 0u, 0u, 0u};
+    else if (valid < 8)
+        v = load8_masked(p, valid);
+    else
+        v = (reinterpret_cast<uintptr_t>(p) & 3) == 0 ? *reinterpret_cast<const u32x4_g *>(p) : load8_words(p);
+    return __builtin_bit_cast(half8, v);
+}
+
+struct RaggedArgs {
+    int groups, R, M, N, K;   // grouped: K columns of A; wgrad: M columns of A
+    float alpha, beta;
+    const uint16_t *A;
+    int a_rows;
+    long long lda;
+    const int32_t *rowsA;
+    const uint16_t *B;
+    int b_rows;               // wgrad
+    long long ldb, strideB;
+    const int32_t *rowsB;     // wgrad
+    const int32_t *offsets;
+    float *C;
+    long long ldc, strideC;
+    int tiles_m, tiles_n;
+    bool product;             // false: C is only scaled
+    AdapterArgs ad;           // lora
+};
+
+// A direct-to-LDS load whose lanes each name a whole address (dma16 with one
+// base for all lanes is in stage16.h; the notes there hold here too).
+__device__ __forceinline__ void dma16_at(const void *p, unsigned lds_addr)
+{
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(p), "s"(lds_addr) : "memory", "m0");
+}
+
+// A pointer that is the same in every lane, in scalar registers (dma16's base).
+__device__ __forceinline__ const char *uniform(const char *p)
+{
+    const uint64_t b = reinterpret_cast<uint64_t>(p);
+    const uint64_t lo = (unsigned)__builtin_amdgcn_readfirstlane((int)b);
+    const uint64_t hi = (unsigned)__builtin_amdgcn_readfirstlane((int)(b >> 32));
+    return reinterpret_cast<const char *>(lo | (hi << 32));
+}
+
+// What a lane reads in place of a chunk outside its operand.
+__device__ const unsigned zero_chunk[4] = {0u, 0u, 0u, 0u};
+
+typedef const __attribute__((address_space(4))) int32_t *scalar_ints;   // read through the scalar cache
+
+enum RaggedKind { kGrouped, kWgrad, kLora };
+
+// ---------------------------------------------------------------------------
+// The ring, its loads and its K loop are those of the whole-matrix kernel
+// (hgemm_mfma.hip): slices of 64 k go straight from global memory into a ring of
+// STAGES LDS slots, and the MFMAs of one 16-k substep run while the next one's
+// fragments are read.  What differs is where rows come from:
+//   * kGrouped, kLora: a lane's rows of A are fixed for the whole K loop, so their
+//     addresses are formed once (rows[] looked up, clamped) and kept as pointers;
+//   * kWgrad: the k are the group's rows.  With rows[] each slice's addresses
+//     are formed from indices read by scalar loads one slice ahead; their counter is
+//     not the one the ring's waits count;
+//   * in a slice that the k range does not fill, chunks outside it are read from a
+//     16-byte block of zeros, so nothing past an operand is read and whatever lies
+//     between rows cannot reach a sum.  A group of fewer slices than the ring has
+//     slots loads such zeros for the missing ones.
+// Rows and columns of the tile outside the group or N re-read valid ones; their
+// results are not stored.
+// Needs: dword-aligned operand rows; K % 8 == 0 for K-contiguous operands and N (M) % 8
+// == 0 for the others, so that no 16-byte chunk straddles an edge; 64 (BN) rows of B
+// below 2^31 bytes apart.  K may be anything else.
+// TB: B stored N x K (not wgrad).  GA, GB: the rows of A, B are looked up (wgrad).
+template <class Cfg, bool BF, int KIND, bool TB, bool GA, bool GB>
+__global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
+{
+    constexpr int BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK, S = Cfg::STAGES;
+    constexpr bool WG = KIND == kWgrad;
+    constexpr bool A_KC = !WG, B_KC = !WG && TB;
+    static_assert((A_KC || BM >= 128) && (B_KC || BN >= 128), "MN-contiguous slices need 16 chunks per row");
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[S * Cfg::STAGE_BYTES];
+    const unsigned lds0 = (unsigned)(uintptr_t)lds;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+
+    int group = 0, m0, m_end, n0, K, k_lo = 0;   // K: this tile's k range [k_lo, k_lo + K)
+    if constexpr (KIND == kGrouped) {
+        const int total = count_row_tiles(p.offsets, p.groups, p.R, BM);
+        if ((long long)blockIdx.x >= (long long)total * p.tiles_n) return;
+        int one, tm, tn;
+        tile_coords((int)blockIdx.x, 0, 1, total, p.tiles_n, &one, &tm, &tn);
+        const RowTile rt = find_row_tile(p.offsets, p.groups, p.R, BM, tm);
+        if (rt.group < 0) return;
+        group = rt.group;
+        m0 = rt.first;
+        m_end = rt.end;
+        n0 = tn * BN;
+        K = p.K;
+    } else {
+        int tm, tn;
+        tile_coords(blockIdx.x, blockIdx.z, gridDim.z, p.tiles_m, p.tiles_n, &group, &tm, &tn);
+        m0 = tm * BM;
+        m_end = p.M;
+        n0 = tn * BN;
+        K = p.K;
+        if constexpr (WG) {
+            int hi;
+            group_rows(p.offsets, group, p.R, &k_lo, &hi);
+            k_lo = __builtin_amdgcn_readfirstlane(k_lo);
+            K = __builtin_amdgcn_readfirstlane(hi - k_lo);
+        }
+    }
+    const int N = p.N;
+    const long long lda = p.lda, ldb = p.ldb, ldc = p.ldc;
+    float *C = WG ? p.C + (long long)group * p.strideC : p.C;
+    const uint16_t *Bg = WG ? p.B : p.B + (long long)group * p.strideB;
+
+    const int uwave = __builtin_amdgcn_readfirstlane(wave);
+    const bool loader = uwave >= Cfg::NW - Cfg::LW;
+    const int lw = loader ? uwave - (Cfg::NW - Cfg::LW) : 0;
+    constexpr int A_LOADS = Cfg::A_LOADS, B_LOADS = Cfg::B_LOADS;
+    constexpr int LOADS = A_LOADS + B_LOADS;
+    const int limA = m_end - m0 < BM ? m_end - m0 : BM, limB = N - n0 < BN ? N - n0 : BN;
+
+    // K-contiguous A: the lane's chunk of each of its rows.
+    const uint16_t *rowA[A_KC ? A_LOADS : 1];
+    if constexpr (A_KC) {
+        constexpr int CPR = Cfg::A_CPR;
+#pragma unroll
+        for (int i = 0; i < A_LOADS; ++i) {
+            const int r = (64 / CPR) * (lw * A_LOADS + i) + lane / CPR;
+            int at = m0 + (r < limA ? r : limA - 1);
+            if (KIND == kGrouped && p.rowsA) at = p.rowsA[at];
+            if (at < 0 || at >= p.a_rows) at = 0;   // (its products are dropped in the epilogue)
+            rowA[i] = p.A + (long long)at * lda + 8 * ((lane % CPR) ^ swz_a<CPR>(r));
+        }
+    }
+    // Operands addressed from one base: byte offsets within a slice.
+    unsigned offA[A_KC ? 1 : A_LOADS], offB[B_LOADS];
+    if constexpr (!A_KC)
+#pragma unroll
+        for (int i = 0; i < A_LOADS; ++i) offA[i] = dma_offset<false, BM, BK, true>(lw * A_LOADS + i, lane, lda, limA);
+#pragma unroll
+    for (int i = 0; i < B_LOADS; ++i) offB[i] = dma_offset<B_KC, BN, BK, true>(lw * B_LOADS + i, lane, ldb, limB);
+    const long long stepA = BK * lda * 2, stepB = B_KC ? BK * 2 : BK * ldb * 2;
+    const char *Ab = reinterpret_cast<const char *>(p.A + (WG ? (long long)k_lo * lda + m0 : 0));
+    const char *Bb = reinterpret_cast<const char *>(Bg + (WG ? (long long)k_lo * ldb + n0 : B_KC ? (long long)n0 * ldb : n0));
+
+    // k (of the slice) and column chunk of load g of an MN-contiguous operand.
+    auto mn_k = [&](auto r, int g) -> int {
+        constexpr int CPR = decltype(r)::value / 8;
+        return (64 / CPR) * g + lane / CPR;
+    };
+    auto mn_col = [&](auto r, int g, int lim) -> int {
+        constexpr int CPR = decltype(r)::value / 8;
+        const int c = 8 * ((lane % CPR) ^ swz_b(mn_k(r, g)));
+        return c < lim ? c : 0;
+    };
+    // wgrad, rows looked up: the indices of this wave's k rows of one slice, by scalar
+    // loads all at once, one slice ahead of their use.  The lane then takes its row's.
+    constexpr int RPL_A = 64 / (BM / 8), RPL_B = 64 / (BN / 8);   // k rows per load: 2 or 4
+    // (vectors, so that they stay in registers)
+    typedef int IdxA __attribute__((ext_vector_type(A_LOADS * RPL_A)));
+    typedef int IdxB __attribute__((ext_vector_type(B_LOADS * RPL_B)));
+    IdxA idxA = {};
+    IdxB idxB = {};
+    auto fetch = [&](const int32_t *rows, auto &idx, auto count_c, int kt) __attribute__((always_inline)) {
+        constexpr int count = decltype(count_c)::value;
+        const int first = kt * BK + lw * count;
+        scalar_ints from = (scalar_ints)(const int32_t *)uniform((const char *)(rows + k_lo));
+        if (first + count <= K) {
+#pragma unroll
+            for (int j = 0; j < count; ++j) idx[j] = from[first + j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < count; ++j) idx[j] = from[first + j < K ? first + j : K - 1];
+        }
+    };
+    auto gathered = [&](auto r, const uint16_t *X, int cols0, long long ld, const auto &idx, int i, int x_rows, int kt, int g,
+                        int lim) __attribute__((always_inline)) -> const void * {
+        constexpr int RPL = 64 / (decltype(r)::value / 8);
+        const int sub = lane / (64 / RPL);
+        int at = idx[RPL * i];
+#pragma unroll
+        for (int j = 1; j < RPL; ++j) at = sub == j ? idx[RPL * i + j] : at;
+        const bool ok = kt * BK + RPL * g + sub < K && (unsigned)at < (unsigned)x_rows;
+        return ok ? (const void *)(X + (long long)at * ld + cols0 + mn_col(r, g, lim)) : (const void *)zero_chunk;
+    };
+    using RA = std::integral_constant<int, BM>;
+    using RB = std::integral_constant<int, BN>;
+    auto issue_slice = [&](int kt, int slot) __attribute__((always_inline)) {
+        if (!loader) return;
+        const unsigned la = __builtin_amdgcn_readfirstlane(lds0 + slot * Cfg::A_BYTES + lw * A_LOADS * 1024);
+        const unsigned lb = __builtin_amdgcn_readfirstlane(lds0 + S * Cfg::A_BYTES + slot * Cfg::B_BYTES + lw * B_LOADS * 1024);
+        const bool whole = (kt + 1) * BK <= K;
+        const char *b = uniform(Bb + (long long)kt * stepB);
+        if constexpr (!WG) {
+            if (whole) {
+#pragma unroll
+                for (int i = 0; i < A_LOADS; ++i) dma16_at(rowA[i] + (long long)kt * BK, la + 1024 * i);
+#pragma unroll
+                for (int i = 0; i < B_LOADS; ++i) dma16(b, offB[i], lb + 1024 * i);
+            } else {
+                constexpr int CPR = BK / 8;
+#pragma unroll
+                for (int i = 0; i < A_LOADS; ++i) {
+                    const int r = (64 / CPR) * (lw * A_LOADS + i) + lane / CPR;
+                    const int k = kt * BK + 8 * ((lane % CPR) ^ swz_a<CPR>(r));
+                    dma16_at(k < K ? (const void *)(rowA[i] + (long long)kt * BK) : (const void *)zero_chunk, la + 1024 * i);
+                }
+#pragma unroll
+                for (int i = 0; i < B_LOADS; ++i) {
+                    const int g = lw * B_LOADS + i;
+                    int k;
+                    if constexpr (B_KC) {
+                        const int r = (64 / CPR) * g + lane / CPR;
+                        k = kt * BK + 8 * ((lane % CPR) ^ swz_a<CPR>(r));
+                    } else {
+                        k = kt * BK + mn_k(RB{}, g);
+                    }
+                    dma16_at(k < K ? (const void *)(b + offB[i]) : (const void *)zero_chunk, lb + 1024 * i);
+                }
+            }
+        } else {
+            const char *a = Ab + (long long)kt * stepA;
+            // without an index array, row r of the group is row k_lo + r, inside the operand
+            auto plain = [&](auto r, const char *xb, const unsigned *off, auto loads_c, int x_rows, unsigned dst) __attribute__((always_inline)) {
+                constexpr int loads = decltype(loads_c)::value;
+                const char *x = uniform(xb);
+                if (whole && k_lo + (kt + 1) * BK <= x_rows) {
+#pragma unroll
+                    for (int i = 0; i < loads; ++i) dma16(x, off[i], dst + 1024 * i);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < loads; ++i) {
+                        const int k = kt * BK + mn_k(r, lw * loads + i);
+                        dma16_at(k < K && k_lo + k < x_rows ? (const void *)(x + off[i]) : (const void *)zero_chunk, dst + 1024 * i);
+                    }
+                }
+            };
+            if constexpr (GA) {
+#pragma unroll
+                for (int i = 0; i < A_LOADS; ++i)
+                    dma16_at(gathered(RA{}, p.A, m0, lda, idxA, i, p.a_rows, kt, lw * A_LOADS + i, limA), la + 1024 * i);
+                fetch(p.rowsA, idxA, std::integral_constant<int, A_LOADS * RPL_A>{}, kt + 1);
+            } else {
+                plain(RA{}, a, offA, std::integral_constant<int, A_LOADS>{}, p.a_rows, la);
+            }
+            if constexpr (GB) {
+#pragma unroll
+                for (int i = 0; i < B_LOADS; ++i)
+                    dma16_at(gathered(RB{}, p.B, n0, ldb, idxB, i, p.b_rows, kt, lw * B_LOADS + i, limB), lb + 1024 * i);
+                fetch(p.rowsB, idxB, std::integral_constant<int, B_LOADS * RPL_B>{}, kt + 1);
+            } else {
+                plain(RB{}, b, offB, std::integral_constant<int, B_LOADS>{}, p.b_rows, lb);
+            }
+        }
+    };
+
+    const int wm = wave / Cfg::WN, wn = wave % Cfg::WN;
+    const int lr = lane & 31, lk = lane >> 5;
+    constexpr int NS = BK / 16;
+    constexpr int NFA = A_KC ? NS : Cfg::FM, NFB = B_KC ? NS : Cfg::FN;
+    unsigned fragA[NFA], fragB[NFB];
+#pragma unroll
+    for (int x = 0; x < NFA; ++x)
+        fragA[x] = A_KC ? frag_offset<true, BM, BK>(wm * Cfg::TM, lane, x)
+                        : frag_offset<false, BM, BK>(wm * Cfg::TM + 32 * x, lane, 0);
+#pragma unroll
+    for (int x = 0; x < NFB; ++x)
+        fragB[x] = S * Cfg::A_BYTES + (B_KC ? frag_offset<true, BN, BK>(wn * Cfg::TN, lane, x)
+                                            : frag_offset<false, BN, BK>(wn * Cfg::TN + 32 * x, lane, 0));
+    f32x16 acc[Cfg::FM][Cfg::FN];
+#pragma unroll
+    for (int i = 0; i < Cfg::FM; ++i)
+#pragma unroll
+        for (int jj = 0; jj < Cfg::FN; ++jj)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][jj][r] = 0.f;
+    auto frag = [&](auto kc, auto rr, unsigned base, const unsigned *off, int x, int s) -> half8 {
+        constexpr int R = decltype(rr)::value;
+        if constexpr (decltype(kc)::value) {
+            return *(const lds_half8 *)(uintptr_t)(base + off[s] + x * 32 * BK * 2);
+        } else {
+            const unsigned at = base + off[x] + 16 * s * R * 2;
+            const short4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(uintptr_t)at);
+            const short4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(uintptr_t)(at + 4 * R * 2));
+            const short4v both[2] = {lo, hi};
+            return __builtin_bit_cast(half8, both);
+        }
+    };
+    half8 fa[2][Cfg::FM], fb[2][Cfg::FN];
+    auto read_frags = [&](int slot, int s, half8 *a, half8 *b) {
+        const unsigned base_a = lds0 + slot * Cfg::A_BYTES, base_b = lds0 + slot * Cfg::B_BYTES;
+#pragma unroll
+        for (int i = 0; i < Cfg::FM; ++i) a[i] = frag(std::bool_constant<A_KC>{}, RA{}, base_a, fragA, i, s);
+#pragma unroll
+        for (int jj = 0; jj < Cfg::FN; ++jj) b[jj] = frag(std::bool_constant<B_KC>{}, RB{}, base_b, fragB, jj, s);
+    };
+    auto mfmas = [&](const half8 *a, const half8 *b) {
+#pragma unroll
+        for (int i = 0; i < Cfg::FM; ++i)
+#pragma unroll
+            for (int jj = 0; jj < Cfg::FN; ++jj) acc[i][jj] = mfma16<BF>(b[jj], a[i], acc[i][jj]);
+    };
+    auto lds_barrier = [&]() {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    };
+    auto interleave = [&]() {
+#pragma unroll
+        for (int i = 0; i < Cfg::FM * Cfg::FN; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
+        }
+    };
+    const bool late = Cfg::STAGGER && uwave >= Cfg::NW / 2;
+    auto step_in = [&](int t, auto pending, auto refill, bool late_refill, auto slot_c) __attribute__((always_inline)) {
+        constexpr int SC = decltype(slot_c)::value;   // < 0: not known at compile time
+        const int slot = SC >= 0 ? SC : t % S;
+        const int next = SC >= 0 ? (SC + 1) % S : (t + 1) % S;
+        const int prev = SC >= 0 ? (SC + S - 1) % S : (t - 1 + S) % S;
+#pragma unroll
+        for (int sub = 0; sub < NS; ++sub) {
+            const int cur = sub & 1, nxt = cur ^ 1;
+            if (sub + 1 < NS) {
+                read_frags(slot, sub + 1, fa[nxt], fb[nxt]);
+                if (Cfg::STAGGER && sub == NS - 2 && late && late_refill) issue_slice(t - 1 + S, prev);
+            } else {
+                wait_vmcnt<LOADS * decltype(pending)::value>();
+                __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's slice-t reads are done
+                lds_barrier();
+                if (decltype(refill)::value && !late) issue_slice(t + S, slot);
+                read_frags(next, 0, fa[nxt], fb[nxt]);
+            }
+            mfmas(fa[cur], fb[cur]);
+            interleave();
+        }
+    };
+    auto step = [&](int t, auto pending, auto refill, bool late_refill) __attribute__((always_inline)) {
+        step_in(t, pending, refill, late_refill, std::integral_constant<int, -1>{});
+    };
+
+    if (K > 0) {   // (uniform)
+        // slices past the last are zeros: at least as many as the ring has slots
+        const int slices = (K + BK - 1) / BK, nk = slices < S ? S : slices;
+        if constexpr (WG) {
+            if constexpr (GA) fetch(p.rowsA, idxA, std::integral_constant<int, A_LOADS * RPL_A>{}, 0);
+            if constexpr (GB) fetch(p.rowsB, idxB, std::integral_constant<int, B_LOADS * RPL_B>{}, 0);
+        }
+#pragma unroll
+        for (int st = 0; st < S; ++st) issue_slice(st, st);
+        if constexpr (KIND == kLora) {
+            // The adapters first: of each distinct adapter of the wave's rows, LB's
+            // columns against the parts of those rows (zeros for the others), then every row
+            // by its factor; the K loop goes on from there.  The wave's own loads are
+            // waited for by the compiler's count, which only waits for more of the ring.
+            const AdapterArgs &ad = p.ad;
+            int aid[Cfg::FM];
+#pragma unroll
+            for (int i = 0; i < Cfg::FM; ++i)
+                aid[i] = ad.adapters > 0 ? adapter_of(ad.ids, ad.adapters, m0 + wm * Cfg::TM + 32 * i + lr, p.M) : -1;
+            int todo[Cfg::FM];
+#pragma unroll
+            for (int i = 0; i < Cfg::FM; ++i) todo[i] = aid[i];
+            for (;;) {
+                int a = -1;
+#pragma unroll
+                for (int i = Cfg::FM - 1; i >= 0; --i) {
+                    const uint64_t m = __ballot(todo[i] >= 0);
+                    if (m) a = __builtin_amdgcn_readlane(todo[i], __builtin_ctzll(m));
+                }
+                if (a < 0) break;
+                const int ra = rank_of(ad.ranks, ad.rank, a);
+                const uint16_t *lbase = ad.LB + (long long)a * ad.strideLB;
+                for (int k0 = 0; k0 < ra; k0 += 16) {
+                    const int kq = k0 + 8 * lk;
+                    half8 tb[Cfg::FN];
+#pragma unroll
+                    for (int jj = 0; jj < Cfg::FN; ++jj) {
+                        const int c = n0 + wn * Cfg::TN + 32 * jj + lr;
+                        tb[jj] = load8_any(lbase + (long long)(c < N ? c : N - 1) * ad.ldlb + kq, ra - kq);
+                    }
+#pragma unroll
+                    for (int part = 0; part < kParts<BF>; ++part) {
+                        half8 ta[Cfg::FM];
+#pragma unroll
+                        for (int i = 0; i < Cfg::FM; ++i) {
+                            const long long row = m0 + wm * Cfg::TM + 32 * i + lr;
+                            ta[i] = half8{};
+                            if (aid[i] == a)
+                                ta[i] = *reinterpret_cast<const half8 *>(ad.parts + ((long long)part * p.M + row) * ad.pitch + kq);
+                        }
+                        mfmas(ta, tb);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < Cfg::FM; ++i)
+                    if (todo[i] == a) todo[i] = -1;
+            }
+#pragma unroll
+            for (int i = 0; i < Cfg::FM; ++i) {
+                const float f = aid[i] >= 0 ? ad.factor[m0 + wm * Cfg::TM + 32 * i + lr] : 0.f;
+#pragma unroll
+                for (int jj = 0; jj < Cfg::FN; ++jj)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[i][jj][r] *= f;
+            }
+        }
+        wait_vmcnt<LOADS * (S - 1)>();
+        lds_barrier();
+        read_frags(0, 0, fa[0], fb[0]);
+        {
+            int t = 0;
+            constexpr bool UNROLL = BM >= 128 && !B_KC;   // (as in the whole-matrix kernel)
+            for (; UNROLL && t + S - 1 + S < nk; t += S) {
+                [&]<int... I>(std::integer_sequence<int, I...>) {
+                    (step_in(t + I, std::integral_constant<int, S - 2>{}, std::true_type{}, t + I >= 1,
+                             std::integral_constant<int, I>{}),
+                     ...);
+                }(std::make_integer_sequence<int, S>{});
+            }
+            for (; t + S < nk; ++t) step(t, std::integral_constant<int, S - 2>{}, std::true_type{}, t >= 1);
+        }
+        const int t0 = nk - S;
+        step(t0, std::integral_constant<int, S - 2>{}, std::false_type{}, t0 >= 1);
+        if constexpr (S >= 3) step(t0 + 1, std::integral_constant<int, S - 3>{}, std::false_type{}, false);
+        if constexpr (S >= 4) step(t0 + 2, std::integral_constant<int, S - 4>{}, std::false_type{}, false);
+        const int slot = (nk - 1) % S;
+#pragma unroll
+        for (int sub = 0; sub < NS; ++sub) {
+            const int cur = sub & 1, nxt = cur ^ 1;
+            if (sub + 1 < NS) read_frags(slot, sub + 1, fa[nxt], fb[nxt]);
+            mfmas(fa[cur], fb[cur]);
+        }
+    }
+
+    const float alpha = p.alpha, beta = p.beta;
+    auto epilogue = [&](auto with_c) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < Cfg::FM; ++i) {
+            const int row = m0 + wm * Cfg::TM + 32 * i + lr;
+            bool drop = false;   // a row index outside A: a row of zeros
+            if (KIND == kGrouped && row < m_end) {
+                const int at = p.rowsA ? p.rowsA[row] : row;
+                drop = at < 0 || at >= p.a_rows;
+            }
+#pragma unroll
+            for (int jj = 0; jj < Cfg::FN; ++jj)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    f32x4_t v = {acc[i][jj][4 * g], acc[i][jj][4 * g + 1], acc[i][jj][4 * g + 2], acc[i][jj][4 * g + 3]};
+                    if (KIND == kGrouped && drop) v = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                    store_row4<true, decltype(with_c)::value>(C, ldc, row, n0 + wn * Cfg::TN + 32 * jj + 8 * g + 4 * lk, v, alpha,
+                                                              beta, m_end, N);
+                }
+        }
+    };
+    if (beta != 0.f)
+        epilogue(std::true_type{});
+    else
+        epilogue(std::false_type{});
+}
+
+using Ragged256 = HgDmaCfg<256, 256, 2, 2, 4, 64>;
+using Ragged128 = HgDmaCfg<128, 128, 4, 2, 4, 64>;
+using Ragged64 = HgDmaCfg<64, 128, 4, 2, 4, 64>;   // K-contiguous A alone
+
+}  // namespace
+}  // namespace mi355gemm

@@ -536,31 +536,59 @@ __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
         }
     }
 
+    // Epilogue by rows: straight from the accumulators a store instruction would write
+    // 32 bytes of each of 32 rows; here each wave passes 32 rows at a time through its
+    // part of the ring (free once every wave is past the barrier) and writes whole row
+    // segments of its tile, TN * 4 bytes each.  16-byte chunk c of staged row r sits at
+    // chunk c ^ (r % LPR), which keeps both directions off each other's banks.
     const float alpha = p.alpha, beta = p.beta;
-    auto epilogue = [&](auto with_c) __attribute__((always_inline)) {
+    constexpr int LPR = Cfg::TN / 4, RPI = 64 / LPR, NQ = 32 / RPI;
+    static_assert(Cfg::NW * 32 * Cfg::TN * 4 <= S * Cfg::STAGE_BYTES, "staging area exceeds the ring");
+    const unsigned stage = lds0 + wave * 32 * Cfg::TN * 4;
+    lds_barrier();
+    const int er = lane / LPR, ec = lane % LPR;   // row and chunk within RPI rows
+    const int col = n0 + wn * Cfg::TN + 4 * ec;
 #pragma unroll
-        for (int i = 0; i < Cfg::FM; ++i) {
-            const int row = m0 + wm * Cfg::TM + 32 * i + lr;
-            bool drop = false;   // a row index outside A: a row of zeros
-            if (KIND == kGrouped && row < m_end) {
-                const int at = p.rowsA ? p.rowsA[row] : row;
-                drop = at < 0 || at >= p.a_rows;
+    for (int i = 0; i < Cfg::FM; ++i) {
+        const int first = m0 + wm * Cfg::TM + 32 * i;
+        if (first >= m_end) break;   // (uniform)
+#pragma unroll
+        for (int jj = 0; jj < Cfg::FN; ++jj)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x4_t v = {acc[i][jj][4 * g], acc[i][jj][4 * g + 1], acc[i][jj][4 * g + 2], acc[i][jj][4 * g + 3]};
+                *(lds_f32x4 *)(uintptr_t)(stage + lr * Cfg::TN * 4 + (((8 * jj + 2 * g + lk) ^ (lr & (LPR - 1))) * 16)) = v;
             }
+        // a wave's LDS accesses complete in order; this orders the compiler's too
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        f32x4_t v[NQ];
 #pragma unroll
-            for (int jj = 0; jj < Cfg::FN; ++jj)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    f32x4_t v = {acc[i][jj][4 * g], acc[i][jj][4 * g + 1], acc[i][jj][4 * g + 2], acc[i][jj][4 * g + 3]};
-                    if (KIND == kGrouped && drop) v = f32x4_t{0.f, 0.f, 0.f, 0.f};
-                    store_row4<true, decltype(with_c)::value>(C, ldc, row, n0 + wn * Cfg::TN + 32 * jj + 8 * g + 4 * lk, v, alpha,
-                                                              beta, m_end, N);
-                }
+        for (int q = 0; q < NQ; ++q) {
+            const int r = q * RPI + er;
+            v[q] = *(const lds_f32x4 *)(uintptr_t)(stage + r * Cfg::TN * 4 + ((ec ^ (r & (LPR - 1))) * 16));
         }
-    };
-    if (beta != 0.f)
-        epilogue(std::true_type{});
-    else
-        epilogue(std::false_type{});
+        if constexpr (KIND == kGrouped) {
+            // a row index outside A: a row of zeros
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                const int row = first + q * RPI + er;
+                const int at = p.rowsA && row < m_end ? p.rowsA[row] : row;
+                if (row < m_end && (unsigned)at >= (unsigned)p.a_rows) v[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            }
+        }
+        if (beta != 0.f) {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+                store_row4<true, true>(C, ldc, first + q * RPI + er, col, v[q], alpha, beta, m_end, N);
+        } else if (first + 32 <= m_end && n0 + BN <= N) {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) store_row4<false, false>(C, ldc, first + q * RPI + er, col, v[q], alpha, beta, m_end, N);
+        } else {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) store_row4<true, false>(C, ldc, first + q * RPI + er, col, v[q], alpha, beta, m_end, N);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
 }
 
 using Ragged256 = HgDmaCfg<256, 256, 2, 2, 4, 64>;

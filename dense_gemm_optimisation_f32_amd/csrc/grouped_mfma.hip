@@ -173,6 +173,13 @@ __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
     }
 }
 
+template <class Cfg, bool BF, bool TB>
+__global__ __launch_bounds__(Cfg::NT) void grouped_stream_kernel(RaggedArgs p)
+{
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[Cfg::LDS];
+    stream_tile<Cfg, BF, kGrouped, TB>(p, lds, blockIdx.x, 0, 1);
+}
+
 RaggedArgs grouped_args(const GroupedProblem &q)
 {
     RaggedArgs a = {};
@@ -240,10 +247,27 @@ hipError_t launch_tiles(RaggedArgs a, long long row_tiles, int batch, hipStream_
     return hipGetLastError();
 }
 
+template <class Cfg, bool BF, bool TB>
+hipError_t launch_stream(RaggedArgs a, hipStream_t stream)
+{
+    a.tiles_n = (a.N + Cfg::BN - 1) / Cfg::BN;
+    const long long tiles = most_row_tiles(a.R, a.groups, Cfg::BM) * a.tiles_n;
+    if (tiles > INT_MAX / Cfg::NT) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((grouped_stream_kernel<Cfg, BF, TB>), dim3((unsigned)tiles), dim3(Cfg::NT), 0, stream, a);
+    return hipGetLastError();
+}
+
 template <bool BF, bool TB>
 hipError_t grouped_tiles(const GroupedProblem &q, hipStream_t stream)
 {
     const RaggedArgs a = grouped_args(q);
+    const double rows = (double)q.R / q.groups;
+    // Few rows per group: the time is the weights', streamed.  32 columns a workgroup for weights
+    // stored N x K (two workgroups of 64 KB per CU; 64 groups x 2048 x 1024, 2 rows each: 56 us,
+    // against 66 with 64 columns), 64 for K x N, whose rows would otherwise be read 64 bytes at a
+    // time (53 against 58 us).  At 64 rows a group 128x128 and 64x128 tiles are as fast or faster
+    // (57 us against 78), at 32 the streaming is (58 against 61).
+    if (rows <= 32) return launch_stream<std::conditional_t<TB, StreamCfg<1, 1, 2, 4>, StreamCfg<1, 2, 3, 2>>, BF, TB>(a, stream);
     // tiles to expect: half of the part-filled ones
     const double part = 0.5 * (q.groups < q.R ? q.groups : q.R);
     const double n256 = (q.N + 255) / 256, n128 = (q.N + 127) / 128;

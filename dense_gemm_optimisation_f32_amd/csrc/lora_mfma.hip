@@ -1,8 +1,21 @@
 // lora_mfma.hip -- a shared projection with a low-rank adapter per row:
 //   C[i,:] = alpha (A[i,:] op(B) + scales[a] (A[i,:] LA_a^T) LB_a^T) + beta C[i,:],  a = ids[i]
-#include "routed_internal.h"
+//
+// The narrow product t = A LA^T is a few rank columns per row; it is kept in fp32
+// precision throughout.  Two ways:
+//   * up to 64 rows (decode), where the time is that of reading op(B) once: one
+//     launch streams op(B) (stream_tile, the K range shared by several workgroups)
+//     and, in further workgroups, forms t; a second adds up both, K share by K
+//     share, multiplies t by LB's columns in fp32 and writes C;
+//   * more rows: t first, split into 16-bit parts whose sum carries its 24 bits, then
+//     the tiles of ragged_dma.h, whose accumulators start from the parts times
+//     LB before the K loop.
+// Operands that direct-to-LDS loads cannot take (rows at odd halves, ragged
+// 16-byte chunks) run the library's GEMM, then t and the product with LB.
 #include "gemm_internal.h"
-#include "stage16.h"
+#include "ragged_dma.h"
+
+#include <limits.h>
 
 namespace mi355gemm {
 namespace {
@@ -27,116 +40,403 @@ __device__ __forceinline__ float widen16(uint16_t h)
     else
         return (float)__builtin_bit_cast(_Float16, h);
 }
-
-// Eight values at p of which the first `valid` may be read; the others are zero.
-__device__ __forceinline__ half8 load8_any(const uint16_t *p, int valid)
+template <bool BF>
+__device__ __forceinline__ uint16_t round16(float v)
 {
-    u32x4 v;
-    if (valid <= 0)
-        v = u32x4{0u, 0u, 0u, 0u};
-    else if (valid < 8)
-        v = load8_masked(p, valid);
+    if constexpr (BF)
+        return __builtin_bit_cast(uint16_t, (__bf16)v);
     else
-        v = (reinterpret_cast<uintptr_t>(p) & 3) == 0 ? *reinterpret_cast<const u32x4_g *>(p) : load8_words(p);
-    return __builtin_bit_cast(half8, v);
+        return __builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
-__device__ __forceinline__ int adapter_of(const LoraProblem &p, int row)
+// Workspace.  pitch: rank rounded up to 16.
+//   t: `shares` partial narrow products, each M x pitch fp32;
+//   parts: kParts<BF> x M x pitch 16-bit values, then M factors (tiles);
+//   sums: `splits` partial products, each M x N fp32 (decode).
+__host__ __device__ inline int rank_pitch(int rank)
 {
-    const int a = row < p.M ? p.ids[row] : -1;
-    return a >= 0 && a < p.adapters ? a : -1;
-}
-__device__ __forceinline__ int rank_of(const LoraProblem &p, int a)
-{
-    const int r = p.ranks ? p.ranks[a] : p.rank;
-    return r < 0 ? 0 : r > p.rank ? p.rank : r;
+    return (rank + 15) / 16 * 16;
 }
 
-// The narrow product t[i,:] = A[i,:] LA_a^T in 32 bits.  Block (b, j): the
-// 16 rows of row block b that use its j-th distinct adapter; surplus blocks
-// return.  The four waves share K and add up in wave order.
-constexpr int kTPitch = kMaxRank;   // floats per row of t
+struct NarrowArgs {
+    int M, K, adapters, rank, pitch;
+    const uint16_t *A;
+    long long lda;
+    const uint16_t *LA;
+    long long ldla, strideLA;
+    const float *scales;
+    const int32_t *ranks, *ids;
+    float *t;             // shares x M x pitch, or
+    uint16_t *parts;      // kParts x M x pitch with
+    float *factor;        // M
+};
 
-template <bool BF, int NR>
-__global__ __launch_bounds__(256) void lora_narrow_kernel(LoraProblem p)
+// The narrow product of the rows of 16-row block `rb` that use its `nth` distinct
+// adapter: t[i,:] = A[i,:] LA_a^T over share `share` of `shares` of K.  The NT / 64 waves
+// take chunks of 64 k in turn and add up in wave order.  PARTS: the whole K, t
+// rounded to 16-bit parts: of t / 2^e, 2^e such that the row's largest value is
+// near 2^14 (fp16, whose exponents a row's t may leave), e = 0 for bf16.
+template <bool BF, int NR, int NT, bool PARTS>
+__device__ __forceinline__ void narrow_block(const NarrowArgs &p, unsigned char *lds, int rb, int nth, int share, int shares)
 {
+    constexpr int NW = NT / 64;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, li = lane & 15, lq = lane >> 4;
-    const int row0 = blockIdx.x * 16;
-    const int mine = adapter_of(p, row0 + li);
+    const int row0 = rb * 16;
+    const int mine = adapter_of(p.ids, p.adapters, row0 + li, p.M);
     // lanes whose adapter no earlier row of the block has
     bool first = lane < 16 && mine >= 0;
+#pragma unroll
     for (int i = 0; i < 15; ++i) {
-        const int o = __shfl(mine, i);
+        const int o = __builtin_amdgcn_readlane(mine, i);
         if (i < lane && o == mine) first = false;
     }
     uint64_t firsts = __ballot(first);
-    for (int j = 0; j < (int)blockIdx.y && firsts; ++j) firsts &= firsts - 1;
+    for (int j = 0; j < nth && firsts; ++j) firsts &= firsts - 1;
     if (!firsts) return;
-    const int a = __builtin_amdgcn_readfirstlane(__shfl(mine, __builtin_ctzll(firsts)));
-    const int ra = rank_of(p, a);
+    const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(firsts));
+    const int ra = rank_of(p.ranks, p.rank, a);
     const uint16_t *la = p.LA + (long long)a * p.strideLA;
     const int row = row0 + li;
-    const uint16_t *x = row < p.M ? p.A + (long long)row * p.lda : nullptr;
+    const uint16_t *x = p.A + (long long)(row < p.M ? row : p.M - 1) * p.lda;
     f32x4v acc[NR];
 #pragma unroll
     for (int n = 0; n < NR; ++n) acc[n] = f32x4v{0.f, 0.f, 0.f, 0.f};
-    for (int k = 32 * wave; k < p.K; k += 128) {
-        const int kq = k + 8 * lq;
-        const half8 xb = x ? load8_any(x + kq, p.K - kq) : half8{};
+    const int blocks = (p.K + 63) / 64, turn = NW * shares;
+    // LA's rows that this lane loads; those past the adapter's rank are not read
+    const uint16_t *lrow[NR];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) lrow[n] = la + (long long)(16 * n + li) * p.ldla;
+    const bool vec = p.K % 64 == 0 && p.lda % 2 == 0 && p.ldla % 2 == 0 && reinterpret_cast<uintptr_t>(x) % 4 == 0 &&
+                     reinterpret_cast<uintptr_t>(la) % 4 == 0;
+    if (__builtin_amdgcn_readfirstlane(vec)) {
+#pragma unroll(NR > 2 ? 1 : 2)
+        for (int b = share * NW + wave; b < blocks; b += turn) {
+            half8 xb[2], f[2][NR];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int kq = 64 * b + 32 * h + 8 * lq;
+                xb[h] = __builtin_bit_cast(half8, *reinterpret_cast<const u32x4_g *>(x + kq));
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    u32x4 v = {0u, 0u, 0u, 0u};
+                    if (16 * n + li < ra) v = *reinterpret_cast<const u32x4_g *>(lrow[n] + kq);
+                    f[h][n] = __builtin_bit_cast(half8, v);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int n = 0; n < NR; ++n) acc[n] = mfma16x16<BF>(f[h][n], xb[h], acc[n]);
+        }
+    } else {
+        for (int b = share * NW + wave; b < blocks; b += turn)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int kq = 64 * b + 32 * h + 8 * lq;
+                const half8 xb = load8_any(x + kq, p.K - kq);
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+                    acc[n] = mfma16x16<BF>(load8_any(lrow[n] + kq, 16 * n + li < ra ? p.K - kq : 0), xb, acc[n]);
+            }
+    }
+    // lane: columns 16n + 4*lq .. +3 of row li
+    f32x4v *part = reinterpret_cast<f32x4v *>(lds);   // NW x NR x 64
+#pragma unroll
+    for (int n = 0; n < NR; ++n) part[(wave * NR + n) * 64 + lane] = acc[n];
+    __syncthreads();
+    if constexpr (!PARTS) {
+        if (mine != a) return;
+        for (int n = wave; n < NR; n += NW) {
+            if (16 * n >= p.pitch) break;
+            f32x4v s = part[n * 64 + lane];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) s += part[(w * NR + n) * 64 + lane];
+            *reinterpret_cast<f32x4v *>(p.t + ((long long)share * p.M + row) * p.pitch + 16 * n + 4 * lq) = s;
+        }
+    } else {
+        if (wave != 0) return;
+        f32x4v s[NR];
+        float most = 0.f;
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            const int j = 16 * n + li;
-            const half8 f = load8_any(la + (long long)j * p.ldla + kq, j < ra ? p.K - kq : 0);
-            acc[n] = mfma16x16<BF>(f, xb, acc[n]);
-        }
-    }
-    __shared__ f32x4v part[4][NR][64];
+            s[n] = part[n * 64 + lane];
 #pragma unroll
-    for (int n = 0; n < NR; ++n) part[wave][n][lane] = acc[n];
-    __syncthreads();
-    if (mine != a || row >= p.M) return;
-    for (int n = wave; n < NR; n += 4) {
-        const f32x4v s = (part[0][n][lane] + part[1][n][lane]) + (part[2][n][lane] + part[3][n][lane]);
-        *reinterpret_cast<f32x4v *>(p.t + (long long)row * kTPitch + 16 * n + 4 * lq) = s;
+            for (int w = 1; w < NW; ++w) s[n] += part[(w * NR + n) * 64 + lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) most = fmaxf(most, fabsf(s[n][e]));
+        }
+        most = fmaxf(most, __shfl_xor(most, 16));
+        most = fmaxf(most, __shfl_xor(most, 32));
+        int ex = 0;
+        if (!BF && most > 0.f && most < INFINITY) {
+            (void)frexpf(most, &ex);   // most = m 2^ex, 1/2 <= m < 1
+            ex -= 15;
+        }
+        if (mine != a) return;
+        if (lq == 0) p.factor[row] = ldexpf(p.scales ? p.scales[a] : 1.f, ex);
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            if (16 * n >= p.pitch) break;
+            float rest[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) rest[e] = BF ? s[n][e] : ldexpf(s[n][e], -ex);
+#pragma unroll
+            for (int part_i = 0; part_i < kParts<BF>; ++part_i) {
+                uint16_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    h[e] = round16<BF>(rest[e]);
+                    const float got = widen16<BF>(h[e]);
+                    rest[e] = got - got == 0.f ? rest[e] - got : 0.f;   // (infinities and NaN stand in the first part alone)
+                }
+                unsigned *dst = reinterpret_cast<unsigned *>(p.parts + ((long long)part_i * p.M + row) * p.pitch + 16 * n + 4 * lq);
+                dst[0] = h[0] | ((unsigned)h[1] << 16);
+                dst[1] = h[2] | ((unsigned)h[3] << 16);
+            }
+        }
     }
 }
 
-// C[i,n] += alpha * scale * sum_j t[i,j] LB_a[n,j].
+template <bool BF, int NR, bool PARTS>
+__global__ __launch_bounds__(512) void narrow_kernel(NarrowArgs p)
+{
+    __shared__ __attribute__((aligned(16))) unsigned char lds[8 * NR * 64 * 16];
+    narrow_block<BF, NR, 512, PARTS>(p, lds, blockIdx.x, blockIdx.y, 0, 1);
+}
+
+// Decode: the first `narrow` workgroups form t, the others stream op(B).
+template <class Cfg, bool BF, bool TB, int NR>
+__global__ __launch_bounds__(Cfg::NT) void decode_kernel(RaggedArgs base, NarrowArgs thin, int narrow, int slots, int shares,
+                                                         int tiles, int splits)
+{
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[Cfg::LDS];
+    static_assert((Cfg::NT / 64) * NR * 64 * 16 <= Cfg::LDS, "the narrow product's sums fit");
+    int b = blockIdx.x;
+    if (b < narrow) {
+        const int share = b % shares;
+        b /= shares;
+        narrow_block<BF, NR, Cfg::NT, false>(thin, lds, b / slots, b % slots, share, shares);
+        return;
+    }
+    b -= narrow;
+    stream_tile<Cfg, BF, kLora, TB>(base, lds, b / splits, b % splits, splits);
+    (void)tiles;
+}
+
+struct FinishArgs {
+    int M, N, adapters, rank, pitch, shares, splits;
+    float alpha, beta;
+    const uint16_t *LB;
+    long long ldlb, strideLB;
+    const float *scales, *t, *sums;   // sums: splits x M x N, or nullptr: C holds alpha A op(B) + beta C already
+    const int32_t *ranks, *ids;
+    float *C;
+    long long ldc;
+};
+
+// C[i,n] = alpha (sum of the products' shares + scale * sum_j t[i,j] LB_a[n,j]) + beta C[i,n].
+// A thread per column, a block per row and 256 columns.
 template <bool BF>
-__global__ __launch_bounds__(256) void lora_widen_kernel(LoraProblem p)
+__global__ __launch_bounds__(256) void finish_kernel(FinishArgs p)
 {
     const int row = blockIdx.y;
-    const int a = adapter_of(p, row);
-    if (a < 0) return;
-    const int ra = rank_of(p, a);
-    const float f = p.alpha * (p.scales ? p.scales[a] : 1.f);
+    const int a = adapter_of(p.ids, p.adapters, row, p.M);
+    if (a < 0 && p.sums == nullptr) return;
+    const int ra = a < 0 ? 0 : rank_of(p.ranks, p.rank, a);
     __shared__ float t[kMaxRank];
-    if ((int)threadIdx.x < ra) t[threadIdx.x] = p.t[(long long)row * kTPitch + threadIdx.x];
+    if ((int)threadIdx.x < ra) {
+        float s = 0.f;
+        for (int i = 0; i < p.shares; ++i) s += p.t[((long long)i * p.M + row) * p.pitch + threadIdx.x];
+        t[threadIdx.x] = s;
+    }
     __syncthreads();
     const int n = blockIdx.x * 256 + threadIdx.x;
     if (n >= p.N) return;
-    const uint16_t *b = p.LB + (long long)a * p.strideLB + (long long)n * p.ldlb;
-    float s = 0.f;
-    for (int j = 0; j < ra; ++j) s = __builtin_fmaf(t[j], widen16<BF>(b[j]), s);
     float *c = p.C + (long long)row * p.ldc + n;
-    *c = __builtin_fmaf(f, s, *c);
+    float base = 0.f;
+    if (p.sums)
+        for (int i = 0; i < p.splits; ++i) base += p.sums[((long long)i * p.M + row) * p.N + n];
+    float s = 0.f;
+    if (a >= 0) {
+        const uint16_t *b = p.LB + (long long)a * p.strideLB + (long long)n * p.ldlb;
+        for (int j = 0; j < ra; j += 8) {
+            const half8 h = load8_any(b + j, ra - j);
+            const int m = ra - j < 8 ? ra - j : 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const _Float16 v = h[e];   // (its 16 bits)
+                if (e < m) s = __builtin_fmaf(t[j + e], widen16<BF>(__builtin_bit_cast(uint16_t, v)), s);
+            }
+        }
+        s *= p.scales ? p.scales[a] : 1.f;
+    }
+    if (p.sums) {
+        const float v = p.alpha * (base + s);
+        *c = p.beta != 0.f ? __builtin_fmaf(p.beta, *c, v) : v;
+    } else {
+        *c = __builtin_fmaf(p.alpha, s, *c);
+    }
+}
+
+constexpr int kDecodeRows = 64;
+
+// Workgroups that share a strip's K range in decode, so that about 512 stream op(B):
+// at least one slice of 64 k for each of the four waves.
+int decode_splits(int N, int K)
+{
+    const int strips = (N + 31) / 32, most = (K + 255) / 256;
+    int s = (512 + strips - 1) / strips;
+    return s < 1 ? 1 : s > most ? most : s > 16 ? 16 : s;
+}
+// Workgroups that share K in a narrow product: 1024 k or more each.
+int narrow_shares(int K)
+{
+    const int s = K / 1024;
+    return s < 1 ? 1 : s > 8 ? 8 : s;
+}
+
+NarrowArgs narrow_args(const LoraProblem &p)
+{
+    NarrowArgs a = {};
+    a.M = p.M; a.K = p.K; a.adapters = p.adapters; a.rank = p.rank; a.pitch = rank_pitch(p.rank);
+    a.A = p.A; a.lda = p.lda;
+    a.LA = p.LA; a.ldla = p.ldla; a.strideLA = p.strideLA;
+    a.scales = p.scales; a.ranks = p.ranks; a.ids = p.ids;
+    a.t = p.t;
+    return a;
+}
+RaggedArgs base_args(const LoraProblem &p)
+{
+    RaggedArgs a = {};
+    a.M = p.M; a.N = p.N; a.K = p.K; a.a_rows = p.M;
+    a.alpha = p.alpha; a.beta = p.beta;
+    a.A = p.A; a.lda = p.lda;
+    a.B = p.B; a.ldb = p.ldb;
+    a.C = p.C; a.ldc = p.ldc;
+    return a;
+}
+FinishArgs finish_args(const LoraProblem &p)
+{
+    FinishArgs a = {};
+    a.M = p.M; a.N = p.N; a.adapters = p.adapters; a.rank = p.rank; a.pitch = rank_pitch(p.rank);
+    a.shares = 1; a.splits = 0;
+    a.alpha = p.alpha; a.beta = p.beta;
+    a.LB = p.LB; a.ldlb = p.ldlb; a.strideLB = p.strideLB;
+    a.scales = p.scales; a.ranks = p.ranks; a.ids = p.ids;
+    a.t = p.t;
+    a.C = p.C; a.ldc = p.ldc;
+    return a;
+}
+
+template <bool BF, bool PARTS>
+hipError_t launch_narrow(const LoraProblem &p, const NarrowArgs &a, hipStream_t stream)
+{
+    const dim3 grid((p.M + 15) / 16, p.adapters < 16 ? p.adapters : 16), block(512);
+    if (p.rank <= 16)
+        hipLaunchKernelGGL((narrow_kernel<BF, 1, PARTS>), grid, block, 0, stream, a);
+    else if (p.rank <= 32)
+        hipLaunchKernelGGL((narrow_kernel<BF, 2, PARTS>), grid, block, 0, stream, a);
+    else if (p.rank <= 64)
+        hipLaunchKernelGGL((narrow_kernel<BF, 4, PARTS>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((narrow_kernel<BF, 8, PARTS>), grid, block, 0, stream, a);
+    return hipGetLastError();
+}
+
+template <bool BF>
+hipError_t launch_finish(FinishArgs a, hipStream_t stream)
+{
+    const int M = a.M;
+    for (int r0 = 0; r0 < M; r0 += 65535) {   // (rows from r0 on: t and sums are indexed by the whole M, with one share beyond 64 rows)
+        FinishArgs q = a;
+        const int rows = M - r0 < 65535 ? M - r0 : 65535;
+        if (r0 > 0) {
+            q.M = M - r0;
+            q.ids += r0;
+            q.t += (long long)r0 * a.pitch;
+            q.C += (long long)r0 * a.ldc;
+        }
+        hipLaunchKernelGGL(finish_kernel<BF>, dim3((a.N + 255) / 256, rows), dim3(256), 0, stream, q);
+    }
+    return hipGetLastError();
+}
+
+bool dwords(const void *p, long long ld)
+{
+    return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld % 2 == 0;
+}
+bool lora_dma_ok(const LoraProblem &p)
+{
+    return p.K > 0 && p.K % 8 == 0 && (p.transB || p.N % 8 == 0) && dwords(p.A, p.lda) && dwords(p.B, p.ldb) &&
+           256 * p.ldb * 2 < (1LL << 31);
+}
+
+template <class Cfg, bool BF, bool TB>
+hipError_t launch_decode(const LoraProblem &p, hipStream_t stream)
+{
+    RaggedArgs base = base_args(p);
+    NarrowArgs thin = narrow_args(p);
+    const int splits = decode_splits(p.N, p.K), shares = narrow_shares(p.K);
+    float *sums = p.t + (size_t)shares * p.M * thin.pitch;
+    base.tiles_m = (p.M + Cfg::BM - 1) / Cfg::BM;
+    base.tiles_n = (p.N + Cfg::BN - 1) / Cfg::BN;
+    base.C = sums; base.ldc = p.N; base.strideC = (long long)p.M * p.N;
+    const int slots = p.adapters < 16 ? p.adapters : 16;
+    const int narrow = (p.M + 15) / 16 * slots * shares;
+    const int tiles = base.tiles_m * base.tiles_n;
+    const dim3 grid(narrow + tiles * splits), block(Cfg::NT);
+    auto run = [&](auto nr) {
+        hipLaunchKernelGGL((decode_kernel<Cfg, BF, TB, decltype(nr)::value>), grid, block, 0, stream, base, thin, narrow, slots,
+                           shares, tiles, splits);
+    };
+    if (p.rank <= 16)
+        run(std::integral_constant<int, 1>{});
+    else if (p.rank <= 32)
+        run(std::integral_constant<int, 2>{});
+    else if (p.rank <= 64)
+        run(std::integral_constant<int, 4>{});
+    else
+        run(std::integral_constant<int, 8>{});
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    FinishArgs f = finish_args(p);
+    f.shares = shares; f.splits = splits; f.sums = sums;
+    return launch_finish<BF>(f, stream);
+}
+
+template <class Cfg, bool BF, bool TB>
+hipError_t launch_tiles(RaggedArgs a, hipStream_t stream)
+{
+    a.tiles_m = (a.M + Cfg::BM - 1) / Cfg::BM;
+    a.tiles_n = (a.N + Cfg::BN - 1) / Cfg::BN;
+    const long long tiles = (long long)a.tiles_m * a.tiles_n;
+    if (tiles > INT_MAX / Cfg::NT) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((ragged_dma_kernel<Cfg, BF, kLora, TB, false, false>), dim3((unsigned)tiles), dim3(Cfg::NT), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <bool BF, bool TB>
+hipError_t lora_tiles(const LoraProblem &p, hipStream_t stream)
+{
+    NarrowArgs thin = narrow_args(p);
+    thin.parts = reinterpret_cast<uint16_t *>(p.t);
+    thin.factor = reinterpret_cast<float *>(thin.parts + (size_t)kParts<BF> * p.M * thin.pitch);
+    if (p.adapters > 0)
+        if (const hipError_t e = launch_narrow<BF, true>(p, thin, stream); e != hipSuccess) return e;
+    RaggedArgs a = base_args(p);
+    a.ad.ids = p.ids; a.ad.ranks = p.ranks; a.ad.adapters = p.adapters; a.ad.rank = p.rank;
+    a.ad.LB = p.LB; a.ad.ldlb = p.ldlb; a.ad.strideLB = p.strideLB;
+    a.ad.parts = thin.parts; a.ad.pitch = thin.pitch; a.ad.factor = thin.factor;
+    auto rounds = [&](int bm, int bn) { return (((p.M + bm - 1LL) / bm) * ((p.N + bn - 1LL) / bn) + 255) / 256; };
+    // in the time of a 256x256 tile: a 128x128 tile takes 0.4, a 64x128 tile 0.25
+    const double c256 = rounds(256, 256), c128 = 0.4 * rounds(128, 128), c64 = 0.25 * rounds(64, 128);
+    if (c256 <= c128 && c256 <= c64) return launch_tiles<Ragged256, BF, TB>(a, stream);
+    if (c128 <= c64) return launch_tiles<Ragged128, BF, TB>(a, stream);
+    return launch_tiles<Ragged64, BF, TB>(a, stream);
 }
 
 template <bool BF>
 hipError_t lora(const LoraProblem &p, hipStream_t stream)
 {
-    const dim3 ngrid((p.M + 15) / 16, p.adapters < 16 ? p.adapters : 16), block(256);
-    if (p.K > 0 && p.adapters > 0) {
-        if (p.rank <= 16)
-            hipLaunchKernelGGL((lora_narrow_kernel<BF, 1>), ngrid, block, 0, stream, p);
-        else if (p.rank <= 32)
-            hipLaunchKernelGGL((lora_narrow_kernel<BF, 2>), ngrid, block, 0, stream, p);
-        else if (p.rank <= 64)
-            hipLaunchKernelGGL((lora_narrow_kernel<BF, 4>), ngrid, block, 0, stream, p);
-        else
-            hipLaunchKernelGGL((lora_narrow_kernel<BF, 8>), ngrid, block, 0, stream, p);
-        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    }
     GemmProblem g = {};
     g.transB = p.transB;
     g.M = p.M; g.N = p.N; g.K = p.K; g.batch = 1;
@@ -144,24 +444,32 @@ hipError_t lora(const LoraProblem &p, hipStream_t stream)
     g.A = p.A; g.lda = p.lda;
     g.B = p.B; g.ldb = p.ldb;
     g.C = p.C; g.ldc = p.ldc;
-    const hipError_t e = p.K == 0 ? launch_scale_c(g, stream) : BF ? launch_bgemm(g, stream) : launch_hgemm(g, stream);
-    if (e != hipSuccess || p.K == 0 || p.adapters == 0) return e;
-    for (int r0 = 0; r0 < p.M; r0 += 65535) {
-        LoraProblem q = p;
-        q.M = p.M - r0 < 65535 ? p.M - r0 : 65535;
-        q.ids += r0;
-        q.C += (long long)r0 * p.ldc;
-        q.t += (long long)r0 * kTPitch;
-        hipLaunchKernelGGL(lora_widen_kernel<BF>, dim3((p.N + 255) / 256, q.M), block, 0, stream, q);
+    if (p.K == 0) return launch_scale_c(g, stream);
+    if (p.adapters > 0 && lora_dma_ok(p)) {
+        if (p.M <= 32) {
+            if (p.transB) return launch_decode<StreamCfg<1, 1, 2, 4>, BF, true>(p, stream);
+            return launch_decode<StreamCfg<1, 1, 2, 4>, BF, false>(p, stream);
+        }
+        if (p.M <= kDecodeRows) {
+            if (p.transB) return launch_decode<StreamCfg<2, 1, 2, 4>, BF, true>(p, stream);
+            return launch_decode<StreamCfg<2, 1, 2, 4>, BF, false>(p, stream);
+        }
+        return p.transB ? lora_tiles<BF, true>(p, stream) : lora_tiles<BF, false>(p, stream);
     }
-    return hipGetLastError();
+    const hipError_t e = BF ? launch_bgemm(g, stream) : launch_hgemm(g, stream);
+    if (e != hipSuccess || p.adapters == 0) return e;
+    if (const hipError_t n = launch_narrow<BF, false>(p, narrow_args(p), stream); n != hipSuccess) return n;
+    return launch_finish<BF>(finish_args(p), stream);
 }
 
 }  // namespace
 
-size_t lora_workspace(int M, int, int, int)
+size_t lora_workspace(int M, int N, int K, int rank)
 {
-    return (size_t)M * kTPitch * sizeof(float);
+    const size_t cells = (size_t)M * rank_pitch(rank);
+    if (M <= kDecodeRows)
+        return (cells * narrow_shares(K) + (size_t)M * N * decode_splits(N, K)) * sizeof(float);
+    return cells * 3 * sizeof(uint16_t) + (size_t)M * sizeof(float);   // at least the cells' fp32
 }
 
 hipError_t launch_lora(const LoraProblem &p, bool bf, hipStream_t stream)

@@ -484,15 +484,15 @@ __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
                     }
 #pragma unroll
                     for (int part = 0; part < kParts<BF>; ++part) {
-                        half8 ta[Cfg::FM];
 #pragma unroll
                         for (int i = 0; i < Cfg::FM; ++i) {
                             const long long row = m0 + wm * Cfg::TM + 32 * i + lr;
-                            ta[i] = half8{};
+                            half8 ta = {};
                             if (aid[i] == a)
-                                ta[i] = *reinterpret_cast<const half8 *>(ad.parts + ((long long)part * p.M + row) * ad.pitch + kq);
+                                ta = *reinterpret_cast<const half8 *>(ad.parts + ((long long)part * p.M + row) * ad.pitch + kq);
+#pragma unroll
+                            for (int jj = 0; jj < Cfg::FN; ++jj) acc[i][jj] = mfma16<BF>(tb[jj], ta, acc[i][jj]);
                         }
-                        mfmas(ta, tb);
                     }
                 }
 #pragma unroll
@@ -588,6 +588,221 @@ __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
             for (int q = 0; q < NQ; ++q) store_row4<true, false>(C, ldc, first + q * RPI + er, col, v[q], alpha, beta, m_end, N);
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: the weights are read once and multiplied by up to 32 FM rows, so the
+// time is that of streaming them.  A workgroup takes 32 FN columns; its NW waves
+// (and, lora, the gridDim.y workgroups of a strip) share the slices of 64 k in
+// turn.  Every wave has a ring of S slots of its own that only it loads and reads:
+// no barrier until the end, and S slices of loads in flight per wave.  The waves'
+// sums are added in wave order.
+//   kGrouped: C as in ragged_dma_kernel.  kLora: the plain sum of the
+//   workgroup's slices goes to C + blockIdx.y * strideC (workspace), lora's last
+//   kernel adds them up.
+// Needs what ragged_dma_kernel needs.
+constexpr int kStreamBK = 64;
+
+// XOR of an MN-contiguous slice's chunks in row k, rows of CPR chunks: the four rows
+// that a transposed read touches fall on different banks.
+template <int CPR>
+__device__ __forceinline__ int swz_n(int k)
+{
+    return CPR == 8 ? 2 * (k & 3) : (k & 2);
+}
+
+template <int FM_, int FN_, int S_, int NW_>
+struct StreamCfg {
+    static constexpr int FM = FM_, FN = FN_, S = S_, NW = NW_;
+    static constexpr int BM = 32 * FM, BN = 32 * FN, BK = kStreamBK, NT = 64 * NW;
+    static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE = A_BYTES + B_BYTES;
+    static constexpr int A_LOADS = A_BYTES / 1024, B_LOADS = B_BYTES / 1024, LOADS = A_LOADS + B_LOADS;
+    static constexpr int LDS = NW * S * STAGE;
+    static_assert(FN == 1 || FN == 2, "rows of four or eight chunks");
+    static_assert(NW * BM * BN * 4 <= LDS, "the waves' sums fit the rings");
+    static_assert(LDS <= 160 * 1024 && LOADS * S < 64, "LDS, outstanding loads");
+};
+
+template <class Cfg, bool BF, int KIND, bool TB>
+__device__ __forceinline__ void stream_tile(const RaggedArgs &p, unsigned char *lds, int block, int part, int parts)
+{
+    constexpr int FM = Cfg::FM, FN = Cfg::FN, S = Cfg::S, NW = Cfg::NW, BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK;
+    constexpr int A_LOADS = Cfg::A_LOADS, B_LOADS = Cfg::B_LOADS, LOADS = Cfg::LOADS;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int uwave = __builtin_amdgcn_readfirstlane(wave);
+    const unsigned lds0 = (unsigned)(uintptr_t)lds;
+
+    int group = 0, m0, m_end, n0;
+    {
+        int one, tm, tn;
+        if constexpr (KIND == kGrouped) {
+            const int total = count_row_tiles(p.offsets, p.groups, p.R, BM);
+            if ((long long)block >= (long long)total * p.tiles_n) return;
+            tile_coords(block, 0, 1, total, p.tiles_n, &one, &tm, &tn);
+            const RowTile rt = find_row_tile(p.offsets, p.groups, p.R, BM, tm);
+            if (rt.group < 0) return;
+            group = rt.group;
+            m0 = rt.first;
+            m_end = rt.end;
+        } else {
+            tile_coords(block, 0, 1, p.tiles_m, p.tiles_n, &one, &tm, &tn);
+            m0 = tm * BM;
+            m_end = p.M;
+        }
+        n0 = tn * BN;
+    }
+    const int N = p.N, K = p.K;
+    const long long lda = p.lda, ldb = p.ldb;
+    const uint16_t *Bg = p.B + (long long)group * p.strideB;
+    const int limA = m_end - m0 < BM ? m_end - m0 : BM, limB = N - n0 < BN ? N - n0 : BN;
+
+    // chunk addresses of slice 0
+    const uint16_t *rowA[A_LOADS];
+#pragma unroll
+    for (int i = 0; i < A_LOADS; ++i) {
+        const int r = 8 * i + lane / 8;
+        int at = m0 + (r < limA ? r : limA - 1);
+        if (KIND == kGrouped && p.rowsA) at = p.rowsA[at];
+        if ((unsigned)at >= (unsigned)p.a_rows) at = 0;   // (its products are dropped at the end)
+        rowA[i] = p.A + (long long)at * lda + 8 * ((lane % 8) ^ swz_a<8>(r));
+    }
+    constexpr int BCPR = BN / 8, BRPL = 64 / BCPR;   // MN-contiguous B: chunks per k row, k rows per load
+    unsigned offB[B_LOADS];
+#pragma unroll
+    for (int i = 0; i < B_LOADS; ++i) {
+        if constexpr (TB) {
+            const int r = 8 * i + lane / 8;
+            offB[i] = (unsigned)((r < limB ? r : limB - 1) * ldb + 8 * ((lane % 8) ^ swz_a<8>(r))) * 2u;
+        } else {
+            const int k = BRPL * i + lane / BCPR;
+            int c = 8 * ((lane % BCPR) ^ swz_n<BCPR>(k));
+            if (c >= limB) c = 0;
+            offB[i] = (unsigned)(k * ldb + c) * 2u;
+        }
+    }
+    const char *Bb = reinterpret_cast<const char *>(Bg + (TB ? (long long)n0 * ldb : n0));
+    const long long stepB = TB ? BK * 2 : BK * ldb * 2;
+    const unsigned ring = lds0 + uwave * S * Cfg::STAGE;
+    auto issue = [&](int s, int slot) __attribute__((always_inline)) {
+        const unsigned la = ring + slot * Cfg::STAGE, lb = la + Cfg::A_BYTES;
+        const char *b = uniform(Bb + (long long)s * stepB);
+        if ((s + 1) * BK <= K) {
+#pragma unroll
+            for (int i = 0; i < B_LOADS; ++i) dma16(b, offB[i], lb + 1024 * i);
+#pragma unroll
+            for (int i = 0; i < A_LOADS; ++i) dma16_at(rowA[i] + (long long)s * BK, la + 1024 * i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < B_LOADS; ++i) {
+                const int k = s * BK + (TB ? 8 * ((lane % 8) ^ swz_a<8>(8 * i + lane / 8)) : BRPL * i + lane / BCPR);
+                dma16_at(k < K ? (const void *)(b + offB[i]) : (const void *)zero_chunk, lb + 1024 * i);
+            }
+#pragma unroll
+            for (int i = 0; i < A_LOADS; ++i) {
+                const int k = s * BK + 8 * ((lane % 8) ^ swz_a<8>(8 * i + lane / 8));
+                dma16_at(k < K ? (const void *)(rowA[i] + (long long)s * BK) : (const void *)zero_chunk, la + 1024 * i);
+            }
+        }
+    };
+    // fragment addresses within a slot (see frag_offset; rows 32 apart per block)
+    const int lr = lane & 31, lk = lane >> 5, q = lane >> 4, j = lane & 15;
+    auto kc_frag = [&](unsigned base, int x, int s) -> half8 {
+        return *(const lds_half8 *)(uintptr_t)(base + (32 * x + lr) * BK * 2 + 16 * ((2 * s + lk) ^ swz_a<8>(lr)));
+    };
+    auto mn_frag = [&](unsigned base, int x, int s) -> half8 {
+        const int k = 16 * s + 8 * (q >> 1) + (j >> 2), n = 32 * x + 16 * (q & 1) + 4 * (j & 3);
+        const unsigned at = base + k * BN * 2 + 16 * ((n >> 3) ^ swz_n<BCPR>(k)) + 2 * (n & 7);
+        const short4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(uintptr_t)at);
+        const short4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(uintptr_t)(at + 4 * BN * 2));
+        const short4v both[2] = {lo, hi};
+        return __builtin_bit_cast(half8, both);
+    };
+
+    f32x16 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int x = 0; x < FN; ++x)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][x][r] = 0.f;
+
+    // this wave's slices: first, first + turn, ...
+    const int slices = (K + BK - 1) / BK, first = part * NW + uwave, turn = parts * NW;
+    const int ns = slices > first ? (slices - first + turn - 1) / turn : 0;
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+        if (i < ns) issue(first + i * turn, i);
+    auto compute = [&](int slot, bool refill, int s) __attribute__((always_inline)) {
+        const unsigned la = ring + slot * Cfg::STAGE, lb = la + Cfg::A_BYTES;
+        half8 fa[4][FM], fb[4][FN];
+#pragma unroll
+        for (int ss = 0; ss < 4; ++ss) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i) fa[ss][i] = kc_frag(la, i, ss);
+#pragma unroll
+            for (int x = 0; x < FN; ++x) fb[ss][x] = TB ? kc_frag(lb, x, ss) : mn_frag(lb, x, ss);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slot is read: it may be loaded again
+        if (refill) issue(s, slot);
+#pragma unroll
+        for (int ss = 0; ss < 4; ++ss)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int x = 0; x < FN; ++x) acc[i][x] = mfma16<BF>(fb[ss][x], fa[ss][i], acc[i][x]);
+    };
+    int i = 0, slot = 0;
+    for (; i + S < ns; ++i) {
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS * (S - 1)) : "memory");
+        compute(slot, true, first + (i + S) * turn);
+        slot = slot + 1 == S ? 0 : slot + 1;
+    }
+    for (; i < ns; ++i) {   // the last slices: everything has been issued
+        const int left = ns - 1 - i;
+        if (S > 2 && left >= 2)
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S > 2 ? LOADS * 2 : 0) : "memory");
+        else if (left == 1)
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        compute(slot, false, 0);
+        slot = slot + 1 == S ? 0 : slot + 1;
+    }
+    static_assert(S <= 3, "the last slices' waits");
+
+    // the waves' sums, 16-byte chunk c of row r at chunk c ^ (r % CH), added in wave order
+    constexpr int CH = BN / 4;   // chunks per row: 8 or 16
+    __syncthreads();             // every wave has left its ring
+#pragma unroll
+    for (int i2 = 0; i2 < FM; ++i2)
+#pragma unroll
+        for (int x = 0; x < FN; ++x)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int r = 32 * i2 + lr, c = 8 * x + 2 * g + lk;
+                const f32x4_t v = {acc[i2][x][4 * g], acc[i2][x][4 * g + 1], acc[i2][x][4 * g + 2], acc[i2][x][4 * g + 3]};
+                *(lds_f32x4 *)(uintptr_t)(lds0 + wave * BM * BN * 4 + r * BN * 4 + ((c ^ (r & (CH - 1))) * 16)) = v;
+            }
+    __syncthreads();
+    float *C = KIND == kLora ? p.C + (long long)part * p.strideC : p.C;
+    for (int e = tid; e < limA * CH; e += Cfg::NT) {
+        const int r = e / CH, c = e % CH;
+        f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+            v += *(const lds_f32x4 *)(uintptr_t)(lds0 + w * BM * BN * 4 + r * BN * 4 + ((c ^ (r & (CH - 1))) * 16));
+        const int row = m0 + r;
+        if constexpr (KIND == kGrouped) {
+            const int at = p.rowsA ? p.rowsA[row] : row;
+            if ((unsigned)at >= (unsigned)p.a_rows) v = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            if (p.beta != 0.f)
+                store_row4<true, true>(C, p.ldc, row, n0 + 4 * c, v, p.alpha, p.beta, m_end, N);
+            else
+                store_row4<true, false>(C, p.ldc, row, n0 + 4 * c, v, p.alpha, p.beta, m_end, N);
+        } else {
+            store_row4<true, false>(C, p.ldc, row, n0 + 4 * c, v, 1.f, 0.f, m_end, N);
+        }
     }
 }
 

@@ -307,69 +307,91 @@ def gemm_batched_bf16_f32acc_ex(transA, transB, M, N, K, alpha, A, lda, strideA,
 # ------------------------------------------------------------------ products whose right operand is chosen per row
 #
 # These calls serve single tokens, whose kernels take a few microseconds, so their
-# marshalling is kept short: one pass over an operand's properties, sizes of
-# workspaces remembered by the sizes they belong to.
+# marshalling is kept short: one test of an operand's properties where all is as
+# expected, sizes of workspaces remembered by the sizes they belong to.
 _torch = None
+_DTYPES = {}
+
+
+class _Elsewhere(Exception):
+    """An operand is on another device than the current one."""
+
+    def __init__(self, index: int):
+        self.index = index
 
 
 def _load_torch():
     global _torch
     import torch
 
+    _DTYPES.update(float32=torch.float32, float16=torch.float16, bfloat16=torch.bfloat16, int32=torch.int32)
     _torch = torch
     return torch
 
 
-def _strided(x, name: str, dtype_name: str, need: int):
-    """_ptr with a short way for a contiguous tensor that holds ``need`` elements."""
+def _on_operands_device(fn):
+    """Run ``fn`` with the device current that its tensors are on (one for all of them)."""
+
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        try:
+            return fn(*args, **kwargs)
+        except _Elsewhere as e:
+            index = e.index
+        with _torch.cuda.device(index):
+            try:
+                return fn(*args, **kwargs)
+            except _Elsewhere as e:
+                raise ValueError(f"{fn.__name__}: operands on more than one device: cuda:{index} and cuda:{e.index}") from None
+
+    return call
+
+
+def _strided(x, name: str, dtype_name: str, need: int, packed: bool = False):
+    """Device address of an operand of which the call reads or writes ``need`` elements (see _ptr); the short way is a
+    contiguous tensor that holds them."""
     if x is None or type(x) is int:
         return x
     torch = _torch or _load_torch()
-    if isinstance(x, torch.Tensor) and x.is_cuda and x.dtype is getattr(torch, dtype_name) and x.is_contiguous() and x.numel() >= need:
-        return x.data_ptr()
+    if isinstance(x, torch.Tensor):
+        dev = x.get_device()
+        if dev >= 0:
+            if dev != torch.cuda.current_device():
+                raise _Elsewhere(dev)
+            if x.is_contiguous():
+                if x.dtype is _DTYPES[dtype_name] and x.numel() >= need:
+                    return x.data_ptr()
+            elif packed:
+                raise ValueError(f"{name} must be contiguous")
     return _ptr(x, name, "torch." + dtype_name, need)
 
 
 def _packed(x, name: str, dtype_name: str, need: int):
     """Device address of an array the kernels read or write without strides."""
-    if x is None or type(x) is int:
-        return x
-    torch = _torch or _load_torch()
-    if isinstance(x, torch.Tensor) and x.is_cuda and not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return _strided(x, name, dtype_name, need)
+    return _strided(x, name, dtype_name, need, True)
 
 
-def _call(fn, args, operands, stream, workspace=None, workspace_bytes=None) -> None:
-    """Run library function ``fn`` on the device that holds ``operands`` (one for all of them): on ``stream``, or on
-    that device's current stream.  With ``workspace_bytes`` the call takes a workspace: the caller's, or one that torch's
-    allocator hands out for that stream (graph capture included) and takes back in its order."""
-    dev = -1
-    for x in operands:
-        if x is not None and type(x) is not int:
-            d = x.get_device()
-            if dev < 0:
-                dev = d
-            elif d != dev:
-                raise ValueError(f"{fn.__name__}: operands on more than one device: cuda:{dev} and cuda:{d}")
-    if dev < 0 and stream is not None and not (workspace_bytes and workspace is None):
-        rc = fn(*args, *(() if workspace_bytes is None else (workspace, workspace_bytes)), _stream(stream))   # addresses alone
-    else:
+def _call(fn, args, stream, workspace=None, workspace_bytes=None) -> None:
+    """Run library function ``fn`` on ``stream``, or on the current stream.  With ``workspace_bytes`` the call takes a
+    workspace: the caller's, or one that torch's allocator hands out for that stream (graph capture included) and
+    takes back in its order."""
+    if stream is None:
         torch = _torch or _load_torch()
-        here = torch.cuda.current_device()
-        if dev >= 0 and dev != here:
-            with torch.cuda.device(dev):
-                return _call(fn, args, operands, stream, workspace, workspace_bytes)
-        h = torch.cuda.current_stream(here).cuda_stream if stream is None else _stream(stream)
-        if workspace_bytes is None:
-            rc = fn(*args, h)
-        else:
-            if workspace is None and workspace_bytes > 0:
-                if stream is None:
+        h = torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    else:
+        h = _stream(stream)
+    if workspace_bytes is None:
+        rc = fn(*args, h)
+    else:
+        if workspace is None and workspace_bytes > 0:
+            torch = _torch or _load_torch()
+            if stream is None:
+                workspace = torch.empty(workspace_bytes, dtype=torch.uint8, device="cuda")
+            else:
+                with torch.cuda.stream(torch.cuda.ExternalStream(h)):
                     workspace = torch.empty(workspace_bytes, dtype=torch.uint8, device="cuda")
-                else:
-                    with torch.cuda.stream(torch.cuda.ExternalStream(h)):
-                        workspace = torch.empty(workspace_bytes, dtype=torch.uint8, device="cuda")
+            rc = fn(*args, workspace.data_ptr(), workspace_bytes, h)
+        else:
             rc = fn(*args, *_room(workspace, workspace_bytes), h)
     if rc != 0:
         raise GemmError(rc, fn.__name__)
@@ -379,6 +401,8 @@ def _room(workspace, need: int):
     """Address and bytes the library may use: what a tensor's storage holds from its start, or for a raw address what the call needs."""
     if workspace is None or type(workspace) is int:
         return workspace, need
+    if workspace.is_cuda and workspace.get_device() != (_torch or _load_torch()).cuda.current_device():
+        raise _Elsewhere(workspace.get_device())
     at = _ptr(workspace, "workspace", None, 0)
     st = workspace.untyped_storage()
     return at, st.nbytes() - (at - st.data_ptr())
@@ -390,6 +414,7 @@ def moe_route_workspace(T, E, k) -> int:
     return load_library().moe_route_workspace(T, E, k)
 
 
+@_on_operands_device
 def moe_route_f32(T, E, logits, ldl, bias, score, groups, group_k, group_top, k, renorm, scale, ids, weights, offsets=None,
                   rows=None, slots=None, workspace=None, stream=None) -> None:
     """Each of T tokens chooses k of E experts (ids, weights), and the choices sorted by expert (offsets, rows, slots)."""
@@ -399,16 +424,17 @@ def moe_route_f32(T, E, logits, ldl, bias, score, groups, group_k, group_top, k,
             _packed(weights, "weights", "float32", n), _packed(offsets, "offsets", "int32", E + 1),
             _packed(rows, "rows", "int32", n), _packed(slots, "slots", "int32", n))
     need = moe_route_workspace(T, E, k) if offsets is not None else 0
-    _call(load_library().moe_route_f32, args, (logits, bias, ids, weights, offsets, rows, slots, workspace), stream, workspace, need)
+    _call(load_library().moe_route_f32, args, stream, workspace, need)
 
 
+@_on_operands_device
 def moe_route_f32_grad(T, E, logits, ldl, score, k, renorm, scale, ids, dweights, dlogits, lddl, stream=None) -> None:
     """dlogits from dweights: the gradient of moe_route_f32's weights in its logits."""
     n = max(T, 0) * max(k, 0)
     args = (T, E, _strided(logits, "logits", "float32", _extent(T, E, ldl)), ldl, int(score), k, int(renorm), scale,
             _packed(ids, "ids", "int32", n), _packed(dweights, "dweights", "float32", n),
             _strided(dlogits, "dlogits", "float32", _extent(T, E, lddl)), lddl)
-    _call(load_library().moe_route_f32_grad, args, (logits, ids, dweights, dlogits), stream)
+    _call(load_library().moe_route_f32_grad, args, stream)
 
 
 def _grouped(t, dtype_name, transB, groups, R, N, K, alpha, A, M, lda, rows, B, ldb, strideB, offsets, beta, C, ldc, stream):
@@ -420,9 +446,10 @@ def _grouped(t, dtype_name, transB, groups, R, N, K, alpha, A, M, lda, rows, B, 
             _packed(rows, "rows", "int32", R if reads else 0), _strided(B, "B", dtype_name, b if reads else 0), ldb, strideB,
             _packed(offsets, "offsets", "int32", groups + 1 if work else 0), beta,
             _strided(C, "C", "float32", _extent(R, N, ldc)), ldc)
-    _call(getattr(load_library(), f"gemm_grouped_{t}_f32acc_ex"), args, (A, rows, B, offsets, C), stream)
+    _call(getattr(load_library(), f"gemm_grouped_{t}_f32acc_ex"), args, stream)
 
 
+@_on_operands_device
 def gemm_grouped_f16_f32acc_ex(transB, groups, R, N, K, alpha, A, M, lda, rows, B, ldb, strideB, offsets, beta, C, ldc,
                                stream=None) -> None:
     """C[r,:] <- alpha*A[rows[r],:]*op(B_g) + beta*C[r,:] for the rows r of every group g; fp16 A and B, fp32 C."""
@@ -430,6 +457,7 @@ def gemm_grouped_f16_f32acc_ex(transB, groups, R, N, K, alpha, A, M, lda, rows, 
              stream)
 
 
+@_on_operands_device
 def gemm_grouped_bf16_f32acc_ex(transB, groups, R, N, K, alpha, A, M, lda, rows, B, ldb, strideB, offsets, beta, C, ldc,
                                 stream=None) -> None:
     """gemm_grouped_f16_f32acc_ex with bf16 A and B."""
@@ -447,9 +475,10 @@ def _wgrad(t, dtype_name, groups, R, M, N, alpha, A, a_rows, lda, rowsA, B, b_ro
             _packed(rowsB, "rowsB", "int32", R if reads else 0),
             _packed(offsets, "offsets", "int32", groups + 1 if reads else 0), beta,
             _strided(C, "C", "float32", _extent(M, N, ldc) + (groups - 1) * strideC if work else 0), ldc, strideC)
-    _call(getattr(load_library(), f"gemm_grouped_wgrad_{t}_f32acc"), args, (A, rowsA, B, rowsB, offsets, C), stream)
+    _call(getattr(load_library(), f"gemm_grouped_wgrad_{t}_f32acc"), args, stream)
 
 
+@_on_operands_device
 def gemm_grouped_wgrad_f16_f32acc(groups, R, M, N, alpha, A, a_rows, lda, rowsA, B, b_rows, ldb, rowsB, offsets, beta, C, ldc,
                                   strideC, stream=None) -> None:
     """C_g <- alpha * sum over group g's rows r of A[rowsA[r],:]^T B[rowsB[r],:] + beta*C_g; fp16 A and B, fp32 C."""
@@ -457,6 +486,7 @@ def gemm_grouped_wgrad_f16_f32acc(groups, R, M, N, alpha, A, a_rows, lda, rowsA,
            strideC, stream)
 
 
+@_on_operands_device
 def gemm_grouped_wgrad_bf16_f32acc(groups, R, M, N, alpha, A, a_rows, lda, rowsA, B, b_rows, ldb, rowsB, offsets, beta, C, ldc,
                                    strideC, stream=None) -> None:
     """gemm_grouped_wgrad_f16_f32acc with bf16 A and B."""
@@ -464,13 +494,14 @@ def gemm_grouped_wgrad_bf16_f32acc(groups, R, M, N, alpha, A, a_rows, lda, rowsA
            strideC, stream)
 
 
+@_on_operands_device
 def moe_combine_f32(T, k, N, Y, R, ldy, slots, weights, beta, C, ldc, stream=None) -> None:
     """C[t,:] <- sum_j weights[t,j]*Y[slots[t,j],:] + beta*C[t,:] (weights None: ones)."""
     n = max(T, 0) * max(k, 0) if N > 0 else 0
     args = (T, k, N, _strided(Y, "Y", "float32", _extent(R, N, ldy) if n else 0), R, ldy,
             _packed(slots, "slots", "int32", n), _packed(weights, "weights", "float32", n), beta,
             _strided(C, "C", "float32", _extent(T, N, ldc)), ldc)
-    _call(load_library().moe_combine_f32, args, (Y, slots, weights, C), stream)
+    _call(load_library().moe_combine_f32, args, stream)
 
 
 def _combine_grad(t, dtype_name, T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream):
@@ -479,14 +510,16 @@ def _combine_grad(t, dtype_name, T, k, N, dC, lddc, Y, R, ldy, slots, weights, d
             _strided(Y, "Y", "float32", _extent(R, N, ldy) if n else 0), R, ldy, _packed(slots, "slots", "int32", n),
             _packed(weights, "weights", "float32", n), _strided(dY, "dY", dtype_name, _extent(R, N, lddy) if n else 0), lddy,
             _packed(dweights, "dweights", "float32", n))
-    _call(getattr(load_library(), f"moe_combine_grad_{t}"), args, (dC, Y, slots, weights, dY, dweights), stream)
+    _call(getattr(load_library(), f"moe_combine_grad_{t}"), args, stream)
 
 
+@_on_operands_device
 def moe_combine_grad_f16(T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream=None) -> None:
     """The gradient of moe_combine_f32: dY in fp16 (what the grouped products take) and dweights in fp32."""
     _combine_grad("f16", "float16", T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream)
 
 
+@_on_operands_device
 def moe_combine_grad_bf16(T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream=None) -> None:
     """moe_combine_grad_f16 with dY in bf16."""
     _combine_grad("bf16", "bfloat16", T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream)
@@ -511,9 +544,10 @@ def _lora(t, dtype_name, transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb,
             _packed(ranks, "ranks", "int32", adapters if thin else 0),
             _packed(ids, "ids", "int32", M if thin else 0), beta, _strided(C, "C", "float32", nc), ldc)
     need = gemm_lora_workspace(M, N, K, rank) if thin else 0
-    _call(getattr(load_library(), f"gemm_lora_{t}_f32acc_ex"), args, (A, B, LA, LB, scales, ranks, ids, C, workspace), stream, workspace, need)
+    _call(getattr(load_library(), f"gemm_lora_{t}_f32acc_ex"), args, stream, workspace, need)
 
 
+@_on_operands_device
 def gemm_lora_f16_f32acc_ex(transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb, LA, ldla, strideLA, LB, ldlb, strideLB, scales,
                             ranks, ids, beta, C, ldc, workspace=None, stream=None) -> None:
     """C[i,:] <- alpha*(A[i,:]*op(B) + scales[a]*(A[i,:]*LA_a^T)*LB_a^T) + beta*C[i,:], a = ids[i]; fp16 inputs, fp32 C."""
@@ -521,6 +555,7 @@ def gemm_lora_f16_f32acc_ex(transB, M, N, K, rank, adapters, alpha, A, lda, B, l
           scales, ranks, ids, beta, C, ldc, workspace, stream)
 
 
+@_on_operands_device
 def gemm_lora_bf16_f32acc_ex(transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb, LA, ldla, strideLA, LB, ldlb, strideLB,
                              scales, ranks, ids, beta, C, ldc, workspace=None, stream=None) -> None:
     """gemm_lora_f16_f32acc_ex with bf16 inputs."""

@@ -8,8 +8,8 @@
 //     and, in further workgroups, forms t; a second adds up both, K share by K
 //     share, multiplies t by LB's columns in fp32 and writes C;
 //   * more rows: t first, split into 16-bit parts whose sum carries its 24 bits, then
-//     the tiles of ragged_dma.h, whose accumulators start from the parts times
-//     LB before the K loop.
+//     the tiles of ragged_dma.h, which add the parts times LB's
+//     columns after the K loop.
 // Operands that direct-to-LDS loads cannot take (rows at odd halves, ragged
 // 16-byte chunks) run the library's GEMM, then t and the product with LB.
 #include "gemm_internal.h"
@@ -235,64 +235,87 @@ struct FinishArgs {
 };
 
 // C[i,n] = alpha (sum of the products' shares + scale * sum_j t[i,j] LB_a[n,j]) + beta C[i,n].
-// A thread per column, a block per row and 256 columns.
-template <bool BF>
-__global__ __launch_bounds__(256) void finish_kernel(FinishArgs p)
+// A thread per column, a block per row and NT columns.
+template <bool BF, int NT>
+__global__ __launch_bounds__(NT) void finish_kernel(FinishArgs p)
 {
     const int row = blockIdx.y;
     const int a = adapter_of(p.ids, p.adapters, row, p.M);
     if (a < 0 && p.sums == nullptr) return;
     const int ra = a < 0 ? 0 : rank_of(p.ranks, p.rank, a);
     __shared__ float t[kMaxRank];
-    if ((int)threadIdx.x < ra) {
+    for (int j = threadIdx.x; j < kMaxRank; j += NT) {
         float s = 0.f;
-        for (int i = 0; i < p.shares; ++i) s += p.t[((long long)i * p.M + row) * p.pitch + threadIdx.x];
-        t[threadIdx.x] = s;
+        if (j < ra)
+#pragma unroll 4
+            for (int i = 0; i < p.shares; ++i) s += p.t[((long long)i * p.M + row) * p.pitch + j];
+        t[j] = s;
     }
+    // (loads first: they do not depend on one another)
+    const int n = blockIdx.x * NT + threadIdx.x;
+    const int nc = n < p.N ? n : p.N - 1;
+    float base[4] = {0.f, 0.f, 0.f, 0.f};   // shares i, i + 4, ..., added in a fixed order
+    if (p.sums) {
+        const float *sum = p.sums + (long long)row * p.N + nc;
+        const long long apart = (long long)p.M * p.N;
+        for (int i = 0; i < p.splits; i += 4)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < p.splits) base[e] += sum[(i + e) * apart];
+    }
+    const uint16_t *b = p.LB + (a < 0 ? 0 : (long long)a * p.strideLB + (long long)nc * p.ldlb);
+    float *c = p.C + (long long)row * p.ldc + nc;
+    const float old = p.beta != 0.f || p.sums == nullptr ? *c : 0.f;
+    const float scale = a >= 0 && p.scales ? p.scales[a] : 1.f;
+    half8 h[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) h[x] = load8_any(b + 8 * x, ra - 8 * x);
     __syncthreads();
-    const int n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= p.N) return;
-    float *c = p.C + (long long)row * p.ldc + n;
-    float base = 0.f;
-    if (p.sums)
-        for (int i = 0; i < p.splits; ++i) base += p.sums[((long long)i * p.M + row) * p.N + n];
     float s = 0.f;
-    if (a >= 0) {
-        const uint16_t *b = p.LB + (long long)a * p.strideLB + (long long)n * p.ldlb;
-        for (int j = 0; j < ra; j += 8) {
-            const half8 h = load8_any(b + j, ra - j);
-            const int m = ra - j < 8 ? ra - j : 8;
+    for (int j = 0; j < ra; j += 16) {
+        half8 next[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) next[x] = load8_any(b + j + 16 + 8 * x, ra - j - 16 - 8 * x);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const _Float16 v = h[e];   // (its 16 bits)
-                if (e < m) s = __builtin_fmaf(t[j + e], widen16<BF>(__builtin_bit_cast(uint16_t, v)), s);
+                const _Float16 v = h[x][e];   // (its 16 bits; past the rank t and v are zero)
+                s = __builtin_fmaf(t[j + 8 * x + e], widen16<BF>(__builtin_bit_cast(uint16_t, v)), s);
             }
-        }
-        s *= p.scales ? p.scales[a] : 1.f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) h[x] = next[x];
     }
+    if (n >= p.N) return;
     if (p.sums) {
-        const float v = p.alpha * (base + s);
-        *c = p.beta != 0.f ? __builtin_fmaf(p.beta, *c, v) : v;
+        const float v = p.alpha * (((base[0] + base[1]) + (base[2] + base[3])) + s * scale);
+        *c = p.beta != 0.f ? __builtin_fmaf(p.beta, old, v) : v;
     } else {
-        *c = __builtin_fmaf(p.alpha, s, *c);
+        *c = __builtin_fmaf(p.alpha, s * scale, old);
     }
 }
 
 constexpr int kDecodeRows = 64;
 
-// Workgroups that share a strip's K range in decode, so that about 512 stream op(B):
-// at least one slice of 64 k for each of the four waves.
+// Workgroups that share a strip of 64 columns in decode, so that about 256 stream op(B) (4096 x 4096,
+// 48 rows: 18.7 us, with twice as many 23.1): at least two slices of 64 k for each of their two waves.
 int decode_splits(int N, int K)
 {
-    const int strips = (N + 31) / 32, most = (K + 255) / 256;
-    int s = (512 + strips - 1) / strips;
+    const int strips = (N + 63) / 64, most = (K + 255) / 256;
+    int s = (256 + strips - 1) / strips;
     return s < 1 ? 1 : s > most ? most : s > 16 ? 16 : s;
 }
-// Workgroups that share K in a narrow product: 1024 k or more each.
-int narrow_shares(int K)
+// Workgroups that share K in a narrow product, at most: 256 k or more each.
+int most_shares(int K)
 {
-    const int s = K / 1024;
-    return s < 1 ? 1 : s > 8 ? 8 : s;
+    const int s = K / 256;
+    return s < 1 ? 1 : s > 16 ? 16 : s;
+}
+// Distinct adapters that 16 rows can have.
+int row_block_adapters(const LoraProblem &p)
+{
+    const int rows = p.M < 16 ? p.M : 16;
+    return p.adapters < rows ? p.adapters : rows;
 }
 
 NarrowArgs narrow_args(const LoraProblem &p)
@@ -331,7 +354,7 @@ FinishArgs finish_args(const LoraProblem &p)
 template <bool BF, bool PARTS>
 hipError_t launch_narrow(const LoraProblem &p, const NarrowArgs &a, hipStream_t stream)
 {
-    const dim3 grid((p.M + 15) / 16, p.adapters < 16 ? p.adapters : 16), block(512);
+    const dim3 grid((p.M + 15) / 16, row_block_adapters(p)), block(512);
     if (p.rank <= 16)
         hipLaunchKernelGGL((narrow_kernel<BF, 1, PARTS>), grid, block, 0, stream, a);
     else if (p.rank <= 32)
@@ -356,7 +379,10 @@ hipError_t launch_finish(FinishArgs a, hipStream_t stream)
             q.t += (long long)r0 * a.pitch;
             q.C += (long long)r0 * a.ldc;
         }
-        hipLaunchKernelGGL(finish_kernel<BF>, dim3((a.N + 255) / 256, rows), dim3(256), 0, stream, q);
+        if (rows <= 8)   // (few rows: smaller blocks reach more CUs)
+            hipLaunchKernelGGL((finish_kernel<BF, 64>), dim3((a.N + 63) / 64, rows), dim3(64), 0, stream, q);
+        else
+            hipLaunchKernelGGL((finish_kernel<BF, 256>), dim3((a.N + 255) / 256, rows), dim3(256), 0, stream, q);
     }
     return hipGetLastError();
 }
@@ -376,12 +402,14 @@ hipError_t launch_decode(const LoraProblem &p, hipStream_t stream)
 {
     RaggedArgs base = base_args(p);
     NarrowArgs thin = narrow_args(p);
-    const int splits = decode_splits(p.N, p.K), shares = narrow_shares(p.K);
+    const int splits = decode_splits(p.N, p.K), slots = row_block_adapters(p), most = most_shares(p.K);
+    // about 256 workgroups for the narrow product beside as many that stream: two per CU
+    int shares = 256 / ((p.M + 15) / 16 * slots);
+    shares = shares < 1 ? 1 : shares > most ? most : shares;
     float *sums = p.t + (size_t)shares * p.M * thin.pitch;
     base.tiles_m = (p.M + Cfg::BM - 1) / Cfg::BM;
     base.tiles_n = (p.N + Cfg::BN - 1) / Cfg::BN;
     base.C = sums; base.ldc = p.N; base.strideC = (long long)p.M * p.N;
-    const int slots = p.adapters < 16 ? p.adapters : 16;
     const int narrow = (p.M + 15) / 16 * slots * shares;
     const int tiles = base.tiles_m * base.tiles_n;
     const dim3 grid(narrow + tiles * splits), block(Cfg::NT);
@@ -447,12 +475,12 @@ hipError_t lora(const LoraProblem &p, hipStream_t stream)
     if (p.K == 0) return launch_scale_c(g, stream);
     if (p.adapters > 0 && lora_dma_ok(p)) {
         if (p.M <= 32) {
-            if (p.transB) return launch_decode<StreamCfg<1, 1, 2, 4>, BF, true>(p, stream);
-            return launch_decode<StreamCfg<1, 1, 2, 4>, BF, false>(p, stream);
+            if (p.transB) return launch_decode<StreamCfg<1, 2, 3, 2>, BF, true>(p, stream);
+            return launch_decode<StreamCfg<1, 2, 3, 2>, BF, false>(p, stream);
         }
         if (p.M <= kDecodeRows) {
-            if (p.transB) return launch_decode<StreamCfg<2, 1, 2, 4>, BF, true>(p, stream);
-            return launch_decode<StreamCfg<2, 1, 2, 4>, BF, false>(p, stream);
+            if (p.transB) return launch_decode<StreamCfg<2, 2, 2, 2>, BF, true>(p, stream);
+            return launch_decode<StreamCfg<2, 2, 2, 2>, BF, false>(p, stream);
         }
         return p.transB ? lora_tiles<BF, true>(p, stream) : lora_tiles<BF, false>(p, stream);
     }
@@ -468,7 +496,7 @@ size_t lora_workspace(int M, int N, int K, int rank)
 {
     const size_t cells = (size_t)M * rank_pitch(rank);
     if (M <= kDecodeRows)
-        return (cells * narrow_shares(K) + (size_t)M * N * decode_splits(N, K)) * sizeof(float);
+        return (cells * most_shares(K) + (size_t)M * N * decode_splits(N, K)) * sizeof(float);
     return cells * 3 * sizeof(uint16_t) + (size_t)M * sizeof(float);   // at least the cells' fp32
 }
 

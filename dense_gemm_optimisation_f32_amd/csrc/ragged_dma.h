@@ -215,6 +215,15 @@ __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
     float *C = WG ? p.C + (long long)group * p.strideC : p.C;
     const uint16_t *Bg = WG ? p.B : p.B + (long long)group * p.strideB;
 
+    const int wm = wave / Cfg::WN, wn = wave % Cfg::WN;
+    const int lr = lane & 31, lk = lane >> 5;
+    f32x16 acc[Cfg::FM][Cfg::FN];
+#pragma unroll
+    for (int i = 0; i < Cfg::FM; ++i)
+#pragma unroll
+        for (int jj = 0; jj < Cfg::FN; ++jj)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][jj][r] = 0.f;
     const int uwave = __builtin_amdgcn_readfirstlane(wave);
     const bool loader = uwave >= Cfg::NW - Cfg::LW;
     const int lw = loader ? uwave - (Cfg::NW - Cfg::LW) : 0;
@@ -357,8 +366,6 @@ __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
         }
     };
 
-    const int wm = wave / Cfg::WN, wn = wave % Cfg::WN;
-    const int lr = lane & 31, lk = lane >> 5;
     constexpr int NS = BK / 16;
     constexpr int NFA = A_KC ? NS : Cfg::FM, NFB = B_KC ? NS : Cfg::FN;
     unsigned fragA[NFA], fragB[NFB];
@@ -370,13 +377,6 @@ __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
     for (int x = 0; x < NFB; ++x)
         fragB[x] = S * Cfg::A_BYTES + (B_KC ? frag_offset<true, BN, BK>(wn * Cfg::TN, lane, x)
                                             : frag_offset<false, BN, BK>(wn * Cfg::TN + 32 * x, lane, 0));
-    f32x16 acc[Cfg::FM][Cfg::FN];
-#pragma unroll
-    for (int i = 0; i < Cfg::FM; ++i)
-#pragma unroll
-        for (int jj = 0; jj < Cfg::FN; ++jj)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][jj][r] = 0.f;
     auto frag = [&](auto kc, auto rr, unsigned base, const unsigned *off, int x, int s) -> half8 {
         constexpr int R = decltype(rr)::value;
         if constexpr (decltype(kc)::value) {
@@ -451,63 +451,6 @@ __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
         }
 #pragma unroll
         for (int st = 0; st < S; ++st) issue_slice(st, st);
-        if constexpr (KIND == kLora) {
-            // The adapters first: of each distinct adapter of the wave's rows, LB's
-            // columns against the parts of those rows (zeros for the others), then every row
-            // by its factor; the K loop goes on from there.  The wave's own loads are
-            // waited for by the compiler's count, which only waits for more of the ring.
-            const AdapterArgs &ad = p.ad;
-            int aid[Cfg::FM];
-#pragma unroll
-            for (int i = 0; i < Cfg::FM; ++i)
-                aid[i] = ad.adapters > 0 ? adapter_of(ad.ids, ad.adapters, m0 + wm * Cfg::TM + 32 * i + lr, p.M) : -1;
-            int todo[Cfg::FM];
-#pragma unroll
-            for (int i = 0; i < Cfg::FM; ++i) todo[i] = aid[i];
-            for (;;) {
-                int a = -1;
-#pragma unroll
-                for (int i = Cfg::FM - 1; i >= 0; --i) {
-                    const uint64_t m = __ballot(todo[i] >= 0);
-                    if (m) a = __builtin_amdgcn_readlane(todo[i], __builtin_ctzll(m));
-                }
-                if (a < 0) break;
-                const int ra = rank_of(ad.ranks, ad.rank, a);
-                const uint16_t *lbase = ad.LB + (long long)a * ad.strideLB;
-                for (int k0 = 0; k0 < ra; k0 += 16) {
-                    const int kq = k0 + 8 * lk;
-                    half8 tb[Cfg::FN];
-#pragma unroll
-                    for (int jj = 0; jj < Cfg::FN; ++jj) {
-                        const int c = n0 + wn * Cfg::TN + 32 * jj + lr;
-                        tb[jj] = load8_any(lbase + (long long)(c < N ? c : N - 1) * ad.ldlb + kq, ra - kq);
-                    }
-#pragma unroll
-                    for (int part = 0; part < kParts<BF>; ++part) {
-#pragma unroll
-                        for (int i = 0; i < Cfg::FM; ++i) {
-                            const long long row = m0 + wm * Cfg::TM + 32 * i + lr;
-                            half8 ta = {};
-                            if (aid[i] == a)
-                                ta = *reinterpret_cast<const half8 *>(ad.parts + ((long long)part * p.M + row) * ad.pitch + kq);
-#pragma unroll
-                            for (int jj = 0; jj < Cfg::FN; ++jj) acc[i][jj] = mfma16<BF>(tb[jj], ta, acc[i][jj]);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < Cfg::FM; ++i)
-                    if (todo[i] == a) todo[i] = -1;
-            }
-#pragma unroll
-            for (int i = 0; i < Cfg::FM; ++i) {
-                const float f = aid[i] >= 0 ? ad.factor[m0 + wm * Cfg::TM + 32 * i + lr] : 0.f;
-#pragma unroll
-                for (int jj = 0; jj < Cfg::FN; ++jj)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[i][jj][r] *= f;
-            }
-        }
         wait_vmcnt<LOADS * (S - 1)>();
         lds_barrier();
         read_frags(0, 0, fa[0], fb[0]);
@@ -546,12 +489,61 @@ __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
     static_assert(Cfg::NW * 32 * Cfg::TN * 4 <= S * Cfg::STAGE_BYTES, "staging area exceeds the ring");
     const unsigned stage = lds0 + wave * 32 * Cfg::TN * 4;
     lds_barrier();
+    // The adapters of 32 rows: for each distinct one, LB's columns against the parts of its
+    // rows (zeros for the others); then every row by its factor.  Here, where the
+    // K loop's registers are free: before the loop its accumulators spilled.
+    const AdapterArgs &ad = p.ad;
+    int aid[Cfg::FM];
+    if constexpr (KIND == kLora)
+#pragma unroll
+        for (int i = 0; i < Cfg::FM; ++i)
+            aid[i] = ad.adapters > 0 ? adapter_of(ad.ids, ad.adapters, m0 + wm * Cfg::TM + 32 * i + lr, p.M) : -1;
+    auto add_adapters = [&](int first, int mine, f32x16 *sums) __attribute__((always_inline)) {
+        const long long row = first + lr;
+        const float f = mine >= 0 ? ad.factor[row] : 0.f;
+        f32x16 add[Cfg::FN];
+#pragma unroll
+        for (int jj = 0; jj < Cfg::FN; ++jj)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) add[jj][r] = 0.f;
+        int todo = mine;
+        for (uint64_t left = __ballot(todo >= 0); left; left = __ballot(todo >= 0)) {
+            const int a = __builtin_amdgcn_readlane(todo, __builtin_ctzll(left));
+            const int ra = rank_of(ad.ranks, ad.rank, a);
+            const uint16_t *lb = ad.LB + (long long)a * ad.strideLB;
+            for (int k0 = 0; k0 < ra; k0 += 16) {
+                const int kq = k0 + 8 * lk;
+                half8 ta[kParts<BF>], tb[Cfg::FN];
+#pragma unroll
+                for (int part = 0; part < kParts<BF>; ++part) {
+                    ta[part] = half8{};
+                    if (mine == a)
+                        ta[part] = *reinterpret_cast<const half8 *>(ad.parts + ((long long)part * p.M + row) * ad.pitch + kq);
+                }
+#pragma unroll
+                for (int jj = 0; jj < Cfg::FN; ++jj) {
+                    const int c = n0 + wn * Cfg::TN + 32 * jj + lr;
+                    tb[jj] = load8_any(lb + (long long)(c < N ? c : N - 1) * ad.ldlb + kq, ra - kq);
+                }
+#pragma unroll
+                for (int part = 0; part < kParts<BF>; ++part)
+#pragma unroll
+                    for (int jj = 0; jj < Cfg::FN; ++jj) add[jj] = mfma16<BF>(tb[jj], ta[part], add[jj]);
+            }
+            if (todo == a) todo = -1;
+        }
+#pragma unroll
+        for (int jj = 0; jj < Cfg::FN; ++jj)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sums[jj][r] = __builtin_fmaf(f, add[jj][r], sums[jj][r]);
+    };
     const int er = lane / LPR, ec = lane % LPR;   // row and chunk within RPI rows
     const int col = n0 + wn * Cfg::TN + 4 * ec;
 #pragma unroll
     for (int i = 0; i < Cfg::FM; ++i) {
         const int first = m0 + wm * Cfg::TM + 32 * i;
         if (first >= m_end) break;   // (uniform)
+        if constexpr (KIND == kLora) add_adapters(first, aid[i], acc[i]);
 #pragma unroll
         for (int jj = 0; jj < Cfg::FN; ++jj)
 #pragma unroll

@@ -356,7 +356,7 @@ def _strided(x, name: str, dtype_name: str, need: int, packed: bool = False):
     if isinstance(x, torch.Tensor):
         dev = x.get_device()
         if dev >= 0:
-            if dev != torch.cuda.current_device():
+            if dev != torch._C._cuda_getDevice():
                 raise _Elsewhere(dev)
             if x.is_contiguous():
                 if x.dtype is _DTYPES[dtype_name] and x.numel() >= need:

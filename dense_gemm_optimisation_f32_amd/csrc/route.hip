@@ -97,6 +97,39 @@ __device__ __forceinline__ uint64_t logit_key(float c)
     return (uint64_t)((b >> 31) ? ~b : (b | 0x80000000u)) << 32;
 }
 
+// A 32-bit score as such a key, without the NaN case; and back.
+__device__ __forceinline__ unsigned key32(float c)
+{
+    const unsigned b = __builtin_bit_cast(unsigned, c);
+    return b ^ ((unsigned)((int)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float score32(unsigned k)
+{
+    return __builtin_bit_cast(float, k ^ ((unsigned)((int)~k >> 31) | 0x80000000u));
+}
+__device__ __forceinline__ unsigned max_u(unsigned a, unsigned b) { return a > b ? a : b; }
+__device__ __forceinline__ unsigned min_u(unsigned a, unsigned b) { return a < b ? a : b; }
+
+// A lane's NE keys in descending order: bitonic merges of runs of w into runs of
+// 2w, the second run read backwards.
+template <int NE, class K>
+__device__ __forceinline__ void sort_keys(K *key)
+{
+#pragma unroll
+    for (int w = 1; w < NE; w <<= 1)
+#pragma unroll
+        for (int d = w; d > 0; d >>= 1)
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+                const int o = d == w ? (i / (2 * w)) * 2 * w + (2 * w - 1 - i % (2 * w)) : i ^ d;
+                if (o > i) {
+                    const K hi = key[i] > key[o] ? key[i] : key[o], lo = key[i] > key[o] ? key[o] : key[i];
+                    key[i] = hi;
+                    key[o] = lo;
+                }
+            }
+}
+
 // v[i] = row[lane*NE + i], `none` from E on: 16-byte loads where all four are inside.
 template <int NE>
 __device__ __forceinline__ void load_experts(const float *row, int lane, int E, float none, float *v)
@@ -135,6 +168,90 @@ __device__ __forceinline__ void load_experts(const float *row, int lane, int E, 
 //     64 by a prefix over their counts, so the order never depends on timing.
 //     With one block the counts are scanned here; otherwise they go to `counts`
 //     and place_kernel turns local numbers into rows.
+// Where scores are needed, 32 bits decide first (choose32): scores below 4 in
+// size are formed to kNear, and a choice stands if every decision in it (a group
+// kept or not, a choice before the next) is by more than the errors of what it compares;
+// else the token is done again in 64 bits.  With scores of some hundred experts spread over a
+// unit a few tokens in a thousand are.
+constexpr float kLog2e = 1.44269504f;
+constexpr float kNear = 1.f / (1 << 17);   // exp, sum and quotient 4e-6 together, a place in the key's low 4 bits 4 * 2^-20
+
+// The k choices (lane j's is `mine`), or false.  x: logits, b: biases (-inf: unavailable).
+template <int NE>
+__device__ __forceinline__ bool choose32(const RouteProblem &p, const float *x, const float *b, float mx, int lane,
+                                         int lanes_per_group, int *mine)
+{
+    float s[NE];
+    if (p.score == 0) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            s[i] = __builtin_amdgcn_exp2f((x[i] - mx) * kLog2e);
+            sum += s[i];
+        }
+        sum = __builtin_amdgcn_rcpf(wave_sum(sum));
+#pragma unroll
+        for (int i = 0; i < NE; ++i) s[i] *= sum;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) s[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-x[i] * kLog2e));
+    }
+    unsigned key[NE];
+    bool odd = false;   // a score that this path does not take: NaN, or 4 and more in size
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        const float c = s[i] + b[i];
+        const bool gone = x[i] == -INFINITY || b[i] == -INFINITY;
+        odd |= !gone && !(fabsf(c) < 4.f);
+        key[i] = gone ? 0u : (key32(c) & ~(unsigned)(NE - 1)) | (NE - 1 - i);
+    }
+    if (__ballot(odd)) return false;
+    sort_keys<NE>(key);
+    if (p.groups > 1) {
+        if (lanes_per_group == 0) return false;
+        // the group's two best keys by exchanges between its lanes
+        unsigned k1 = key[0], k2 = NE > 1 ? key[NE > 1 ? 1 : 0] : 0u;
+        auto merge = [&](unsigned o1, unsigned o2) {
+            k2 = max_u(min_u(k1, o1), max_u(k2, o2));
+            k1 = max_u(k1, o1);
+        };
+        if (lanes_per_group > 1) merge(dpp<0xB1, 0xF>(0u, k1), dpp<0xB1, 0xF>(0u, k2));     // lane ^ 1
+        if (lanes_per_group > 2) merge(dpp<0x4E, 0xF>(0u, k1), dpp<0x4E, 0xF>(0u, k2));     // lane ^ 2
+        if (lanes_per_group > 4) merge(dpp<0x141, 0xF>(0u, k1), dpp<0x141, 0xF>(0u, k2));   // mirrored in 8
+        if (lanes_per_group > 8) merge(dpp<0x140, 0xF>(0u, k1), dpp<0x140, 0xF>(0u, k2));   // mirrored in 16
+        float score = k1 == 0 ? -1e30f : score32(k1);
+        if (p.group_top == 2 && k2 != 0) score += score32(k2);
+        int surely = 0, maybe = 0;   // groups that come before this lane's
+        for (int g = 0; g < p.groups; ++g) {
+            const float d = lane_value(score, g * lanes_per_group) - score;
+            surely += d > 4 * kNear;
+            maybe += d > -4 * kNear;
+        }
+        const bool kept = maybe - 1 < p.group_k;   // (its own group counts once)
+        if (__ballot(lane < p.groups * lanes_per_group && !kept && surely < p.group_k)) return false;
+        if (!kept)
+#pragma unroll
+            for (int i = 0; i < NE; ++i) key[i] = 0;
+    }
+    float gap = 1.f, last = 1e30f;
+    for (int j = 0; j <= p.k; ++j) {
+        const unsigned top = wave_max(key[0]);
+        if (top == 0) break;
+        const float c = score32(top & ~(unsigned)(NE - 1));
+        gap = fminf(gap, last - c);
+        last = c;
+        if (j == p.k) break;
+        const int win = __builtin_ctzll(__ballot(key[0] == top));
+        if (lane == j) *mine = win * NE + (NE - 1 - (int)(top & (NE - 1)));
+        if (lane == win) {
+#pragma unroll
+            for (int i = 0; i + 1 < NE; ++i) key[i] = key[i + 1];
+            key[NE - 1] = 0;
+        }
+    }
+    return !__ballot(gap <= 2 * kNear);
+}
+
 constexpr int kSegments = 16;                  // runs of 64 choices in a block
 constexpr int kChunkIds = 64 * kSegments;
 
@@ -152,19 +269,21 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteProblem p, int chunk, in
     __shared__ int total[kMaxExperts + 2];
     double *sc = reinterpret_cast<double *>(smem) + (size_t)wave * E;
 
+    float b[NE];
+    if (p.bias)
+        load_experts<NE>(p.bias, lane, E, -INFINITY, b);
+    else
+#pragma unroll
+        for (int i = 0; i < NE; ++i) b[i] = 0.f;
+    float x[NE], ahead[NE];   // a token's logits are read while the one before it is chosen for
+    if (t0 + wave < t1) load_experts<NE>(p.logits + (long long)(t0 + wave) * p.ldl, lane, E, -INFINITY, ahead);
     for (int t = t0 + wave; t < t1; t += NW) {
         const float *row = p.logits + (long long)t * p.ldl;
-        float x[NE];
-        load_experts<NE>(row, lane, E, -INFINITY, x);
-        float b[NE];
-        if (p.bias)
-            load_experts<NE>(p.bias, lane, E, -INFINITY, b);
-        else
 #pragma unroll
-            for (int i = 0; i < NE; ++i) b[i] = 0.f;
+        for (int i = 0; i < NE; ++i) x[i] = ahead[i];
+        if (t + NW < t1) load_experts<NE>(row + NW * p.ldl, lane, E, -INFINITY, ahead);
         float mx = -INFINITY;
         bool bad = false;   // a softmax whose scores are NaN: the row holds NaN or +inf
-        double sum = 1.0;
         uint64_t key[NE];
         if (BY_LOGIT || p.score == 0) {
 #pragma unroll
@@ -181,18 +300,23 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteProblem p, int chunk, in
                 key[i] = x[i] == -INFINITY ? 0
                          : p.score == 0 && bad ? kNanKey | (NE - 1 - i)
                                                : logit_key(x[i]) | (NE - 1 - i);
-            if (p.score == 0 && !p.renorm) {
-                // (32 bits: this sum only scales weights)
-                float s = 0.f;
-#pragma unroll
-                for (int i = 0; i < NE; ++i) s += x[i] == -INFINITY ? 0.f : expf(x[i] - mx);
-                sum = (double)wave_sum(s);
-            }
         }
+        auto sum32 = [&]() {   // the softmax's sum (32 bits: it only scales weights)
+            float v = 0.f;
+#pragma unroll
+            for (int i = 0; i < NE; ++i) v += x[i] == -INFINITY ? 0.f : expf(x[i] - mx);
+            return wave_sum(v);
+        };
+        int mine = -1;   // lane j: choice j
+        bool done = false;
         if constexpr (!BY_LOGIT) {
+            done = !bad && choose32<NE>(p, x, b, mx, lane, lanes_per_group, &mine);
+            if (!done) mine = -1;
+        }
+        if (!BY_LOGIT && !done) {
             double c[NE];
             if (p.score == 0) {
-                sum = 0.0;
+                double sum = 0.0;
 #pragma unroll
                 for (int i = 0; i < NE; ++i) {
                     c[i] = x[i] == -INFINITY ? 0.0 : exp((double)x[i] - (double)mx);
@@ -308,23 +432,8 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteProblem p, int chunk, in
                 __builtin_amdgcn_wave_barrier();
             }
         }
-        // the lane's keys in descending order (odd-even transposition for NE <= 2, merging networks beyond)
-#pragma unroll
-        for (int w = 1; w < NE; w <<= 1)
-#pragma unroll
-            for (int d = w; d > 0; d >>= 1)
-#pragma unroll
-                for (int i = 0; i < NE; ++i) {
-                    // bitonic merges of runs of w into runs of 2w, the second run read backwards
-                    const int o = d == w ? (i / (2 * w)) * 2 * w + (2 * w - 1 - i % (2 * w)) : i ^ d;
-                    if (o > i) {
-                        const uint64_t hi = key[i] > key[o] ? key[i] : key[o], lo = key[i] > key[o] ? key[o] : key[i];
-                        key[i] = hi;
-                        key[o] = lo;
-                    }
-                }
-        int mine = -1;   // lane j: choice j
-        for (int j = 0; j < k; ++j) {
+        if (!done) sort_keys<NE>(key);
+        for (int j = 0; !done && j < k; ++j) {
             const unsigned top = wave_max((unsigned)(key[0] >> 32));
             if (top == 0) break;
             uint64_t at = __ballot((unsigned)(key[0] >> 32) == top);
@@ -344,23 +453,35 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteProblem p, int chunk, in
             }
         }
         // weights, from the chosen logits alone where they are renormalised; in 64
-        // bits, where scores that 32 bits lose still have a quotient
+        // bits where scores that 32 bits lose still have a quotient
         const bool has = lane < k && mine >= 0;
         const float xl = has ? row[mine] : -INFINITY;
-        double w = 0.0;
-        if (p.score == 1) {
-            w = has ? 1.0 / (1.0 + exp(-(double)xl)) : 0.0;
+        const float ref = p.score == 1 ? 0.f : p.renorm ? wave_max(xl) : mx;
+        const float over = p.renorm || p.score == 1 ? 1.f : sum32();   // (every lane takes part)
+        float weight = 0.f;
+        if (__ballot(has && (bad || !(fabsf(xl - ref) < 60.f))) == 0) {
+            // (hardware exponentials and reciprocals: 2 u each and 1.44 u per unit of the exponent)
+            const float x2 = (p.score == 1 ? -xl : xl - ref) * kLog2e;
+            float w = __builtin_amdgcn_exp2f(x2);
+            if (p.score == 1) w = __builtin_amdgcn_rcpf(1.f + w);
+            if (!has) w = 0.f;
+            const float all = p.renorm ? wave_sum(w) : over;
+            if (has) weight = w * __builtin_amdgcn_rcpf(all) * p.scale;
         } else {
-            const float ref = p.renorm ? wave_max(xl) : mx;
-            w = !has ? 0.0 : bad ? (double)NAN : exp((double)xl - (double)ref) / sum;
-        }
-        if (p.renorm) {
-            const double s = wave_sum(w);
-            if (s != 0.0) w /= s;   // scores that are all zero keep weights of zero
+            double w = 0.0;
+            if (p.score == 1)
+                w = has ? 1.0 / (1.0 + exp(-(double)xl)) : 0.0;
+            else
+                w = !has ? 0.0 : bad ? (double)NAN : exp((double)xl - (double)ref) / (double)over;
+            if (p.renorm) {
+                const double s = wave_sum(w);
+                if (s != 0.0) w /= s;   // scores that are all zero keep weights of zero
+            }
+            if (has) weight = (float)(w * (double)p.scale);
         }
         if (lane < k) {
             p.ids[(long long)t * k + lane] = mine;
-            p.weights[(long long)t * k + lane] = (float)(has ? w * (double)p.scale : 0.0);
+            p.weights[(long long)t * k + lane] = weight;
             cid[(t - t0) * k + lane] = mine < 0 ? E : mine;
         }
     }
@@ -557,33 +678,36 @@ hipError_t route_ne(const RouteProblem &p, hipStream_t stream)
 //
 // A wave per token.  s: the scores of all experts (softmax) or of the chosen
 // ones; g_j = scale * dweights_j.
-//   renormalised, p_j = s_j / sum of the chosen s: ds-side factor
-//     q_j = p_j (g_j - sum_i p_i g_i);   softmax: dl = q_j (the softmax's own sum cancels; other experts 0),
-//     sigmoid: dl = q_j (1 - s_j)
+//   renormalised, p_j = s_j / sum of the chosen s:  q_j = p_j (g_j - sum_i p_i g_i);
+//     softmax: dl = q_j (the softmax's own sum cancels; other experts 0),  sigmoid: dl = q_j (1 - s_j)
 //   otherwise  softmax: dl_e = s_e (g_e - sum_i g_i s_i) over all experts,  sigmoid: dl = g_j s_j (1 - s_j)
-// The k chosen values are formed in 64 bits (differences of near numbers), the
-// row in 32.
+// Where near numbers are subtracted (renormalised) the k chosen values are formed in
+// 64 bits, all else in 32.  The k values reach their experts' lanes through a row
+// in LDS, of which a wave has one of its own (64 NE floats).
 template <int NE>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradProblem p)
 {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    __shared__ __attribute__((aligned(16))) float rows[4][64 * NE];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int t = blockIdx.x * 4 + wave;
     const int E = p.E, k = p.k;
     if (t >= p.T) return;
     const float *row = p.logits + (long long)t * p.ldl;
-    float *out = p.dlogits + (long long)t * p.lddl;
-    int id = lane < k ? p.ids[(long long)t * k + lane] : -1;
-    if (id >= E) id = -1;
-    const bool has = id >= 0;
-    const double g = has ? (double)p.scale * (double)p.dweights[(long long)t * k + lane] : 0.0;
-    const float xl = has ? row[id] : -INFINITY;
+    const int32_t *ids = p.ids + (long long)t * k;
+    const float *dw = p.dweights + (long long)t * k;
+    int id = lane < k ? ids[lane] : -1;
+    const float g = lane < k ? p.scale * dw[lane] : 0.f;
     const bool whole = p.score == 0 && !p.renorm;   // every expert gets a gradient
     float s[NE];
-    float v = 0.f;          // lane j: the gradient of choice j's own logit (g_j where whole)
-    float dot = 0.f;
+    if (whole) load_experts<NE>(row, lane, E, -INFINITY, s);
+    const bool has = (unsigned)id < (unsigned)E;
+    const float xl = has ? row[id] : -INFINITY;
+    float *mine = rows[wave];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) mine[lane * NE + i] = 0.f;
+    float v = 0.f, dot = 0.f;   // lane j: the value choice j adds to its expert
     if (whole) {
         float mx = -INFINITY;
-        load_experts<NE>(row, lane, E, -INFINITY, s);
 #pragma unroll
         for (int i = 0; i < NE; ++i) mx = s[i] > mx ? s[i] : mx;
         mx = wave_max(mx);
@@ -594,41 +718,34 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradProblem p)
             sum += s[i];
         }
         sum = wave_sum(sum);
+        const float over = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-        for (int i = 0; i < NE; ++i) s[i] = sum == 0.f ? 0.f : s[i] / sum;
-        const double sl = !has ? 0.0 : xl == -INFINITY ? 0.0 : exp((double)xl - (double)mx) / (double)sum;
-        dot = (float)wave_sum(g * sl);
-        v = (float)g;
+        for (int i = 0; i < NE; ++i) s[i] *= over;
+        dot = wave_sum(has && xl != -INFINITY ? g * (expf(xl - mx) * over) : 0.f);
+        v = g;
+    } else if (p.renorm) {
+        const double gd = has ? (double)p.scale * (double)dw[lane] : 0.0;
+        const float cm = wave_max(xl);
+        double raw = 0.0;
+        if (has) raw = p.score == 1 ? 1.0 / (1.0 + exp(-(double)xl)) : xl == -INFINITY ? 0.0 : exp((double)xl - (double)cm);
+        const double sum = wave_sum(raw);
+        const double pj = sum != 0.0 ? raw / sum : 0.0;
+        const double mean = wave_sum(pj * gd);
+        v = (float)(pj * (gd - mean) * (p.score == 1 ? 1.0 - raw : 1.0));
     } else {
-        double sl, d = g;
-        if (p.score == 0) {
-            const float cm = wave_max(xl);
-            sl = !has || xl == -INFINITY ? 0.0 : exp((double)xl - (double)cm);
-        } else {
-            sl = has ? 1.0 / (1.0 + exp(-(double)xl)) : 0.0;
-        }
-        const double raw = sl;
-        if (p.renorm) {
-            const double sum = wave_sum(sl);
-            sl = sum != 0.0 ? sl / sum : 0.0;
-            d = g - wave_sum(sl * g);
-        }
-        v = (float)(sl * d * (p.score == 1 ? 1.0 - raw : 1.0));
-        if (!has) v = 0.f;
+        // s (1 - s) = s(x) s(-x), neither factor a difference
+        const float e = expf(-fabsf(xl)), q = 1.f / (1.f + e);
+        v = g * (e * q * q);
     }
+    if (has) atomicAdd(&mine[id], v);   // (distinct experts: no two lanes add to one)
+    __builtin_amdgcn_wave_barrier();
     float acc[NE];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) acc[i] = 0.f;
-    for (int j = 0; j < k; ++j) {
-        const int e = (int)lane_value((unsigned)id, j);
-        const float d = lane_value(v, j);
-#pragma unroll
-        for (int i = 0; i < NE; ++i)
-            if (lane * NE + i == e) acc[i] += d;
-    }
-#pragma unroll
-    for (int i = 0; i < NE; ++i)
+    for (int i = 0; i < NE; ++i) {
+        acc[i] = mine[lane * NE + i];
         if (whole) acc[i] = s[i] * (acc[i] - dot);
+    }
+    float *out = p.dlogits + (long long)t * p.lddl;
     const int e0 = lane * NE;
     if constexpr (NE % 4 == 0) {
         if (e0 + NE <= E) {

@@ -13,14 +13,48 @@
 namespace mi355gemm {
 namespace {
 
-// Eight consecutive values from column c of a row of `cols` (nullptr: zeros),
-// wherever the row starts; columns at or past the end read as zero.
-__device__ __forceinline__ u32x4 load8_row(const uint16_t *row, long long c, long long cols)
+// Eight consecutive values from column c of a row, wherever the row starts, in two
+// halves: the loads (words), whose results nothing touches while other loads are on
+// their way, and the values (value8).  The words are the five dwords from the one that
+// holds the first value on; past the last that holds one of the row's `cols` columns,
+// that one again, so no load leaves the words the row occupies.  whole (the same in all
+// lanes): no chunk of this slice ends before its eighth column, so four of the dwords are
+// one load.  row == nullptr: zeros.
+struct Words {
+    unsigned w[5], shift;
+};
+__device__ __forceinline__ void words(const uint16_t *row, long long c, long long cols, bool whole, Words *out)
 {
-    if (row == nullptr || c >= cols) return u32x4{0u, 0u, 0u, 0u};
-    const uint16_t *p = row + c;
-    if (c + 8 > cols) return load8_masked(p, (int)(cols - c));
-    return (reinterpret_cast<uintptr_t>(p) & 3) == 0 ? *reinterpret_cast<const u32x4_g *>(p) : load8_words(p);
+    const uintptr_t p = reinterpret_cast<uintptr_t>(row + c);
+    if (whole) {
+        const unsigned odd = row ? (unsigned)(p & 2) >> 1 : 0u;
+        const unsigned *at = row ? reinterpret_cast<const unsigned *>(p & ~(uintptr_t)3) : zero_chunk;
+        const u32x4 v = *reinterpret_cast<const u32x4_g *>(at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out->w[i] = v[i];
+        out->w[4] = at[3 + odd];
+        out->shift = 16 * odd;
+        return;
+    }
+    const int valid = row == nullptr || c >= cols ? 0 : cols - c < 8 ? (int)(cols - c) : 8;
+    const unsigned odd = valid > 0 ? (unsigned)(p & 2) >> 1 : 0u;
+    const int last = valid > 0 ? ((int)odd + valid - 1) >> 1 : 0;
+    const unsigned *at = valid > 0 ? reinterpret_cast<const unsigned *>(p & ~(uintptr_t)3) : zero_chunk;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) out->w[i] = at[i < last ? i : last];
+    out->shift = 16 * odd;
+}
+__device__ __forceinline__ u32x4 value8(const Words &x, long long c, long long cols)
+{
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_alignbit(x.w[i + 1], x.w[i], x.shift);
+    if (cols - c < 8) {   // columns at or past the end are zero
+        const int valid = (int)(cols - c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = valid >= 2 * i + 2 ? v[i] : valid == 2 * i + 1 ? v[i] & 0xFFFFu : 0u;
+    }
+    return v;
 }
 
 // ---------------------------------------------------------------------------
@@ -72,7 +106,9 @@ __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
     float *C = WG ? p.C + (long long)group * p.strideC : p.C;
     const long long lda = p.lda, ldb = p.ldb, ldc = p.ldc;
 
-    u32x4 ra[TileA::LOADS], rb[TileB::LOADS];
+    // operand slices on their way: AHEAD of them in registers
+    constexpr int AHEAD = 2;
+    Words ra[AHEAD][TileA::LOADS], rb[AHEAD][TileB::LOADS];
     auto row_of = [](const uint16_t *X, long long ld, const int32_t *rows, int r, int end, int x_rows) -> const uint16_t * {
         if (r >= end) return nullptr;
         const int at = rows ? rows[r] : r;
@@ -85,26 +121,26 @@ __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
         for (int i = 0; i < TileA::LOADS; ++i)
             arow[i] = row_of(p.A, lda, p.rowsA, m0 + (i * NT + tid) / TileA::CPR, m_end, p.a_rows);
     }
-    auto load_tiles = [&](int k0) {
+    auto load_tiles = [&](int k0, Words *ra, Words *rb) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < TileA::LOADS; ++i) {
             const int id = i * NT + tid;
             const int r = id / TileA::CPR, c = (id % TileA::CPR) * 8;
             if constexpr (WG)
-                ra[i] = load8_row(row_of(p.A, lda, p.rowsA, k_lo + k0 + r, k_lo + K, p.a_rows), m0 + c, p.M);
+                words(row_of(p.A, lda, p.rowsA, k_lo + k0 + r, k_lo + K, p.a_rows), m0 + c, p.M, m0 + BM <= p.M, &ra[i]);
             else
-                ra[i] = load8_row(arow[i], k0 + c, K);
+                words(arow[i], k0 + c, K, k0 + BK <= K, &ra[i]);
         }
 #pragma unroll
         for (int i = 0; i < TileB::LOADS; ++i) {
             const int id = i * NT + tid;
             const int r = id / TileB::CPR, c = (id % TileB::CPR) * 8;
             if constexpr (WG)
-                rb[i] = load8_row(row_of(p.B, ldb, p.rowsB, k_lo + k0 + r, k_lo + K, p.b_rows), n0 + c, N);
+                words(row_of(p.B, ldb, p.rowsB, k_lo + k0 + r, k_lo + K, p.b_rows), n0 + c, N, n0 + BN <= N, &rb[i]);
             else if constexpr (TB)
-                rb[i] = load8_row(n0 + r < N ? B + (long long)(n0 + r) * ldb : nullptr, k0 + c, K);
+                words(n0 + r < N ? B + (long long)(n0 + r) * ldb : nullptr, k0 + c, K, k0 + BK <= K, &rb[i]);
             else
-                rb[i] = load8_row(k0 + r < K ? B + (long long)(k0 + r) * ldb : nullptr, n0 + c, N);
+                words(k0 + r < K ? B + (long long)(k0 + r) * ldb : nullptr, n0 + c, N, n0 + BN <= N, &rb[i]);
         }
     };
     auto store_one = [&](auto tile, uint16_t *dst, int i, const u32x4 &v) {
@@ -116,13 +152,19 @@ __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
         else
             *reinterpret_cast<u32x4 *>(dst + r * T::PITCH + 8 * c) = v;
     };
-    auto store_tiles = [&](int buf) {
+    auto store_tiles = [&](int buf, int k0, const Words *ra, const Words *rb) __attribute__((always_inline)) {
         uint16_t *la = lds + buf * BUF_HALVES;
         uint16_t *lb = la + TileA::HALVES;
 #pragma unroll
-        for (int i = 0; i < TileA::LOADS; ++i) store_one(TileA{}, la, i, ra[i]);
+        for (int i = 0; i < TileA::LOADS; ++i) {
+            const int c = (i * NT + tid) % TileA::CPR * 8;
+            store_one(TileA{}, la, i, WG ? value8(ra[i], m0 + c, p.M) : value8(ra[i], k0 + c, K));
+        }
 #pragma unroll
-        for (int i = 0; i < TileB::LOADS; ++i) store_one(TileB{}, lb, i, rb[i]);
+        for (int i = 0; i < TileB::LOADS; ++i) {
+            const int c = (i * NT + tid) % TileB::CPR * 8;
+            store_one(TileB{}, lb, i, !WG && TB ? value8(rb[i], k0 + c, K) : value8(rb[i], n0 + c, N));
+        }
     };
     const int wave = tid >> 6, lane = tid & 63;
     const int wm = wave / Cfg::WN, wn = wave % Cfg::WN;
@@ -147,11 +189,13 @@ __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
         }
     };
     const int nk = (K + BK - 1) / BK;
-    if (nk > 0) load_tiles(0);
-    for (int t = 0; t < nk; ++t) {
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d)
+        if (d < nk) load_tiles(d * BK, ra[d], rb[d]);
+    auto step = [&](int t, Words *a, Words *b) __attribute__((always_inline)) {
         const int buf = t & 1;
-        store_tiles(buf);
-        if (t + 1 < nk) load_tiles((t + 1) * BK);
+        store_tiles(buf, t * BK, a, b);
+        if (t + AHEAD < nk) load_tiles((t + AHEAD) * BK, a, b);
         // one barrier a step: the buffer written next was last read in the step
         // before this one, which every wave has left when it passes here
         __syncthreads();
@@ -160,7 +204,11 @@ __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
 #pragma unroll
         for (int s = 0; s < BK / 16; ++s)
             acc = mfma16<BF>(read_frag(TileB{}, lb, wn * Cfg::TN, s), read_frag(TileA{}, la, wm * Cfg::TM, s), acc);
-    }
+    };
+    for (int t = 0; t < nk; t += AHEAD)
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d)
+            if (t + d < nk) step(t + d, ra[d], rb[d]);
     const long long row = m0 + wm * Cfg::TM + lr;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {

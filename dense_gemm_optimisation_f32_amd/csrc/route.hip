@@ -97,16 +97,6 @@ __device__ __forceinline__ uint64_t logit_key(float c)
     return (uint64_t)((b >> 31) ? ~b : (b | 0x80000000u)) << 32;
 }
 
-// A 32-bit score as such a key, without the NaN case; and back.
-__device__ __forceinline__ unsigned key32(float c)
-{
-    const unsigned b = __builtin_bit_cast(unsigned, c);
-    return b ^ ((unsigned)((int)b >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float score32(unsigned k)
-{
-    return __builtin_bit_cast(float, k ^ ((unsigned)((int)~k >> 31) | 0x80000000u));
-}
 __device__ __forceinline__ unsigned max_u(unsigned a, unsigned b) { return a > b ? a : b; }
 __device__ __forceinline__ unsigned min_u(unsigned a, unsigned b) { return a < b ? a : b; }
 
@@ -123,9 +113,9 @@ __device__ __forceinline__ void sort_keys(K *key)
             for (int i = 0; i < NE; ++i) {
                 const int o = d == w ? (i / (2 * w)) * 2 * w + (2 * w - 1 - i % (2 * w)) : i ^ d;
                 if (o > i) {
-                    const K hi = key[i] > key[o] ? key[i] : key[o], lo = key[i] > key[o] ? key[o] : key[i];
-                    key[i] = hi;
-                    key[o] = lo;
+                    const K u = key[i], v = key[o];
+                    key[i] = u > v ? u : v;
+                    key[o] = u > v ? v : u;
                 }
             }
 }
@@ -168,13 +158,16 @@ __device__ __forceinline__ void load_experts(const float *row, int lane, int E, 
 //     64 by a prefix over their counts, so the order never depends on timing.
 //     With one block the counts are scanned here; otherwise they go to `counts`
 //     and place_kernel turns local numbers into rows.
-// Where scores are needed, 32 bits decide first (choose32): scores below 4 in
-// size are formed to kNear, and a choice stands if every decision in it (a group
+// Where scores are needed, 32 bits decide first (choose32): scores between -3.9 and 3.9
+// as whole numbers of 2^-27, and a choice stands if every decision in it (a group
 // kept or not, a choice before the next) is by more than the errors of what it compares;
 // else the token is done again in 64 bits.  With scores of some hundred experts spread over a
 // unit a few tokens in a thousand are.
 constexpr float kLog2e = 1.44269504f;
-constexpr float kNear = 1.f / (1 << 17);   // exp, sum and quotient 4e-6 together, a place in the key's low 4 bits 4 * 2^-20
+constexpr float kUnits = 1 << 27, kZero = 4.f * (1 << 27);   // key = score * kUnits + kZero; 0: unavailable
+// Error of a key: exp, sum and quotient 4e-6, the rounding of score + 4 2.4e-7, the place of
+// the expert in the lowest 4 bits 1.2e-7; together below 2^-17.
+constexpr unsigned kNear = 1 << 10;
 
 // The k choices (lane j's is `mine`), or false.  x: logits, b: biases (-inf: unavailable).
 template <int NE>
@@ -197,13 +190,13 @@ __device__ __forceinline__ bool choose32(const RouteProblem &p, const float *x, 
         for (int i = 0; i < NE; ++i) s[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-x[i] * kLog2e));
     }
     unsigned key[NE];
-    bool odd = false;   // a score that this path does not take: NaN, or 4 and more in size
+    bool odd = false;   // a score that this path does not take
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
         const float c = s[i] + b[i];
         const bool gone = x[i] == -INFINITY || b[i] == -INFINITY;
-        odd |= !gone && !(fabsf(c) < 4.f);
-        key[i] = gone ? 0u : (key32(c) & ~(unsigned)(NE - 1)) | (NE - 1 - i);
+        odd |= !gone && !(fabsf(c) < 3.9f);
+        key[i] = gone ? 0u : ((unsigned)__builtin_fmaf(c, kUnits, kZero) & ~(unsigned)(NE - 1)) | (NE - 1 - i);
     }
     if (__ballot(odd)) return false;
     sort_keys<NE>(key);
@@ -219,37 +212,38 @@ __device__ __forceinline__ bool choose32(const RouteProblem &p, const float *x, 
         if (lanes_per_group > 2) merge(dpp<0x4E, 0xF>(0u, k1), dpp<0x4E, 0xF>(0u, k2));     // lane ^ 2
         if (lanes_per_group > 4) merge(dpp<0x141, 0xF>(0u, k1), dpp<0x141, 0xF>(0u, k2));   // mirrored in 8
         if (lanes_per_group > 8) merge(dpp<0x140, 0xF>(0u, k1), dpp<0x140, 0xF>(0u, k2));   // mirrored in 16
-        float score = k1 == 0 ? -1e30f : score32(k1);
-        if (p.group_top == 2 && k2 != 0) score += score32(k2);
+        // two keys' sum below 2^31; a lone one's other half is the score 0
+        int score = (int)k1;
+        if (p.group_top == 2) score = k1 == 0 ? 0 : (int)k1 + (int)(k2 == 0 ? (unsigned)kZero : k2);
         int surely = 0, maybe = 0;   // groups that come before this lane's
         for (int g = 0; g < p.groups; ++g) {
-            const float d = lane_value(score, g * lanes_per_group) - score;
-            surely += d > 4 * kNear;
-            maybe += d > -4 * kNear;
+            const int d = (int)lane_value((unsigned)score, g * lanes_per_group) - score;
+            surely += d > (int)(4 * kNear);
+            maybe += d > -(int)(4 * kNear);
         }
         const bool kept = maybe - 1 < p.group_k;   // (its own group counts once)
         if (__ballot(lane < p.groups * lanes_per_group && !kept && surely < p.group_k)) return false;
-        if (!kept)
 #pragma unroll
-            for (int i = 0; i < NE; ++i) key[i] = 0;
+        for (int i = 0; i < NE; ++i) key[i] = kept ? key[i] : 0u;
     }
-    float gap = 1.f, last = 1e30f;
+    unsigned gap = ~0u, last = ~0u;
     for (int j = 0; j <= p.k; ++j) {
         const unsigned top = wave_max(key[0]);
         if (top == 0) break;
-        const float c = score32(top & ~(unsigned)(NE - 1));
-        gap = fminf(gap, last - c);
-        last = c;
+        gap = min_u(gap, last - top);
+        last = top;
         if (j == p.k) break;
-        const int win = __builtin_ctzll(__ballot(key[0] == top));
-        if (lane == j) *mine = win * NE + (NE - 1 - (int)(top & (NE - 1)));
-        if (lane == win) {
+        const bool won = key[0] == top;   // (one lane, or the gap to the next choice is zero)
+        const int win = __builtin_ctzll(__ballot(won));
+        const int e = win * NE + (NE - 1 - (int)(top & (NE - 1)));
+        *mine = lane == j ? e : *mine;
 #pragma unroll
-            for (int i = 0; i + 1 < NE; ++i) key[i] = key[i + 1];
-            key[NE - 1] = 0;
+        for (int i = 0; i < NE; ++i) {
+            const unsigned here = key[i], next = i + 1 < NE ? key[i + 1 < NE ? i + 1 : i] : 0u;   // (values, not places, to choose from)
+            key[i] = won ? next : here;
         }
     }
-    return !__ballot(gap <= 2 * kNear);
+    return gap > 2 * kNear;
 }
 
 constexpr int kSegments = 16;                  // runs of 64 choices in a block

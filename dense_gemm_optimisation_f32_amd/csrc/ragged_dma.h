@@ -416,7 +416,8 @@ __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
         }
     };
     const bool late = Cfg::STAGGER && uwave >= Cfg::NW / 2;
-    auto step_in = [&](int t, auto pending, auto refill, bool late_refill, auto slot_c) __attribute__((always_inline)) {
+    auto step_in = [&](int t, auto pending, auto refill, bool late_refill, auto slot_c, auto works) __attribute__((always_inline)) {
+        constexpr bool WORKS = decltype(works)::value;   // false: this wave only loads its share
         constexpr int SC = decltype(slot_c)::value;   // < 0: not known at compile time
         const int slot = SC >= 0 ? SC : t % S;
         const int next = SC >= 0 ? (SC + 1) % S : (t + 1) % S;
@@ -425,21 +426,23 @@ __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
         for (int sub = 0; sub < NS; ++sub) {
             const int cur = sub & 1, nxt = cur ^ 1;
             if (sub + 1 < NS) {
-                read_frags(slot, sub + 1, fa[nxt], fb[nxt]);
+                if constexpr (WORKS) read_frags(slot, sub + 1, fa[nxt], fb[nxt]);
                 if (Cfg::STAGGER && sub == NS - 2 && late && late_refill) issue_slice(t - 1 + S, prev);
             } else {
                 wait_vmcnt<LOADS * decltype(pending)::value>();
                 __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's slice-t reads are done
                 lds_barrier();
                 if (decltype(refill)::value && !late) issue_slice(t + S, slot);
-                read_frags(next, 0, fa[nxt], fb[nxt]);
+                if constexpr (WORKS) read_frags(next, 0, fa[nxt], fb[nxt]);
             }
-            mfmas(fa[cur], fb[cur]);
-            interleave();
+            if constexpr (WORKS) {
+                mfmas(fa[cur], fb[cur]);
+                interleave();
+            }
         }
     };
-    auto step = [&](int t, auto pending, auto refill, bool late_refill) __attribute__((always_inline)) {
-        step_in(t, pending, refill, late_refill, std::integral_constant<int, -1>{});
+    auto step = [&](int t, auto pending, auto refill, bool late_refill, auto works) __attribute__((always_inline)) {
+        step_in(t, pending, refill, late_refill, std::integral_constant<int, -1>{}, works);
     };
 
     if (K > 0) {   // (uniform)
@@ -451,32 +454,41 @@ __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
         }
 #pragma unroll
         for (int st = 0; st < S; ++st) issue_slice(st, st);
-        wait_vmcnt<LOADS * (S - 1)>();
-        lds_barrier();
-        read_frags(0, 0, fa[0], fb[0]);
-        {
+        auto loop = [&](auto works) __attribute__((always_inline)) {
+            constexpr bool WORKS = decltype(works)::value;
+            wait_vmcnt<LOADS * (S - 1)>();
+            lds_barrier();
+            if constexpr (WORKS) read_frags(0, 0, fa[0], fb[0]);
             int t = 0;
-            constexpr bool UNROLL = BM >= 128 && !B_KC;   // (as in the whole-matrix kernel)
+            constexpr bool UNROLL = WORKS && BM >= 128 && !B_KC;   // (as in the whole-matrix kernel)
             for (; UNROLL && t + S - 1 + S < nk; t += S) {
                 [&]<int... I>(std::integer_sequence<int, I...>) {
                     (step_in(t + I, std::integral_constant<int, S - 2>{}, std::true_type{}, t + I >= 1,
-                             std::integral_constant<int, I>{}),
+                             std::integral_constant<int, I>{}, works),
                      ...);
                 }(std::make_integer_sequence<int, S>{});
             }
-            for (; t + S < nk; ++t) step(t, std::integral_constant<int, S - 2>{}, std::true_type{}, t >= 1);
-        }
-        const int t0 = nk - S;
-        step(t0, std::integral_constant<int, S - 2>{}, std::false_type{}, t0 >= 1);
-        if constexpr (S >= 3) step(t0 + 1, std::integral_constant<int, S - 3>{}, std::false_type{}, false);
-        if constexpr (S >= 4) step(t0 + 2, std::integral_constant<int, S - 4>{}, std::false_type{}, false);
-        const int slot = (nk - 1) % S;
+            for (; t + S < nk; ++t) step(t, std::integral_constant<int, S - 2>{}, std::true_type{}, t >= 1, works);
+            const int t0 = nk - S;
+            step(t0, std::integral_constant<int, S - 2>{}, std::false_type{}, t0 >= 1, works);
+            if constexpr (S >= 3) step(t0 + 1, std::integral_constant<int, S - 3>{}, std::false_type{}, false, works);
+            if constexpr (S >= 4) step(t0 + 2, std::integral_constant<int, S - 4>{}, std::false_type{}, false, works);
+            if constexpr (WORKS) {
+                const int slot = (nk - 1) % S;
 #pragma unroll
-        for (int sub = 0; sub < NS; ++sub) {
-            const int cur = sub & 1, nxt = cur ^ 1;
-            if (sub + 1 < NS) read_frags(slot, sub + 1, fa[nxt], fb[nxt]);
-            mfmas(fa[cur], fb[cur]);
-        }
+                for (int sub = 0; sub < NS; ++sub) {
+                    const int cur = sub & 1, nxt = cur ^ 1;
+                    if (sub + 1 < NS) read_frags(slot, sub + 1, fa[nxt], fb[nxt]);
+                    mfmas(fa[cur], fb[cur]);
+                }
+            }
+        };
+        // A wave whose rows all lie past the group's end only loads: the matrix cores
+        // of a part-filled tile are left to the waves beside it on its SIMD.
+        if (KIND == kGrouped && m0 + (uwave / Cfg::WN) * Cfg::TM >= m_end)
+            loop(std::false_type{});
+        else
+            loop(std::true_type{});
     }
 
     // Epilogue by rows: straight from the accumulators a store instruction would write

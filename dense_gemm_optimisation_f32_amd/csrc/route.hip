@@ -233,8 +233,10 @@ __device__ __forceinline__ bool choose32(const RouteProblem &p, const float *x, 
         gap = min_u(gap, last - top);
         last = top;
         if (j == p.k) break;
-        const bool won = key[0] == top;   // (one lane, or the gap to the next choice is zero)
-        const int win = __builtin_ctzll(__ballot(won));
+        const bool won = key[0] == top;
+        const uint64_t at = __ballot(won);
+        if (at & (at - 1)) return false;   // two lanes' keys are equal
+        const int win = __builtin_ctzll(at);
         const int e = win * NE + (NE - 1 - (int)(top & (NE - 1)));
         *mine = lane == j ? e : *mine;
 #pragma unroll

@@ -181,6 +181,29 @@ def test_route_extreme_values(score):
     route_check(x, None, score, 1, 1, 1, 2, 0, 1.0)
 
 
+@pytest.mark.parametrize("score,seed", [(1, 88), (1, 89), (0, 3)])
+def test_route_near_ties(score, seed):
+    """Many tokens, so that some hold scores nearer to one another than 32 bits tell; and scores made so: experts in
+    pairs whose biases differ by a few 2^-24."""
+    T, E, k = 20000, 256, 8
+    g = torch.Generator().manual_seed(seed)
+    x, b = torch.randn(T, E, generator=g) * 2, torch.randn(E, generator=g) * 0.1
+    x[:300, 1::2] = x[:300, ::2]
+    b[1::2] = torch.where(torch.rand(E // 2, generator=g) < 0.5, b[::2] + 2.0 ** -23, b[1::2])
+    s = torch.sigmoid(x.double()) if score else torch.softmax(x.double(), 1)
+    c = s + b.double()
+    for groups, group_k, top in ((1, 1, 1), (8, 4, 2)):
+        d = c
+        if groups > 1:
+            best = c.view(T, groups, -1).sort(dim=2, descending=True).values[:, :, :top].sum(2)
+            keep = best.sort(dim=1, descending=True, stable=True).indices[:, :group_k]
+            d = torch.where(torch.zeros(T, groups, dtype=torch.bool).scatter_(1, keep, True)[:, :, None], c.view(T, groups, -1), -math.inf).view(T, E)
+        want = d.sort(dim=1, descending=True, stable=True).indices[:, :k]
+        got = route_call(x.cuda(), E, b.cuda(), score, groups, group_k, top, k, 1, 1.0, T, E)["ids"].view(T, k).cpu().long()
+        done()
+        assert torch.equal(got, want), (got != want).any(1).nonzero()[:5]
+
+
 def test_route_without_layout_and_empty():
     x = dev(np.random.default_rng(5).standard_normal((300, 32)).astype(np.float32))
     a = route_call(x, 32, None, 0, 1, 1, 1, 4, 1, 1.0, 300, 32)

@@ -11,7 +11,7 @@
 //     the tiles of ragged_dma.h, which add the parts times LB's
 //     columns after the K loop.
 // Operands that direct-to-LDS loads cannot take (rows at odd halves, ragged
-// 16-byte chunks) run the library's GEMM, then t and the product with LB.
+// 16-byte chunks) run the kernel for every alignment, then t and the product with LB.
 #include "gemm_internal.h"
 #include "ragged_dma.h"
 
@@ -133,10 +133,15 @@ __device__ __forceinline__ void narrow_block(const NarrowArgs &p, unsigned char 
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int kq = 64 * b + 32 * h + 8 * lq;
-                const half8 xb = load8_any(x + kq, p.K - kq);
+                const bool whole = 64 * (b + 1) <= p.K;
+                Words xw, w[NR];
+                words(x, kq, p.K, whole, &xw);
+#pragma unroll
+                for (int n = 0; n < NR; ++n) words(16 * n + li < ra ? lrow[n] : nullptr, kq, p.K, whole, &w[n]);
+                const half8 xb = __builtin_bit_cast(half8, value8(xw, kq, p.K));
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
-                    acc[n] = mfma16x16<BF>(load8_any(lrow[n] + kq, 16 * n + li < ra ? p.K - kq : 0), xb, acc[n]);
+                    acc[n] = mfma16x16<BF>(__builtin_bit_cast(half8, value8(w[n], kq, p.K)), xb, acc[n]);
             }
     }
     // lane: columns 16n + 4*lq .. +3 of row li
@@ -462,6 +467,44 @@ hipError_t lora_tiles(const LoraProblem &p, hipStream_t stream)
     return launch_tiles<Ragged64, BF, TB>(a, stream);
 }
 
+// Any strides and alignments: the projection (few rows: K shared by several workgroups per
+// tile), the narrow product, then both joined.
+template <bool BF, bool TB>
+hipError_t lora_any(const LoraProblem &p, hipStream_t stream)
+{
+    RaggedArgs a = base_args(p);
+    FinishArgs f = finish_args(p);
+    auto run = [&](auto cfg, int splits) {
+        using Cfg = decltype(cfg);
+        a.tiles_m = (p.M + Cfg::BM - 1) / Cfg::BM;
+        a.tiles_n = (p.N + Cfg::BN - 1) / Cfg::BN;
+        const long long tiles = (long long)a.tiles_m * a.tiles_n;
+        if (tiles > INT_MAX / 256) return hipErrorInvalidValue;
+        hipLaunchKernelGGL((ragged_any_kernel<Cfg, BF, kLora, TB>), dim3((unsigned)tiles, splits), dim3(256), 0, stream, a);
+        return hipGetLastError();
+    };
+    hipError_t e = hipSuccess;
+    if (p.M <= kDecodeRows) {
+        const int splits = decode_splits(p.N, p.K);
+        if (splits > 1) {
+            float *sums = p.t + (size_t)p.M * f.pitch;
+            a.C = sums; a.ldc = p.N; a.strideC = (long long)p.M * p.N;
+            f.splits = splits; f.sums = sums;
+        }
+        e = run(HgCfg<64, 64>{}, splits);
+    } else {
+        // (128x128 tiles as in the grouped product)
+        bool large = false;
+        if constexpr (TB) large = ((p.M + 127LL) / 128) * ((p.N + 127LL) / 128) >= 256;
+        if constexpr (TB)
+            if (large) e = run(HgCfg<128, 128>{}, 1);
+        if (!large) e = run(HgCfg<64, 64>{}, 1);
+    }
+    if (e != hipSuccess) return e;
+    if (e = launch_narrow<BF, false>(p, narrow_args(p), stream); e != hipSuccess) return e;
+    return launch_finish<BF>(f, stream);
+}
+
 template <bool BF>
 hipError_t lora(const LoraProblem &p, hipStream_t stream)
 {
@@ -484,10 +527,8 @@ hipError_t lora(const LoraProblem &p, hipStream_t stream)
         }
         return p.transB ? lora_tiles<BF, true>(p, stream) : lora_tiles<BF, false>(p, stream);
     }
-    const hipError_t e = BF ? launch_bgemm(g, stream) : launch_hgemm(g, stream);
-    if (e != hipSuccess || p.adapters == 0) return e;
-    if (const hipError_t n = launch_narrow<BF, false>(p, narrow_args(p), stream); n != hipSuccess) return n;
-    return launch_finish<BF>(finish_args(p), stream);
+    if (p.adapters == 0) return BF ? launch_bgemm(g, stream) : launch_hgemm(g, stream);
+    return p.transB ? lora_any<BF, true>(p, stream) : lora_any<BF, false>(p, stream);
 }
 
 }  // namespace

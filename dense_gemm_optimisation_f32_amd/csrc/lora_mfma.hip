@@ -160,31 +160,34 @@ __device__ __forceinline__ void narrow_block(const NarrowArgs &p, unsigned char 
         }
     } else {
         if (wave != 0) return;
-        f32x4v s[NR];
-        float most = 0.f;
+        auto sum = [&](int n) {
+            f32x4v v = part[n * 64 + lane];
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            s[n] = part[n * 64 + lane];
-#pragma unroll
-            for (int w = 1; w < NW; ++w) s[n] += part[(w * NR + n) * 64 + lane];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) most = fmaxf(most, fabsf(s[n][e]));
-        }
-        most = fmaxf(most, __shfl_xor(most, 16));
-        most = fmaxf(most, __shfl_xor(most, 32));
+            for (int w = 1; w < NW; ++w) v += part[(w * NR + n) * 64 + lane];
+            return v;
+        };
         int ex = 0;
-        if (!BF && most > 0.f && most < INFINITY) {
-            (void)frexpf(most, &ex);   // most = m 2^ex, 1/2 <= m < 1
-            ex -= 15;
+        if constexpr (!BF) {
+            float most = 0.f;
+            for (int n = 0; n < NR; ++n) {
+                const f32x4v v = sum(n);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) most = fmaxf(most, fabsf(v[e]));
+            }
+            most = fmaxf(most, __shfl_xor(most, 16));
+            most = fmaxf(most, __shfl_xor(most, 32));
+            if (most > 0.f && most < INFINITY) {
+                (void)frexpf(most, &ex);   // most = m 2^ex, 1/2 <= m < 1
+                ex -= 15;
+            }
         }
         if (mine != a) return;
         if (lq == 0) p.factor[row] = ldexpf(p.scales ? p.scales[a] : 1.f, ex);
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            if (16 * n >= p.pitch) break;
+        for (int n = 0; 16 * n < p.pitch; ++n) {
+            const f32x4v v = sum(n);
             float rest[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) rest[e] = BF ? s[n][e] : ldexpf(s[n][e], -ex);
+            for (int e = 0; e < 4; ++e) rest[e] = BF ? v[e] : ldexpf(v[e], -ex);
 #pragma unroll
             for (int part_i = 0; part_i < kParts<BF>; ++part_i) {
                 uint16_t h[4];

@@ -14,6 +14,7 @@ namespace {
 // fewer than 2^32 threads, and a grid's second axis 65535 blocks.
 constexpr int kMaxTokens = 1 << 23;
 constexpr int kMaxCols = 1 << 25;
+constexpr int kMaxRows = 1 << 30;   // of a weight gradient: row numbers within a slice past the last stay ints
 
 bool misaligned(const void *p, uintptr_t align)
 {
@@ -88,7 +89,8 @@ int wgrad(int groups, int R, int M, int N, float alpha, const uint16_t *A, int a
           const uint16_t *B, int b_rows, int ldb, const int32_t *rowsB, const int32_t *offsets, float beta, float *C,
           int ldc, long long strideC, bool bf, hipStream_t stream)
 {
-    if (groups < 0 || R < 0 || M < 0 || N < 0 || a_rows < 0 || b_rows < 0 || groups > 65535) return GEMM_ERR_SIZE;
+    if (groups < 0 || R < 0 || M < 0 || N < 0 || a_rows < 0 || b_rows < 0 || groups > 65535 || R > kMaxRows)
+        return GEMM_ERR_SIZE;
     if (lda < (M > 1 ? M : 1) || ldb < (N > 1 ? N : 1) || ldc < (N > 1 ? N : 1)) return GEMM_ERR_LD;
     long long ea, eb, ec;
     if (!extent(a_rows, M, lda, &ea) || !extent(b_rows, N, ldb, &eb) || !extent(M, N, ldc, &ec)) return GEMM_ERR_SIZE;

@@ -266,10 +266,10 @@ int gemm_grouped_bf16_f32acc_ex(int transB, int groups, int R, int N, int K, flo
  * gemm_grouped_wgrad_*_f32acc -- the gradient in the groups' right operands:
  *     C_g <- alpha * sum over offsets[g] <= r < offsets[g+1] of A[rowsA[r],:]^T B[rowsB[r],:] + beta * C_g
  *   A : a_rows x M, lda >= max(1,M); B : b_rows x N, ldb >= max(1,N); rowsA, rowsB: R indices or
- *       NULL for r; a row outside its operand adds nothing.
+ *       NULL for r; outside the operand: a row of zeros.
  *   C : groups members M x N, strideC apart (at least (M-1)*ldc + N); an empty group's is
  *       beta * C_g.
- * For weights stored N x K swap the two operands.  groups <= 65535.
+ * For weights stored N x K swap the two operands.  groups <= 65535, R <= 2^30.
  */
 int gemm_grouped_wgrad_f16_f32acc(int groups, int R, int M, int N, float alpha,
                                   const uint16_t *A, int a_rows, int lda, const int32_t *rowsA,
@@ -315,7 +315,8 @@ int moe_combine_grad_bf16(int T, int k, int N, const float *dC, int lddc, const 
  *   ranks   : a rank per adapter (clamped to 0 .. rank), or NULL for rank; what LA and LB hold
  *             past an adapter's rank is not used.
  *   ids     : M int32 values; outside 0 .. adapters-1: no adapter for that row.
- * The narrow product A LA^T stays in fp32 precision.  M <= 2^23, N <= 2^25, 1 <= rank <= 128.
+ * The narrow product A LA^T stays in fp32 precision.  A row's result depends on its own
+ * adapter alone, whatever the others hold.  M <= 2^23, N <= 2^25, 1 <= rank <= 128.
  */
 int gemm_lora_f16_f32acc_ex(int transB, int M, int N, int K, int rank, int adapters, float alpha,
                             const uint16_t *A, int lda, const uint16_t *B, int ldb,

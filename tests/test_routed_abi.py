@@ -92,7 +92,7 @@ WGRAD = dict(groups=3, R=10, M=5, N=6, alpha=1.0, A=FAKE, a_rows=10, lda=5, rows
 @pytest.mark.parametrize("kw,want", [
     (dict(groups=-1), ESIZE), (dict(groups=65536), ESIZE), (dict(R=-1), ESIZE), (dict(M=-1), ESIZE), (dict(N=-1), ESIZE),
     (dict(a_rows=-1), ESIZE), (dict(b_rows=-1), ESIZE), (dict(lda=4), ELD), (dict(ldb=5), ELD), (dict(ldc=5), ELD),
-    (dict(strideC=29), ELD), (dict(strideC=-1), ELD), (dict(strideC=1 << 62), ESIZE),
+    (dict(R=(1 << 30) + 1), ESIZE), (dict(strideC=29), ELD), (dict(strideC=-1), ELD), (dict(strideC=1 << 62), ESIZE),
     (dict(A=None), ENULL), (dict(B=None), ENULL), (dict(C=None), ENULL), (dict(offsets=None), ENULL),
     (dict(A=FAKE + 1), EALIGN), (dict(B=FAKE + 1), EALIGN), (dict(C=FAKE + 2), EALIGN), (dict(rowsA=FAKE + 1), EALIGN),
     (dict(rowsB=FAKE + 2), EALIGN), (dict(groups=0, C=None), OK), (dict(M=0, C=None), OK),

@@ -619,6 +619,83 @@ def test_lora_narrow_product_outside_16_bits(M):
         assert torch.equal(C.cpu(), torch.full((M, N), K * 2.0 ** (2 * e) * r / 64))
 
 
+@pytest.mark.parametrize("M", [3, 40, 200])
+@pytest.mark.parametrize("K", [256, 255])
+def test_lora_rows_keep_apart(M, K):
+    """An adapter, or a row, that holds infinities and NaN reaches no other request's row."""
+    N, r, n = 136, 16, 3
+    g = torch.Generator().manual_seed(M)
+    mk = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    a, b, la, lb = mk(M, K), mk(N, K), mk(n, r, K), mk(n, N, r)
+    ids = (torch.arange(M) % n).to(I32).cuda()
+
+    def run():
+        C = torch.empty(M, N, device="cuda")
+        dg.gemm_lora_bf16_f32acc_ex(1, M, N, K, r, n, 1.0, a, K, b, K, la, K, r * K, lb, r, N * r, None, None, ids, 0.0, C, N)
+        done()
+        return C
+
+    want = run()
+    lb[1] = math.inf
+    la[1, 3:] = math.nan
+    got = run()
+    own = ids == 1
+    assert torch.isnan(got[own]).all() and torch.equal(got[~own], want[~own])
+    a[0] = math.nan
+    again = run()
+    assert torch.isnan(again[0]).all() and torch.equal(again[2::3], want[2::3]) and torch.equal(again[3::3], want[3::3])
+
+
+@pytest.mark.parametrize("M", [5, 100])
+def test_lora_without_adapters(M):
+    a, b, C = torch.ones(M, 64, dtype=torch.float16, device="cuda"), torch.ones(72, 64, dtype=torch.float16, device="cuda"), torch.ones(M, 72, device="cuda")
+    dg.gemm_lora_f16_f32acc_ex(1, M, 72, 64, 4, 0, 0.5, a, 64, b, 64, None, 64, 0, None, 4, 0, None, None, None, 2.0, C, 72)
+    done()
+    assert (C == 34).all()
+
+
+def test_offsets_past_32_bits():
+    """Rows a few MB apart, so that operands and results span more than 4 GiB each."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GiB of device memory")
+    far, M, K, N, G = (1 << 20) + 8, 2200, 128, 64, 3
+    g = torch.Generator().manual_seed(1)
+    A = torch.empty(M * far, dtype=torch.bfloat16, device="cuda").view(M, far)
+    A[:, :K] = torch.randint(-3, 4, (M, K), generator=g).to(torch.bfloat16)
+    a = A[:, :K].double()
+    off = torch.tensor([0, 700, 1500, M], dtype=I32, device="cuda")
+    rows = torch.randperm(M, generator=g).to(I32).cuda()
+    B = torch.empty(G << 30, dtype=torch.bfloat16, device="cuda")
+    w = torch.randint(-3, 4, (G, K, N), generator=g).to(torch.bfloat16).cuda()
+    for i in range(G):
+        B[i << 30 : (i << 30) + K * N] = w[i].reshape(-1)
+    C = torch.empty(M * far, device="cuda").view(M, far)
+    dg.gemm_grouped_bf16_f32acc_ex(0, G, M, N, K, 1.0, A, M, far, rows, B, N, 1 << 30, off, 0.0, C, far)
+    done()
+    pick = a[rows.long()]
+    want = torch.cat([pick[lo:hi] @ w[i].double() for i, (lo, hi) in enumerate(((0, 700), (700, 1500), (1500, M)))])
+    assert torch.equal(C[:, :N].double(), want)
+    # a group's few rows, streamed
+    few = torch.tensor([0, 2, 2, 5], dtype=I32, device="cuda")
+    C[:8, :N] = -1
+    dg.gemm_grouped_bf16_f32acc_ex(0, G, 5, N, K, 1.0, A, M, far, rows, B, N, 1 << 30, few, 0.0, C, far)
+    done()
+    assert torch.equal(C[:5, :N].double(), torch.cat([pick[:2] @ w[0].double(), pick[2:5] @ w[2].double()]))
+    D = torch.empty(G << 30, device="cuda")
+    y = torch.randint(-3, 4, (M, N), generator=g).to(torch.bfloat16).cuda()
+    dg.gemm_grouped_wgrad_bf16_f32acc(G, M, K, N, 1.0, A, M, far, rows, y, M, N, None, off, 0.0, D, N, 1 << 30)
+    done()
+    for i, (lo, hi) in enumerate(((0, 700), (700, 1500), (1500, M))):
+        assert torch.equal(D[i << 30 : (i << 30) + K * N].view(K, N).double(), pick[lo:hi].t() @ y[lo:hi].double())
+    del D, B
+    slots = torch.randperm(M, generator=g)[: 1100 * 2].view(1100, 2).to(I32).cuda()
+    out = torch.empty(1100, N, device="cuda")
+    C[:, :N] = torch.randint(-3, 4, (M, N), generator=g).float()
+    dg.moe_combine_f32(1100, 2, N, C, M, far, slots, None, 0.0, out, N)
+    done()
+    assert torch.equal(out, C[slots[:, 0].long(), :N] + C[slots[:, 1].long(), :N])
+
+
 def test_lora_no_product():
     c = torch.randn(5, 6)
     nan = torch.full((64,), math.nan, dtype=torch.float16, device="cuda")

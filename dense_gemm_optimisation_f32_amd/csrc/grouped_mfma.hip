@@ -20,6 +20,10 @@ __global__ __launch_bounds__(Cfg::NT) void grouped_stream_kernel(RaggedArgs p)
     stream_tile<Cfg, BF, kGrouped, TB>(p, lds, blockIdx.x, 0, 1);
 }
 
+// C of so many bytes goes past the caches.  The memory-side cache holds 256 MiB: with C of 128 MiB the product and
+// the kernel that reads C next take 177 us together and 183 with such stores, with 256 MiB 351 and 346.
+constexpr long long kPastCache = 192LL << 20;
+
 RaggedArgs grouped_args(const GroupedProblem &q)
 {
     RaggedArgs a = {};
@@ -30,6 +34,7 @@ RaggedArgs grouped_args(const GroupedProblem &q)
     a.offsets = q.offsets;
     a.C = q.C; a.ldc = q.ldc;
     a.product = q.K > 0;
+    a.past_cache = 4LL * q.R * q.N >= kPastCache;
     return a;
 }
 RaggedArgs wgrad_args(const WgradProblem &q)
@@ -42,6 +47,7 @@ RaggedArgs wgrad_args(const WgradProblem &q)
     a.offsets = q.offsets;
     a.C = q.C; a.ldc = q.ldc; a.strideC = q.strideC;
     a.product = q.R > 0;
+    a.past_cache = 4LL * q.M * q.N * q.groups >= kPastCache;
     return a;
 }
 

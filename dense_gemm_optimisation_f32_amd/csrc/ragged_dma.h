@@ -126,6 +126,7 @@ struct RaggedArgs {
     long long ldc, strideC;
     int tiles_m, tiles_n;
     bool product;             // false: C is only scaled
+    bool past_cache;          // C is larger than what the memory-side cache keeps of it
     AdapterArgs ad;           // lora
 };
 
@@ -496,6 +497,8 @@ __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
     // part of the ring (free once every wave is past the barrier) and writes whole row
     // segments of its tile, TN * 4 bytes each.  16-byte chunk c of staged row r sits at
     // chunk c ^ (r % LPR), which keeps both directions off each other's banks.
+    // past_cache: stores that leave the caches to A and B (32768 x 2048 x 2048 over 32 groups 332 -> 305 us, weight
+    // gradients of 32 x 2048 x 1024 128 -> 108), where C is not kept for its reader anyway.
     const float alpha = p.alpha, beta = p.beta;
     constexpr int LPR = Cfg::TN / 4, RPI = 64 / LPR, NQ = 32 / RPI;
     static_assert(Cfg::NW * 32 * Cfg::TN * 4 <= S * Cfg::STAGE_BYTES, "staging area exceeds the ring");
@@ -588,6 +591,10 @@ __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
 #pragma unroll
             for (int q = 0; q < NQ; ++q)
                 store_row4<true, true>(C, ldc, first + q * RPI + er, col, v[q], alpha, beta, m_end, N);
+        } else if (first + 32 <= m_end && n0 + BN <= N && p.past_cache) {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+                __builtin_nontemporal_store(alpha * v[q], reinterpret_cast<f32x4_g *>(C + (long long)(first + q * RPI + er) * ldc + col));
         } else if (first + 32 <= m_end && n0 + BN <= N) {
 #pragma unroll
             for (int q = 0; q < NQ; ++q) store_row4<false, false>(C, ldc, first + q * RPI + er, col, v[q], alpha, beta, m_end, N);

@@ -696,6 +696,30 @@ def test_offsets_past_32_bits():
     assert torch.equal(out, C[slots[:, 0].long(), :N] + C[slots[:, 1].long(), :N])
 
 
+def test_results_larger_than_the_caches():
+    """C of more than 192 MiB, whose whole tiles are stored past the caches: every element."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    ints = lambda *s: torch.randint(-3, 4, s, generator=g, device="cuda").to(torch.float16)  # noqa: E731
+    G, R, N, K = 3, 49300, 1032, 72
+    a, b = ints(R, K), ints(G, K, N)
+    off = torch.tensor([0, 20001, 20001, R], dtype=I32, device="cuda")
+    C = torch.full((R, N), math.nan, device="cuda")
+    dg.gemm_grouped_f16_f32acc_ex(0, G, R, N, K, 2.0, a, R, K, None, b, N, K * N, off, 0.0, C, N)
+    done()
+    assert torch.equal(C[:20001], 2 * (a[:20001].float() @ b[0].float()))
+    assert torch.equal(C[20001:], 2 * (a[20001:].float() @ b[2].float()))
+    del C
+    G, R, M, N = 13, 300, 2048, 2040
+    x, y = ints(R, M), ints(R, N)
+    off = torch.linspace(0, R, G + 1).to(I32).cuda()
+    D = torch.full((G, M, N), math.nan, device="cuda")
+    dg.gemm_grouped_wgrad_f16_f32acc(G, R, M, N, 1.0, x, R, M, None, y, R, N, None, off, 0.0, D, N, M * N)
+    done()
+    at = off.tolist()
+    for i in range(G):
+        assert torch.equal(D[i], x[at[i] : at[i + 1]].float().t() @ y[at[i] : at[i + 1]].float())
+
+
 def test_lora_no_product():
     c = torch.randn(5, 6)
     nan = torch.full((64,), math.nan, dtype=torch.float16, device="cuda")

@@ -310,6 +310,7 @@ def gemm_batched_bf16_f32acc_ex(transA, transB, M, N, K, alpha, A, lda, strideA,
 # marshalling is kept short: one test of an operand's properties where all is as
 # expected, sizes of workspaces remembered by the sizes they belong to.
 _torch = None
+_Tensor = _device = _raw_stream = None   # torch.Tensor; the current device's index; its current stream's handle
 _DTYPES = {}
 
 
@@ -321,9 +322,10 @@ class _Elsewhere(Exception):
 
 
 def _load_torch():
-    global _torch
+    global _torch, _Tensor, _device, _raw_stream
     import torch
 
+    _Tensor, _device, _raw_stream = torch.Tensor, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _DTYPES.update(float32=torch.float32, float16=torch.float16, bfloat16=torch.bfloat16, int32=torch.int32)
     _torch = torch
     return torch
@@ -348,21 +350,20 @@ def _on_operands_device(fn):
 
 
 def _strided(x, name: str, dtype_name: str, need: int, packed: bool = False):
-    """Device address of an operand of which the call reads or writes ``need`` elements (see _ptr); the short way is a
-    contiguous tensor that holds them."""
-    if x is None or type(x) is int:
+    """Device address of an operand of which the call reads or writes ``need`` elements; the short way is a contiguous
+    tensor on the current device that holds them."""
+    if type(x) is _Tensor:
+        if (x.is_cuda and x.dtype is _DTYPES[dtype_name] and x.numel() >= need and x.is_contiguous()
+                and x.get_device() == _device()):
+            return x.data_ptr()
+    elif x is None or type(x) is int:
         return x
     torch = _torch or _load_torch()
-    if isinstance(x, torch.Tensor):
-        dev = x.get_device()
-        if dev >= 0:
-            if dev != torch._C._cuda_getDevice():
-                raise _Elsewhere(dev)
-            if x.is_contiguous():
-                if x.dtype is _DTYPES[dtype_name] and x.numel() >= need:
-                    return x.data_ptr()
-            elif packed:
-                raise ValueError(f"{name} must be contiguous")
+    if isinstance(x, torch.Tensor) and x.is_cuda:
+        if x.get_device() != _device():
+            raise _Elsewhere(x.get_device())
+        if packed and not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
     return _ptr(x, name, "torch." + dtype_name, need)
 
 
@@ -376,8 +377,9 @@ def _call(fn, args, stream, workspace=None, workspace_bytes=None) -> None:
     workspace: the caller's, or one that torch's allocator hands out for that stream (graph capture included) and
     takes back in its order."""
     if stream is None:
-        torch = _torch or _load_torch()
-        h = torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if _torch is None:
+            _load_torch()
+        h = _raw_stream(_device())
     else:
         h = _stream(stream)
     if workspace_bytes is None:
@@ -386,7 +388,7 @@ def _call(fn, args, stream, workspace=None, workspace_bytes=None) -> None:
         if workspace is None and workspace_bytes > 0:
             torch = _torch or _load_torch()
             if stream is None:
-                workspace = torch.empty(workspace_bytes, dtype=torch.uint8, device="cuda")
+                workspace = torch.empty(workspace_bytes, dtype=torch.uint8, device="cuda")   # (the current device)
             else:
                 with torch.cuda.stream(torch.cuda.ExternalStream(h)):
                     workspace = torch.empty(workspace_bytes, dtype=torch.uint8, device="cuda")
@@ -408,6 +410,11 @@ def _room(workspace, need: int):
     return at, st.nbytes() - (at - st.data_ptr())
 
 
+@functools.lru_cache(maxsize=None)
+def _function(name: str):
+    return getattr(load_library(), name)
+
+
 @functools.lru_cache(maxsize=1024)
 def moe_route_workspace(T, E, k) -> int:
     """Bytes of workspace moe_route_f32 needs for its sorted choices (0: none)."""
@@ -424,7 +431,7 @@ def moe_route_f32(T, E, logits, ldl, bias, score, groups, group_k, group_top, k,
             _packed(weights, "weights", "float32", n), _packed(offsets, "offsets", "int32", E + 1),
             _packed(rows, "rows", "int32", n), _packed(slots, "slots", "int32", n))
     need = moe_route_workspace(T, E, k) if offsets is not None else 0
-    _call(load_library().moe_route_f32, args, stream, workspace, need)
+    _call(_function("moe_route_f32"), args, stream, workspace, need)
 
 
 @_on_operands_device
@@ -434,7 +441,7 @@ def moe_route_f32_grad(T, E, logits, ldl, score, k, renorm, scale, ids, dweights
     args = (T, E, _strided(logits, "logits", "float32", _extent(T, E, ldl)), ldl, int(score), k, int(renorm), scale,
             _packed(ids, "ids", "int32", n), _packed(dweights, "dweights", "float32", n),
             _strided(dlogits, "dlogits", "float32", _extent(T, E, lddl)), lddl)
-    _call(load_library().moe_route_f32_grad, args, stream)
+    _call(_function("moe_route_f32_grad"), args, stream)
 
 
 def _grouped(t, dtype_name, transB, groups, R, N, K, alpha, A, M, lda, rows, B, ldb, strideB, offsets, beta, C, ldc, stream):
@@ -446,7 +453,7 @@ def _grouped(t, dtype_name, transB, groups, R, N, K, alpha, A, M, lda, rows, B, 
             _packed(rows, "rows", "int32", R if reads else 0), _strided(B, "B", dtype_name, b if reads else 0), ldb, strideB,
             _packed(offsets, "offsets", "int32", groups + 1 if work else 0), beta,
             _strided(C, "C", "float32", _extent(R, N, ldc)), ldc)
-    _call(getattr(load_library(), f"gemm_grouped_{t}_f32acc_ex"), args, stream)
+    _call(_function(f"gemm_grouped_{t}_f32acc_ex"), args, stream)
 
 
 @_on_operands_device
@@ -475,7 +482,7 @@ def _wgrad(t, dtype_name, groups, R, M, N, alpha, A, a_rows, lda, rowsA, B, b_ro
             _packed(rowsB, "rowsB", "int32", R if reads else 0),
             _packed(offsets, "offsets", "int32", groups + 1 if reads else 0), beta,
             _strided(C, "C", "float32", _extent(M, N, ldc) + (groups - 1) * strideC if work else 0), ldc, strideC)
-    _call(getattr(load_library(), f"gemm_grouped_wgrad_{t}_f32acc"), args, stream)
+    _call(_function(f"gemm_grouped_wgrad_{t}_f32acc"), args, stream)
 
 
 @_on_operands_device
@@ -501,7 +508,7 @@ def moe_combine_f32(T, k, N, Y, R, ldy, slots, weights, beta, C, ldc, stream=Non
     args = (T, k, N, _strided(Y, "Y", "float32", _extent(R, N, ldy) if n else 0), R, ldy,
             _packed(slots, "slots", "int32", n), _packed(weights, "weights", "float32", n), beta,
             _strided(C, "C", "float32", _extent(T, N, ldc)), ldc)
-    _call(load_library().moe_combine_f32, args, stream)
+    _call(_function("moe_combine_f32"), args, stream)
 
 
 def _combine_grad(t, dtype_name, T, k, N, dC, lddc, Y, R, ldy, slots, weights, dY, lddy, dweights, stream):
@@ -510,7 +517,7 @@ def _combine_grad(t, dtype_name, T, k, N, dC, lddc, Y, R, ldy, slots, weights, d
             _strided(Y, "Y", "float32", _extent(R, N, ldy) if n else 0), R, ldy, _packed(slots, "slots", "int32", n),
             _packed(weights, "weights", "float32", n), _strided(dY, "dY", dtype_name, _extent(R, N, lddy) if n else 0), lddy,
             _packed(dweights, "dweights", "float32", n))
-    _call(getattr(load_library(), f"moe_combine_grad_{t}"), args, stream)
+    _call(_function(f"moe_combine_grad_{t}"), args, stream)
 
 
 @_on_operands_device
@@ -534,7 +541,12 @@ def gemm_lora_workspace(M, N, K, rank) -> int:
 def _lora(t, dtype_name, transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb, LA, ldla, strideLA, LB, ldlb, strideLB, scales,
           ranks, ids, beta, C, ldc, workspace, stream):
     tB = int(transB)
-    na, nb, nc = _needs(M, N, K, alpha, lda, ldb, ldc, transB=tB)
+    na = nb = nc = 0
+    if M > 0 and N > 0:
+        nc = (M - 1) * ldc + N
+        if K > 0 and alpha != 0:
+            na = (M - 1) * lda + K
+            nb = (N - 1) * ldb + K if tB else (K - 1) * ldb + N
     thin = na > 0 and adapters > 0
     last = max(adapters - 1, 0)
     args = (tB, M, N, K, rank, adapters, alpha, _strided(A, "A", dtype_name, na), lda, _strided(B, "B", dtype_name, nb), ldb,
@@ -544,7 +556,7 @@ def _lora(t, dtype_name, transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb,
             _packed(ranks, "ranks", "int32", adapters if thin else 0),
             _packed(ids, "ids", "int32", M if thin else 0), beta, _strided(C, "C", "float32", nc), ldc)
     need = gemm_lora_workspace(M, N, K, rank) if thin else 0
-    _call(getattr(load_library(), f"gemm_lora_{t}_f32acc_ex"), args, stream, workspace, need)
+    _call(_function(f"gemm_lora_{t}_f32acc_ex"), args, stream, workspace, need)
 
 
 @_on_operands_device

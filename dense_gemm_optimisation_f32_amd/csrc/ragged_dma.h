@@ -833,12 +833,16 @@ __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const long long row = m0 + wm * Cfg::TM + 32 * i + lr;
+        // a row index outside A: a row of zeros, also where the group's weights hold infinities
+        const int at = KIND == kGrouped && p.rowsA && row < m_end ? p.rowsA[row] : 0;
+        const bool none = KIND == kGrouped && p.rowsA && (unsigned)at >= (unsigned)p.a_rows;
 #pragma unroll
         for (int x = 0; x < FN; ++x)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const long long col = n0 + wn * Cfg::TN + 32 * x + 8 * g + 4 * lk;
-                const f32x4_t v = {acc[i][x][4 * g], acc[i][x][4 * g + 1], acc[i][x][4 * g + 2], acc[i][x][4 * g + 3]};
+                f32x4_t v = {acc[i][x][4 * g], acc[i][x][4 * g + 1], acc[i][x][4 * g + 2], acc[i][x][4 * g + 3]};
+                if (none) v = f32x4_t{0.f, 0.f, 0.f, 0.f};
                 if (beta != 0.f)
                     store_row4<true, true>(C, ldc, row, col, v, alpha, beta, m_end, N);
                 else

@@ -245,8 +245,8 @@ int moe_route_f32_grad(int T, int E, const float *logits, int ldl, int score, in
  *     C[r,:] <- alpha * A[rows[r],:] * op(B_g) + beta * C[r,:]   for offsets[g] <= r < offsets[g+1]
  *   R, N, K : C is R x N, op(B_g) is K x N.
  *   A, M    : M x K, lda >= max(1,K).
- *   rows    : R int32 indices of rows of A, or NULL for r itself; outside 0 .. M-1: a row
- *             of zeros.
+ *   rows    : R int32 indices of rows of A, or NULL for r itself; outside 0 .. M-1: the row's
+ *             product is zeros, whatever B_g holds.
  *   B       : groups members strideB elements apart (0: one shared), each stored K x N
  *             (transB = 0, ldb >= max(1,N)) or N x K (transB = 1, ldb >= max(1,K)).
  *   offsets : groups + 1 ascending int32 values; they are clamped to 0 .. R.  Rows of C in no
@@ -266,7 +266,8 @@ int gemm_grouped_bf16_f32acc_ex(int transB, int groups, int R, int N, int K, flo
  * gemm_grouped_wgrad_*_f32acc -- the gradient in the groups' right operands:
  *     C_g <- alpha * sum over offsets[g] <= r < offsets[g+1] of A[rowsA[r],:]^T B[rowsB[r],:] + beta * C_g
  *   A : a_rows x M, lda >= max(1,M); B : b_rows x N, ldb >= max(1,N); rowsA, rowsB: R indices or
- *       NULL for r; outside the operand: a row of zeros.
+ *       NULL for r; outside the operand: a row of zeros (0 times an infinity is NaN here as
+ *       elsewhere: where the other operand may hold one, take its row out too).
  *   C : groups members M x N, strideC apart (at least (M-1)*ldc + N); an empty group's is
  *       beta * C_g.
  * For weights stored N x K swap the two operands.  groups <= 65535, R <= 2^30.

@@ -403,6 +403,21 @@ def test_grouped_no_product_and_bad_offsets(transB):
             assert (C[:8] == 4).all()
 
 
+@pytest.mark.parametrize("R,K,N", [(20, 64, 64), (200, 64, 128), (600, 128, 256), (20, 63, 65), (200, 63, 65), (200, 64, 65)])
+@pytest.mark.parametrize("transB", [0, 1])
+def test_grouped_rows_outside_meet_infinite_weights(transB, R, K, N):
+    rows = torch.arange(R, dtype=I32)
+    rows[::3], rows[1::7] = -1, R
+    b = torch.full((1, N, K) if transB else (1, K, N), math.inf, dtype=torch.float16)
+    a = torch.ones(R, K, dtype=torch.float16)
+    C = torch.full((R, N), math.nan, device="cuda")
+    off = torch.tensor([0, R], dtype=I32, device="cuda")
+    dg.gemm_grouped_f16_f32acc_ex(transB, 1, R, N, K, 1.0, a.cuda(), R, K, rows.cuda(), b.cuda(), K if transB else N, K * N, off, 0.0, C, N)
+    done()
+    out = ((rows < 0) | (rows >= R))
+    assert (C.cpu()[out] == 0).all() and (C.cpu()[~out] == math.inf).all()
+
+
 # ------------------------------------------------------------------ weight gradients
 def wgrad_check(t, G, R, M, N, *, how="skewed", ga=True, gb=False, alpha=1.0, beta=0.0, vals="pm1", pads=(0, 0, 0), offset=0, bad=False):
     rng = rng_of("wgrad", t, G, R, M, N, how, ga, gb, alpha, beta, vals, pads, offset, bad)

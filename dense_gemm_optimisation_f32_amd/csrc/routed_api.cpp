@@ -78,7 +78,7 @@ int grouped(int transB, int groups, int R, int N, int K, float alpha, const uint
     mi355gemm::GroupedProblem p;
     p.transB = transB; p.groups = groups; p.R = R; p.N = N; p.K = product ? K : 0;
     p.alpha = alpha; p.beta = beta;
-    p.A = A; p.M = M; p.lda = lda; p.rows = rows;
+    p.A = A; p.M = M; p.lda = lda; p.rows = product ? rows : nullptr;   // (not read without a product)
     p.B = B; p.ldb = ldb; p.strideB = strideB;
     p.offsets = offsets;
     p.C = C; p.ldc = ldc;

@@ -403,6 +403,18 @@ def test_grouped_no_product_and_bad_offsets(transB):
             assert (C[:8] == 4).all()
 
 
+def test_grouped_no_product_reads_no_rows():
+    # fewer row indices than rows of C: without a product none is read
+    off = torch.tensor([0, 5000], dtype=I32, device="cuda")
+    rows = torch.zeros(1, dtype=I32, device="cuda")
+    x = torch.zeros(64, dtype=torch.float16, device="cuda")
+    for K, M, alpha in ((0, 8, 1.0), (5, 8, 0.0), (5, 0, 1.0)):
+        C = torch.ones(5000, 6, device="cuda")
+        dg.gemm_grouped_f16_f32acc_ex(0, 1, 5000, 6, K, alpha, x, M, max(K, 1), rows, x, 6, 0, off, 3.0, C, 6)
+        done()
+        assert (C.cpu() == 3).all()
+
+
 @pytest.mark.parametrize("R,K,N", [(20, 64, 64), (200, 64, 128), (600, 128, 256), (20, 63, 65), (200, 63, 65), (200, 64, 65)])
 @pytest.mark.parametrize("transB", [0, 1])
 def test_grouped_rows_outside_meet_infinite_weights(transB, R, K, N):

@@ -834,8 +834,8 @@ __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
     for (int i = 0; i < FM; ++i) {
         const long long row = m0 + wm * Cfg::TM + 32 * i + lr;
         // a row index outside A: a row of zeros, also where the group's weights hold infinities
-        const int at = KIND == kGrouped && p.rowsA && row < m_end ? p.rowsA[row] : 0;
-        const bool none = KIND == kGrouped && p.rowsA && (unsigned)at >= (unsigned)p.a_rows;
+        const int at = KIND == kGrouped && p.rowsA && row < m_end ? p.rowsA[row] : (int)row;
+        const bool none = KIND == kGrouped && (unsigned)at >= (unsigned)p.a_rows;
 #pragma unroll
         for (int x = 0; x < FN; ++x)
 #pragma unroll

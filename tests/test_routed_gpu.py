@@ -428,6 +428,10 @@ def test_grouped_rows_outside_meet_infinite_weights(transB, R, K, N):
     done()
     out = ((rows < 0) | (rows >= R))
     assert (C.cpu()[out] == 0).all() and (C.cpu()[~out] == math.inf).all()
+    C.fill_(math.nan)   # without indices: rows of C past A's last
+    dg.gemm_grouped_f16_f32acc_ex(transB, 1, R, N, K, 1.0, a.cuda(), R - 7, K, None, b.cuda(), K if transB else N, K * N, off, 0.0, C, N)
+    done()
+    assert (C.cpu()[R - 7:] == 0).all() and (C.cpu()[:R - 7] == math.inf).all()
 
 
 # ------------------------------------------------------------------ weight gradients

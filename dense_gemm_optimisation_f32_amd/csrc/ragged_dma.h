@@ -725,13 +725,41 @@ __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
         for (int i = 0; i < TileA::LOADS; ++i)
             arow[i] = row_of(p.A, lda, KIND == kLora ? nullptr : p.rowsA, m0 + (i * NT + tid) / TileA::CPR, m_end, p.a_rows);
     }
+    // wgrad: the rows of the slice to load next, looked up a step before their loads and ahead of
+    // the loads of that step, so that waiting for an index does not wait for those
+    int na[TileA::LOADS], nb[TileB::LOADS];
+    auto look_up = [&](int k0) __attribute__((always_inline)) {
+        if constexpr (WG) {
+            const int end = k_lo + K;   // (K > 0)
+#pragma unroll
+            for (int i = 0; i < TileA::LOADS; ++i) {
+                const int r = k_lo + k0 + (i * NT + tid) / TileA::CPR, in = r < end ? r : end - 1;
+                const int at = p.rowsA ? p.rowsA[in] : in;
+                na[i] = r < end ? at : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < TileB::LOADS; ++i) {
+                const int r = k_lo + k0 + (i * NT + tid) / TileB::CPR, in = r < end ? r : end - 1;
+                const int at = p.rowsB ? p.rowsB[in] : in;
+                nb[i] = r < end ? at : -1;
+            }
+        }
+    };
     auto load_tiles = [&](int k0, Words *ra, Words *rb) __attribute__((always_inline)) {
+        int ia[TileA::LOADS], ib[TileB::LOADS];
+        if constexpr (WG) {
+#pragma unroll
+            for (int i = 0; i < TileA::LOADS; ++i) ia[i] = na[i];
+#pragma unroll
+            for (int i = 0; i < TileB::LOADS; ++i) ib[i] = nb[i];
+            look_up(k0 + BK);
+        }
 #pragma unroll
         for (int i = 0; i < TileA::LOADS; ++i) {
             const int id = i * NT + tid;
-            const int r = id / TileA::CPR, c = (id % TileA::CPR) * 8;
+            const int c = (id % TileA::CPR) * 8;
             if constexpr (WG)
-                words(row_of(p.A, lda, p.rowsA, k_lo + k0 + r, k_lo + K, p.a_rows), m0 + c, p.M, m0 + BM <= p.M, &ra[i]);
+                words((unsigned)ia[i] < (unsigned)p.a_rows ? p.A + (long long)ia[i] * lda : nullptr, m0 + c, p.M, m0 + BM <= p.M, &ra[i]);
             else
                 words(arow[i], k0 + c, K, k0 + BK <= K, &ra[i]);
         }
@@ -740,7 +768,7 @@ __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
             const int id = i * NT + tid;
             const int r = id / TileB::CPR, c = (id % TileB::CPR) * 8;
             if constexpr (WG)
-                words(row_of(p.B, ldb, p.rowsB, k_lo + k0 + r, k_lo + K, p.b_rows), n0 + c, N, n0 + BN <= N, &rb[i]);
+                words((unsigned)ib[i] < (unsigned)p.b_rows ? p.B + (long long)ib[i] * ldb : nullptr, n0 + c, N, n0 + BN <= N, &rb[i]);
             else if constexpr (TB)
                 words(n0 + r < N ? B + (long long)(n0 + r) * ldb : nullptr, k0 + c, K, k0 + BK <= K, &rb[i]);
             else
@@ -800,6 +828,7 @@ __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
     const int slices = (K + BK - 1) / BK;
     const int parts = KIND == kLora ? (int)gridDim.y : 1, part = KIND == kLora ? (int)blockIdx.y : 0;
     const int s0 = (int)((long long)slices * part / parts), nk = (int)((long long)slices * (part + 1) / parts);
+    if (s0 < nk) look_up(s0 * BK);
 #pragma unroll
     for (int d = 0; d < AHEAD; ++d)
         if (s0 + d < nk) load_tiles((s0 + d) * BK, ra[d], rb[d]);

@@ -71,13 +71,15 @@ __device__ __forceinline__ T wave_sum(T v)
     return wave_reduce(v, T(0), [](T a, T b) { return a + b; });
 }
 // Sums over the lanes up to and including one's own.
-__device__ __forceinline__ int wave_scan(int v, int lane)
+__device__ __forceinline__ int wave_scan(int v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(v, d);
-        if (lane >= d) v += o;
-    }
+    auto add = [&](unsigned o) { v += (int)o; };
+    add(dpp<0x111, 0xF>(0u, (unsigned)v));
+    add(dpp<0x112, 0xF>(0u, (unsigned)v));
+    add(dpp<0x114, 0xF>(0u, (unsigned)v));
+    add(dpp<0x118, 0xF>(0u, (unsigned)v));
+    add(dpp<0x142, 0xA>(0u, (unsigned)v));
+    add(dpp<0x143, 0xC>(0u, (unsigned)v));
     return v;
 }
 
@@ -526,12 +528,12 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteProblem p, int chunk, in
         for (int e0 = 0; e0 < per; e0 += 64) {
             const int e = e0 + lane;
             const int v = e < per ? total[e] : 0;
-            const int s = wave_scan(v, lane);
+            const int s = wave_scan(v);
             if (e < per) {
                 total[e] = carry + s - v;
                 p.offsets[e] = carry + s - v;
             }
-            carry += __shfl(s, 63);
+            carry += __builtin_amdgcn_readlane(s, 63);
         }
     }
     if (alone) __syncthreads();
@@ -552,31 +554,37 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteProblem p, int chunk, in
 
 // The chunks' counts (chunks rows of E + 1) to the counts before each chunk, in
 // place, and their totals as one more row.  A block takes 64 experts, one per
-// lane; its waves share the chunks.
+// lane; its waves take 16 chunks each in turn, read at once.
 __global__ __launch_bounds__(1024) void prefix_kernel(RouteProblem p, int chunks)
 {
+    constexpr int PW = 16;   // chunks per wave and turn
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int per = p.E + 1, e = blockIdx.x * 64 + lane;
-    __shared__ int part[16][64];
-    const int each = (chunks + 15) / 16;
-    const int b0 = wave * each, b1 = b0 + each < chunks ? b0 + each : chunks;
-    int sum = 0;
-    if (e < per)
-#pragma unroll 8
-        for (int b = b0; b < b1; ++b) sum += p.counts[(long long)b * per + e];
-    part[wave][lane] = sum;
-    __syncthreads();
-    if (e >= per) return;
-    int run = 0;
-    for (int w = 0; w < wave; ++w) run += part[w][lane];
-#pragma unroll 8
-    for (int b = b0; b < b1; ++b) {
-        int32_t *at = p.counts + (long long)b * per + e;
-        const int v = *at;
-        *at = run;
-        run += v;
+    __shared__ int part[2][16][64];   // (two: one barrier a turn)
+    int carry = 0;
+    for (int b0 = 0, turn = 0; b0 < chunks; b0 += 16 * PW, turn ^= 1) {
+        const int first = b0 + wave * PW;
+        int v[PW], sum = 0;
+#pragma unroll
+        for (int i = 0; i < PW; ++i) v[i] = e < per && first + i < chunks ? p.counts[(long long)(first + i) * per + e] : 0;
+#pragma unroll
+        for (int i = 0; i < PW; ++i) sum += v[i];
+        part[turn][wave][lane] = sum;
+        __syncthreads();
+        int run = carry;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) {
+            const int s = part[turn][w][lane];
+            run += w < wave ? s : 0;
+            carry += s;
+        }
+#pragma unroll
+        for (int i = 0; i < PW; ++i) {
+            if (e < per && first + i < chunks) p.counts[(long long)(first + i) * per + e] = run;
+            run += v[i];
+        }
     }
-    if (wave == 15) p.counts[(long long)chunks * per + e] = run;
+    if (wave == 0 && e < per) p.counts[(long long)chunks * per + e] = carry;
 }
 
 // Local numbers to rows.  PREFIXED: prefix_kernel has run; otherwise each block
@@ -586,6 +594,11 @@ __global__ __launch_bounds__(1024) void place_kernel(RouteProblem p, int chunk, 
 {
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, k = p.k, E = p.E, per = E + 1;
     __shared__ int base[kMaxExperts + 2], total[kMaxExperts + 2];
+    const int t0 = blockIdx.x * chunk, t1 = t0 + chunk < p.T ? t0 + chunk : p.T;
+    // a thread's choice (a block has at most 1024), on its way while the counts are added up
+    const int i = t0 * k + tid;
+    const bool has = i < t1 * k;
+    const int id = has ? p.ids[i] : -1, local = has ? p.slots[i] : 0;
     if constexpr (PREFIXED) {
         for (int e = tid; e < per; e += 1024) {
             base[e] = p.counts[(long long)blockIdx.x * per + e];
@@ -615,23 +628,21 @@ __global__ __launch_bounds__(1024) void place_kernel(RouteProblem p, int chunk, 
         for (int e0 = 0; e0 < per; e0 += 64) {
             const int e = e0 + lane;
             const int v = e < per ? total[e] : 0;
-            const int s = wave_scan(v, lane);
+            const int s = wave_scan(v);
             if (e < per) {
                 base[e] += carry + s - v;
                 if (blockIdx.x == 0) p.offsets[e] = carry + s - v;
             }
-            carry += __shfl(s, 63);
+            carry += __builtin_amdgcn_readlane(s, 63);
         }
     }
     __syncthreads();
-    const int t0 = blockIdx.x * chunk, t1 = t0 + chunk < p.T ? t0 + chunk : p.T;
-    for (int i = t0 * k + tid; i < t1 * k; i += 1024) {
-        const int e = p.ids[i];
-        const int at = base[e < 0 ? E : e] + p.slots[i];
-        p.slots[i] = e < 0 ? -1 : at;
-        p.rows[at] = e < 0 ? -1 : i / k;
-    }
+    if (!has) return;
+    const int at = base[id < 0 ? E : id] + local;
+    p.slots[i] = id < 0 ? -1 : at;
+    p.rows[at] = id < 0 ? -1 : i / k;
 }
+static_assert(kChunkIds <= 1024, "place_kernel: a choice per thread");
 
 // Tokens per block.  One block for a few tokens (one launch); else 16 tokens or
 // more, such that 256 blocks hold all of them while a block's choices fit

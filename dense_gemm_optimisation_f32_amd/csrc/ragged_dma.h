@@ -173,6 +173,12 @@ enum RaggedKind { kGrouped, kWgrad, kLora };
 // == 0 for the others, so that no 16-byte chunk straddles an edge; 64 (BN) rows of B
 // below 2^31 bytes apart.  K may be anything else.
 // TB: B stored N x K (not wgrad).  GA, GB: the rows of A, B are looked up (wgrad).
+//
+// Bound by the matrix cores, as the whole-matrix kernel is, less what part-filled tiles take.  Measured, bf16, whole
+// calls back to back: 32768 gathered rows over 32 unequal groups, 2048 x 2048, B stored K x N: 305 us, 901 TFLOP/s;
+// weight gradients of 16384 rows over 32 groups, 2048 x 1024: 109-114 us, 603-630 TFLOP/s (its 268 MB of C are 57 us
+// of a copy's time); 4096 rows with adapters of rank 16, 4096 x 4096: 124 us of tiles.  Two other tile
+// shapes for the weight gradient: 128x256 138, 256x128 133, against 127 for 256x256 before C's stores left the caches.
 template <class Cfg, bool BF, int KIND, bool TB, bool GA, bool GB>
 __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
 {
@@ -658,6 +664,9 @@ __device__ __forceinline__ u32x4 value8(const Words &x, long long c, long long c
 // rows) outermost.  kLora: workgroup blockIdx.y takes its share of the slices, and
 // with several the plain sums go to C + blockIdx.y * strideC.
 // 64x64 tiles, or 128x128 (half the loads per product, the launchers say where).
+// Bound by its loads, five dwords a chunk against one direct load, and at small sizes by one workgroup's chain of slices:
+// fp16, 1001 rows over 5 groups, 777 x 513: 14 us (its bytes are 1.6 us of a copy);
+// weight gradients of 11725 rows over 8 groups, 640 x 913: 72 us, 190 TFLOP/s.
 template <class Cfg, bool BF, int KIND, bool TB>
 __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
 {
@@ -891,6 +900,9 @@ __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
 //   workgroup's slices goes to C + blockIdx.y * strideC (workspace), lora's last
 //   kernel adds them up.
 // Needs what ragged_dma_kernel needs.
+// Bound by reading the weights: 64 groups of 2048 x 1024, 2 rows each, bf16, N x K: 268 MB in 37 us back to back (a part of
+// the weights stays in the 256 MiB memory-side cache from one call to the next) and 47 with other weights
+// each call, 5.7 TB/s, where a copy reaches 4.7 (it writes half of what it moves).
 constexpr int kStreamBK = 64;
 
 // XOR of an MN-contiguous slice's chunks in row k, rows of CPR chunks: the four rows

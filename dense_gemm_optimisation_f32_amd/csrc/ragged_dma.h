@@ -6,6 +6,7 @@
 #include "routed_internal.h"
 #include "stage16.h"
 #include "tile_order.h"
+#include "wave.h"
 
 #include <type_traits>
 #include <utility>
@@ -38,11 +39,9 @@ __device__ __forceinline__ int count_row_tiles(const int32_t *offsets, int group
             group_rows(offsets, g0 + lane, R, &lo, &hi);
             n = (hi - lo + bm - 1) / bm;
         }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) n += __shfl_xor(n, d);
-        total += n;
+        total += (int)wave_sum((unsigned)n);
     }
-    return __builtin_amdgcn_readfirstlane(total);
+    return total;
 }
 __device__ __forceinline__ RowTile find_row_tile(const int32_t *offsets, int groups, int R, int bm, int want)
 {
@@ -53,20 +52,13 @@ __device__ __forceinline__ RowTile find_row_tile(const int32_t *offsets, int gro
             group_rows(offsets, g0 + lane, R, &lo, &hi);
             n = (hi - lo + bm - 1) / bm;
         }
-        int s = n;   // inclusive sum
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(s, d);
-            if (lane >= d) s += o;
-        }
+        const int s = wave_scan(n);
         const uint64_t hit = __ballot(want >= s - n && want < s);
         if (hit) {
-            const int at = __builtin_ctzll(hit);
-            const int first = __shfl(lo + (want - (s - n)) * bm, at);
-            return {__builtin_amdgcn_readfirstlane(g0 + at), __builtin_amdgcn_readfirstlane(first),
-                    __builtin_amdgcn_readfirstlane(__shfl(hi, at))};
+            const int at = __builtin_ctzll(hit), first = lo + (want - (s - n)) * bm;
+            return {g0 + at, __builtin_amdgcn_readlane(first, at), __builtin_amdgcn_readlane(hi, at)};
         }
-        want -= __builtin_amdgcn_readfirstlane(__shfl(s, 63));
+        want -= __builtin_amdgcn_readlane(s, 63);
     }
     return {-1, 0, 0};
 }

@@ -611,16 +611,20 @@ __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
 // that one again, so no load leaves the words the row occupies.  whole (the same in all
 // lanes): no chunk of this slice ends before its eighth column, so four of the dwords are
 // one load.  row == nullptr: zeros.
+// The pointers are named global: loads that may go to LDS too (flat ones, what a pointer
+// made of a number gives) count as LDS accesses, and every barrier would wait for them.
 struct Words {
     unsigned w[5], shift;
 };
+typedef const __attribute__((address_space(1))) unsigned *global_words;
+typedef const __attribute__((address_space(1))) u32x4_g *global_chunk;
 __device__ __forceinline__ void words(const uint16_t *row, long long c, long long cols, bool whole, Words *out)
 {
     const uintptr_t p = reinterpret_cast<uintptr_t>(row + c);
     if (whole) {
         const unsigned odd = row ? (unsigned)(p & 2) >> 1 : 0u;
-        const unsigned *at = row ? reinterpret_cast<const unsigned *>(p & ~(uintptr_t)3) : zero_chunk;
-        const u32x4 v = *reinterpret_cast<const u32x4_g *>(at);
+        const global_words at = (global_words)(row ? p & ~(uintptr_t)3 : reinterpret_cast<uintptr_t>(zero_chunk));
+        const u32x4 v = *(global_chunk)at;
 #pragma unroll
         for (int i = 0; i < 4; ++i) out->w[i] = v[i];
         out->w[4] = at[3 + odd];
@@ -630,7 +634,7 @@ __device__ __forceinline__ void words(const uint16_t *row, long long c, long lon
     const int valid = row == nullptr || c >= cols ? 0 : cols - c < 8 ? (int)(cols - c) : 8;
     const unsigned odd = valid > 0 ? (unsigned)(p & 2) >> 1 : 0u;
     const int last = valid > 0 ? ((int)odd + valid - 1) >> 1 : 0;
-    const unsigned *at = valid > 0 ? reinterpret_cast<const unsigned *>(p & ~(uintptr_t)3) : zero_chunk;
+    const global_words at = (global_words)(valid > 0 ? p & ~(uintptr_t)3 : reinterpret_cast<uintptr_t>(zero_chunk));
 #pragma unroll
     for (int i = 0; i < 5; ++i) out->w[i] = at[i < last ? i : last];
     out->shift = 16 * odd;

@@ -139,9 +139,9 @@ template <bool BF, bool TB>
 hipError_t grouped_any(const GroupedProblem &q, hipStream_t stream)
 {
     const double part = 0.5 * (q.groups < q.R ? q.groups : q.R);
-    // 128x128 tiles where they fill the chip and B is stored N x K (16 groups, 8000 rows, 1001 x 1001: 46 against
-    // 65 us; with half as many tiles 36.8 against 24.1); stored K x N their registers leave one wave per
-    // SIMD (100 against 80 us)
+    // 128x128 tiles where they fill the chip and B is stored N x K (16 groups, 8000 rows, 1001 x 1001, 564 tiles: 44
+    // against 62 us; 8 groups, 4000 rows, 777 x 1001, 282 tiles: 26 against 30; 2000 rows, 157 tiles: 22 against 17.5);
+    // stored K x N they gain nothing (564 tiles 76.3 against 75.6 us, 282 43 against 38)
     if constexpr (TB)
         if ((q.R / 128.0 + part) * ((q.N + 127) / 128) >= 256) return grouped_any_tiles<HgCfg<128, 128>, BF, TB>(q, stream);
     return grouped_any_tiles<HgCfg<64, 64>, BF, TB>(q, stream);
@@ -171,9 +171,10 @@ hipError_t wgrad(const WgradProblem &q, hipStream_t stream)
                            stream, a);
         return hipGetLastError();
     };
-    // 128x128 tiles, two on a CU, where there are that many (16384 rows, 512 x 1023, 32 groups: 69 against 83 us; with
-    // 320 tiles, 11725 rows, 640 x 913, 71 against 73; with 192, 6752 rows, 1024 x 341, 39 against 30)
-    if ((q.M + 127LL) / 128 * ((q.N + 127) / 128) * q.groups >= 512) return any(HgCfg<128, 128>{});
+    // 128x128 tiles where there are several for a CU (1024 tiles: 16384 rows, 512 x 1023, 32 groups 63.5 against 75 us,
+    // 4000 rows, 1001 x 1001, 16 groups 47 against 50; 560: 8000 rows, 513 x 777, 16 groups 45.5 against 41.5; 192: 6752
+    // rows, 1024 x 341, 8 groups 37 against 29)
+    if ((q.M + 127LL) / 128 * ((q.N + 127) / 128) * q.groups >= 768) return any(HgCfg<128, 128>{});
     return any(HgCfg<64, 64>{});
 }
 

@@ -660,11 +660,12 @@ __device__ __forceinline__ u32x4 value8(const Words &x, long long c, long long c
 // rows) outermost.  kLora: workgroup blockIdx.y takes its share of the slices, and
 // with several the plain sums go to C + blockIdx.y * strideC.
 // 64x64 tiles, or 128x128 (half the loads per product, the launchers say where).
-// Bound by its loads, five dwords a chunk against one direct load, and at small sizes by one workgroup's chain of slices:
-// fp16, 1001 rows over 5 groups, 777 x 513: 14 us (its bytes are 1.6 us of a copy);
-// weight gradients of 11725 rows over 8 groups, 640 x 913: 72 us, 190 TFLOP/s.
+// Bound by its loads through registers, two or five a chunk against one direct load, and at small sizes by one
+// workgroup's chain of slices: fp16, 1001 rows over 5 groups, 777 x 513: 10.8 us (its bytes are 1.6 us of a copy);
+// weight gradients of 11725 rows over 8 groups, 640 x 913: 68 us, 201 TFLOP/s.  Registers are held to what four (wgrad: three, its LDS allows no more) waves per SIMD
+// leave, or two with 128x128 tiles: else the sums were copied between register files in every slice.
 template <class Cfg, bool BF, int KIND, bool TB>
-__global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
+__global__ __launch_bounds__(256, Cfg::BM == 64 ? (KIND == kWgrad ? 3 : 4) : 2) void ragged_any_kernel(RaggedArgs p)
 {
     constexpr bool WG = KIND == kWgrad;
     constexpr int FM = Cfg::FM, FN = Cfg::FN;
@@ -750,7 +751,9 @@ __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
             }
         }
     };
-    auto load_tiles = [&](int k0, Words *ra, Words *rb) __attribute__((always_inline)) {
+    // whole: it is known that no chunk of the slice ends before its eighth column
+    auto load_tiles = [&](auto whole_c, int k0, Words *ra, Words *rb) __attribute__((always_inline)) {
+        constexpr bool WHOLE = decltype(whole_c)::value;
         int ia[TileA::LOADS], ib[TileB::LOADS];
         if constexpr (WG) {
 #pragma unroll
@@ -764,20 +767,20 @@ __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
             const int id = i * NT + tid;
             const int c = (id % TileA::CPR) * 8;
             if constexpr (WG)
-                words((unsigned)ia[i] < (unsigned)p.a_rows ? p.A + (long long)ia[i] * lda : nullptr, m0 + c, p.M, m0 + BM <= p.M, &ra[i]);
+                words((unsigned)ia[i] < (unsigned)p.a_rows ? p.A + (long long)ia[i] * lda : nullptr, m0 + c, p.M, WHOLE || m0 + BM <= p.M, &ra[i]);
             else
-                words(arow[i], k0 + c, K, k0 + BK <= K, &ra[i]);
+                words(arow[i], k0 + c, K, WHOLE || k0 + BK <= K, &ra[i]);
         }
 #pragma unroll
         for (int i = 0; i < TileB::LOADS; ++i) {
             const int id = i * NT + tid;
             const int r = id / TileB::CPR, c = (id % TileB::CPR) * 8;
             if constexpr (WG)
-                words((unsigned)ib[i] < (unsigned)p.b_rows ? p.B + (long long)ib[i] * ldb : nullptr, n0 + c, N, n0 + BN <= N, &rb[i]);
+                words((unsigned)ib[i] < (unsigned)p.b_rows ? p.B + (long long)ib[i] * ldb : nullptr, n0 + c, N, WHOLE || n0 + BN <= N, &rb[i]);
             else if constexpr (TB)
-                words(n0 + r < N ? B + (long long)(n0 + r) * ldb : nullptr, k0 + c, K, k0 + BK <= K, &rb[i]);
+                words(n0 + r < N ? B + (long long)(n0 + r) * ldb : nullptr, k0 + c, K, WHOLE || k0 + BK <= K, &rb[i]);
             else
-                words(k0 + r < K ? B + (long long)(k0 + r) * ldb : nullptr, n0 + c, N, n0 + BN <= N, &rb[i]);
+                words(k0 + r < K ? B + (long long)(k0 + r) * ldb : nullptr, n0 + c, N, WHOLE || n0 + BN <= N, &rb[i]);
         }
     };
     auto store_one = [&](auto tile, uint16_t *dst, int i, const u32x4 &v) {
@@ -789,18 +792,21 @@ __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
         else
             *reinterpret_cast<u32x4 *>(dst + r * T::PITCH + 8 * c) = v;
     };
-    auto store_tiles = [&](int buf, int k0, const Words *ra, const Words *rb) __attribute__((always_inline)) {
+    auto store_tiles = [&](auto whole_c, int buf, int k0, const Words *ra, const Words *rb) __attribute__((always_inline)) {
+        auto value = [&](const Words &x, long long c, long long cols) __attribute__((always_inline)) {
+            return value8(x, c, decltype(whole_c)::value ? c + 8 : cols);
+        };
         uint16_t *la = lds + buf * BUF_HALVES;
         uint16_t *lb = la + TileA::HALVES;
 #pragma unroll
         for (int i = 0; i < TileA::LOADS; ++i) {
             const int c = (i * NT + tid) % TileA::CPR * 8;
-            store_one(TileA{}, la, i, WG ? value8(ra[i], m0 + c, p.M) : value8(ra[i], k0 + c, K));
+            store_one(TileA{}, la, i, WG ? value(ra[i], m0 + c, p.M) : value(ra[i], k0 + c, K));
         }
 #pragma unroll
         for (int i = 0; i < TileB::LOADS; ++i) {
             const int c = (i * NT + tid) % TileB::CPR * 8;
-            store_one(TileB{}, lb, i, !WG && TB ? value8(rb[i], k0 + c, K) : value8(rb[i], n0 + c, N));
+            store_one(TileB{}, lb, i, !WG && TB ? value(rb[i], k0 + c, K) : value(rb[i], n0 + c, N));
         }
     };
     const int wave = tid >> 6, lane = tid & 63;
@@ -833,14 +839,10 @@ __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
     const int slices = (K + BK - 1) / BK;
     const int parts = KIND == kLora ? (int)gridDim.y : 1, part = KIND == kLora ? (int)blockIdx.y : 0;
     const int s0 = (int)((long long)slices * part / parts), nk = (int)((long long)slices * (part + 1) / parts);
-    if (s0 < nk) look_up(s0 * BK);
-#pragma unroll
-    for (int d = 0; d < AHEAD; ++d)
-        if (s0 + d < nk) load_tiles((s0 + d) * BK, ra[d], rb[d]);
-    auto step = [&](int t, Words *a, Words *b) __attribute__((always_inline)) {
+    auto step = [&](auto whole_c, bool load, int t, Words *a, Words *b) __attribute__((always_inline)) {
         const int buf = (t - s0) & 1;
-        store_tiles(buf, t * BK, a, b);
-        if (t + AHEAD < nk) load_tiles((t + AHEAD) * BK, a, b);
+        store_tiles(whole_c, buf, t * BK, a, b);
+        if (load) load_tiles(whole_c, (t + AHEAD) * BK, a, b);
         // one barrier a step: the buffer written next was last read in the step
         // before this one, which every wave has left when it passes here
         __syncthreads();
@@ -859,10 +861,26 @@ __global__ __launch_bounds__(256) void ragged_any_kernel(RaggedArgs p)
                 for (int x = 0; x < FN; ++x) acc[i][x] = mfma16<BF>(fb[x], fa[i], acc[i][x]);
         }
     };
-    for (int t = s0; t < nk; t += AHEAD)
+    // Whole slices first, a loop whose steps all issue the same loads without a branch, so that the
+    // waits for a slice's words leave the next slice's on their way; then the others.
+    const int wholes = WG || (!TB && n0 + BN > N) ? s0 : K / BK > nk ? nk : K / BK;
+    int t = s0;
+    if (s0 < nk) look_up(s0 * BK);
+    if (!WG && s0 + 2 * AHEAD <= wholes) {
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d) load_tiles(std::true_type{}, (s0 + d) * BK, ra[d], rb[d]);
+        for (; t + 2 * AHEAD <= wholes; t += AHEAD)
+#pragma unroll
+            for (int d = 0; d < AHEAD; ++d) step(std::true_type{}, true, t + d, ra[d], rb[d]);
+    } else {
 #pragma unroll
         for (int d = 0; d < AHEAD; ++d)
-            if (t + d < nk) step(t + d, ra[d], rb[d]);
+            if (s0 + d < nk) load_tiles(std::false_type{}, (s0 + d) * BK, ra[d], rb[d]);
+    }
+    for (; t < nk; t += AHEAD)
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d)
+            if (t + d < nk) step(std::false_type{}, t + d + AHEAD < nk, t + d, ra[d], rb[d]);
     const float alpha = parts > 1 ? 1.f : p.alpha, beta = parts > 1 ? 0.f : p.beta;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {

@@ -14,7 +14,7 @@ namespace {
 // fewer than 2^32 threads, and a grid's second axis 65535 blocks.
 constexpr int kMaxTokens = 1 << 23;
 constexpr int kMaxCols = 1 << 25;
-constexpr int kMaxRows = 1 << 30;   // of a weight gradient: row numbers within a slice past the last stay ints
+constexpr int kMaxSum = 1 << 30;   // a sum's length (K, or a weight gradient's R): positions in slices past the last stay ints
 
 bool misaligned(const void *p, uintptr_t align)
 {
@@ -61,7 +61,7 @@ int grouped(int transB, int groups, int R, int N, int K, float alpha, const uint
             float *C, int ldc, bool bf, hipStream_t stream)
 {
     if (!flag(transB)) return GEMM_ERR_OP;
-    if (groups < 0 || R < 0 || N < 0 || K < 0 || M < 0 || groups > 65535) return GEMM_ERR_SIZE;
+    if (groups < 0 || R < 0 || N < 0 || K < 0 || M < 0 || groups > 65535 || K > kMaxSum) return GEMM_ERR_SIZE;
     const long long b_rows = transB ? N : K, b_cols = transB ? K : N;
     if (lda < (K > 1 ? K : 1) || ldb < (b_cols > 1 ? b_cols : 1) || ldc < (N > 1 ? N : 1)) return GEMM_ERR_LD;
     long long ea, eb, ec;
@@ -89,7 +89,7 @@ int wgrad(int groups, int R, int M, int N, float alpha, const uint16_t *A, int a
           const uint16_t *B, int b_rows, int ldb, const int32_t *rowsB, const int32_t *offsets, float beta, float *C,
           int ldc, long long strideC, bool bf, hipStream_t stream)
 {
-    if (groups < 0 || R < 0 || M < 0 || N < 0 || a_rows < 0 || b_rows < 0 || groups > 65535 || R > kMaxRows)
+    if (groups < 0 || R < 0 || M < 0 || N < 0 || a_rows < 0 || b_rows < 0 || groups > 65535 || R > kMaxSum)
         return GEMM_ERR_SIZE;
     if (lda < (M > 1 ? M : 1) || ldb < (N > 1 ? N : 1) || ldc < (N > 1 ? N : 1)) return GEMM_ERR_LD;
     long long ea, eb, ec;
@@ -142,7 +142,7 @@ int combine_grad(int T, int k, int N, const float *dC, int lddc, const float *Y,
 
 bool lora_sizes_ok(int M, int N, int K, int rank)
 {
-    return M >= 0 && N >= 0 && K >= 0 && rank >= 1 && rank <= mi355gemm::kMaxRank && M <= kMaxTokens && N <= kMaxCols;
+    return M >= 0 && N >= 0 && K >= 0 && K <= kMaxSum && rank >= 1 && rank <= mi355gemm::kMaxRank && M <= kMaxTokens && N <= kMaxCols;
 }
 
 int lora(int transB, int M, int N, int K, int rank, int adapters, float alpha, const uint16_t *A, int lda,

@@ -251,7 +251,7 @@ int moe_route_f32_grad(int T, int E, const float *logits, int ldl, int score, in
  *             (transB = 0, ldb >= max(1,N)) or N x K (transB = 1, ldb >= max(1,K)).
  *   offsets : groups + 1 ascending int32 values; they are clamped to 0 .. R.  Rows of C in no
  *             group are left as they are.
- * With transB flipped this is also the gradient in A's rows.  groups <= 65535.
+ * With transB flipped this is also the gradient in A's rows.  groups <= 65535, K <= 2^30.
  */
 int gemm_grouped_f16_f32acc_ex(int transB, int groups, int R, int N, int K, float alpha,
                                const uint16_t *A, int M, int lda, const int32_t *rows,
@@ -317,7 +317,7 @@ int moe_combine_grad_bf16(int T, int k, int N, const float *dC, int lddc, const 
  *             past an adapter's rank is not used.
  *   ids     : M int32 values; outside 0 .. adapters-1: no adapter for that row.
  * The narrow product A LA^T stays in fp32 precision.  A row's result depends on its own
- * adapter alone, whatever the others hold.  M <= 2^23, N <= 2^25, 1 <= rank <= 128.
+ * adapter alone, whatever the others hold.  M <= 2^23, N <= 2^25, K <= 2^30, 1 <= rank <= 128.
  */
 int gemm_lora_f16_f32acc_ex(int transB, int M, int N, int K, int rank, int adapters, float alpha,
                             const uint16_t *A, int lda, const uint16_t *B, int ldb,

@@ -73,7 +73,7 @@ GROUPED = dict(transB=0, groups=3, R=10, N=6, K=5, alpha=1.0, A=FAKE, M=10, lda=
 @pytest.mark.parametrize("t", ["f16", "bf16"])
 @pytest.mark.parametrize("kw,want", [
     (dict(transB=2), EOP), (dict(groups=-1), ESIZE), (dict(groups=65536), ESIZE), (dict(R=-1), ESIZE), (dict(N=-1), ESIZE),
-    (dict(K=-1), ESIZE), (dict(M=-1), ESIZE), (dict(lda=4), ELD), (dict(ldb=5), ELD), (dict(transB=1, ldb=4), ELD),
+    (dict(K=-1), ESIZE), (dict(K=(1 << 30) + 1, lda=2**31 - 1), ESIZE), (dict(M=-1), ESIZE), (dict(lda=4), ELD), (dict(ldb=5), ELD), (dict(transB=1, ldb=4), ELD),
     (dict(transB=1, ldb=5, N=0), OK), (dict(ldc=5), ELD), (dict(strideB=-1), ELD), (dict(strideB=1 << 62), ESIZE),
     (dict(A=None), ENULL), (dict(B=None), ENULL), (dict(C=None), ENULL), (dict(offsets=None), ENULL),
     (dict(A=FAKE + 1), EALIGN), (dict(B=FAKE + 1), EALIGN), (dict(C=FAKE + 2), EALIGN), (dict(offsets=FAKE + 2), EALIGN),
@@ -134,7 +134,7 @@ LORA = dict(transB=0, M=4, N=6, K=5, rank=3, adapters=2, alpha=1.0, A=FAKE, lda=
 @pytest.mark.parametrize("t", ["f16", "bf16"])
 @pytest.mark.parametrize("kw,want", [
     (dict(transB=-1), EOP), (dict(M=-1), ESIZE), (dict(M=(1 << 23) + 1), ESIZE), (dict(N=-1), ESIZE), (dict(K=-1), ESIZE),
-    (dict(rank=0), ESIZE), (dict(rank=129, ldlb=129), ESIZE), (dict(adapters=-1), ESIZE),
+    (dict(K=(1 << 30) + 1, lda=2**31 - 1, ldla=2**31 - 1), ESIZE), (dict(rank=0), ESIZE), (dict(rank=129, ldlb=129), ESIZE), (dict(adapters=-1), ESIZE),
     (dict(lda=4), ELD), (dict(ldb=5), ELD), (dict(transB=1, ldb=4), ELD), (dict(ldc=5), ELD), (dict(ldla=4), ELD), (dict(ldlb=2), ELD),
     (dict(strideLA=-1), ELD), (dict(strideLB=-1), ELD), (dict(strideLA=1 << 62), ESIZE),
     (dict(A=None), ENULL), (dict(B=None), ENULL), (dict(C=None), ENULL), (dict(LA=None), ENULL), (dict(LB=None), ENULL),

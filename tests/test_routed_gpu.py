@@ -493,8 +493,8 @@ def test_wgrad_layouts(t):
     wgrad_check(t, 3, 200, 128, 256, bad=True, vals="int4")
     wgrad_check(t, 3, 200, 128, 256, ga=False, gb=False, vals="int4")
     wgrad_check(t, 2, 3000, 512, 768, gb=True)
-    wgrad_check(t, 33, 900, 509, 515, gb=True, vals="int4")                             # odd sizes, many tiles
-    wgrad_check(t, 33, 900, 509, 515, bad=True, beta=1.0)
+    wgrad_check(t, 40, 900, 509, 515, gb=True, vals="int4")                             # odd sizes, many tiles
+    wgrad_check(t, 40, 900, 509, 515, bad=True, beta=1.0)
 
 
 def test_wgrad_without_rows():

@@ -662,8 +662,9 @@ __device__ __forceinline__ u32x4 value8(const Words &x, long long c, long long c
 // 64x64 tiles, or 128x128 (half the loads per product, the launchers say where).
 // Bound by its loads through registers, two or five a chunk against one direct load, and at small sizes by one
 // workgroup's chain of slices: fp16, 1001 rows over 5 groups, 777 x 513: 10.8 us (its bytes are 1.6 us of a copy);
-// weight gradients of 11725 rows over 8 groups, 640 x 913: 68 us, 201 TFLOP/s.  Registers are held to what four (wgrad: three, its LDS allows no more) waves per SIMD
-// leave, or two with 128x128 tiles: else the sums were copied between register files in every slice.
+// weight gradients of 11725 rows over 8 groups, 640 x 913: 68 us, 201 TFLOP/s.  Registers are held to what
+// four waves per SIMD leave (wgrad: three, its LDS allows no more), or two with 128x128 tiles: else the
+// sums were copied between register files in every slice.
 template <class Cfg, bool BF, int KIND, bool TB>
 __global__ __launch_bounds__(256, Cfg::BM == 64 ? (KIND == kWgrad ? 3 : 4) : 2) void ragged_any_kernel(RaggedArgs p)
 {
@@ -914,9 +915,9 @@ __global__ __launch_bounds__(256, Cfg::BM == 64 ? (KIND == kWgrad ? 3 : 4) : 2) 
 //   workgroup's slices goes to C + blockIdx.y * strideC (workspace), lora's last
 //   kernel adds them up.
 // Needs what ragged_dma_kernel needs.
-// Bound by reading the weights: 64 groups of 2048 x 1024, 2 rows each, bf16, N x K: 268 MB in 37 us back to back (a part of
-// the weights stays in the 256 MiB memory-side cache from one call to the next) and 47 with other weights
-// each call, 5.7 TB/s, where a copy reaches 4.7 (it writes half of what it moves).
+// Bound by reading the weights: 64 groups of 2048 x 1024, 2 rows each, bf16, N x K: 268 MB in 35 us back to back (a part of
+// the weights stays in the 256 MiB memory-side cache from one call to the next) and 46 with other weights
+// each call, 5.9 TB/s, where a copy reaches 4.7 (it writes half of what it moves).
 constexpr int kStreamBK = 64;
 
 // XOR of an MN-contiguous slice's chunks in row k, rows of CPR chunks: the four rows

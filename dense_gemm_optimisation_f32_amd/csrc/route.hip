@@ -94,10 +94,11 @@ __device__ __forceinline__ void load_experts(const float *row, int lane, int E, 
 // kept or not, a choice before the next) is by more than the errors of what it compares;
 // else the token is done again in 64 bits.  With scores of some hundred experts spread over a
 // unit a few tokens in a thousand are.
-// Bound by instructions, not by its reads: 32768 tokens of 256 experts (8 of 8 groups of 32, 8 choices, bias,
-// sigmoid) take 41 us, their 33.6 MB 7.1 us at a copy's rate.  Of whole calls without the layout, 37 us: a round of the choice 2.0
-// us each, the groups 7, loads, scores, sort and weights 14.  Two waves per SIMD for every one (64 registers)
-// gave 39 us and a longer prefix.  16 tokens: 8.9 us, one token's chain of dependent steps.
+// Bound by instructions, not by its reads: 32768 tokens of 256 experts (the best 4 of 8 groups, 8 choices, bias,
+// sigmoid) take 41 us, their 33.6 MB 7.1 us at a copy's rate.  Of a call without the layout, 37 us, a round
+// of the choice takes 2.0 each, the groups 7, loads, scores, sort and weights 14.  Two waves per SIMD for
+// every one (64 registers) gave 39 us and a longer prefix.  16 tokens: 8.7 us, one token's chain of
+// dependent steps.
 constexpr float kLog2e = 1.44269504f;
 constexpr float kUnits = 1 << 27, kZero = 4.f * (1 << 27);   // key = score * kUnits + kZero; 0: unavailable
 // Error of a key: exp, sum and quotient 4e-6, the rounding of score + 4 2.4e-7, the place of
@@ -522,8 +523,8 @@ __global__ __launch_bounds__(1024) void prefix_kernel(RouteProblem p, int chunks
 }
 
 // Local numbers to rows.  PREFIXED: prefix_kernel has run; otherwise each block
-// adds up the counts of the chunks before its own, and of all of them.  262144 choices: 4.9 us, of which 3 MB moved
-// are 0.7: a chain of loads, a scan and scattered stores.
+// adds up the counts of the chunks before its own, and of all of them.  262144 choices: 4.9 us, of
+// which the 4 MB moved are 0.9: a chain of loads, a scan and scattered stores.
 template <bool PREFIXED>
 __global__ __launch_bounds__(1024) void place_kernel(RouteProblem p, int chunk, int chunks)
 {
@@ -626,8 +627,8 @@ hipError_t route_ne(const RouteProblem &p, hipStream_t stream)
 // Where near numbers are subtracted (renormalised) the k chosen values are formed in
 // 64 bits, all else in 32.  The k values reach their experts' lanes through a row
 // in LDS, of which a wave has one of its own (64 NE floats).
-// Bound by its bytes: 16384 tokens of 128 experts, softmax, 8 choices: 17.8 MB in 7.4 us, 2.4 TB/s (3.8 us at a copy's rate; the
-// rest is a launch's ramp and one token's chain of loads, reductions and stores).
+// Bound by its bytes: 16384 tokens of 128 experts, softmax, 8 choices: 17.8 MB in 7.4 us, 2.4 TB/s (3.8 us
+// at a copy's rate; the rest is a launch's ramp and one token's chain of loads, reductions and stores).
 template <int NE>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradProblem p)
 {
@@ -707,8 +708,9 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradProblem p)
 // ---------------------------------------------------------------- combining
 //
 // C[t,:] = sum_j w_j Y[slot_j,:] + beta C[t,:]: four columns per thread, the k
-// rows read independently of one another, added in the order of the choices.  Bound by its bytes (4096 tokens of 2048 columns, 8 choices:
-// 302 MB in 48 us, 6.3 TB/s, part of Y being in the memory-side cache still).
+// rows read independently of one another, added in the order of the choices.  Bound by its
+// bytes (4096 tokens of 2048 columns, 8 choices: 302 MB in 48 us, 6.3 TB/s, part of Y being in the
+// memory-side cache still; 61 us on other data each call).
 constexpr int kCombineCols = 1024;   // columns of a block of 256 threads
 
 __global__ __launch_bounds__(256) void combine_kernel(CombineProblem p)
@@ -754,8 +756,9 @@ typedef unsigned int u32x2_g __attribute__((ext_vector_type(2), aligned(4)));
 
 // dY[slot_j,:] = w_j dC[t,:] rounded once to 16 bits, which is what the experts'
 // gradient products take; dw_j = <dC[t,:], Y[slot_j,:]> summed in 32 bits: each
-// thread its columns, then the wave, then the block's four waves in order.  A block takes a token, so that dC's row is read once for
-// its k choices.  Bound by its bytes (8192 tokens of 1024 columns, 4 choices: 235 MB in 38.5 us, 6.1 TB/s).
+// thread its columns, then the wave, then the block's four waves in order.  A block takes a
+// token, so that dC's row is read once for its k choices.  Bound by its bytes (8192 tokens of 1024
+// columns, 4 choices: 235 MB in 38.5 us, 6.1 TB/s; 54 us on other data each call).
 template <bool BF>
 __global__ __launch_bounds__(256) void combine_grad_kernel(CombineGradProblem p)
 {

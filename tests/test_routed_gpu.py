@@ -204,6 +204,23 @@ def test_route_near_ties(score, seed):
         assert torch.equal(got, want), (got != want).any(1).nonzero()[:5]
 
 
+@pytest.mark.parametrize("T,E,k", [(20011, 100, 32), (70001, 40, 8), (9000, 1000, 32)])
+def test_route_many_choices(T, E, k):
+    """More runs of choices than one pass over their counts takes."""
+    x = torch.randn(T, E, generator=torch.Generator().manual_seed(T))
+    x[::5] = -math.inf                                            # padded tokens
+    got = {n: v.cpu().long() for n, v in route_call(x.cuda(), E, None, 0, 1, 1, 1, k, 1, 1.0, T, E).items()}
+    ids = torch.where(x[:, :1] == -math.inf, -1, x.sort(dim=1, descending=True, stable=True).indices[:, :k]).reshape(-1)
+    flat = torch.where(ids < 0, E, ids)
+    by = flat.sort(stable=True).indices
+    assert torch.equal(got["ids"], ids)
+    assert torch.equal(got["offsets"], torch.searchsorted(flat[by], torch.arange(E + 1)))
+    assert torch.equal(got["rows"], torch.where(flat[by] < E, by // k, -1))
+    slots = torch.empty_like(by)
+    slots[by] = torch.arange(T * k)
+    assert torch.equal(got["slots"], torch.where(flat < E, slots, -1))
+
+
 def test_route_without_layout_and_empty():
     x = dev(np.random.default_rng(5).standard_normal((300, 32)).astype(np.float32))
     a = route_call(x, 32, None, 0, 1, 1, 1, 4, 1, 1.0, 300, 32)

@@ -163,15 +163,14 @@ __device__ __forceinline__ bool choose32(const RouteProblem &p, const float *x, 
         for (int i = 0; i < NE; ++i) key[i] = kept ? key[i] : 0u;
     }
     unsigned gap = ~0u, last = ~0u;
-    for (int j = 0; j <= p.k; ++j) {
-        const unsigned top = wave_max(key[0]);
-        if (top == 0) break;
+    uint64_t twice = 0;   // two lanes' keys were equal
+    unsigned top = wave_max(key[0]);
+    for (int j = 0; j < p.k && top != 0; ++j) {
         gap = min_u(gap, last - top);
         last = top;
-        if (j == p.k) break;
         const bool won = key[0] == top;
         const uint64_t at = __ballot(won);
-        if (at & (at - 1)) return false;   // two lanes' keys are equal
+        twice |= at & (at - 1);
         const int win = __builtin_ctzll(at);
         const int e = win * NE + (NE - 1 - (int)(top & (NE - 1)));
         *mine = lane == j ? e : *mine;
@@ -180,8 +179,10 @@ __device__ __forceinline__ bool choose32(const RouteProblem &p, const float *x, 
             const unsigned here = key[i], next = i + 1 < NE ? key[i + 1 < NE ? i + 1 : i] : 0u;   // (values, not places, to choose from)
             key[i] = won ? next : here;
         }
+        top = wave_max(key[0]);
     }
-    return gap > 2 * kNear;
+    if (top != 0) gap = min_u(gap, last - top);   // the first that is not chosen
+    return gap > 2 * kNear && twice == 0;
 }
 
 constexpr int kSegments = 16;                  // runs of 64 choices in a block

@@ -96,8 +96,10 @@ hipError_t launch_tiles(RaggedArgs a, long long row_tiles, int batch, hipStream_
 template <class Cfg, bool BF, bool TB>
 hipError_t launch_stream(RaggedArgs a, hipStream_t stream)
 {
+    const long long row_tiles = most_row_tiles(a.R, a.groups, Cfg::BM);
+    a.tiles_m = (int)row_tiles;
     a.tiles_n = (a.N + Cfg::BN - 1) / Cfg::BN;
-    const long long tiles = most_row_tiles(a.R, a.groups, Cfg::BM) * a.tiles_n;
+    const long long tiles = row_tiles * a.tiles_n;
     if (tiles > INT_MAX / Cfg::NT) return hipErrorInvalidValue;
     hipLaunchKernelGGL((grouped_stream_kernel<Cfg, BF, TB>), dim3((unsigned)tiles), dim3(Cfg::NT), 0, stream, a);
     return hipGetLastError();
@@ -129,8 +131,10 @@ template <class Cfg, bool BF, bool TB>
 hipError_t grouped_any_tiles(const GroupedProblem &q, hipStream_t stream)
 {
     RaggedArgs a = grouped_args(q);
+    const long long row_tiles = most_row_tiles(q.R, q.groups, Cfg::BM);
+    a.tiles_m = (int)row_tiles;
     a.tiles_n = (q.N + Cfg::BN - 1) / Cfg::BN;
-    const long long tiles = most_row_tiles(q.R, q.groups, Cfg::BM) * a.tiles_n;
+    const long long tiles = row_tiles * a.tiles_n;
     if (tiles > INT_MAX / 256) return hipErrorInvalidValue;
     hipLaunchKernelGGL((ragged_any_kernel<Cfg, BF, kGrouped, TB>), dim3((unsigned)tiles), dim3(256), 0, stream, a);
     return hipGetLastError();

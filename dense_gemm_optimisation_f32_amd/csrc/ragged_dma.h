@@ -23,12 +23,12 @@ __device__ __forceinline__ void group_rows(const int32_t *offsets, int g, int R,
 }
 
 // The row tiles (of BM rows, per group) of all groups, counted in order:
-// `total` of them, and of tile `want` its group, first row and the group's end.
+// `total` of them (at most `most`, the launch's), and of tile `want` its group, first row and the group's end.
 // Every wave does this by itself, 64 groups at a time, one per lane.
 struct RowTile {
     int group, first, end;
 };
-__device__ __forceinline__ int count_row_tiles(const int32_t *offsets, int groups, int R, int bm)
+__device__ __forceinline__ int count_row_tiles(const int32_t *offsets, int groups, int R, int bm, int most)
 {
     const int lane = threadIdx.x & 63;
     int total = 0;
@@ -39,7 +39,7 @@ __device__ __forceinline__ int count_row_tiles(const int32_t *offsets, int group
             group_rows(offsets, g0 + lane, R, &lo, &hi);
             n = (hi - lo + bm - 1) / bm;
         }
-        total += (int)wave_sum((unsigned)n);
+        total = add_row_tiles(total, wave_sum((unsigned)n), most);
     }
     return total;
 }
@@ -116,7 +116,7 @@ struct RaggedArgs {
     const int32_t *offsets;
     float *C;
     long long ldc, strideC;
-    int tiles_m, tiles_n;
+    int tiles_m, tiles_n;     // grouped: tiles_m is what any ascending offsets can need
     bool product;             // false: C is only scaled
     bool past_cache;          // C is larger than what the memory-side cache keeps of it
     AdapterArgs ad;           // lora
@@ -184,7 +184,7 @@ __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
 
     int group = 0, m0, m_end, n0, K, k_lo = 0;   // K: this tile's k range [k_lo, k_lo + K)
     if constexpr (KIND == kGrouped) {
-        const int total = count_row_tiles(p.offsets, p.groups, p.R, BM);
+        const int total = count_row_tiles(p.offsets, p.groups, p.R, BM, p.tiles_m);
         if ((long long)blockIdx.x >= (long long)total * p.tiles_n) return;
         int one, tm, tn;
         tile_coords((int)blockIdx.x, 0, 1, total, p.tiles_n, &one, &tm, &tn);
@@ -699,7 +699,7 @@ __global__ __launch_bounds__(256, Cfg::BM == 64 ? (KIND == kWgrad ? 3 : 4) : 2) 
         n0 = tn * BN;
         K = p.K;
     } else {
-        const int total = count_row_tiles(p.offsets, p.groups, p.R, BM);
+        const int total = count_row_tiles(p.offsets, p.groups, p.R, BM, p.tiles_m);
         if ((long long)blockIdx.x >= (long long)total * p.tiles_n) return;
         int one, tm, tn;
         // the XCD-aware order over the tiles that exist
@@ -953,7 +953,7 @@ __device__ __forceinline__ void stream_tile(const RaggedArgs &p, unsigned char *
     {
         int one, tm, tn;
         if constexpr (KIND == kGrouped) {
-            const int total = count_row_tiles(p.offsets, p.groups, p.R, BM);
+            const int total = count_row_tiles(p.offsets, p.groups, p.R, BM, p.tiles_m);
             if ((long long)block >= (long long)total * p.tiles_n) return;
             tile_coords(block, 0, 1, total, p.tiles_n, &one, &tm, &tn);
             const RowTile rt = find_row_tile(p.offsets, p.groups, p.R, BM, tm);

@@ -420,6 +420,39 @@ def test_grouped_no_product_and_bad_offsets(transB):
             assert (C[:8] == 4).all()
 
 
+@pytest.mark.parametrize("G", [4, 40])
+@pytest.mark.parametrize("N,K", [(64, 64), (65, 63), (256, 128)])
+@pytest.mark.parametrize("transB", [0, 1])
+def test_grouped_offsets_that_rise_again(transB, N, K, G):
+    """Offsets 0, R, 0, R, ...: more row tiles than any ascending offsets hold.  What is written is written once more with
+    the same values (one shared operand), and nothing outside C."""
+    R = 200
+    a = torch.ones(R, K, dtype=torch.float16, device="cuda")
+    b = torch.ones(N * K, dtype=torch.float16, device="cuda")
+    off = torch.tensor([0, R] * (G // 2) + [0], dtype=I32, device="cuda")
+    buf = torch.full((R + 600, N), -1.0, device="cuda")
+    dg.gemm_grouped_f16_f32acc_ex(transB, G, R, N, K, 1.0, a, R, K, None, b, K if transB else N, 0, off, 0.0, buf[300:], N)
+    done()
+    assert (buf[:300] == -1).all() and (buf[300 + R:] == -1).all()
+    assert (buf[300 : 300 + R] == K).all()
+
+
+def test_grouped_offsets_that_rise_again_past_32_bits():
+    """The same with 32767 times 16384 row tiles of 16 columns of tiles each."""
+    R, G, N, K = 16384 * 64, 65535, 1024, 3
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GiB of device memory")
+    a = torch.ones(R, K, dtype=torch.float16, device="cuda")
+    b = torch.ones(K * N, dtype=torch.float16, device="cuda")
+    off = torch.tensor([0, R], dtype=I32).repeat((G + 1) // 2)
+    off[-1] = R - 37 * 64
+    buf = torch.full((R + 2048, N), -1.0, device="cuda")
+    dg.gemm_grouped_f16_f32acc_ex(0, G, R, N, K, 1.0, a, R, K, None, b, N, 0, off.cuda(), 0.0, buf[1024:], N)
+    done()
+    assert (buf[:1024] == -1).all() and (buf[1024 + R:] == -1).all()
+    assert (buf[1024 : 1024 + R] == K).all()
+
+
 def test_grouped_no_product_reads_no_rows():
     # fewer row indices than rows of C: without a product none is read
     off = torch.tensor([0, 5000], dtype=I32, device="cuda")

@@ -91,3 +91,51 @@ def test_tile_order_is_a_bijection(tmp_path):
                     str(src), "-o", str(exe)], check=True)
     out = subprocess.run([str(exe)], capture_output=True, text=True)
     assert out.returncode == 0 and out.stdout.strip() == "ok", out.stdout
+
+
+RAGGED = r"""
+#include <cstdio>
+#include "tile_order.h"
+int main() {
+    // 65535 groups whose offsets go 0, R, 0, R, ...: 32767 times the rows, 64 a tile, and a shorter last one.  Counted
+    // whole, tiles x column tiles leave 32 bits and some workgroups get a column outside; counted up to the launch, none.
+    const long long R = 16384LL * 64;
+    const int tiles_n = 16, groups = 65535, most = (int)(R / 64 + groups);
+    long long outside = 0;
+    for (int cap = 0; cap < 2; ++cap) {
+        long long all = 0;
+        int total = 0;
+        for (int g = 0; g < 32768; ++g) {
+            const unsigned n = g < 32767 ? 16384 : 16384 - 37;
+            all += n;
+            total = mi355gemm::add_row_tiles(total, n, most);
+        }
+        if (total != most) { std::printf("count %d\n", total); return 1; }
+        if (!cap) total = (int)all;
+        for (long long b = 0; b < (long long)most * tiles_n; ++b) {
+            int one, tm, tn;
+            mi355gemm::tile_coords((int)b, 0, 1, total, tiles_n, &one, &tm, &tn);
+            const bool bad = (tm >= 0 && tm < total) && (tn < 0 || tn >= tiles_n);
+            if (cap && (bad || tm < 0 || tm >= total)) { std::printf("outside %lld\n", b); return 1; }
+            outside += bad;
+        }
+    }
+    if (!outside) { std::printf("the whole count stays inside\n"); return 1; }
+    // below the bound nothing is lost, and no count passes it
+    int t = mi355gemm::add_row_tiles(0, 7, 10);
+    if (t != 7 || mi355gemm::add_row_tiles(t, 3, 10) != 10 || mi355gemm::add_row_tiles(t, 4, 10) != 10 ||
+        mi355gemm::add_row_tiles(t, 1u << 30, 10) != 10 || mi355gemm::add_row_tiles(10, 0, 10) != 10) return 1;
+    std::printf("ok\n");
+    return 0;
+}
+"""
+
+
+def test_row_tiles_are_counted_up_to_the_launch(tmp_path):
+    src = tmp_path / "r.cpp"
+    src.write_text(RAGGED)
+    exe = tmp_path / "r"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-D__host__=", "-D__device__=", "-I", HDR_DIR,
+                    str(src), "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert out.returncode == 0 and out.stdout.strip() == "ok", out.stdout

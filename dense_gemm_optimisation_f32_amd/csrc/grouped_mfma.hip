@@ -8,8 +8,6 @@
 #include "routed_internal.h"
 #include "ragged_dma.h"
 
-#include <limits.h>
-
 namespace mi355gemm {
 namespace {
 
@@ -82,13 +80,25 @@ double tile_rounds(double tiles, double each)
     return (double)(long long)((tiles + 255) / 256) * each;
 }
 
+// Workgroups of Cfg's tiles, and whether one launch holds them.
+template <class Cfg>
+bool grouped_holds(const GroupedProblem &q)
+{
+    return grid_holds(most_row_tiles(q.R, q.groups, Cfg::BM) * ((q.N + Cfg::BN - 1LL) / Cfg::BN), Cfg::NT);
+}
+template <class Cfg>
+bool wgrad_holds(const WgradProblem &q)
+{
+    return grid_holds((q.M + Cfg::BM - 1LL) / Cfg::BM * ((q.N + Cfg::BN - 1LL) / Cfg::BN), Cfg::NT);
+}
+
 template <class Cfg, bool BF, int KIND, bool TB, bool GA = false, bool GB = false>
 hipError_t launch_tiles(RaggedArgs a, long long row_tiles, int batch, hipStream_t stream)
 {
     a.tiles_m = (int)row_tiles;
     a.tiles_n = (a.N + Cfg::BN - 1) / Cfg::BN;
     const long long tiles = row_tiles * a.tiles_n;
-    if (tiles > INT_MAX / Cfg::NT) return hipErrorInvalidValue;   // a grid holds fewer than 2^32 threads
+    if (!grid_holds(tiles, Cfg::NT)) return hipErrorInvalidValue;
     hipLaunchKernelGGL((ragged_dma_kernel<Cfg, BF, KIND, TB, GA, GB>), dim3((unsigned)tiles, 1, batch), dim3(Cfg::NT), 0, stream, a);
     return hipGetLastError();
 }
@@ -100,7 +110,7 @@ hipError_t launch_stream(RaggedArgs a, hipStream_t stream)
     a.tiles_m = (int)row_tiles;
     a.tiles_n = (a.N + Cfg::BN - 1) / Cfg::BN;
     const long long tiles = row_tiles * a.tiles_n;
-    if (tiles > INT_MAX / Cfg::NT) return hipErrorInvalidValue;
+    if (!grid_holds(tiles, Cfg::NT)) return hipErrorInvalidValue;
     hipLaunchKernelGGL((grouped_stream_kernel<Cfg, BF, TB>), dim3((unsigned)tiles), dim3(Cfg::NT), 0, stream, a);
     return hipGetLastError();
 }
@@ -115,16 +125,21 @@ hipError_t grouped_tiles(const GroupedProblem &q, hipStream_t stream)
     // against 66 with 64 columns), 64 for K x N, whose rows would otherwise be read 64 bytes at a
     // time (53 against 58 us).  At 64 rows a group 128x128 and 64x128 tiles are as fast or faster
     // (57 us against 78), at 32 the streaming is (58 against 61).
-    if (rows <= 32) return launch_stream<std::conditional_t<TB, StreamCfg<1, 1, 2, 4>, StreamCfg<1, 2, 3, 2>>, BF, TB>(a, stream);
+    // (Here and below: where one launch does not hold the tiles that would be fastest, larger ones.)
+    using Stream = std::conditional_t<TB, StreamCfg<1, 1, 2, 4>, StreamCfg<1, 2, 3, 2>>;
+    if (rows <= 32 && grouped_holds<Stream>(q)) return launch_stream<Stream, BF, TB>(a, stream);
     // tiles to expect: half of the part-filled ones
     const double part = 0.5 * (q.groups < q.R ? q.groups : q.R);
     const double n256 = (q.N + 255) / 256, n128 = (q.N + 127) / 128;
     const double c256 = tile_rounds((q.R / 256.0 + part) * n256, 1.0);
     const double c128 = tile_rounds((q.R / 128.0 + part) * n128, 0.4);
     const double c64 = tile_rounds((q.R / 64.0 + part) * n128, 0.25);
-    if (c256 <= c128 && c256 <= c64) return launch_tiles<Ragged256, BF, kGrouped, TB>(a, most_row_tiles(q.R, q.groups, 256), 1, stream);
-    if (c128 <= c64) return launch_tiles<Ragged128, BF, kGrouped, TB>(a, most_row_tiles(q.R, q.groups, 128), 1, stream);
-    return launch_tiles<Ragged64, BF, kGrouped, TB>(a, most_row_tiles(q.R, q.groups, 64), 1, stream);
+    const bool large = c256 <= c128 && c256 <= c64;
+    if (!large && c64 < c128 && grouped_holds<Ragged64>(q))
+        return launch_tiles<Ragged64, BF, kGrouped, TB>(a, most_row_tiles(q.R, q.groups, 64), 1, stream);
+    if (!large && grouped_holds<Ragged128>(q))
+        return launch_tiles<Ragged128, BF, kGrouped, TB>(a, most_row_tiles(q.R, q.groups, 128), 1, stream);
+    return launch_tiles<Ragged256, BF, kGrouped, TB>(a, most_row_tiles(q.R, q.groups, 256), 1, stream);
 }
 
 template <class Cfg, bool BF, bool TB>
@@ -135,7 +150,7 @@ hipError_t grouped_any_tiles(const GroupedProblem &q, hipStream_t stream)
     a.tiles_m = (int)row_tiles;
     a.tiles_n = (q.N + Cfg::BN - 1) / Cfg::BN;
     const long long tiles = row_tiles * a.tiles_n;
-    if (tiles > INT_MAX / 256) return hipErrorInvalidValue;
+    if (!grid_holds(tiles, 256)) return hipErrorInvalidValue;
     hipLaunchKernelGGL((ragged_any_kernel<Cfg, BF, kGrouped, TB>), dim3((unsigned)tiles), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
@@ -147,7 +162,8 @@ hipError_t grouped_any(const GroupedProblem &q, hipStream_t stream)
     // against 62 us; 8 groups, 4000 rows, 777 x 1001, 282 tiles: 26 against 30; 2000 rows, 157 tiles: 22 against 17.5);
     // stored K x N they gain nothing (564 tiles 76.3 against 75.6 us, 282 43 against 38)
     if constexpr (TB)
-        if ((q.R / 128.0 + part) * ((q.N + 127) / 128) >= 256) return grouped_any_tiles<HgCfg<128, 128>, BF, TB>(q, stream);
+        if ((q.R / 128.0 + part) * ((q.N + 127) / 128) >= 256 || !grouped_holds<HgCfg<64, 64>>(q))
+            return grouped_any_tiles<HgCfg<128, 128>, BF, TB>(q, stream);
     return grouped_any_tiles<HgCfg<64, 64>, BF, TB>(q, stream);
 }
 
@@ -160,7 +176,8 @@ hipError_t wgrad(const WgradProblem &q, hipStream_t stream)
         const double c128 = tile_rounds((double)((q.M + 127) / 128) * ((q.N + 127) / 128) * q.groups, 0.4);
         auto tiles = [&](auto ga, auto gb) {
             constexpr bool GA = decltype(ga)::value, GB = decltype(gb)::value;
-            if (c256 <= c128) return launch_tiles<Ragged256, BF, kWgrad, false, GA, GB>(a, (q.M + 255) / 256, q.groups, stream);
+            if (c256 <= c128 || !wgrad_holds<Ragged128>(q))
+                return launch_tiles<Ragged256, BF, kWgrad, false, GA, GB>(a, (q.M + 255) / 256, q.groups, stream);
             return launch_tiles<Ragged128, BF, kWgrad, false, GA, GB>(a, (q.M + 127) / 128, q.groups, stream);
         };
         if (q.rowsA) return q.rowsB ? tiles(std::true_type{}, std::true_type{}) : tiles(std::true_type{}, std::false_type{});
@@ -170,7 +187,7 @@ hipError_t wgrad(const WgradProblem &q, hipStream_t stream)
         using Cfg = decltype(cfg);
         a.tiles_m = (q.M + Cfg::BM - 1) / Cfg::BM;
         a.tiles_n = (q.N + Cfg::BN - 1) / Cfg::BN;
-        if ((long long)a.tiles_m * a.tiles_n > INT_MAX / 256) return hipErrorInvalidValue;
+        if (!grid_holds((long long)a.tiles_m * a.tiles_n, 256)) return hipErrorInvalidValue;
         hipLaunchKernelGGL((ragged_any_kernel<Cfg, BF, kWgrad, false>), dim3(a.tiles_m * a.tiles_n, 1, q.groups), dim3(256), 0,
                            stream, a);
         return hipGetLastError();
@@ -178,11 +195,22 @@ hipError_t wgrad(const WgradProblem &q, hipStream_t stream)
     // 128x128 tiles where there are several for a CU (1024 tiles: 16384 rows, 512 x 1023, 32 groups 63.5 against 75 us,
     // 4000 rows, 1001 x 1001, 16 groups 47 against 50; 560: 8000 rows, 513 x 777, 16 groups 45.5 against 41.5; 192: 6752
     // rows, 1024 x 341, 8 groups 37 against 29)
-    if ((q.M + 127LL) / 128 * ((q.N + 127) / 128) * q.groups >= 768) return any(HgCfg<128, 128>{});
+    if ((q.M + 127LL) / 128 * ((q.N + 127) / 128) * q.groups >= 768 || !wgrad_holds<HgCfg<64, 64>>(q)) return any(HgCfg<128, 128>{});
     return any(HgCfg<64, 64>{});
 }
 
 }  // namespace
+
+bool grouped_fits(const GroupedProblem &q)
+{
+    if (grouped_dma_ok(q)) return grouped_holds<Ragged256>(q);
+    return q.transB ? grouped_holds<HgCfg<128, 128>>(q) : grouped_holds<HgCfg<64, 64>>(q);
+}
+
+bool wgrad_fits(const WgradProblem &q)
+{
+    return wgrad_dma_ok(q) ? wgrad_holds<Ragged256>(q) : wgrad_holds<HgCfg<128, 128>>(q);
+}
 
 hipError_t launch_grouped(const GroupedProblem &q, bool bf, hipStream_t stream)
 {

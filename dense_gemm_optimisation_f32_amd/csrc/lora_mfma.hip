@@ -21,8 +21,6 @@
 #include "gemm_internal.h"
 #include "ragged_dma.h"
 
-#include <limits.h>
-
 namespace mi355gemm {
 namespace {
 
@@ -417,6 +415,13 @@ bool lora_dma_ok(const LoraProblem &p)
            256 * p.ldb * 2 < (1LL << 31);
 }
 
+// Whether one launch holds Cfg's tiles.
+template <class Cfg>
+bool lora_holds(const LoraProblem &p)
+{
+    return grid_holds((p.M + Cfg::BM - 1LL) / Cfg::BM * ((p.N + Cfg::BN - 1LL) / Cfg::BN), Cfg::NT);
+}
+
 template <class Cfg, bool BF, bool TB>
 hipError_t launch_decode(const LoraProblem &p, hipStream_t stream)
 {
@@ -456,7 +461,7 @@ hipError_t launch_tiles(RaggedArgs a, hipStream_t stream)
     a.tiles_m = (a.M + Cfg::BM - 1) / Cfg::BM;
     a.tiles_n = (a.N + Cfg::BN - 1) / Cfg::BN;
     const long long tiles = (long long)a.tiles_m * a.tiles_n;
-    if (tiles > INT_MAX / Cfg::NT) return hipErrorInvalidValue;
+    if (!grid_holds(tiles, Cfg::NT)) return hipErrorInvalidValue;
     hipLaunchKernelGGL((ragged_dma_kernel<Cfg, BF, kLora, TB, false, false>), dim3((unsigned)tiles), dim3(Cfg::NT), 0, stream, a);
     return hipGetLastError();
 }
@@ -475,9 +480,11 @@ hipError_t lora_tiles(const LoraProblem &p, hipStream_t stream)
     auto rounds = [&](int bm, int bn) { return (((p.M + bm - 1LL) / bm) * ((p.N + bn - 1LL) / bn) + 255) / 256; };
     // in the time of a 256x256 tile: a 128x128 tile takes 0.4, a 64x128 tile 0.25
     const double c256 = rounds(256, 256), c128 = 0.4 * rounds(128, 128), c64 = 0.25 * rounds(64, 128);
-    if (c256 <= c128 && c256 <= c64) return launch_tiles<Ragged256, BF, TB>(a, stream);
-    if (c128 <= c64) return launch_tiles<Ragged128, BF, TB>(a, stream);
-    return launch_tiles<Ragged64, BF, TB>(a, stream);
+    // (where one launch does not hold the tiles that would be fastest, larger ones)
+    const bool large = c256 <= c128 && c256 <= c64;
+    if (!large && c64 < c128 && lora_holds<Ragged64>(p)) return launch_tiles<Ragged64, BF, TB>(a, stream);
+    if (!large && lora_holds<Ragged128>(p)) return launch_tiles<Ragged128, BF, TB>(a, stream);
+    return launch_tiles<Ragged256, BF, TB>(a, stream);
 }
 
 // Any strides and alignments: the projection (few rows: K shared by several workgroups per
@@ -492,7 +499,7 @@ hipError_t lora_any(const LoraProblem &p, hipStream_t stream)
         a.tiles_m = (p.M + Cfg::BM - 1) / Cfg::BM;
         a.tiles_n = (p.N + Cfg::BN - 1) / Cfg::BN;
         const long long tiles = (long long)a.tiles_m * a.tiles_n;
-        if (tiles > INT_MAX / 256) return hipErrorInvalidValue;
+        if (!grid_holds(tiles, 256)) return hipErrorInvalidValue;
         hipLaunchKernelGGL((ragged_any_kernel<Cfg, BF, kLora, TB>), dim3((unsigned)tiles, splits), dim3(256), 0, stream, a);
         return hipGetLastError();
     };
@@ -508,7 +515,7 @@ hipError_t lora_any(const LoraProblem &p, hipStream_t stream)
     } else {
         // (128x128 tiles as in the grouped product)
         bool large = false;
-        if constexpr (TB) large = ((p.M + 127LL) / 128) * ((p.N + 127LL) / 128) >= 256;
+        if constexpr (TB) large = ((p.M + 127LL) / 128) * ((p.N + 127LL) / 128) >= 256 || !lora_holds<HgCfg<64, 64>>(p);
         if constexpr (TB)
             if (large) e = run(HgCfg<128, 128>{}, 1);
         if (!large) e = run(HgCfg<64, 64>{}, 1);
@@ -545,6 +552,14 @@ hipError_t lora(const LoraProblem &p, hipStream_t stream)
 }
 
 }  // namespace
+
+bool lora_fits(const LoraProblem &p)
+{
+    if (p.K == 0 || p.M <= kDecodeRows) return true;   // (64 rows: N <= 2^25 is 2^19 strips)
+    if (p.adapters == 0) return ((p.M + 31LL) / 32) * ((p.N + 31LL) / 32) <= 0x7FFFFFFF;   // (as gemm_*_f32acc_ex)
+    if (lora_dma_ok(p)) return lora_holds<Ragged256>(p);
+    return p.transB ? lora_holds<HgCfg<128, 128>>(p) : lora_holds<HgCfg<64, 64>>(p);
+}
 
 size_t lora_workspace(int M, int N, int K, int rank)
 {

@@ -11,7 +11,8 @@
 namespace {
 
 // Tokens of one call, and columns of the element-wise kernels: a launch holds
-// fewer than 2^32 threads, and a grid's second axis 65535 blocks.
+// fewer than 2^32 threads, and a grid's second axis 65535 blocks.  (The products'
+// grids are checked for the tiles that take a call.)
 constexpr int kMaxTokens = 1 << 23;
 constexpr int kMaxCols = 1 << 25;
 constexpr int kMaxSum = 1 << 30;   // a sum's length (K, or a weight gradient's R): positions in slices past the last stay ints
@@ -68,13 +69,7 @@ int grouped(int transB, int groups, int R, int N, int K, float alpha, const uint
     if (!extent(M, K, lda, &ea) || !extent(b_rows, b_cols, ldb, &eb) || !extent(R, N, ldc, &ec)) return GEMM_ERR_SIZE;
     if (const int rc = batch_extent(groups, eb, strideB, false); rc != GEMM_OK) return rc;
     if (groups == 0 || R == 0 || N == 0) return GEMM_OK;
-    // one workgroup per tile of at least 16 x 32, of 64 threads or more: the grid must fit a launch
-    if (((long long)R / 16 + (groups < R ? groups : R)) * (((long long)N + 31) / 32) > INT_MAX / 256) return GEMM_ERR_SIZE;
     const bool product = K > 0 && alpha != 0.f && M > 0;
-    if (!C || !offsets || (product && (!A || !B))) return GEMM_ERR_NULL;
-    if (misaligned(C, 4) || misaligned(offsets, 4) || misaligned(rows, 4) ||
-        (product && (misaligned(A, 2) || misaligned(B, 2))))
-        return GEMM_ERR_ALIGN;
     mi355gemm::GroupedProblem p;
     p.transB = transB; p.groups = groups; p.R = R; p.N = N; p.K = product ? K : 0;
     p.alpha = alpha; p.beta = beta;
@@ -82,6 +77,11 @@ int grouped(int transB, int groups, int R, int N, int K, float alpha, const uint
     p.B = B; p.ldb = ldb; p.strideB = strideB;
     p.offsets = offsets;
     p.C = C; p.ldc = ldc;
+    if (!mi355gemm::grouped_fits(p)) return GEMM_ERR_SIZE;
+    if (!C || !offsets || (product && (!A || !B))) return GEMM_ERR_NULL;
+    if (misaligned(C, 4) || misaligned(offsets, 4) || misaligned(rows, 4) ||
+        (product && (misaligned(A, 2) || misaligned(B, 2))))
+        return GEMM_ERR_ALIGN;
     return launched(mi355gemm::launch_grouped(p, bf, stream));
 }
 
@@ -96,12 +96,7 @@ int wgrad(int groups, int R, int M, int N, float alpha, const uint16_t *A, int a
     if (!extent(a_rows, M, lda, &ea) || !extent(b_rows, N, ldb, &eb) || !extent(M, N, ldc, &ec)) return GEMM_ERR_SIZE;
     if (const int rc = batch_extent(groups, ec, strideC, true); rc != GEMM_OK) return rc;
     if (groups == 0 || M == 0 || N == 0) return GEMM_OK;
-    if (((long long)M + 63) / 64 * (((long long)N + 63) / 64) > INT_MAX / 512) return GEMM_ERR_SIZE;
     const bool product = R > 0 && alpha != 0.f && a_rows > 0 && b_rows > 0;
-    if (!C || (product && (!A || !B || !offsets))) return GEMM_ERR_NULL;
-    if (misaligned(C, 4) || (product && (misaligned(A, 2) || misaligned(B, 2) || misaligned(offsets, 4) ||
-                                         misaligned(rowsA, 4) || misaligned(rowsB, 4))))
-        return GEMM_ERR_ALIGN;
     mi355gemm::WgradProblem p;
     p.groups = groups; p.R = product ? R : 0; p.M = M; p.N = N;
     p.alpha = alpha; p.beta = beta;
@@ -109,6 +104,11 @@ int wgrad(int groups, int R, int M, int N, float alpha, const uint16_t *A, int a
     p.B = B; p.b_rows = b_rows; p.ldb = ldb; p.rowsB = rowsB;
     p.offsets = offsets;
     p.C = C; p.ldc = ldc; p.strideC = strideC;
+    if (!mi355gemm::wgrad_fits(p)) return GEMM_ERR_SIZE;
+    if (!C || (product && (!A || !B || !offsets))) return GEMM_ERR_NULL;
+    if (misaligned(C, 4) || (product && (misaligned(A, 2) || misaligned(B, 2) || misaligned(offsets, 4) ||
+                                         misaligned(rowsA, 4) || misaligned(rowsB, 4))))
+        return GEMM_ERR_ALIGN;
     return launched(mi355gemm::launch_wgrad(p, bf, stream));
 }
 
@@ -163,8 +163,17 @@ int lora(int transB, int M, int N, int K, int rank, int adapters, float alpha, c
     if (const int rc = batch_extent(adapters, ela, strideLA, false); rc != GEMM_OK) return rc;
     if (const int rc = batch_extent(adapters, elb, strideLB, false); rc != GEMM_OK) return rc;
     if (M == 0 || N == 0) return GEMM_OK;
-    if (((long long)M + 15) / 16 * (((long long)N + 31) / 32) > INT_MAX / 512) return GEMM_ERR_SIZE;
     const bool product = K > 0 && alpha != 0.f;
+    mi355gemm::LoraProblem p;
+    p.transB = transB; p.M = M; p.N = N; p.K = product ? K : 0; p.rank = rank; p.adapters = product ? adapters : 0;
+    p.alpha = alpha; p.beta = beta;
+    p.A = A; p.lda = lda; p.B = B; p.ldb = ldb;
+    p.LA = LA; p.ldla = ldla; p.strideLA = strideLA;
+    p.LB = LB; p.ldlb = ldlb; p.strideLB = strideLB;
+    p.scales = scales; p.ranks = ranks; p.ids = ids;
+    p.C = C; p.ldc = ldc;
+    p.t = static_cast<float *>(workspace);
+    if (!mi355gemm::lora_fits(p)) return GEMM_ERR_SIZE;
     if (!C) return GEMM_ERR_NULL;
     if (product && (!A || !B || (adapters > 0 && (!LA || !LB || !ids)))) return GEMM_ERR_NULL;
     if (misaligned(C, 4)) return GEMM_ERR_ALIGN;
@@ -177,15 +186,6 @@ int lora(int transB, int M, int N, int K, int rank, int adapters, float alpha, c
         if (need > 0 && !workspace) return GEMM_ERR_NULL;
         if (misaligned(workspace, 16)) return GEMM_ERR_ALIGN;
     }
-    mi355gemm::LoraProblem p;
-    p.transB = transB; p.M = M; p.N = N; p.K = product ? K : 0; p.rank = rank; p.adapters = product ? adapters : 0;
-    p.alpha = alpha; p.beta = beta;
-    p.A = A; p.lda = lda; p.B = B; p.ldb = ldb;
-    p.LA = LA; p.ldla = ldla; p.strideLA = strideLA;
-    p.LB = LB; p.ldlb = ldlb; p.strideLB = strideLB;
-    p.scales = scales; p.ranks = ranks; p.ids = ids;
-    p.C = C; p.ldc = ldc;
-    p.t = static_cast<float *>(workspace);
     return launched(mi355gemm::launch_lora(p, bf, stream));
 }
 

@@ -10,6 +10,12 @@
 
 namespace mi355gemm {
 
+// A launch is held below 2^31 threads (the runtime takes fewer than 2^32).
+inline bool grid_holds(long long groups_of_threads, int threads)
+{
+    return groups_of_threads <= 0x7FFFFFFF / threads;
+}
+
 constexpr int kMaxExperts = 1024;   // route: experts, one wave holds a token's scores
 constexpr int kMaxChoices = 32;     // route, combine: choices of a token
 constexpr int kMaxRouteGroups = 64; // route: expert groups, one lane each
@@ -88,6 +94,8 @@ struct GroupedProblem {
     float *C;
     long long ldc;
 };
+// A tile of the kernels that take this call has a grid that one launch holds.
+bool grouped_fits(const GroupedProblem &p);
 hipError_t launch_grouped(const GroupedProblem &p, bool bf, hipStream_t stream);
 
 // C_g = alpha * sum over offsets[g] <= r < offsets[g+1] of A[rowsA[r],:]^T B[rowsB[r],:] + beta * C_g (M x N).
@@ -106,6 +114,7 @@ struct WgradProblem {
     float *C;
     long long ldc, strideC;
 };
+bool wgrad_fits(const WgradProblem &p);
 hipError_t launch_wgrad(const WgradProblem &p, bool bf, hipStream_t stream);
 
 // C[i,:] = alpha * (A[i,:] op(B) + scales[a] * (A[i,:] LA_a^T) LB_a^T) + beta * C[i,:], a = ids[i].
@@ -127,6 +136,7 @@ struct LoraProblem {
     long long ldc;
     float *t;                       // workspace
 };
+bool lora_fits(const LoraProblem &p);
 size_t lora_workspace(int M, int N, int K, int rank);
 hipError_t launch_lora(const LoraProblem &p, bool bf, hipStream_t stream);
 

@@ -56,7 +56,7 @@ enum {
     GEMM_OK = 0,
     GEMM_ERR_SIZE = -1,      /* M, N, K or batch_count negative, an extent overflows 64 bits, or
                                 ceil(M/32)*ceil(N/32) exceeds INT_MAX (one launch's grid); for the
-                                calls by row, also a size outside the range the call documents */
+                                calls by row, a size outside the range they document */
     GEMM_ERR_LD = -2,        /* lda < max(1,K), ldb < max(1,N) (with transA: lda < max(1,M); with
                                 transB: ldb < max(1,K)), ldc < max(1,N), negative stride, or
                                 strideC smaller than one C member when batch_count > 1 */
@@ -198,6 +198,12 @@ int gemm_f16_f32acc_noalloc(int M, int N, int K, float alpha,
  * 16-byte aligned; contents before and after are of no account).  Two calls that
  * can overlap, replays of two captured graphs among them, need two workspaces.
  * Results are bit-identical from call to call for the same arguments.
+ *
+ * C of a product is at most what one launch's tiles cover, beyond it GEMM_ERR_SIZE: 2^23 - 1 tiles
+ * of 64 x 64 (2^35 elements of C), of 128 x 128 with transB = 1 and for weight gradients; 2^22 - 1 of
+ * 256 x 256 where rows start at dwords and hold whole 16-byte chunks (pointers at multiples of 4,
+ * even leading dimensions and strides, K, or the N (M) of operands stored along it, a
+ * multiple of 8).  Rows of groups count R / (tile rows) + min(groups, R) row tiles.
  */
 
 /*

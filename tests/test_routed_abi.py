@@ -146,6 +146,46 @@ def test_lora_arguments(lib, t, kw, want):
     assert getattr(lib, f"gemm_lora_{t}_f32acc_ex")(*changed(LORA, **kw)) == want
 
 
+
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+def test_large_results_are_taken(lib, t):
+    """C of 16 GiB to 512 GiB passes the size check (and stops at the next one); what no launch holds does not."""
+    def grouped(R, N, groups=32, K=64, transB=0, A=FAKE):
+        ld = max(N, K)
+        return getattr(lib, f"gemm_grouped_{t}_f32acc_ex")(*changed(GROUPED, transB=transB, groups=groups, R=R, M=R, N=N, K=K, A=A, lda=ld,
+                                                                    ldb=ld, strideB=0, ldc=N, C=None))
+    assert grouped(1 << 18, 1 << 14) == ENULL
+    assert grouped(1 << 18, (1 << 14) + 8, transB=1) == ENULL
+    assert grouped(1 << 18, (1 << 14) + 1, K=63) == ENULL
+    assert grouped(1 << 18, (1 << 14) + 1, K=63, transB=1) == ENULL
+    assert grouped(1 << 22, 1 << 15) == ENULL                      # 16384 x 128 tiles of 256 x 256
+    assert grouped(100, 1 << 20, groups=65535) == ENULL            # few rows a group, many columns
+    assert grouped(33 * 65535, 8192, groups=65535) == ENULL        # 64-row tiles would be too many
+    assert grouped(1 << 21, 1 << 15, K=63, transB=1) == ENULL      # 16384 x 256 tiles of 128 x 128
+    assert grouped(1 << 22, 1 << 15, K=63) == ESIZE                # 65536 x 512 tiles of 64 x 64
+    assert grouped(1 << 22, 1 << 15, A=FAKE + 2) == ESIZE
+    assert grouped(1 << 25, 1 << 15) == ESIZE
+
+    def wgrad(M, N, A=FAKE):
+        return getattr(lib, f"gemm_grouped_wgrad_{t}_f32acc")(*changed(WGRAD, M=M, N=N, A=A, lda=M, ldb=N, ldc=N, strideC=M * N, C=None))
+    assert wgrad(1 << 17, 1 << 17) == ENULL
+    assert wgrad((1 << 17) - 3, (1 << 17) - 1) == ENULL
+    assert wgrad(1 << 18, 1 << 18) == ENULL
+    assert wgrad(1 << 18, 1 << 20) == ESIZE
+
+    def lora(M, N, K=64, transB=0, adapters=2):
+        ld = max(N, K)
+        return getattr(lib, f"gemm_lora_{t}_f32acc_ex")(*changed(LORA, transB=transB, M=M, N=N, K=K, adapters=adapters, lda=K, ldb=ld, ldc=N,
+                                                                 ldla=K, strideLA=0, strideLB=0, ws=None, ws_bytes=0))
+    assert lora(1 << 14, 1 << 17) == ESCRATCH
+    assert lora(1 << 17, 1 << 15, transB=1) == ESCRATCH
+    assert lora((1 << 17) + 1, 1 << 15, K=63, transB=1) == ESCRATCH
+    assert lora(1 << 17, 1 << 17, K=63) == ESCRATCH
+    assert lora(64, 1 << 25, K=63) == ESCRATCH
+    assert lora(1 << 23, 1 << 25) == ESIZE
+    assert lora(1 << 18, 1 << 18, K=63) == ESIZE
+
+
 def test_lora_workspace(lib):
     assert lib.gemm_lora_workspace(0, 6, 5, 3) == 0
     assert lib.gemm_lora_workspace(4, 6, 5, 0) == 0

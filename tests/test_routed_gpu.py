@@ -803,6 +803,45 @@ def test_results_larger_than_the_caches():
         assert torch.equal(D[i], x[at[i] : at[i + 1]].float().t() @ y[at[i] : at[i + 1]].float())
 
 
+@pytest.mark.parametrize("N,K", [(16392, 72), (16391, 71)])
+def test_grouped_result_past_2_to_32_elements(N, K):
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GiB of device memory")
+    g = torch.Generator(device="cuda").manual_seed(6)
+    ints = lambda *s: torch.randint(-3, 4, s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    G, R = 3, (1 << 18) + 77
+    a, b = ints(R, K), ints(G, K, N)
+    off = [0, 100001, 100001, R]
+    C = torch.full((R, N), math.nan, device="cuda")
+    dg.gemm_grouped_bf16_f32acc_ex(0, G, R, N, K, 1.0, a, R, K, None, b, N, K * N, torch.tensor(off, dtype=I32).cuda(), 0.0, C, N)
+    done()
+    for i in range(G):
+        for lo in range(off[i], off[i + 1], 1 << 14):
+            hi = min(lo + (1 << 14), off[i + 1])
+            assert torch.equal(C[lo:hi], a[lo:hi].float() @ b[i].float())
+
+
+@pytest.mark.parametrize("M,N,K,transB", [(16384, 131072, 64, 1), (16385, 131071, 63, 0)])
+def test_lora_result_past_2_to_31_elements(M, N, K, transB):
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GiB of device memory")
+    g = torch.Generator(device="cuda").manual_seed(7)
+    ints = lambda *s: torch.randint(-3, 4, s, generator=g, device="cuda").half()  # noqa: E731
+    r, n = 4, 3
+    a, b, la, lb = ints(M, K), ints(*((N, K) if transB else (K, N))), ints(n, r, K), ints(n, N, r)
+    ids = (torch.arange(M, device="cuda") // 1000 % (n + 1)).to(I32)
+    C = torch.full((M, N), math.nan, device="cuda")
+    dg.gemm_lora_f16_f32acc_ex(transB, M, N, K, r, n, 1.0, a, K, b, K if transB else N, la, K, r * K, lb, r, N * r, None, None, ids, 0.0, C, N)
+    done()
+    w = (b.t() if transB else b).float()
+    for lo in range(0, M, 1000):
+        rows, i = a[lo : lo + 1000].float(), int(ids[lo])
+        want = rows @ w
+        if i < n:
+            want += (rows @ la[i].float().t()) @ lb[i].float().t()
+        assert torch.equal(C[lo : lo + 1000], want)
+
+
 def test_lora_no_product():
     c = torch.randn(5, 6)
     nan = torch.full((64,), math.nan, dtype=torch.float16, device="cuda")

@@ -99,7 +99,8 @@ __device__ __forceinline__ void load_experts(const float *row, int lane, int E, 
 // of the choice takes 2.0 each, the groups 7, loads, scores, sort and weights 14.  Two waves per SIMD for
 // every one (64 registers) gave 39 us and a longer prefix.  16 tokens: 8.7 us, one token's chain of
 // dependent steps.
-constexpr float kLog2e = 1.44269504f;
+// log2(e) as a 32-bit value and what that leaves out, ln(2)
+constexpr float kLog2e = 1.4426950408889634, kLog2eLow = (float)(1.4426950408889634 - (double)kLog2e), kLn2 = 0.6931471805599453;
 constexpr float kUnits = 1 << 27, kZero = 4.f * (1 << 27);   // key = score * kUnits + kZero; 0: unavailable
 // Error of a key: exp, sum and quotient 4e-6, the rounding of score + 4 2.4e-7, the place of
 // the expert in the lowest 4 bits 1.2e-7; together below 2^-17.
@@ -625,15 +626,31 @@ hipError_t route_ne(const RouteProblem &p, hipStream_t stream)
 //   renormalised, p_j = s_j / sum of the chosen s:  q_j = p_j (g_j - sum_i p_i g_i);
 //     softmax: dl = q_j (the softmax's own sum cancels; other experts 0),  sigmoid: dl = q_j (1 - s_j)
 //   otherwise  softmax: dl_e = s_e (g_e - sum_i g_i s_i) over all experts,  sigmoid: dl = g_j s_j (1 - s_j)
-// Where near numbers are subtracted (renormalised) the k chosen values are formed in
-// 64 bits, all else in 32.  The k values reach their experts' lanes through a row
-// in LDS, of which a wave has one of its own (64 NE floats).
+// A router that is sure of its experts makes g_e and the sum nearly equal (and 1 - s_j small), so neither difference is
+// formed.  With r the chosen expert of the largest score, D_j = dweights_j - dweights_r, and u the sum of the scores that
+// are not chosen, added up by itself:
+//   g_e - sum_i g_i s_i = scale (D_e - sum_i D_i s_i + dweights_r u),   q_j = p_j scale (D_j - sum_i p_i D_i),
+//   1 - s = s(-x) for sigmoid scores.
+// D_r is 0, so what stands at r are the small terms alone.  (Where u is 1/2 or more, or the largest score of all is not
+// chosen, nothing cancels and dweights_r is taken as 0.)  Renormalised, the k values are formed in 64 bits, all else in
+// 32.  They reach their experts' lanes through a row in LDS, of which a wave has one of its own (64 NE floats).
 // Bound by its bytes: 16384 tokens of 128 experts, softmax, 8 choices: 17.8 MB in 7.4 us, 2.4 TB/s (3.8 us
 // at a copy's rate; the rest is a launch's ramp and one token's chain of loads, reductions and stores).
+
+// e^x for |x| <= 200 (below 2^-126: 0): the exponential instruction on the rounded x log2(e), and what that rounding
+// left out to first order; off by 3 u.  (The library's function takes about twice the instructions.)
+__device__ __forceinline__ float exp_of(float x)
+{
+    const float p = x * kLog2e, left = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -p));
+    const float e = __builtin_amdgcn_exp2f(p);
+    return __builtin_fmaf(e, left * kLn2, e);
+}
+
 template <int NE>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradProblem p)
 {
     __shared__ __attribute__((aligned(16))) float rows[4][64 * NE];
+    __shared__ unsigned marks[4][64];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int t = blockIdx.x * 4 + wave;
     const int E = p.E, k = p.k;
@@ -642,54 +659,87 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradProblem p)
     const int32_t *ids = p.ids + (long long)t * k;
     const float *dw = p.dweights + (long long)t * k;
     int id = lane < k ? ids[lane] : -1;
-    const float g = lane < k ? p.scale * dw[lane] : 0.f;
     const bool whole = p.score == 0 && !p.renorm;   // every expert gets a gradient
     float s[NE];
     if (whole) load_experts<NE>(row, lane, E, -INFINITY, s);
     const bool has = (unsigned)id < (unsigned)E;
-    const float xl = has ? row[id] : -INFINITY;
+    const float xl = has && !whole ? row[id] : -INFINITY;
     float *mine = rows[wave];
 #pragma unroll
     for (int i = 0; i < NE; ++i) mine[lane * NE + i] = 0.f;
-    float v = 0.f, dot = 0.f;   // lane j: the value choice j adds to its expert
+    const float d = has ? dw[lane] : 0.f;
+    float acc[NE];
     if (whole) {
+        // the chosen experts: a bit of their lane's word each, and their dweights (added up where the ids name one twice)
+        unsigned *mark = marks[wave];
+        mark[lane] = 0;
+        if (has) {
+            atomicOr(&mark[id / NE], 1u << (id % NE));
+            atomicAdd(&mine[id], d);
+        }
+        __builtin_amdgcn_wave_barrier();
+        const unsigned bits = mark[lane];
         float mx = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < NE; ++i) mx = s[i] > mx ? s[i] : mx;
+        for (int i = 0; i < NE; ++i) {
+            acc[i] = mine[lane * NE + i];
+            mx = s[i] > mx ? s[i] : mx;
+        }
+        const float lane_mx = mx;
         mx = wave_max(mx);
-        float sum = 0.f;
+        const uint64_t best = __ballot(lane_mx == mx);
+        mx = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f, others = 0.f, top = 0.f;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            s[i] = s[i] == -INFINITY ? 0.f : expf(s[i] - mx);
+            top = s[i] == mx ? acc[i] : top;   // (0 if it is not chosen)
+            const float x = s[i] - mx;
+            s[i] = exp_of(x < -200.f ? -200.f : x);
             sum += s[i];
+            others += (bits >> i) & 1 ? 0.f : s[i];
         }
         sum = wave_sum(sum);
-        const float over = sum == 0.f ? 0.f : 1.f / sum;
+        others = wave_sum(others);
+        const float over = sum == 0.f ? 0.f : 1.f / sum, u = others * over;
+        const float gr = best != 0 && u < 0.5f ? lane_value(top, __builtin_ctzll(best)) : 0.f;
+        float mean = 0.f;
 #pragma unroll
-        for (int i = 0; i < NE; ++i) s[i] *= over;
-        dot = wave_sum(has && xl != -INFINITY ? g * (expf(xl - mx) * over) : 0.f);
-        v = g;
-    } else if (p.renorm) {
-        const double gd = has ? (double)p.scale * (double)dw[lane] : 0.0;
-        const float cm = wave_max(xl);
-        double raw = 0.0;
-        if (has) raw = p.score == 1 ? 1.0 / (1.0 + exp(-(double)xl)) : xl == -INFINITY ? 0.0 : exp((double)xl - (double)cm);
-        const double sum = wave_sum(raw);
-        const double pj = sum != 0.0 ? raw / sum : 0.0;
-        const double mean = wave_sum(pj * gd);
-        v = (float)(pj * (gd - mean) * (p.score == 1 ? 1.0 - raw : 1.0));
+        for (int i = 0; i < NE; ++i) {
+            acc[i] = (bits >> i) & 1 ? acc[i] - gr : 0.f;
+            mean = __builtin_fmaf(s[i], acc[i], mean);
+        }
+        mean = wave_sum(mean) * over;
+        const float dot = __builtin_fmaf(gr, 1.f - u, mean);   // sum of g_i s_i; gr = 0 unless 1 - u > 1/2
+        const float rest = __builtin_fmaf(gr, u, -mean), by = p.scale * over;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) acc[i] = by * s[i] * ((bits >> i) & 1 ? acc[i] + rest : -dot);
     } else {
-        // s (1 - s) = s(x) s(-x), neither factor a difference
-        const float e = expf(-fabsf(xl)), q = 1.f / (1.f + e);
-        v = g * (e * q * q);
-    }
-    if (has) atomicAdd(&mine[id], v);   // (distinct experts: no two lanes add to one)
-    __builtin_amdgcn_wave_barrier();
-    float acc[NE];
+        float v;   // lane j: the value choice j adds to its expert
+        if (p.renorm) {
+            const float cm = wave_max(xl);
+            double raw = 0.0, rest = 1.0;   // the score (softmax: up to a factor), and for sigmoid 1 less it
+            if (has && p.score == 1) {
+                const double e = exp(-fabs((double)xl)), q = 1.0 / (1.0 + e);
+                raw = xl < 0.f ? e * q : q;
+                rest = xl < 0.f ? q : e * q;
+            } else if (has) {
+                raw = xl == -INFINITY ? 0.0 : exp((double)xl - (double)cm);
+            }
+            const double sum = wave_sum(raw);
+            const double pj = sum != 0.0 ? raw / sum : 0.0;
+            const uint64_t best = __ballot(has && xl == cm);
+            const double dj = (double)d - (best ? (double)lane_value(d, __builtin_ctzll(best)) : 0.0);
+            const double mean = wave_sum(pj * dj);
+            v = (float)((double)p.scale * (pj * (dj - mean) * rest));
+        } else {
+            // s (1 - s) = s(x) s(-x), neither factor a difference
+            const float e = expf(-fabsf(xl)), q = 1.f / (1.f + e);
+            v = p.scale * d * (e * q * q);
+        }
+        if (has) atomicAdd(&mine[id], v);   // (distinct experts: no two lanes add to one)
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        acc[i] = mine[lane * NE + i];
-        if (whole) acc[i] = s[i] * (acc[i] - dot);
+        for (int i = 0; i < NE; ++i) acc[i] = mine[lane * NE + i];
     }
     float *out = p.dlogits + (long long)t * p.lddl;
     const int e0 = lane * NE;

@@ -288,6 +288,82 @@ def test_route_grad(T, E, k, score, renorm):
             assert abs(float(d) - float(got[t, e])) <= 1e-6 * (1 + abs(float(loss.detach())) + scale * float(dw[t].abs().sum()))
 
 
+def sure_grad(x, ids, dw, score, renorm, scale):
+    """The gradient in 64 bits without a difference of near numbers, and the magnitude of its terms: for the chosen,
+    s_e (sum_i s_i (g_e - g_i) + g_e u), u the scores of the others; renormalised p_e sum_i p_i (g_e - g_i), times s(-x)
+    for sigmoid scores."""
+    T, E = x.shape
+    out, mag = np.zeros((T, E)), np.zeros((T, E))
+    for t in range(T):
+        at = ids[t]
+        g = scale * dw[t]
+        if renorm:
+            p = np.exp(x[t, at] - x[t, at].max()) if score == 0 else 1 / (1 + np.exp(-x[t, at]))
+            p = p / p.sum()
+            d = g[:, None] - g[None, :]
+            f = 1.0 if score == 0 else 1 / (1 + np.exp(x[t, at]))
+            out[t, at], mag[t, at] = p * (d @ p) * f, p * (np.abs(d) @ p) * f
+            continue
+        e = np.exp(x[t] - x[t].max())
+        others = np.ones(E, dtype=bool)
+        others[at] = False
+        u, s = e[others].sum() / e.sum(), e / e.sum()
+        d = g[:, None] - g[None, :]
+        out[t], mag[t] = -s * (g @ s[at]), s * (np.abs(g) @ s[at])
+        out[t, at], mag[t, at] = s[at] * (d @ s[at] + g * u), s[at] * (np.abs(d) @ s[at] + np.abs(g) * u)
+    return out, mag
+
+
+@pytest.mark.parametrize("E,k", [(8, 1), (64, 2), (128, 1), (128, 8), (256, 8), (1000, 4)])
+@pytest.mark.parametrize("gap", [12, 16, 20, 30, 60])
+@pytest.mark.parametrize("score,renorm", [(0, 0), (0, 1), (1, 1)])
+def test_route_grad_of_a_sure_router(E, k, gap, score, renorm):
+    """One expert, or the k chosen ones, far above the rest.  Relative to the magnitude m of the gradient's own terms: a
+    score is off by (range + 8) u (the difference of logits, an exponential, sum and quotient), its product and the sums
+    by 8 u more, and differences from the gradient of the best expert, whose score is 1 / 2k or more of them, have terms
+    |D_e| + sum_i s_i |D_i| of at most (2 + 4 k) m."""
+    rng = rng_of("sure", E, k, gap, score, renorm)
+    T = 12
+    x = rng.standard_normal((T, E)).astype(np.float32)
+    ids = np.argsort(rng.random((T, E)), 1)[:, :k].astype(np.int32)
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    for t in range(T):
+        if t % 3 == 2:
+            x[t, ids[t]] += gap          # all of the chosen
+        else:
+            x[t, ids[t, 0]] += gap       # one of them
+    dw[T // 2 :] = 1 + dw[T // 2 :] * np.float32(2.0 ** -20)   # nearly the same gradient for all
+    out = torch.full((T, E), math.nan, device="cuda")
+    dg.moe_route_f32_grad(T, E, dev(x), E, score, k, renorm, 2.5, dev(ids), dev(dw), out, E)
+    done()
+    want, mag = sure_grad(x.astype(np.float64), ids, dw.astype(np.float64), score, renorm, 2.5)
+    # renormalised: everything is formed in 64 bits and rounded once
+    tol = U * (2 if renorm else (16 + (x.max(1) - x.min(1))[:, None]) * (2 + 4 * k)) * mag + 1e-37
+    off = np.abs(host(out) - want)
+    worst = (off / np.maximum(mag, 1e-37)).max() / U
+    print(f"[sure] {worst:.1f} u", flush=True)
+    assert (off <= tol).all(), worst
+
+
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("renorm", [0, 1])
+def test_route_grad_of_ids_named_twice(score, renorm):
+    """The definition's gradient also where two choices of a token are the same expert."""
+    rng = rng_of("twice", score, renorm)
+    T, E, k = 20, 40, 4
+    x = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32))
+    ids = torch.from_numpy(rng.integers(0, 3, (T, k)).astype(np.int32))
+    dw = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32))
+    out = torch.full((T, E), math.nan, device="cuda")
+    dg.moe_route_f32_grad(T, E, x.cuda(), E, score, k, renorm, 1.0, ids.cuda(), dw.cuda(), out, E)
+    done()
+    xd = x.double().requires_grad_(True)
+    (grad_forward(xd, ids.long(), score, renorm, 1.0) * dw.double()).sum().backward()
+    # each of the k terms, at most |dw| each with a score of at most 1, and their sum: (16 + range + 2 k) u of them
+    tol = (16 + float(x.max() - x.min()) + 2 * k) * U * dw.double().abs().sum(1, keepdim=True) * 2
+    assert ((out.cpu().double() - xd.grad).abs() <= tol).all()
+
+
 def test_route_grad_of_padded_rows():
     x = torch.full((3, 8), -math.inf)
     x[1] = torch.arange(8.0)

@@ -101,6 +101,15 @@ __device__ __forceinline__ void load_experts(const float *row, int lane, int E, 
 // dependent steps.
 // log2(e) as a 32-bit value and what that leaves out, ln(2)
 constexpr float kLog2e = 1.4426950408889634, kLog2eLow = (float)(1.4426950408889634 - (double)kLog2e), kLn2 = 0.6931471805599453;
+// e^(x + low) for |x| <= 200 and a low of some u |x| (below 2^-126: 0): the exponential instruction on the rounded
+// x log2(e), and what that rounding left out, with low, to first order; off by 3 u.  (The library's function takes about
+// twice the instructions.)
+__device__ __forceinline__ float exp_of(float x, float low = 0.f)
+{
+    const float p = x * kLog2e, left = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -p));
+    const float e = __builtin_amdgcn_exp2f(p);
+    return __builtin_fmaf(e, __builtin_fmaf(left, kLn2, low), e);
+}
 constexpr float kUnits = 1 << 27, kZero = 4.f * (1 << 27);   // key = score * kUnits + kZero; 0: unavailable
 // Error of a key: exp, sum and quotient 4e-6, the rounding of score + 4 2.4e-7, the place of
 // the expert in the lowest 4 bits 1.2e-7; together below 2^-17.
@@ -387,16 +396,19 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteProblem p, int chunk, in
             }
         }
         // weights, from the chosen logits alone where they are renormalised; in 64
-        // bits where scores that 32 bits lose still have a quotient
+        // bits where scores that 32 bits lose still have a quotient.  In 32 bits the difference of logits
+        // is carried with its rounding error, so that no weight's error grows with the logits: an
+        // exponential 3 u, 1 + e and a reciprocal 3, the sum of the k 6 and theirs, the quotient 4: 22 u
+        // renormalised (5 measured).  Not renormalised, a softmax's sum over E experts is off by what its terms
+        // are, 3 u and their differences' rounding (their share of the sum weighs that: ln E), and 21 additions.
         const bool has = lane < k && mine >= 0;
         const float xl = has ? row[mine] : -INFINITY;
         const float ref = p.score == 1 ? 0.f : p.renorm ? wave_max(xl) : mx;
         const float over = p.renorm || p.score == 1 ? 1.f : sum32();   // (every lane takes part)
         float weight = 0.f;
         if (__ballot(has && (bad || !(fabsf(xl - ref) < 60.f))) == 0) {
-            // (hardware exponentials and reciprocals: 2 u each and 1.44 u per unit of the exponent)
-            const float x2 = (p.score == 1 ? -xl : xl - ref) * kLog2e;
-            float w = __builtin_amdgcn_exp2f(x2);
+            const float d = xl - ref, back = d - xl, low = (xl - (d - back)) - (ref + back);   // d + low = xl - ref
+            float w = p.score == 1 ? exp_of(-d) : exp_of(d, low);                              // (sigmoid: ref = 0)
             if (p.score == 1) w = __builtin_amdgcn_rcpf(1.f + w);
             if (!has) w = 0.f;
             const float all = p.renorm ? wave_sum(w) : over;
@@ -636,15 +648,6 @@ hipError_t route_ne(const RouteProblem &p, hipStream_t stream)
 // 32.  They reach their experts' lanes through a row in LDS, of which a wave has one of its own (64 NE floats).
 // Bound by its bytes: 16384 tokens of 128 experts, softmax, 8 choices: 17.8 MB in 7.4 us, 2.4 TB/s (3.8 us
 // at a copy's rate; the rest is a launch's ramp and one token's chain of loads, reductions and stores).
-
-// e^x for |x| <= 200 (below 2^-126: 0): the exponential instruction on the rounded x log2(e), and what that rounding
-// left out to first order; off by 3 u.  (The library's function takes about twice the instructions.)
-__device__ __forceinline__ float exp_of(float x)
-{
-    const float p = x * kLog2e, left = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -p));
-    const float e = __builtin_amdgcn_exp2f(p);
-    return __builtin_fmaf(e, left * kLn2, e);
-}
 
 template <int NE>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradProblem p)

@@ -181,6 +181,42 @@ def test_route_extreme_values(score):
     route_check(x, None, score, 1, 1, 1, 2, 0, 1.0)
 
 
+@pytest.mark.parametrize("E,k", [(8, 2), (64, 8), (256, 8), (1000, 32)])
+@pytest.mark.parametrize("score,renorm", [(0, 0), (0, 1), (1, 0), (1, 1)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_weights_of_far_logits(E, k, score, renorm, bias):
+    """Weights keep their digits wherever the logits are: an exponential is off by 3 u, 1 + e and its reciprocal by 3, the
+    k scores' sum by 6 and their own, the quotient by 4: 24 u.  A softmax that is not renormalised divides by a sum of E
+    exponentials, each off by 3 u and its difference's rounding, which its share of the sum weighs (ln E at most), and
+    21 additions: 48 u."""
+    rng = rng_of("far", E, k, score, renorm, bias)
+    T = 300
+    x = (rng.standard_normal((T, E)) * 0.7).astype(np.float32)
+    x += rng.choice([-57.0, -40.0, -20.0, -8.0, 0.0, 20.0], (T, 1)).astype(np.float32)      # all of a token's
+    x[::2, : E // 2] -= rng.uniform(0, 55, (T // 2, 1)).astype(np.float32)                # half of its experts far below
+    b = None
+    if bias:      # the lower half is chosen too
+        b = np.zeros(E, dtype=np.float32)
+        b[: max(1, k // 2)] = 2
+    got = route_call(dev(x), E, None if b is None else dev(b), score, 1, 1, 1, k, renorm, 1.0, T, E)
+    done()
+    ids, w = host(got["ids"]).reshape(T, k), host(got["weights"]).reshape(T, k)
+    xd = x.astype(np.float64)
+    v = np.take_along_axis(xd, ids, 1)
+    if score:
+        want = 1 / (1 + np.exp(-v))
+    elif renorm:
+        want = np.exp(v - v.max(1, keepdims=True))
+    else:
+        want = np.exp(v - xd.max(1, keepdims=True)) / np.exp(xd - xd.max(1, keepdims=True)).sum(1, keepdims=True)
+    if renorm:
+        want = want / want.sum(1, keepdims=True)
+    # (a weight below 2^-126, e^-87.3, is below fp32's normal values and may be held as anything from 0 to that)
+    off = (np.maximum(np.abs(w - want) - 2.0 ** -126, 0) / want).max() / U
+    print(f"[far] {off:.1f} u", flush=True)
+    assert off <= (24 if score or renorm else 48)
+
+
 @pytest.mark.parametrize("score,seed", [(1, 88), (1, 89), (0, 3)])
 def test_route_near_ties(score, seed):
     """Many tokens, so that some hold scores nearer to one another than 32 bits tell; and scores made so: experts in

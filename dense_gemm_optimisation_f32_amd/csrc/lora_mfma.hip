@@ -78,7 +78,7 @@ struct NarrowArgs {
 // The narrow product of the rows of 16-row block `rb` that use its `nth` distinct
 // adapter: t[i,:] = A[i,:] LA_a^T over share `share` of `shares` of K.  The NT / 64 waves
 // take chunks of 64 k in turn and add up in wave order.  PARTS: the whole K, t
-// rounded to 16-bit parts: of t / 2^e, 2^e such that the row's largest value is
+// rounded to 16-bit parts: of t / 2^e, 2^e such that the row's largest finite value is
 // near 2^14 (fp16, whose exponents a row's t may leave), e = 0 for bf16.
 // Two fp16 parts are off by 2^-22 of t at most, three bf16 parts by 2^-24, where the fp32 sums
 // over K that made t may be off by K 2^-24 of their terms.
@@ -167,10 +167,13 @@ __device__ __forceinline__ void narrow_block(const NarrowArgs &p, unsigned char 
         }
     } else {
         if (wave != 0) return;
+        // (columns past the adapter's rank are zeros, which a row's infinities times no row of LA are not)
         auto sum = [&](int n) {
             f32x4v v = part[n * 64 + lane];
 #pragma unroll
             for (int w = 1; w < NW; ++w) v += part[(w * NR + n) * 64 + lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = 16 * n + 4 * lq + e < ra ? v[e] : 0.f;
             return v;
         };
         int ex = 0;
@@ -179,11 +182,11 @@ __device__ __forceinline__ void narrow_block(const NarrowArgs &p, unsigned char 
             for (int n = 0; n < NR; ++n) {
                 const f32x4v v = sum(n);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) most = fmaxf(most, fabsf(v[e]));
+                for (int e = 0; e < 4; ++e) most = fabsf(v[e]) < INFINITY ? fmaxf(most, fabsf(v[e])) : most;
             }
             most = fmaxf(most, __shfl_xor(most, 16));
             most = fmaxf(most, __shfl_xor(most, 32));
-            if (most > 0.f && most < INFINITY) {
+            if (most > 0.f) {
                 (void)frexpf(most, &ex);   // most = m 2^ex, 1/2 <= m < 1
                 ex -= 15;
             }

@@ -841,6 +841,60 @@ def test_lora_rows_keep_apart(M, K):
     assert torch.isnan(again[0]).all() and torch.equal(again[2::3], want[2::3]) and torch.equal(again[3::3], want[3::3])
 
 
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("M", [3, 40, 100])
+@pytest.mark.parametrize("rank,used", [(16, 16), (16, 5), (40, 17)])
+@pytest.mark.parametrize("K", [256, 255])
+def test_lora_infinite_row_of_a(t, M, rank, used, K):
+    """A row of A that holds an infinity: the product and the narrow product are infinite with the signs of the weights it
+    meets, whatever lies past the adapter's rank, and a finite value of the narrow product stays finite."""
+    N, n = 72, 2
+    a = torch.ones(M, K, dtype=DT[t])
+    a[1::3, 0] = math.inf
+    b = torch.ones(N, K, dtype=DT[t])
+    b[N // 2 :] = -1                                        # these columns of the product are -inf
+    la = torch.zeros(n, rank, K, dtype=DT[t])
+    la[:, 0, 0] = 2                                         # t_0 = inf, or 2
+    la[:, 1, 0], la[:, 1, 1:] = 1, -1024
+    lb = torch.zeros(n, N, rank, dtype=DT[t])
+    lb[:, : N // 2, 0] = 1
+    lb[:, N // 2 :, 0] = -1
+    la[:, used:], lb[:, :, used:] = math.nan, math.inf
+    la[:, 2:used] = 1
+    lb[:, :, 2:used] = 0.5
+    lb[:, N // 2 :, 2:used] = -0.5
+    ids = (torch.arange(M) % n).to(I32)
+    lb[:, : N // 2, 1], lb[:, N // 2 :, 1] = 1, -1          # (t is +inf throughout, LB has the product's signs)
+    C = torch.full((M, N), math.nan, device="cuda")
+    getattr(dg, f"gemm_lora_{t}_f32acc_ex")(1, M, N, K, rank, n, 1.0, a.cuda(), K, b.cuda(), K, la.cuda(), K, rank * K, lb.cuda(), rank,
+                                            N * rank, None, torch.full((n,), used, dtype=I32, device="cuda"), ids.cuda(), 0.0, C, N)
+    done()
+    got = C.cpu()
+    assert (got[1::3, : N // 2] == math.inf).all() and (got[1::3, N // 2 :] == -math.inf).all()
+    rest = torch.ones(M, dtype=torch.bool)
+    rest[1::3] = False
+    assert torch.isfinite(got[rest]).all()
+
+
+@pytest.mark.parametrize("M", [3, 40, 100])
+def test_lora_infinity_beside_a_large_narrow_product(M):
+    """A narrow product that is +inf in one column and, in another, finite, past fp16's largest and of the other sign."""
+    N, K, rank = 72, 256, 16
+    a = torch.ones(M, K, dtype=torch.float16)
+    b = torch.zeros(N, K, dtype=torch.float16)
+    la = torch.zeros(1, rank, K, dtype=torch.float16)
+    la[:, 0, 0] = math.inf
+    la[:, 1] = -1024                                        # t_1 = -2^18
+    lb = torch.zeros(1, N, rank, dtype=torch.float16)
+    lb[:, :, 0] = 1
+    lb[:, :, 1] = 1
+    C = torch.full((M, N), math.nan, device="cuda")
+    dg.gemm_lora_f16_f32acc_ex(1, M, N, K, rank, 1, 1.0, a.cuda(), K, b.cuda(), K, la.cuda(), K, rank * K, lb.cuda(), rank, N * rank, None, None,
+                               torch.zeros(M, dtype=I32, device="cuda"), 0.0, C, N)
+    done()
+    assert (C == math.inf).all()
+
+
 @pytest.mark.parametrize("M", [5, 100])
 def test_lora_without_adapters(M):
     a, b, C = torch.ones(M, 64, dtype=torch.float16, device="cuda"), torch.ones(72, 64, dtype=torch.float16, device="cuda"), torch.ones(M, 72, device="cuda")

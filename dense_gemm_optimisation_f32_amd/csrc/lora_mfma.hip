@@ -55,7 +55,7 @@ __device__ __forceinline__ uint16_t round16(float v)
 
 // Workspace.  pitch: rank rounded up to 16.
 //   t: `shares` partial narrow products, each M x pitch fp32;
-//   parts: kParts<BF> x M x pitch 16-bit values, then M factors (tiles);
+//   parts: kParts x M x pitch 16-bit values, then M factors (tiles);
 //   sums: `splits` partial products, each M x N fp32 (decode).
 __host__ __device__ inline int rank_pitch(int rank)
 {
@@ -80,8 +80,7 @@ struct NarrowArgs {
 // take chunks of 64 k in turn and add up in wave order.  PARTS: the whole K, t
 // rounded to 16-bit parts: of t / 2^e, 2^e such that the row's largest finite value is
 // near 2^14 (fp16, whose exponents a row's t may leave), e = 0 for bf16.
-// Two fp16 parts are off by 2^-22 of t at most, three bf16 parts by 2^-24, where the fp32 sums
-// over K that made t may be off by K 2^-24 of their terms.
+// The parts hold t's 24 bits (see kPartStep).
 // Bound by reading A (4096 x 4096, rank 16: 33.6 MB in 10.9 us, 3.1 TB/s).
 template <bool BF, int NR, int NT, bool PARTS>
 __device__ __forceinline__ void narrow_block(const NarrowArgs &p, unsigned char *lds, int rb, int nth, int share, int shares)
@@ -199,13 +198,13 @@ __device__ __forceinline__ void narrow_block(const NarrowArgs &p, unsigned char 
 #pragma unroll
             for (int e = 0; e < 4; ++e) rest[e] = BF ? v[e] : ldexpf(v[e], -ex);
 #pragma unroll
-            for (int part_i = 0; part_i < kParts<BF>; ++part_i) {
+            for (int part_i = 0; part_i < kParts; ++part_i) {
                 uint16_t h[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     h[e] = round16<BF>(rest[e]);
                     const float got = widen16<BF>(h[e]);
-                    rest[e] = got - got == 0.f ? rest[e] - got : 0.f;   // (infinities and NaN stand in the first part alone)
+                    rest[e] = got - got == 0.f ? (rest[e] - got) * (1.f / kPartStep<BF>) : 0.f;   // (infinities and NaN stand in the first part alone)
                 }
                 unsigned *dst = reinterpret_cast<unsigned *>(p.parts + ((long long)part_i * p.M + row) * p.pitch + 16 * n + 4 * lq);
                 dst[0] = h[0] | ((unsigned)h[1] << 16);
@@ -474,7 +473,7 @@ hipError_t lora_tiles(const LoraProblem &p, hipStream_t stream)
 {
     NarrowArgs thin = narrow_args(p);
     thin.parts = reinterpret_cast<uint16_t *>(p.t);
-    thin.factor = reinterpret_cast<float *>(thin.parts + (size_t)kParts<BF> * p.M * thin.pitch);
+    thin.factor = reinterpret_cast<float *>(thin.parts + (size_t)kParts * p.M * thin.pitch);
     if (const hipError_t e = launch_narrow<BF, true>(p, thin, stream); e != hipSuccess) return e;
     RaggedArgs a = base_args(p);
     a.ad.ids = p.ids; a.ad.ranks = p.ranks; a.ad.adapters = p.adapters; a.ad.rank = p.rank;
@@ -569,7 +568,7 @@ size_t lora_workspace(int M, int N, int K, int rank)
     const size_t cells = (size_t)M * rank_pitch(rank);
     if (M <= kDecodeRows)
         return (cells * most_shares(K) + (size_t)M * N * decode_splits(N, K)) * sizeof(float);
-    return cells * 3 * sizeof(uint16_t) + (size_t)M * sizeof(float);   // at least the cells' fp32
+    return cells * kParts * sizeof(uint16_t) + (size_t)M * sizeof(float);   // at least the cells' fp32
 }
 
 hipError_t launch_lora(const LoraProblem &p, bool bf, hipStream_t stream)

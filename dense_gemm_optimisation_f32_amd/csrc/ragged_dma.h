@@ -63,20 +63,26 @@ __device__ __forceinline__ RowTile find_row_tile(const int32_t *offsets, int gro
     return {-1, 0, 0};
 }
 
-// The adapters of the rows (lora): the narrow product t of each row as kParts<BF>
-// 16-bit parts whose sum is t / 2^e, and the row's factor scale * 2^e.
+// The adapters of the rows (lora): the narrow product t of each row as three 16-bit
+// parts, t / 2^e = part 0 + kPartStep (part 1 + kPartStep part 2), and the row's factor
+// scale * 2^e.
 struct AdapterArgs {
     const int32_t *ids, *ranks;
     int adapters, rank;
     const uint16_t *LB;
     long long ldlb, strideLB;
-    const uint16_t *parts;    // kParts x M x pitch
+    const uint16_t *parts;    // 3 x M x pitch
     int pitch;                // halves per row: rank rounded up to 16
     const float *factor;      // M
 };
-// Parts of a 32-bit value: 24 bits as 11-bit (fp16) or 8-bit (bf16) pieces.
+// Parts of a 32-bit value: 24 bits as three pieces of 8 (bf16), or of 11 (fp16).  bf16 has fp32's exponents. In
+// fp16 what a part leaves is scaled up by 2^11, so that it does not fall below fp16's smallest value
+// (2^-24, with a row's largest near 2^14): a value keeps its 24 bits down to 2^-37 of the row's largest,
+// and is off by 2^-61 of that below.  (Two fp16 parts held 22 bits; the third costs 1% of 2048 rows with rank 16,
+// 2% of 4096 with rank 64, 5% of 1024 rows of 2048 x 2048 with rank 128.)
+constexpr int kParts = 3;
 template <bool BF>
-constexpr int kParts = BF ? 3 : 2;
+constexpr float kPartStep = BF ? 1.f : 1.f / 2048;
 
 __device__ __forceinline__ int adapter_of(const int32_t *ids, int adapters, int row, int M)
 {
@@ -527,9 +533,9 @@ __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
                 for (int r = 0; r < 16; ++r) add[jj][r] = 0.f;
             for (int k0 = 0; k0 < ra; k0 += 16) {
                 const int kq = k0 + 8 * lk;
-                half8 ta[kParts<BF>], tb[Cfg::FN];
+                half8 ta[kParts], tb[Cfg::FN];
 #pragma unroll
-                for (int part = 0; part < kParts<BF>; ++part) {
+                for (int part = 0; part < kParts; ++part) {
                     ta[part] = half8{};
                     if (mine == a)
                         ta[part] = *reinterpret_cast<const half8 *>(ad.parts + ((long long)part * p.M + row) * ad.pitch + kq);
@@ -539,10 +545,27 @@ __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
                     const int c = n0 + wn * Cfg::TN + 32 * jj + lr;
                     tb[jj] = load8_any(lb + (long long)(c < N ? c : N - 1) * ad.ldlb + kq, ra - kq);
                 }
+                if constexpr (BF) {
 #pragma unroll
-                for (int part = 0; part < kParts<BF>; ++part)
+                    for (int part = 0; part < kParts; ++part)
 #pragma unroll
-                    for (int jj = 0; jj < Cfg::FN; ++jj) add[jj] = mfma16<BF>(tb[jj], ta[part], add[jj]);
+                        for (int jj = 0; jj < Cfg::FN; ++jj) add[jj] = mfma16<BF>(tb[jj], ta[part], add[jj]);
+                } else {
+                    // (the last parts first, each sum scaled down to the part before it)
+#pragma unroll
+                    for (int jj = 0; jj < Cfg::FN; ++jj) {
+                        f32x16 low = {};
+#pragma unroll
+                        for (int part = kParts - 1; part > 0; --part) {
+                            low = mfma16<BF>(tb[jj], ta[part], low);
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) low[r] *= kPartStep<BF>;
+                        }
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) add[jj][r] += low[r];
+                        add[jj] = mfma16<BF>(tb[jj], ta[0], add[jj]);
+                    }
+                }
             }
             // (a lane holds values of its own row alone: another adapter's infinities stay out)
             if (todo == a) {

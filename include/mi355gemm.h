@@ -322,7 +322,8 @@ int moe_combine_grad_bf16(int T, int k, int N, const float *dC, int lddc, const 
  *   ranks   : a rank per adapter (clamped to 0 .. rank), or NULL for rank; what LA and LB hold
  *             past an adapter's rank is not used.
  *   ids     : M int32 values; outside 0 .. adapters-1: no adapter for that row.
- * The narrow product A LA^T stays in fp32 precision.  A row's result depends on its own
+ * The narrow product A LA^T is a sum in fp32 and stays in fp32 precision (fp16, more than 64 rows: values
+ * below 2^-37 of their row's largest are held to 2^-61 of that).  A row's result depends on its own
  * adapter alone, whatever the others hold.  M <= 2^23, N <= 2^25, K <= 2^30, 1 <= rank <= 128.
  */
 int gemm_lora_f16_f32acc_ex(int transB, int M, int N, int K, int rank, int adapters, float alpha,

@@ -814,6 +814,40 @@ def test_lora_narrow_product_outside_16_bits(M):
         assert torch.equal(C.cpu(), torch.full((M, N), K * 2.0 ** (2 * e) * r / 64))
 
 
+@pytest.mark.parametrize("t", ["f16", "bf16"])
+@pytest.mark.parametrize("M", [40, 100, 300])
+@pytest.mark.parametrize("rank", [5, 16, 40])
+def test_lora_narrow_product_keeps_its_bits(t, M, rank):
+    """LB takes one column of the narrow product at a time, so that C shows each of its values as it is held.  They are
+    sums of two products, x la below 2 and another 2^-2 (bf16: 2^-9) of such, with 24 bits in all, times 2^0 to 2^-26: the
+    result is exact, for few rows and for many."""
+    K, N = 128, 72
+    rng = rng_of("bits", t, M, rank)
+    bits, step = (10, 2.0 ** -2) if t == "f16" else (7, 2.0 ** -9)
+    some = lambda *n: (1 + rng.integers(0, int(0.4 * 2 ** bits), n) / 2.0 ** bits).astype(np.float32)  # noqa: E731
+    e = np.linspace(0, -26, rank).round().astype(int)
+    down = np.maximum(e, -12)                               # LA's part of 2^e, A's is the rest: normal fp16 values both
+    a, w = np.zeros((M, K), dtype=np.float32), np.zeros((1, rank, K), dtype=np.float32)
+    for j in range(rank):
+        up = np.float32(2.0 ** (e[j] - down[j]))
+        a[:, j], a[:, rank + j] = some(M) * up, some(M) * up
+        w[0, j, j], w[0, j, rank + j] = some(1)[0] * 2.0 ** down[j], some(1)[0] * 2.0 ** down[j] * step
+    lb = np.zeros((1, N, rank), dtype=np.float32)
+    lb[0, np.arange(rank), np.arange(rank)] = 1
+    b = np.zeros((N, K), dtype=np.float32)
+    mk = lambda v: torch.from_numpy(v).to(DT[t])  # noqa: E731
+    for v in (a, w):
+        assert torch.equal(mk(v).float(), torch.from_numpy(v))
+    C = torch.full((M, N), math.nan, device="cuda")
+    getattr(dg, f"gemm_lora_{t}_f32acc_ex")(1, M, N, K, rank, 1, 1.0, mk(a).cuda(), K, mk(b).cuda(), K, mk(w).cuda(), K, rank * K,
+                                            mk(lb).cuda(), rank, N * rank, None, None, torch.zeros(M, dtype=I32, device="cuda"), 0.0, C, N)
+    done()
+    want = np.zeros((M, N))
+    want[:, :rank] = a.astype(np.float64) @ w[0].astype(np.float64).T
+    assert np.array_equal(want.astype(np.float32), want)
+    assert np.array_equal(host(C), want), np.abs(host(C) / np.where(want == 0, 1, want) - (want != 0)).max()
+
+
 @pytest.mark.parametrize("M", [3, 40, 200])
 @pytest.mark.parametrize("K", [256, 255])
 def test_lora_rows_keep_apart(M, K):

@@ -51,6 +51,29 @@ __device__ __forceinline__ void sort_keys(K *key)
             }
 }
 
+// The same with each key's place, at[i] = 0 .. NE-1, equal keys in the order of their places.
+template <int NE>
+__device__ __forceinline__ void sort_placed(uint64_t *key, int *at)
+{
+#pragma unroll
+    for (int w = 1; w < NE; w <<= 1)
+#pragma unroll
+        for (int d = w; d > 0; d >>= 1)
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+                const int o = d == w ? (i / (2 * w)) * 2 * w + (2 * w - 1 - i % (2 * w)) : i ^ d;
+                if (o > i) {
+                    const uint64_t u = key[i], v = key[o];
+                    const int a = at[i], b = at[o];
+                    const bool first = u > v || (u == v && a < b);
+                    key[i] = first ? u : v;
+                    key[o] = first ? v : u;
+                    at[i] = first ? a : b;
+                    at[o] = first ? b : a;
+                }
+            }
+}
+
 // v[i] = row[lane*NE + i], `none` from E on: 16-byte loads where all four are inside.
 template <int NE>
 __device__ __forceinline__ void load_experts(const float *row, int lane, int E, float none, float *v)
@@ -77,13 +100,12 @@ __device__ __forceinline__ void load_experts(const float *row, int lane, int E, 
 // holds experts l*NE .. l*NE + NE-1.
 //   choose: choice scores are formed and compared in 64 bits, since neighbouring
 //     scores of a token are often nearer than 32 bits can tell and the choice is
-//     a whole number that is either right or not.  A score becomes a 64-bit key
-//     whose lowest log2(NE) bits hold the place within the lane (4 bits at most:
-//     scores are told apart to 2^-48), so a lane sorts its NE keys without a
-//     payload and equal scores come in the order of the experts.  A round of the
-//     choice is a maximum of the lanes' upper words; the lower words are looked at
-//     only where two lanes tie.  Where the logits order the experts like the
-//     scores (BY_LOGIT: no bias, a group's best score alone) no score is formed.
+//     a whole number that is either right or not.  A score becomes a 64-bit key of all its
+//     bits, which a lane sorts together with the experts' places, so that equal scores come in
+//     the order of the experts.  A round of the choice is a maximum of the lanes' upper words;
+//     the lower words are looked at only where two lanes tie.  Where the logits order the
+//     experts like the scores (BY_LOGIT: no bias, a group's best score alone) no score is
+//     formed, and a key is a logit's 32 bits with the place in the lowest log2(NE) below them.
 //   layout: choices are numbered by expert in token order: within 64 choices by
 //     comparing ids over the wave, across the block's (at most kSegments) runs of
 //     64 by a prefix over their counts, so the order never depends on timing.
@@ -228,6 +250,7 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteProblem p, int chunk, in
         float mx = -INFINITY;
         bool bad = false;   // a softmax whose scores are NaN: the row holds NaN or +inf
         uint64_t key[NE];
+        int at_place[NE];   // of the sorted keys (BY_LOGIT: in the keys)
         if (BY_LOGIT || p.score == 0) {
 #pragma unroll
             for (int i = 0; i < NE; ++i) {
@@ -277,7 +300,8 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteProblem p, int chunk, in
             for (int i = 0; i < NE; ++i) {
                 c[i] += (double)b[i];
                 const bool gone = x[i] == -INFINITY || b[i] == -INFINITY;
-                key[i] = gone ? 0 : (score_key(c[i]) & ~(uint64_t)(NE - 1)) | (NE - 1 - i);
+                key[i] = gone ? 0 : score_key(c[i]);
+                at_place[i] = i;
                 if (gone) c[i] = -INFINITY;
                 nan |= c[i] != c[i];
             }
@@ -375,23 +399,33 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteProblem p, int chunk, in
                 __builtin_amdgcn_wave_barrier();
             }
         }
-        if (!done) sort_keys<NE>(key);
+        if constexpr (BY_LOGIT)
+            sort_keys<NE>(key);
+        else if (!done)
+            sort_placed<NE>(key, at_place);
         for (int j = 0; !done && j < k; ++j) {
             const unsigned top = wave_max((unsigned)(key[0] >> 32));
             if (top == 0) break;
             uint64_t at = __ballot((unsigned)(key[0] >> 32) == top);
             if (at & (at - 1)) {   // lanes whose upper words are equal: the larger lower word, then the lower lane
                 const bool in = (at >> lane) & 1;
-                const unsigned low = in ? (unsigned)(key[0] & 0xFFFFFFFFu & ~(uint64_t)(NE - 1)) : 0u;
+                const unsigned low = in ? (unsigned)key[0] & ~(BY_LOGIT ? NE - 1u : 0u) : 0u;
                 const unsigned most = wave_max(low);   // (every lane takes part)
                 at = __ballot(in && low == most);
             }
             const int win = __builtin_ctzll(at);
-            const int e = win * NE + (NE - 1 - (int)(lane_value((unsigned)key[0], win) & (NE - 1)));
-            if (lane == j) mine = e;
+            int place;
+            if constexpr (BY_LOGIT)
+                place = NE - 1 - (int)(lane_value((unsigned)key[0], win) & (NE - 1));
+            else
+                place = (int)lane_value((unsigned)at_place[0], win);
+            if (lane == j) mine = win * NE + place;
             if (lane == win) {
 #pragma unroll
-                for (int i = 0; i + 1 < NE; ++i) key[i] = key[i + 1];
+                for (int i = 0; i + 1 < NE; ++i) {
+                    key[i] = key[i + 1];
+                    if constexpr (!BY_LOGIT) at_place[i] = at_place[i + 1];
+                }
                 key[NE - 1] = 0;
             }
         }

@@ -240,6 +240,27 @@ def test_route_near_ties(score, seed):
         assert torch.equal(got, want), (got != want).any(1).nonzero()[:5]
 
 
+@pytest.mark.parametrize("E", [40, 100, 256, 500, 1000])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_route_scores_that_differ_in_their_last_bits(E, groups):
+    """Choice scores 1 + m 2^-52, m = 1 .. 24 (sigmoid of a logit near -35 beside a bias of 1, in the middle of what rounds
+    to m), of which equal ones go by index and all others by score; and 1 - m 2^-52 (logits near 35, no bias)."""
+    T, k = 50, min(32, E // 2)
+    rng = rng_of("last bits", E, groups)
+    m = rng.integers(1, 25, (T, E))
+    x = np.log(m * 2.0 ** -52)          # sigmoid(x) = m 2^-52 (1 - m 2^-52): rounded to 32 bits, within 2^-19 of it
+    x = x.astype(np.float32)
+    b = np.ones(E, dtype=np.float32)
+    c = 1 / (1 + np.exp(-x.astype(np.float64))) + 1.0
+    assert np.array_equal(c, 1 + m * 2.0 ** -52)
+    route_check(x, b, 1, groups, max(1, groups // 2), min(2, E // groups), k, 0, 1.0)
+    if groups > 1:                      # (without a bias and groups the logits themselves are compared)
+        y = -np.log(m * 2.0 ** -52).astype(np.float32)
+        c = 1 / (1 + np.exp(-y.astype(np.float64)))
+        assert np.array_equal(c, 1 - m * 2.0 ** -52)
+        route_check(y, None, 1, groups, 2, 2, k, 0, 1.0)
+
+
 @pytest.mark.parametrize("T,E,k", [(20011, 100, 32), (70001, 40, 8), (9000, 1000, 32)])
 def test_route_many_choices(T, E, k):
     """More runs of choices than one pass over their counts takes."""

@@ -193,6 +193,15 @@ def test_lora_workspace(lib):
         assert lib.gemm_lora_workspace(M, 4096, 4096, 16) >= 4 * 16 * M
 
 
+@pytest.mark.parametrize("N", [1, 64, 128, 512, 4096])
+@pytest.mark.parametrize("M", [1, 48, 64])
+def test_lora_workspace_grows_with_k(lib, M, N):
+    """At most 16 shares of K, for a wide or a narrow N: the narrow products of 16 and sums of 16."""
+    sizes = [lib.gemm_lora_workspace(M, N, K, 16) for K in range(64, 70000, 64)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+    assert sizes[-1] <= 4 * (16 * M * 16 + 16 * M * N)
+
+
 def test_binding_refusals():
     torch = pytest.importorskip("torch")
     f, i = torch.zeros(64), torch.zeros(64, dtype=torch.int32)

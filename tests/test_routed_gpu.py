@@ -819,6 +819,12 @@ def test_lora_layouts(t, transB, M):
     lora_check(t, transB, M, 1024, 2048, 16, 4, runs=7)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 64, 8192), (16, 64, 16384), (48, 100, 8200), (33, 512, 7936), (5, 63, 8191)])
+def test_lora_few_columns_long_k(M, N, K):
+    lora_check("f16", 1, M, N, K, 8, 3, beta=0.5)
+    lora_check("bf16", 0, M, N, K, 8, 3, vals="int4")
+
+
 @pytest.mark.parametrize("M", [2, 100])
 def test_lora_narrow_product_outside_16_bits(M):
     """The narrow product reaches 2^20 and 2^-30, outside fp16; the result does not."""

@@ -10,8 +10,8 @@ integer device addresses (passed as they are).  ``stream`` may be None (torch's
 current stream), a ``torch.cuda.Stream`` or a raw ``hipStream_t`` integer.
 
 The functions at the end (routing, grouped products, combining, adapters) run on
-the device their tensors are on, refuse tensors of more than one device, and
-where they need a workspace take ``workspace=`` or let torch allocate it.
+the device their tensors (and a ``torch.cuda.Stream``) are on, refuse more than one
+device, and where they need a workspace take ``workspace=`` or let torch allocate it.
 
 If the library is not built, importing works but every call raises
 ``GemmLibraryMissing``: there is no fallback path.
@@ -315,7 +315,7 @@ _DTYPES = {}
 
 
 class _Elsewhere(Exception):
-    """An operand is on another device than the current one."""
+    """An operand or the stream is on another device than the current one."""
 
     def __init__(self, index: int):
         self.index = index
@@ -332,7 +332,7 @@ def _load_torch():
 
 
 def _on_operands_device(fn):
-    """Run ``fn`` with the device current that its tensors are on (one for all of them)."""
+    """Run ``fn`` with the device current that its tensors and its stream are on (one for all of them)."""
 
     @functools.wraps(fn)
     def call(*args, **kwargs):
@@ -344,7 +344,7 @@ def _on_operands_device(fn):
             try:
                 return fn(*args, **kwargs)
             except _Elsewhere as e:
-                raise ValueError(f"{fn.__name__}: operands on more than one device: cuda:{index} and cuda:{e.index}") from None
+                raise ValueError(f"{fn.__name__}: operands or stream on more than one device: cuda:{index} and cuda:{e.index}") from None
 
     return call
 
@@ -382,6 +382,12 @@ def _call(fn, args, stream, workspace=None, workspace_bytes=None) -> None:
         h = _raw_stream(_device())
     else:
         h = _stream(stream)
+        at = getattr(stream, "device", None)   # (a raw handle has none)
+        if at is not None:
+            if _torch is None:
+                _load_torch()
+            if at.index != _device():
+                raise _Elsewhere(at.index)
     if workspace_bytes is None:
         rc = fn(*args, h)
     else:

@@ -216,3 +216,50 @@ def test_binding_refusals():
     with pytest.raises(dg.GemmError) as e:
         dg.gemm_grouped_f16_f32acc_ex(3, 1, 4, 6, 5, 1.0, FAKE, 4, 5, None, FAKE, 6, 30, FAKE, 0.0, FAKE, 6, stream=0)
     assert e.value.status == EOP
+
+
+def test_binding_stream_of_another_device(monkeypatch):
+    """A call runs on the device of its stream, and is refused when its tensors are on another."""
+    torch = pytest.importorskip("torch")
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *a):
+            current[0] = self.before
+
+    class Stream:
+        cuda_stream, device = 0, torch.device("cuda", 1)
+
+    dg._load_torch()
+    monkeypatch.setattr(dg, "_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    args = (3, 1, 4, 6, 5, 1.0, FAKE, 4, 5, None, FAKE, 6, 30, FAKE, 0.0, FAKE, 6)      # (transB = 3: refused before any launch)
+    lib_fn = dg._function("gemm_grouped_f16_f32acc_ex")
+
+    class Watch:
+        __name__ = "gemm_grouped_f16_f32acc_ex"
+
+        def __call__(self, *a):
+            seen.append(current[0])
+            return lib_fn(*a)
+
+    monkeypatch.setattr(dg, "_function", lambda name: Watch())
+    with pytest.raises(dg.GemmError):
+        dg.gemm_grouped_f16_f32acc_ex(*args, stream=Stream())
+    assert seen == [1] and current == [0]
+
+    def on_device_0(x, name, dtype_name, need, packed=False):
+        if current[0] != 0:
+            raise dg._Elsewhere(0)
+        return x
+
+    monkeypatch.setattr(dg, "_strided", on_device_0)
+    with pytest.raises(ValueError, match="more than one device"):
+        dg.gemm_grouped_f16_f32acc_ex(*args, stream=Stream())
+    assert seen == [1] and current == [0]

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "routed_internal.h"
+#include "row_tiles.h"
 #include "stage16.h"
 #include "tile_order.h"
 #include "wave.h"

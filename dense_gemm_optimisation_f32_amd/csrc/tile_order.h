@@ -61,13 +61,4 @@ __host__ __device__ inline void tile_coords(int wg, int z, int nbatch, int tiles
     tile_coords_split(wg, z, nbatch, tiles_m, tiles_n, 1, member, tm, tn, &split);
 }
 
-// Row tiles of ragged groups are counted on the device, some groups at a time, up to
-// `most`, what the launch holds for ascending offsets.  Offsets that descend and rise
-// again hold rows more than once: their count, times the column tiles, could leave 32
-// bits and with them the ranges above.
-__host__ __device__ inline int add_row_tiles(int total, unsigned more, int most)
-{
-    return more >= (unsigned)(most - total) ? most : total + (int)more;
-}
-
 }  // namespace mi355gemm

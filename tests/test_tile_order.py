@@ -95,6 +95,7 @@ def test_tile_order_is_a_bijection(tmp_path):
 
 RAGGED = r"""
 #include <cstdio>
+#include "row_tiles.h"
 #include "tile_order.h"
 int main() {
     // 65535 groups whose offsets go 0, R, 0, R, ...: 32767 times the rows, 64 a tile, and a shorter last one.  Counted

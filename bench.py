@@ -63,7 +63,7 @@ _CSRC = "dense_gemm_optimisation_f32_amd/csrc/"
 # the files whose code makes up each kernel (its source and the headers it includes)
 KERNEL_SOURCES = {
     "sgemm": [_CSRC + f for f in ("sgemm_mfma.hip", "epilogue.h", "tile_order.h", "gemm_internal.h")],
-    "hgemm": [_CSRC + f for f in ("hgemm_mfma.hip", "epilogue.h", "tile_order.h", "gemm_internal.h")],
+    "hgemm": [_CSRC + f for f in ("hgemm_mfma.hip", "stage16.h", "epilogue.h", "tile_order.h", "gemm_internal.h")],
 }
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "hbm_traffic.md")
 COPY_BYTES = 256 << 20   # size of the calibration copy (read and written)
@@ -662,7 +662,7 @@ TRACE_STEPS, TRACE_WARMUP = 50, 20
 
 
 def _short(n):
-    return n.replace("mi355gemm::(anonymous namespace)::", "").split("(")[0]
+    return n.replace("mi355gemm::(anonymous namespace)::", "").replace("mi355gemm::", "").split("(")[0]
 
 
 def write_trace(stats_csv: str, trace_csv: str, bench_log: str) -> int:

@@ -124,7 +124,8 @@ hipError_t grouped_tiles(const GroupedProblem &q, hipStream_t stream)
     // stored N x K (two workgroups of 64 KB per CU; 64 groups x 2048 x 1024, 2 rows each: 56 us,
     // against 66 with 64 columns), 64 for K x N, whose rows would otherwise be read 64 bytes at a
     // time (53 against 58 us).  At 64 rows a group 128x128 and 64x128 tiles are as fast or faster
-    // (57 us against 78), at 32 the streaming is (58 against 61).
+    // (57 us against 78), at 32 the streaming is (58 against 61).  The host knows the mean alone: a group
+    // far above it has its weights read once for every 32 of its rows.
     // (Here and below: where one launch does not hold the tiles that would be fastest, larger ones.)
     using Stream = std::conditional_t<TB, StreamCfg<1, 1, 2, 4>, StreamCfg<1, 2, 3, 2>>;
     if (rows <= 32 && grouped_holds<Stream>(q)) return launch_stream<Stream, BF, TB>(a, stream);

@@ -14,10 +14,11 @@
 // 16-byte chunks) run the kernel for every alignment, then t and the product with LB.
 //
 // Measured (one MI355X, whole calls back to back): 1 row, 4096 x 4096 stored K x N, rank 16: 13.6 us, two
-// kernels of 7.0 and 5.8 us under a tracer, the weights' 33.6 MB in 7.1 us at a copy's 4.7 TB/s; 48 rows over 32 adapters
-// of rank 32, N x K: 18.2 us (12.6 + 6.7; every row's adapter is read in full, 50 MB in all: 10.9 us); 4096 rows,
-// rank 16: 138 us, 1000 TFLOP/s (narrow product 10.9 us, tiles 124 us, against 114 us for a
-// large matrix product of as many operations).
+// kernels of 6.8 and 5.2 us under a tracer, the weights' 33.6 MB in 7.1 us at a copy's 4.7 TB/s; 48 rows over 32 adapters
+// of rank 32, N x K: 18.2 us (12.3 + 6.8; every row's adapter is read in full, 50 MB in all: 10.9 us); 4096 rows,
+// rank 16: 138 us, 1000 TFLOP/s (narrow product 11.7 us, tiles 124 to 133 us, against 114 us for a
+// large matrix product of as many operations).  Tiles take a 32-row block's distinct adapters one after another, each
+// a chain of loads: rows that each have their own adapter are the slowest.
 #include "gemm_internal.h"
 #include "ragged_dma.h"
 
@@ -81,7 +82,7 @@ struct NarrowArgs {
 // rounded to 16-bit parts: of t / 2^e, 2^e such that the row's largest finite value is
 // near 2^14 (fp16, whose exponents a row's t may leave), e = 0 for bf16.
 // The parts hold t's 24 bits (see kPartStep).
-// Bound by reading A (4096 x 4096, rank 16: 33.6 MB in 10.9 us, 3.1 TB/s).
+// Bound by reading A (4096 x 4096, rank 16: 33.6 MB in 11.7 us, 2.9 TB/s).
 template <bool BF, int NR, int NT, bool PARTS>
 __device__ __forceinline__ void narrow_block(const NarrowArgs &p, unsigned char *lds, int rb, int nth, int share, int shares)
 {

@@ -173,11 +173,13 @@ enum RaggedKind { kGrouped, kWgrad, kLora };
 // below 2^31 bytes apart.  K may be anything else.
 // TB: B stored N x K (not wgrad).  GA, GB: the rows of A, B are looked up (wgrad).
 //
-// Bound by the matrix cores, as the whole-matrix kernel is, less what part-filled tiles take.  Measured, bf16, whole
-// calls back to back: 32768 gathered rows over 32 unequal groups, 2048 x 2048, B stored K x N: 305 us, 901 TFLOP/s;
-// weight gradients of 16384 rows over 32 groups, 2048 x 1024: 109-114 us, 603-630 TFLOP/s (its 268 MB of C are 57 us
-// of a copy's time); 4096 rows with adapters of rank 16, 4096 x 4096: 124 us of tiles.  Two other tile
-// shapes for the weight gradient: 128x256 138, 256x128 133, against 127 for 256x256 before C's stores left the caches.
+// Measured under a tracer, bf16: 32768 gathered rows over 32 unequal groups, 2048 x 2048, B stored K x N: 294 us, 935
+// TFLOP/s, matrix cores busy 53% of the cycles (79% in the whole-matrix kernel at 4096^3), the rest
+// being part-filled tiles and five rounds of workgroups for four and a half of tiles; weight gradients of 16384
+// rows over 32 groups, 2048 x 1024: 114 us, 600 TFLOP/s, 34%: each tile sums some 512 rows between a prologue and an
+// epilogue, C's 268 MB are 57 us of a copy's time, and an XCD takes whole groups whatever their length; 4096
+// rows with adapters of rank 16, 4096 x 4096: 133 us of tiles (124 at the least), 60%.  Two other tile shapes for
+// the weight gradient: 128x256 138, 256x128 133, against 127 for 256x256 before C's stores left the caches.
 template <class Cfg, bool BF, int KIND, bool TB, bool GA, bool GB>
 __global__ __launch_bounds__(Cfg::NT) void ragged_dma_kernel(RaggedArgs p)
 {

@@ -115,12 +115,14 @@ __device__ __forceinline__ void load_experts(const float *row, int lane, int E, 
 // as whole numbers of 2^-27, and a choice stands if every decision in it (a group
 // kept or not, a choice before the next) is by more than the errors of what it compares;
 // else the token is done again in 64 bits.  With scores of some hundred experts spread over a
-// unit a few tokens in a thousand are.
+// unit a few tokens in a thousand are.  With groups of experts that are not 1, 2, 4, 8 or 16 whole lanes
+// (lanes_per_group = 0: 160 experts in 8 groups) every token is, after its 32-bit scores were formed.
 // Bound by instructions, not by its reads: 32768 tokens of 256 experts (the best 4 of 8 groups, 8 choices, bias,
-// sigmoid) take 41 us, their 33.6 MB 7.1 us at a copy's rate.  Of a call without the layout, 37 us, a round
-// of the choice takes 2.0 each, the groups 7, loads, scores, sort and weights 14.  Two waves per SIMD for
-// every one (64 registers) gave 39 us and a longer prefix.  16 tokens: 8.7 us, one token's chain of
-// dependent steps.
+// sigmoid) take 40 us, vector instructions on 67% of the cycles; their 33.6 MB are 7.1 us at a copy's rate.  Of a
+// call without the layout, 36 us, a round of the choice takes 2 each, the groups 6, loads, scores, sort and
+// weights 14.  Two waves per SIMD for every one (64 registers) gave 39 us against 41 and a longer prefix.  16
+// tokens: 8.4 us, one token's chain of dependent steps, then a layout that clears and scans 16 runs of
+// choices where these fill two.
 // log2(e) as a 32-bit value and what that leaves out, ln(2)
 constexpr float kLog2e = 1.4426950408889634, kLog2eLow = (float)(1.4426950408889634 - (double)kLog2e), kLn2 = 0.6931471805599453;
 // e^(x + low) for |x| <= 200 and a low of some u |x| (below 2^-126: 0): the exponential instruction on the rounded
@@ -571,7 +573,7 @@ __global__ __launch_bounds__(1024) void prefix_kernel(RouteProblem p, int chunks
 }
 
 // Local numbers to rows.  PREFIXED: prefix_kernel has run; otherwise each block
-// adds up the counts of the chunks before its own, and of all of them.  262144 choices: 4.9 us, of
+// adds up the counts of the chunks before its own, and of all of them.  262144 choices: 5.0 us, of
 // which the 4 MB moved are 0.9: a chain of loads, a scan and scattered stores.
 template <bool PREFIXED>
 __global__ __launch_bounds__(1024) void place_kernel(RouteProblem p, int chunk, int chunks)
@@ -680,8 +682,9 @@ hipError_t route_ne(const RouteProblem &p, hipStream_t stream)
 // D_r is 0, so what stands at r are the small terms alone.  (Where u is 1/2 or more, or the largest score of all is not
 // chosen, nothing cancels and dweights_r is taken as 0.)  Renormalised, the k values are formed in 64 bits, all else in
 // 32.  They reach their experts' lanes through a row in LDS, of which a wave has one of its own (64 NE floats).
-// Bound by its bytes: 16384 tokens of 128 experts, softmax, 8 choices: 17.8 MB in 7.4 us, 2.4 TB/s (3.8 us
-// at a copy's rate; the rest is a launch's ramp and one token's chain of loads, reductions and stores).
+// 16384 tokens of 128 experts, softmax, 8 choices: 17.8 MB in 7.7 us (6.3 at the least), 2.3 TB/s, 3.8 us at a copy's
+// rate.  Vector instructions take 75% of the cycles: a wave holds one token, two experts a lane, read
+// and written a dword at a time, and its three reductions are a chain.
 
 template <int NE>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradProblem p)
@@ -795,10 +798,11 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradProblem p)
 
 // ---------------------------------------------------------------- combining
 //
-// C[t,:] = sum_j w_j Y[slot_j,:] + beta C[t,:]: four columns per thread, the k
-// rows read independently of one another, added in the order of the choices.  Bound by its
-// bytes (4096 tokens of 2048 columns, 8 choices: 302 MB in 48 us, 6.3 TB/s, part of Y being in the
-// memory-side cache still; 61 us on other data each call).
+// C[t,:] = sum_j w_j Y[slot_j,:] + beta C[t,:]: four columns per thread, added in the order of
+// the choices, one after another: a slot and its weight, then its row (and with beta C's four values one by one).
+// With many tokens other waves' rows are on their way meanwhile and the bytes are the bound (4096 tokens of 2048
+// columns, 8 choices: 302 MB in 49 us, 6.2 TB/s, part of Y being in the memory-side cache still; 61 us on
+// other data each call); a few tokens' time is 2 k trips to memory in turn.
 constexpr int kCombineCols = 1024;   // columns of a block of 256 threads
 
 __global__ __launch_bounds__(256) void combine_kernel(CombineProblem p)
@@ -846,7 +850,7 @@ typedef unsigned int u32x2_g __attribute__((ext_vector_type(2), aligned(4)));
 // gradient products take; dw_j = <dC[t,:], Y[slot_j,:]> summed in 32 bits: each
 // thread its columns, then the wave, then the block's four waves in order.  A block takes a
 // token, so that dC's row is read once for its k choices.  Bound by its bytes (8192 tokens of 1024
-// columns, 4 choices: 235 MB in 38.5 us, 6.1 TB/s; 54 us on other data each call).
+// columns, 4 choices: 235 MB in 38.9 us, 6.1 TB/s; 54 us on other data each call).
 template <bool BF>
 __global__ __launch_bounds__(256) void combine_grad_kernel(CombineGradProblem p)
 {

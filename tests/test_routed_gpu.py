@@ -825,6 +825,13 @@ def test_lora_few_columns_long_k(M, N, K):
     lora_check("bf16", 0, M, N, K, 8, 3, vals="int4")
 
 
+@pytest.mark.parametrize("transB", [0, 1])
+def test_lora_more_rows_than_a_grid_s_second_axis(transB):
+    """More than 65535 rows where the narrow product is joined by a block a row."""
+    lora_check("f16", transB, 70001, 9, 15, 3, 2, beta=0.5)
+    lora_check("bf16", transB, 131200, 7, 9, 2, 5, vals="int4", runs=100)
+
+
 @pytest.mark.parametrize("M", [2, 100])
 def test_lora_narrow_product_outside_16_bits(M):
     """The narrow product reaches 2^20 and 2^-30, outside fp16; the result does not."""

@@ -9,7 +9,7 @@ that a wrong buffer is refused on the host instead of faulting the GPU) or raw
 integer device addresses (passed as they are).  ``stream`` may be None (torch's
 current stream), a ``torch.cuda.Stream`` or a raw ``hipStream_t`` integer.
 
-The functions at the end (routing, grouped products, combining, adapters) run on
+The functions at the end (routing, grouped products, combining, adapters, 8-bit operands, orthogonalised updates) run on
 the device their tensors (and a ``torch.cuda.Stream``) are on, refuse more than one
 device, and where they need a workspace take ``workspace=`` or let torch allocate it.
 
@@ -31,6 +31,8 @@ __all__ = ["gemm_f32", "gemm_f16_f32acc", "gemm_batched_f16_f32acc",
            "gemm_grouped_wgrad_f16_f32acc", "gemm_grouped_wgrad_bf16_f32acc",
            "moe_combine_f32", "moe_combine_grad_f16", "moe_combine_grad_bf16",
            "gemm_lora_f16_f32acc_ex", "gemm_lora_bf16_f32acc_ex", "gemm_lora_workspace",
+           "quant_e4m3_f32", "quant_e4m3_f16", "quant_e4m3_bf16", "gemm_e4m3_f32acc", "gemm_grouped_e4m3_f32acc",
+           "orthogonalise_f32", "orthogonalise_bf16", "orthogonalise_workspace",
            "status_string",
            "GemmError", "GemmLibraryMissing", "LIB_PATH", "load_library", "EXPORTS"]
 
@@ -44,6 +46,8 @@ EXPORTS = ("gemm_f32", "gemm_f16_f32acc", "gemm_batched_f16_f32acc",
            "gemm_grouped_wgrad_f16_f32acc", "gemm_grouped_wgrad_bf16_f32acc",
            "moe_combine_f32", "moe_combine_grad_f16", "moe_combine_grad_bf16",
            "gemm_lora_f16_f32acc_ex", "gemm_lora_bf16_f32acc_ex", "gemm_lora_workspace",
+           "quant_e4m3_f32", "quant_e4m3_f16", "quant_e4m3_bf16", "gemm_e4m3_f32acc", "gemm_grouped_e4m3_f32acc",
+           "orthogonalise_f32", "orthogonalise_bf16", "orthogonalise_workspace",
            "gemm_status_string")
 
 _lib = None
@@ -106,6 +110,17 @@ def load_library(path: str = LIB_PATH):
                  "gemm_grouped_bf16_f32acc_ex", "gemm_grouped_wgrad_f16_f32acc", "gemm_grouped_wgrad_bf16_f32acc",
                  "moe_combine_grad_f16", "moe_combine_grad_bf16", "gemm_lora_f16_f32acc_ex", "gemm_lora_bf16_f32acc_ex"):
         getattr(lib, name).restype = i
+    for t in ("f32", "f16", "bf16"):
+        getattr(lib, f"quant_e4m3_{t}").argtypes = [i, i, i, i, vp, i, ll, vp, i, ll, vp, i, ll, i, vp]
+    lib.gemm_e4m3_f32acc.argtypes = [i, i, i, i, f, vp, i, vp, i, vp, i, vp, i, f, vp, i, vp]
+    lib.gemm_grouped_e4m3_f32acc.argtypes = [i, i, i, i, i, f, vp, i, i, vp, i, vp, vp, i, ll, vp, i, ll, vp, f, vp, i, vp]
+    for t in ("f32", "bf16"):
+        getattr(lib, f"orthogonalise_{t}").argtypes = [i, i, i, vp, f, vp, i, ll, vp, i, ll, i, vp, ll, vp]
+    for name in ("quant_e4m3_f32", "quant_e4m3_f16", "quant_e4m3_bf16", "gemm_e4m3_f32acc", "gemm_grouped_e4m3_f32acc",
+                 "orthogonalise_f32", "orthogonalise_bf16"):
+        getattr(lib, name).restype = i
+    lib.orthogonalise_workspace.argtypes = [i, i, i]
+    lib.orthogonalise_workspace.restype = ll
     lib.moe_route_workspace.argtypes = [i, i, i]
     lib.moe_route_workspace.restype = ll
     lib.gemm_lora_workspace.argtypes = [i, i, i, i]
@@ -326,7 +341,8 @@ def _load_torch():
     import torch
 
     _Tensor, _device, _raw_stream = torch.Tensor, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-    _DTYPES.update(float32=torch.float32, float16=torch.float16, bfloat16=torch.bfloat16, int32=torch.int32)
+    _DTYPES.update(float32=torch.float32, float16=torch.float16, bfloat16=torch.bfloat16, int32=torch.int32,
+                   float8_e4m3fn=torch.float8_e4m3fn)
     _torch = torch
     return torch
 
@@ -579,3 +595,103 @@ def gemm_lora_bf16_f32acc_ex(transB, M, N, K, rank, adapters, alpha, A, lda, B, 
     """gemm_lora_f16_f32acc_ex with bf16 inputs."""
     _lora("bf16", "bfloat16", transB, M, N, K, rank, adapters, alpha, A, lda, B, ldb, LA, ldla, strideLA, LB, ldlb, strideLB,
           scales, ranks, ids, beta, C, ldc, workspace, stream)
+
+
+# ------------------------------------------------------------------ 8-bit operands with a scale per block of 128
+def _blocks(n, block):
+    return -(-max(n, 0) // block) if block > 0 else 0
+
+
+def _members(one, batch, stride):
+    return one + (batch - 1) * stride if one > 0 and batch > 0 else 0
+
+
+def _quant(t, dtype_name, transpose, block, M, K, X, ldx, strideX, Q, ldq, strideQ, S, lds, strideS, batch_count, stream):
+    turned = int(transpose)
+    x = _extent(*((K, M) if turned else (M, K)), ldx)
+    args = (turned, block, M, K, _strided(X, "X", dtype_name, _members(x, batch_count, strideX)), ldx, strideX,
+            _strided(Q, "Q", "float8_e4m3fn", _members(_extent(M, K, ldq), batch_count, strideQ)), ldq, strideQ,
+            _strided(S, "S", "float32", _members(_extent(_blocks(K, 128), _blocks(M, block), lds) if M > 0 else 0, batch_count, strideS)),
+            lds, strideS, batch_count)
+    _call(_function(f"quant_e4m3_{t}"), args, stream)
+
+
+@_on_operands_device
+def quant_e4m3_f32(transpose, block, M, K, X, ldx, strideX, Q, ldq, strideQ, S, lds, strideS, batch_count=1, stream=None) -> None:
+    """Q (e4m3, M x K) and scales S (128 k by ``block`` rows each, k outermost) of X in fp32, or of its transpose."""
+    _quant("f32", "float32", transpose, block, M, K, X, ldx, strideX, Q, ldq, strideQ, S, lds, strideS, batch_count, stream)
+
+
+@_on_operands_device
+def quant_e4m3_f16(transpose, block, M, K, X, ldx, strideX, Q, ldq, strideQ, S, lds, strideS, batch_count=1, stream=None) -> None:
+    """quant_e4m3_f32 of X in fp16."""
+    _quant("f16", "float16", transpose, block, M, K, X, ldx, strideX, Q, ldq, strideQ, S, lds, strideS, batch_count, stream)
+
+
+@_on_operands_device
+def quant_e4m3_bf16(transpose, block, M, K, X, ldx, strideX, Q, ldq, strideQ, S, lds, strideS, batch_count=1, stream=None) -> None:
+    """quant_e4m3_f32 of X in bf16."""
+    _quant("bf16", "bfloat16", transpose, block, M, K, X, ldx, strideX, Q, ldq, strideQ, S, lds, strideS, batch_count, stream)
+
+
+@_on_operands_device
+def gemm_e4m3_f32acc(blockB, M, N, K, alpha, A, lda, SA, ldsa, B, ldb, SB, ldsb, beta, C, ldc, stream=None) -> None:
+    """C <- alpha*A*B^T + beta*C for e4m3 A (M x K) and B (N x K) times their scales; fp32 accumulation and C."""
+    reads = M > 0 and N > 0 and K > 0 and alpha != 0
+    kb = _blocks(K, 128)
+    args = (blockB, M, N, K, alpha, _strided(A, "A", "float8_e4m3fn", _extent(M, K, lda) if reads else 0), lda,
+            _strided(SA, "SA", "float32", _extent(kb, M, ldsa) if reads else 0), ldsa,
+            _strided(B, "B", "float8_e4m3fn", _extent(N, K, ldb) if reads else 0), ldb,
+            _strided(SB, "SB", "float32", _extent(kb, _blocks(N, blockB), ldsb) if reads else 0), ldsb, beta,
+            _strided(C, "C", "float32", _extent(M, N, ldc)), ldc)
+    _call(_function("gemm_e4m3_f32acc"), args, stream)
+
+
+@_on_operands_device
+def gemm_grouped_e4m3_f32acc(blockB, groups, R, N, K, alpha, A, M, lda, SA, ldsa, rows, B, ldb, strideB, SB, ldsb, strideSB, offsets, beta,
+                             C, ldc, stream=None) -> None:
+    """C[r,:] <- alpha*A[rows[r],:]*B_g^T + beta*C[r,:] for the rows r of every group g; e4m3 A and B times their scales, fp32 C."""
+    work = groups > 0 and R > 0 and N > 0
+    reads = work and K > 0 and alpha != 0 and M > 0
+    kb = _blocks(K, 128)
+    args = (blockB, groups, R, N, K, alpha, _strided(A, "A", "float8_e4m3fn", _extent(M, K, lda) if reads else 0), M, lda,
+            _strided(SA, "SA", "float32", _extent(kb, M, ldsa) if reads else 0), ldsa, _packed(rows, "rows", "int32", R if reads else 0),
+            _strided(B, "B", "float8_e4m3fn", _members(_extent(N, K, ldb), groups, strideB) if reads else 0), ldb, strideB,
+            _strided(SB, "SB", "float32", _members(_extent(kb, _blocks(N, blockB), ldsb), groups, strideSB) if reads else 0), ldsb, strideSB,
+            _packed(offsets, "offsets", "int32", groups + 1 if work else 0), beta, _strided(C, "C", "float32", _extent(R, N, ldc)), ldc)
+    _call(_function("gemm_grouped_e4m3_f32acc"), args, stream)
+
+
+# ------------------------------------------------------------------ orthogonalised updates
+@functools.lru_cache(maxsize=1024)
+def orthogonalise_workspace(M, N, batch_count=1) -> int:
+    """Bytes of workspace orthogonalise_f32 and its bf16 form need."""
+    return load_library().orthogonalise_workspace(M, N, batch_count)
+
+
+@functools.lru_cache(maxsize=64)
+def _coefficients(steps):
+    flat = [v for step in steps for v in step]
+    if any(len(step) != 3 for step in steps):
+        raise ValueError("steps: three coefficients each")
+    return (ctypes.c_float * len(flat))(*flat)
+
+
+def _orthogonalise(t, dtype_name, M, N, steps, alpha, G, ldg, strideG, O, ldo, strideO, batch_count, workspace, stream):
+    c = _coefficients(tuple(map(tuple, steps)))
+    args = (M, N, len(steps), ctypes.addressof(c), alpha,
+            _strided(G, "G", dtype_name, _members(_extent(M, N, ldg), batch_count, strideG)), ldg, strideG,
+            _strided(O, "O", "bfloat16", _members(_extent(M, N, ldo), batch_count, strideO)), ldo, strideO, batch_count)
+    _call(_function(f"orthogonalise_{t}"), args, stream, workspace, orthogonalise_workspace(M, N, batch_count))
+
+
+@_on_operands_device
+def orthogonalise_f32(M, N, steps, alpha, G, ldg, strideG, O, ldo, strideO, batch_count=1, workspace=None, stream=None) -> None:
+    """O <- alpha*X after X <- G/|G| and, for each (a, b, c) of steps, X <- a*X + (b*A + c*A*A)*X with A = X*X^T; G fp32, O bf16."""
+    _orthogonalise("f32", "float32", M, N, steps, alpha, G, ldg, strideG, O, ldo, strideO, batch_count, workspace, stream)
+
+
+@_on_operands_device
+def orthogonalise_bf16(M, N, steps, alpha, G, ldg, strideG, O, ldo, strideO, batch_count=1, workspace=None, stream=None) -> None:
+    """orthogonalise_f32 of G in bf16."""
+    _orthogonalise("bf16", "bfloat16", M, N, steps, alpha, G, ldg, strideG, O, ldo, strideO, batch_count, workspace, stream)

@@ -1,0 +1,314 @@
+// quant_e4m3.hip -- a matrix, or its transpose, laid out in 8-bit floating point
+// (e4m3: four exponent bits, three fraction bits, largest value 448, no infinity) with
+// a scale for each block of 128 columns of one row or of 128 rows.
+//
+//   s = the least power of two with max|y| / s <= 448 over the block's finite values
+//       (not below 2^-126; 1 for a block of zeros)
+//   q = y / s rounded to the nearest e4m3 value, ties to the even one
+//
+// A power of two loses nothing against 448 / max|y|: the fraction bits are the same,
+// only the block's smallest values reach 2^-9 half a step earlier.  y / s is then exact in
+// fp32, so q is the nearest value of the quotient itself, with one rounding.
+#include "e4m3_internal.h"
+#include "routed_internal.h"
+#include "stage16.h"
+#include "wave.h"
+
+namespace mi355gemm {
+namespace {
+
+struct QuantArgs {
+    int rows, cols;          // X as stored
+    int tiles_r, tiles_c;    // of 128 x 128
+    const void *X;
+    long long ldx, strideX;
+    uint8_t *Q;
+    long long ldq, strideQ;
+    float *S;
+    long long lds, strideS;
+};
+
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x2_g __attribute__((ext_vector_type(2), aligned(4)));
+
+template <class T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32(_Float16 v) { return (float)v; }
+template <>
+__device__ __forceinline__ float to_f32(__bf16 v)
+{
+    return __builtin_bit_cast(float, (unsigned)__builtin_bit_cast(uint16_t, v) << 16);
+}
+
+// Eight values from column c of a row as fp32; columns at or past `cols` are zero.
+// VEC: the row starts at a dword, so eight values inside it are one or two 16-byte loads.
+template <class T, bool VEC>
+__device__ __forceinline__ void load8_f32(const T *row, int c, int cols, float *y)
+{
+    if (VEC && c + 8 <= cols) {
+        if constexpr (sizeof(T) == 4) {
+            const f32x4_t a = *reinterpret_cast<const f32x4_g *>(row + c), b = *reinterpret_cast<const f32x4_g *>(row + c + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                y[e] = a[e];
+                y[e + 4] = b[e];
+            }
+        } else {
+            const u32x4 a = *reinterpret_cast<const u32x4_g *>(row + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                y[2 * e] = to_f32(__builtin_bit_cast(T, (uint16_t)a[e]));
+                y[2 * e + 1] = to_f32(__builtin_bit_cast(T, (uint16_t)(a[e] >> 16)));
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = c + e < cols ? to_f32(row[c + e]) : 0.f;
+}
+
+__device__ __forceinline__ unsigned magnitude(float v)
+{
+    return __builtin_bit_cast(unsigned, v) & 0x7FFFFFFFu;
+}
+constexpr unsigned kInfinity = 0x7F800000u;
+
+// The exponent bits of the block's scale from the bits of its largest magnitude
+// 2^e m: 2^(e-8) if m <= 1.75 (448 = 1.75 * 2^8), else 2^(e-7).
+__device__ __forceinline__ unsigned scale_exponent(unsigned top)
+{
+    if (top == 0) return 127u;
+    const int e = (int)((top + 0x1FFFFFu) >> 23) - 8;
+    return (unsigned)(e < 1 ? 1 : e);
+}
+
+// Four values to e4m3, in order from the lowest byte.  |y| <= 448 or NaN.
+__device__ __forceinline__ unsigned to_e4m3(float a, float b, float c, float d)
+{
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+}
+
+__device__ __forceinline__ void store8_e4m3(uint8_t *dst, u32x2 v, int valid, bool vec)
+{
+    if (vec && valid >= 8) {
+        *reinterpret_cast<u32x2_g *>(dst) = v;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < valid) dst[e] = (uint8_t)(v[e >> 2] >> (8 * (e & 3)));
+}
+
+// The largest of 16 lanes' values, in each of the 16.
+__device__ __forceinline__ unsigned row16_max(unsigned v)
+{
+    auto take = [&](unsigned o) { v = o > v ? o : v; };
+    take(dpp<0x128, 0xF>(0u, v));   // rotations within the row by 8, 4, 2, 1
+    take(dpp<0x124, 0xF>(0u, v));
+    take(dpp<0x122, 0xF>(0u, v));
+    take(dpp<0x121, 0xF>(0u, v));
+    return v;
+}
+
+// A workgroup takes a 128 x 128 tile of X as it is stored: thread t holds 8 columns
+// (8 (t % 16) ..) of 8 consecutive rows (8 (t / 16) ..).
+template <class T, bool TRANS, bool SQUARE, bool VEC>
+__global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
+{
+    __shared__ unsigned part[TRANS && !SQUARE ? 4 * 128 : 4];
+    __shared__ __attribute__((aligned(16))) unsigned char turned[TRANS ? 128 * 128 : 16];
+    const int tid = threadIdx.x, wave = tid >> 6;
+    const int tiles = p.tiles_r * p.tiles_c;
+    const int z = blockIdx.x / tiles, tile = blockIdx.x % tiles;
+    const int tr = tile / p.tiles_c, tc = tile % p.tiles_c;
+    const int r0 = tr * 128 + 8 * (tid >> 4), c0 = tc * 128 + 8 * (tid & 15);
+    const T *X = reinterpret_cast<const T *>(p.X) + z * p.strideX;
+
+    float y[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (r0 + i < p.rows) {
+            load8_f32<T, VEC>(X + (long long)(r0 + i) * p.ldx, c0, p.cols, y[i]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[i][e] = 0.f;
+        }
+    }
+
+    // exponent bits of the scales: of row i, of column e (TRANS), or of the tile (SQUARE)
+    unsigned ex[8];
+    auto tops = [&](auto counted) __attribute__((always_inline)) {
+        unsigned top[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top[i] = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const unsigned m = counted(magnitude(y[i][e]));
+                unsigned &t = top[SQUARE ? 0 : TRANS ? e : i];
+                t = m > t ? m : t;
+            }
+        if constexpr (SQUARE) {
+            const unsigned w = wave_max(top[0]);
+            __syncthreads();
+            if ((tid & 63) == 0) part[wave] = w;
+            __syncthreads();
+            unsigned all = part[0];
+#pragma unroll
+            for (int k = 1; k < 4; ++k) all = part[k] > all ? part[k] : all;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top[i] = all;
+        } else if constexpr (TRANS) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                unsigned o = (unsigned)__shfl_xor((int)top[e], 16);
+                top[e] = o > top[e] ? o : top[e];
+                o = (unsigned)__shfl_xor((int)top[e], 32);
+                top[e] = o > top[e] ? o : top[e];
+            }
+            __syncthreads();
+            if ((tid & 63) < 16)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) part[wave * 128 + 8 * (tid & 15) + e] = top[e];
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const unsigned o = part[k * 128 + 8 * (tid & 15) + e];
+                    top[e] = o > top[e] ? o : top[e];
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top[i] = row16_max(top[i]);
+        }
+        bool finite = true;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            finite = finite && top[i] < kInfinity;
+            ex[i] = scale_exponent(top[i]);
+        }
+        return finite;
+    };
+    const bool finite = tops([](unsigned m) { return m; });
+    if (__syncthreads_or(!finite)) {
+        // infinities and NaN do not count, and become NaN
+        tops([](unsigned m) { return m < kInfinity ? m : 0u; });
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (magnitude(y[i][e]) >= kInfinity) y[i][e] = __builtin_nanf("");
+    }
+    // y / s = y * 2^-(ex - 127)
+    float inv[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) inv[i] = __builtin_bit_cast(float, (254u - ex[i]) << 23);
+
+    uint8_t *Q = p.Q + z * p.strideQ;
+    float *S = p.S + z * p.strideS;
+    if constexpr (!TRANS) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = y[i][e] * inv[i];
+            const u32x2 q = {to_e4m3(v[0], v[1], v[2], v[3]), to_e4m3(v[4], v[5], v[6], v[7])};
+            if (r0 + i < p.rows) store8_e4m3(Q + (long long)(r0 + i) * p.ldq + c0, q, p.cols - c0, VEC);
+        }
+        if constexpr (SQUARE) {
+            if (tid == 0) S[(long long)tc * p.lds + tr] = __builtin_bit_cast(float, ex[0] << 23);
+        } else {
+            // lane i of each 16 has row i's
+            const int i = tid & 15;
+            unsigned mine = ex[0];
+#pragma unroll
+            for (int k = 1; k < 8; ++k) mine = i == k ? ex[k] : mine;
+            if (i < 8 && r0 + i < p.rows) S[(long long)tc * p.lds + r0 + i] = __builtin_bit_cast(float, mine << 23);
+        }
+    } else {
+        // Q's rows are X's columns: eight k of one row of Q per thread, 128 rows of 128 bytes
+        // through LDS, 8-byte piece j of row m at piece j ^ (m % 16)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = y[i][e] * inv[SQUARE ? 0 : e];
+            const u32x2 q = {to_e4m3(v[0], v[1], v[2], v[3]), to_e4m3(v[4], v[5], v[6], v[7])};
+            const int m = 8 * (tid & 15) + e, j = tid >> 4;
+            *reinterpret_cast<u32x2 *>(turned + m * 128 + 8 * (j ^ ((m >> 3) & 15))) = q;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int m = 16 * i + (tid >> 4), j = tid & 15;
+            const u32x2 q = *reinterpret_cast<const u32x2 *>(turned + m * 128 + 8 * (j ^ ((m >> 3) & 15)));
+            const int row = tc * 128 + m, k = tr * 128 + 8 * j;
+            if (row < p.cols && k < p.rows) store8_e4m3(Q + (long long)row * p.ldq + k, q, p.rows - k, VEC);
+        }
+        if constexpr (SQUARE) {
+            if (tid == 0) S[(long long)tr * p.lds + tc] = __builtin_bit_cast(float, ex[0] << 23);
+        } else if (tid < 16) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c0 + e < p.cols) S[(long long)tr * p.lds + c0 + e] = __builtin_bit_cast(float, ex[e] << 23);
+        }
+    }
+}
+
+template <class T, bool TRANS, bool SQUARE>
+hipError_t launch(const QuantArgs &a, unsigned blocks, bool vec, hipStream_t stream)
+{
+    if (vec)
+        hipLaunchKernelGGL((quant_kernel<T, TRANS, SQUARE, true>), dim3(blocks), dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((quant_kernel<T, TRANS, SQUARE, false>), dim3(blocks), dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_type(const QuantProblem &q, const QuantArgs &a, unsigned blocks, hipStream_t stream)
+{
+    const bool vec = reinterpret_cast<uintptr_t>(q.X) % 4 == 0 && q.ldx * sizeof(T) % 4 == 0 && q.strideX * sizeof(T) % 4 == 0 &&
+                     reinterpret_cast<uintptr_t>(q.Q) % 4 == 0 && q.ldq % 4 == 0 && q.strideQ % 4 == 0;
+    if (q.transpose) return q.block == 1 ? launch<T, true, false>(a, blocks, vec, stream) : launch<T, true, true>(a, blocks, vec, stream);
+    return q.block == 1 ? launch<T, false, false>(a, blocks, vec, stream) : launch<T, false, true>(a, blocks, vec, stream);
+}
+
+long long quant_tiles(const QuantProblem &p)
+{
+    return (p.M + 127LL) / 128 * ((p.K + 127LL) / 128);
+}
+
+}  // namespace
+
+bool quant_fits(const QuantProblem &p)
+{
+    const long long tiles = quant_tiles(p);
+    return grid_holds(tiles, 256) && grid_holds(tiles * p.batch, 256);
+}
+
+hipError_t launch_quant(const QuantProblem &p, QuantType type, hipStream_t stream)
+{
+    QuantArgs a;
+    a.rows = p.transpose ? p.K : p.M;
+    a.cols = p.transpose ? p.M : p.K;
+    a.tiles_r = (a.rows + 127) / 128;
+    a.tiles_c = (a.cols + 127) / 128;
+    a.X = p.X; a.ldx = p.ldx; a.strideX = p.strideX;
+    a.Q = p.Q; a.ldq = p.ldq; a.strideQ = p.strideQ;
+    a.S = p.S; a.lds = p.lds; a.strideS = p.strideS;
+    const unsigned blocks = (unsigned)(quant_tiles(p) * p.batch);
+    switch (type) {
+    case QuantType::f32: return launch_type<float>(p, a, blocks, stream);
+    case QuantType::f16: return launch_type<_Float16>(p, a, blocks, stream);
+    default: return launch_type<__bf16>(p, a, blocks, stream);
+    }
+}
+
+}  // namespace mi355gemm

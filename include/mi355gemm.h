@@ -342,6 +342,82 @@ int gemm_lora_bf16_f32acc_ex(int transB, int M, int N, int K, int rank, int adap
                              void *workspace, long long workspace_bytes, hipStream_t stream);
 long long gemm_lora_workspace(int M, int N, int K, int rank);
 
+/*
+ * 8-bit floating point (e4m3: four exponent bits, three fraction bits, 448 the largest value,
+ * NaN but no infinity) with a scale for each block of 128 k.  The number at (i, k) of a matrix
+ * is its 8-bit value times S[(k / 128) * lds + i / block]: a scale belongs to 128 k of one row
+ * (block 1) or of 128 rows (block 128), and scales lie with the blocks of k outermost.
+ */
+
+/*
+ * quant_e4m3_* -- Q and S from op(X), X in fp32, fp16 or bf16, for batch_count members:
+ *   transpose = 0: X is stored M x K (ldx >= max(1,K)); 1: K x M (ldx >= max(1,M)), Q is of its transpose.
+ *   Q : M x K, ldq >= max(1,K); bytes between rows are left as they are.
+ *   S : ceil(K / 128) x ceil(M / block), lds >= max(1, ceil(M / block)); block is 1 or 128.
+ *   strideX, strideQ, strideS: elements between members (strideQ and strideS at least a member).
+ * A scale is the least power of two s with max|x| / s <= 448 over the block's finite values, at least 2^-126,
+ * and 1 for a block of zeros; a value is x / s rounded to the nearest e4m3 value, ties to the even one (x / s itself
+ * is not rounded).  Infinities and NaN become NaN and do not count for the scale.
+ * ceil(M / 128) * ceil(K / 128) * batch_count < 2^23.
+ */
+int quant_e4m3_f32(int transpose, int block, int M, int K, const float *X, int ldx, long long strideX,
+                   uint8_t *Q, int ldq, long long strideQ, float *S, int lds, long long strideS,
+                   int batch_count, hipStream_t stream);
+int quant_e4m3_f16(int transpose, int block, int M, int K, const uint16_t *X, int ldx, long long strideX,
+                   uint8_t *Q, int ldq, long long strideQ, float *S, int lds, long long strideS,
+                   int batch_count, hipStream_t stream);
+int quant_e4m3_bf16(int transpose, int block, int M, int K, const uint16_t *X, int ldx, long long strideX,
+                    uint8_t *Q, int ldq, long long strideQ, float *S, int lds, long long strideS,
+                    int batch_count, hipStream_t stream);
+
+/*
+ * gemm_e4m3_f32acc -- C <- alpha * A * B^T + beta * C for the numbers that A (M x K) and B (N x K) stand for:
+ *     C[i,j] <- alpha * sum over kb of SA[kb,i] * SB[kb,j/blockB] * (sum over k in block kb of A[i,k] * B[j,k]) + beta * C[i,j]
+ *   A, lda, SA, ldsa : 8-bit values, lda >= max(1,K), and a scale per row and 128 k, ldsa >= max(1,M).
+ *   B, ldb, SB, ldsb : 8-bit values, ldb >= max(1,K), and a scale per blockB (1 or 128) rows and 128 k,
+ *                      ldsb >= max(1, ceil(N / blockB)).
+ * Scales are any fp32 values; a product of two scales is formed first, and rounded as fp32 rounds it.
+ * C is fp32, M x N.  A layer's output is x W^T with blocks of 128 of W; its input gradient is g W with W turned
+ * (quant_e4m3_* with transpose, or the same values and scales transposed), its weight gradient g^T x with both turned and blockB = 1.
+ * K <= 2^30.
+ */
+int gemm_e4m3_f32acc(int blockB, int M, int N, int K, float alpha,
+                     const uint8_t *A, int lda, const float *SA, int ldsa,
+                     const uint8_t *B, int ldb, const float *SB, int ldsb,
+                     float beta, float *C, int ldc, hipStream_t stream);
+
+/*
+ * gemm_grouped_e4m3_f32acc -- the same for rows in groups, each group with its own right operand:
+ *     C[r,:] <- alpha * A[rows[r],:] * B_g^T + beta * C[r,:]   for offsets[g] <= r < offsets[g+1]
+ * rows, offsets, groups, R and M as for gemm_grouped_*_f32acc_ex (a row takes its own row's scales along); B and SB hold
+ * groups members, strideB and strideSB apart (0: one shared).  groups <= 65535, K <= 2^30.
+ */
+int gemm_grouped_e4m3_f32acc(int blockB, int groups, int R, int N, int K, float alpha,
+                             const uint8_t *A, int M, int lda, const float *SA, int ldsa, const int32_t *rows,
+                             const uint8_t *B, int ldb, long long strideB, const float *SB, int ldsb, long long strideSB,
+                             const int32_t *offsets, float beta, float *C, int ldc, hipStream_t stream);
+
+/*
+ * orthogonalise_* -- an update (momentum, gradient) with its singular values moved towards 1 by Newton-Schulz steps, for
+ * batch_count members:
+ *     X <- G / |G|_F;  for each step (a, b, c):  X <- a X + (b A + c A A) X,  A = X X^T;   O <- alpha * X
+ *   G           : fp32 or bf16, M x N, ldg >= max(1,N), members strideG apart.
+ *   coefficients: host memory, a, b, c of each of the `steps` (1 to 100) steps; read during the call.
+ *   O           : bf16, M x N, ldo >= max(1,N), members strideO apart (at least a member).
+ * M > N is computed from the other side (A = X^T X), which is the same X.  |G|_F is summed in 64 bits; G = 0 gives 0,
+ * and an infinity or NaN in G makes its member NaN.  X is kept in fp32, the products are of fp16 copies (see
+ * orthogonalise.hip): the result is within 1e-3 of its norm, 4e-3 where G is of rank one, before it is rounded to bf16.
+ * Singular values that pass 7 on their way, or coefficients beyond some hundreds, leave fp16's range (infinities, NaN).
+ * M, N <= 65536; batch_count <= 65535; ceil(M / 64) * ceil(N / 64) * batch_count < 2^23.
+ */
+int orthogonalise_f32(int M, int N, int steps, const float *coefficients, float alpha,
+                      const float *G, int ldg, long long strideG, uint16_t *O, int ldo, long long strideO,
+                      int batch_count, void *workspace, long long workspace_bytes, hipStream_t stream);
+int orthogonalise_bf16(int M, int N, int steps, const float *coefficients, float alpha,
+                       const uint16_t *G, int ldg, long long strideG, uint16_t *O, int ldo, long long strideO,
+                       int batch_count, void *workspace, long long workspace_bytes, hipStream_t stream);
+long long orthogonalise_workspace(int M, int N, int batch_count);
+
 /* gemm_status_string -- a static, NUL-terminated description of a status code. */
 const char *gemm_status_string(int status);
 

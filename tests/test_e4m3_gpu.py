@@ -1,0 +1,416 @@
+"""8-bit operands with a scale per block of 128, against their definitions in 64 bits (GPU).
+
+Tolerances, u = 2^-24 (half a step of fp32, relative):
+  * quantising: scales and values are equal, bit for bit: x / s is exact for a power of two s, and e4m3 rounds it once.
+  * products: normalized error |C - ref| / (|alpha| sum of |terms| + |beta c|) <= 1e-5, the library's own bound for fp32
+    accumulation; bit-exact where every value is a small whole number and every scale a power of two.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import dense_gemm_optimisation_f32_amd as dg
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+TOL = 1e-5
+I32 = torch.int32
+E4M3 = torch.float8_e4m3fn
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    dg.load_library()
+    yield
+    torch.cuda.synchronize()
+
+
+def rng_of(*key):
+    return np.random.default_rng(list(str(key).encode()))
+
+
+# every e4m3 code's value
+CODES = np.array([(-1.0) ** (v >> 7) * ((8 + (v & 7)) * 2.0 ** ((v >> 3 & 15) - 10) if v >> 3 & 15 else (v & 7) * 2.0 ** -9) for v in range(256)])
+CODES[[0x7F, 0xFF]] = np.nan
+# the codes of the positive values in order, to round by comparison with the middles between neighbours
+POS = CODES[:0x7F]
+MIDDLE = (POS[1:] + POS[:-1]) / 2
+
+
+def nearest_e4m3(v):
+    """The code of the nearest e4m3 value of |v| <= 448, ties to the even code."""
+    a = np.abs(v)
+    lo = np.searchsorted(MIDDLE, a, side="left")          # middles below a
+    tie = (lo < len(MIDDLE)) & (MIDDLE[np.minimum(lo, len(MIDDLE) - 1)] == a)
+    code = np.where(tie & (lo % 2 == 1), lo + 1, lo)
+    return (code + 128 * np.signbit(v)).astype(np.uint8)
+
+
+def quant_oracle(y, block):
+    """codes (M, K) and scales (K blocks, M blocks) of y (64 bits)."""
+    M, K = y.shape
+    kb, mb = -(-K // 128), -(-M // block)
+    codes, scales = np.zeros((M, K), np.uint8), np.ones((kb, mb), np.float32)
+    for b in range(kb):
+        for i in range(mb):
+            part = y[i * block:(i + 1) * block, 128 * b:128 * b + 128]
+            fine = np.isfinite(part)
+            top = np.max(np.abs(part), where=fine, initial=0.0)
+            s = 1.0
+            if top > 0:
+                f, e = np.frexp(top / 448)
+                s = max(2.0 ** (e - (f == 0.5)), 2.0 ** -126)
+            scales[b, i] = s
+            codes[i * block:(i + 1) * block, 128 * b:128 * b + 128] = np.where(fine, nearest_e4m3(np.where(fine, part, 0) / s), 0x7F)
+    return codes, scales
+
+
+def to64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def codes_of(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def run_quant(t, transpose, block, M, K, X, ldx=None, ldq=None, lds=None, batch=1, fill=0x55):
+    """Q and S (whole buffers, gaps filled with a pattern) for X as (batch, stored rows, ldx)."""
+    ldx = ldx or X.shape[-1]
+    ldq, mb, kb = ldq or K, -(-M // block), -(-K // 128)
+    lds = lds or mb
+    Q = torch.full((batch, M, ldq), fill, dtype=torch.uint8, device="cuda").view(E4M3)
+    S = torch.full((batch, kb, lds), -7.0, device="cuda")
+    getattr(dg, f"quant_e4m3_{t}")(transpose, block, M, K, X, ldx, X.shape[-2] * ldx, Q, ldq, M * ldq, S, lds, kb * lds, batch)
+    torch.cuda.synchronize()
+    return codes_of(Q), S.cpu().numpy()
+
+
+# ------------------------------------------------------------------ quantising
+@pytest.mark.parametrize("t", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("transpose", [0, 1])
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("M,K", [(1, 1), (1, 128), (3, 127), (16, 256), (128, 128), (129, 130), (200, 513), (257, 1001)])
+def test_quant(t, transpose, block, M, K):
+    rng = rng_of(t, transpose, block, M, K)
+    y = rng.standard_normal((2, M, K)) * np.exp(2 * rng.standard_normal((2, M, 1)))
+    if M > 2:
+        y[0, 1] = 0                                                   # blocks of zeros
+    X = torch.from_numpy(np.ascontiguousarray(y.transpose(0, 2, 1) if transpose else y)).cuda().to(DT[t])
+    q, s = run_quant(t, transpose, block, M, K, X, batch=2)
+    for b in range(2):
+        x = to64(X[b])
+        codes, scales = quant_oracle(x.T if transpose else x, block)
+        assert np.array_equal(s[b], scales)
+        # (a zero's sign is kept, which the oracle's division does too)
+        assert np.array_equal(q[b], codes)
+
+
+@pytest.mark.parametrize("t,ldx,ldq,off", [("f32", 141, 131, 0), ("f16", 143, 133, 1), ("bf16", 144, 136, 0), ("bf16", 140, 132, 2)])
+@pytest.mark.parametrize("transpose", [0, 1])
+def test_quant_strides(t, transpose, ldx, ldq, off):
+    """Rows apart, starts at odd elements, scales wider than their blocks: the gaps are left alone."""
+    M, K = 130, 129
+    rng = rng_of("strides", t, ldx)
+    rows, cols = (K, M) if transpose else (M, K)
+    flat = torch.from_numpy(rng.standard_normal(off + rows * ldx)).cuda().to(DT[t])
+    X = flat[off:off + rows * ldx].view(rows, ldx)
+    q, s = run_quant(t, transpose, 1, M, K, X, ldx=ldx, ldq=ldq, lds=M + 3)
+    x = to64(X)[:, :cols]
+    codes, scales = quant_oracle(x.T if transpose else x, 1)
+    assert np.array_equal(q[0][:, :K], codes) and np.all(q[0][:, K:] == 0x55)
+    assert np.array_equal(s[0][:, :M], scales) and np.all(s[0][:, M:] == -7)
+
+
+@pytest.mark.parametrize("transpose", [0, 1])
+@pytest.mark.parametrize("block", [1, 128])
+def test_quant_special_values(transpose, block):
+    """Infinities and NaN become NaN and do not count; the smallest and largest numbers; ties go to the even code."""
+    M, K = 130, 260
+    rng = rng_of("special", transpose, block)
+    y = rng.standard_normal((M, K)).astype(np.float32)
+    y[0, :128] = 3e38                                   # largest scales
+    y[1, :] = 1e-42                                     # below fp32's normal numbers
+    y[2, 5], y[2, 200], y[3, 7] = np.inf, -np.inf, np.nan
+    y[4, :128] = np.nan                                 # nothing finite in the block
+    y[5, :128] = -0.0
+    y[6, :16] = np.arange(16) * 28.0                    # 448 / 16 steps: scale 1 or a power of two
+    y[7, :128] = np.float32(448 * 1.0000001)            # one step past 448: the next power
+    y[8, :64], y[8, 64] = (np.arange(64) + 8.5) * 4, 448.0    # middles between neighbours
+    X = torch.from_numpy(np.ascontiguousarray(y.T if transpose else y)).cuda()[None]
+    q, s = run_quant("f32", transpose, block, M, K, X)
+    codes, scales = quant_oracle(y.astype(np.float64), block)
+    assert np.array_equal(s[0], scales)
+    nan = np.isnan(CODES[codes])
+    assert np.array_equal(np.isnan(CODES[q[0]]), nan) and nan.sum() == 131
+    assert np.array_equal(q[0][~nan], codes[~nan])
+
+
+def test_quant_is_torchs_rounding():
+    """Every fp16 value in e4m3's range, at scale 1, as torch rounds it."""
+    x = np.arange(65536, dtype=np.uint16).view(np.float16)
+    x = x[np.abs(x.astype(np.float64)) < 256]
+    x = np.concatenate([x, np.zeros(-len(x) % 127, np.float16)]).reshape(-1, 127)
+    X = torch.from_numpy(np.concatenate([np.full((len(x), 1), 448, np.float16), x], 1)).cuda()
+    q, s = run_quant("f16", 0, 1, X.shape[0], 128, X[None])
+    assert np.all(s == 1)
+    assert np.array_equal(q[0], codes_of(X.float().to(E4M3)))
+
+
+def test_quant_large():
+    """More than 2^32 bytes of input, the last rows."""
+    M, K = 8200, 262144
+    X = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    X[-130:] = torch.randn(130, K, device="cuda")
+    Q = torch.empty(M, K, dtype=E4M3, device="cuda")
+    S = torch.empty(K // 128, M, device="cuda")
+    dg.quant_e4m3_bf16(0, 1, M, K, X, K, 0, Q, K, 0, S, M, 0)
+    torch.cuda.synchronize()
+    assert torch.all(S[:, :-130] == 1) and not torch.any(Q[:-130].view(torch.uint8))
+    codes, scales = quant_oracle(to64(X[-130:, -256:]), 1)
+    assert np.array_equal(codes_of(Q[-130:, -256:].contiguous()), codes) and np.array_equal(S[-2:, -130:].cpu().numpy(), scales)
+
+
+# ------------------------------------------------------------------ products
+def operand(rng, rows, K, block, ints=False, ld=None, lds=None, offset=0):
+    """Device values and scales, the numbers they stand for in 64 bits, and what the call takes as ld and lds."""
+    ld, kb, rb = ld or K, -(-K // 128), -(-rows // block)
+    lds = lds or rb
+    if ints:
+        codes = nearest_e4m3(rng.integers(-4, 5, (rows, ld)).astype(np.float64))
+        scales = 2.0 ** rng.integers(-2, 3, (kb, lds))
+    else:
+        codes = nearest_e4m3(np.clip(rng.standard_normal((rows, ld)) * 100, -448, 448))
+        scales = np.exp(rng.standard_normal((kb, lds)))
+    scales = scales.astype(np.float32)
+    codes[:, K:] = 0x7F                                              # NaN between the rows must not matter
+    scales[:, rb:] = np.nan
+    flat = torch.zeros(offset + codes.size, dtype=torch.uint8, device="cuda")
+    flat[offset:] = torch.from_numpy(codes.reshape(-1)).cuda()
+    full = np.repeat(np.repeat(scales[:, :rb].T.astype(np.float64), block, 0)[:rows], 128, 1)[:, :K]
+    return flat[offset:].view(E4M3), torch.from_numpy(scales).cuda(), CODES[codes[:, :K]] * full, ld, lds
+
+
+def check(C, ref, bound, ints=False):
+    C = C.astype(np.float64)
+    if ints:
+        assert np.array_equal(C, ref)
+    else:
+        assert np.all(np.isfinite(C))
+        err = np.max(np.abs(C - ref) / np.maximum(bound, 1e-300)) if C.size else 0.0
+        assert err <= TOL, err
+
+
+@pytest.mark.parametrize("ints", [False, True])
+@pytest.mark.parametrize("blockB", [1, 128])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 33, 128), (1, 4096, 256), (2, 130, 1000), (16, 512, 2048), (31, 100, 16), (33, 64, 144),
+                                   (64, 64, 128), (65, 129, 400), (100, 300, 4096), (128, 128, 128), (200, 257, 777), (256, 256, 512), (257, 385, 640),
+                                   (300, 1024, 129), (513, 500, 1024), (1001, 777, 513), (1024, 1024, 256)])
+def test_product(blockB, M, N, K, ints):
+    rng = rng_of("product", blockB, M, N, K, ints)
+    A, SA, a, lda, ldsa = operand(rng, M, K, 1, ints)
+    B, SB, b, ldb, ldsb = operand(rng, N, K, blockB, ints)
+    c0 = rng.integers(-8, 9, (M, N)).astype(np.float32) if ints else rng.standard_normal((M, N)).astype(np.float32)
+    for alpha, beta in ((1.0, 0.0), (1.5, -0.5)):
+        C = torch.from_numpy(c0.copy()).cuda() if beta else torch.full((M, N), float("nan"), device="cuda")
+        dg.gemm_e4m3_f32acc(blockB, M, N, K, alpha, A, lda, SA, ldsa, B, ldb, SB, ldsb, beta, C, N)
+        check(C.cpu().numpy(), alpha * (a @ b.T) + beta * c0, abs(alpha) * (np.abs(a) @ np.abs(b).T) + abs(beta * c0), ints)
+
+
+@pytest.mark.parametrize("M,N,K,lda,ldb,offA,offB", [
+    (70, 90, 200, 203, 201, 1, 3),          # odd rows and starts
+    (70, 90, 200, 204, 208, 4, 0),          # dword-aligned rows
+    (300, 260, 256, 272, 288, 16, 16), (8, 300, 384, 400, 386, 0, 2), (5, 64, 130, 160, 160, 0, 0), (260, 270, 272, 288, 276, 0, 4)])
+@pytest.mark.parametrize("blockB", [1, 128])
+def test_product_strides(blockB, M, N, K, lda, ldb, offA, offB):
+    """Rows apart, starts at any byte, wide scales and C; NaN in all gaps."""
+    rng = rng_of("strides", blockB, M, N, K, lda)
+    A, SA, a, _, ldsa = operand(rng, M, K, 1, ld=lda, lds=M + 5, offset=offA)
+    B, SB, b, _, ldsb = operand(rng, N, K, blockB, ld=ldb, lds=-(-N // blockB) + 2, offset=offB)
+    C = torch.full((M, N + 7), 3.0, device="cuda")
+    dg.gemm_e4m3_f32acc(blockB, M, N, K, 1.0, A, lda, SA, ldsa, B, ldb, SB, ldsb, 0.0, C, N + 7)
+    got = C.cpu().numpy()
+    check(got[:, :N], a @ b.T, np.abs(a) @ np.abs(b).T)
+    assert np.all(got[:, N:] == 3)
+
+
+@pytest.mark.parametrize("M,N,K", [(4, 96, 512), (300, 300, 400)])
+def test_product_special_values(M, N, K):
+    """A NaN value reaches its row (column) alone, an infinite scale its row's block, and scale 0 gives zeros."""
+    rng = rng_of("special", M)
+    A, SA, a, lda, ldsa = operand(rng, M, K, 1)
+    B, SB, b, ldb, ldsb = operand(rng, N, K, 1)
+    A.view(torch.uint8)[1 * K + 130] = 0x7F
+    B.view(torch.uint8)[5 * K + 3] = 0xFF
+    SA[:, 2] = 0
+    a[1, 130], b[5, 3] = np.nan, np.nan
+    a[2] = 0
+    C = torch.empty(M, N, device="cuda")
+    dg.gemm_e4m3_f32acc(1, M, N, K, 1.0, A, lda, SA, ldsa, B, ldb, SB, ldsb, 0.0, C, N)
+    got, ref = C.cpu().numpy(), a @ b.T
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    fine = ~np.isnan(ref)
+    bound = (np.nan_to_num(np.abs(a)) @ np.nan_to_num(np.abs(b)).T)[fine]
+    assert np.max(np.abs(got[fine] - ref[fine]) / np.maximum(bound, 1e-30)) <= TOL
+    assert np.all(got[2][fine[2]] == 0)
+
+
+@pytest.mark.parametrize("M,N", [(3, 200), (40, 70)])
+def test_product_without_a_product(M, N):
+    """K = 0 or alpha = 0: C <- beta * C, operands not read."""
+    c0 = torch.randn(M, N, device="cuda")
+    for K, alpha in ((0, 1.0), (256, 0.0)):
+        for beta in (0.0, 2.0):
+            C = c0.clone() if beta else torch.full_like(c0, float("nan"))
+            dg.gemm_e4m3_f32acc(128, M, N, K, alpha, None, max(K, 1), None, M, None, max(K, 1), None, 2, beta, C, N)
+            assert torch.equal(C, beta * c0 if beta else torch.zeros_like(c0))
+
+
+def grouped_case(rng, blockB, G, counts, N, K, T, ints=False, lda=None, ldb=None):
+    R = int(sum(counts))
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    A, SA, a, lda, ldsa = operand(rng, T or R, K, 1, ints, ld=lda)
+    members = [operand(rng, N, K, blockB, ints, ld=ldb) for _ in range(G)]
+    B = torch.stack([m[0].view(torch.uint8) for m in members]).view(E4M3)
+    SB = torch.stack([m[1] for m in members])
+    rows = rng.integers(0, T, R).astype(np.int32) if T else None
+    x = a if rows is None else a[rows]
+    ref, bound = np.zeros((R, N)), np.zeros((R, N))
+    for g in range(G):
+        s = slice(offsets[g], offsets[g + 1])
+        ref[s], bound[s] = x[s] @ members[g][2].T, np.abs(x[s]) @ np.abs(members[g][2]).T
+    return R, A, lda, SA, ldsa, rows, B, members[0][3], SB, members[0][4], offsets, ref, bound
+
+
+@pytest.mark.parametrize("ints", [False, True])
+@pytest.mark.parametrize("blockB,counts,N,K,T", [
+    (128, [1], 64, 128, 0), (128, [0, 3, 0, 0, 1], 200, 256, 0), (1, [2, 0, 5], 100, 384, 4), (128, [2] * 64, 256, 512, 16),
+    (128, [40, 0, 1, 300, 25], 300, 272, 0), (128, [40, 0, 1, 300, 25], 300, 272, 90), (1, [130, 70], 260, 400, 50),
+    (128, [500, 13, 700], 512, 256, 0), (128, [257, 255, 0, 256], 384, 640, 300), (128, [33, 64, 65], 77, 131, 40), (1, [1000], 130, 129, 0)])
+def test_grouped(blockB, counts, N, K, T, ints):
+    rng = rng_of("grouped", blockB, counts, N, K, T, ints)
+    G = len(counts)
+    R, A, lda, SA, ldsa, rows, B, ldb, SB, ldsb, offsets, ref, bound = grouped_case(rng, blockB, G, counts, N, K, T, ints)
+    at = None if rows is None else torch.from_numpy(rows).cuda()
+    c0 = rng.integers(-8, 9, (R, N)).astype(np.float32)
+    for alpha, beta in ((1.0, 0.0), (-2.0, 0.5)):
+        C = torch.from_numpy(c0.copy()).cuda() if beta else torch.full((R, N), float("nan"), device="cuda")
+        dg.gemm_grouped_e4m3_f32acc(blockB, G, R, N, K, alpha, A, T or R, lda, SA, ldsa, at, B, ldb, N * ldb, SB, ldsb, SB[0].numel(),
+                                    torch.from_numpy(offsets).cuda(), beta, C, N)
+        check(C.cpu().numpy(), alpha * ref + beta * c0, abs(alpha) * bound + abs(beta * c0), ints)
+
+
+@pytest.mark.parametrize("R,N,K", [(20, 90, 256), (200, 300, 256), (60, 90, 131)])
+def test_grouped_rows_outside(R, N, K):
+    """Row indices outside A give zeros even where B holds NaN, rows in no group stay as they are, offsets are clamped."""
+    rng = rng_of("outside", R)
+    A, SA, a, lda, ldsa = operand(rng, 10, K, 1)
+    B, SB, b, ldb, ldsb = operand(rng, N, K, 128)
+    B.view(torch.uint8)[3 * K + 1] = 0x7F
+    b[3] = np.nan
+    rows = rng.integers(0, 10, R).astype(np.int32)
+    rows[[2, 5, R - 6]] = [-1, 10, 2**31 - 1]
+    C = torch.full((R, N), 5.0, device="cuda")
+    offsets = torch.tensor([-3, R - 4], dtype=I32, device="cuda")
+    dg.gemm_grouped_e4m3_f32acc(128, 1, R, N, K, 1.0, A, 10, lda, SA, ldsa, torch.from_numpy(rows).cuda(), B, ldb, 0, SB, ldsb, 0, offsets,
+                                0.0, C, N)
+    got = C.cpu().numpy()
+    assert np.all(got[R - 4:] == 5)
+    held = (rows >= 0) & (rows < 10)
+    ref = a[np.where(held, rows, 0)] @ b.T
+    bound = np.abs(a)[np.where(held, rows, 0)] @ np.nan_to_num(np.abs(b)).T
+    ref[~held] = 0
+    got, ref, bound = got[:R - 4], ref[:R - 4], bound[:R - 4]
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    fine = ~np.isnan(ref)
+    assert np.max(np.abs(got[fine] - ref[fine]) / np.maximum(bound[fine], 1e-30)) <= TOL   # (a column of NaN has no bound: 0 / 0)
+
+
+def test_grouped_descending_offsets():
+    """Offsets that descend and rise again stay inside every operand."""
+    rng = rng_of("descending")
+    A, SA, _, lda, ldsa = operand(rng, 300, 128, 1)
+    B, SB, _, ldb, ldsb = operand(rng, 64, 128, 128)
+    C = torch.zeros(300 + 64, 64, device="cuda")
+    for offsets in ([0, 300, 0, 300, 0, 300], [300, 0, 300, -5, 2**31 - 1, 7]):
+        dg.gemm_grouped_e4m3_f32acc(128, 5, 300, 64, 128, 1.0, A, 300, lda, SA, ldsa, None, B, ldb, 0, SB, ldsb, 0,
+                                    torch.tensor(offsets, dtype=I32, device="cuda"), 0.0, C, 64)
+    torch.cuda.synchronize()
+    assert not torch.any(C[300:])
+
+
+def test_same_bits_again_and_elsewhere():
+    """The same bits from call to call, on another stream, and in a captured graph replayed between eager calls."""
+    rng = rng_of("again")
+    M, N, K = 300, 520, 1024
+    A, SA, _, lda, ldsa = operand(rng, M, K, 1)
+    B, SB, _, ldb, ldsb = operand(rng, N, K, 128)
+    X = torch.from_numpy(rng.standard_normal((M, K)).astype(np.float32)).cuda()
+    Q, S = torch.empty(M, K, dtype=E4M3, device="cuda"), torch.empty(K // 128, M, device="cuda")
+    C, D, E = (torch.empty(M, N, device="cuda") for _ in range(3))
+
+    def both(out):
+        dg.quant_e4m3_f32(0, 1, M, K, X, K, 0, Q, K, 0, S, M, 0)
+        dg.gemm_e4m3_f32acc(128, M, N, K, 1.0, Q, K, S, M, B, ldb, SB, ldsb, 0.0, out, N)
+
+    both(C)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both(D)
+    torch.cuda.synchronize()
+    assert torch.equal(C, D)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both(E)
+    for i in range(3):
+        X.mul_(-1.5)
+        both(C)
+        E.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(C, E), i
+
+
+def test_linear_layer_and_update():
+    """A layer's training step in 8 bits: output, input gradient and weight gradient against the same formulas in 64 bits on the
+    quantised numbers, then the weight's update from its gradient."""
+    T, D, F = 200, 384, 260
+    rng = rng_of("layer")
+    x = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32)).cuda().bfloat16()
+    w = torch.from_numpy(rng.standard_normal((F, D)).astype(np.float32) * D ** -0.5).cuda()
+    g = torch.from_numpy(rng.standard_normal((T, F)).astype(np.float32)).cuda()
+
+    def quant(t, v, transpose, block):
+        M, K = v.shape[::-1] if transpose else v.shape
+        Q, S = torch.empty(M, K, dtype=E4M3, device="cuda"), torch.empty(-(-K // 128), -(-M // block), device="cuda")
+        getattr(dg, f"quant_e4m3_{t}")(transpose, block, M, K, v, v.shape[1], 0, Q, K, 0, S, S.shape[1], 0)
+        full = np.repeat(np.repeat(to64(S).T, block, 0)[:M], 128, 1)[:, :K]
+        return Q, S, CODES[codes_of(Q)] * full
+
+    def product(blockB, a, b):
+        M, N, K = a[0].shape[0], b[0].shape[0], a[0].shape[1]
+        C = torch.empty(M, N, device="cuda")
+        dg.gemm_e4m3_f32acc(blockB, M, N, K, 1.0, a[0], K, a[1], M, b[0], K, b[1], b[1].shape[1], 0.0, C, N)
+        check(C.cpu().numpy(), a[2] @ b[2].T, np.abs(a[2]) @ np.abs(b[2]).T)
+        return C
+
+    y = product(128, quant("bf16", x, 0, 1), quant("f32", w, 0, 128))
+    dx = product(128, quant("f32", g, 0, 1), quant("f32", w, 1, 128))
+    dw = product(1, quant("f32", g, 1, 1), quant("bf16", x, 1, 1))
+    assert y.shape == (T, F) and dx.shape == (T, D) and dw.shape == (F, D)
+    # 8 bits: every value within 2^-4 of itself or 2^-10 of its scale, two operands; the sums' errors add up at random
+    for got, ref in ((y, x.double() @ w.double().t()), (dx, g.double() @ w.double()), (dw, g.double().t() @ x.double())):
+        assert torch.linalg.norm(got.double() - ref) <= 2 * 2.0 ** -4 * torch.linalg.norm(ref)
+    O = torch.empty(F, D, dtype=torch.bfloat16, device="cuda")
+    dg.orthogonalise_f32(F, D, [(1.875, -1.25, 0.375)] * 12, 1.0, dw, D, 0, O, D, 0)
+    # dw is a sum over T tokens, of rank T < F: T singular values at 1, and nothing in the directions it does not have
+    s = np.linalg.svd(to64(O), compute_uv=False)
+    assert np.all(np.abs(s[:T] - 1) < 2e-2) and np.all(s[T:] < 2e-2), (s[:T].min(), s.max(), s[T:].max())
+    u, _, vt = np.linalg.svd(to64(dw), full_matrices=False)
+    polar = u[:, :T] @ vt[:T]
+    assert np.linalg.norm(to64(O) - polar) <= 5e-3 * np.linalg.norm(polar)

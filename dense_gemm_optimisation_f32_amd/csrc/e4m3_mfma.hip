@@ -35,6 +35,7 @@ struct E4m3Args {
     float *C;
     long long ldc;
     int tiles_m, tiles_n;     // with offsets: tiles_m is what any ascending offsets can need
+    bool past_cache;          // C is larger than what the memory-side cache keeps of it
 };
 
 // Sixteen e4m3 values as fp16, exactly (NaN stays NaN), in order.
@@ -182,6 +183,293 @@ __global__ __launch_bounds__(256) void e4m3_any_kernel(E4m3Args p)
     }
 }
 
+// Direct-to-LDS load of a dword per lane (dma16 in stage16.h has the notes).
+__device__ __forceinline__ void dma4_at(const void *p, unsigned lds_addr)
+{
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" : : "v"(p), "s"(lds_addr) : "memory", "m0");
+}
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) float lds_float;
+
+template <int BM_, int BN_, int STAGES_, int WM_, int WN_>
+struct E4m3Cfg {
+    static constexpr int BM = BM_, BN = BN_, BK = 128, STAGES = STAGES_, WM = WM_, WN = WN_;
+    static constexpr int NW = WM * WN, NT = 64 * NW;
+    static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
+    static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK;                            // a slice
+    static constexpr int A_LOADS = A_BYTES / 1024 / NW, B_LOADS = B_BYTES / 1024 / NW;    // per wave
+    static constexpr int S_LOADS = ((BM + BN) / 64 + NW - 1) / NW;                        // of 64 scales
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 256 * NW * S_LOADS;
+    static constexpr int LOADS = A_LOADS + B_LOADS + S_LOADS;
+    static constexpr int LDS = STAGES * STAGE_BYTES;
+    static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0 && BM % 64 == 0 && BN % 64 == 0,
+                  "slices split evenly over the waves");
+    static_assert(LDS <= 160 * 1024 && LOADS * STAGES < 64 && TN <= 128, "LDS, outstanding loads");
+};
+
+// ---------------------------------------------------------------------------
+// Tiles fed by direct-to-LDS loads.  A slice of 128 k (one block of scales) of both
+// operands, with the scales of its rows and columns, is a slot of a ring of STAGES; a lane
+// reads 16 bytes of a row, makes fp16 of them and has the operands of two matrix-core ops.
+// Needs: dword-aligned rows, K % 16 == 0 (no chunk straddles the end), the rows' offsets
+// from the operand's start (A, rows looked up) or from the tile's within 32 bits.
+template <class Cfg, int BLOCKB>
+__global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
+{
+    constexpr int BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK, S = Cfg::STAGES, FM = Cfg::FM, FN = Cfg::FN;
+    constexpr int A_LOADS = Cfg::A_LOADS, B_LOADS = Cfg::B_LOADS, S_LOADS = Cfg::S_LOADS, LOADS = Cfg::LOADS;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[Cfg::LDS];
+    const unsigned lds0 = (unsigned)(uintptr_t)lds;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int uwave = __builtin_amdgcn_readfirstlane(wave);
+    int group = 0, m0, m_end, one, tm, tn;
+    if (p.offsets) {
+        const int total = count_row_tiles(p.offsets, p.groups, p.R, BM, p.tiles_m);
+        if ((long long)blockIdx.x >= (long long)total * p.tiles_n) return;
+        tile_coords((int)blockIdx.x, 0, 1, total, p.tiles_n, &one, &tm, &tn);
+        const RowTile rt = find_row_tile(p.offsets, p.groups, p.R, BM, tm);
+        if (rt.group < 0) return;
+        group = rt.group;
+        m0 = rt.first;
+        m_end = rt.end;
+    } else {
+        tile_coords((int)blockIdx.x, 0, 1, p.tiles_m, p.tiles_n, &one, &tm, &tn);
+        m0 = tm * BM;
+        m_end = p.R;
+    }
+    const int n0 = tn * BN, N = p.N, K = p.K;
+    const int limA = m_end - m0 < BM ? m_end - m0 : BM, limB = N - n0 < BN ? N - n0 : BN;
+
+    // rows outside the tile's re-read valid ones; their results are not stored
+    auto row_of = [&](int r) {
+        int at = m0 + (r < limA ? r : limA - 1);
+        if (p.rows) at = p.rows[at];
+        return (unsigned)at < (unsigned)p.a_rows ? at : 0;   // (its products are dropped in the epilogue)
+    };
+    unsigned offA[A_LOADS], offB[B_LOADS];
+    const char *Ab = reinterpret_cast<const char *>(p.A) + (p.rows ? 0 : (long long)m0 * p.lda);
+    const char *Bb = reinterpret_cast<const char *>(p.B) + (long long)group * p.strideB + (long long)n0 * p.ldb;
+#pragma unroll
+    for (int i = 0; i < A_LOADS; ++i) {
+        const int r = 8 * (uwave * A_LOADS + i) + lane / 8;
+        offA[i] = (unsigned)((row_of(r) - (p.rows ? 0 : m0)) * p.lda) + 16 * ((lane % 8) ^ swz_a<8>(r));
+    }
+#pragma unroll
+    for (int i = 0; i < B_LOADS; ++i) {
+        const int r = 8 * (uwave * B_LOADS + i) + lane / 8;
+        offB[i] = (unsigned)((r < limB ? r : limB - 1) * p.ldb) + 16 * ((lane % 8) ^ swz_a<8>(r));
+    }
+    // 64 rows' or columns' scales a load: those of A, then those of B, spread to one for each column
+    const float *scale[S_LOADS];
+    long long scale_step[S_LOADS];
+#pragma unroll
+    for (int i = 0; i < S_LOADS; ++i) {
+        const int r = 64 * (uwave * S_LOADS + i) + lane;
+        if (64 * (uwave * S_LOADS + i) < BM) {
+            scale[i] = p.SA + row_of(r);
+            scale_step[i] = p.ldsa;
+        } else {
+            const int c = r - BM;
+            scale[i] = p.SB + (long long)group * p.strideSB + (n0 + (c < limB ? c : limB - 1)) / BLOCKB;
+            scale_step[i] = p.ldsb;
+        }
+    }
+    const int slices = (K + BK - 1) / BK, nk = slices < S ? S : slices;   // (slices past the last are zeros)
+    auto issue = [&](int t, int slot) __attribute__((always_inline)) {
+        const unsigned at = __builtin_amdgcn_readfirstlane(lds0 + slot * Cfg::STAGE_BYTES);
+        const unsigned la = at + uwave * A_LOADS * 1024, lb = at + Cfg::A_BYTES + uwave * B_LOADS * 1024;
+        const unsigned ls = at + Cfg::A_BYTES + Cfg::B_BYTES + uwave * S_LOADS * 256;
+        const char *a = uniform(Ab + (long long)t * BK), *b = uniform(Bb + (long long)t * BK);
+        const int kb = t < slices ? t : slices - 1;
+#pragma unroll
+        for (int i = 0; i < S_LOADS; ++i) dma4_at(scale[i] + kb * scale_step[i], ls + 256 * i);
+        if ((t + 1) * BK <= K) {
+#pragma unroll
+            for (int i = 0; i < A_LOADS; ++i) dma16(a, offA[i], la + 1024 * i);
+#pragma unroll
+            for (int i = 0; i < B_LOADS; ++i) dma16(b, offB[i], lb + 1024 * i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < A_LOADS; ++i) {
+                const int k = t * BK + 16 * ((lane % 8) ^ swz_a<8>(8 * (uwave * A_LOADS + i) + lane / 8));
+                dma16_at(k < K ? (const void *)(a + offA[i]) : (const void *)zero_chunk, la + 1024 * i);
+            }
+#pragma unroll
+            for (int i = 0; i < B_LOADS; ++i) {
+                const int k = t * BK + 16 * ((lane % 8) ^ swz_a<8>(8 * (uwave * B_LOADS + i) + lane / 8));
+                dma16_at(k < K ? (const void *)(b + offB[i]) : (const void *)zero_chunk, lb + 1024 * i);
+            }
+        }
+    };
+
+    const int wm = wave / Cfg::WN, wn = wave % Cfg::WN, lr = lane & 31, lk = lane >> 5;
+    unsigned chunk[4];   // of substep s, within a row's 128 bytes (rows 32 apart have the same swizzle)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) chunk[s] = 16 * ((2 * s + lk) ^ swz_a<8>(lr));
+    const unsigned baseA = lds0 + (wm * Cfg::TM + lr) * BK, baseB = lds0 + Cfg::A_BYTES + (wn * Cfg::TN + lr) * BK;
+    const unsigned baseS = lds0 + Cfg::A_BYTES + Cfg::B_BYTES;
+
+    f32x16 acc[FM][FN], sum[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
+    u32x4 ra[FM], rb[FN];
+    Half16 fa[FM], fb[FN];
+    auto read = [&](int slot, int s) __attribute__((always_inline)) {
+        const unsigned at = slot * Cfg::STAGE_BYTES + chunk[s];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) ra[i] = *(const lds_u32x4 *)(uintptr_t)(baseA + at + i * 32 * BK);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) rb[j] = *(const lds_u32x4 *)(uintptr_t)(baseB + at + j * 32 * BK);
+    };
+    auto convert = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) fa[i] = to_f16(ra[i]);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) fb[j] = to_f16(rb[j]);
+    };
+    // the slice's scales
+    float sa[FM], sb[BLOCKB == 1 ? 16 * FN : 1];
+    auto read_scales = [&](int slot) __attribute__((always_inline)) {
+        const unsigned at = baseS + slot * Cfg::STAGE_BYTES;
+#pragma unroll
+        for (int i = 0; i < FM; ++i) sa[i] = *(const lds_float *)(uintptr_t)(at + 4 * (wm * Cfg::TM + 32 * i + lr));
+        const unsigned ab = at + 4 * (BM + wn * Cfg::TN);
+        if constexpr (BLOCKB == 1) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const f32x4_t v = *(const lds_f32x4 *)(uintptr_t)(ab + 4 * (32 * j + 8 * g + 4 * lk));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sb[16 * j + 4 * g + e] = v[e];
+                }
+        } else {
+            sb[0] = *(const lds_float *)(uintptr_t)ab;   // (the wave's columns lie in one block)
+#pragma unroll
+            for (int i = 0; i < FM; ++i) sa[i] *= sb[0];
+        }
+    };
+    auto add = [&](int i, int j) __attribute__((always_inline)) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            acc[i][j][r] = __builtin_fmaf(BLOCKB == 1 ? sa[i] * sb[16 * j + r] : sa[i], sum[i][j][r], acc[i][j][r]);
+    };
+    auto lds_barrier = [&]() {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    };
+
+    if (K > 0) {
+#pragma unroll
+        for (int t = 0; t < S; ++t) issue(t, t);
+        wait_vmcnt<LOADS * (S - 1)>();
+        lds_barrier();
+        read(0, 0);
+        auto slice = [&](int t, int slot, auto pending, auto refill, auto more) __attribute__((always_inline)) {
+            const int next = slot + 1 == S ? 0 : slot + 1;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                convert();
+                if (s < 3) {
+                    read(slot, s + 1);
+                    if (s == 2) read_scales(slot);
+                } else if constexpr (decltype(more)::value) {
+                    wait_vmcnt<LOADS * decltype(pending)::value>();
+                    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave has read its slot
+                    lds_barrier();
+                    if constexpr (decltype(refill)::value) issue(t + S, slot);
+                    read(next, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+                        sum[i][j] = mfma16<false>(fb[j].lo, fa[i].lo, s == 0 ? f32x16{} : sum[i][j]);
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) sum[i][j] = mfma16<false>(fb[j].hi, fa[i].hi, sum[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) add(i, j);
+        };
+        int t = 0, slot = 0;
+        for (; t + S < nk; ++t) {
+            slice(t, slot, std::integral_constant<int, S - 2>{}, std::true_type{}, std::true_type{});
+            slot = slot + 1 == S ? 0 : slot + 1;
+        }
+        auto after = [&](int d) { return (slot + d) % S; };
+        slice(t, slot, std::integral_constant<int, S - 2>{}, std::false_type{}, std::true_type{});
+        if constexpr (S >= 3) slice(t + 1, after(1), std::integral_constant<int, S - 3>{}, std::false_type{}, std::true_type{});
+        if constexpr (S >= 4) slice(t + 2, after(2), std::integral_constant<int, S - 4>{}, std::false_type{}, std::true_type{});
+        slice(nk - 1, after(S - 1), std::integral_constant<int, 0>{}, std::false_type{}, std::false_type{});
+    }
+
+    // Epilogue by rows through the ring: 32 rows of the wave's tile at a time, 16-byte chunk c of row r at
+    // chunk c ^ (r % LPR).
+    constexpr int LPR = Cfg::TN / 4, RPI = 64 / LPR, NQ = 32 / RPI;
+    static_assert(Cfg::NW * 32 * Cfg::TN * 4 <= Cfg::LDS, "staging area exceeds the ring");
+    const unsigned stage = lds0 + wave * 32 * Cfg::TN * 4;
+    lds_barrier();
+    const int er = lane / LPR, ec = lane % LPR;
+    const int col = n0 + wn * Cfg::TN + 4 * ec;
+    const float alpha = p.alpha, beta = p.beta;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int first = m0 + wm * Cfg::TM + 32 * i;
+        if (first >= m_end) break;
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x4_t v = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+                *(lds_f32x4 *)(uintptr_t)(stage + lr * Cfg::TN * 4 + (((8 * j + 2 * g + lk) ^ (lr & (LPR - 1))) * 16)) = v;
+            }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        f32x4_t v[NQ];
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            const int r = q * RPI + er;
+            v[q] = *(const lds_f32x4 *)(uintptr_t)(stage + r * Cfg::TN * 4 + ((ec ^ (r & (LPR - 1))) * 16));
+        }
+        if (p.rows) {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                const int row = first + q * RPI + er;
+                if (row < m_end && (unsigned)p.rows[row] >= (unsigned)p.a_rows) v[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            }
+        } else if (m_end > p.a_rows) {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+                if (first + q * RPI + er >= p.a_rows) v[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+        if (beta != 0.f) {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+                store_row4<true, true>(p.C, p.ldc, first + q * RPI + er, col, v[q], alpha, beta, m_end, N);
+        } else if (first + 32 <= m_end && n0 + BN <= N && p.past_cache) {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+                __builtin_nontemporal_store(alpha * v[q], reinterpret_cast<f32x4_g *>(p.C + (long long)(first + q * RPI + er) * p.ldc + col));
+        } else if (first + 32 <= m_end && n0 + BN <= N) {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+                store_row4<false, false>(p.C, p.ldc, first + q * RPI + er, col, v[q], alpha, beta, m_end, N);
+        } else {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+                store_row4<true, false>(p.C, p.ldc, first + q * RPI + er, col, v[q], alpha, beta, m_end, N);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+}
+
 E4m3Args arguments(const E4m3Problem &q)
 {
     E4m3Args a = {};
@@ -191,6 +479,7 @@ E4m3Args arguments(const E4m3Problem &q)
     a.B = q.B; a.ldb = q.ldb; a.strideB = q.strideB; a.SB = q.SB; a.ldsb = q.ldsb; a.strideSB = q.strideSB;
     a.offsets = q.offsets;
     a.C = q.C; a.ldc = q.ldc;
+    a.past_cache = 4LL * q.R * q.N >= (192LL << 20);   // (the memory-side cache holds 256 MiB)
     return a;
 }
 
@@ -198,6 +487,30 @@ E4m3Args arguments(const E4m3Problem &q)
 long long row_tiles(const E4m3Problem &q, int bm)
 {
     return q.offsets ? q.R / bm + (q.groups < q.R ? q.groups : q.R) : (q.R + (long long)bm - 1) / bm;
+}
+
+// The direct-to-LDS kernels take these operands.
+bool dma_ok(const E4m3Problem &q)
+{
+    auto words = [](const void *p, long long ld, long long stride) {
+        return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld % 4 == 0 && stride % 4 == 0;
+    };
+    return q.K > 0 && q.K % 16 == 0 && words(q.A, q.lda, 0) && words(q.B, q.ldb, q.strideB) && 256 * q.lda < (1LL << 31) &&
+           256 * q.ldb < (1LL << 31) && (!q.rows || q.M * q.lda < (1LL << 32));
+}
+
+template <class Cfg>
+hipError_t launch_dma(const E4m3Problem &q, hipStream_t stream)
+{
+    E4m3Args a = arguments(q);
+    a.tiles_m = (int)row_tiles(q, Cfg::BM);
+    a.tiles_n = (q.N + Cfg::BN - 1) / Cfg::BN;
+    const dim3 grid((unsigned)((long long)a.tiles_m * a.tiles_n));
+    if (q.blockB == 1)
+        hipLaunchKernelGGL((e4m3_dma_kernel<Cfg, 1>), grid, dim3(Cfg::NT), 0, stream, a);
+    else
+        hipLaunchKernelGGL((e4m3_dma_kernel<Cfg, 128>), grid, dim3(Cfg::NT), 0, stream, a);
+    return hipGetLastError();
 }
 
 bool holds(const E4m3Problem &q, int bm, int bn, int threads)
@@ -227,6 +540,9 @@ bool e4m3_fits(const E4m3Problem &q)
 
 hipError_t launch_e4m3(const E4m3Problem &q, hipStream_t stream)
 {
+    if (dma_ok(q)) {
+        return launch_dma<E4m3Cfg<128, 128, 2, 2, 2>>(q, stream);
+    }
     return launch_any(q, stream);
 }
 

@@ -379,7 +379,7 @@ int quant_e4m3_bf16(int transpose, int block, int M, int K, const uint16_t *X, i
  * Scales are any fp32 values; a product of two scales is formed first, and rounded as fp32 rounds it.
  * C is fp32, M x N.  A layer's output is x W^T with blocks of 128 of W; its input gradient is g W with W turned
  * (quant_e4m3_* with transpose, or the same values and scales transposed), its weight gradient g^T x with both turned and blockB = 1.
- * K <= 2^30.
+ * K <= 2^30; at most 2^23 - 1 tiles of 64 x 64 of C (2^35 elements).
  */
 int gemm_e4m3_f32acc(int blockB, int M, int N, int K, float alpha,
                      const uint8_t *A, int lda, const float *SA, int ldsa,
@@ -390,7 +390,7 @@ int gemm_e4m3_f32acc(int blockB, int M, int N, int K, float alpha,
  * gemm_grouped_e4m3_f32acc -- the same for rows in groups, each group with its own right operand:
  *     C[r,:] <- alpha * A[rows[r],:] * B_g^T + beta * C[r,:]   for offsets[g] <= r < offsets[g+1]
  * rows, offsets, groups, R and M as for gemm_grouped_*_f32acc_ex (a row takes its own row's scales along); B and SB hold
- * groups members, strideB and strideSB apart (0: one shared).  groups <= 65535, K <= 2^30.
+ * groups members, strideB and strideSB apart (0: one shared).  groups <= 65535, K <= 2^30, R / 64 + min(groups, R) row tiles.
  */
 int gemm_grouped_e4m3_f32acc(int blockB, int groups, int R, int N, int K, float alpha,
                              const uint8_t *A, int M, int lda, const float *SA, int ldsa, const int32_t *rows,

@@ -13,6 +13,8 @@
 #include "e4m3_internal.h"
 #include "ragged_dma.h"
 
+#include <cmath>
+
 namespace mi355gemm {
 namespace {
 
@@ -191,17 +193,19 @@ __device__ __forceinline__ void dma4_at(const void *p, unsigned lds_addr)
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) float lds_float;
 
-template <int BM_, int BN_, int STAGES_, int WM_, int WN_>
+// A BM x BN tile of KG groups of WM x WN waves; the groups take the slices of k in turn, each
+// through a ring of STAGES slots.
+template <int BM_, int BN_, int STAGES_, int WM_, int WN_, int KG_ = 1>
 struct E4m3Cfg {
-    static constexpr int BM = BM_, BN = BN_, BK = 128, STAGES = STAGES_, WM = WM_, WN = WN_;
-    static constexpr int NW = WM * WN, NT = 64 * NW;
+    static constexpr int BM = BM_, BN = BN_, BK = 128, STAGES = STAGES_, WM = WM_, WN = WN_, KG = KG_;
+    static constexpr int NW = WM * WN, NT = 64 * NW * KG;   // (waves of a group)
     static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
     static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK;                            // a slice
     static constexpr int A_LOADS = A_BYTES / 1024 / NW, B_LOADS = B_BYTES / 1024 / NW;    // per wave
     static constexpr int S_LOADS = ((BM + BN) / 64 + NW - 1) / NW;                        // of 64 scales
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 256 * NW * S_LOADS;
     static constexpr int LOADS = A_LOADS + B_LOADS + S_LOADS;
-    static constexpr int LDS = STAGES * STAGE_BYTES;
+    static constexpr int RING = STAGES * STAGE_BYTES, LDS = KG * RING;
     static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0 && BM % 64 == 0 && BN % 64 == 0,
                   "slices split evenly over the waves");
     static_assert(LDS <= 160 * 1024 && LOADS * STAGES < 64 && TN <= 128, "LDS, outstanding loads");
@@ -219,9 +223,10 @@ __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
     constexpr int BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK, S = Cfg::STAGES, FM = Cfg::FM, FN = Cfg::FN;
     constexpr int A_LOADS = Cfg::A_LOADS, B_LOADS = Cfg::B_LOADS, S_LOADS = Cfg::S_LOADS, LOADS = Cfg::LOADS;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[Cfg::LDS];
-    const unsigned lds0 = (unsigned)(uintptr_t)lds;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    const int uwave = __builtin_amdgcn_readfirstlane(wave);
+    constexpr int KG = Cfg::KG;
+    const int tid = threadIdx.x, lane = tid & 63, wave = (tid >> 6) % Cfg::NW;   // (of its group)
+    const int uwave = __builtin_amdgcn_readfirstlane(wave), kg = __builtin_amdgcn_readfirstlane((tid >> 6) / Cfg::NW);
+    const unsigned lds0 = (unsigned)(uintptr_t)lds + kg * Cfg::RING;
     int group = 0, m0, m_end, one, tm, tn;
     if (p.offsets) {
         const int total = count_row_tiles(p.offsets, p.groups, p.R, BM, p.tiles_m);
@@ -274,8 +279,10 @@ __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
             scale_step[i] = p.ldsb;
         }
     }
-    const int slices = (K + BK - 1) / BK, nk = slices < S ? S : slices;   // (slices past the last are zeros)
-    auto issue = [&](int t, int slot) __attribute__((always_inline)) {
+    // this group's slices are kg, kg + KG, ..: nk steps, in which slices past the last are zeros
+    const int slices = (K + BK - 1) / BK, steps = (slices + KG - 1) / KG, nk = steps < S ? S : steps;
+    auto issue = [&](int step, int slot) __attribute__((always_inline)) {
+        const int t = step * KG + kg;
         const unsigned at = __builtin_amdgcn_readfirstlane(lds0 + slot * Cfg::STAGE_BYTES);
         const unsigned la = at + uwave * A_LOADS * 1024, lb = at + Cfg::A_BYTES + uwave * B_LOADS * 1024;
         const unsigned ls = at + Cfg::A_BYTES + Cfg::B_BYTES + uwave * S_LOADS * 256;
@@ -411,10 +418,44 @@ __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
         slice(nk - 1, after(S - 1), std::integral_constant<int, 0>{}, std::false_type{}, std::false_type{});
     }
 
+    if constexpr (KG > 1) {
+        // the groups' results, added in their order by the first
+        lds_barrier();
+        static_assert((KG - 1) * BM * BN * 4 <= Cfg::LDS, "the groups' results fit the rings");
+        auto at = [&](int g, int i, int j, int c) {
+            return (unsigned)(uintptr_t)lds + ((((g - 1) * Cfg::NW + wave) * FM + i) * FN + j) * 4096 + c * 1024 + lane * 16;
+        };
+        if (kg > 0)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        *(lds_f32x4 *)(uintptr_t)at(kg, i, j, c) =
+                            f32x4_t{acc[i][j][4 * c], acc[i][j][4 * c + 1], acc[i][j][4 * c + 2], acc[i][j][4 * c + 3]};
+        __builtin_amdgcn_s_waitcnt(0xC07F);
+        lds_barrier();
+        if (kg > 0) return;
+#pragma unroll
+        for (int g = 1; g < KG; ++g)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const f32x4_t v = *(const lds_f32x4 *)(uintptr_t)at(g, i, j, c);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][j][4 * c + e] += v[e];
+                    }
+        __builtin_amdgcn_s_waitcnt(0xC07F);
+    }
+
     // Epilogue by rows through the ring: 32 rows of the wave's tile at a time, 16-byte chunk c of row r at
     // chunk c ^ (r % LPR).
     constexpr int LPR = Cfg::TN / 4, RPI = 64 / LPR, NQ = 32 / RPI;
-    static_assert(Cfg::NW * 32 * Cfg::TN * 4 <= Cfg::LDS, "staging area exceeds the ring");
+    static_assert(Cfg::NW * 32 * Cfg::TN * 4 <= Cfg::RING, "staging area exceeds the ring");
     const unsigned stage = lds0 + wave * 32 * Cfg::TN * 4;
     lds_barrier();
     const int er = lane / LPR, ec = lane % LPR;
@@ -470,6 +511,197 @@ __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
     }
 }
 
+template <int RB_, int CB_, int NW_, int S_>
+struct E4m3StreamCfg {
+    static constexpr int RB = RB_, CB = CB_, NW = NW_, S = S_;   // blocks of 16 rows and columns, waves, slots
+    static constexpr int BM = 16 * RB, BN = 16 * CB, BK = 128, NT = 64 * NW;
+    static constexpr int A_LOADS = 2 * RB, B_LOADS = 2 * CB, S_LOADS = (BM + BN + 63) / 64;
+    static constexpr int LOADS = A_LOADS + B_LOADS + S_LOADS;
+    static constexpr int STAGE = (A_LOADS + B_LOADS) * 1024 + S_LOADS * 256;
+    static constexpr int LDS = NW * S * STAGE;
+    static_assert(NW * BM * BN * 4 <= LDS, "the waves' sums fit the rings");
+    static_assert(LDS <= 160 * 1024 && LOADS * S < 64 && S >= 2 && S <= 4 && BN <= 128, "LDS, outstanding loads");
+};
+
+// ---------------------------------------------------------------------------
+// Few rows: the time is that of reading B once.  A workgroup takes 16 CB columns and up to
+// 16 RB rows; its waves take the slices of 128 k in turn, each through a ring of S
+// slots that only it loads and reads: no barrier until the end, S slices on their way per
+// wave.  The waves' results are added in wave order.  Needs what e4m3_dma_kernel needs.
+template <class Cfg, int BLOCKB>
+__global__ __launch_bounds__(Cfg::NT) void e4m3_stream_kernel(E4m3Args p)
+{
+    constexpr int RB = Cfg::RB, CB = Cfg::CB, S = Cfg::S, NW = Cfg::NW, BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK;
+    constexpr int A_LOADS = Cfg::A_LOADS, B_LOADS = Cfg::B_LOADS, S_LOADS = Cfg::S_LOADS, LOADS = Cfg::LOADS;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[Cfg::LDS];
+    const unsigned lds0 = (unsigned)(uintptr_t)lds;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int uwave = __builtin_amdgcn_readfirstlane(wave);
+    int group = 0, m0, m_end, one, tm, tn;
+    if (p.offsets) {
+        const int total = count_row_tiles(p.offsets, p.groups, p.R, BM, p.tiles_m);
+        if ((long long)blockIdx.x >= (long long)total * p.tiles_n) return;
+        tile_coords((int)blockIdx.x, 0, 1, total, p.tiles_n, &one, &tm, &tn);
+        const RowTile rt = find_row_tile(p.offsets, p.groups, p.R, BM, tm);
+        if (rt.group < 0) return;
+        group = rt.group;
+        m0 = rt.first;
+        m_end = rt.end;
+    } else {
+        tile_coords((int)blockIdx.x, 0, 1, p.tiles_m, p.tiles_n, &one, &tm, &tn);
+        m0 = tm * BM;
+        m_end = p.R;
+    }
+    const int n0 = tn * BN, N = p.N, K = p.K;
+    const int limA = m_end - m0 < BM ? m_end - m0 : BM, limB = N - n0 < BN ? N - n0 : BN;
+    auto row_of = [&](int r) {
+        int at = m0 + (r < limA ? r : limA - 1);
+        if (p.rows) at = p.rows[at];
+        return (unsigned)at < (unsigned)p.a_rows ? at : 0;   // (its products are dropped at the end)
+    };
+    unsigned offA[A_LOADS], offB[B_LOADS];
+    const char *Ab = reinterpret_cast<const char *>(p.A) + (p.rows ? 0 : (long long)m0 * p.lda);
+    const char *Bb = reinterpret_cast<const char *>(p.B) + (long long)group * p.strideB + (long long)n0 * p.ldb;
+    auto swizzled = [&](int load) { return 16 * ((lane % 8) ^ swz_a<8>(8 * load + lane / 8)); };   // byte of the lane's chunk
+#pragma unroll
+    for (int i = 0; i < B_LOADS; ++i) {
+        const int r = 8 * i + lane / 8;
+        offB[i] = (unsigned)((r < limB ? r : limB - 1) * p.ldb) + swizzled(i);
+    }
+#pragma unroll
+    for (int i = 0; i < A_LOADS; ++i) offA[i] = (unsigned)((row_of(8 * i + lane / 8) - (p.rows ? 0 : m0)) * p.lda) + swizzled(i);
+    // scales: the rows', then the columns'
+    const float *scale[S_LOADS];
+    long long scale_step[S_LOADS];
+#pragma unroll
+    for (int i = 0; i < S_LOADS; ++i) {
+        const int r = 64 * i + lane, c = r - BM;
+        scale[i] = r < BM ? p.SA + row_of(r) : p.SB + (long long)group * p.strideSB + (n0 + (c < limB ? c : limB - 1)) / BLOCKB;
+        scale_step[i] = r < BM ? p.ldsa : p.ldsb;
+    }
+    const int slices = (K + BK - 1) / BK;
+    const unsigned ring = lds0 + uwave * S * Cfg::STAGE;
+    auto issue = [&](int t, int slot) __attribute__((always_inline)) {
+        const unsigned lb = __builtin_amdgcn_readfirstlane(ring + slot * Cfg::STAGE), la = lb + B_LOADS * 1024, ls = la + A_LOADS * 1024;
+        const char *a = uniform(Ab + (long long)t * BK), *b = uniform(Bb + (long long)t * BK);
+        if ((t + 1) * BK <= K) {
+#pragma unroll
+            for (int i = 0; i < B_LOADS; ++i) dma16(b, offB[i], lb + 1024 * i);
+#pragma unroll
+            for (int i = 0; i < A_LOADS; ++i) dma16(a, offA[i], la + 1024 * i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < B_LOADS; ++i)
+                dma16_at(t * BK + swizzled(i) < K ? (const void *)(b + offB[i]) : (const void *)zero_chunk, lb + 1024 * i);
+#pragma unroll
+            for (int i = 0; i < A_LOADS; ++i)
+                dma16_at(t * BK + swizzled(i) < K ? (const void *)(a + offA[i]) : (const void *)zero_chunk, la + 1024 * i);
+        }
+#pragma unroll
+        for (int i = 0; i < S_LOADS; ++i) dma4_at(scale[i] + t * scale_step[i], ls + 256 * i);
+    };
+    const int lr = lane & 15, q = lane >> 4;
+    f32x4_t acc[RB][CB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < CB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    auto compute = [&](int slot, bool refill, int t) __attribute__((always_inline)) {
+        const unsigned lb = ring + slot * Cfg::STAGE, la = lb + B_LOADS * 1024, ls = la + A_LOADS * 1024;
+        u32x4 ra[RB][2], rb[CB][2];
+        float sa[RB];
+        f32x4_t sb[CB];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const unsigned at = lr * BK + 16 * ((4 * s + q) ^ swz_a<8>(lr));   // (rows 16 apart: swizzles 2 apart)
+#pragma unroll
+            for (int j = 0; j < CB; ++j) rb[j][s] = *(const lds_u32x4 *)(uintptr_t)(lb + j * 16 * BK + (at ^ (32 * (j & 1))));
+#pragma unroll
+            for (int i = 0; i < RB; ++i) ra[i][s] = *(const lds_u32x4 *)(uintptr_t)(la + i * 16 * BK + (at ^ (32 * (i & 1))));
+        }
+#pragma unroll
+        for (int i = 0; i < RB; ++i) sa[i] = *(const lds_float *)(uintptr_t)(ls + 4 * (16 * i + lr));
+#pragma unroll
+        for (int j = 0; j < CB; ++j) {
+            if constexpr (BLOCKB == 1) {
+                sb[j] = *(const lds_f32x4 *)(uintptr_t)(ls + 4 * (BM + 16 * j + 4 * q));
+            } else {
+                const float v = *(const lds_float *)(uintptr_t)(ls + 4 * BM);   // (the columns lie in one block)
+                sb[j] = f32x4_t{v, v, v, v};
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slot is read: it may be loaded again
+        if (refill) issue(t, slot);
+        Half16 fa[RB][2];
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) fa[i][s] = to_f16(ra[i][s]);
+#pragma unroll
+        for (int j = 0; j < CB; ++j) {
+            const Half16 b0 = to_f16(rb[j][0]), b1 = to_f16(rb[j][1]);
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+                sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(b0.lo, fa[i][0].lo, sum, 0, 0, 0);
+                sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(b0.hi, fa[i][0].hi, sum, 0, 0, 0);
+                sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(b1.lo, fa[i][1].lo, sum, 0, 0, 0);
+                sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(b1.hi, fa[i][1].hi, sum, 0, 0, 0);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(sa[i] * sb[j][r], sum[r], acc[i][j][r]);
+            }
+        }
+    };
+    const int ns = slices > uwave ? (slices - uwave + NW - 1) / NW : 0;   // this wave's slices: uwave, uwave + NW, ...
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+        if (i < ns) issue(uwave + i * NW, i);
+    int i = 0, slot = 0;
+    for (; i + S < ns; ++i) {
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS * (S - 1)) : "memory");
+        compute(slot, true, uwave + (i + S) * NW);
+        slot = slot + 1 == S ? 0 : slot + 1;
+    }
+    for (; i < ns; ++i) {   // the last slices: everything has been issued
+        const int left = ns - 1 - i;
+        if (S > 3 && left >= 3)
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S > 3 ? LOADS * 3 : 0) : "memory");
+        else if (S > 2 && left >= 2)
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S > 2 ? LOADS * 2 : 0) : "memory");
+        else if (left == 1)
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        compute(slot, false, 0);
+        slot = slot + 1 == S ? 0 : slot + 1;
+    }
+
+    // the waves' results, 16-byte chunk c of row r at chunk c ^ (r % CH), added in wave order
+    constexpr int CH = BN / 4;
+    __syncthreads();   // every wave has left its ring
+#pragma unroll
+    for (int i2 = 0; i2 < RB; ++i2)
+#pragma unroll
+        for (int j = 0; j < CB; ++j) {
+            const int r = 16 * i2 + lr, c = 4 * j + q;
+            *(lds_f32x4 *)(uintptr_t)(lds0 + wave * BM * BN * 4 + r * BN * 4 + ((c ^ (r & (CH - 1))) * 16)) = acc[i2][j];
+        }
+    __syncthreads();
+    for (int e = tid; e < limA * CH; e += Cfg::NT) {
+        const int r = e / CH, c = e % CH, row = m0 + r;
+        f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+            v += *(const lds_f32x4 *)(uintptr_t)(lds0 + w * BM * BN * 4 + r * BN * 4 + ((c ^ (r & (CH - 1))) * 16));
+        const int at = p.rows ? p.rows[row] : row;
+        if ((unsigned)at >= (unsigned)p.a_rows) v = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        if (p.beta != 0.f)
+            store_row4<true, true>(p.C, p.ldc, row, n0 + 4 * c, v, p.alpha, p.beta, m_end, N);
+        else
+            store_row4<true, false>(p.C, p.ldc, row, n0 + 4 * c, v, p.alpha, p.beta, m_end, N);
+    }
+}
+
 E4m3Args arguments(const E4m3Problem &q)
 {
     E4m3Args a = {};
@@ -513,6 +745,20 @@ hipError_t launch_dma(const E4m3Problem &q, hipStream_t stream)
     return hipGetLastError();
 }
 
+template <class Cfg>
+hipError_t launch_stream(const E4m3Problem &q, hipStream_t stream)
+{
+    E4m3Args a = arguments(q);
+    a.tiles_m = (int)row_tiles(q, Cfg::BM);
+    a.tiles_n = (q.N + Cfg::BN - 1) / Cfg::BN;
+    const dim3 grid((unsigned)((long long)a.tiles_m * a.tiles_n));
+    if (q.blockB == 1)
+        hipLaunchKernelGGL((e4m3_stream_kernel<Cfg, 1>), grid, dim3(Cfg::NT), 0, stream, a);
+    else
+        hipLaunchKernelGGL((e4m3_stream_kernel<Cfg, 128>), grid, dim3(Cfg::NT), 0, stream, a);
+    return hipGetLastError();
+}
+
 bool holds(const E4m3Problem &q, int bm, int bn, int threads)
 {
     return grid_holds(row_tiles(q, bm) * ((q.N + (long long)bn - 1) / bn), threads);
@@ -531,6 +777,43 @@ hipError_t launch_any(const E4m3Problem &q, hipStream_t stream)
     return hipGetLastError();
 }
 
+// The time of a tile's 128 k, of its start and end (us, one CU), and how many workgroups a CU holds: measured on
+// square and flat plain products and on 8 to 64 groups of 10 to 500 rows each.
+struct TileTime {
+    double slice, fixed;
+};
+using Tile128 = E4m3Cfg<128, 128, 2, 2, 2>;
+using Tile64x128 = E4m3Cfg<64, 128, 2, 1, 4, 2>;
+using Tile64 = E4m3Cfg<64, 64, 2, 2, 2, 2>;
+using Stream32 = E4m3StreamCfg<2, 2, 4, 2>;
+using Stream16 = E4m3StreamCfg<1, 2, 4, 2>;
+constexpr TileTime kTime128 = {1.15, 2}, kTime64x128 = {0.63, 4}, kTime64 = {0.42, 1}, kTime32 = {0.22, 1};
+
+hipError_t launch_tiles(const E4m3Problem &q, hipStream_t stream)
+{
+    const double rows = (double)q.R / q.groups, slices = (q.K + 127) / 128;
+    // Up to 16 rows a group: streamed (64 groups, 128 rows, 1024 x 2048: 25.8 us, against 34 with 128x128 tiles; 512
+    // rows 31.9 against 34.3 with the best tile; a plain 16 x 4096 x 4096 5.8 against 17).
+    if (rows <= 16 && holds(q, Stream16::BM, Stream16::BN, Stream16::NT)) return launch_stream<Stream16>(q, stream);
+    // Otherwise the tile whose rounds of 256 workgroups take the least time.  Groups part-fill half of their tiles,
+    // and how many exist the host does not know: there the rounds are not whole numbers.
+    auto time = [&](int bm, int bn, int threads, int per_round, TileTime t) {
+        if (!holds(q, bm, bn, threads)) return 1e300;
+        const double down = q.offsets ? (double)q.R / bm + 0.5 * (q.groups < q.R ? q.groups : q.R) : (q.R + bm - 1) / bm;
+        const double rounds = down * ((q.N + bn - 1) / bn) / per_round;
+        return (rounds <= 1 ? 1. : q.offsets ? rounds : std::ceil(rounds)) * (slices * t.slice + t.fixed);
+    };
+    const double c128 = time(128, 128, Tile128::NT, 256, kTime128), c64x128 = time(64, 128, Tile64x128::NT, 256, kTime64x128);
+    const double c64 = time(64, 64, Tile64::NT, 256, kTime64);
+    // (streaming 32 rows reads B once for each 32: for plain products, whose B then comes from the caches: 64 x 4096 x 4096
+    // 7.4 us against 13, 512 x 512 x 4096 7.2 against 14; 64 groups of 47 rows 64 against 38)
+    const double c32 = q.offsets ? 1e300 : time(32, 32, Stream32::NT, 512, kTime32);
+    if (c32 < c64 && c32 < c64x128 && c32 < c128) return launch_stream<Stream32>(q, stream);
+    if (c64 <= c64x128 && c64 <= c128) return launch_dma<Tile64>(q, stream);
+    if (c64x128 < c128) return launch_dma<Tile64x128>(q, stream);
+    return launch_dma<Tile128>(q, stream);
+}
+
 }  // namespace
 
 bool e4m3_fits(const E4m3Problem &q)
@@ -540,10 +823,7 @@ bool e4m3_fits(const E4m3Problem &q)
 
 hipError_t launch_e4m3(const E4m3Problem &q, hipStream_t stream)
 {
-    if (dma_ok(q)) {
-        return launch_dma<E4m3Cfg<128, 128, 2, 2, 2>>(q, stream);
-    }
-    return launch_any(q, stream);
+    return dma_ok(q) ? launch_tiles(q, stream) : launch_any(q, stream);
 }
 
 }  // namespace mi355gemm

@@ -19,9 +19,11 @@
 #include "orthogonalise_internal.h"
 #include "routed_internal.h"
 #include "stage16.h"
+#include "tile_order.h"
 #include "wave.h"
 
 #include <cmath>
+#include <type_traits>
 
 namespace mi355gemm {
 namespace {
@@ -87,6 +89,21 @@ __device__ __forceinline__ T *of_member(T *p, long long stride_bytes, int z)
     return reinterpret_cast<T *>(reinterpret_cast<uintptr_t>(p) + (uintptr_t)(z * stride_bytes));
 }
 
+__device__ __forceinline__ uint16_t bf16_bits(float v)
+{
+    return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
+// A pointer that is the same in every lane, in scalar registers (dma16's base).
+__device__ __forceinline__ const char *uniform(const char *p)
+{
+    const uint64_t b = reinterpret_cast<uint64_t>(p);
+    const uint64_t lo = (unsigned)__builtin_amdgcn_readfirstlane((int)b);
+    const uint64_t hi = (unsigned)__builtin_amdgcn_readfirstlane((int)(b >> 32));
+    return reinterpret_cast<const char *>(lo | (hi << 32));
+}
+typedef __attribute__((address_space(3))) float lds_float;
+
 template <bool BF>
 __device__ __forceinline__ float g_at(const OrthoArgs &p, int z, long long r, long long c)
 {
@@ -146,115 +163,290 @@ __global__ __launch_bounds__(256) void start_kernel(OrthoArgs p)
 
 enum Product { kGram, kSquare, kApply };
 
+// The tile a workgroup takes, XCD by XCD (see tile_order.h).  The symmetric products compute the tiles on and above
+// the diagonal alone, row by row; a workgroup also stores its tile's mirror image.
+template <Product KIND>
+__device__ __forceinline__ void tile_of(int rows, int cols, int *member, int *tm, int *tn)
+{
+    if constexpr (KIND == kApply) {
+        tile_coords(blockIdx.x, blockIdx.z, gridDim.z, rows, cols, member, tm, tn);
+    } else {
+        const int each = rows * (rows + 1) / 2;
+        const long long total = (long long)each * gridDim.z, lin = (long long)blockIdx.z * each + blockIdx.x;
+        const long long xcd = lin % kNumXcd, per = total / kNumXcd, extra = total % kNumXcd;
+        const long long logical = xcd * per + (xcd < extra ? xcd : extra) + lin / kNumXcd;
+        *member = (int)(logical / each);
+        int left = (int)(logical - (long long)*member * each), r = 0;
+        // row r holds rows - r tiles (at most 1024 rows)
+        while (left >= rows - r) {
+            left -= rows - r;
+            ++r;
+        }
+        *tm = r;
+        *tn = r + left;
+    }
+}
+
 // The three products of a step, each P Q^T of fp16 rows with k contiguous and whole slices of 64:
 //   kGram    A = X X^T            P = Q = X
 //   kSquare  B = b A + c A A      P = Q = A - diag(A)
 //   kApply   X <- a X + B X       P = B - diag(B), Q = X^T
-// 64 x 64 tiles of four waves of 32 x 32.
-template <Product KIND>
-__global__ __launch_bounds__(256) void product_kernel(OrthoArgs p)
+// The ring, its loads and its K loop are those of the whole-matrix kernel (hgemm_mfma.hip).  The epilogue passes 32 rows of
+// a wave's tile at a time through LDS: by rows for what belongs to them, by columns for the transposed copies.
+template <class Cfg, Product KIND>
+__global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
 {
-    __shared__ __attribute__((aligned(16))) u32x4 lds[2][128 * 8];
-    const int z = blockIdx.z, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
+    constexpr int BM = Cfg::BM, BN = Cfg::BN, BK = 64, S = Cfg::STAGES, FM = Cfg::FM, FN = Cfg::FN;
+    static_assert(KIND == kApply || BM == BN, "tiles of symmetric products are square");
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[S * Cfg::STAGE_BYTES];
+    const unsigned lds0 = (unsigned)(uintptr_t)lds;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int uwave = __builtin_amdgcn_readfirstlane(wave);
+    const int cols = KIND == kApply ? p.n : p.m, K = KIND == kGram ? p.n : p.m;
+    int z, tm, tn;
+    tile_of<KIND>((p.m + BM - 1) / BM, (cols + BN - 1) / BN, &z, &tm, &tn);
+    const int m0 = tm * BM, n0 = tn * BN;
     const _Float16 *P = of_member(KIND == kGram ? p.x16 : KIND == kSquare ? p.a16 : p.b16, p.ws_stride, z);
     const _Float16 *Q = of_member(KIND == kGram ? p.x16 : KIND == kSquare ? p.a16 : p.xt_in, p.ws_stride, z);
-    const int K = KIND == kGram ? p.n : p.m;
-    const long long ld = K;
-    const _Float16 *row[4];
-    const int ch = tid & 7;
+
+    constexpr int A_LOADS = Cfg::A_LOADS, B_LOADS = Cfg::B_LOADS, LOADS = A_LOADS + B_LOADS;
+    const bool loader = uwave >= Cfg::NW - Cfg::LW;
+    const int lw = loader ? uwave - (Cfg::NW - Cfg::LW) : 0;
+    unsigned offA[A_LOADS], offB[B_LOADS];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = (tid >> 3) + 32 * (i & 1);
-        row[i] = (i < 2 ? P + (m0 + r) * ld : Q + (n0 + r) * ld) + 8 * ch;
-    }
-    u32x4 v[4];
-    auto load = [&](int k0) {
+    for (int i = 0; i < A_LOADS; ++i) offA[i] = dma_offset<true, BM, BK, true>(lw * A_LOADS + i, lane, K, p.m - m0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const u32x4 *>(row[i] + k0);
+    for (int i = 0; i < B_LOADS; ++i) offB[i] = dma_offset<true, BN, BK, true>(lw * B_LOADS + i, lane, K, cols - n0);
+    const char *Pb = reinterpret_cast<const char *>(P + (long long)m0 * K), *Qb = reinterpret_cast<const char *>(Q + (long long)n0 * K);
+    const int nk = K / BK;
+    auto issue = [&](int t, int slot) __attribute__((always_inline)) {
+        if (!loader) return;
+        const unsigned la = __builtin_amdgcn_readfirstlane(lds0 + slot * Cfg::A_BYTES + lw * A_LOADS * 1024);
+        const unsigned lb = __builtin_amdgcn_readfirstlane(lds0 + S * Cfg::A_BYTES + slot * Cfg::B_BYTES + lw * B_LOADS * 1024);
+        // (a K of fewer slices than the ring has slots re-reads the last, which is not multiplied)
+        const int at = t < nk ? t : nk - 1;
+        const char *a = uniform(Pb + (long long)at * BK * 2), *b = uniform(Qb + (long long)at * BK * 2);
+#pragma unroll
+        for (int i = 0; i < A_LOADS; ++i) dma16(a, offA[i], la + 1024 * i);
+#pragma unroll
+        for (int i = 0; i < B_LOADS; ++i) dma16(b, offB[i], lb + 1024 * i);
     };
-    const int lr = lane & 31, lk = lane >> 5, wm = wave >> 1, wn = wave & 1;
-    f32x16 acc = {};
-    load(0);
-    for (int t = 0; t < K / 64; ++t) {
-        const int buf = t & 1;
+    const int wm = wave / Cfg::WN, wn = wave % Cfg::WN, lr = lane & 31, lk = lane >> 5;
+    constexpr int NS = BK / 16;
+    unsigned fragA[NS], fragB[NS];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = (tid >> 3) + 32 * i;
-            lds[buf][r * 8 + (ch ^ swz_a<8>(r))] = v[i];
+    for (int s = 0; s < NS; ++s) {
+        fragA[s] = lds0 + frag_offset<true, BM, BK>(wm * Cfg::TM, lane, s);
+        fragB[s] = lds0 + S * Cfg::A_BYTES + frag_offset<true, BN, BK>(wn * Cfg::TN, lane, s);
+    }
+    f32x16 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
+    half8 fa[2][FM], fb[2][FN];
+    auto read = [&](int slot, int s, half8 *a, half8 *b) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) a[i] = *(const lds_half8 *)(uintptr_t)(fragA[s] + slot * Cfg::A_BYTES + i * 32 * BK * 2);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) b[j] = *(const lds_half8 *)(uintptr_t)(fragB[s] + slot * Cfg::B_BYTES + j * 32 * BK * 2);
+    };
+    auto mfmas = [&](const half8 *a, const half8 *b) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = mfma16<false>(b[j], a[i], acc[i][j]);
+#pragma unroll
+        for (int i = 0; i < FM * FN; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
         }
-        if (t + 1 < K / 64) load((t + 1) * 64);
-        __syncthreads();
-        const u32x4 *la = lds[buf] + (32 * wm + lr) * 8, *lb = lds[buf] + (64 + 32 * wn + lr) * 8;
+    };
+    auto lds_barrier = [&]() {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    };
+    const bool late = Cfg::STAGGER && uwave >= Cfg::NW / 2;
+    auto step = [&](int t, auto pending, auto refill, bool late_refill) __attribute__((always_inline)) {
+        const int slot = t % S, next = (t + 1) % S, prev = (t - 1 + S) % S;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int c = (2 * s + lk) ^ swz_a<8>(lr);
-            acc = mfma16<false>(__builtin_bit_cast(half8, lb[c]), __builtin_bit_cast(half8, la[c]), acc);
+        for (int sub = 0; sub < NS; ++sub) {
+            const int cur = sub & 1, nxt = cur ^ 1;
+            if (sub + 1 < NS) {
+                read(slot, sub + 1, fa[nxt], fb[nxt]);
+                if (Cfg::STAGGER && sub == NS - 2 && late && late_refill) issue(t - 1 + S, prev);
+            } else {
+                wait_vmcnt<LOADS * decltype(pending)::value>();
+                __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's slice-t reads are done
+                lds_barrier();
+                if (decltype(refill)::value && !late) issue(t + S, slot);
+                read(next, 0, fa[nxt], fb[nxt]);
+            }
+            mfmas(fa[cur], fb[cur]);
+        }
+    };
+#pragma unroll
+    for (int st = 0; st < S; ++st) issue(st, st);
+    wait_vmcnt<LOADS * (S - 1)>();
+    lds_barrier();
+    read(0, 0, fa[0], fb[0]);
+    {
+        // the last S - 1 of at least S steps find nothing left to load; a shorter K stops early
+        int t = 0;
+        for (; t + S < nk; ++t) step(t, std::integral_constant<int, S - 2>{}, std::true_type{}, t >= 1);
+        const int t0 = t;
+        auto tail = [&](int u, auto pending) __attribute__((always_inline)) {
+            if (u + 1 < nk) step(u, pending, std::false_type{}, u == t0 && u >= 1);
+        };
+        tail(t0, std::integral_constant<int, S - 2>{});
+        if constexpr (S >= 3) tail(t0 + 1, std::integral_constant<int, S - 3>{});
+        if constexpr (S >= 4) tail(t0 + 2, std::integral_constant<int, S - 4>{});
+        const int slot = (nk - 1) % S;
+#pragma unroll
+        for (int sub = 0; sub < NS; ++sub) {
+            const int cur = sub & 1, nxt = cur ^ 1;
+            if (sub + 1 < NS) read(slot, sub + 1, fa[nxt], fb[nxt]);
+            mfmas(fa[cur], fb[cur]);
         }
     }
-    const int r = m0 + 32 * wm + lr;
-    float *da = of_member(p.da, p.ws_stride, z), *db = of_member(p.db, p.ws_stride, z);
+
+    constexpr int TN = Cfg::TN, LPR = TN / 4, RPI = 64 / LPR, NQ = 32 / RPI;
+    static_assert(Cfg::NW * 32 * TN * 4 <= S * Cfg::STAGE_BYTES, "staging area exceeds the ring");
+    const unsigned stage = lds0 + wave * 32 * TN * 4;
+    wait_vmcnt<0>();   // (slices that a short K did not use)
+    lds_barrier();
+    float *x = of_member(p.x, p.ws_stride, z), *da = of_member(p.da, p.ws_stride, z), *db = of_member(p.db, p.ws_stride, z);
     _Float16 *a16 = of_member(p.a16, p.ws_stride, z), *b16 = of_member(p.b16, p.ws_stride, z);
+    _Float16 *x16 = of_member(p.x16, p.ws_stride, z), *xt = of_member(p.xt_out, p.ws_stride, z);
+    uint16_t *O = p.O + z * p.strideO;
+    const int er = lane / LPR, c = n0 + wn * TN + 4 * (lane % LPR);
+    const bool mirrored = KIND != kApply && tm != tn;
+    // chunk of the staged row: 16 bytes of columns 4 k.. at chunk k ^ (row % LPR)
+    auto chunk = [&](int r, int k) { return stage + r * TN * 4 + 16 * (k ^ (r & (LPR - 1))); };
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const int c = n0 + 32 * wn + 8 * g + 4 * lk;
-        const f32x4_t s = {acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
-        if constexpr (KIND == kGram) {
-            const float back = 1.f / (p.x_scale * p.x_scale);
+    for (int i = 0; i < FM; ++i) {
+        const int first = m0 + wm * Cfg::TM + 32 * i;
+        if (first >= p.m || n0 + wn * TN >= cols) break;   // (uniform; padded sizes are multiples of 64)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *(lds_f32x4 *)(uintptr_t)chunk(lr, 8 * j + 2 * g + lk) =
+                    f32x4_t{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            const int lrow = q * RPI + er, r = first + lrow;
+            const unsigned at = chunk(lrow, lane % LPR);
+            f32x4_t v = *(const lds_f32x4 *)(uintptr_t)at;
             half4 h;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float v = s[e] * back;
-                if (r == c + e) da[r] = v;
-                h[e] = r == c + e ? (_Float16)0.f : (_Float16)(v * kOffScale);
-            }
-            *reinterpret_cast<half4 *>(a16 + (long long)r * p.m + c) = h;
-        } else if constexpr (KIND == kSquare) {
-            const half4 o = *reinterpret_cast<const half4 *>(a16 + (long long)r * p.m + c);
-            half4 h;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float off = (float)o[e] * (1.f / kOffScale), sq = s[e] * (1.f / (kOffScale * kOffScale));
-                if (r == c + e) db[r] = p.b * da[r] + p.c * (da[r] * da[r] + sq);
-                const float v = p.b * off + p.c * ((da[r] + da[c + e]) * off + sq);
-                h[e] = r == c + e ? (_Float16)0.f : (_Float16)(v * p.b_scale);
-            }
-            *reinterpret_cast<half4 *>(b16 + (long long)r * p.m + c) = h;
-        } else {
-            float *x = of_member(p.x, p.ws_stride, z) + (long long)r * p.n + c;
-            const f32x4_t old = *reinterpret_cast<const f32x4_t *>(x);
-            const float f = p.a + db[r], back = 1.f / p.b_scale;
-            f32x4_t v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, old[e], back * s[e]);
-            if (p.last) {
-                const float out = p.alpha / p.x_scale;
+            if constexpr (KIND == kGram) {
+                const float back = 1.f / (p.x_scale * p.x_scale);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int row_o = p.tall ? c + e : r, col_o = p.tall ? r : c + e;
-                    if (row_o < p.M && col_o < p.N)
-                        p.O[z * p.strideO + (long long)row_o * p.ldo + col_o] = __builtin_bit_cast(uint16_t, (__bf16)(v[e] * out));
+                    v[e] *= back;
+                    if (r == c + e) {
+                        da[r] = v[e];
+                        v[e] = 0.f;
+                    }
+                    v[e] *= kOffScale;
+                    h[e] = (_Float16)v[e];
                 }
+                *reinterpret_cast<half4 *>(a16 + (long long)r * p.m + c) = h;
+            } else if constexpr (KIND == kSquare) {
+                const half4 o = *reinterpret_cast<const half4 *>(a16 + (long long)r * p.m + c);
+                const f32x4_t dc = *reinterpret_cast<const f32x4_t *>(da + c);
+                const float dr = da[r];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float off = (float)o[e] * (1.f / kOffScale), sq = v[e] * (1.f / (kOffScale * kOffScale));
+                    if (r == c + e) {
+                        db[r] = p.b * dr + p.c * (dr * dr + sq);
+                        v[e] = 0.f;
+                    } else {
+                        v[e] = (p.b * off + p.c * ((dr + dc[e]) * off + sq)) * p.b_scale;
+                    }
+                    h[e] = (_Float16)v[e];
+                }
+                *reinterpret_cast<half4 *>(b16 + (long long)r * p.m + c) = h;
             } else {
-                *reinterpret_cast<f32x4_t *>(x) = v;
-                half4 h;
+                f32x4_t *px = reinterpret_cast<f32x4_t *>(x + (long long)r * p.n + c);
+                const f32x4_t old = *px;
+                const float f = p.a + db[r], back = 1.f / p.b_scale;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) h[e] = (_Float16)v[e];
-                *reinterpret_cast<half4 *>(of_member(p.x16, p.ws_stride, z) + (long long)r * p.n + c) = h;
-                _Float16 *xt = of_member(p.xt_out, p.ws_stride, z);
+                for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, old[e], back * v[e]);
+                if (!p.last) {
+                    *px = v;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) xt[(long long)(c + e) * p.m + r] = h[e];
+                    for (int e = 0; e < 4; ++e) h[e] = (_Float16)v[e];
+                    *reinterpret_cast<half4 *>(x16 + (long long)r * p.n + c) = h;
+                } else if (!p.tall && r < p.M) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (c + e < p.N) O[(long long)r * p.ldo + c + e] = bf16_bits(v[e] * (p.alpha / p.x_scale));
+                }
+            }
+            if (KIND == kApply || mirrored) *(lds_f32x4 *)(uintptr_t)at = v;
+        }
+        if (KIND != kApply && !mirrored) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            continue;
+        }
+        if (KIND == kApply && p.last && !p.tall) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            continue;
+        }
+        // by columns: lane l has 32 rows of column l (TN = 64), or 16 of column l % 32 (TN = 32)
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        constexpr int HALF = TN == 64 ? 32 : 16;
+        const int cl = lane % TN, r0 = lane / TN * HALF, col = n0 + wn * TN + cl;
+        float t[HALF];
+#pragma unroll
+        for (int e = 0; e < HALF; ++e) t[e] = *(const lds_float *)(uintptr_t)(chunk(r0 + e, cl >> 2) + 4 * (cl & 3));
+        if (KIND == kApply && p.last) {
+            if (col < p.M)
+#pragma unroll
+                for (int e = 0; e < HALF; ++e)
+                    if (first + r0 + e < p.N) O[(long long)col * p.ldo + first + r0 + e] = bf16_bits(t[e] * (p.alpha / p.x_scale));
+        } else {
+            _Float16 *dst = (KIND == kGram ? a16 : KIND == kSquare ? b16 : xt) + (long long)col * p.m + first + r0;
+#pragma unroll
+            for (int e = 0; e < HALF; e += 8) {
+                half8 h;
+#pragma unroll
+                for (int d = 0; d < 8; ++d) h[d] = (_Float16)t[e + d];
+                *reinterpret_cast<half8 *>(dst + e) = h;
             }
         }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
 }
+
+template <class Cfg, Product KIND>
+hipError_t launch_tiles(const OrthoArgs &a, int batch, hipStream_t stream)
+{
+    const int rows = (a.m + Cfg::BM - 1) / Cfg::BM, cols = (a.n + Cfg::BN - 1) / Cfg::BN;
+    const int tiles = KIND == kApply ? rows * cols : rows * (rows + 1) / 2;
+    hipLaunchKernelGGL((product_kernel<Cfg, KIND>), dim3(tiles, 1, batch), dim3(Cfg::NT), 0, stream, a);
+    return hipGetLastError();
+}
+
+using Large = HgDmaCfg<256, 256, 2, 2, 4, 64>;
+using Middle = HgDmaCfg<128, 128, 4, 2, 4, 64>;
+using Small = HgDmaCfg<64, 64, 4, 2, 2, 64>;
 
 template <Product KIND>
 hipError_t launch_product(const OrthoArgs &a, int batch, hipStream_t stream)
 {
-    const int cols = KIND == kApply ? a.n : a.m;
-    hipLaunchKernelGGL(product_kernel<KIND>, dim3(cols / 64, a.m / 64, batch), dim3(256), 0, stream, a);
-    return hipGetLastError();
+    auto time = [&](int side, double each) {
+        const double rows = (a.m + side - 1) / side, cols = (a.n + side - 1) / side;
+        return std::ceil((KIND == kApply ? rows * cols : rows * (rows + 1) / 2) * batch / 256) * each;
+    };
+    const double large = time(256, 1.0), middle = time(128, 0.4), small = time(64, 0.16);
+    if (large <= middle && large <= small) return launch_tiles<Large, KIND>(a, batch, stream);
+    if (middle <= small) return launch_tiles<Middle, KIND>(a, batch, stream);
+    return launch_tiles<Small, KIND>(a, batch, stream);
 }
 
 template <bool BF>

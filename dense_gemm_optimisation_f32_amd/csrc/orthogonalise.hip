@@ -10,7 +10,7 @@
 //     hardly has grows by a factor a in every step (3.4445^5 = 485): rounded to 16 bits in
 //     each step, a G of low rank came out 4e-2 off.
 //   * The products' operands are fp16 copies.  There an error only multiplies X (from the left,
-//     through A), and stays as small as it is.  The copies are scaled by powers of two into fp16's range.
+//     through A), and stays as small as it is.  X's is scaled by a power of two into fp16's range.
 //   * The diagonals of A and of B = b A + c A A, which come to be much larger than the rest, are
 //     kept apart in fp32, and the fp16 copies hold zeros there: with A = D + O,
 //       A A = D D + D O + O D + O O,   B X = diag(B) X + (B - diag(B)) X.
@@ -31,7 +31,6 @@ namespace {
 typedef _Float16 half4 __attribute__((ext_vector_type(4)));
 
 constexpr int kNormBlocks = 64;      // workgroups (and partial sums) of a matrix's norm
-constexpr float kOffScale = 1024.f;  // of A's fp16 copy: entries are at most the largest singular value squared
 
 // One matrix's part of the workspace.  Rows and columns are filled up to multiples of 64 with zeros,
 // which the products keep.
@@ -70,7 +69,6 @@ struct OrthoArgs {
     bool tall, last;
     float a, b, c;                   // this step's coefficients
     float x_scale;                   // x16 and x hold x_scale * X
-    float b_scale;                   // b16 holds b_scale * (B - diag(B))
     float alpha;
     const void *G;
     long long ldg, strideG;
@@ -350,7 +348,6 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
                         da[r] = v[e];
                         v[e] = 0.f;
                     }
-                    v[e] *= kOffScale;
                     h[e] = (_Float16)v[e];
                 }
                 *reinterpret_cast<half4 *>(a16 + (long long)r * p.m + c) = h;
@@ -360,12 +357,12 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
                 const float dr = da[r];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float off = (float)o[e] * (1.f / kOffScale), sq = v[e] * (1.f / (kOffScale * kOffScale));
+                    const float off = o[e];
                     if (r == c + e) {
-                        db[r] = p.b * dr + p.c * (dr * dr + sq);
+                        db[r] = p.b * dr + p.c * (dr * dr + v[e]);
                         v[e] = 0.f;
                     } else {
-                        v[e] = (p.b * off + p.c * ((dr + dc[e]) * off + sq)) * p.b_scale;
+                        v[e] = p.b * off + p.c * ((dr + dc[e]) * off + v[e]);
                     }
                     h[e] = (_Float16)v[e];
                 }
@@ -373,9 +370,9 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
             } else {
                 f32x4_t *px = reinterpret_cast<f32x4_t *>(x + (long long)r * p.n + c);
                 const f32x4_t old = *px;
-                const float f = p.a + db[r], back = 1.f / p.b_scale;
+                const float f = p.a + db[r];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, old[e], back * v[e]);
+                for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, old[e], v[e]);
                 if (!p.last) {
                     *px = v;
 #pragma unroll
@@ -457,8 +454,7 @@ hipError_t launch(const OrthoProblem &q, hipStream_t stream)
     a.M = q.M; a.N = q.N;
     a.m = (int)l.m; a.n = (int)l.n;
     a.tall = q.M > q.N;
-    // X's rows end up with a norm near 1 over n entries: entries near 2^0 after this
-    a.x_scale = std::exp2(std::floor(0.5f * std::log2((float)(q.M > q.N ? q.M : q.N))));
+    a.x_scale = ortho_x_scale(q.M, q.N);
     a.alpha = q.alpha;
     a.G = q.G; a.ldg = q.ldg; a.strideG = q.strideG;
     a.O = q.O; a.ldo = q.ldo; a.strideO = q.strideO;
@@ -481,10 +477,6 @@ hipError_t launch(const OrthoProblem &q, hipStream_t stream)
         a.a = q.coefficients[3 * s];
         a.b = q.coefficients[3 * s + 1];
         a.c = q.coefficients[3 * s + 2];
-        // entries of B for entries of A up to 4, below 2^15
-        const float most = 4.f * std::fabs(a.b) + 16.f * std::fabs(a.c);
-        a.b_scale = most > 0 && most < 32768.f ? std::exp2(std::floor(std::log2(32768.f / most))) : 1.f;
-        if (a.b_scale > 1024.f) a.b_scale = 1024.f;
         a.xt_in = xt[s & 1];
         a.xt_out = xt[(s & 1) ^ 1];
         a.last = s + 1 == q.steps;
@@ -505,11 +497,12 @@ bool ortho_fits(int M, int N, int batch)
 
 size_t ortho_workspace(int M, int N, int batch)
 {
-    return (size_t)layout(M, N).bytes * batch;
+    return ortho_small(M, N) ? 0 : (size_t)layout(M, N).bytes * batch;
 }
 
 hipError_t launch_ortho(const OrthoProblem &p, bool bf, hipStream_t stream)
 {
+    if (ortho_small(p.M, p.N)) return launch_ortho_small(p, bf, stream);
     return bf ? launch<true>(p, stream) : launch<false>(p, stream);
 }
 

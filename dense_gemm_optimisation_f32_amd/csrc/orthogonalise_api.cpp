@@ -27,7 +27,7 @@ int orthogonalise(int M, int N, int steps, const float *coefficients, float alph
     if (misaligned(G, bf ? 2 : 4) || misaligned(O, 2)) return GEMM_ERR_ALIGN;
     const size_t need = mi355gemm::ortho_workspace(M, N, batch_count);
     if (workspace_bytes < 0 || (size_t)workspace_bytes < need) return GEMM_ERR_SCRATCH;
-    if (!workspace) return GEMM_ERR_NULL;
+    if (need > 0 && !workspace) return GEMM_ERR_NULL;
     if (misaligned(workspace, 16)) return GEMM_ERR_ALIGN;
     mi355gemm::OrthoProblem p;
     p.M = M; p.N = N; p.steps = steps;

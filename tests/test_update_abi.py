@@ -78,7 +78,7 @@ def test_grouped_arguments(lib, kw, want):
 
 
 FIVE = (ctypes.c_float * 15)(*[3.4445, -4.775, 2.0315] * 5)
-ORTHO = dict(M=20, N=30, steps=5, coefficients=ctypes.addressof(FIVE), alpha=1.0, G=FAKE, ldg=30, strideG=600, O=FAKE, ldo=30, strideO=600, batch=2,
+ORTHO = dict(M=200, N=300, steps=5, coefficients=ctypes.addressof(FIVE), alpha=1.0, G=FAKE, ldg=300, strideG=60000, O=FAKE, ldo=300, strideO=60000, batch=2,
              ws=FAKE, ws_bytes=1 << 30, stream=None)
 
 
@@ -86,7 +86,7 @@ ORTHO = dict(M=20, N=30, steps=5, coefficients=ctypes.addressof(FIVE), alpha=1.0
 @pytest.mark.parametrize("kw,want", [
     (dict(M=-1), ESIZE), (dict(N=-1), ESIZE), (dict(M=65537), ESIZE), (dict(N=65537, ldg=65537, ldo=65537), ESIZE), (dict(steps=0), ESIZE),
     (dict(steps=101), ESIZE), (dict(batch=-1), ESIZE), (dict(batch=65536), ESIZE), (dict(M=65536, N=65536, ldg=65536, ldo=65536, batch=9), ESIZE),
-    (dict(ldg=29), ELD), (dict(ldo=29), ELD), (dict(strideG=-1), ELD), (dict(strideO=599), ELD), (dict(strideG=1 << 62), ESIZE),
+    (dict(ldg=299), ELD), (dict(ldo=299), ELD), (dict(strideG=-1), ELD), (dict(strideO=59999), ELD), (dict(strideG=1 << 62), ESIZE),
     (dict(coefficients=None), ENULL), (dict(G=None), ENULL), (dict(O=None), ENULL), (dict(ws=None), ENULL), (dict(G=FAKE + 1), EALIGN),
     (dict(O=FAKE + 1), EALIGN), (dict(ws=FAKE + 8), EALIGN), (dict(ws_bytes=64), ESCRATCH), (dict(ws_bytes=-1), ESCRATCH),
     (dict(M=0, G=None, ws=None), OK), (dict(N=0, G=None, ws=None), OK), (dict(batch=0, G=None, ws=None), OK),
@@ -99,9 +99,9 @@ def test_orthogonalise_workspace(lib):
     size = lib.orthogonalise_workspace
     assert size(0, 8, 1) == size(8, 0, 1) == size(8, 8, 0) == 0
     assert size(-1, 8, 1) == size(70000, 8, 1) == size(8, 8, 65536) == 0       # not calls that can be made
-    for M, N in ((1, 1), (100, 1000), (513, 300), (4096, 4096)):
+    for M, N in ((1, 1), (64, 1024), (512, 128), (129, 129), (513, 300), (4096, 4096)):
         one = size(M, N, 1)
-        assert one > 0 and one % 16 == 0 and size(M, N, 3) == 3 * one and size(N, M, 1) == one
+        assert one % 16 == 0 and (one > 0) == (min(M, N) > 128) and size(M, N, 3) == 3 * one and size(N, M, 1) == one
         assert one <= 12 * (M + 127) * (N + 127) + 8 * (min(M, N) + 127) ** 2 + 8192
 
 

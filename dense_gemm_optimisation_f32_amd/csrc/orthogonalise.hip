@@ -30,7 +30,7 @@ namespace {
 
 typedef _Float16 half4 __attribute__((ext_vector_type(4)));
 
-constexpr int kNormBlocks = 64;      // workgroups (and partial sums) of a matrix's norm
+constexpr int kNormBlocks = 512;     // workgroups (and partial sums) of a matrix's norm at most
 
 // One matrix's part of the workspace.  Rows and columns are filled up to multiples of 64 with zeros,
 // which the products keep.
@@ -67,6 +67,7 @@ struct OrthoArgs {
     int M, N;                        // of G and O
     int m, n;                        // of X, padded
     bool tall, last;
+    int norm_blocks;
     float a, b, c;                   // this step's coefficients
     float x_scale;                   // x16 and x hold x_scale * X
     float alpha;
@@ -112,20 +113,52 @@ __device__ __forceinline__ float g_at(const OrthoArgs &p, int z, long long r, lo
         return reinterpret_cast<const float *>(p.G)[at];
 }
 
-// Sums of squares in 64 bits: neither large nor small entries leave the range.
-template <bool BF>
+// Sums of squares in 64 bits: neither large nor small entries leave the range.  A wave takes 256 columns of a row at a
+// time, four such pieces together.
+template <bool BF, bool VEC>
 __global__ __launch_bounds__(256) void norm_kernel(OrthoArgs p)
 {
     __shared__ double part[4];
-    const int z = blockIdx.z, tid = threadIdx.x;
+    const int z = blockIdx.z, tid = threadIdx.x, lane = tid & 63;
+    const int across = (p.N + 255) / 256, turn = gridDim.x * 4;
+    const int pieces = p.M * across;   // (at most 2^24)
     double sum = 0;
-    for (int r = blockIdx.x; r < p.M; r += kNormBlocks)
-        for (int c = tid; c < p.N; c += 256) {
-            const double v = g_at<BF>(p, z, r, c);
-            sum = __builtin_fma(v, v, sum);
+    for (int first = blockIdx.x * 4 + (tid >> 6); first < pieces; first += 4 * turn) {
+        float v[4][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int piece = first + u * turn, r = piece / across, c = piece % across * 256 + 4 * lane;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[u][e] = 0.f;
+            if (piece >= pieces) continue;
+            if (VEC && c + 4 <= p.N) {
+                const long long at = z * p.strideG + r * p.ldg + c;
+                if constexpr (BF) {
+                    typedef unsigned u32x2_g __attribute__((ext_vector_type(2), aligned(4)));
+                    const u32x2_g w = *reinterpret_cast<const u32x2_g *>(reinterpret_cast<const uint16_t *>(p.G) + at);
+                    const unsigned w0 = w.x, w1 = w.y;
+                    v[u][0] = __builtin_bit_cast(float, w0 << 16);
+                    v[u][1] = __builtin_bit_cast(float, w0 & 0xFFFF0000u);
+                    v[u][2] = __builtin_bit_cast(float, w1 << 16);
+                    v[u][3] = __builtin_bit_cast(float, w1 & 0xFFFF0000u);
+                } else {
+                    const f32x4_t w = *reinterpret_cast<const f32x4_g *>(reinterpret_cast<const float *>(p.G) + at);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[u][e] = w[e];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < p.N) v[u][e] = g_at<BF>(p, z, r, c + e);
+            }
         }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum = __builtin_fma((double)v[u][e], (double)v[u][e], sum);
+    }
     sum = wave_sum(sum);
-    if ((tid & 63) == 0) part[tid >> 6] = sum;
+    if (lane == 0) part[tid >> 6] = sum;
     __syncthreads();
     if (tid == 0) of_member(p.norm, p.ws_stride, z)[blockIdx.x] = part[0] + part[1] + part[2] + part[3];
 }
@@ -138,24 +171,42 @@ __global__ __launch_bounds__(256) void start_kernel(OrthoArgs p)
     const int z = blockIdx.z, tid = threadIdx.x;
     const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;   // of X
     const double *norm = of_member(p.norm, p.ws_stride, z);
+    float g[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        // (consecutive threads along G's rows)
+        const int e = tid + 256 * k, i = p.tall ? e % 64 : e / 64, j = p.tall ? e / 64 : e % 64;
+        const int gr = p.tall ? c0 + j : r0 + i, gc = p.tall ? r0 + i : c0 + j;
+        g[k] = gr < p.M && gc < p.N ? g_at<BF>(p, z, gr, gc) : 0.f;
+    }
     double sum = 0;
-    for (int i = 0; i < kNormBlocks; ++i) sum += norm[i];
+    for (int i = tid & 63; i < p.norm_blocks; i += 64) sum += norm[i];
+    sum = wave_sum(sum);
     // zeros stay zeros; an infinity or NaN makes everything NaN
     const double f = sum == 0 ? 0 : sum < __builtin_inf() ? p.x_scale / __builtin_sqrt(sum) : __builtin_nan("");
-    for (int e = tid; e < 64 * 64; e += 256) {
-        // (consecutive threads along G's rows)
-        const int i = p.tall ? e % 64 : e / 64, j = p.tall ? e / 64 : e % 64;
-        const int gr = p.tall ? c0 + j : r0 + i, gc = p.tall ? r0 + i : c0 + j;
-        tile[i][j] = gr < p.M && gc < p.N ? (float)(g_at<BF>(p, z, gr, gc) * f) : 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const int e = tid + 256 * k, i = p.tall ? e % 64 : e / 64, j = p.tall ? e / 64 : e % 64;
+        tile[i][j] = (float)(g[k] * f);
     }
     __syncthreads();
     float *x = of_member(p.x, p.ws_stride, z);
     _Float16 *x16 = of_member(p.x16, p.ws_stride, z), *xt = of_member(p.xt_out, p.ws_stride, z);
-    for (int e = tid; e < 64 * 64; e += 256) {
-        const int i = e / 64, j = e % 64;
-        x[(long long)(r0 + i) * p.n + c0 + j] = tile[i][j];
-        x16[(long long)(r0 + i) * p.n + c0 + j] = (_Float16)tile[i][j];
-        xt[(long long)(c0 + i) * p.m + r0 + j] = (_Float16)tile[j][i];
+    // four columns of X (rows of its transposed copy) a thread
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int e = tid + 256 * k, i = e / 16, j = e % 16 * 4;
+        f32x4_t v;
+        half4 h, t;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            v[d] = tile[i][j + d];
+            h[d] = (_Float16)v[d];
+            t[d] = (_Float16)tile[j + d][i];
+        }
+        *reinterpret_cast<f32x4_t *>(x + (long long)(r0 + i) * p.n + c0 + j) = v;
+        *reinterpret_cast<half4 *>(x16 + (long long)(r0 + i) * p.n + c0 + j) = h;
+        *reinterpret_cast<half4 *>(xt + (long long)(c0 + i) * p.m + r0 + j) = t;
     }
 }
 
@@ -468,7 +519,14 @@ hipError_t launch(const OrthoProblem &q, hipStream_t stream)
     a.db = reinterpret_cast<float *>(w + l.db);
     a.norm = reinterpret_cast<double *>(w + l.norm);
     _Float16 *xt[2] = {reinterpret_cast<_Float16 *>(w + l.xt[0]), reinterpret_cast<_Float16 *>(w + l.xt[1])};
-    hipLaunchKernelGGL(norm_kernel<BF>, dim3(kNormBlocks, 1, q.batch), dim3(256), 0, stream, a);
+    // 4096 values a workgroup (four pieces of 256 for each wave), or more
+    const long long share = ((long long)q.M * ((q.N + 255) / 256) + 15) / 16;
+    a.norm_blocks = (int)(share < kNormBlocks ? share : kNormBlocks);
+    const bool vec = !BF || (reinterpret_cast<uintptr_t>(q.G) % 4 == 0 && q.ldg % 2 == 0 && q.strideG % 2 == 0);
+    if (vec)
+        hipLaunchKernelGGL((norm_kernel<BF, true>), dim3(a.norm_blocks, 1, q.batch), dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((norm_kernel<BF, false>), dim3(a.norm_blocks, 1, q.batch), dim3(256), 0, stream, a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     a.xt_out = xt[0];
     hipLaunchKernelGGL(start_kernel<BF>, dim3(a.n / 64, a.m / 64, q.batch), dim3(256), 0, stream, a);

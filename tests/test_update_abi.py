@@ -102,7 +102,7 @@ def test_orthogonalise_workspace(lib):
     for M, N in ((1, 1), (64, 1024), (512, 128), (129, 129), (513, 300), (4096, 4096)):
         one = size(M, N, 1)
         assert one % 16 == 0 and (one > 0) == (min(M, N) > 128) and size(M, N, 3) == 3 * one and size(N, M, 1) == one
-        assert one <= 12 * (M + 127) * (N + 127) + 8 * (min(M, N) + 127) ** 2 + 8192
+        assert one <= 12 * (M + 127) * (N + 127) + 8 * (min(M, N) + 127) ** 2 + 16384
 
 
 def test_binding_refuses(lib):

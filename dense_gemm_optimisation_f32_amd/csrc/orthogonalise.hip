@@ -212,27 +212,33 @@ __global__ __launch_bounds__(256) void start_kernel(OrthoArgs p)
 
 enum Product { kGram, kSquare, kApply };
 
-// The tile a workgroup takes, XCD by XCD (see tile_order.h).  The symmetric products compute the tiles on and above
-// the diagonal alone, row by row; a workgroup also stores its tile's mirror image.
+// The tile a workgroup takes.  XCD by XCD (see tile_order.h; here within 32 bits, whose divisions are short): the
+// workgroups of one XCD take consecutive tiles, four tile rows at a time.  The symmetric products compute the tiles on and
+// above the diagonal alone, row by row; a workgroup also stores its tile's mirror image.
 template <Product KIND>
-__device__ __forceinline__ void tile_of(int rows, int cols, int *member, int *tm, int *tn)
+__device__ __forceinline__ void tile_of(unsigned rows, unsigned cols, int *member, int *tm, int *tn)
 {
+    const unsigned each = KIND == kApply ? rows * cols : rows * (rows + 1) / 2;
+    const unsigned total = each * gridDim.z, lin = blockIdx.z * each + blockIdx.x;   // (below 2^23)
+    const unsigned xcd = lin % kNumXcd, per = total / kNumXcd, extra = total % kNumXcd;
+    const unsigned logical = xcd * per + (xcd < extra ? xcd : extra) + lin / kNumXcd;
+    const unsigned z = gridDim.z == 1 ? 0u : logical / each;
+    unsigned left = logical - z * each;
+    *member = (int)z;
     if constexpr (KIND == kApply) {
-        tile_coords(blockIdx.x, blockIdx.z, gridDim.z, rows, cols, member, tm, tn);
+        const unsigned group = left / (kGroupM * cols), first = group * kGroupM;
+        const unsigned down = rows - first < kGroupM ? rows - first : kGroupM;
+        left -= group * kGroupM * cols;
+        *tm = (int)(first + left % down);
+        *tn = (int)(left / down);
     } else {
-        const int each = rows * (rows + 1) / 2;
-        const long long total = (long long)each * gridDim.z, lin = (long long)blockIdx.z * each + blockIdx.x;
-        const long long xcd = lin % kNumXcd, per = total / kNumXcd, extra = total % kNumXcd;
-        const long long logical = xcd * per + (xcd < extra ? xcd : extra) + lin / kNumXcd;
-        *member = (int)(logical / each);
-        int left = (int)(logical - (long long)*member * each), r = 0;
-        // row r holds rows - r tiles (at most 1024 rows)
+        unsigned r = 0;   // row r holds rows - r tiles (at most 1024 rows)
         while (left >= rows - r) {
             left -= rows - r;
             ++r;
         }
-        *tm = r;
-        *tn = r + left;
+        *tm = (int)r;
+        *tn = (int)(r + left);
     }
 }
 
@@ -281,6 +287,31 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
         for (int i = 0; i < B_LOADS; ++i) dma16(b, offB[i], lb + 1024 * i);
     };
     const int wm = wave / Cfg::WN, wn = wave % Cfg::WN, lr = lane & 31, lk = lane >> 5;
+    // What the epilogue reads (rows first + q RPI + er, columns c ..).  A wave of one block of 32 x 32 reads it here, ahead
+    // of the K loop, which small matrices leave after a few microseconds.
+    constexpr int TN = Cfg::TN, LPR = TN / 4, RPI = 64 / LPR, NQ = 32 / RPI;
+    constexpr bool EARLY = FM == 1 && FN == 1;
+    float *x = of_member(p.x, p.ws_stride, z), *da = of_member(p.da, p.ws_stride, z), *db = of_member(p.db, p.ws_stride, z);
+    _Float16 *a16 = of_member(p.a16, p.ws_stride, z), *b16 = of_member(p.b16, p.ws_stride, z);
+    const int er = lane / LPR, c = n0 + wn * TN + 4 * (lane % LPR);
+    f32x4_t xs[NQ], dcs;
+    half4 os[NQ];
+    float drs[NQ];
+    auto read_epilogue = [&](int first) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            const int r = first + q * RPI + er;
+            if constexpr (KIND == kSquare) {
+                os[q] = *reinterpret_cast<const half4 *>(a16 + (long long)r * p.m + c);
+                drs[q] = da[r];
+            } else if constexpr (KIND == kApply) {
+                xs[q] = *reinterpret_cast<const f32x4_t *>(x + (long long)r * p.n + c);
+                drs[q] = db[r];
+            }
+        }
+        if constexpr (KIND == kSquare) dcs = *reinterpret_cast<const f32x4_t *>(da + c);
+    };
+    if constexpr (EARLY) read_epilogue(m0 + wm * Cfg::TM);   // (64 x 64 tiles lie within the padded sizes)
     constexpr int NS = BK / 16;
     unsigned fragA[NS], fragB[NS];
 #pragma unroll
@@ -360,16 +391,13 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
         }
     }
 
-    constexpr int TN = Cfg::TN, LPR = TN / 4, RPI = 64 / LPR, NQ = 32 / RPI;
     static_assert(Cfg::NW * 32 * TN * 4 <= S * Cfg::STAGE_BYTES, "staging area exceeds the ring");
+    static_assert(!EARLY || (BM == 64 && BN == 64), "early reads stay inside the padded matrices");
     const unsigned stage = lds0 + wave * 32 * TN * 4;
     wait_vmcnt<0>();   // (slices that a short K did not use)
     lds_barrier();
-    float *x = of_member(p.x, p.ws_stride, z), *da = of_member(p.da, p.ws_stride, z), *db = of_member(p.db, p.ws_stride, z);
-    _Float16 *a16 = of_member(p.a16, p.ws_stride, z), *b16 = of_member(p.b16, p.ws_stride, z);
     _Float16 *x16 = of_member(p.x16, p.ws_stride, z), *xt = of_member(p.xt_out, p.ws_stride, z);
     uint16_t *O = p.O + z * p.strideO;
-    const int er = lane / LPR, c = n0 + wn * TN + 4 * (lane % LPR);
     const bool mirrored = KIND != kApply && tm != tn;
     // chunk of the staged row: 16 bytes of columns 4 k.. at chunk k ^ (row % LPR)
     auto chunk = [&](int r, int k) { return stage + r * TN * 4 + 16 * (k ^ (r & (LPR - 1))); };
@@ -377,6 +405,7 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
     for (int i = 0; i < FM; ++i) {
         const int first = m0 + wm * Cfg::TM + 32 * i;
         if (first >= p.m || n0 + wn * TN >= cols) break;   // (uniform; padded sizes are multiples of 64)
+        if constexpr (!EARLY) read_epilogue(first);
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
@@ -403,9 +432,8 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
                 }
                 *reinterpret_cast<half4 *>(a16 + (long long)r * p.m + c) = h;
             } else if constexpr (KIND == kSquare) {
-                const half4 o = *reinterpret_cast<const half4 *>(a16 + (long long)r * p.m + c);
-                const f32x4_t dc = *reinterpret_cast<const f32x4_t *>(da + c);
-                const float dr = da[r];
+                const half4 o = os[q];
+                const float dr = drs[q];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float off = o[e];
@@ -413,19 +441,17 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
                         db[r] = p.b * dr + p.c * (dr * dr + v[e]);
                         v[e] = 0.f;
                     } else {
-                        v[e] = p.b * off + p.c * ((dr + dc[e]) * off + v[e]);
+                        v[e] = p.b * off + p.c * ((dr + dcs[e]) * off + v[e]);
                     }
                     h[e] = (_Float16)v[e];
                 }
                 *reinterpret_cast<half4 *>(b16 + (long long)r * p.m + c) = h;
             } else {
-                f32x4_t *px = reinterpret_cast<f32x4_t *>(x + (long long)r * p.n + c);
-                const f32x4_t old = *px;
-                const float f = p.a + db[r];
+                const float f = p.a + drs[q];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, old[e], v[e]);
+                for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, xs[q][e], v[e]);
                 if (!p.last) {
-                    *px = v;
+                    *reinterpret_cast<f32x4_t *>(x + (long long)r * p.n + c) = v;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) h[e] = (_Float16)v[e];
                     *reinterpret_cast<half4 *>(x16 + (long long)r * p.n + c) = h;

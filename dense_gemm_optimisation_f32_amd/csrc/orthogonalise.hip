@@ -513,11 +513,15 @@ using Small = HgDmaCfg<64, 64, 4, 2, 2, 64>;
 template <Product KIND>
 hipError_t launch_product(const OrthoArgs &a, int batch, hipStream_t stream)
 {
-    auto time = [&](int side, double each) {
+    // Rounds of 256 workgroups, each with so long for a slice and for its start and end (us, measured on products of 512 x
+    // 512 to 4096 x 4096).  Two 64 x 64 tiles share a CU, so their rounds need not be whole.
+    auto time = [&](int side, double slice, double fixed, bool whole) {
         const double rows = (a.m + side - 1) / side, cols = (a.n + side - 1) / side;
-        return std::ceil((KIND == kApply ? rows * cols : rows * (rows + 1) / 2) * batch / 256) * each;
+        const double rounds = (KIND == kApply ? rows * cols : rows * (rows + 1) / 2) * batch / 256;
+        const double slices = (KIND == kGram ? a.n : a.m) / 64;
+        return (rounds <= 1 ? 1. : whole ? std::ceil(rounds) : rounds) * (slices * slice + fixed);
     };
-    const double large = time(256, 1.0), middle = time(128, 0.4), small = time(64, 0.16);
+    const double large = time(256, 1.4, 5, true), middle = time(128, 0.44, 4, true), small = time(64, 0.25, 1.4, false);
     if (large <= middle && large <= small) return launch_tiles<Large, KIND>(a, batch, stream);
     if (middle <= small) return launch_tiles<Middle, KIND>(a, batch, stream);
     return launch_tiles<Small, KIND>(a, batch, stream);

@@ -36,7 +36,7 @@ constexpr int kNormBlocks = 512;     // workgroups (and partial sums) of a matri
 // which the products keep.
 struct Layout {
     long long m, n;                  // padded
-    long long x, x16, xt[2], a16, b16, da, db, norm, bytes;   // byte offsets
+    long long x, x16[2], a16, b16, da, db, norm, bytes;   // byte offsets
 };
 long long up64(long long v) { return (v + 63) / 64 * 64; }
 Layout layout(int M, int N)
@@ -51,9 +51,8 @@ Layout layout(int M, int N)
         return here;
     };
     l.x = take(l.m * l.n * 4);
-    l.x16 = take(l.m * l.n * 2);
-    l.xt[0] = take(l.m * l.n * 2);
-    l.xt[1] = take(l.m * l.n * 2);
+    l.x16[0] = take(l.m * l.n * 2);   // (a step reads the one and writes the other)
+    l.x16[1] = take(l.m * l.n * 2);
     l.a16 = take(l.m * l.m * 2);
     l.b16 = take(l.m * l.m * 2);
     l.da = take(l.m * 4);
@@ -77,7 +76,7 @@ struct OrthoArgs {
     long long ldo, strideO;
     long long ws_stride;             // bytes per matrix
     float *x;
-    _Float16 *x16, *xt_in, *xt_out, *a16, *b16;
+    _Float16 *x16, *x16_next, *a16, *b16;
     float *da, *db;
     double *norm;
 };
@@ -163,7 +162,7 @@ __global__ __launch_bounds__(256) void norm_kernel(OrthoArgs p)
     if (tid == 0) of_member(p.norm, p.ws_stride, z)[blockIdx.x] = part[0] + part[1] + part[2] + part[3];
 }
 
-// X and its copies from G: a 64 x 64 tile of X per workgroup.
+// X and its copy from G: a 64 x 64 tile of X per workgroup.
 template <bool BF>
 __global__ __launch_bounds__(256) void start_kernel(OrthoArgs p)
 {
@@ -191,22 +190,20 @@ __global__ __launch_bounds__(256) void start_kernel(OrthoArgs p)
     }
     __syncthreads();
     float *x = of_member(p.x, p.ws_stride, z);
-    _Float16 *x16 = of_member(p.x16, p.ws_stride, z), *xt = of_member(p.xt_out, p.ws_stride, z);
-    // four columns of X (rows of its transposed copy) a thread
+    _Float16 *x16 = of_member(p.x16, p.ws_stride, z);
+    // four columns a thread
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int e = tid + 256 * k, i = e / 16, j = e % 16 * 4;
         f32x4_t v;
-        half4 h, t;
+        half4 h;
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
             v[d] = tile[i][j + d];
             h[d] = (_Float16)v[d];
-            t[d] = (_Float16)tile[j + d][i];
         }
         *reinterpret_cast<f32x4_t *>(x + (long long)(r0 + i) * p.n + c0 + j) = v;
         *reinterpret_cast<half4 *>(x16 + (long long)(r0 + i) * p.n + c0 + j) = h;
-        *reinterpret_cast<half4 *>(xt + (long long)(c0 + i) * p.m + r0 + j) = t;
     }
 }
 
@@ -242,12 +239,36 @@ __device__ __forceinline__ void tile_of(unsigned rows, unsigned cols, int *membe
     }
 }
 
-// The three products of a step, each P Q^T of fp16 rows with k contiguous and whole slices of 64:
-//   kGram    A = X X^T            P = Q = X
-//   kSquare  B = b A + c A A      P = Q = A - diag(A)
-//   kApply   X <- a X + B X       P = B - diag(B), Q = X^T
+// An operand stored with k outermost (X as the right operand of B X), in slices of 64 k of R columns: 16-byte chunk c of row k
+// sits at chunk c ^ swz_k(k), which puts the four rows that a transposed read touches on different banks.
+template <int R>
+__device__ __forceinline__ int swz_k(int k)
+{
+    return R == 64 ? 2 * (k & 3) : swz_b(k);
+}
+// Byte offset within a slice of the chunk that lane `lane` of wave load g fetches; chunks past the `lim` columns re-read the first.
+template <int R>
+__device__ __forceinline__ unsigned dma_offset_k(int g, int lane, long long ld, int lim)
+{
+    constexpr int CPR = R / 8;
+    const int k = 64 / CPR * g + lane / CPR;
+    const int c = 8 * ((lane % CPR) ^ swz_k<R>(k));
+    return (unsigned)(k * ld + (c < lim ? c : 0)) * 2u;
+}
+// Where a lane reads four k of the columns from `first` on, of 16 k; four k further for the other four.
+template <int R>
+__device__ __forceinline__ unsigned frag_offset_k(int first, int lane)
+{
+    const int q = lane >> 4, l = lane & 15, k = 8 * (q >> 1) + (l >> 2), n = first + 16 * (q & 1) + 4 * (l & 3);
+    return (unsigned)(k * R * 2 + 16 * ((n >> 3) ^ swz_k<R>(k)) + 2 * (n & 7));
+}
+
+// The three products of a step, of fp16 copies, k in whole slices of 64:
+//   kGram    A = X X^T            P Q^T with P = Q = X
+//   kSquare  B = b A + c A A      P Q^T with P = Q = A - diag(A)
+//   kApply   X <- a X + B X       P Q   with P = B - diag(B), Q = X
 // The ring, its loads and its K loop are those of the whole-matrix kernel (hgemm_mfma.hip).  The epilogue passes 32 rows of
-// a wave's tile at a time through LDS: by rows for what belongs to them, by columns for the transposed copies.
+// a wave's tile at a time through LDS: by rows, and by columns for what is stored transposed.
 template <class Cfg, Product KIND>
 __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
 {
@@ -262,7 +283,8 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
     tile_of<KIND>((p.m + BM - 1) / BM, (cols + BN - 1) / BN, &z, &tm, &tn);
     const int m0 = tm * BM, n0 = tn * BN;
     const _Float16 *P = of_member(KIND == kGram ? p.x16 : KIND == kSquare ? p.a16 : p.b16, p.ws_stride, z);
-    const _Float16 *Q = of_member(KIND == kGram ? p.x16 : KIND == kSquare ? p.a16 : p.xt_in, p.ws_stride, z);
+    const _Float16 *Q = of_member(KIND == kSquare ? p.a16 : p.x16, p.ws_stride, z);
+    constexpr bool K_OUT = KIND == kApply;   // Q is stored with k outermost
 
     constexpr int A_LOADS = Cfg::A_LOADS, B_LOADS = Cfg::B_LOADS, LOADS = A_LOADS + B_LOADS;
     const bool loader = uwave >= Cfg::NW - Cfg::LW;
@@ -271,8 +293,12 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
 #pragma unroll
     for (int i = 0; i < A_LOADS; ++i) offA[i] = dma_offset<true, BM, BK, true>(lw * A_LOADS + i, lane, K, p.m - m0);
 #pragma unroll
-    for (int i = 0; i < B_LOADS; ++i) offB[i] = dma_offset<true, BN, BK, true>(lw * B_LOADS + i, lane, K, cols - n0);
-    const char *Pb = reinterpret_cast<const char *>(P + (long long)m0 * K), *Qb = reinterpret_cast<const char *>(Q + (long long)n0 * K);
+    for (int i = 0; i < B_LOADS; ++i)
+        offB[i] = K_OUT ? dma_offset_k<BN>(lw * B_LOADS + i, lane, p.n, cols - n0)
+                        : dma_offset<true, BN, BK, true>(lw * B_LOADS + i, lane, K, cols - n0);
+    const char *Pb = reinterpret_cast<const char *>(P + (long long)m0 * K);
+    const char *Qb = reinterpret_cast<const char *>(Q + (K_OUT ? (long long)n0 : (long long)n0 * K));
+    const long long stepQ = K_OUT ? (long long)BK * p.n * 2 : BK * 2;
     const int nk = K / BK;
     auto issue = [&](int t, int slot) __attribute__((always_inline)) {
         if (!loader) return;
@@ -280,7 +306,7 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
         const unsigned lb = __builtin_amdgcn_readfirstlane(lds0 + S * Cfg::A_BYTES + slot * Cfg::B_BYTES + lw * B_LOADS * 1024);
         // (a K of fewer slices than the ring has slots re-reads the last, which is not multiplied)
         const int at = t < nk ? t : nk - 1;
-        const char *a = uniform(Pb + (long long)at * BK * 2), *b = uniform(Qb + (long long)at * BK * 2);
+        const char *a = uniform(Pb + (long long)at * BK * 2), *b = uniform(Qb + at * stepQ);
 #pragma unroll
         for (int i = 0; i < A_LOADS; ++i) dma16(a, offA[i], la + 1024 * i);
 #pragma unroll
@@ -313,12 +339,14 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
     };
     if constexpr (EARLY) read_epilogue(m0 + wm * Cfg::TM);   // (64 x 64 tiles lie within the padded sizes)
     constexpr int NS = BK / 16;
-    unsigned fragA[NS], fragB[NS];
+    constexpr int NFB = K_OUT ? FN : NS;
+    unsigned fragA[NS], fragB[NFB];
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-        fragA[s] = lds0 + frag_offset<true, BM, BK>(wm * Cfg::TM, lane, s);
-        fragB[s] = lds0 + S * Cfg::A_BYTES + frag_offset<true, BN, BK>(wn * Cfg::TN, lane, s);
-    }
+    for (int s = 0; s < NS; ++s) fragA[s] = lds0 + frag_offset<true, BM, BK>(wm * Cfg::TM, lane, s);
+#pragma unroll
+    for (int s = 0; s < NFB; ++s)
+        fragB[s] = lds0 + S * Cfg::A_BYTES +
+                   (K_OUT ? frag_offset_k<BN>(wn * Cfg::TN + 32 * s, lane) : frag_offset<true, BN, BK>(wn * Cfg::TN, lane, s));
     f32x16 acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -329,7 +357,16 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
 #pragma unroll
         for (int i = 0; i < FM; ++i) a[i] = *(const lds_half8 *)(uintptr_t)(fragA[s] + slot * Cfg::A_BYTES + i * 32 * BK * 2);
 #pragma unroll
-        for (int j = 0; j < FN; ++j) b[j] = *(const lds_half8 *)(uintptr_t)(fragB[s] + slot * Cfg::B_BYTES + j * 32 * BK * 2);
+        for (int j = 0; j < FN; ++j) {
+            if constexpr (K_OUT) {
+                const unsigned at = fragB[j] + slot * Cfg::B_BYTES + 16 * s * BN * 2;
+                const short4v both[2] = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(uintptr_t)at),
+                                         __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(uintptr_t)(at + 4 * BN * 2))};
+                b[j] = __builtin_bit_cast(half8, both);
+            } else {
+                b[j] = *(const lds_half8 *)(uintptr_t)(fragB[s] + slot * Cfg::B_BYTES + j * 32 * BK * 2);
+            }
+        }
     };
     auto mfmas = [&](const half8 *a, const half8 *b) __attribute__((always_inline)) {
 #pragma unroll
@@ -396,9 +433,10 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
     const unsigned stage = lds0 + wave * 32 * TN * 4;
     wait_vmcnt<0>();   // (slices that a short K did not use)
     lds_barrier();
-    _Float16 *x16 = of_member(p.x16, p.ws_stride, z), *xt = of_member(p.xt_out, p.ws_stride, z);
+    _Float16 *x16 = of_member(p.x16_next, p.ws_stride, z);
     uint16_t *O = p.O + z * p.strideO;
-    const bool mirrored = KIND != kApply && tm != tn;
+    // what also goes out by columns: a symmetric tile's mirror image, a tall result
+    const bool turned = KIND == kApply ? p.last && p.tall : tm != tn;
     // chunk of the staged row: 16 bytes of columns 4 k.. at chunk k ^ (row % LPR)
     auto chunk = [&](int r, int k) { return stage + r * TN * 4 + 16 * (k ^ (r & (LPR - 1))); };
 #pragma unroll
@@ -461,16 +499,10 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
                         if (c + e < p.N) O[(long long)r * p.ldo + c + e] = bf16_bits(v[e] * (p.alpha / p.x_scale));
                 }
             }
-            if (KIND == kApply || mirrored) *(lds_f32x4 *)(uintptr_t)at = v;
+            if (turned) *(lds_f32x4 *)(uintptr_t)at = v;
         }
-        if (KIND != kApply && !mirrored) {
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            continue;
-        }
-        if (KIND == kApply && p.last && !p.tall) {
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            continue;
-        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (!turned) continue;
         // by columns: lane l has 32 rows of column l (TN = 64), or 16 of column l % 32 (TN = 32)
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         constexpr int HALF = TN == 64 ? 32 : 16;
@@ -478,13 +510,13 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
         float t[HALF];
 #pragma unroll
         for (int e = 0; e < HALF; ++e) t[e] = *(const lds_float *)(uintptr_t)(chunk(r0 + e, cl >> 2) + 4 * (cl & 3));
-        if (KIND == kApply && p.last) {
+        if constexpr (KIND == kApply) {
             if (col < p.M)
 #pragma unroll
                 for (int e = 0; e < HALF; ++e)
                     if (first + r0 + e < p.N) O[(long long)col * p.ldo + first + r0 + e] = bf16_bits(t[e] * (p.alpha / p.x_scale));
         } else {
-            _Float16 *dst = (KIND == kGram ? a16 : KIND == kSquare ? b16 : xt) + (long long)col * p.m + first + r0;
+            _Float16 *dst = (KIND == kGram ? a16 : b16) + (long long)col * p.m + first + r0;
 #pragma unroll
             for (int e = 0; e < HALF; e += 8) {
                 half8 h;
@@ -542,13 +574,12 @@ hipError_t launch(const OrthoProblem &q, hipStream_t stream)
     a.ws_stride = l.bytes;
     char *w = static_cast<char *>(q.workspace);
     a.x = reinterpret_cast<float *>(w + l.x);
-    a.x16 = reinterpret_cast<_Float16 *>(w + l.x16);
     a.a16 = reinterpret_cast<_Float16 *>(w + l.a16);
     a.b16 = reinterpret_cast<_Float16 *>(w + l.b16);
     a.da = reinterpret_cast<float *>(w + l.da);
     a.db = reinterpret_cast<float *>(w + l.db);
     a.norm = reinterpret_cast<double *>(w + l.norm);
-    _Float16 *xt[2] = {reinterpret_cast<_Float16 *>(w + l.xt[0]), reinterpret_cast<_Float16 *>(w + l.xt[1])};
+    _Float16 *x16[2] = {reinterpret_cast<_Float16 *>(w + l.x16[0]), reinterpret_cast<_Float16 *>(w + l.x16[1])};
     // 4096 values a workgroup (four pieces of 256 for each wave), or more
     const long long share = ((long long)q.M * ((q.N + 255) / 256) + 15) / 16;
     a.norm_blocks = (int)(share < kNormBlocks ? share : kNormBlocks);
@@ -558,15 +589,15 @@ hipError_t launch(const OrthoProblem &q, hipStream_t stream)
     else
         hipLaunchKernelGGL((norm_kernel<BF, false>), dim3(a.norm_blocks, 1, q.batch), dim3(256), 0, stream, a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    a.xt_out = xt[0];
+    a.x16 = x16[0];
     hipLaunchKernelGGL(start_kernel<BF>, dim3(a.n / 64, a.m / 64, q.batch), dim3(256), 0, stream, a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     for (int s = 0; s < q.steps; ++s) {
         a.a = q.coefficients[3 * s];
         a.b = q.coefficients[3 * s + 1];
         a.c = q.coefficients[3 * s + 2];
-        a.xt_in = xt[s & 1];
-        a.xt_out = xt[(s & 1) ^ 1];
+        a.x16 = x16[s & 1];
+        a.x16_next = x16[(s & 1) ^ 1];
         a.last = s + 1 == q.steps;
         if (hipError_t e = launch_product<kGram>(a, q.batch, stream); e != hipSuccess) return e;
         if (hipError_t e = launch_product<kSquare>(a, q.batch, stream); e != hipSuccess) return e;

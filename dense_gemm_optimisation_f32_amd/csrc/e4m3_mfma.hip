@@ -45,7 +45,7 @@ typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 struct Half16 {
     half8 lo, hi;
 };
-__device__ __forceinline__ Half16 to_f16(const u32x4 &v)
+__device__ __forceinline__ Half16 to_f16(u32x4 v)
 {
     half2v h[8];
 #pragma unroll
@@ -191,19 +191,29 @@ __device__ __forceinline__ void dma4_at(const void *p, unsigned lds_addr)
     asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" : : "v"(p), "s"(lds_addr) : "memory", "m0");
 }
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) unsigned lds_unsigned;
+// Sixteen bytes from byte `by` (0 to 3) of v on, of which `next` holds the last.
+__device__ __forceinline__ u32x4 shifted(const u32x4 &v, unsigned next, unsigned by)
+{
+    return u32x4{__builtin_amdgcn_alignbyte(v.y, v.x, by), __builtin_amdgcn_alignbyte(v.z, v.y, by),
+                 __builtin_amdgcn_alignbyte(v.w, v.z, by), __builtin_amdgcn_alignbyte(next, v.w, by)};
+}
 typedef __attribute__((address_space(3))) float lds_float;
 
 // A BM x BN tile of KG groups of WM x WN waves; the groups take the slices of k in turn, each
 // through a ring of STAGES slots.
-template <int BM_, int BN_, int STAGES_, int WM_, int WN_, int KG_ = 1>
+template <int BM_, int BN_, int STAGES_, int WM_, int WN_, int KG_ = 1, bool SHIFT_ = false>
 struct E4m3Cfg {
+    static constexpr bool SHIFT = SHIFT_;   // rows at any byte
+    using Shifted = E4m3Cfg<BM_, BN_, STAGES_, WM_, WN_, KG_, true>;
     static constexpr int BM = BM_, BN = BN_, BK = 128, STAGES = STAGES_, WM = WM_, WN = WN_, KG = KG_;
     static constexpr int NW = WM * WN, NT = 64 * NW * KG;   // (waves of a group)
     static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
     static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK;                            // a slice
     static constexpr int A_LOADS = A_BYTES / 1024 / NW, B_LOADS = B_BYTES / 1024 / NW;    // per wave
     static constexpr int S_LOADS = ((BM + BN) / 64 + NW - 1) / NW;                        // of 64 scales
-    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 256 * NW * S_LOADS;
+    static constexpr int S_BYTES = 256 * NW * S_LOADS;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + (SHIFT ? 2 : 1) * S_BYTES;     // (SHIFT: and as many dwords)
     static constexpr int LOADS = A_LOADS + B_LOADS + S_LOADS;
     static constexpr int RING = STAGES * STAGE_BYTES, LDS = KG * RING;
     static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0 && BM % 64 == 0 && BN % 64 == 0,
@@ -215,13 +225,19 @@ struct E4m3Cfg {
 // Tiles fed by direct-to-LDS loads.  A slice of 128 k (one block of scales) of both
 // operands, with the scales of its rows and columns, is a slot of a ring of STAGES; a lane
 // reads 16 bytes of a row, makes fp16 of them and has the operands of two matrix-core ops.
-// Needs: dword-aligned rows, K % 16 == 0 (no chunk straddles the end), the rows' offsets
-// from the operand's start (A, rows looked up) or from the tile's within 32 bits.
+// Needs: the rows' offsets from the operand's start (A, rows looked up) or from the tile's within 32 bits; without SHIFT
+// dword-aligned rows and K % 16 == 0 (no chunk straddles the end).
+// SHIFT: rows start at any byte.  A direct-to-LDS load takes whole dwords, so a row comes from the dword that holds its
+// first byte on, with the dword behind each slice beside it; fragments are shifted into place when they are read.  The last k
+// that do not fill a slice come through registers.
 template <class Cfg, int BLOCKB>
 __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
 {
+    constexpr bool SHIFT = Cfg::SHIFT;
     constexpr int BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK, S = Cfg::STAGES, FM = Cfg::FM, FN = Cfg::FN;
-    constexpr int A_LOADS = Cfg::A_LOADS, B_LOADS = Cfg::B_LOADS, S_LOADS = Cfg::S_LOADS, LOADS = Cfg::LOADS;
+    constexpr int A_LOADS = Cfg::A_LOADS, B_LOADS = Cfg::B_LOADS, S_LOADS = Cfg::S_LOADS;
+    constexpr int LOADS = Cfg::LOADS + (SHIFT ? S_LOADS : 0);
+    static_assert(LOADS * S < 64, "outstanding loads");
     __shared__ __attribute__((aligned(1024))) unsigned char lds[Cfg::LDS];
     constexpr int KG = Cfg::KG;
     const int tid = threadIdx.x, lane = tid & 63, wave = (tid >> 6) % Cfg::NW;   // (of its group)
@@ -252,35 +268,46 @@ __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
         return (unsigned)at < (unsigned)p.a_rows ? at : 0;   // (its products are dropped in the epilogue)
     };
     unsigned offA[A_LOADS], offB[B_LOADS];
-    const char *Ab = reinterpret_cast<const char *>(p.A) + (p.rows ? 0 : (long long)m0 * p.lda);
-    const char *Bb = reinterpret_cast<const char *>(p.B) + (long long)group * p.strideB + (long long)n0 * p.ldb;
+    // the tile's first byte of each operand, and the dword that holds it
+    const char *At = reinterpret_cast<const char *>(p.A) + (p.rows ? 0 : (long long)m0 * p.lda);
+    const char *Bt = reinterpret_cast<const char *>(p.B) + (long long)group * p.strideB + (long long)n0 * p.ldb;
+    const unsigned skipA = SHIFT ? (unsigned)(reinterpret_cast<uintptr_t>(At) & 3) : 0u;
+    const unsigned skipB = SHIFT ? (unsigned)(reinterpret_cast<uintptr_t>(Bt) & 3) : 0u;
+    const char *Ab = At - skipA, *Bb = Bt - skipB;
+    // a row's first byte, from there
+    auto byteA = [&](int r) { return skipA + (unsigned)((row_of(r) - (p.rows ? 0 : m0)) * p.lda); };
+    auto byteB = [&](int c) { return skipB + (unsigned)((c < limB ? c : limB - 1) * p.ldb); };
 #pragma unroll
     for (int i = 0; i < A_LOADS; ++i) {
         const int r = 8 * (uwave * A_LOADS + i) + lane / 8;
-        offA[i] = (unsigned)((row_of(r) - (p.rows ? 0 : m0)) * p.lda) + 16 * ((lane % 8) ^ swz_a<8>(r));
+        offA[i] = (byteA(r) & (SHIFT ? ~3u : ~0u)) + 16 * ((lane % 8) ^ swz_a<8>(r));
     }
 #pragma unroll
     for (int i = 0; i < B_LOADS; ++i) {
         const int r = 8 * (uwave * B_LOADS + i) + lane / 8;
-        offB[i] = (unsigned)((r < limB ? r : limB - 1) * p.ldb) + 16 * ((lane % 8) ^ swz_a<8>(r));
+        offB[i] = (byteB(r) & (SHIFT ? ~3u : ~0u)) + 16 * ((lane % 8) ^ swz_a<8>(r));
     }
     // 64 rows' or columns' scales a load: those of A, then those of B, spread to one for each column
     const float *scale[S_LOADS];
     long long scale_step[S_LOADS];
+    const char *behind[SHIFT ? S_LOADS : 1];   // the dword behind a row's slice 0 (that slice's last where all of it is inside)
 #pragma unroll
     for (int i = 0; i < S_LOADS; ++i) {
         const int r = 64 * (uwave * S_LOADS + i) + lane;
         if (64 * (uwave * S_LOADS + i) < BM) {
             scale[i] = p.SA + row_of(r);
             scale_step[i] = p.ldsa;
+            if constexpr (SHIFT) behind[i] = Ab + ((byteA(r) + (BK - 1)) & ~3u);
         } else {
             const int c = r - BM;
             scale[i] = p.SB + (long long)group * p.strideSB + (n0 + (c < limB ? c : limB - 1)) / BLOCKB;
             scale_step[i] = p.ldsb;
+            if constexpr (SHIFT) behind[i] = Bb + ((byteB(c) + (BK - 1)) & ~3u);
         }
     }
     // this group's slices are kg, kg + KG, ..: nk steps, in which slices past the last are zeros
-    const int slices = (K + BK - 1) / BK, steps = (slices + KG - 1) / KG, nk = steps < S ? S : steps;
+    const int slices = (K + BK - 1) / BK, looped = SHIFT ? K / BK : slices;   // (SHIFT: the whole ones)
+    const int steps = (looped + KG - 1) / KG, nk = steps < S ? S : steps;
     auto issue = [&](int step, int slot) __attribute__((always_inline)) {
         const int t = step * KG + kg;
         const unsigned at = __builtin_amdgcn_readfirstlane(lds0 + slot * Cfg::STAGE_BYTES);
@@ -290,21 +317,25 @@ __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
         const int kb = t < slices ? t : slices - 1;
 #pragma unroll
         for (int i = 0; i < S_LOADS; ++i) dma4_at(scale[i] + kb * scale_step[i], ls + 256 * i);
+        if constexpr (SHIFT)
+#pragma unroll
+            for (int i = 0; i < S_LOADS; ++i)
+                dma4_at(t < looped ? (const void *)(behind[i] + (long long)t * BK) : (const void *)zero_chunk, ls + Cfg::S_BYTES + 256 * i);
         if ((t + 1) * BK <= K) {
 #pragma unroll
             for (int i = 0; i < A_LOADS; ++i) dma16(a, offA[i], la + 1024 * i);
 #pragma unroll
             for (int i = 0; i < B_LOADS; ++i) dma16(b, offB[i], lb + 1024 * i);
-        } else {
+        } else {   // (SHIFT: a step without a slice; the k that fill none come later)
 #pragma unroll
             for (int i = 0; i < A_LOADS; ++i) {
                 const int k = t * BK + 16 * ((lane % 8) ^ swz_a<8>(8 * (uwave * A_LOADS + i) + lane / 8));
-                dma16_at(k < K ? (const void *)(a + offA[i]) : (const void *)zero_chunk, la + 1024 * i);
+                dma16_at(!SHIFT && k < K ? (const void *)(a + offA[i]) : (const void *)zero_chunk, la + 1024 * i);
             }
 #pragma unroll
             for (int i = 0; i < B_LOADS; ++i) {
                 const int k = t * BK + 16 * ((lane % 8) ^ swz_a<8>(8 * (uwave * B_LOADS + i) + lane / 8));
-                dma16_at(k < K ? (const void *)(b + offB[i]) : (const void *)zero_chunk, lb + 1024 * i);
+                dma16_at(!SHIFT && k < K ? (const void *)(b + offB[i]) : (const void *)zero_chunk, lb + 1024 * i);
             }
         }
     };
@@ -316,12 +347,31 @@ __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
     const unsigned baseA = lds0 + (wm * Cfg::TM + lr) * BK, baseB = lds0 + Cfg::A_BYTES + (wn * Cfg::TN + lr) * BK;
     const unsigned baseS = lds0 + Cfg::A_BYTES + Cfg::B_BYTES;
 
+    // SHIFT: bytes by which the lane's rows are off a dword (rows 32 apart alike, if not looked up), and where the dword behind a
+    // chunk is: the next chunk's first, or the one behind the slice
+    unsigned offbyA[SHIFT ? FM : 1], offbyB = 0, nextA[SHIFT ? 4 : 1], nextB[SHIFT ? 4 : 1];
+    constexpr int STRIDE_BEHIND = 32 * 4;
+    const bool last_chunk = lk == 1;   // (of substep 3)
+    if constexpr (SHIFT) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) offbyA[i] = byteA(wm * Cfg::TM + 32 * i + lr) & 3;
+        offbyB = byteB(wn * Cfg::TN + lr) & 3;
+        const unsigned ex = lds0 + Cfg::A_BYTES + Cfg::B_BYTES + Cfg::S_BYTES;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const unsigned next = 16 * ((2 * s + lk + 1) ^ swz_a<8>(lr));
+            nextA[s] = s == 3 && last_chunk ? ex + 4 * (wm * Cfg::TM + lr) : baseA + next;
+            nextB[s] = s == 3 && last_chunk ? ex + 4 * (BM + wn * Cfg::TN + lr) : baseB + next;
+        }
+    }
+
     f32x16 acc[FM][FN], sum[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
     u32x4 ra[FM], rb[FN];
+    unsigned na[SHIFT ? FM : 1], nb[SHIFT ? FN : 1];
     Half16 fa[FM], fb[FN];
     auto read = [&](int slot, int s) __attribute__((always_inline)) {
         const unsigned at = slot * Cfg::STAGE_BYTES + chunk[s];
@@ -329,12 +379,19 @@ __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
         for (int i = 0; i < FM; ++i) ra[i] = *(const lds_u32x4 *)(uintptr_t)(baseA + at + i * 32 * BK);
 #pragma unroll
         for (int j = 0; j < FN; ++j) rb[j] = *(const lds_u32x4 *)(uintptr_t)(baseB + at + j * 32 * BK);
+        if constexpr (SHIFT) {
+            const int apart = s == 3 && last_chunk ? STRIDE_BEHIND : 32 * BK;
+#pragma unroll
+            for (int i = 0; i < FM; ++i) na[i] = *(const lds_unsigned *)(uintptr_t)(nextA[s] + slot * Cfg::STAGE_BYTES + i * apart);
+#pragma unroll
+            for (int j = 0; j < FN; ++j) nb[j] = *(const lds_unsigned *)(uintptr_t)(nextB[s] + slot * Cfg::STAGE_BYTES + j * apart);
+        }
     };
     auto convert = [&]() __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < FM; ++i) fa[i] = to_f16(ra[i]);
+        for (int i = 0; i < FM; ++i) fa[i] = to_f16(SHIFT ? shifted(ra[i], na[SHIFT ? i : 0], offbyA[SHIFT ? i : 0]) : ra[i]);
 #pragma unroll
-        for (int j = 0; j < FN; ++j) fb[j] = to_f16(rb[j]);
+        for (int j = 0; j < FN; ++j) fb[j] = to_f16(SHIFT ? shifted(rb[j], nb[SHIFT ? j : 0], offbyB) : rb[j]);
     };
     // the slice's scales
     float sa[FM], sb[BLOCKB == 1 ? 16 * FN : 1];
@@ -369,7 +426,7 @@ __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
     };
 
-    if (K > 0) {
+    if (looped > 0) {
 #pragma unroll
         for (int t = 0; t < S; ++t) issue(t, t);
         wait_vmcnt<LOADS * (S - 1)>();
@@ -418,6 +475,59 @@ __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
         slice(nk - 1, after(S - 1), std::integral_constant<int, 0>{}, std::false_type{}, std::false_type{});
     }
 
+    if constexpr (SHIFT) {
+        if (looped < slices) {   // the last k, by the first group
+            lds_barrier();
+            if (kg == 0) {
+                constexpr int CHUNKS = (BM + BN) * 8 / (64 * Cfg::NW);
+#pragma unroll
+                for (int i = 0; i < CHUNKS; ++i) {
+                    const int id = i * 64 * Cfg::NW + (wave * 64 + lane), r = id / 8, ch = id % 8;   // (rows of B follow those of A)
+                    const int k = looped * BK + 16 * ch;
+                    const char *row = r < BM ? Ab + byteA(r) : Bb + byteB(r - BM);
+                    *(lds_u32x4 *)(uintptr_t)(lds0 + r * BK + 16 * (ch ^ swz_a<8>(r))) = load16_any(reinterpret_cast<const uint8_t *>(row) + k, K - k);
+                }
+                // (the scales of the last slice a wave has read, replaced)
+                auto at = [&](int c) { return p.SB + (long long)group * p.strideSB + (long long)looped * p.ldsb + (c < N ? c : N - 1) / BLOCKB; };
+#pragma unroll
+                for (int i = 0; i < FM; ++i) sa[i] = p.SA[(long long)looped * p.ldsa + row_of(wm * Cfg::TM + 32 * i + lr)];
+                if constexpr (BLOCKB == 1) {
+#pragma unroll
+                    for (int r = 0; r < 16 * FN; ++r) sb[r] = *at(n0 + wn * Cfg::TN + 32 * (r >> 4) + 8 * ((r >> 2) & 3) + 4 * lk + (r & 3));
+                } else {
+                    const float v = *at(n0 + wn * Cfg::TN);
+#pragma unroll
+                    for (int i = 0; i < FM; ++i) sa[i] *= v;
+                }
+            }
+            __builtin_amdgcn_s_waitcnt(0xC07F);
+            lds_barrier();
+            if (kg == 0) {
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) sum[i][j] = f32x16{};
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+#pragma unroll
+                    for (int i = 0; i < FM; ++i) fa[i] = to_f16(*(const lds_u32x4 *)(uintptr_t)(baseA + chunk[s] + i * 32 * BK));
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) fb[j] = to_f16(*(const lds_u32x4 *)(uintptr_t)(baseB + chunk[s] + j * 32 * BK));
+#pragma unroll
+                    for (int i = 0; i < FM; ++i)
+#pragma unroll
+                        for (int j = 0; j < FN; ++j) {
+                            sum[i][j] = mfma16<false>(fb[j].lo, fa[i].lo, sum[i][j]);
+                            sum[i][j] = mfma16<false>(fb[j].hi, fa[i].hi, sum[i][j]);
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) add(i, j);
+            }
+        }
+    }
     if constexpr (KG > 1) {
         // the groups' results, added in their order by the first
         lds_barrier();
@@ -511,13 +621,15 @@ __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
     }
 }
 
-template <int RB_, int CB_, int NW_, int S_>
+template <int RB_, int CB_, int NW_, int S_, bool SHIFT_ = false>
 struct E4m3StreamCfg {
+    static constexpr bool SHIFT = SHIFT_;   // rows at any byte
+    using Shifted = E4m3StreamCfg<RB_, CB_, NW_, S_, true>;
     static constexpr int RB = RB_, CB = CB_, NW = NW_, S = S_;   // blocks of 16 rows and columns, waves, slots
     static constexpr int BM = 16 * RB, BN = 16 * CB, BK = 128, NT = 64 * NW;
     static constexpr int A_LOADS = 2 * RB, B_LOADS = 2 * CB, S_LOADS = (BM + BN + 63) / 64;
-    static constexpr int LOADS = A_LOADS + B_LOADS + S_LOADS;
-    static constexpr int STAGE = (A_LOADS + B_LOADS) * 1024 + S_LOADS * 256;
+    static constexpr int LOADS = A_LOADS + B_LOADS + (SHIFT ? 2 : 1) * S_LOADS;
+    static constexpr int STAGE = (A_LOADS + B_LOADS) * 1024 + (SHIFT ? 2 : 1) * S_LOADS * 256;
     static constexpr int LDS = NW * S * STAGE;
     static_assert(NW * BM * BN * 4 <= LDS, "the waves' sums fit the rings");
     static_assert(LDS <= 160 * 1024 && LOADS * S < 64 && S >= 2 && S <= 4 && BN <= 128, "LDS, outstanding loads");
@@ -533,6 +645,7 @@ __global__ __launch_bounds__(Cfg::NT) void e4m3_stream_kernel(E4m3Args p)
 {
     constexpr int RB = Cfg::RB, CB = Cfg::CB, S = Cfg::S, NW = Cfg::NW, BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK;
     constexpr int A_LOADS = Cfg::A_LOADS, B_LOADS = Cfg::B_LOADS, S_LOADS = Cfg::S_LOADS, LOADS = Cfg::LOADS;
+    constexpr bool SHIFT = Cfg::SHIFT;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[Cfg::LDS];
     const unsigned lds0 = (unsigned)(uintptr_t)lds;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
@@ -560,26 +673,32 @@ __global__ __launch_bounds__(Cfg::NT) void e4m3_stream_kernel(E4m3Args p)
         return (unsigned)at < (unsigned)p.a_rows ? at : 0;   // (its products are dropped at the end)
     };
     unsigned offA[A_LOADS], offB[B_LOADS];
-    const char *Ab = reinterpret_cast<const char *>(p.A) + (p.rows ? 0 : (long long)m0 * p.lda);
-    const char *Bb = reinterpret_cast<const char *>(p.B) + (long long)group * p.strideB + (long long)n0 * p.ldb;
+    const char *At = reinterpret_cast<const char *>(p.A) + (p.rows ? 0 : (long long)m0 * p.lda);
+    const char *Bt = reinterpret_cast<const char *>(p.B) + (long long)group * p.strideB + (long long)n0 * p.ldb;
+    const unsigned skipA = SHIFT ? (unsigned)(reinterpret_cast<uintptr_t>(At) & 3) : 0u;
+    const unsigned skipB = SHIFT ? (unsigned)(reinterpret_cast<uintptr_t>(Bt) & 3) : 0u;
+    const char *Ab = At - skipA, *Bb = Bt - skipB;
+    auto byteA = [&](int r) { return skipA + (unsigned)((row_of(r) - (p.rows ? 0 : m0)) * p.lda); };
+    auto byteB = [&](int c) { return skipB + (unsigned)((c < limB ? c : limB - 1) * p.ldb); };
     auto swizzled = [&](int load) { return 16 * ((lane % 8) ^ swz_a<8>(8 * load + lane / 8)); };   // byte of the lane's chunk
 #pragma unroll
     for (int i = 0; i < B_LOADS; ++i) {
-        const int r = 8 * i + lane / 8;
-        offB[i] = (unsigned)((r < limB ? r : limB - 1) * p.ldb) + swizzled(i);
+        offB[i] = (byteB(8 * i + lane / 8) & (SHIFT ? ~3u : ~0u)) + swizzled(i);
     }
 #pragma unroll
-    for (int i = 0; i < A_LOADS; ++i) offA[i] = (unsigned)((row_of(8 * i + lane / 8) - (p.rows ? 0 : m0)) * p.lda) + swizzled(i);
+    for (int i = 0; i < A_LOADS; ++i) offA[i] = (byteA(8 * i + lane / 8) & (SHIFT ? ~3u : ~0u)) + swizzled(i);
     // scales: the rows', then the columns'
     const float *scale[S_LOADS];
     long long scale_step[S_LOADS];
+    const char *behind[SHIFT ? S_LOADS : 1];   // the dword behind a row's slice (see e4m3_dma_kernel)
 #pragma unroll
     for (int i = 0; i < S_LOADS; ++i) {
         const int r = 64 * i + lane, c = r - BM;
         scale[i] = r < BM ? p.SA + row_of(r) : p.SB + (long long)group * p.strideSB + (n0 + (c < limB ? c : limB - 1)) / BLOCKB;
         scale_step[i] = r < BM ? p.ldsa : p.ldsb;
+        if constexpr (SHIFT) behind[i] = r < BM ? Ab + ((byteA(r) + (BK - 1)) & ~3u) : Bb + ((byteB(c) + (BK - 1)) & ~3u);
     }
-    const int slices = (K + BK - 1) / BK;
+    const int slices = (K + BK - 1) / BK, looped = SHIFT ? K / BK : slices;   // (SHIFT: the whole ones)
     const unsigned ring = lds0 + uwave * S * Cfg::STAGE;
     auto issue = [&](int t, int slot) __attribute__((always_inline)) {
         const unsigned lb = __builtin_amdgcn_readfirstlane(ring + slot * Cfg::STAGE), la = lb + B_LOADS * 1024, ls = la + A_LOADS * 1024;
@@ -599,16 +718,28 @@ __global__ __launch_bounds__(Cfg::NT) void e4m3_stream_kernel(E4m3Args p)
         }
 #pragma unroll
         for (int i = 0; i < S_LOADS; ++i) dma4_at(scale[i] + t * scale_step[i], ls + 256 * i);
+        if constexpr (SHIFT)
+#pragma unroll
+            for (int i = 0; i < S_LOADS; ++i) dma4_at(behind[i] + (long long)t * BK, ls + S_LOADS * 256 + 256 * i);
     };
     const int lr = lane & 15, q = lane >> 4;
+    unsigned offbyA[SHIFT ? RB : 1], offbyB = 0;   // bytes by which the lane's rows are off a dword (16 rows apart alike, if not looked up)
+    if constexpr (SHIFT) {
+#pragma unroll
+        for (int i = 0; i < RB; ++i) offbyA[i] = byteA(16 * i + lr) & 3;
+        offbyB = byteB(lr) & 3;
+    }
     f32x4_t acc[RB][CB];
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
         for (int j = 0; j < CB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    auto compute = [&](int slot, bool refill, int t) __attribute__((always_inline)) {
+    // tail: a slice that came through registers, at its place
+    auto compute = [&](int slot, bool refill, int t, auto tail) __attribute__((always_inline)) {
+        constexpr bool MOVE = SHIFT && !decltype(tail)::value;
         const unsigned lb = ring + slot * Cfg::STAGE, la = lb + B_LOADS * 1024, ls = la + A_LOADS * 1024;
         u32x4 ra[RB][2], rb[CB][2];
+        unsigned na[RB][2], nb[CB][2];
         float sa[RB];
         f32x4_t sb[CB];
 #pragma unroll
@@ -618,6 +749,17 @@ __global__ __launch_bounds__(Cfg::NT) void e4m3_stream_kernel(E4m3Args p)
             for (int j = 0; j < CB; ++j) rb[j][s] = *(const lds_u32x4 *)(uintptr_t)(lb + j * 16 * BK + (at ^ (32 * (j & 1))));
 #pragma unroll
             for (int i = 0; i < RB; ++i) ra[i][s] = *(const lds_u32x4 *)(uintptr_t)(la + i * 16 * BK + (at ^ (32 * (i & 1))));
+            if constexpr (MOVE) {
+                // the dword behind each chunk: the next chunk's first, or the one behind the slice
+                const unsigned next = lr * BK + 16 * ((4 * s + q + 1) ^ swz_a<8>(lr)), ex = ls + S_LOADS * 256;
+                const bool over = s == 1 && q == 3;
+#pragma unroll
+                for (int j = 0; j < CB; ++j)
+                    nb[j][s] = *(const lds_unsigned *)(uintptr_t)(over ? ex + 4 * (BM + 16 * j + lr) : lb + j * 16 * BK + (next ^ (32 * (j & 1))));
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+                    na[i][s] = *(const lds_unsigned *)(uintptr_t)(over ? ex + 4 * (16 * i + lr) : la + i * 16 * BK + (next ^ (32 * (i & 1))));
+            }
         }
 #pragma unroll
         for (int i = 0; i < RB; ++i) sa[i] = *(const lds_float *)(uintptr_t)(ls + 4 * (16 * i + lr));
@@ -632,6 +774,15 @@ __global__ __launch_bounds__(Cfg::NT) void e4m3_stream_kernel(E4m3Args p)
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slot is read: it may be loaded again
         if (refill) issue(t, slot);
+        if constexpr (MOVE) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+#pragma unroll
+                for (int j = 0; j < CB; ++j) rb[j][s] = shifted(rb[j][s], nb[j][s], offbyB);
+#pragma unroll
+                for (int i = 0; i < RB; ++i) ra[i][s] = shifted(ra[i][s], na[i][s], offbyA[SHIFT ? i : 0]);
+            }
+        }
         Half16 fa[RB][2];
 #pragma unroll
         for (int i = 0; i < RB; ++i)
@@ -652,14 +803,14 @@ __global__ __launch_bounds__(Cfg::NT) void e4m3_stream_kernel(E4m3Args p)
             }
         }
     };
-    const int ns = slices > uwave ? (slices - uwave + NW - 1) / NW : 0;   // this wave's slices: uwave, uwave + NW, ...
+    const int ns = looped > uwave ? (looped - uwave + NW - 1) / NW : 0;   // this wave's slices: uwave, uwave + NW, ...
 #pragma unroll
     for (int i = 0; i < S; ++i)
         if (i < ns) issue(uwave + i * NW, i);
     int i = 0, slot = 0;
     for (; i + S < ns; ++i) {
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS * (S - 1)) : "memory");
-        compute(slot, true, uwave + (i + S) * NW);
+        compute(slot, true, uwave + (i + S) * NW, std::false_type{});
         slot = slot + 1 == S ? 0 : slot + 1;
     }
     for (; i < ns; ++i) {   // the last slices: everything has been issued
@@ -672,8 +823,24 @@ __global__ __launch_bounds__(Cfg::NT) void e4m3_stream_kernel(E4m3Args p)
             asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
         else
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        compute(slot, false, 0);
+        compute(slot, false, 0, std::false_type{});
         slot = slot + 1 == S ? 0 : slot + 1;
+    }
+
+    if constexpr (SHIFT) {
+        if (looped < slices && uwave == looped % NW) {   // the last k, by the wave whose turn it is, into its first slot
+            const unsigned lb = ring, la = lb + B_LOADS * 1024, ls = la + A_LOADS * 1024;
+#pragma unroll
+            for (int l = 0; l < A_LOADS + B_LOADS; ++l) {
+                const int of = l < B_LOADS ? l : l - B_LOADS, r = 8 * of + lane / 8, k = looped * BK + 16 * (lane % 8);
+                const char *row = l < B_LOADS ? Bb + byteB(r) : Ab + byteA(r);
+                *(lds_u32x4 *)(uintptr_t)((l < B_LOADS ? lb : la) + r * BK + swizzled(of)) = load16_any(reinterpret_cast<const uint8_t *>(row) + k, K - k);
+            }
+#pragma unroll
+            for (int l = 0; l < S_LOADS; ++l) *(lds_float *)(uintptr_t)(ls + 256 * l + 4 * lane) = scale[l][looped * scale_step[l]];
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            compute(0, false, 0, std::true_type{});
+        }
     }
 
     // the waves' results, 16-byte chunk c of row r at chunk c ^ (r % CH), added in wave order
@@ -721,19 +888,25 @@ long long row_tiles(const E4m3Problem &q, int bm)
     return q.offsets ? q.R / bm + (q.groups < q.R ? q.groups : q.R) : (q.R + (long long)bm - 1) / bm;
 }
 
-// The direct-to-LDS kernels take these operands.
+// The direct-to-LDS kernels take these operands ..
 bool dma_ok(const E4m3Problem &q)
+{
+    return q.K > 0 && 256 * q.lda < (1LL << 31) && 256 * q.ldb < (1LL << 31) && (!q.rows || q.M * q.lda < (1LL << 32) - 4096);
+}
+// .. and these without shifting.
+bool aligned(const E4m3Problem &q)
 {
     auto words = [](const void *p, long long ld, long long stride) {
         return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld % 4 == 0 && stride % 4 == 0;
     };
-    return q.K > 0 && q.K % 16 == 0 && words(q.A, q.lda, 0) && words(q.B, q.ldb, q.strideB) && 256 * q.lda < (1LL << 31) &&
-           256 * q.ldb < (1LL << 31) && (!q.rows || q.M * q.lda < (1LL << 32));
+    return q.K % 16 == 0 && words(q.A, q.lda, 0) && words(q.B, q.ldb, q.strideB);
 }
 
 template <class Cfg>
 hipError_t launch_dma(const E4m3Problem &q, hipStream_t stream)
 {
+    if constexpr (!Cfg::SHIFT)
+        if (!aligned(q)) return launch_dma<typename Cfg::Shifted>(q, stream);
     E4m3Args a = arguments(q);
     a.tiles_m = (int)row_tiles(q, Cfg::BM);
     a.tiles_n = (q.N + Cfg::BN - 1) / Cfg::BN;
@@ -748,6 +921,8 @@ hipError_t launch_dma(const E4m3Problem &q, hipStream_t stream)
 template <class Cfg>
 hipError_t launch_stream(const E4m3Problem &q, hipStream_t stream)
 {
+    if constexpr (!Cfg::SHIFT)
+        if (!aligned(q)) return launch_stream<typename Cfg::Shifted>(q, stream);
     E4m3Args a = arguments(q);
     a.tiles_m = (int)row_tiles(q, Cfg::BM);
     a.tiles_n = (q.N + Cfg::BN - 1) / Cfg::BN;

@@ -209,7 +209,8 @@ def check(C, ref, bound, ints=False):
 @pytest.mark.parametrize("blockB", [1, 128])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 33, 128), (1, 4096, 256), (2, 130, 1000), (16, 512, 2048), (31, 100, 16), (33, 64, 144),
                                    (64, 64, 128), (65, 129, 400), (100, 300, 4096), (128, 128, 128), (200, 257, 777), (256, 256, 512), (257, 385, 640),
-                                   (300, 1024, 129), (513, 500, 1024), (1001, 777, 513), (1024, 1024, 256)])
+                                   (300, 1024, 129), (513, 500, 1024), (1001, 777, 513), (1024, 1024, 256), (2000, 2100, 300), (2100, 2000, 259),
+                                   (500, 4000, 515), (520, 4100, 528), (9, 700, 127), (30, 300, 1999), (3, 5000, 130)])
 def test_product(blockB, M, N, K, ints):
     rng = rng_of("product", blockB, M, N, K, ints)
     A, SA, a, lda, ldsa = operand(rng, M, K, 1, ints)
@@ -236,6 +237,44 @@ def test_product_strides(blockB, M, N, K, lda, ldb, offA, offB):
     got = C.cpu().numpy()
     check(got[:, :N], a @ b.T, np.abs(a) @ np.abs(b).T)
     assert np.all(got[:, N:] == 3)
+
+
+@pytest.mark.parametrize("blockB", [1, 128])
+@pytest.mark.parametrize("K", [128, 203])
+def test_far_rows(blockB, K):
+    """Rows so far apart that a tile's do not fit 32-bit offsets."""
+    M, N, ld = 40, 70, (1 << 23) + 13
+    rng = rng_of("far", blockB, K)
+    A, SA, a, _, ldsa = operand(rng, M, K, 1)
+    B, SB, b, _, ldsb = operand(rng, N, K, blockB)
+    wide = [torch.zeros(n, ld, dtype=torch.uint8, device="cuda") for n in (M, N)]
+    for w, x, n in zip(wide, (A, B), (M, N)):
+        w[:, :K] = x.view(torch.uint8).view(n, K)
+    C = torch.empty(M, N, device="cuda")
+    dg.gemm_e4m3_f32acc(blockB, M, N, K, 1.0, wide[0].view(E4M3), ld, SA, ldsa, wide[1].view(E4M3), ld, SB, ldsb, 0.0, C, N)
+    check(C.cpu().numpy(), a @ b.T, np.abs(a) @ np.abs(b).T)
+
+
+@pytest.mark.parametrize("lda", [1 << 22, (1 << 22) + 7])
+def test_far_gather(lda):
+    """Rows looked up past 4 GiB."""
+    M, R, N, K = 1100, 90, 100, 256
+    rng = rng_of("gather", lda)
+    few = rng.permutation(M)[:20]
+    few[0] = M - 1
+    A, _, a, _, _ = operand(rng, 20, K, 1)
+    SA = torch.from_numpy(np.exp(rng.standard_normal((2, M))).astype(np.float32)).cuda()
+    B, SB, b, ldb, ldsb = operand(rng, N, K, 128)
+    wide = torch.zeros(M * lda, dtype=torch.uint8, device="cuda")
+    at = torch.from_numpy(few.astype(np.int64)).cuda()
+    wide.view(M, lda)[at, :K] = A.view(torch.uint8).view(20, K)
+    pick = rng.integers(0, 20, R)
+    rows = few[pick].astype(np.int32)
+    C = torch.empty(R, N, device="cuda")
+    dg.gemm_grouped_e4m3_f32acc(128, 1, R, N, K, 1.0, wide.view(E4M3), M, lda, SA, M, torch.from_numpy(rows).cuda(), B, ldb, 0, SB, ldsb, 0,
+                                torch.tensor([0, R], dtype=I32, device="cuda"), 0.0, C, N)
+    codes = CODES[codes_of(A).reshape(20, K)][pick] * np.repeat(to64(SA)[:, rows].T, 128, 1)
+    check(C.cpu().numpy(), codes @ b.T, np.abs(codes) @ np.abs(b).T)
 
 
 @pytest.mark.parametrize("M,N,K", [(4, 96, 512), (300, 300, 400)])
@@ -290,7 +329,8 @@ def grouped_case(rng, blockB, G, counts, N, K, T, ints=False, lda=None, ldb=None
 @pytest.mark.parametrize("blockB,counts,N,K,T", [
     (128, [1], 64, 128, 0), (128, [0, 3, 0, 0, 1], 200, 256, 0), (1, [2, 0, 5], 100, 384, 4), (128, [2] * 64, 256, 512, 16),
     (128, [40, 0, 1, 300, 25], 300, 272, 0), (128, [40, 0, 1, 300, 25], 300, 272, 90), (1, [130, 70], 260, 400, 50),
-    (128, [500, 13, 700], 512, 256, 0), (128, [257, 255, 0, 256], 384, 640, 300), (128, [33, 64, 65], 77, 131, 40), (1, [1000], 130, 129, 0)])
+    (128, [500, 13, 700], 512, 256, 0), (128, [257, 255, 0, 256], 384, 640, 300), (128, [33, 64, 65], 77, 131, 40), (1, [1000], 130, 129, 0),
+    (128, [1, 0, 7, 3], 200, 389, 5), (1, [9, 2], 70, 127, 0), (128, [700, 650], 2000, 261, 400), (1, [400, 0, 380], 1000, 385, 77)])
 def test_grouped(blockB, counts, N, K, T, ints):
     rng = rng_of("grouped", blockB, counts, N, K, T, ints)
     G = len(counts)

@@ -19,7 +19,7 @@ namespace {
 
 struct QuantArgs {
     int rows, cols;          // X as stored
-    int tiles_r, tiles_c;    // of 128 x 128
+    int tiles_r, tiles_c;
     const void *X;
     long long ldx, strideX;
     uint8_t *Q;
@@ -114,8 +114,12 @@ __device__ __forceinline__ unsigned row16_max(unsigned v)
     return v;
 }
 
-// A workgroup takes a 128 x 128 tile of X as it is stored: thread t holds 8 columns
-// (8 (t % 16) ..) of 8 consecutive rows (8 (t / 16) ..).
+// A workgroup takes a tile of X as it is stored: thread t holds 8 columns (8 (t % W) ..) of 8 consecutive rows (8 (t /
+// W) ..).  Where scales belong to rows (neither TRANS nor SQUARE) the tile is WIDE, 32 rows of 512 columns (W = 64); else 128 x
+// 128 (W = 16).
+template <bool TRANS, bool SQUARE>
+constexpr int kWide = !TRANS && !SQUARE ? 64 : 16;
+
 template <class T, bool TRANS, bool SQUARE, bool VEC>
 __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
 {
@@ -125,7 +129,8 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
     const int tiles = p.tiles_r * p.tiles_c;
     const int z = blockIdx.x / tiles, tile = blockIdx.x % tiles;
     const int tr = tile / p.tiles_c, tc = tile % p.tiles_c;
-    const int r0 = tr * 128 + 8 * (tid >> 4), c0 = tc * 128 + 8 * (tid & 15);
+    constexpr int W = kWide<TRANS, SQUARE>;
+    const int r0 = tr * (2048 / W) + 8 * (tid / W), c0 = tc * (8 * W) + 8 * (tid % W);
     const T *X = reinterpret_cast<const T *>(p.X) + z * p.strideX;
 
     float y[8][8];
@@ -229,7 +234,8 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
             unsigned mine = ex[0];
 #pragma unroll
             for (int k = 1; k < 8; ++k) mine = i == k ? ex[k] : mine;
-            if (i < 8 && r0 + i < p.rows) S[(long long)tc * p.lds + r0 + i] = __builtin_bit_cast(float, mine << 23);
+            if (i < 8 && r0 + i < p.rows && c0 - 8 * i < p.cols)
+                S[(long long)(c0 / 128) * p.lds + r0 + i] = __builtin_bit_cast(float, mine << 23);
         }
     } else {
         // Q's rows are X's columns: eight k of one row of Q per thread, 128 rows of 128 bytes
@@ -280,9 +286,19 @@ hipError_t launch_type(const QuantProblem &q, const QuantArgs &a, unsigned block
     return q.block == 1 ? launch<T, false, false>(a, blocks, vec, stream) : launch<T, false, true>(a, blocks, vec, stream);
 }
 
+// Rows and columns of X, as stored, that a workgroup takes.
+int tile_rows(const QuantProblem &p)
+{
+    return !p.transpose && p.block == 1 ? 2048 / kWide<false, false> : 128;
+}
+int tile_cols(const QuantProblem &p)
+{
+    return !p.transpose && p.block == 1 ? 8 * kWide<false, false> : 128;
+}
 long long quant_tiles(const QuantProblem &p)
 {
-    return (p.M + 127LL) / 128 * ((p.K + 127LL) / 128);
+    const long long rows = p.transpose ? p.K : p.M, cols = p.transpose ? p.M : p.K;
+    return (rows + tile_rows(p) - 1) / tile_rows(p) * ((cols + tile_cols(p) - 1) / tile_cols(p));
 }
 
 }  // namespace
@@ -298,8 +314,8 @@ hipError_t launch_quant(const QuantProblem &p, QuantType type, hipStream_t strea
     QuantArgs a;
     a.rows = p.transpose ? p.K : p.M;
     a.cols = p.transpose ? p.M : p.K;
-    a.tiles_r = (a.rows + 127) / 128;
-    a.tiles_c = (a.cols + 127) / 128;
+    a.tiles_r = (int)((a.rows + (long long)tile_rows(p) - 1) / tile_rows(p));
+    a.tiles_c = (int)((a.cols + (long long)tile_cols(p) - 1) / tile_cols(p));
     a.X = p.X; a.ldx = p.ldx; a.strideX = p.strideX;
     a.Q = p.Q; a.ldq = p.ldq; a.strideQ = p.strideQ;
     a.S = p.S; a.lds = p.lds; a.strideS = p.strideS;

@@ -34,7 +34,7 @@ QUANT = dict(transpose=0, block=1, M=10, K=300, X=FAKE, ldx=300, strideX=3000, Q
     (dict(strideX=1 << 62), ESIZE), (dict(X=None), ENULL), (dict(Q=None), ENULL), (dict(S=None), ENULL), (dict(S=FAKE + 2), EALIGN),
     (dict(X=FAKE + 1), EALIGN), (dict(M=0, X=None), OK), (dict(K=0, X=None, S=None), OK), (dict(batch=0, Q=None), OK),
     (dict(M=2**30, K=2**20, ldx=2**20, ldq=2**20, lds=2**30, strideQ=2**51, strideS=2**44), ESIZE),     # more tiles than a launch holds
-    (dict(batch=2**23), ESIZE), (dict(batch=2**23 // 3 + 1), ESIZE),
+    (dict(batch=2**23), ESIZE), (dict(transpose=1, ldx=10, batch=2**23 // 3 + 1), ESIZE),
 ])
 def test_quant_arguments(lib, t, kw, want):
     assert getattr(lib, f"quant_e4m3_{t}")(*changed(QUANT, **kw)) == want

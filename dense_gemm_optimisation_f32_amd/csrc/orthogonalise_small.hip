@@ -44,8 +44,10 @@ template <int RB_, int CB_, int WR_, int WC_>
 struct SmallCfg {
     static constexpr int RB = RB_, CB = CB_, WR = WR_, WC = WC_, NW = WR * WC, NT = 64 * NW;
     static constexpr int RF = RB * WR, M = 32 * RF, N = 32 * CB * WC;
-    // rows apart by what spreads a transposed read's four rows (X) or eight rows' chunks (A, B) over the banks
-    static constexpr int X_PITCH = 2 * M + (N * (2 * M + 32) < 156 * 1024 ? 32 : 16), A_PITCH = 2 * M + 16;
+    // X's copy, column by column: whole multiples of 128 bytes a column with 16-byte chunk c of column n at chunk c ^ swz(n) (SWZ),
+    // or columns 32 bytes further apart: a transposed read's four columns are on different banks, a store's 16 on many
+    static constexpr bool SWZ = RF % 2 == 0;
+    static constexpr int X_PITCH = SWZ ? 2 * M : 2 * M + 32, A_PITCH = 2 * M + 16;
     static constexpr int X_BYTES = N * X_PITCH, A_BYTES = M * A_PITCH;
     static constexpr int SMALL = 8 * M + 8 * NW;   // the diagonals of A and B, and the waves' norms
     static constexpr bool KEEP = X_BYTES + 2 * A_BYTES + SMALL <= 160 * 1024;   // X's copy stays beside A and B
@@ -62,6 +64,13 @@ __device__ __forceinline__ half4 to_half(const f32x16 &v, int r)
 {
     const half2v h[2] = {__builtin_convertvector((f32x2{v[r], v[r + 1]}), half2v), __builtin_convertvector((f32x2{v[r + 2], v[r + 3]}), half2v)};
     return __builtin_bit_cast(half4, h);
+}
+
+// (four consecutive columns: different pairs of chunks; sixteen: eight chunks)
+template <class Cfg>
+__device__ __forceinline__ unsigned swz(int column)
+{
+    return Cfg::SWZ ? 16 * (2 * (column & 3) + ((column >> 2) & 1)) : 0;
 }
 
 template <class Cfg, bool BF>
@@ -90,7 +99,6 @@ __global__ __launch_bounds__(Cfg::NT) void small_kernel(SmallArgs p)
 
     // G by blocks: the lane's column, rows 4 (lane / 32) + 8 g + e
     const long long dr = p.tall ? 1 : p.ldg, dc = p.tall ? p.ldg : 1;
-    double sum = 0;
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
@@ -109,14 +117,27 @@ __global__ __launch_bounds__(Cfg::NT) void small_kernel(SmallArgs p)
             }
             __builtin_amdgcn_sched_barrier(0);   // (addresses of one block at a time in registers)
         }
+    // The lane's sum of squares in 32 bits, of its values over the power of two of its largest; the rest in 64, so that
+    // neither large nor small entries leave the range (64 bits for every entry: 13 us of 60 at 128 x 512).
+    float top = 0.f;
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
-        for (int j = 0; j < CB; ++j) {
+        for (int j = 0; j < CB; ++j)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) sum = __builtin_fma((double)x[i][j][r], (double)x[i][j][r], sum);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(x[i][j][r]));
+    const int power = top > 0.f && top < INFINITY ? __builtin_amdgcn_frexp_expf(top) : 0;
+    float squares = 0.f;
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < CB; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float v = __builtin_ldexpf(x[i][j][r], -power);
+                squares = __builtin_fmaf(v, v, squares);
+            }
+    double sum = __builtin_ldexp((double)squares, 2 * power);
     sum = wave_sum(sum);
     if (lane == 0) *(lds_double *)(uintptr_t)(ldsN + 8 * wave) = sum;
     __syncthreads();
@@ -125,14 +146,15 @@ __global__ __launch_bounds__(Cfg::NT) void small_kernel(SmallArgs p)
     for (int w = 0; w < NW; ++w) sum += *(const lds_double *)(uintptr_t)(ldsN + 8 * w);
     // zeros stay zeros; an infinity or NaN makes everything NaN
     const double f = sum == 0 ? 0 : sum < __builtin_inf() ? p.x_scale / __builtin_sqrt(sum) : __builtin_nan("");
+    // (f leaves 32 bits where G's entries are near their ends: its power of two is applied by itself)
+    const int f_power = f > 0 ? __builtin_amdgcn_frexp_exp(f) : 0;
+    const float f_rest = (float)__builtin_ldexp(f, -f_power);
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
-        for (int j = 0; j < CB; ++j) {
+        for (int j = 0; j < CB; ++j)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) x[i][j][r] = (float)(x[i][j][r] * f);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+            for (int r = 0; r < 16; ++r) x[i][j][r] = __builtin_ldexpf(x[i][j][r], f_power) * f_rest;
 
     // this wave's blocks of A: number b = wave, wave + NW, .. of the upper triangle by rows
     int bi[MINE], bj[MINE];
@@ -188,18 +210,18 @@ __global__ __launch_bounds__(Cfg::NT) void small_kernel(SmallArgs p)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const half4 h = to_half(x[i][j], 4 * g);
-                    *(lds_half4 *)(uintptr_t)(lds0 + col_of(j) * XP + 2 * (32 * (rb0 + i) + 8 * g + 4 * lk)) = h;
+                    *(lds_half4 *)(uintptr_t)(lds0 + col_of(j) * XP + ((2 * (32 * (rb0 + i) + 8 * g + 4 * lk)) ^ swz<Cfg>(lr))) = h;
                 }
         __syncthreads();
         f32x16 blk[MINE];
         {
             // transposed reads: four rows (columns of X) of 32 bytes for each 16 lanes
             const int q = here >> 4, l = here & 15;
-            const unsigned at = lds0 + (8 * (q >> 1) + (l >> 2)) * XP + 2 * (16 * (q & 1) + 4 * (l & 3));
+            const unsigned col = 8 * (q >> 1) + (l >> 2), at = lds0 + col * XP, rows = 2 * (16 * (q & 1) + 4 * (l & 3));
             auto frag = [&](int b, int s) -> half8 {
-                const unsigned a = at + 16 * s * XP + 64 * b;
-                const short4v both[2] = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(uintptr_t)a),
-                                         __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(uintptr_t)(a + 4 * XP))};
+                const unsigned lo = at + 16 * s * XP + ((64 * b + rows) ^ swz<Cfg>(col)), hi = at + (16 * s + 4) * XP + ((64 * b + rows) ^ swz<Cfg>(col + 4));
+                const short4v both[2] = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(uintptr_t)lo),
+                                         __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(uintptr_t)hi)};
                 return __builtin_bit_cast(half8, both);
             };
 #pragma unroll
@@ -279,7 +301,7 @@ __global__ __launch_bounds__(Cfg::NT) void small_kernel(SmallArgs p)
         for (int s = 0; s < 2 * RF; ++s) {
             if constexpr (KEEP)
 #pragma unroll
-                for (int j = 0; j < CB; ++j) xh[0][j] = *(const lds_half8 *)(uintptr_t)(lds0 + col_of(j) * XP + 2 * (16 * s + 8 * lk));
+                for (int j = 0; j < CB; ++j) xh[0][j] = *(const lds_half8 *)(uintptr_t)(lds0 + col_of(j) * XP + ((2 * (16 * s + 8 * lk)) ^ swz<Cfg>(lr)));
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
                 const half8 b = *(const lds_half8 *)(uintptr_t)(ldsB + (32 * (rb0 + i) + lr) * AP + 2 * (16 * s + 8 * lk));

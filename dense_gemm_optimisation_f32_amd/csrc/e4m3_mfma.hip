@@ -262,20 +262,22 @@ __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
     const int limA = m_end - m0 < BM ? m_end - m0 : BM, limB = N - n0 < BN ? N - n0 : BN;
 
     // rows outside the tile's re-read valid ones; their results are not stored
+    // (offsets count from this row; rows that A does not hold read it, and their products are dropped in the epilogue)
+    const int base = p.rows ? 0 : m0 < p.a_rows ? m0 : p.a_rows - 1;
     auto row_of = [&](int r) {
         int at = m0 + (r < limA ? r : limA - 1);
         if (p.rows) at = p.rows[at];
-        return (unsigned)at < (unsigned)p.a_rows ? at : 0;   // (its products are dropped in the epilogue)
+        return (unsigned)at < (unsigned)p.a_rows ? at : base;
     };
     unsigned offA[A_LOADS], offB[B_LOADS];
     // the tile's first byte of each operand, and the dword that holds it
-    const char *At = reinterpret_cast<const char *>(p.A) + (p.rows ? 0 : (long long)m0 * p.lda);
+    const char *At = reinterpret_cast<const char *>(p.A) + base * p.lda;
     const char *Bt = reinterpret_cast<const char *>(p.B) + (long long)group * p.strideB + (long long)n0 * p.ldb;
     const unsigned skipA = SHIFT ? (unsigned)(reinterpret_cast<uintptr_t>(At) & 3) : 0u;
     const unsigned skipB = SHIFT ? (unsigned)(reinterpret_cast<uintptr_t>(Bt) & 3) : 0u;
     const char *Ab = At - skipA, *Bb = Bt - skipB;
     // a row's first byte, from there
-    auto byteA = [&](int r) { return skipA + (unsigned)((row_of(r) - (p.rows ? 0 : m0)) * p.lda); };
+    auto byteA = [&](int r) { return skipA + (unsigned)((row_of(r) - base) * p.lda); };
     auto byteB = [&](int c) { return skipB + (unsigned)((c < limB ? c : limB - 1) * p.ldb); };
 #pragma unroll
     for (int i = 0; i < A_LOADS; ++i) {
@@ -667,18 +669,20 @@ __global__ __launch_bounds__(Cfg::NT) void e4m3_stream_kernel(E4m3Args p)
     }
     const int n0 = tn * BN, N = p.N, K = p.K;
     const int limA = m_end - m0 < BM ? m_end - m0 : BM, limB = N - n0 < BN ? N - n0 : BN;
+    // (offsets count from this row; rows that A does not hold read it, and their products are dropped at the end)
+    const int base = p.rows ? 0 : m0 < p.a_rows ? m0 : p.a_rows - 1;
     auto row_of = [&](int r) {
         int at = m0 + (r < limA ? r : limA - 1);
         if (p.rows) at = p.rows[at];
-        return (unsigned)at < (unsigned)p.a_rows ? at : 0;   // (its products are dropped at the end)
+        return (unsigned)at < (unsigned)p.a_rows ? at : base;
     };
     unsigned offA[A_LOADS], offB[B_LOADS];
-    const char *At = reinterpret_cast<const char *>(p.A) + (p.rows ? 0 : (long long)m0 * p.lda);
+    const char *At = reinterpret_cast<const char *>(p.A) + base * p.lda;
     const char *Bt = reinterpret_cast<const char *>(p.B) + (long long)group * p.strideB + (long long)n0 * p.ldb;
     const unsigned skipA = SHIFT ? (unsigned)(reinterpret_cast<uintptr_t>(At) & 3) : 0u;
     const unsigned skipB = SHIFT ? (unsigned)(reinterpret_cast<uintptr_t>(Bt) & 3) : 0u;
     const char *Ab = At - skipA, *Bb = Bt - skipB;
-    auto byteA = [&](int r) { return skipA + (unsigned)((row_of(r) - (p.rows ? 0 : m0)) * p.lda); };
+    auto byteA = [&](int r) { return skipA + (unsigned)((row_of(r) - base) * p.lda); };
     auto byteB = [&](int c) { return skipB + (unsigned)((c < limB ? c : limB - 1) * p.ldb); };
     auto swizzled = [&](int load) { return 16 * ((lane % 8) ^ swz_a<8>(8 * load + lane / 8)); };   // byte of the lane's chunk
 #pragma unroll

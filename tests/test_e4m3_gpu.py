@@ -370,6 +370,22 @@ def test_grouped_rows_outside(R, N, K):
     assert np.max(np.abs(got[fine] - ref[fine]) / np.maximum(bound[fine], 1e-30)) <= TOL   # (a column of NaN has no bound: 0 / 0)
 
 
+@pytest.mark.parametrize("blockB", [1, 128])
+@pytest.mark.parametrize("R,M,N,K,G", [(14, 5, 96, 256, 1), (30, 17, 70, 131, 3), (200, 70, 130, 384, 1), (200, 1, 96, 203, 1), (600, 130, 1100, 256, 2),
+                                       (900, 500, 2100, 400, 2), (900, 260, 2100, 333, 1)])
+def test_grouped_more_rows_than_a(blockB, R, M, N, K, G):
+    """Rows past A's last, without a list of rows: zeros, whatever tile they begin or end in."""
+    rng = rng_of("past", R, N)
+    A, SA, a, lda, ldsa = operand(rng, M, K, 1)
+    B, SB, b, ldb, ldsb = operand(rng, N, K, blockB)
+    C = torch.full((R, N), float("nan"), device="cuda")
+    offsets = torch.tensor([R * g // G for g in range(G + 1)], dtype=I32, device="cuda")
+    dg.gemm_grouped_e4m3_f32acc(blockB, G, R, N, K, 1.0, A, M, lda, SA, ldsa, None, B, ldb, 0, SB, ldsb, 0, offsets, 0.0, C, N)
+    got = C.cpu().numpy()
+    assert np.all(got[M:] == 0)
+    check(got[:M], a @ b.T, np.abs(a) @ np.abs(b).T)
+
+
 def test_grouped_descending_offsets():
     """Offsets that descend and rise again stay inside every operand."""
     rng = rng_of("descending")

@@ -706,7 +706,7 @@ def _coefficients(steps):
 
 
 def _orthogonalise(t, dtype_name, M, N, steps, alpha, G, ldg, strideG, O, ldo, strideO, batch_count, workspace, stream):
-    c = _coefficients(tuple(map(tuple, steps)))
+    c = _coefficients(tuple([tuple(map(float, step)) for step in steps]))   # (numbers: a tensor's value can change)
     args = (M, N, len(steps), ctypes.addressof(c), alpha,
             _strided(G, "G", dtype_name, _members(_extent(M, N, ldg), batch_count, strideG)), ldg, strideG,
             _strided(O, "O", "bfloat16", _members(_extent(M, N, ldo), batch_count, strideO)), ldo, strideO, batch_count)

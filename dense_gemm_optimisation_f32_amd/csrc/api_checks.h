@@ -9,7 +9,7 @@
 
 namespace {
 
-constexpr int kMaxSum = 1 << 30;   // a sum's length (K, or a weight gradient's R): positions in slices past the last stay ints
+constexpr int kMaxSum = 1 << 30;   // a sum's length (K, or a weight gradient's R), a quantised side: positions in slices and tiles past the last stay ints
 
 inline bool misaligned(const void *p, uintptr_t align)
 {

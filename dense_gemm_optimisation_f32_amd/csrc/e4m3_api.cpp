@@ -26,7 +26,7 @@ int quant(int transpose, int block, int M, int K, const void *X, int ldx, long l
           float *S, int lds, long long strideS, int batch_count, mi355gemm::QuantType type, hipStream_t stream)
 {
     if (!flag(transpose)) return GEMM_ERR_OP;
-    if (!block_ok(block) || M < 0 || K < 0 || batch_count < 0) return GEMM_ERR_SIZE;
+    if (!block_ok(block) || M < 0 || K < 0 || M > kMaxSum || K > kMaxSum || batch_count < 0) return GEMM_ERR_SIZE;
     const int rows = transpose ? K : M, cols = transpose ? M : K, kb = ceil_div(K, 128), rb = ceil_div(M, block);
     if (ldx < at_least_1(cols) || ldq < at_least_1(K) || lds < at_least_1(rb)) return GEMM_ERR_LD;
     long long ex, eq, es;

@@ -118,3 +118,21 @@ def test_binding_refuses(lib):
         dg.gemm_e4m3_f32acc(7, 4, 4, 4, 1.0, None, 4, None, 4, None, 4, None, 4, 0.0, None, 4, stream=0)
     with pytest.raises(dg.GemmError):
         dg.orthogonalise_bf16(4, 4, [], 1.0, FAKE, 4, 0, FAKE, 4, 0, workspace=FAKE, stream=0)
+
+
+def test_quant_long_sides(lib):
+    assert lib.quant_e4m3_bf16(*changed(QUANT, M=1, K=2**30 + 1, ldx=2**31 - 1, ldq=2**31 - 1, batch=1)) == ESIZE
+    assert lib.quant_e4m3_bf16(*changed(QUANT, transpose=1, M=2**30 + 1, K=1, ldx=2**31 - 1, lds=2**31 - 1, batch=1)) == ESIZE
+
+
+def test_coefficients_are_read_at_the_call(monkeypatch):
+    """Coefficients that are tensors of one value, changed in place between calls."""
+    torch = pytest.importorskip("torch")
+    seen = []
+    monkeypatch.setattr(dg, "_call", lambda fn, args, *rest: seen.append(list((ctypes.c_float * 3).from_address(args[3]))))
+    steps = torch.tensor([[1.0, 2.0, 3.0]])
+    kept = [list(step) for step in steps]
+    for _ in range(2):
+        dg.orthogonalise_f32(4, 4, kept, 1.0, FAKE, 4, 0, FAKE, 4, 0, workspace=FAKE, stream=0)
+        steps.mul_(2)
+    assert seen == [[1.0, 2.0, 3.0], [2.0, 4.0, 6.0]]

@@ -316,9 +316,10 @@ __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
         const unsigned la = at + uwave * A_LOADS * 1024, lb = at + Cfg::A_BYTES + uwave * B_LOADS * 1024;
         const unsigned ls = at + Cfg::A_BYTES + Cfg::B_BYTES + uwave * S_LOADS * 256;
         const char *a = uniform(Ab + (long long)t * BK), *b = uniform(Bb + (long long)t * BK);
-        const int kb = t < slices ? t : slices - 1;
+        // (a step without a slice: scales of zero too, an infinite one times its sum would be NaN)
 #pragma unroll
-        for (int i = 0; i < S_LOADS; ++i) dma4_at(scale[i] + kb * scale_step[i], ls + 256 * i);
+        for (int i = 0; i < S_LOADS; ++i)
+            dma4_at(t < looped ? (const void *)(scale[i] + t * scale_step[i]) : (const void *)zero_chunk, ls + 256 * i);
         if constexpr (SHIFT)
 #pragma unroll
             for (int i = 0; i < S_LOADS; ++i)

@@ -298,6 +298,30 @@ def test_product_special_values(M, N, K):
     assert np.all(got[2][fine[2]] == 0)
 
 
+@pytest.mark.parametrize("M,N", [(4, 96), (40, 70), (200, 300), (300, 2500), (1100, 2200)])
+@pytest.mark.parametrize("K", [128, 131, 384, 399])
+def test_infinite_scales(M, N, K):
+    """Infinite scales, and scales whose product is infinite, give the infinities that their blocks' sums give."""
+    rng = rng_of("infinite", M, K)
+    A, SA, a, lda, ldsa = operand(rng, M, K, 1)
+    B, SB, b, ldb, ldsb = operand(rng, N, K, 1)
+    for X in (A, B):                                                 # all above zero: the sums' signs are the scales'
+        codes = X.view(torch.uint8)
+        codes &= 0x7F
+        codes[codes == 0] = 8
+    SA[-1, 1] = float("inf")
+    SA[-1, 2], SB[-1, 3] = 2.0 ** 100, 2.0 ** 100
+    SB[-1, 5] = -float("inf")
+    C = torch.empty(M, N, device="cuda")
+    dg.gemm_e4m3_f32acc(1, M, N, K, 1.0, A, lda, SA, ldsa, B, ldb, SB, ldsb, 0.0, C, N)
+    want = torch.zeros(M, N)
+    want[1] = float("inf")
+    want[2, 3] = float("inf")
+    want[:, 5] = -float("inf")
+    got = C.cpu()
+    assert torch.equal(torch.isinf(got), torch.isinf(want)) and torch.equal(torch.sign(got[torch.isinf(got)]), torch.sign(want[torch.isinf(got)]))
+
+
 @pytest.mark.parametrize("M,N", [(3, 200), (40, 70)])
 def test_product_without_a_product(M, N):
     """K = 0 or alpha = 0: C <- beta * C, operands not read."""
@@ -430,6 +454,39 @@ def test_same_bits_again_and_elsewhere():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(C, E), i
+
+
+def test_grouped_replayed_with_other_offsets():
+    """A captured grouped product reads offsets and rows at each replay; two streams' calls at once do not meet."""
+    rng = rng_of("replayed")
+    G, R, N, K, T = 8, 500, 260, 512, 90
+    A, SA, _, lda, ldsa = operand(rng, T, K, 1)
+    B, SB, _, ldb, ldsb = operand(rng, G * N, K, 1)
+    offsets, rows = torch.zeros(G + 1, dtype=I32, device="cuda"), torch.zeros(R, dtype=I32, device="cuda")
+    C, D, E = (torch.empty(R, N, device="cuda") for _ in range(3))
+
+    def call(out):
+        dg.gemm_grouped_e4m3_f32acc(1, G, R, N, K, 1.0, A, T, lda, SA, ldsa, rows, B, ldb, N * ldb, SB, G * N, N, offsets, 0.0, out, N)
+
+    call(C)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(D)
+    side = torch.cuda.Stream()
+    for i, counts in enumerate(([R] + [0] * 7, [0] * 7 + [R], [1, 0, 130, 64, 65, 0, 200, 40], [62, 63] * 4)):
+        offsets[1:] = torch.tensor(np.cumsum(counts), dtype=I32)
+        rows.copy_(torch.from_numpy(rng.integers(0, T, R).astype(np.int32)))
+        side.wait_stream(torch.cuda.current_stream())
+        for out in (C, D, E):
+            out.fill_(7.0)
+        side.wait_stream(torch.cuda.current_stream())
+        call(C)
+        with torch.cuda.stream(side):
+            call(E)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert not torch.any(torch.isnan(C)) and torch.equal(C, D) and torch.equal(C, E), i
+        assert torch.all(C[sum(counts):] == 7.0)
 
 
 def test_linear_layer_and_update():

@@ -161,6 +161,38 @@ def test_sizes_of_numbers():
     assert off(got[0], ref) <= tol and np.array_equal(got[0], got[4])
 
 
+@pytest.mark.parametrize("M,N", [(150, 200), (300, 140)])
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_sizes_of_numbers_in_larger_updates(t, M, N):
+    """test_sizes_of_numbers where a member takes many workgroups, with a workspace full of NaN."""
+    rng = rng_of("larger range", M)
+    g = gradient(rng, M, N)
+    tol = tolerance(g, FAST)
+    dt = torch.float32 if t == "f32" else torch.bfloat16
+    for scale in (1e-30, 1e36):
+        G = torch.from_numpy(g * scale).cuda().to(dt)[None]
+        got = run(G, FAST, t=t)[0]
+        assert off(got, oracle(G[0].cpu().double().numpy() / scale, FAST)) <= tol, scale
+    G = torch.from_numpy(np.stack([g, g, g, g * 0, g])).cuda().to(dt)
+    G[1, 3, 5], G[2, M - 1, N - 1] = float("nan"), float("inf")
+    O = torch.empty(5, M, N, dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((dg.orthogonalise_workspace(M, N, 5),), 0xFF, dtype=torch.uint8, device="cuda")
+    getattr(dg, f"orthogonalise_{t}")(M, N, FAST, 1.0, G, N, M * N, O, N, M * N, 5, workspace=ws)
+    got = O.cpu().double().numpy()
+    assert np.all(np.isnan(got[1])) and np.all(np.isnan(got[2])) and np.all(got[3] == 0)
+    assert np.array_equal(got[0], got[4]) and np.array_equal(got[0], run(G[:1], FAST, t=t)[0])
+
+
+def test_one_gradient_for_all_members():
+    """Members a stride of 0 apart: the same G for each."""
+    for M, N in ((40, 60), (140, 150)):
+        G = torch.from_numpy(gradient(rng_of("shared", M), M, N)).cuda().float()
+        O = torch.empty(3, M, N, dtype=torch.bfloat16, device="cuda")
+        dg.orthogonalise_f32(M, N, FAST, 1.0, G, N, 0, O, N, M * N, 3)
+        got = O.cpu().double().numpy()
+        assert all(np.array_equal(got[i], run(G[None], FAST)[0]) for i in range(3))
+
+
 def test_singular_values():
     """What it is for: singular values near 1, singular vectors kept, the sign of every direction too."""
     rng = rng_of("values")

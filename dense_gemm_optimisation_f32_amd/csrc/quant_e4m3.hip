@@ -14,6 +14,8 @@
 #include "stage16.h"
 #include "wave.h"
 
+#include <type_traits>
+
 namespace mi355gemm {
 namespace {
 
@@ -114,12 +116,128 @@ __device__ __forceinline__ unsigned row16_max(unsigned v)
     return v;
 }
 
-// A workgroup takes a tile of X as it is stored: thread t holds 8 columns (8 (t % W) ..) of 8 consecutive rows (8 (t /
-// W) ..).  Where scales belong to rows (neither TRANS nor SQUARE) the tile is WIDE, 32 rows of 512 columns (W = 64); else 128 x
-// 128 (W = 16).
-template <bool TRANS, bool SQUARE>
-constexpr int kWide = !TRANS && !SQUARE ? 64 : 16;
+// Eight values of a row as they are stored.
+template <class T>
+struct Row8 {
+    static constexpr int PER = 4 / sizeof(T);   // values a word
+    unsigned w[8 / PER];
+};
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
+template <class T, bool VEC>
+__device__ __forceinline__ Row8<T> load8(const T *row, int c, int cols)
+{
+    Row8<T> v;
+    if (VEC && c + 8 <= cols) {
+#pragma unroll
+        for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
+            const u32x4 x = reinterpret_cast<const u32x4_g *>(row + c)[h];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v.w[4 * h + e] = x[e];
+        }
+        return v;
+    }
+    typedef std::conditional_t<sizeof(T) == 4, unsigned, uint16_t> Bits;
+    const Bits *b = reinterpret_cast<const Bits *>(row);
+#pragma unroll
+    for (int i = 0; i < 8 / Row8<T>::PER; ++i) {
+        v.w[i] = c + i * Row8<T>::PER < cols ? b[c + i * Row8<T>::PER] : 0u;
+        if constexpr (sizeof(T) == 2)
+            if (c + 2 * i + 1 < cols) v.w[i] |= (unsigned)b[c + 2 * i + 1] << 16;
+    }
+    return v;
+}
+// The largest magnitude's bits as fp32 (16-bit values are compared as they are, two at a time).
+template <class T>
+__device__ __forceinline__ unsigned top8(const Row8<T> &v)
+{
+    if constexpr (sizeof(T) == 4) {
+        unsigned t = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const unsigned m = v.w[e] & 0x7FFFFFFFu;
+            t = m > t ? m : t;
+        }
+        return t;
+    } else {
+        u16x2 t = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t = __builtin_elementwise_max(t, __builtin_bit_cast(u16x2, v.w[e] & 0x7FFF7FFFu));
+        const unsigned short a = t.x, b = t.y, m = a > b ? a : b;
+        return __builtin_bit_cast(unsigned, to_f32(__builtin_bit_cast(T, m)));
+    }
+}
+// Infinities and NaN become NaN, or zeros.
+template <class T>
+__device__ __forceinline__ Row8<T> replaced(Row8<T> v, bool zeros)
+{
+    constexpr unsigned MASK = sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFFu;
+    const T inf = (T)__builtin_inff();
+    unsigned least;
+    if constexpr (sizeof(T) == 4)
+        least = __builtin_bit_cast(unsigned, inf);
+    else
+        least = __builtin_bit_cast(uint16_t, inf);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int shift = sizeof(T) == 4 ? 0 : 16 * (e & 1);
+        unsigned &w = v.w[e / Row8<T>::PER];
+        if (((w >> shift) & MASK) >= least) w = zeros ? w & ~(MASK << shift) : w | (MASK << shift);
+    }
+    return v;
+}
+template <class T>
+__device__ __forceinline__ float value(const Row8<T> &v, int e)
+{
+    if constexpr (sizeof(T) == 4)
+        return __builtin_bit_cast(float, v.w[e]);
+    else
+        return to_f32(__builtin_bit_cast(T, (uint16_t)(v.w[e / 2] >> (16 * (e & 1)))));
+}
+
+// Scales of single rows of X as it is stored: a wave takes 8 rows of 512 columns, 1 KB of a 16-bit row at a time, and 16
+// lanes a block.  Values stay as they are stored until their scale is known.
+constexpr int kRowsR = 32, kRowsC = 512;
+template <class T, bool VEC>
+__global__ __launch_bounds__(256) void rows_kernel(QuantArgs p)
+{
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int tiles = p.tiles_r * p.tiles_c;
+    const int z = blockIdx.x / tiles, tile = blockIdx.x % tiles;
+    const int r0 = tile / p.tiles_c * kRowsR + 8 * (tid >> 6), c0 = tile % p.tiles_c * kRowsC + 8 * lane;
+    const T *X = reinterpret_cast<const T *>(p.X) + z * p.strideX;
+    uint8_t *Q = p.Q + z * p.strideQ;
+    Row8<T> v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        // (rows past the last are read from it)
+        const int r = r0 + i < p.rows ? r0 + i : p.rows - 1;
+        v[i] = load8<T, VEC>(X + r * p.ldx, c0, p.cols);
+    }
+    unsigned mine = 0;   // lane i of each 16: the exponent bits of row i's scale
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        unsigned top = row16_max(top8(v[i]));
+        if (top >= kInfinity) {   // infinities and NaN do not count, and become NaN
+            top = row16_max(top8(replaced(v[i], true)));
+            v[i] = replaced(v[i], false);
+        }
+        const unsigned ex = scale_exponent(top);
+        mine = (lane & 15) == i ? ex : mine;
+        const float inv = __builtin_bit_cast(float, (254u - ex) << 23);   // y / s = y * 2^-(ex - 127)
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = value(v[i], e) * inv;
+        const u32x2 q = {to_e4m3(y[0], y[1], y[2], y[3]), to_e4m3(y[4], y[5], y[6], y[7])};
+        if (r0 + i < p.rows) store8_e4m3(Q + (r0 + i) * p.ldq + c0, q, p.cols - c0, VEC);
+    }
+    const int i = lane & 15;
+    if (i < 8 && r0 + i < p.rows && c0 - 8 * i < p.cols)
+        p.S[z * p.strideS + c0 / 128 * p.lds + r0 + i] = __builtin_bit_cast(float, mine << 23);
+}
+
+// A workgroup takes a 128 x 128 tile of X as it is stored: thread t holds 8 columns (8 (t % 16) ..) of 8 consecutive rows (8 (t /
+// 16) ..).  For scales of single rows of X^T (TRANS) or of 128 rows (SQUARE).
 template <class T, bool TRANS, bool SQUARE, bool VEC>
 __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
 {
@@ -129,8 +247,8 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
     const int tiles = p.tiles_r * p.tiles_c;
     const int z = blockIdx.x / tiles, tile = blockIdx.x % tiles;
     const int tr = tile / p.tiles_c, tc = tile % p.tiles_c;
-    constexpr int W = kWide<TRANS, SQUARE>;
-    const int r0 = tr * (2048 / W) + 8 * (tid / W), c0 = tc * (8 * W) + 8 * (tid % W);
+    static_assert(TRANS || SQUARE, "scales of single rows are rows_kernel's");
+    const int r0 = tr * 128 + 8 * (tid >> 4), c0 = tc * 128 + 8 * (tid & 15);
     const T *X = reinterpret_cast<const T *>(p.X) + z * p.strideX;
 
     float y[8][8];
@@ -144,7 +262,7 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
         }
     }
 
-    // exponent bits of the scales: of row i, of column e (TRANS), or of the tile (SQUARE)
+    // exponent bits of the scales: of column e, or of the tile (SQUARE)
     unsigned ex[8];
     auto tops = [&](auto counted) __attribute__((always_inline)) {
         unsigned top[8];
@@ -155,7 +273,7 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const unsigned m = counted(magnitude(y[i][e]));
-                unsigned &t = top[SQUARE ? 0 : TRANS ? e : i];
+                unsigned &t = top[SQUARE ? 0 : e];
                 t = m > t ? m : t;
             }
         if constexpr (SQUARE) {
@@ -168,7 +286,7 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
             for (int k = 1; k < 4; ++k) all = part[k] > all ? part[k] : all;
 #pragma unroll
             for (int i = 0; i < 8; ++i) top[i] = all;
-        } else if constexpr (TRANS) {
+        } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 unsigned o = (unsigned)__shfl_xor((int)top[e], 16);
@@ -188,9 +306,6 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
                     const unsigned o = part[k * 128 + 8 * (tid & 15) + e];
                     top[e] = o > top[e] ? o : top[e];
                 }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top[i] = row16_max(top[i]);
         }
         bool finite = true;
 #pragma unroll
@@ -226,17 +341,7 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
             const u32x2 q = {to_e4m3(v[0], v[1], v[2], v[3]), to_e4m3(v[4], v[5], v[6], v[7])};
             if (r0 + i < p.rows) store8_e4m3(Q + (long long)(r0 + i) * p.ldq + c0, q, p.cols - c0, VEC);
         }
-        if constexpr (SQUARE) {
-            if (tid == 0) S[(long long)tc * p.lds + tr] = __builtin_bit_cast(float, ex[0] << 23);
-        } else {
-            // lane i of each 16 has row i's
-            const int i = tid & 15;
-            unsigned mine = ex[0];
-#pragma unroll
-            for (int k = 1; k < 8; ++k) mine = i == k ? ex[k] : mine;
-            if (i < 8 && r0 + i < p.rows && c0 - 8 * i < p.cols)
-                S[(long long)(c0 / 128) * p.lds + r0 + i] = __builtin_bit_cast(float, mine << 23);
-        }
+        if (tid == 0) S[(long long)tc * p.lds + tr] = __builtin_bit_cast(float, ex[0] << 23);
     } else {
         // Q's rows are X's columns: eight k of one row of Q per thread, 128 rows of 128 bytes
         // through LDS, 8-byte piece j of row m at piece j ^ (m % 16)
@@ -267,6 +372,16 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
     }
 }
 
+template <class T>
+hipError_t launch_rows(const QuantArgs &a, unsigned blocks, bool vec, hipStream_t stream)
+{
+    if (vec)
+        hipLaunchKernelGGL((rows_kernel<T, true>), dim3(blocks), dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((rows_kernel<T, false>), dim3(blocks), dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
 template <class T, bool TRANS, bool SQUARE>
 hipError_t launch(const QuantArgs &a, unsigned blocks, bool vec, hipStream_t stream)
 {
@@ -283,17 +398,17 @@ hipError_t launch_type(const QuantProblem &q, const QuantArgs &a, unsigned block
     const bool vec = reinterpret_cast<uintptr_t>(q.X) % 4 == 0 && q.ldx * sizeof(T) % 4 == 0 && q.strideX * sizeof(T) % 4 == 0 &&
                      reinterpret_cast<uintptr_t>(q.Q) % 4 == 0 && q.ldq % 4 == 0 && q.strideQ % 4 == 0;
     if (q.transpose) return q.block == 1 ? launch<T, true, false>(a, blocks, vec, stream) : launch<T, true, true>(a, blocks, vec, stream);
-    return q.block == 1 ? launch<T, false, false>(a, blocks, vec, stream) : launch<T, false, true>(a, blocks, vec, stream);
+    return q.block == 1 ? launch_rows<T>(a, blocks, vec, stream) : launch<T, false, true>(a, blocks, vec, stream);
 }
 
 // Rows and columns of X, as stored, that a workgroup takes.
 int tile_rows(const QuantProblem &p)
 {
-    return !p.transpose && p.block == 1 ? 2048 / kWide<false, false> : 128;
+    return !p.transpose && p.block == 1 ? kRowsR : 128;
 }
 int tile_cols(const QuantProblem &p)
 {
-    return !p.transpose && p.block == 1 ? 8 * kWide<false, false> : 128;
+    return !p.transpose && p.block == 1 ? kRowsC : 128;
 }
 long long quant_tiles(const QuantProblem &p)
 {

@@ -45,37 +45,6 @@ __device__ __forceinline__ float to_f32(__bf16 v)
     return __builtin_bit_cast(float, (unsigned)__builtin_bit_cast(uint16_t, v) << 16);
 }
 
-// Eight values from column c of a row as fp32; columns at or past `cols` are zero.
-// VEC: the row starts at a dword, so eight values inside it are one or two 16-byte loads.
-template <class T, bool VEC>
-__device__ __forceinline__ void load8_f32(const T *row, int c, int cols, float *y)
-{
-    if (VEC && c + 8 <= cols) {
-        if constexpr (sizeof(T) == 4) {
-            const f32x4_t a = *reinterpret_cast<const f32x4_g *>(row + c), b = *reinterpret_cast<const f32x4_g *>(row + c + 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                y[e] = a[e];
-                y[e + 4] = b[e];
-            }
-        } else {
-            const u32x4 a = *reinterpret_cast<const u32x4_g *>(row + c);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                y[2 * e] = to_f32(__builtin_bit_cast(T, (uint16_t)a[e]));
-                y[2 * e + 1] = to_f32(__builtin_bit_cast(T, (uint16_t)(a[e] >> 16)));
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = c + e < cols ? to_f32(row[c + e]) : 0.f;
-}
-
-__device__ __forceinline__ unsigned magnitude(float v)
-{
-    return __builtin_bit_cast(unsigned, v) & 0x7FFFFFFFu;
-}
 constexpr unsigned kInfinity = 0x7F800000u;
 
 // The exponent bits of the block's scale from the bits of its largest magnitude
@@ -147,25 +116,35 @@ __device__ __forceinline__ Row8<T> load8(const T *row, int c, int cols)
     }
     return v;
 }
-// The largest magnitude's bits as fp32 (16-bit values are compared as they are, two at a time).
+// Magnitudes of a word's values, and the larger of each: 16-bit values are compared as they are, two at a time.
 template <class T>
-__device__ __forceinline__ unsigned top8(const Row8<T> &v)
+constexpr unsigned kMagnitudes = sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+template <class T>
+__device__ __forceinline__ unsigned larger(unsigned a, unsigned b)
 {
-    if constexpr (sizeof(T) == 4) {
-        unsigned t = 0;
+    if constexpr (sizeof(T) == 4)
+        return a > b ? a : b;
+    else
+        return __builtin_bit_cast(unsigned, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+// A magnitude's bits as fp32, from those of value e of the words.
+template <class T>
+__device__ __forceinline__ unsigned as_f32(const unsigned *w, int e)
+{
+    if constexpr (sizeof(T) == 4)
+        return w[e];
+    else
+        return __builtin_bit_cast(unsigned, to_f32(__builtin_bit_cast(T, (uint16_t)(w[e / 2] >> (16 * (e & 1))))));
+}
+// The largest of the words' magnitudes, as fp32.
+template <class T>
+__device__ __forceinline__ unsigned largest(const unsigned *w)
+{
+    unsigned t = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const unsigned m = v.w[e] & 0x7FFFFFFFu;
-            t = m > t ? m : t;
-        }
-        return t;
-    } else {
-        u16x2 t = {0, 0};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t = __builtin_elementwise_max(t, __builtin_bit_cast(u16x2, v.w[e] & 0x7FFF7FFFu));
-        const unsigned short a = t.x, b = t.y, m = a > b ? a : b;
-        return __builtin_bit_cast(unsigned, to_f32(__builtin_bit_cast(T, m)));
-    }
+    for (int e = 0; e < 8 / Row8<T>::PER; ++e) t = larger<T>(t, w[e] & kMagnitudes<T>);
+    if constexpr (sizeof(T) == 2) t = larger<T>(t, t >> 16);
+    return as_f32<T>(&t, 0);
 }
 // Infinities and NaN become NaN, or zeros.
 template <class T>
@@ -217,9 +196,9 @@ __global__ __launch_bounds__(256) void rows_kernel(QuantArgs p)
     unsigned mine = 0;   // lane i of each 16: the exponent bits of row i's scale
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        unsigned top = row16_max(top8(v[i]));
+        unsigned top = row16_max(largest<T>(v[i].w));
         if (top >= kInfinity) {   // infinities and NaN do not count, and become NaN
-            top = row16_max(top8(replaced(v[i], true)));
+            top = row16_max(largest<T>(replaced(v[i], true).w));
             v[i] = replaced(v[i], false);
         }
         const unsigned ex = scale_exponent(top);
@@ -241,7 +220,7 @@ __global__ __launch_bounds__(256) void rows_kernel(QuantArgs p)
 template <class T, bool TRANS, bool SQUARE, bool VEC>
 __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
 {
-    __shared__ unsigned part[TRANS && !SQUARE ? 4 * 128 : 4];
+    __shared__ unsigned part[SQUARE ? 4 : 4 * 16 * 8 / Row8<T>::PER];
     __shared__ __attribute__((aligned(16))) unsigned char turned[TRANS ? 128 * 128 : 16];
     const int tid = threadIdx.x, wave = tid >> 6;
     const int tiles = p.tiles_r * p.tiles_c;
@@ -251,94 +230,82 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
     const int r0 = tr * 128 + 8 * (tid >> 4), c0 = tc * 128 + 8 * (tid & 15);
     const T *X = reinterpret_cast<const T *>(p.X) + z * p.strideX;
 
-    float y[8][8];
+    constexpr int WORDS = 8 / Row8<T>::PER;
+    Row8<T> v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (r0 + i < p.rows) {
-            load8_f32<T, VEC>(X + (long long)(r0 + i) * p.ldx, c0, p.cols, y[i]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[i][e] = 0.f;
-        }
+        // (rows past the last are read from it)
+        const int r = r0 + i < p.rows ? r0 + i : p.rows - 1;
+        v[i] = load8<T, VEC>(X + r * p.ldx, c0, p.cols);
     }
 
     // exponent bits of the scales: of column e, or of the tile (SQUARE)
     unsigned ex[8];
     auto tops = [&](auto counted) __attribute__((always_inline)) {
-        unsigned top[8];
+        unsigned top[WORDS];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top[i] = 0u;
+        for (int w = 0; w < WORDS; ++w) top[w] = 0u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i) {
+            const Row8<T> c = counted(v[i]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const unsigned m = counted(magnitude(y[i][e]));
-                unsigned &t = top[SQUARE ? 0 : e];
-                t = m > t ? m : t;
-            }
+            for (int w = 0; w < WORDS; ++w) top[w] = larger<T>(top[w], c.w[w] & kMagnitudes<T>);
+        }
+        bool finite = true;
+        __syncthreads();
         if constexpr (SQUARE) {
-            const unsigned w = wave_max(top[0]);
-            __syncthreads();
+            const unsigned w = wave_max(largest<T>(top));
             if ((tid & 63) == 0) part[wave] = w;
             __syncthreads();
             unsigned all = part[0];
 #pragma unroll
             for (int k = 1; k < 4; ++k) all = part[k] > all ? part[k] : all;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top[i] = all;
+            finite = all < kInfinity;
+            ex[0] = scale_exponent(all);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                unsigned o = (unsigned)__shfl_xor((int)top[e], 16);
-                top[e] = o > top[e] ? o : top[e];
-                o = (unsigned)__shfl_xor((int)top[e], 32);
-                top[e] = o > top[e] ? o : top[e];
+            for (int w = 0; w < WORDS; ++w) {
+                top[w] = larger<T>(top[w], (unsigned)__shfl_xor((int)top[w], 16));
+                top[w] = larger<T>(top[w], (unsigned)__shfl_xor((int)top[w], 32));
             }
-            __syncthreads();
             if ((tid & 63) < 16)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) part[wave * 128 + 8 * (tid & 15) + e] = top[e];
+                for (int w = 0; w < WORDS; ++w) part[(wave * 16 + (tid & 15)) * WORDS + w] = top[w];
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int w = 0; w < WORDS; ++w)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const unsigned o = part[k * 128 + 8 * (tid & 15) + e];
-                    top[e] = o > top[e] ? o : top[e];
-                }
-        }
-        bool finite = true;
+                for (int k = 0; k < 4; ++k) top[w] = larger<T>(top[w], part[(k * 16 + (tid & 15)) * WORDS + w]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            finite = finite && top[i] < kInfinity;
-            ex[i] = scale_exponent(top[i]);
+            for (int e = 0; e < 8; ++e) {
+                const unsigned t = as_f32<T>(top, e);
+                finite = finite && t < kInfinity;
+                ex[e] = scale_exponent(t);
+            }
         }
         return finite;
     };
-    const bool finite = tops([](unsigned m) { return m; });
+    const bool finite = tops([](const Row8<T> &c) { return c; });
     if (__syncthreads_or(!finite)) {
         // infinities and NaN do not count, and become NaN
-        tops([](unsigned m) { return m < kInfinity ? m : 0u; });
+        tops([](const Row8<T> &c) { return replaced(c, true); });
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (magnitude(y[i][e]) >= kInfinity) y[i][e] = __builtin_nanf("");
+        for (int i = 0; i < 8; ++i) v[i] = replaced(v[i], false);
     }
     // y / s = y * 2^-(ex - 127)
-    float inv[8];
+    float inv[SQUARE ? 1 : 8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) inv[i] = __builtin_bit_cast(float, (254u - ex[i]) << 23);
+    for (int e = 0; e < (SQUARE ? 1 : 8); ++e) inv[e] = __builtin_bit_cast(float, (254u - ex[e]) << 23);
 
     uint8_t *Q = p.Q + z * p.strideQ;
     float *S = p.S + z * p.strideS;
     if constexpr (!TRANS) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float v[8];
+            float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = y[i][e] * inv[i];
-            const u32x2 q = {to_e4m3(v[0], v[1], v[2], v[3]), to_e4m3(v[4], v[5], v[6], v[7])};
+            for (int e = 0; e < 8; ++e) y[e] = value(v[i], e) * inv[0];
+            const u32x2 q = {to_e4m3(y[0], y[1], y[2], y[3]), to_e4m3(y[4], y[5], y[6], y[7])};
             if (r0 + i < p.rows) store8_e4m3(Q + (long long)(r0 + i) * p.ldq + c0, q, p.cols - c0, VEC);
         }
         if (tid == 0) S[(long long)tc * p.lds + tr] = __builtin_bit_cast(float, ex[0] << 23);
@@ -347,10 +314,10 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
         // through LDS, 8-byte piece j of row m at piece j ^ (m % 16)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float v[8];
+            float y[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = y[i][e] * inv[SQUARE ? 0 : e];
-            const u32x2 q = {to_e4m3(v[0], v[1], v[2], v[3]), to_e4m3(v[4], v[5], v[6], v[7])};
+            for (int i = 0; i < 8; ++i) y[i] = value(v[i], e) * inv[SQUARE ? 0 : e];
+            const u32x2 q = {to_e4m3(y[0], y[1], y[2], y[3]), to_e4m3(y[4], y[5], y[6], y[7])};
             const int m = 8 * (tid & 15) + e, j = tid >> 4;
             *reinterpret_cast<u32x2 *>(turned + m * 128 + 8 * (j ^ ((m >> 3) & 15))) = q;
         }

@@ -41,7 +41,7 @@ int quant(int transpose, int block, int M, int K, const void *X, int ldx, long l
     p.Q = Q; p.ldq = ldq; p.strideQ = strideQ;
     p.S = S; p.lds = lds; p.strideS = strideS;
     p.batch = batch_count;
-    if (!mi355gemm::quant_fits(p)) return GEMM_ERR_SIZE;
+    if (!mi355gemm::quant_fits(p, type)) return GEMM_ERR_SIZE;
     if (!X || !Q || !S) return GEMM_ERR_NULL;
     if (misaligned(X, type == mi355gemm::QuantType::f32 ? 4 : 2) || misaligned(S, 4)) return GEMM_ERR_ALIGN;
     return launched(mi355gemm::launch_quant(p, type, stream));

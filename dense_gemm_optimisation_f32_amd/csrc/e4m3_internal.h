@@ -23,7 +23,7 @@ struct QuantProblem {
     long long lds, strideS;
     int batch;
 };
-bool quant_fits(const QuantProblem &p);
+bool quant_fits(const QuantProblem &p, QuantType type);
 hipError_t launch_quant(const QuantProblem &p, QuantType type, hipStream_t stream);
 
 // C[r,:] = alpha * A[rows[r],:] B_g^T + beta * C[r,:] for offsets[g] <= r < offsets[g+1], the

@@ -215,25 +215,30 @@ __global__ __launch_bounds__(256) void rows_kernel(QuantArgs p)
         p.S[z * p.strideS + c0 / 128 * p.lds + r0 + i] = __builtin_bit_cast(float, mine << 23);
 }
 
-// A workgroup takes a 128 x 128 tile of X as it is stored: thread t holds 8 columns (8 (t % 16) ..) of 8 consecutive rows (8 (t /
+// A workgroup takes a 128 x 128 tile of X as it is stored: thread t holds 8 columns (8 (t % 16) ..) of R consecutive rows (R (t /
 // 16) ..).  For scales of single rows of X^T (TRANS) or of 128 rows (SQUARE).
+template <class T>
+constexpr int kTileR = sizeof(T) == 4 ? 4 : 8;
+template <class T>
+constexpr int kTileThreads = 16 * 128 / kTileR<T>;
+
 template <class T, bool TRANS, bool SQUARE, bool VEC>
-__global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
+__global__ __launch_bounds__(kTileThreads<T>) void quant_kernel(QuantArgs p)
 {
-    __shared__ unsigned part[SQUARE ? 4 : 4 * 16 * 8 / Row8<T>::PER];
+    constexpr int R = kTileR<T>, NW = kTileThreads<T> / 64, WORDS = 8 / Row8<T>::PER;
+    __shared__ unsigned part[SQUARE ? NW : NW * 16 * WORDS];
     __shared__ __attribute__((aligned(16))) unsigned char turned[TRANS ? 128 * 128 : 16];
     const int tid = threadIdx.x, wave = tid >> 6;
     const int tiles = p.tiles_r * p.tiles_c;
     const int z = blockIdx.x / tiles, tile = blockIdx.x % tiles;
     const int tr = tile / p.tiles_c, tc = tile % p.tiles_c;
     static_assert(TRANS || SQUARE, "scales of single rows are rows_kernel's");
-    const int r0 = tr * 128 + 8 * (tid >> 4), c0 = tc * 128 + 8 * (tid & 15);
+    const int r0 = tr * 128 + R * (tid >> 4), c0 = tc * 128 + 8 * (tid & 15);
     const T *X = reinterpret_cast<const T *>(p.X) + z * p.strideX;
 
-    constexpr int WORDS = 8 / Row8<T>::PER;
-    Row8<T> v[8];
+    Row8<T> v[R];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < R; ++i) {
         // (rows past the last are read from it)
         const int r = r0 + i < p.rows ? r0 + i : p.rows - 1;
         v[i] = load8<T, VEC>(X + r * p.ldx, c0, p.cols);
@@ -246,7 +251,7 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
 #pragma unroll
         for (int w = 0; w < WORDS; ++w) top[w] = 0u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < R; ++i) {
             const Row8<T> c = counted(v[i]);
 #pragma unroll
             for (int w = 0; w < WORDS; ++w) top[w] = larger<T>(top[w], c.w[w] & kMagnitudes<T>);
@@ -259,7 +264,7 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
             __syncthreads();
             unsigned all = part[0];
 #pragma unroll
-            for (int k = 1; k < 4; ++k) all = part[k] > all ? part[k] : all;
+            for (int k = 1; k < NW; ++k) all = part[k] > all ? part[k] : all;
             finite = all < kInfinity;
             ex[0] = scale_exponent(all);
         } else {
@@ -275,7 +280,7 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
 #pragma unroll
             for (int w = 0; w < WORDS; ++w)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) top[w] = larger<T>(top[w], part[(k * 16 + (tid & 15)) * WORDS + w]);
+                for (int k = 0; k < NW; ++k) top[w] = larger<T>(top[w], part[(k * 16 + (tid & 15)) * WORDS + w]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const unsigned t = as_f32<T>(top, e);
@@ -290,7 +295,7 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
         // infinities and NaN do not count, and become NaN
         tops([](const Row8<T> &c) { return replaced(c, true); });
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = replaced(v[i], false);
+        for (int i = 0; i < R; ++i) v[i] = replaced(v[i], false);
     }
     // y / s = y * 2^-(ex - 127)
     float inv[SQUARE ? 1 : 8];
@@ -301,7 +306,7 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
     float *S = p.S + z * p.strideS;
     if constexpr (!TRANS) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < R; ++i) {
             float y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = value(v[i], e) * inv[0];
@@ -310,21 +315,22 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p)
         }
         if (tid == 0) S[(long long)tc * p.lds + tr] = __builtin_bit_cast(float, ex[0] << 23);
     } else {
-        // Q's rows are X's columns: eight k of one row of Q per thread, 128 rows of 128 bytes
-        // through LDS, 8-byte piece j of row m at piece j ^ (m % 16)
+        // Q's rows are X's columns: R k of one row of Q per thread, 128 rows of 128 bytes
+        // through LDS, 8-byte piece j of row m at piece j ^ (m / 8 % 16)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float y[8];
+            float y[R];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = value(v[i], e) * inv[SQUARE ? 0 : e];
-            const u32x2 q = {to_e4m3(y[0], y[1], y[2], y[3]), to_e4m3(y[4], y[5], y[6], y[7])};
-            const int m = 8 * (tid & 15) + e, j = tid >> 4;
-            *reinterpret_cast<u32x2 *>(turned + m * 128 + 8 * (j ^ ((m >> 3) & 15))) = q;
+            for (int i = 0; i < R; ++i) y[i] = value(v[i], e) * inv[SQUARE ? 0 : e];
+            const int m = 8 * (tid & 15) + e, k = R * (tid >> 4);
+            unsigned char *to = turned + m * 128 + 8 * ((k >> 3) ^ ((m >> 3) & 15)) + (k & 7);
+#pragma unroll
+            for (int i = 0; i < R; i += 4) *reinterpret_cast<unsigned *>(to + i) = to_e4m3(y[i], y[i + 1], y[i + 2], y[i + 3]);
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int m = 16 * i + (tid >> 4), j = tid & 15;
+        for (int i = 0; i < R; ++i) {
+            const int m = 128 / R * i + (tid >> 4), j = tid & 15;
             const u32x2 q = *reinterpret_cast<const u32x2 *>(turned + m * 128 + 8 * (j ^ ((m >> 3) & 15)));
             const int row = tc * 128 + m, k = tr * 128 + 8 * j;
             if (row < p.cols && k < p.rows) store8_e4m3(Q + (long long)row * p.ldq + k, q, p.rows - k, VEC);
@@ -353,9 +359,9 @@ template <class T, bool TRANS, bool SQUARE>
 hipError_t launch(const QuantArgs &a, unsigned blocks, bool vec, hipStream_t stream)
 {
     if (vec)
-        hipLaunchKernelGGL((quant_kernel<T, TRANS, SQUARE, true>), dim3(blocks), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((quant_kernel<T, TRANS, SQUARE, true>), dim3(blocks), dim3(kTileThreads<T>), 0, stream, a);
     else
-        hipLaunchKernelGGL((quant_kernel<T, TRANS, SQUARE, false>), dim3(blocks), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((quant_kernel<T, TRANS, SQUARE, false>), dim3(blocks), dim3(kTileThreads<T>), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -385,10 +391,11 @@ long long quant_tiles(const QuantProblem &p)
 
 }  // namespace
 
-bool quant_fits(const QuantProblem &p)
+bool quant_fits(const QuantProblem &p, QuantType type)
 {
     const long long tiles = quant_tiles(p);
-    return grid_holds(tiles, 256) && grid_holds(tiles * p.batch, 256);
+    const int threads = type == QuantType::f32 && tile_cols(p) == 128 ? kTileThreads<float> : 256;
+    return grid_holds(tiles, threads) && grid_holds(tiles * p.batch, threads);
 }
 
 hipError_t launch_quant(const QuantProblem &p, QuantType type, hipStream_t stream)

@@ -358,7 +358,7 @@ long long gemm_lora_workspace(int M, int N, int K, int rank);
  * A scale is the least power of two s with max|x| / s <= 448 over the block's finite values, at least 2^-126,
  * and 1 for a block of zeros; a value is x / s rounded to the nearest e4m3 value, ties to the even one (x / s itself
  * is not rounded).  Infinities and NaN become NaN and do not count for the scale.
- * M, K <= 2^30; fewer than 2^23 tiles of 128 x 128 over all members (32 x 512 with transpose = 0 and block 1).
+ * M, K <= 2^30; fewer than 2^23 tiles of 128 x 128 (2^22 in fp32) over all members, of 32 x 512 with transpose = 0 and block 1.
  */
 int quant_e4m3_f32(int transpose, int block, int M, int K, const float *X, int ldx, long long strideX,
                    uint8_t *Q, int ldq, long long strideQ, float *S, int lds, long long strideS,

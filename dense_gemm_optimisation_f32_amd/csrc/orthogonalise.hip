@@ -300,7 +300,8 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
     const char *Qb = reinterpret_cast<const char *>(Q + (K_OUT ? (long long)n0 : (long long)n0 * K));
     const long long stepQ = K_OUT ? (long long)BK * p.n * 2 : BK * 2;
     const int nk = K / BK;
-    auto issue = [&](int t, int slot) __attribute__((always_inline)) {
+    // loads `from` to `to` of slice t
+    auto issue_part = [&](int t, int slot, int from, int to) __attribute__((always_inline)) {
         if (!loader) return;
         const unsigned la = __builtin_amdgcn_readfirstlane(lds0 + slot * Cfg::A_BYTES + lw * A_LOADS * 1024);
         const unsigned lb = __builtin_amdgcn_readfirstlane(lds0 + S * Cfg::A_BYTES + slot * Cfg::B_BYTES + lw * B_LOADS * 1024);
@@ -308,22 +309,25 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
         const int at = t < nk ? t : nk - 1;
         const char *a = uniform(Pb + (long long)at * BK * 2), *b = uniform(Qb + at * stepQ);
 #pragma unroll
-        for (int i = 0; i < A_LOADS; ++i) dma16(a, offA[i], la + 1024 * i);
+        for (int i = 0; i < A_LOADS; ++i)
+            if (i >= from && i < to) dma16(a, offA[i], la + 1024 * i);
 #pragma unroll
-        for (int i = 0; i < B_LOADS; ++i) dma16(b, offB[i], lb + 1024 * i);
+        for (int i = 0; i < B_LOADS; ++i)
+            if (A_LOADS + i >= from && A_LOADS + i < to) dma16(b, offB[i], lb + 1024 * i);
     };
+    auto issue = [&](int t, int slot) __attribute__((always_inline)) { issue_part(t, slot, 0, LOADS); };
     const int wm = wave / Cfg::WN, wn = wave % Cfg::WN, lr = lane & 31, lk = lane >> 5;
     // What the epilogue reads (rows first + q RPI + er, columns c ..).  A wave of one block of 32 x 32 reads it here, ahead
     // of the K loop, which small matrices leave after a few microseconds.
-    constexpr int TN = Cfg::TN, LPR = TN / 4, RPI = 64 / LPR, NQ = 32 / RPI;
+    constexpr int TN = Cfg::TN, EP = TN % 64 == 0 ? 64 : 32, LPR = EP / 4, RPI = 64 / LPR, NQ = 32 / RPI;   // (EP columns at a time)
     constexpr bool EARLY = FM == 1 && FN == 1;
     float *x = of_member(p.x, p.ws_stride, z), *da = of_member(p.da, p.ws_stride, z), *db = of_member(p.db, p.ws_stride, z);
     _Float16 *a16 = of_member(p.a16, p.ws_stride, z), *b16 = of_member(p.b16, p.ws_stride, z);
-    const int er = lane / LPR, c = n0 + wn * TN + 4 * (lane % LPR);
+    const int er = lane / LPR, c0 = n0 + wn * TN + 4 * (lane % LPR);
     f32x4_t xs[NQ], dcs;
     half4 os[NQ];
     float drs[NQ];
-    auto read_epilogue = [&](int first) __attribute__((always_inline)) {
+    auto read_epilogue = [&](int first, int c) __attribute__((always_inline)) {
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
             const int r = first + q * RPI + er;
@@ -337,7 +341,7 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
         }
         if constexpr (KIND == kSquare) dcs = *reinterpret_cast<const f32x4_t *>(da + c);
     };
-    if constexpr (EARLY) read_epilogue(m0 + wm * Cfg::TM);   // (64 x 64 tiles lie within the padded sizes)
+    if constexpr (EARLY) read_epilogue(m0 + wm * Cfg::TM, c0);   // (64 x 64 tiles lie within the padded sizes)
     constexpr int NS = BK / 16;
     constexpr int NFB = K_OUT ? FN : NS;
     unsigned fragA[NS], fragB[NFB];
@@ -384,7 +388,9 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
     };
-    const bool late = Cfg::STAGGER && uwave >= Cfg::NW / 2;
+    // One wave a SIMD (SPREAD) has nobody to multiply while it issues loads: its loads go out a few at a time between products.
+    constexpr bool SPREAD = BM == 192;
+    const bool late = SPREAD || (Cfg::STAGGER && uwave >= Cfg::NW / 2);
     auto step = [&](int t, auto pending, auto refill, bool late_refill) __attribute__((always_inline)) {
         const int slot = t % S, next = (t + 1) % S, prev = (t - 1 + S) % S;
 #pragma unroll
@@ -392,7 +398,11 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
             const int cur = sub & 1, nxt = cur ^ 1;
             if (sub + 1 < NS) {
                 read(slot, sub + 1, fa[nxt], fb[nxt]);
-                if (Cfg::STAGGER && sub == NS - 2 && late && late_refill) issue(t - 1 + S, prev);
+                if (SPREAD) {
+                    if (late_refill) issue_part(t - 1 + S, prev, LOADS * sub / (NS - 1), LOADS * (sub + 1) / (NS - 1));
+                } else if (Cfg::STAGGER && sub == NS - 2 && late && late_refill) {
+                    issue(t - 1 + S, prev);
+                }
             } else {
                 wait_vmcnt<LOADS * decltype(pending)::value>();
                 __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's slice-t reads are done
@@ -428,9 +438,9 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
         }
     }
 
-    static_assert(Cfg::NW * 32 * TN * 4 <= S * Cfg::STAGE_BYTES, "staging area exceeds the ring");
+    static_assert(Cfg::NW * 32 * EP * 4 <= S * Cfg::STAGE_BYTES, "staging area exceeds the ring");
     static_assert(!EARLY || (BM == 64 && BN == 64), "early reads stay inside the padded matrices");
-    const unsigned stage = lds0 + wave * 32 * TN * 4;
+    const unsigned stage = lds0 + wave * 32 * EP * 4;
     wait_vmcnt<0>();   // (slices that a short K did not use)
     lds_barrier();
     _Float16 *x16 = of_member(p.x16_next, p.ws_stride, z);
@@ -438,18 +448,19 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
     // what also goes out by columns: a symmetric tile's mirror image, a tall result
     const bool turned = KIND == kApply ? p.last && p.tall : tm != tn;
     // chunk of the staged row: 16 bytes of columns 4 k.. at chunk k ^ (row % LPR)
-    auto chunk = [&](int r, int k) { return stage + r * TN * 4 + 16 * (k ^ (r & (LPR - 1))); };
+    auto chunk = [&](int r, int k) { return stage + r * EP * 4 + 16 * (k ^ (r & (LPR - 1))); };
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-        const int first = m0 + wm * Cfg::TM + 32 * i;
-        if (first >= p.m || n0 + wn * TN >= cols) break;   // (uniform; padded sizes are multiples of 64)
-        if constexpr (!EARLY) read_epilogue(first);
+    for (int part = 0; part < FM * (TN / EP); ++part) {
+        const int i = part / (TN / EP), jp = part % (TN / EP), first = m0 + wm * Cfg::TM + 32 * i, c = c0 + jp * EP;
+        if (first >= p.m || n0 + wn * TN + jp * EP >= cols) continue;   // (uniform; padded sizes are multiples of 64)
+        if constexpr (!EARLY) read_epilogue(first, c);
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
+        for (int j = 0; j < EP / 32; ++j)
 #pragma unroll
             for (int g = 0; g < 4; ++g)
                 *(lds_f32x4 *)(uintptr_t)chunk(lr, 8 * j + 2 * g + lk) =
-                    f32x4_t{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+                    f32x4_t{acc[i][jp * EP / 32 + j][4 * g], acc[i][jp * EP / 32 + j][4 * g + 1], acc[i][jp * EP / 32 + j][4 * g + 2],
+                            acc[i][jp * EP / 32 + j][4 * g + 3]};
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
@@ -503,10 +514,10 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         if (!turned) continue;
-        // by columns: lane l has 32 rows of column l (TN = 64), or 16 of column l % 32 (TN = 32)
+        // by columns: lane l has 32 rows of column l (EP = 64), or 16 of column l % 32 (EP = 32)
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        constexpr int HALF = TN == 64 ? 32 : 16;
-        const int cl = lane % TN, r0 = lane / TN * HALF, col = n0 + wn * TN + cl;
+        constexpr int HALF = EP / 2;
+        const int cl = lane % EP, r0 = lane / EP * HALF, col = n0 + wn * TN + jp * EP + cl;
         float t[HALF];
 #pragma unroll
         for (int e = 0; e < HALF; ++e) t[e] = *(const lds_float *)(uintptr_t)(chunk(r0 + e, cl >> 2) + 4 * (cl & 3));
@@ -539,6 +550,7 @@ hipError_t launch_tiles(const OrthoArgs &a, int batch, hipStream_t stream)
 }
 
 using Large = HgDmaCfg<256, 256, 2, 2, 4, 64>;
+using Wide = HgDmaCfg<192, 192, 3, 2, 2, 64>;     // symmetric products only
 using Middle = HgDmaCfg<128, 128, 4, 2, 4, 64>;
 using Small = HgDmaCfg<64, 64, 4, 2, 2, 64>;
 
@@ -546,7 +558,9 @@ template <Product KIND>
 hipError_t launch_product(const OrthoArgs &a, int batch, hipStream_t stream)
 {
     // Rounds of 256 workgroups, each with so long for a slice and for its start and end (us, measured on products of 512 x
-    // 512 to 4096 x 4096).  Two 64 x 64 tiles share a CU, so their rounds need not be whole.
+    // 512 to 4096 x 4096).  Two 64 x 64 tiles share a CU, so their rounds need not be whole.  (192 x 192 tiles fill a
+    // round with one triangle of 4224 rows: 4096 x 4096 1593 -> 1480 us an update, 4096 x 8192 2819 -> 2522, against 256 x 256 on
+    // 136 CUs.)
     auto time = [&](int side, double slice, double fixed, bool whole) {
         const double rows = (a.m + side - 1) / side, cols = (a.n + side - 1) / side;
         const double rounds = (KIND == kApply ? rows * cols : rows * (rows + 1) / 2) * batch / 256;
@@ -554,6 +568,10 @@ hipError_t launch_product(const OrthoArgs &a, int batch, hipStream_t stream)
         return (rounds <= 1 ? 1. : whole ? std::ceil(rounds) : rounds) * (slices * slice + fixed);
     };
     const double large = time(256, 1.4, 5, true), middle = time(128, 0.44, 4, true), small = time(64, 0.25, 1.4, false);
+    if constexpr (KIND != kApply) {
+        const double wide = time(192, 1.25, 5, true);
+        if (wide < large && wide < middle && wide < small) return launch_tiles<Wide, KIND>(a, batch, stream);
+    }
     if (large <= middle && large <= small) return launch_tiles<Large, KIND>(a, batch, stream);
     if (middle <= small) return launch_tiles<Middle, KIND>(a, batch, stream);
     return launch_tiles<Small, KIND>(a, batch, stream);

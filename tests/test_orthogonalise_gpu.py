@@ -255,6 +255,23 @@ def test_large():
     assert float(torch.linalg.norm(O.double() - ref) / torch.linalg.norm(ref)) <= tol
 
 
+@pytest.mark.parametrize("M,N", [(4100, 4170), (4040, 4000)])
+def test_largest_tiles(M, N):
+    """Updates whose products are tiles of 192 x 192 and 256 x 256, cut off at their ends."""
+    tol = tolerance(rng_of("large").standard_normal((1000, 1400)), FAST)     # (as in test_large)
+    g = torch.randn(M, N, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5))
+    O = torch.full((M + 1, N + 2), 9.0, dtype=torch.bfloat16, device="cuda")
+    dg.orthogonalise_f32(M, N, FAST, 1.0, g, N, 0, O, N + 2, 0)
+    x = (g if M < N else g.t()).double()
+    x = x / torch.linalg.norm(x)
+    for a, b, c in FAST:
+        s = x @ x.t()
+        x = a * x + b * (s @ x) + c * (s @ (s @ x))
+    ref = x if M < N else x.t()
+    assert torch.all(O[M:] == 9) and torch.all(O[:, N:] == 9)
+    assert float(torch.linalg.norm(O[:M, :N].double() - ref) / torch.linalg.norm(ref)) <= tol
+
+
 def test_expert_gradients():
     """The weight gradients of an expert layer, as the grouped product leaves them (all experts, one call), orthogonalised in one call."""
     G, R, D, F = 4, 300, 128, 192

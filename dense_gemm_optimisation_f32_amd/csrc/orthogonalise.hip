@@ -207,12 +207,12 @@ __global__ __launch_bounds__(256) void start_kernel(OrthoArgs p)
     }
 }
 
-enum Product { kGram, kSquare, kApply };
+constexpr int kGram = 0, kSquare = 1, kApply = 2;   // a step's products (below)
 
 // The tile a workgroup takes.  XCD by XCD (see tile_order.h; here within 32 bits, whose divisions are short): the
 // workgroups of one XCD take consecutive tiles, four tile rows at a time.  The symmetric products compute the tiles on and
 // above the diagonal alone, row by row; a workgroup also stores its tile's mirror image.
-template <Product KIND>
+template <int KIND>
 __device__ __forceinline__ void tile_of(unsigned rows, unsigned cols, int *member, int *tm, int *tn)
 {
     const unsigned each = KIND == kApply ? rows * cols : rows * (rows + 1) / 2;
@@ -269,7 +269,7 @@ __device__ __forceinline__ unsigned frag_offset_k(int first, int lane)
 //   kApply   X <- a X + B X       P Q   with P = B - diag(B), Q = X
 // The ring, its loads and its K loop are those of the whole-matrix kernel (hgemm_mfma.hip).  The epilogue passes 32 rows of
 // a wave's tile at a time through LDS: by rows, and by columns for what is stored transposed.
-template <class Cfg, Product KIND>
+template <class Cfg, int KIND>
 __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
 {
     constexpr int BM = Cfg::BM, BN = Cfg::BN, BK = 64, S = Cfg::STAGES, FM = Cfg::FM, FN = Cfg::FN;
@@ -540,7 +540,7 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
     }
 }
 
-template <class Cfg, Product KIND>
+template <class Cfg, int KIND>
 hipError_t launch_tiles(const OrthoArgs &a, int batch, hipStream_t stream)
 {
     const int rows = (a.m + Cfg::BM - 1) / Cfg::BM, cols = (a.n + Cfg::BN - 1) / Cfg::BN;
@@ -554,7 +554,7 @@ using Wide = HgDmaCfg<192, 192, 3, 2, 2, 64>;     // symmetric products only
 using Middle = HgDmaCfg<128, 128, 4, 2, 4, 64>;
 using Small = HgDmaCfg<64, 64, 4, 2, 2, 64>;
 
-template <Product KIND>
+template <int KIND>
 hipError_t launch_product(const OrthoArgs &a, int batch, hipStream_t stream)
 {
     // Rounds of 256 workgroups, each with so long for a slice and for its start and end (us, measured on products of 512 x

@@ -33,6 +33,10 @@ struct QuantArgs {
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x2_g __attribute__((ext_vector_type(2), aligned(4)));
 
+// The element types by number, for the kernels' names: QuantType's order.
+template <int TYPE>
+using Stored = std::conditional_t<TYPE == 0, float, std::conditional_t<TYPE == 1, _Float16, __bf16>>;
+
 template <class T>
 __device__ __forceinline__ float to_f32(T v);
 template <>
@@ -177,9 +181,10 @@ __device__ __forceinline__ float value(const Row8<T> &v, int e)
 // Scales of single rows of X as it is stored: a wave takes 8 rows of 512 columns, 1 KB of a 16-bit row at a time, and 16
 // lanes a block.  Values stay as they are stored until their scale is known.
 constexpr int kRowsR = 32, kRowsC = 512;
-template <class T, bool VEC>
+template <int TYPE, bool VEC>
 __global__ __launch_bounds__(256) void rows_kernel(QuantArgs p)
 {
+    typedef Stored<TYPE> T;
     const int tid = threadIdx.x, lane = tid & 63;
     const int tiles = p.tiles_r * p.tiles_c;
     const int z = blockIdx.x / tiles, tile = blockIdx.x % tiles;
@@ -222,9 +227,10 @@ constexpr int kTileR = sizeof(T) == 4 ? 4 : 8;
 template <class T>
 constexpr int kTileThreads = 16 * 128 / kTileR<T>;
 
-template <class T, bool TRANS, bool SQUARE, bool VEC>
-__global__ __launch_bounds__(kTileThreads<T>) void quant_kernel(QuantArgs p)
+template <int TYPE, bool TRANS, bool SQUARE, bool VEC>
+__global__ __launch_bounds__(kTileThreads<Stored<TYPE>>) void quant_kernel(QuantArgs p)
 {
+    typedef Stored<TYPE> T;
     constexpr int R = kTileR<T>, NW = kTileThreads<T> / 64, WORDS = 8 / Row8<T>::PER;
     __shared__ unsigned part[SQUARE ? NW : NW * 16 * WORDS];
     __shared__ __attribute__((aligned(16))) unsigned char turned[TRANS ? 128 * 128 : 16];
@@ -345,33 +351,33 @@ __global__ __launch_bounds__(kTileThreads<T>) void quant_kernel(QuantArgs p)
     }
 }
 
-template <class T>
+template <int TYPE>
 hipError_t launch_rows(const QuantArgs &a, unsigned blocks, bool vec, hipStream_t stream)
 {
     if (vec)
-        hipLaunchKernelGGL((rows_kernel<T, true>), dim3(blocks), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((rows_kernel<TYPE, true>), dim3(blocks), dim3(256), 0, stream, a);
     else
-        hipLaunchKernelGGL((rows_kernel<T, false>), dim3(blocks), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((rows_kernel<TYPE, false>), dim3(blocks), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
-template <class T, bool TRANS, bool SQUARE>
+template <int TYPE, bool TRANS, bool SQUARE>
 hipError_t launch(const QuantArgs &a, unsigned blocks, bool vec, hipStream_t stream)
 {
     if (vec)
-        hipLaunchKernelGGL((quant_kernel<T, TRANS, SQUARE, true>), dim3(blocks), dim3(kTileThreads<T>), 0, stream, a);
+        hipLaunchKernelGGL((quant_kernel<TYPE, TRANS, SQUARE, true>), dim3(blocks), dim3(kTileThreads<Stored<TYPE>>), 0, stream, a);
     else
-        hipLaunchKernelGGL((quant_kernel<T, TRANS, SQUARE, false>), dim3(blocks), dim3(kTileThreads<T>), 0, stream, a);
+        hipLaunchKernelGGL((quant_kernel<TYPE, TRANS, SQUARE, false>), dim3(blocks), dim3(kTileThreads<Stored<TYPE>>), 0, stream, a);
     return hipGetLastError();
 }
 
-template <class T>
+template <int TYPE>
 hipError_t launch_type(const QuantProblem &q, const QuantArgs &a, unsigned blocks, hipStream_t stream)
 {
-    const bool vec = reinterpret_cast<uintptr_t>(q.X) % 4 == 0 && q.ldx * sizeof(T) % 4 == 0 && q.strideX * sizeof(T) % 4 == 0 &&
+    const bool vec = reinterpret_cast<uintptr_t>(q.X) % 4 == 0 && q.ldx * sizeof(Stored<TYPE>) % 4 == 0 && q.strideX * sizeof(Stored<TYPE>) % 4 == 0 &&
                      reinterpret_cast<uintptr_t>(q.Q) % 4 == 0 && q.ldq % 4 == 0 && q.strideQ % 4 == 0;
-    if (q.transpose) return q.block == 1 ? launch<T, true, false>(a, blocks, vec, stream) : launch<T, true, true>(a, blocks, vec, stream);
-    return q.block == 1 ? launch_rows<T>(a, blocks, vec, stream) : launch<T, false, true>(a, blocks, vec, stream);
+    if (q.transpose) return q.block == 1 ? launch<TYPE, true, false>(a, blocks, vec, stream) : launch<TYPE, true, true>(a, blocks, vec, stream);
+    return q.block == 1 ? launch_rows<TYPE>(a, blocks, vec, stream) : launch<TYPE, false, true>(a, blocks, vec, stream);
 }
 
 // Rows and columns of X, as stored, that a workgroup takes.
@@ -410,9 +416,9 @@ hipError_t launch_quant(const QuantProblem &p, QuantType type, hipStream_t strea
     a.S = p.S; a.lds = p.lds; a.strideS = p.strideS;
     const unsigned blocks = (unsigned)(quant_tiles(p) * p.batch);
     switch (type) {
-    case QuantType::f32: return launch_type<float>(p, a, blocks, stream);
-    case QuantType::f16: return launch_type<_Float16>(p, a, blocks, stream);
-    default: return launch_type<__bf16>(p, a, blocks, stream);
+    case QuantType::f32: return launch_type<0>(p, a, blocks, stream);
+    case QuantType::f16: return launch_type<1>(p, a, blocks, stream);
+    default: return launch_type<2>(p, a, blocks, stream);
     }
 }
 

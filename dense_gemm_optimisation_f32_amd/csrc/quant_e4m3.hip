@@ -31,7 +31,9 @@ struct QuantArgs {
 };
 
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef unsigned int u32x2_g __attribute__((ext_vector_type(2), aligned(4)));
+// 16 and 8 bytes at any address that holds the elements: loads and stores of this target need no other alignment
+typedef unsigned int u32x4_h __attribute__((ext_vector_type(4), aligned(2)));
+typedef unsigned int u32x2_b __attribute__((ext_vector_type(2), aligned(1)));
 
 // The element types by number, for the kernels' names: QuantType's order.
 template <int TYPE>
@@ -67,10 +69,10 @@ __device__ __forceinline__ unsigned to_e4m3(float a, float b, float c, float d)
     return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
 }
 
-__device__ __forceinline__ void store8_e4m3(uint8_t *dst, u32x2 v, int valid, bool vec)
+__device__ __forceinline__ void store8_e4m3(uint8_t *dst, u32x2 v, int valid)
 {
-    if (vec && valid >= 8) {
-        *reinterpret_cast<u32x2_g *>(dst) = v;
+    if (valid >= 8) {
+        *reinterpret_cast<u32x2_b *>(dst) = v;
         return;
     }
 #pragma unroll
@@ -97,14 +99,15 @@ struct Row8 {
 };
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
-template <class T, bool VEC>
+// Eight values from column c on; columns at or past `cols` are zero.
+template <class T>
 __device__ __forceinline__ Row8<T> load8(const T *row, int c, int cols)
 {
     Row8<T> v;
-    if (VEC && c + 8 <= cols) {
+    if (c + 8 <= cols) {
 #pragma unroll
         for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
-            const u32x4 x = reinterpret_cast<const u32x4_g *>(row + c)[h];
+            const u32x4 x = reinterpret_cast<const u32x4_h *>(row + c)[h];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v.w[4 * h + e] = x[e];
         }
@@ -181,7 +184,7 @@ __device__ __forceinline__ float value(const Row8<T> &v, int e)
 // Scales of single rows of X as it is stored: a wave takes 8 rows of 512 columns, 1 KB of a 16-bit row at a time, and 16
 // lanes a block.  Values stay as they are stored until their scale is known.
 constexpr int kRowsR = 32, kRowsC = 512;
-template <int TYPE, bool VEC>
+template <int TYPE>
 __global__ __launch_bounds__(256) void rows_kernel(QuantArgs p)
 {
     typedef Stored<TYPE> T;
@@ -196,7 +199,7 @@ __global__ __launch_bounds__(256) void rows_kernel(QuantArgs p)
     for (int i = 0; i < 8; ++i) {
         // (rows past the last are read from it)
         const int r = r0 + i < p.rows ? r0 + i : p.rows - 1;
-        v[i] = load8<T, VEC>(X + r * p.ldx, c0, p.cols);
+        v[i] = load8<T>(X + r * p.ldx, c0, p.cols);
     }
     unsigned mine = 0;   // lane i of each 16: the exponent bits of row i's scale
 #pragma unroll
@@ -213,7 +216,7 @@ __global__ __launch_bounds__(256) void rows_kernel(QuantArgs p)
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = value(v[i], e) * inv;
         const u32x2 q = {to_e4m3(y[0], y[1], y[2], y[3]), to_e4m3(y[4], y[5], y[6], y[7])};
-        if (r0 + i < p.rows) store8_e4m3(Q + (r0 + i) * p.ldq + c0, q, p.cols - c0, VEC);
+        if (r0 + i < p.rows) store8_e4m3(Q + (r0 + i) * p.ldq + c0, q, p.cols - c0);
     }
     const int i = lane & 15;
     if (i < 8 && r0 + i < p.rows && c0 - 8 * i < p.cols)
@@ -227,7 +230,7 @@ constexpr int kTileR = sizeof(T) == 4 ? 4 : 8;
 template <class T>
 constexpr int kTileThreads = 16 * 128 / kTileR<T>;
 
-template <int TYPE, bool TRANS, bool SQUARE, bool VEC>
+template <int TYPE, bool TRANS, bool SQUARE>
 __global__ __launch_bounds__(kTileThreads<Stored<TYPE>>) void quant_kernel(QuantArgs p)
 {
     typedef Stored<TYPE> T;
@@ -247,7 +250,7 @@ __global__ __launch_bounds__(kTileThreads<Stored<TYPE>>) void quant_kernel(Quant
     for (int i = 0; i < R; ++i) {
         // (rows past the last are read from it)
         const int r = r0 + i < p.rows ? r0 + i : p.rows - 1;
-        v[i] = load8<T, VEC>(X + r * p.ldx, c0, p.cols);
+        v[i] = load8<T>(X + r * p.ldx, c0, p.cols);
     }
 
     // exponent bits of the scales: of column e, or of the tile (SQUARE)
@@ -317,7 +320,7 @@ __global__ __launch_bounds__(kTileThreads<Stored<TYPE>>) void quant_kernel(Quant
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = value(v[i], e) * inv[0];
             const u32x2 q = {to_e4m3(y[0], y[1], y[2], y[3]), to_e4m3(y[4], y[5], y[6], y[7])};
-            if (r0 + i < p.rows) store8_e4m3(Q + (long long)(r0 + i) * p.ldq + c0, q, p.cols - c0, VEC);
+            if (r0 + i < p.rows) store8_e4m3(Q + (long long)(r0 + i) * p.ldq + c0, q, p.cols - c0);
         }
         if (tid == 0) S[(long long)tc * p.lds + tr] = __builtin_bit_cast(float, ex[0] << 23);
     } else {
@@ -339,7 +342,7 @@ __global__ __launch_bounds__(kTileThreads<Stored<TYPE>>) void quant_kernel(Quant
             const int m = 128 / R * i + (tid >> 4), j = tid & 15;
             const u32x2 q = *reinterpret_cast<const u32x2 *>(turned + m * 128 + 8 * (j ^ ((m >> 3) & 15)));
             const int row = tc * 128 + m, k = tr * 128 + 8 * j;
-            if (row < p.cols && k < p.rows) store8_e4m3(Q + (long long)row * p.ldq + k, q, p.rows - k, VEC);
+            if (row < p.cols && k < p.rows) store8_e4m3(Q + (long long)row * p.ldq + k, q, p.rows - k);
         }
         if constexpr (SQUARE) {
             if (tid == 0) S[(long long)tr * p.lds + tc] = __builtin_bit_cast(float, ex[0] << 23);
@@ -351,33 +354,21 @@ __global__ __launch_bounds__(kTileThreads<Stored<TYPE>>) void quant_kernel(Quant
     }
 }
 
-template <int TYPE>
-hipError_t launch_rows(const QuantArgs &a, unsigned blocks, bool vec, hipStream_t stream)
-{
-    if (vec)
-        hipLaunchKernelGGL((rows_kernel<TYPE, true>), dim3(blocks), dim3(256), 0, stream, a);
-    else
-        hipLaunchKernelGGL((rows_kernel<TYPE, false>), dim3(blocks), dim3(256), 0, stream, a);
-    return hipGetLastError();
-}
-
 template <int TYPE, bool TRANS, bool SQUARE>
-hipError_t launch(const QuantArgs &a, unsigned blocks, bool vec, hipStream_t stream)
+hipError_t launch(const QuantArgs &a, unsigned blocks, hipStream_t stream)
 {
-    if (vec)
-        hipLaunchKernelGGL((quant_kernel<TYPE, TRANS, SQUARE, true>), dim3(blocks), dim3(kTileThreads<Stored<TYPE>>), 0, stream, a);
+    if constexpr (TRANS || SQUARE)
+        hipLaunchKernelGGL((quant_kernel<TYPE, TRANS, SQUARE>), dim3(blocks), dim3(kTileThreads<Stored<TYPE>>), 0, stream, a);
     else
-        hipLaunchKernelGGL((quant_kernel<TYPE, TRANS, SQUARE, false>), dim3(blocks), dim3(kTileThreads<Stored<TYPE>>), 0, stream, a);
+        hipLaunchKernelGGL(rows_kernel<TYPE>, dim3(blocks), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
 template <int TYPE>
 hipError_t launch_type(const QuantProblem &q, const QuantArgs &a, unsigned blocks, hipStream_t stream)
 {
-    const bool vec = reinterpret_cast<uintptr_t>(q.X) % 4 == 0 && q.ldx * sizeof(Stored<TYPE>) % 4 == 0 && q.strideX * sizeof(Stored<TYPE>) % 4 == 0 &&
-                     reinterpret_cast<uintptr_t>(q.Q) % 4 == 0 && q.ldq % 4 == 0 && q.strideQ % 4 == 0;
-    if (q.transpose) return q.block == 1 ? launch<TYPE, true, false>(a, blocks, vec, stream) : launch<TYPE, true, true>(a, blocks, vec, stream);
-    return q.block == 1 ? launch_rows<TYPE>(a, blocks, vec, stream) : launch<TYPE, false, true>(a, blocks, vec, stream);
+    if (q.transpose) return q.block == 1 ? launch<TYPE, true, false>(a, blocks, stream) : launch<TYPE, true, true>(a, blocks, stream);
+    return q.block == 1 ? launch<TYPE, false, false>(a, blocks, stream) : launch<TYPE, false, true>(a, blocks, stream);
 }
 
 // Rows and columns of X, as stored, that a workgroup takes.

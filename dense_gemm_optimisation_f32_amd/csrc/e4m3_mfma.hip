@@ -80,8 +80,9 @@ __device__ __forceinline__ u32x4 load16_any(const uint8_t *p, int valid)
 }
 
 // ---------------------------------------------------------------------------
-// The kernel for every shape, stride and alignment: a 64 x 64 tile of four waves of 32 x
-// 32, slices of 128 k through registers into a double-buffered LDS.
+// The kernel for what the others cannot address (rows 2^23 bytes apart and more, rows looked up in 4 GiB and more) and for
+// K = 0: a 64 x 64 tile of four waves of 32 x 32, slices of 128 k through registers into a double-buffered LDS.  Each byte of
+// an operand is loaded, shifted and stored by vector instructions: 581 us at 4096 x 4096 x 4096.
 template <int BLOCKB>
 __global__ __launch_bounds__(256) void e4m3_any_kernel(E4m3Args p)
 {
@@ -230,6 +231,14 @@ struct E4m3Cfg {
 // SHIFT: rows start at any byte.  A direct-to-LDS load takes whole dwords, so a row comes from the dword that holds its
 // first byte on, with the dword behind each slice beside it; fragments are shifted into place when they are read.  The last k
 // that do not fill a slice come through registers.
+//
+// Bound by the matrix cores and the vector instructions beside them: for a slice, a wave of the 128 x 128 tile has 32 matrix-core
+// ops (1024 cycles) and 221 vector instructions (128 conversions, 64 multiply-adds; some 970 cycles with two waves a SIMD).
+// 4096 x 4096 x 4096: 124 us (1.11 PFLOP/s, matrix cores busy 57% of the cycles; the fp16 product, which converts nothing, 113).
+// Two workgroups a CU fill each other's gaps: with four slots and one 157, 256 x 128 and 128 x 256 tiles with three 127.5.
+// 2048 x 4096 x 8192 with a scale for each row of B: 135 us, 64 products of two scales more a slice.  Shifted: 4096 x 4096 x 4001
+// 160 us (through registers 488), 1001 x 777 x 513 6.3 to 7.6 us (12.1), a chain of 5 slices, KG = 2 of them at a time.
+// Sums promoted in the next slice, beside its products: both sets of registers live, 64 moves a slice and spills.
 template <class Cfg, int BLOCKB>
 __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
 {
@@ -642,7 +651,9 @@ struct E4m3StreamCfg {
 // Few rows: the time is that of reading B once.  A workgroup takes 16 CB columns and up to
 // 16 RB rows; its waves take the slices of 128 k in turn, each through a ring of S
 // slots that only it loads and reads: no barrier until the end, S slices on their way per
-// wave.  The waves' results are added in wave order.  Needs what e4m3_dma_kernel needs.
+// wave.  The waves' results are added in wave order.  Needs what e4m3_dma_kernel needs.  16 x 4096 x 4096: 5.9 us with its launch;
+// 128 rows over 64 groups of 1024 x 2048: 20.4 us, 114 MB read at 5.6 TB/s (with 128 x 128 tiles 34); 16 x 4096 x 4001 8.8 us
+// (through registers 61).
 template <class Cfg, int BLOCKB>
 __global__ __launch_bounds__(Cfg::NT) void e4m3_stream_kernel(E4m3Args p)
 {

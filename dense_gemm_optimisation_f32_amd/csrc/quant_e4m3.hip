@@ -9,6 +9,11 @@
 // A power of two loses nothing against 448 / max|y|: the fraction bits are the same,
 // only the block's smallest values reach 2^-9 half a step earlier.  y / s is then exact in
 // fp32, so q is the nearest value of the quotient itself, with one rounding.
+//
+// Bound by memory: one pass, every value read once and written once.  What carries it is loads on their way, so values stay
+// in registers as they are stored until their scale is known (as fp32 from the start, with a third of the waves: 8192 x 4096
+// bf16 27.1 us).  Now 17.7 us there (5.7 TB/s; a large copy 4.7), 30.8 in fp32; 4096 x 8192 turned 18.1 in bf16, 31.6 in fp32;
+// 4 of 4096 x 4096 in blocks of 128 rows 33.0 in bf16, 60.4 in fp32; 8191 x 4001 19.6; 16 x 4096 3.8, of which a launch is 3.
 #include "e4m3_internal.h"
 #include "routed_internal.h"
 #include "stage16.h"
@@ -182,7 +187,7 @@ __device__ __forceinline__ float value(const Row8<T> &v, int e)
 }
 
 // Scales of single rows of X as it is stored: a wave takes 8 rows of 512 columns, 1 KB of a 16-bit row at a time, and 16
-// lanes a block.  Values stay as they are stored until their scale is known.
+// lanes a block (128 x 128 tiles, whose waves read 256 bytes of four rows: 27.3 us where this took 22.0).
 constexpr int kRowsR = 32, kRowsC = 512;
 template <int TYPE>
 __global__ __launch_bounds__(256) void rows_kernel(QuantArgs p)
@@ -224,7 +229,8 @@ __global__ __launch_bounds__(256) void rows_kernel(QuantArgs p)
 }
 
 // A workgroup takes a 128 x 128 tile of X as it is stored: thread t holds 8 columns (8 (t % 16) ..) of R consecutive rows (R (t /
-// 16) ..).  For scales of single rows of X^T (TRANS) or of 128 rows (SQUARE).
+// 16) ..).  For scales of single rows of X^T (TRANS) or of 128 rows (SQUARE).  8 rows of fp32 would take 172 registers: 4096 x
+// 8192 turned 33.9 us, against 31.8 with 4.
 template <class T>
 constexpr int kTileR = sizeof(T) == 4 ? 4 : 8;
 template <class T>

@@ -407,7 +407,10 @@ int gemm_grouped_e4m3_f32acc(int blockB, int groups, int R, int N, int K, float 
  * M > N is computed from the other side (A = X^T X), which is the same X.  |G|_F is summed in 64 bits; G = 0 gives 0,
  * and an infinity or NaN in G makes its member NaN.  X is kept in fp32, the products are of fp16 copies (see
  * orthogonalise.hip): the result is within 1e-3 of its norm, 4e-3 where G is of rank one, before it is rounded to bf16.
- * Singular values that pass 7 on their way, or coefficients beyond some hundreds, leave fp16's range (infinities, NaN).
+ * fp16's range has to hold s^2, s sqrt(max(M,N)) and |b| s^2 + |c| s^4 for every singular value s on its way (to 1 and a
+ * little above with the usual coefficients); what leaves it becomes infinite or NaN.
+ * The workspace (orthogonalise_workspace bytes, 16-byte aligned) holds all members; 0 and NULL where one workgroup holds a member
+ * (the smaller side up to 64 and the larger up to 1024, or up to 128 and 512).
  * M, N <= 65536; batch_count <= 65535; ceil(M / 64) * ceil(N / 64) * batch_count < 2^23.
  */
 int orthogonalise_f32(int M, int N, int steps, const float *coefficients, float alpha,

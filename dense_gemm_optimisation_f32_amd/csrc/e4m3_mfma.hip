@@ -237,7 +237,7 @@ struct E4m3Cfg {
 // 4096 x 4096 x 4096: 124 us (1.11 PFLOP/s, matrix cores busy 57% of the cycles; the fp16 product, which converts nothing, 113).
 // Two workgroups a CU fill each other's gaps: with four slots and one 157, 256 x 128 and 128 x 256 tiles with three 127.5.
 // 2048 x 4096 x 8192 with a scale for each row of B: 135 us, 64 products of two scales more a slice.  Shifted: 4096 x 4096 x 4001
-// 160 us (through registers 488), 1001 x 777 x 513 6.3 to 7.6 us (12.1), a chain of 5 slices, KG = 2 of them at a time.
+// 160 us (through registers 488), 1001 x 777 x 513 7.3 us (12.1), a chain of 5 slices, KG = 2 of them at a time.
 // Sums promoted in the next slice, beside its products: both sets of registers live, 64 moves a slice and spills.
 template <class Cfg, int BLOCKB>
 __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)

@@ -347,6 +347,7 @@ long long gemm_lora_workspace(int M, int N, int K, int rank);
  * NaN but no infinity) with a scale for each block of 128 k.  The number at (i, k) of a matrix
  * is its 8-bit value times S[(k / 128) * lds + i / block]: a scale belongs to 128 k of one row
  * (block 1) or of 128 rows (block 128), and scales lie with the blocks of k outermost.
+ * What a call writes (Q, S, C, O) overlaps none of its operands.
  */
 
 /*

@@ -136,3 +136,59 @@ def test_coefficients_are_read_at_the_call(monkeypatch):
         dg.orthogonalise_f32(4, 4, kept, 1.0, FAKE, 4, 0, FAKE, 4, 0, workspace=FAKE, stream=0)
         steps.mul_(2)
     assert seen == [[1.0, 2.0, 3.0], [2.0, 4.0, 6.0]]
+
+
+CALLS = {
+    "quant_e4m3_bf16": (2, 1, 4, 6, FAKE, 6, 24, FAKE, 6, 24, FAKE, 4, 4),                    # (each refused before any launch)
+    "gemm_e4m3_f32acc": (7, 4, 6, 5, 1.0, FAKE, 5, FAKE, 4, FAKE, 5, FAKE, 1, 0.0, FAKE, 6),
+    "gemm_grouped_e4m3_f32acc": (7, 2, 4, 6, 5, 1.0, FAKE, 4, 5, FAKE, 4, None, FAKE, 5, 30, FAKE, 1, 1, FAKE, 0.0, FAKE, 6),
+    "orthogonalise_f32": (4, 6, [], 1.0, FAKE, 6, 24, FAKE, 6, 24),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_binding_devices(monkeypatch, name):
+    """A call runs on the device of its stream, and is refused when an operand is on another."""
+    torch = pytest.importorskip("torch")
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *a):
+            current[0] = self.before
+
+    class Stream:
+        cuda_stream, device = 0, torch.device("cuda", 1)
+
+    dg._load_torch()
+    monkeypatch.setattr(dg, "_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    lib_fn = dg._function(name)
+
+    class Watch:
+        __name__ = name
+
+        def __call__(self, *a):
+            seen.append(current[0])
+            return lib_fn(*a)
+
+    monkeypatch.setattr(dg, "_function", lambda name: Watch())
+    kw = {"workspace": FAKE} if name.startswith("orthogonalise") else {}
+    with pytest.raises(dg.GemmError):
+        getattr(dg, name)(*CALLS[name], stream=Stream(), **kw)
+    assert seen == [1] and current == [0]
+
+    def on_device_0(x, name, dtype_name, need, packed=False):
+        if current[0] != 0:
+            raise dg._Elsewhere(0)
+        return x
+
+    monkeypatch.setattr(dg, "_strided", on_device_0)
+    with pytest.raises(ValueError, match="more than one device"):
+        getattr(dg, name)(*CALLS[name], stream=Stream(), **kw)
+    assert seen == [1] and current == [0]

@@ -489,6 +489,51 @@ def test_grouped_replayed_with_other_offsets():
         assert torch.all(C[sum(counts):] == 7.0)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1000003), (3, 2, 8000000), (2, 3, 8388613)])
+def test_long_sums(M, N, K):
+    """Sums over millions, in each kernel (K of 2^23 and more goes through registers), of numbers of either sign."""
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    A, B = (torch.randint(0, 256, (n, K), dtype=torch.uint8, device="cuda", generator=gen) for n in (M, N))
+    for X in (A, B):
+        X[(X & 0x7F) == 0x7F] = 0
+    kb = -(-K // 128)
+    SA, SB = (torch.rand(kb, n, device="cuda", generator=gen) + 0.5 for n in (M, N))
+    table = torch.from_numpy(CODES).cuda()
+    a, b = ((table[X.long()].view(-1, K) * SX.t().double().repeat_interleave(128, 1)[:, :K]) for X, SX in ((A, SA), (B, SB)))
+    C = torch.empty(M, N, device="cuda")
+    dg.gemm_e4m3_f32acc(1, M, N, K, 1.0, A.view(E4M3), K, SA, M, B.view(E4M3), K, SB, N, 0.0, C, N)
+    ref, bound = torch.empty(M, N, dtype=torch.float64), torch.empty(M, N, dtype=torch.float64)
+    for i in range(M):
+        for j in range(N):
+            t = a[i] * b[j]
+            ref[i, j], bound[i, j] = t.sum().item(), t.abs().sum().item()
+    check(C.cpu().numpy(), ref.numpy(), bound.numpy())
+
+
+def test_many_members_and_groups():
+    """More members than a grid's third dimension holds, and thousands of groups, most of them empty."""
+    n = 70001
+    X = torch.randn(n, 2, 5, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    for transpose in (0, 1):
+        M, K = (5, 2) if transpose else (2, 5)
+        Q, S = torch.empty(n, M, K, dtype=E4M3, device="cuda"), torch.empty(n, 1, M, device="cuda")
+        dg.quant_e4m3_f32(transpose, 1, M, K, X, 5, 10, Q, K, 10, S, M, M, n)
+        for i in (0, 1, 65535, 65536, n - 1):
+            y = to64(X[i])
+            codes, scales = quant_oracle(y.T if transpose else y, 1)
+            assert np.array_equal(codes_of(Q[i]), codes) and np.array_equal(S[i].cpu().numpy(), scales)
+    rng = rng_of("groups")
+    G, R, N, K = 5000, 40, 30, 200
+    A, SA, a, lda, ldsa = operand(rng, R, K, 1)
+    B, SB, b, ldb, ldsb = operand(rng, G * N, K, 1)
+    group = np.sort(rng.integers(0, G, R))
+    offsets = np.searchsorted(group, np.arange(G + 1)).astype(np.int32)
+    C = torch.empty(R, N, device="cuda")
+    dg.gemm_grouped_e4m3_f32acc(1, G, R, N, K, 1.0, A, R, lda, SA, ldsa, None, B, ldb, N * ldb, SB, G * N, N, torch.from_numpy(offsets).cuda(), 0.0, C, N)
+    members = b.reshape(G, N, K)[group]
+    check(C.cpu().numpy(), np.einsum("rk,rnk->rn", a, members), np.einsum("rk,rnk->rn", np.abs(a), np.abs(members)))
+
+
 def test_linear_layer_and_update():
     """A layer's training step in 8 bits: output, input gradient and weight gradient against the same formulas in 64 bits on the
     quantised numbers, then the weight's update from its gradient."""

@@ -263,6 +263,67 @@ __device__ __forceinline__ unsigned frag_offset_k(int first, int lane)
     return (unsigned)(k * R * 2 + 16 * ((n >> 3) ^ swz_k<R>(k)) + 2 * (n & 7));
 }
 
+// A member's arrays.
+struct Parts {
+    float *x, *da, *db;
+    _Float16 *a16, *b16, *x16_next;
+    uint16_t *O;
+};
+__device__ __forceinline__ Parts parts_of(const OrthoArgs &p, int z)
+{
+    return {of_member(p.x, p.ws_stride, z), of_member(p.da, p.ws_stride, z), of_member(p.db, p.ws_stride, z), of_member(p.a16, p.ws_stride, z),
+            of_member(p.b16, p.ws_stride, z), of_member(p.x16_next, p.ws_stride, z), p.O + z * p.strideO};
+}
+
+// Four values of row r from column c on of a step's product: what comes of them (v, for the mirror image or a turned result), and
+// their stores by rows.  xv, o, dr, dc: what stands there in X, in A's copy, and the diagonal's entries of the row and the columns.
+template <int KIND>
+__device__ __forceinline__ void finish(const OrthoArgs &p, const Parts &w, f32x4_t &v, int r, int c, const f32x4_t &xv, const half4 &o, float dr,
+                                       const f32x4_t &dc)
+{
+    half4 h;
+    if constexpr (KIND == kGram) {
+        const float back = 1.f / (p.x_scale * p.x_scale);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] *= back;
+            if (r == c + e) {
+                w.da[r] = v[e];
+                v[e] = 0.f;
+            }
+            h[e] = (_Float16)v[e];
+        }
+        *reinterpret_cast<half4 *>(w.a16 + (long long)r * p.m + c) = h;
+    } else if constexpr (KIND == kSquare) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float off = o[e];
+            if (r == c + e) {
+                w.db[r] = p.b * dr + p.c * (dr * dr + v[e]);
+                v[e] = 0.f;
+            } else {
+                v[e] = p.b * off + p.c * ((dr + dc[e]) * off + v[e]);
+            }
+            h[e] = (_Float16)v[e];
+        }
+        *reinterpret_cast<half4 *>(w.b16 + (long long)r * p.m + c) = h;
+    } else {
+        const float f = p.a + dr;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, xv[e], v[e]);
+        if (!p.last) {
+            *reinterpret_cast<f32x4_t *>(w.x + (long long)r * p.n + c) = v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = (_Float16)v[e];
+            *reinterpret_cast<half4 *>(w.x16_next + (long long)r * p.n + c) = h;
+        } else if (!p.tall && r < p.M) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < p.N) w.O[(long long)r * p.ldo + c + e] = bf16_bits(v[e] * (p.alpha / p.x_scale));
+        }
+    }
+}
+
 // The three products of a step, of fp16 copies, k in whole slices of 64:
 //   kGram    A = X X^T            P Q^T with P = Q = X
 //   kSquare  B = b A + c A A      P Q^T with P = Q = A - diag(A)
@@ -273,7 +334,7 @@ __device__ __forceinline__ unsigned frag_offset_k(int first, int lane)
 // 4096 x 4096, a step: A 80 us, B 83, X 126 (1.09 PFLOP/s, matrix cores busy 68% of the cycles).  With all CUs multiplying
 // the clock falls: a slice of a 256 x 256 tile takes 1.25 us on 136 CUs and 1.97 on 256, so leaving tiles out gains less than
 // their count.  1001 x 513: 24 products of 5 to 6.7 us, each a chain: 2 us between kernels, 0.8 until its loads are on their
-// way, 1.3 to 3.8 in the loop (16 KB a slice into each CU), 1.4 for the epilogue.
+// way, 1.3 to 3.8 in the loop (16 KB a slice into each CU), 1.4 for the epilogue; see wave_kernel.
 template <class Cfg, int KIND>
 __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
 {
@@ -326,8 +387,7 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
     // of the K loop, which small matrices leave after a few microseconds.
     constexpr int TN = Cfg::TN, EP = TN % 64 == 0 ? 64 : 32, LPR = EP / 4, RPI = 64 / LPR, NQ = 32 / RPI;   // (EP columns at a time)
     constexpr bool EARLY = FM == 1 && FN == 1;
-    float *x = of_member(p.x, p.ws_stride, z), *da = of_member(p.da, p.ws_stride, z), *db = of_member(p.db, p.ws_stride, z);
-    _Float16 *a16 = of_member(p.a16, p.ws_stride, z), *b16 = of_member(p.b16, p.ws_stride, z);
+    const Parts w = parts_of(p, z);
     const int er = lane / LPR, c0 = n0 + wn * TN + 4 * (lane % LPR);
     f32x4_t xs[NQ], dcs;
     half4 os[NQ];
@@ -337,14 +397,14 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
         for (int q = 0; q < NQ; ++q) {
             const int r = first + q * RPI + er;
             if constexpr (KIND == kSquare) {
-                os[q] = *reinterpret_cast<const half4 *>(a16 + (long long)r * p.m + c);
-                drs[q] = da[r];
+                os[q] = *reinterpret_cast<const half4 *>(w.a16 + (long long)r * p.m + c);
+                drs[q] = w.da[r];
             } else if constexpr (KIND == kApply) {
-                xs[q] = *reinterpret_cast<const f32x4_t *>(x + (long long)r * p.n + c);
-                drs[q] = db[r];
+                xs[q] = *reinterpret_cast<const f32x4_t *>(w.x + (long long)r * p.n + c);
+                drs[q] = w.db[r];
             }
         }
-        if constexpr (KIND == kSquare) dcs = *reinterpret_cast<const f32x4_t *>(da + c);
+        if constexpr (KIND == kSquare) dcs = *reinterpret_cast<const f32x4_t *>(w.da + c);
     };
     if constexpr (EARLY) read_epilogue(m0 + wm * Cfg::TM, c0);   // (64 x 64 tiles lie within the padded sizes)
     constexpr int NS = BK / 16;
@@ -448,8 +508,6 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
     const unsigned stage = lds0 + wave * 32 * EP * 4;
     wait_vmcnt<0>();   // (slices that a short K did not use)
     lds_barrier();
-    _Float16 *x16 = of_member(p.x16_next, p.ws_stride, z);
-    uint16_t *O = p.O + z * p.strideO;
     // what also goes out by columns: a symmetric tile's mirror image, a tall result
     const bool turned = KIND == kApply ? p.last && p.tall : tm != tn;
     // chunk of the staged row: 16 bytes of columns 4 k.. at chunk k ^ (row % LPR)
@@ -472,49 +530,7 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
             const int lrow = q * RPI + er, r = first + lrow;
             const unsigned at = chunk(lrow, lane % LPR);
             f32x4_t v = *(const lds_f32x4 *)(uintptr_t)at;
-            half4 h;
-            if constexpr (KIND == kGram) {
-                const float back = 1.f / (p.x_scale * p.x_scale);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[e] *= back;
-                    if (r == c + e) {
-                        da[r] = v[e];
-                        v[e] = 0.f;
-                    }
-                    h[e] = (_Float16)v[e];
-                }
-                *reinterpret_cast<half4 *>(a16 + (long long)r * p.m + c) = h;
-            } else if constexpr (KIND == kSquare) {
-                const half4 o = os[q];
-                const float dr = drs[q];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float off = o[e];
-                    if (r == c + e) {
-                        db[r] = p.b * dr + p.c * (dr * dr + v[e]);
-                        v[e] = 0.f;
-                    } else {
-                        v[e] = p.b * off + p.c * ((dr + dcs[e]) * off + v[e]);
-                    }
-                    h[e] = (_Float16)v[e];
-                }
-                *reinterpret_cast<half4 *>(b16 + (long long)r * p.m + c) = h;
-            } else {
-                const float f = p.a + drs[q];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, xs[q][e], v[e]);
-                if (!p.last) {
-                    *reinterpret_cast<f32x4_t *>(x + (long long)r * p.n + c) = v;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) h[e] = (_Float16)v[e];
-                    *reinterpret_cast<half4 *>(x16 + (long long)r * p.n + c) = h;
-                } else if (!p.tall && r < p.M) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (c + e < p.N) O[(long long)r * p.ldo + c + e] = bf16_bits(v[e] * (p.alpha / p.x_scale));
-                }
-            }
+            finish<KIND>(p, w, v, r, c, xs[q], os[q], drs[q], dcs);
             if (turned) *(lds_f32x4 *)(uintptr_t)at = v;
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -530,9 +546,9 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
             if (col < p.M)
 #pragma unroll
                 for (int e = 0; e < HALF; ++e)
-                    if (first + r0 + e < p.N) O[(long long)col * p.ldo + first + r0 + e] = bf16_bits(t[e] * (p.alpha / p.x_scale));
+                    if (first + r0 + e < p.N) w.O[(long long)col * p.ldo + first + r0 + e] = bf16_bits(t[e] * (p.alpha / p.x_scale));
         } else {
-            _Float16 *dst = (KIND == kGram ? a16 : b16) + (long long)col * p.m + first + r0;
+            _Float16 *dst = (KIND == kGram ? w.a16 : w.b16) + (long long)col * p.m + first + r0;
 #pragma unroll
             for (int e = 0; e < HALF; e += 8) {
                 half8 h;
@@ -542,6 +558,133 @@ __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
             }
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+}
+
+// Small products: a 32 x 32 tile of four waves, which take the slices of 64 k in turn, each through a ring of two slots
+// that only it loads and reads: no barrier until the waves' results are added, in wave order.  Against 64 x 64 tiles, four
+// times the CUs read half as much each, and a wave's first slices are all on their way at once: 129 x 129 67.5 -> 52 us, 1001 x 513
+// 105 -> 88, 300 x 2000 104 -> 81.5, 700 x 700 105 -> 86 (four slots: the same).
+template <int KIND>
+__global__ __launch_bounds__(256) void wave_kernel(OrthoArgs p)
+{
+    constexpr int T = 32, BK = 64, NW = 4, S = 2, SLICE = T * BK * 2, LOADS = 2 * SLICE / 1024;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[NW * S * 2 * SLICE];
+    const unsigned lds0 = (unsigned)(uintptr_t)lds;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int uwave = __builtin_amdgcn_readfirstlane(wave);
+    const int K = KIND == kGram ? p.n : p.m, nk = K / BK;
+    int z, tm, tn;
+    tile_of<KIND>(p.m / T, p.n / T, &z, &tm, &tn);
+    const int m0 = tm * T, n0 = tn * T;   // (padded sizes are multiples of 64: tiles are whole)
+    const _Float16 *P = of_member(KIND == kGram ? p.x16 : KIND == kSquare ? p.a16 : p.b16, p.ws_stride, z) + (long long)m0 * K;
+    const _Float16 *Q = of_member(KIND == kSquare ? p.a16 : p.x16, p.ws_stride, z);
+    constexpr bool K_OUT = KIND == kApply;   // Q is stored with k outermost: rows of 32 columns, 64 bytes, whose four banks of a
+                                             // transposed read differ as they lie
+    const char *Pb = reinterpret_cast<const char *>(P), *Qb = reinterpret_cast<const char *>(Q + (K_OUT ? (long long)n0 : (long long)n0 * K));
+    const long long stepQ = K_OUT ? (long long)BK * p.n * 2 : BK * 2;
+    unsigned offP[LOADS / 2], offQ[LOADS / 2];
+#pragma unroll
+    for (int i = 0; i < LOADS / 2; ++i) {
+        offP[i] = dma_offset<true, T, BK, false>(i, lane, K, T);
+        offQ[i] = K_OUT ? (unsigned)((16 * i + lane / 4) * (long long)p.n + 8 * (lane % 4)) * 2u : offP[i];
+    }
+    const unsigned ring = lds0 + uwave * S * 2 * SLICE;
+    auto issue = [&](int t, int slot) __attribute__((always_inline)) {
+        const unsigned at = __builtin_amdgcn_readfirstlane(ring + slot * 2 * SLICE);
+        const char *a = uniform(Pb + (long long)t * BK * 2), *b = uniform(Qb + t * stepQ);
+#pragma unroll
+        for (int i = 0; i < LOADS / 2; ++i) dma16(a, offP[i], at + 1024 * i);
+#pragma unroll
+        for (int i = 0; i < LOADS / 2; ++i) dma16(b, offQ[i], at + SLICE + 1024 * i);
+    };
+    // what the epilogue reads: four columns of a row a thread
+    const Parts w = parts_of(p, z);
+    const int er = tid / 8, ec = tid % 8, r = m0 + er, c = n0 + 4 * ec;
+    f32x4_t xv = {}, dc = {};
+    half4 o = {};
+    float dr = 0.f;
+    if constexpr (KIND == kSquare) {
+        o = *reinterpret_cast<const half4 *>(w.a16 + (long long)r * p.m + c);
+        dr = w.da[r];
+        dc = *reinterpret_cast<const f32x4_t *>(w.da + c);
+    } else if constexpr (KIND == kApply) {
+        xv = *reinterpret_cast<const f32x4_t *>(w.x + (long long)r * p.n + c);
+        dr = w.db[r];
+    }
+    unsigned fragP[BK / 16], fragQ[BK / 16];
+#pragma unroll
+    for (int s = 0; s < BK / 16; ++s) {
+        const int q = lane >> 4, l = lane & 15;
+        fragP[s] = frag_offset<true, T, BK>(0, lane, s);
+        fragQ[s] = SLICE + (K_OUT ? (unsigned)((16 * s + 8 * (q >> 1) + (l >> 2)) * T + 16 * (q & 1) + 4 * (l & 3)) * 2u : fragP[s]);
+    }
+    f32x16 acc = {};
+    const int ns = nk > uwave ? (nk - uwave + NW - 1) / NW : 0;   // this wave's slices: uwave, uwave + NW, ..
+    auto compute = [&](int slot, bool refill, int t) __attribute__((always_inline)) {
+        const unsigned at = ring + slot * 2 * SLICE;
+        half8 a[BK / 16], b[BK / 16];
+#pragma unroll
+        for (int s = 0; s < BK / 16; ++s) {
+            a[s] = *(const lds_half8 *)(uintptr_t)(at + fragP[s]);
+            if constexpr (K_OUT) {
+                const short4v both[2] = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(uintptr_t)(at + fragQ[s])),
+                                         __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(uintptr_t)(at + fragQ[s] + 4 * T * 2))};
+                b[s] = __builtin_bit_cast(half8, both);
+            } else {
+                b[s] = *(const lds_half8 *)(uintptr_t)(at + fragQ[s]);
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slot is read: it may be loaded again
+        if (refill) issue(t, slot);
+#pragma unroll
+        for (int s = 0; s < BK / 16; ++s) acc = mfma16<false>(b[s], a[s], acc);
+    };
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+        if (i < ns) issue(uwave + i * NW, i);
+    int i = 0, slot = 0;
+    for (; i + S < ns; ++i) {
+        wait_vmcnt<LOADS *(S - 1)>();
+        compute(slot, true, uwave + (i + S) * NW);
+        slot = slot + 1 == S ? 0 : slot + 1;
+    }
+    for (; i < ns; ++i) {   // the last slices: everything has been issued
+        if (i + 1 < ns)
+            wait_vmcnt<LOADS>();
+        else
+            wait_vmcnt<0>();
+        compute(slot, false, 0);
+        slot = slot + 1 == S ? 0 : slot + 1;
+    }
+    // the waves' results: 16 bytes of columns 4 k.. of row r at chunk k ^ (r % 8)
+    auto chunk = [&](int row, int k) { return lds0 + row * T * 4 + 16 * (k ^ (row & 7)); };
+    __syncthreads();   // every wave has left its ring
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+        *(lds_f32x4 *)(uintptr_t)(chunk(lane & 31, 2 * g + (lane >> 5)) + wave * T * T * 4) =
+            f32x4_t{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
+    __syncthreads();
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < NW; ++k) v += *(const lds_f32x4 *)(uintptr_t)(chunk(er, ec) + k * T * T * 4);
+    finish<KIND>(p, w, v, r, c, xv, o, dr, dc);
+    const bool turned = KIND == kApply ? p.last && p.tall : tm != tn;
+    if (!turned) return;
+    *(lds_f32x4 *)(uintptr_t)chunk(er, ec) = v;   // (read by this thread alone until now)
+    __syncthreads();
+    // by columns: column er, rows 4 ec ..
+    float t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] = *(const lds_float *)(uintptr_t)(chunk(4 * ec + e, er >> 2) + 4 * (er & 3));
+    const int col = n0 + er, row = m0 + 4 * ec;
+    if constexpr (KIND == kApply) {
+        if (col < p.M)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (row + e < p.N) w.O[(long long)col * p.ldo + row + e] = bf16_bits(t[e] * (p.alpha / p.x_scale));
+    } else {
+        *reinterpret_cast<half4 *>((KIND == kGram ? w.a16 : w.b16) + (long long)col * p.m + row) = half4{(_Float16)t[0], (_Float16)t[1], (_Float16)t[2], (_Float16)t[3]};
     }
 }
 
@@ -562,7 +705,14 @@ using Small = HgDmaCfg<64, 64, 4, 2, 2, 64>;
 template <int KIND>
 hipError_t launch_product(const OrthoArgs &a, int batch, hipStream_t stream)
 {
-    // Rounds of 256 workgroups, each with so long for a slice and for its start and end (us, measured on products of 512 x
+    // Up to 512 tiles of 32 x 32 (two share a CU), those: 960 x 2000 156.5 -> 149.7 us with 465 for A and B; beyond, 1024 x 1024
+    // with 528 126.8 -> 135.5, 300 x 2000 with 630 for X 82 -> 87.
+    const long long rows32 = a.m / 32, tiles32 = KIND == kApply ? rows32 * (a.n / 32) : rows32 * (rows32 + 1) / 2;
+    if (tiles32 * batch <= 512) {
+        hipLaunchKernelGGL(wave_kernel<KIND>, dim3((unsigned)tiles32, 1, batch), dim3(256), 0, stream, a);
+        return hipGetLastError();
+    }
+    // Otherwise rounds of 256 workgroups, each with so long for a slice and for its start and end (us, measured on products of 512 x
     // 512 to 4096 x 4096).  Two 64 x 64 tiles share a CU, so their rounds need not be whole.  (192 x 192 tiles fill a
     // round with one triangle of 4224 rows: 4096 x 4096 1593 -> 1480 us an update, 4096 x 8192 2819 -> 2522, against 256 x 256 on
     // 136 CUs.)

@@ -272,6 +272,24 @@ def test_largest_tiles(M, N):
     assert float(torch.linalg.norm(O[:M, :N].double() - ref) / torch.linalg.norm(ref)) <= tol
 
 
+@pytest.mark.parametrize("n,M,N", [(5, 500, 520), (5, 520, 500), (1, 1100, 1300), (3, 1020, 1030), (9, 260, 700), (1, 960, 990)])
+def test_numbers_of_tiles(n, M, N):
+    """Members whose products are some hundreds of tiles, of the sizes that the numbers choose."""
+    tol = tolerance(rng_of("tiles").standard_normal((500, 520)), FAST)
+    g = torch.randn(n, M, N, device="cuda", generator=torch.Generator(device="cuda").manual_seed(7))
+    O = torch.full((n, M, N + 3), 9.0, dtype=torch.bfloat16, device="cuda")
+    dg.orthogonalise_f32(M, N, FAST, 1.0, g, N, M * N, O, N + 3, M * (N + 3), n)
+    assert torch.all(O[:, :, N:] == 9)
+    for i in range(n):
+        x = (g[i] if M < N else g[i].t()).double()
+        x = x / torch.linalg.norm(x)
+        for a, b, c in FAST:
+            s = x @ x.t()
+            x = a * x + b * (s @ x) + c * (s @ (s @ x))
+        ref = x if M < N else x.t()
+        assert float(torch.linalg.norm(O[i, :, :N].double() - ref) / torch.linalg.norm(ref)) <= tol
+
+
 def test_expert_gradients():
     """The weight gradients of an expert layer, as the grouped product leaves them (all experts, one call), orthogonalised in one call."""
     G, R, D, F = 4, 300, 128, 192

@@ -104,15 +104,17 @@ struct Row8 {
 };
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
-// Eight values from column c on; columns at or past `cols` are zero.
+// Eight values of a row from column c on, or where that leaves the row from column cols - 8 on: into_place moves them then.
+// (Loads under a condition would wait for one another; here all rows' are on their way together.)
 template <class T>
 __device__ __forceinline__ Row8<T> load8(const T *row, int c, int cols)
 {
     Row8<T> v;
-    if (c + 8 <= cols) {
+    if (cols >= 8) {   // (uniform)
+        const T *from = row + (c < cols - 8 ? c : cols - 8);
 #pragma unroll
         for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
-            const u32x4 x = reinterpret_cast<const u32x4_h *>(row + c)[h];
+            const u32x4 x = reinterpret_cast<const u32x4_h *>(from)[h];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v.w[4 * h + e] = x[e];
         }
@@ -120,13 +122,38 @@ __device__ __forceinline__ Row8<T> load8(const T *row, int c, int cols)
     }
     typedef std::conditional_t<sizeof(T) == 4, unsigned, uint16_t> Bits;
     const Bits *b = reinterpret_cast<const Bits *>(row);
+    Bits x[8];
 #pragma unroll
-    for (int i = 0; i < 8 / Row8<T>::PER; ++i) {
-        v.w[i] = c + i * Row8<T>::PER < cols ? b[c + i * Row8<T>::PER] : 0u;
-        if constexpr (sizeof(T) == 2)
-            if (c + 2 * i + 1 < cols) v.w[i] |= (unsigned)b[c + 2 * i + 1] << 16;
-    }
+    for (int e = 0; e < 8; ++e) x[e] = b[c + e < cols ? c + e : cols - 1];
+#pragma unroll
+    for (int i = 0; i < 8 / Row8<T>::PER; ++i) v.w[i] = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v.w[e / Row8<T>::PER] |= (c + e < cols ? (unsigned)x[e] : 0u) << (sizeof(T) == 2 ? 16 * (e & 1) : 0);
     return v;
+}
+// The values `by` (1 and more) places down, zeros behind them.
+template <class T>
+__device__ __forceinline__ void move_down(Row8<T> &v, int by)
+{
+    constexpr int W = 8 / Row8<T>::PER;
+    const int words = by / Row8<T>::PER;
+#pragma unroll
+    for (int step = W; step >= 1; step /= 2)
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const unsigned from = i + step < W ? v.w[i + step] : 0u;
+            v.w[i] = (step == W ? words >= W : (words & step) != 0) ? from : v.w[i];
+        }
+    if constexpr (Row8<T>::PER == 2)
+#pragma unroll
+        for (int i = 0; i < W; ++i) v.w[i] = by & 1 ? __builtin_amdgcn_alignbit(i + 1 < W ? v.w[i + 1] : 0u, v.w[i], 16) : v.w[i];
+}
+template <class T, int R>
+__device__ __forceinline__ void into_place(Row8<T> (&v)[R], int c, int cols)
+{
+    if (cols >= 8 && c > cols - 8)
+#pragma unroll
+        for (int i = 0; i < R; ++i) move_down(v[i], c - (cols - 8));
 }
 // Magnitudes of a word's values, and the larger of each: 16-bit values are compared as they are, two at a time.
 template <class T>
@@ -206,6 +233,7 @@ __global__ __launch_bounds__(256) void rows_kernel(QuantArgs p)
         const int r = r0 + i < p.rows ? r0 + i : p.rows - 1;
         v[i] = load8<T>(X + r * p.ldx, c0, p.cols);
     }
+    into_place(v, c0, p.cols);
     unsigned mine = 0;   // lane i of each 16: the exponent bits of row i's scale
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -258,6 +286,7 @@ __global__ __launch_bounds__(kTileThreads<Stored<TYPE>>) void quant_kernel(Quant
         const int r = r0 + i < p.rows ? r0 + i : p.rows - 1;
         v[i] = load8<T>(X + r * p.ldx, c0, p.cols);
     }
+    into_place(v, c0, p.cols);
 
     // exponent bits of the scales: of column e, or of the tile (SQUARE)
     unsigned ex[8];

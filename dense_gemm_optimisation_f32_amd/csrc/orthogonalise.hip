@@ -147,8 +147,10 @@ __global__ __launch_bounds__(256) void norm_kernel(OrthoArgs p)
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (c + e < p.N) v[u][e] = g_at<BF>(p, z, r, c + e);
+                for (int e = 0; e < 4; ++e) {
+                    const float at = g_at<BF>(p, z, r, c + e < p.N ? c + e : p.N - 1);   // (loaded in any case: loads under a
+                    v[u][e] = c + e < p.N ? at : 0.f;                                    // condition would wait for one another)
+                }
             }
         }
 #pragma unroll
@@ -176,7 +178,8 @@ __global__ __launch_bounds__(256) void start_kernel(OrthoArgs p)
         // (consecutive threads along G's rows)
         const int e = tid + 256 * k, i = p.tall ? e % 64 : e / 64, j = p.tall ? e / 64 : e % 64;
         const int gr = p.tall ? c0 + j : r0 + i, gc = p.tall ? r0 + i : c0 + j;
-        g[k] = gr < p.M && gc < p.N ? g_at<BF>(p, z, gr, gc) : 0.f;
+        // (outside: a value inside, not counted below.  Loads under a condition would wait for one another.)
+        g[k] = g_at<BF>(p, z, gr < p.M ? gr : p.M - 1, gc < p.N ? gc : p.N - 1);
     }
     double sum = 0;
     for (int i = tid & 63; i < p.norm_blocks; i += 64) sum += norm[i];
@@ -186,7 +189,8 @@ __global__ __launch_bounds__(256) void start_kernel(OrthoArgs p)
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
         const int e = tid + 256 * k, i = p.tall ? e % 64 : e / 64, j = p.tall ? e / 64 : e % 64;
-        tile[i][j] = (float)(g[k] * f);
+        const int gr = p.tall ? c0 + j : r0 + i, gc = p.tall ? r0 + i : c0 + j;
+        tile[i][j] = gr < p.M && gc < p.N ? (float)(g[k] * f) : 0.f;
     }
     __syncthreads();
     float *x = of_member(p.x, p.ws_stride, z);

@@ -111,12 +111,12 @@ __global__ __launch_bounds__(Cfg::NT) void small_kernel(SmallArgs p)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) x[i][j][r] = g_at(at + (8 * (r >> 2) + (r & 3)) * dr);
             } else {
+                // (outside: the first entry, dropped.  Loads under a condition would wait for one another.)
                 const bool col_in = col_of(j) < n;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    x[i][j][r] = 0.f;
-                    if (col_in && row_of(i, r) < m) x[i][j][r] = g_at(at + (8 * (r >> 2) + (r & 3)) * dr);
-                }
+                for (int r = 0; r < 16; ++r) x[i][j][r] = g_at(col_in && row_of(i, r) < m ? at + (8 * (r >> 2) + (r & 3)) * dr : base);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) x[i][j][r] = col_in && row_of(i, r) < m ? x[i][j][r] : 0.f;
             }
             __builtin_amdgcn_sched_barrier(0);   // (addresses of one block at a time in registers)
         }

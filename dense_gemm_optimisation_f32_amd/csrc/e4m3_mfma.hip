@@ -57,22 +57,29 @@ __device__ __forceinline__ Half16 to_f16(u32x4 v)
     return __builtin_bit_cast(Half16, h);
 }
 
-// Sixteen bytes from p on, wherever p is; bytes at or past `valid` are zero.  The words
-// read all hold one of the valid bytes.
-__device__ __forceinline__ u32x4 load16_any(const uint8_t *p, int valid)
-{
-    if (valid <= 0) return u32x4{0u, 0u, 0u, 0u};
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    const unsigned skip = (unsigned)(at & 3);
-    const unsigned *w = reinterpret_cast<const unsigned *>(at & ~(uintptr_t)3);
-    const int last = ((int)skip + (valid < 16 ? valid : 16) - 1) >> 2;
+// The words of sixteen bytes from p on, wherever p is, of which `valid` are looked at: those read all hold one of these.  (With
+// none a place that is always there is read: loads under a condition would wait for one another.)
+struct Words16 {
     unsigned x[5];
+};
+__device__ __forceinline__ Words16 load_words(const uint8_t *p, int valid)
+{
+    const uintptr_t at = valid > 0 ? reinterpret_cast<uintptr_t>(p) : reinterpret_cast<uintptr_t>(&zero_chunk);
+    const unsigned *w = reinterpret_cast<const unsigned *>(at & ~(uintptr_t)3);
+    const int last = valid > 0 ? ((int)(at & 3) + (valid < 16 ? valid : 16) - 1) >> 2 : 0;
+    Words16 v;
 #pragma unroll
-    for (int i = 0; i < 5; ++i) x[i] = w[i < last ? i : last];
+    for (int i = 0; i < 5; ++i) v.x[i] = w[i < last ? i : last];
+    return v;
+}
+// The sixteen bytes; those at or past `valid` are zero.
+__device__ __forceinline__ u32x4 bytes_of(const Words16 &w, const uint8_t *p, int valid)
+{
+    const unsigned skip = (unsigned)(reinterpret_cast<uintptr_t>(p) & 3);
     u32x4 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        v[i] = __builtin_amdgcn_alignbit(x[i + 1], x[i], 8 * skip);
+        v[i] = __builtin_amdgcn_alignbit(w.x[i + 1], w.x[i], 8 * skip);
         const int left = valid - 4 * i;   // valid bytes of this word
         if (left < 4) v[i] = left <= 0 ? 0u : v[i] & (0xFFFFFFFFu >> (32 - 8 * left));
     }
@@ -122,19 +129,17 @@ __global__ __launch_bounds__(256) void e4m3_any_kernel(E4m3Args p)
             row[i] = n0 + r < N ? B + (long long)(n0 + r) * p.ldb : nullptr;
         }
     }
-    u32x4 v[4];
+    Words16 v[4];
+    auto valid = [&](int i, int k0) { return row[i] ? K - (k0 + 16 * ch) : 0; };
     auto load = [&](int k0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int k = k0 + 16 * ch;
-            v[i] = load16_any(row[i] + k, row[i] ? K - k : 0);
-        }
+        for (int i = 0; i < 4; ++i) v[i] = load_words(row[i] + (k0 + 16 * ch), valid(i, k0));
     };
-    auto store = [&](int buf) {
+    auto store = [&](int buf, int k0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = (tid >> 3) + 32 * i;   // (rows of B follow those of A)
-            lds[buf][r * 8 + (ch ^ swz_a<8>(r))] = v[i];
+            lds[buf][r * 8 + (ch ^ swz_a<8>(r))] = bytes_of(v[i], row[i] + (k0 + 16 * ch), valid(i, k0));
         }
     };
     const int lr = lane & 31, lk = lane >> 5, wm = wave >> 1, wn = wave & 1;
@@ -147,7 +152,7 @@ __global__ __launch_bounds__(256) void e4m3_any_kernel(E4m3Args p)
     if (slices > 0) load(0);
     for (int t = 0; t < slices; ++t) {
         const int buf = t & 1;
-        store(buf);
+        store(buf, t * BK);
         if (t + 1 < slices) load((t + 1) * BK);
         const float fa = sa[(long long)t * p.ldsa];
         const float *sb = SB + (long long)t * p.ldsb;
@@ -492,13 +497,20 @@ __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
             lds_barrier();
             if (kg == 0) {
                 constexpr int CHUNKS = (BM + BN) * 8 / (64 * Cfg::NW);
+                const int ch = lane % 8, k = looped * BK + 16 * ch;
+                auto row = [&](int i) { return i * 8 * Cfg::NW + wave * 8 + lane / 8; };   // (rows of B follow those of A)
+                const uint8_t *from[CHUNKS];
+                Words16 words[CHUNKS];
 #pragma unroll
                 for (int i = 0; i < CHUNKS; ++i) {
-                    const int id = i * 64 * Cfg::NW + (wave * 64 + lane), r = id / 8, ch = id % 8;   // (rows of B follow those of A)
-                    const int k = looped * BK + 16 * ch;
-                    const char *row = r < BM ? Ab + byteA(r) : Bb + byteB(r - BM);
-                    *(lds_u32x4 *)(uintptr_t)(lds0 + r * BK + 16 * (ch ^ swz_a<8>(r))) = load16_any(reinterpret_cast<const uint8_t *>(row) + k, K - k);
+                    const int r = row(i);
+                    from[i] = reinterpret_cast<const uint8_t *>(r < BM ? Ab + byteA(r) : Bb + byteB(r - BM)) + k;
                 }
+#pragma unroll
+                for (int i = 0; i < CHUNKS; ++i) words[i] = load_words(from[i], K - k);
+#pragma unroll
+                for (int i = 0; i < CHUNKS; ++i)
+                    *(lds_u32x4 *)(uintptr_t)(lds0 + row(i) * BK + 16 * (ch ^ swz_a<8>(row(i)))) = bytes_of(words[i], from[i], K - k);
                 // (the scales of the last slice a wave has read, replaced)
                 auto at = [&](int c) { return p.SB + (long long)group * p.strideSB + (long long)looped * p.ldsb + (c < N ? c : N - 1) / BLOCKB; };
 #pragma unroll
@@ -846,14 +858,23 @@ __global__ __launch_bounds__(Cfg::NT) void e4m3_stream_kernel(E4m3Args p)
     if constexpr (SHIFT) {
         if (looped < slices && uwave == looped % NW) {   // the last k, by the wave whose turn it is, into its first slot
             const unsigned lb = ring, la = lb + B_LOADS * 1024, ls = la + A_LOADS * 1024;
+            const int k = looped * BK + 16 * (lane % 8);
+            auto row = [&](int l) { return 8 * (l < B_LOADS ? l : l - B_LOADS) + lane / 8; };
+            const uint8_t *from[A_LOADS + B_LOADS];
+            Words16 words[A_LOADS + B_LOADS];
+            float s[S_LOADS];
 #pragma unroll
-            for (int l = 0; l < A_LOADS + B_LOADS; ++l) {
-                const int of = l < B_LOADS ? l : l - B_LOADS, r = 8 * of + lane / 8, k = looped * BK + 16 * (lane % 8);
-                const char *row = l < B_LOADS ? Bb + byteB(r) : Ab + byteA(r);
-                *(lds_u32x4 *)(uintptr_t)((l < B_LOADS ? lb : la) + r * BK + swizzled(of)) = load16_any(reinterpret_cast<const uint8_t *>(row) + k, K - k);
-            }
+            for (int l = 0; l < A_LOADS + B_LOADS; ++l)
+                from[l] = reinterpret_cast<const uint8_t *>(l < B_LOADS ? Bb + byteB(row(l)) : Ab + byteA(row(l))) + k;
 #pragma unroll
-            for (int l = 0; l < S_LOADS; ++l) *(lds_float *)(uintptr_t)(ls + 256 * l + 4 * lane) = scale[l][looped * scale_step[l]];
+            for (int l = 0; l < S_LOADS; ++l) s[l] = scale[l][looped * scale_step[l]];
+#pragma unroll
+            for (int l = 0; l < A_LOADS + B_LOADS; ++l) words[l] = load_words(from[l], K - k);
+#pragma unroll
+            for (int l = 0; l < A_LOADS + B_LOADS; ++l)
+                *(lds_u32x4 *)(uintptr_t)((l < B_LOADS ? lb : la) + row(l) * BK + swizzled(l < B_LOADS ? l : l - B_LOADS)) = bytes_of(words[l], from[l], K - k);
+#pragma unroll
+            for (int l = 0; l < S_LOADS; ++l) *(lds_float *)(uintptr_t)(ls + 256 * l + 4 * lane) = s[l];
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             compute(0, false, 0, std::true_type{});
         }

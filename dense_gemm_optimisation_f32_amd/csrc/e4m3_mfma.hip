@@ -40,6 +40,37 @@ struct E4m3Args {
     bool past_cache;          // C is larger than what the memory-side cache keeps of it
 };
 
+// The workgroup's rows and column of tiles; group -1: none.  Up to 64 groups are read once, for the count of the tiles and for
+// the workgroup's own.
+struct E4m3Tile {
+    int group, m0, m_end, tn;
+};
+__device__ __forceinline__ E4m3Tile tile_of(const E4m3Args &p, int bm)
+{
+    int one, tm, tn;
+    if (!p.offsets) {
+        tile_coords((int)blockIdx.x, 0, 1, p.tiles_m, p.tiles_n, &one, &tm, &tn);
+        return {0, tm * bm, p.R, tn};
+    }
+    if (p.groups <= 64) {
+        const int lane = threadIdx.x & 63;
+        int lo = 0, hi = 0;
+        if (lane < p.groups) group_rows(p.offsets, lane, p.R, &lo, &hi);
+        const int n = (hi - lo + bm - 1) / bm, s = wave_scan(n);
+        const int total = add_row_tiles(0, (unsigned)__builtin_amdgcn_readlane(s, 63), p.tiles_m);
+        if ((long long)blockIdx.x >= (long long)total * p.tiles_n) return {-1, 0, 0, 0};
+        tile_coords((int)blockIdx.x, 0, 1, total, p.tiles_n, &one, &tm, &tn);
+        const int at = __builtin_ctzll(__ballot(tm >= s - n && tm < s));   // (tm is below the total)
+        const int first = lo + (tm - (s - n)) * bm;
+        return {at, __builtin_amdgcn_readlane(first, at), __builtin_amdgcn_readlane(hi, at), tn};
+    }
+    const int total = count_row_tiles(p.offsets, p.groups, p.R, bm, p.tiles_m);
+    if ((long long)blockIdx.x >= (long long)total * p.tiles_n) return {-1, 0, 0, 0};
+    tile_coords((int)blockIdx.x, 0, 1, total, p.tiles_n, &one, &tm, &tn);
+    const RowTile rt = find_row_tile(p.offsets, p.groups, p.R, bm, tm);
+    return {rt.group, rt.first, rt.end, tn};
+}
+
 // Sixteen e4m3 values as fp16, exactly (NaN stays NaN), in order.
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 struct Half16 {
@@ -96,22 +127,10 @@ __global__ __launch_bounds__(256) void e4m3_any_kernel(E4m3Args p)
     constexpr int BM = 64, BN = 64, BK = 128;
     __shared__ __attribute__((aligned(16))) u32x4 lds[2][(BM + BN) * 8];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    int group = 0, m0, m_end, one, tm, tn;
-    if (p.offsets) {
-        const int total = count_row_tiles(p.offsets, p.groups, p.R, BM, p.tiles_m);
-        if ((long long)blockIdx.x >= (long long)total * p.tiles_n) return;
-        tile_coords((int)blockIdx.x, 0, 1, total, p.tiles_n, &one, &tm, &tn);
-        const RowTile rt = find_row_tile(p.offsets, p.groups, p.R, BM, tm);
-        if (rt.group < 0) return;
-        group = rt.group;
-        m0 = rt.first;
-        m_end = rt.end;
-    } else {
-        tile_coords((int)blockIdx.x, 0, 1, p.tiles_m, p.tiles_n, &one, &tm, &tn);
-        m0 = tm * BM;
-        m_end = p.R;
-    }
-    const int n0 = tn * BN, N = p.N, K = p.K;
+    const E4m3Tile tile = tile_of(p, BM);
+    if (tile.group < 0) return;
+    const int group = tile.group, m0 = tile.m0, m_end = tile.m_end;
+    const int n0 = tile.tn * BN, N = p.N, K = p.K;
     const uint8_t *B = p.B + (long long)group * p.strideB;
     const float *SB = p.SB + (long long)group * p.strideSB;
 
@@ -257,22 +276,10 @@ __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
     const int tid = threadIdx.x, lane = tid & 63, wave = (tid >> 6) % Cfg::NW;   // (of its group)
     const int uwave = __builtin_amdgcn_readfirstlane(wave), kg = __builtin_amdgcn_readfirstlane((tid >> 6) / Cfg::NW);
     const unsigned lds0 = (unsigned)(uintptr_t)lds + kg * Cfg::RING;
-    int group = 0, m0, m_end, one, tm, tn;
-    if (p.offsets) {
-        const int total = count_row_tiles(p.offsets, p.groups, p.R, BM, p.tiles_m);
-        if ((long long)blockIdx.x >= (long long)total * p.tiles_n) return;
-        tile_coords((int)blockIdx.x, 0, 1, total, p.tiles_n, &one, &tm, &tn);
-        const RowTile rt = find_row_tile(p.offsets, p.groups, p.R, BM, tm);
-        if (rt.group < 0) return;
-        group = rt.group;
-        m0 = rt.first;
-        m_end = rt.end;
-    } else {
-        tile_coords((int)blockIdx.x, 0, 1, p.tiles_m, p.tiles_n, &one, &tm, &tn);
-        m0 = tm * BM;
-        m_end = p.R;
-    }
-    const int n0 = tn * BN, N = p.N, K = p.K;
+    const E4m3Tile tile = tile_of(p, BM);
+    if (tile.group < 0) return;
+    const int group = tile.group, m0 = tile.m0, m_end = tile.m_end;
+    const int n0 = tile.tn * BN, N = p.N, K = p.K;
     const int limA = m_end - m0 < BM ? m_end - m0 : BM, limB = N - n0 < BN ? N - n0 : BN;
 
     // rows outside the tile's re-read valid ones; their results are not stored
@@ -676,22 +683,10 @@ __global__ __launch_bounds__(Cfg::NT) void e4m3_stream_kernel(E4m3Args p)
     const unsigned lds0 = (unsigned)(uintptr_t)lds;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const int uwave = __builtin_amdgcn_readfirstlane(wave);
-    int group = 0, m0, m_end, one, tm, tn;
-    if (p.offsets) {
-        const int total = count_row_tiles(p.offsets, p.groups, p.R, BM, p.tiles_m);
-        if ((long long)blockIdx.x >= (long long)total * p.tiles_n) return;
-        tile_coords((int)blockIdx.x, 0, 1, total, p.tiles_n, &one, &tm, &tn);
-        const RowTile rt = find_row_tile(p.offsets, p.groups, p.R, BM, tm);
-        if (rt.group < 0) return;
-        group = rt.group;
-        m0 = rt.first;
-        m_end = rt.end;
-    } else {
-        tile_coords((int)blockIdx.x, 0, 1, p.tiles_m, p.tiles_n, &one, &tm, &tn);
-        m0 = tm * BM;
-        m_end = p.R;
-    }
-    const int n0 = tn * BN, N = p.N, K = p.K;
+    const E4m3Tile tile = tile_of(p, BM);
+    if (tile.group < 0) return;
+    const int group = tile.group, m0 = tile.m0, m_end = tile.m_end;
+    const int n0 = tile.tn * BN, N = p.N, K = p.K;
     const int limA = m_end - m0 < BM ? m_end - m0 : BM, limB = N - n0 < BN ? N - n0 : BN;
     // (offsets count from this row; rows that A does not hold read it, and their products are dropped at the end)
     const int base = p.rows ? 0 : m0 < p.a_rows ? m0 : p.a_rows - 1;
@@ -727,6 +722,7 @@ __global__ __launch_bounds__(Cfg::NT) void e4m3_stream_kernel(E4m3Args p)
         if constexpr (SHIFT) behind[i] = r < BM ? Ab + ((byteA(r) + (BK - 1)) & ~3u) : Bb + ((byteB(c) + (BK - 1)) & ~3u);
     }
     const int slices = (K + BK - 1) / BK, looped = SHIFT ? K / BK : slices;   // (SHIFT: the whole ones)
+    const int my_row = m0 + (tid / (BN / 4) < limA ? tid / (BN / 4) : limA - 1), my_at = p.rows ? p.rows[my_row] : my_row;   // (of the epilogue)
     const unsigned ring = lds0 + uwave * S * Cfg::STAGE;
     auto issue = [&](int t, int slot) __attribute__((always_inline)) {
         const unsigned lb = __builtin_amdgcn_readfirstlane(ring + slot * Cfg::STAGE), la = lb + B_LOADS * 1024, ls = la + A_LOADS * 1024;
@@ -891,14 +887,14 @@ __global__ __launch_bounds__(Cfg::NT) void e4m3_stream_kernel(E4m3Args p)
             *(lds_f32x4 *)(uintptr_t)(lds0 + wave * BM * BN * 4 + r * BN * 4 + ((c ^ (r & (CH - 1))) * 16)) = acc[i2][j];
         }
     __syncthreads();
-    for (int e = tid; e < limA * CH; e += Cfg::NT) {
-        const int r = e / CH, c = e % CH, row = m0 + r;
+    static_assert(BM * CH <= Cfg::NT, "four columns of a row a thread");
+    if (tid < limA * CH) {
+        const int r = tid / CH, c = tid % CH, row = m0 + r;
         f32x4_t v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < NW; ++w)
             v += *(const lds_f32x4 *)(uintptr_t)(lds0 + w * BM * BN * 4 + r * BN * 4 + ((c ^ (r & (CH - 1))) * 16));
-        const int at = p.rows ? p.rows[row] : row;
-        if ((unsigned)at >= (unsigned)p.a_rows) v = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        if ((unsigned)my_at >= (unsigned)p.a_rows) v = f32x4_t{0.f, 0.f, 0.f, 0.f};
         if (p.beta != 0.f)
             store_row4<true, true>(p.C, p.ldc, row, n0 + 4 * c, v, p.alpha, p.beta, m_end, N);
         else

@@ -621,11 +621,12 @@ __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
             v[q] = *(const lds_f32x4 *)(uintptr_t)(stage + r * Cfg::TN * 4 + ((ec ^ (r & (LPR - 1))) * 16));
         }
         if (p.rows) {
+            int at[NQ];   // (loads under a condition would wait for one another)
 #pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-                const int row = first + q * RPI + er;
-                if (row < m_end && (unsigned)p.rows[row] >= (unsigned)p.a_rows) v[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            }
+            for (int q = 0; q < NQ; ++q) at[q] = p.rows[first + q * RPI + er < m_end ? first + q * RPI + er : m_end - 1];
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+                if ((unsigned)at[q] >= (unsigned)p.a_rows) v[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         } else if (m_end > p.a_rows) {
 #pragma unroll
             for (int q = 0; q < NQ; ++q)

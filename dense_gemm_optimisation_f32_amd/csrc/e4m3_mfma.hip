@@ -632,7 +632,13 @@ __global__ __launch_bounds__(Cfg::NT, 2) void e4m3_dma_kernel(E4m3Args p)
             for (int q = 0; q < NQ; ++q)
                 if (first + q * RPI + er >= p.a_rows) v[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
-        if (beta != 0.f) {
+        if (beta != 0.f && first + 32 <= m_end && n0 + BN <= N) {
+            f32x4_t c[NQ];   // (all of C that is read here on its way before the first is used)
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) c[q] = load_row4<false>(p.C, p.ldc, first + q * RPI + er, col, m_end, N);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) store_row4_v(p.C, p.ldc, first + q * RPI + er, col, fma_row4(v[q], c[q], alpha, beta));
+        } else if (beta != 0.f) {
 #pragma unroll
             for (int q = 0; q < NQ; ++q)
                 store_row4<true, true>(p.C, p.ldc, first + q * RPI + er, col, v[q], alpha, beta, m_end, N);

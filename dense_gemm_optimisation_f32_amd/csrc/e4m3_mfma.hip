@@ -258,7 +258,7 @@ struct E4m3Cfg {
 //
 // Bound by the matrix cores and the vector instructions beside them: for a slice, a wave of the 128 x 128 tile has 32 matrix-core
 // ops (1024 cycles) and 221 vector instructions (128 conversions, 64 multiply-adds; some 970 cycles with two waves a SIMD).
-// 4096 x 4096 x 4096: 124 us (1.11 PFLOP/s, matrix cores busy 57% of the cycles; the fp16 product, which converts nothing, 113).
+// 4096 x 4096 x 4096: 124 us (1.11 PFLOP/s, matrix cores busy 56% of the cycles; the fp16 product, which converts nothing, 113).
 // Two workgroups a CU fill each other's gaps: with four slots and one 157, 256 x 128 and 128 x 256 tiles with three 127.5.
 // 2048 x 4096 x 8192 with a scale for each row of B: 135 us, 64 products of two scales more a slice.  Shifted: 4096 x 4096 x 4001
 // 160 us (through registers 488), 1001 x 777 x 513 7.3 us (12.1), a chain of 5 slices, KG = 2 of them at a time.
@@ -678,7 +678,7 @@ struct E4m3StreamCfg {
 // 16 RB rows; its waves take the slices of 128 k in turn, each through a ring of S
 // slots that only it loads and reads: no barrier until the end, S slices on their way per
 // wave.  The waves' results are added in wave order.  Needs what e4m3_dma_kernel needs.  16 x 4096 x 4096: 5.9 us with its launch;
-// 128 rows over 64 groups of 1024 x 2048: 20.4 us, 114 MB read at 5.6 TB/s (with 128 x 128 tiles 34); 16 x 4096 x 4001 8.8 us
+// 128 rows over 64 groups of 1024 x 2048: 19.2 us, 114 MB read at 5.9 TB/s (with 128 x 128 tiles 34); 16 x 4096 x 4001 8.3 us
 // (through registers 61).
 template <class Cfg, int BLOCKB>
 __global__ __launch_bounds__(Cfg::NT) void e4m3_stream_kernel(E4m3Args p)

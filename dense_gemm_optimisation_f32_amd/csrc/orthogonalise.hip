@@ -164,7 +164,7 @@ __global__ __launch_bounds__(256) void norm_kernel(OrthoArgs p)
     if (tid == 0) of_member(p.norm, p.ws_stride, z)[blockIdx.x] = part[0] + part[1] + part[2] + part[3];
 }
 
-// X and its copy from G: a 64 x 64 tile of X per workgroup.  4096 x 4096: 41 us, 168 MB at 4.1 TB/s.
+// X and its copy from G: a 64 x 64 tile of X per workgroup.  4096 x 4096: 34 us, 168 MB at 4.9 TB/s.
 template <bool BF>
 __global__ __launch_bounds__(256) void start_kernel(OrthoArgs p)
 {
@@ -337,8 +337,8 @@ __device__ __forceinline__ void finish(const OrthoArgs &p, const Parts &w, f32x4
 //
 // 4096 x 4096, a step: A 80 us, B 83, X 126 (1.09 PFLOP/s, matrix cores busy 68% of the cycles).  With all CUs multiplying
 // the clock falls: a slice of a 256 x 256 tile takes 1.25 us on 136 CUs and 1.97 on 256, so leaving tiles out gains less than
-// their count.  1001 x 513: 24 products of 5 to 6.7 us, each a chain: 2 us between kernels, 0.8 until its loads are on their
-// way, 1.3 to 3.8 in the loop (16 KB a slice into each CU), 1.4 for the epilogue; see wave_kernel.
+// their count.  On 64 x 64 tiles a product of 1001 x 513 takes 5 to 6.7 us, a chain: 2 us to start and end, 0.8 until its loads
+// are on their way, 1.3 to 3.8 in the loop (16 KB a slice into each CU), 1.4 for the epilogue; wave_kernel takes 3.3 to 4.7.
 template <class Cfg, int KIND>
 __global__ __launch_bounds__(Cfg::NT) void product_kernel(OrthoArgs p)
 {

@@ -12,7 +12,7 @@
 //
 // Bound by memory: one pass, every value read once and written once.  What carries it is loads on their way, so values stay
 // in registers as they are stored until their scale is known (as fp32 from the start, with a third of the waves: 8192 x 4096
-// bf16 27.1 us).  Now 17.7 us there (5.7 TB/s; a large copy 4.7), 30.8 in fp32; 4096 x 8192 turned 18.1 in bf16, 31.6 in fp32;
+// bf16 27.1 us).  Now 17.7 us there (5.7 TB/s; a large copy 4.7), 30.6 in fp32; 4096 x 8192 turned 18.1 in bf16, 31.6 in fp32;
 // 4 of 4096 x 4096 in blocks of 128 rows 33.0 in bf16, 60.4 in fp32; 8191 x 4001 19.6; 16 x 4096 3.8, of which a launch is 3.
 #include "e4m3_internal.h"
 #include "routed_internal.h"

@@ -9,13 +9,17 @@
 //   * X itself stays in fp32.  A rounding of X is noise in all directions, and a direction that G
 //     hardly has grows by a factor a in every step (3.4445^5 = 485): rounded to 16 bits in
 //     each step, a G of low rank came out 4e-2 off.
-//   * The products' operands are fp16 copies.  There an error only multiplies X (from the left,
-//     through A), and stays as small as it is.  X's is scaled by a power of two into fp16's range.
-//   * The diagonals of A and of B = b A + c A A, which come to be much larger than the rest, are
-//     kept apart in fp32, and the fp16 copies hold zeros there: with A = D + O,
-//       A A = D D + D O + O D + O O,   B X = diag(B) X + (B - diag(B)) X.
-// Together the result is 4e-4 to 9e-4 off before it is rounded to bf16 (which costs 1.7e-3), 3e-3
-// for a G of rank one.
+//   * The products' operands are fp16 copies, each value off by at most 2^-11 of itself.  An error of
+//     A or B multiplies X from the left, and X's own copy X + E is multiplied by B, which is made of A:
+//     neither brings in directions (left singular vectors) that X does not have.  X's is scaled by a power of two into fp16's range.
+//   * The diagonal of A, which comes to be much larger than the rest, is kept apart in fp32, and the
+//     fp16 copy holds zeros there: with A = D + O,  A A = D D + D O + O D + O O.
+//   * The diagonal of B = b A + c A A is split: what goes with the rest of B in its fp16 copy, times X's copy, and what is left, in
+//     fp32, times fp32's X (diagonal_of_copy in orthogonalise_internal.h has the rule and its reason).
+// A model of this arithmetic against 64 bits, before the result is rounded to bf16 (which costs 1.7e-3): five steps of (3.4445, -4.775,
+// 2.0315) 1.4e-3 off for gradients of full rank, mostly below 3e-3 for those of low rank, of few or of unequal rows (4.4e-3 at most); eight of (1.875, -1.25,
+// 0.375), which bring back what is a little off, 2e-4 to 1e-3.  Where the copies' roundings all agree (entries of one size) the
+// first steps, which amplify a relative error up to 10 times, are up to 1.2e-2 off.
 #include "orthogonalise_internal.h"
 #include "routed_internal.h"
 #include "stage16.h"
@@ -303,8 +307,9 @@ __device__ __forceinline__ void finish(const OrthoArgs &p, const Parts &w, f32x4
         for (int e = 0; e < 4; ++e) {
             const float off = o[e];
             if (r == c + e) {
-                w.db[r] = p.b * dr + p.c * (dr * dr + v[e]);
-                v[e] = 0.f;
+                const float d = p.b * dr + p.c * (dr * dr + v[e]);
+                v[e] = (float)diagonal_of_copy(d, dr, v[e]);
+                w.db[r] = d - v[e];
             } else {
                 v[e] = p.b * off + p.c * ((dr + dc[e]) * off + v[e]);
             }
@@ -331,7 +336,7 @@ __device__ __forceinline__ void finish(const OrthoArgs &p, const Parts &w, f32x4
 // The three products of a step, of fp16 copies, k in whole slices of 64:
 //   kGram    A = X X^T            P Q^T with P = Q = X
 //   kSquare  B = b A + c A A      P Q^T with P = Q = A - diag(A)
-//   kApply   X <- a X + B X       P Q   with P = B - diag(B), Q = X
+//   kApply   X <- a X + B X       P Q   with P = B less the rest of its diagonal, Q = X
 // The ring, its loads and its K loop are those of the whole-matrix kernel (hgemm_mfma.hip).  The epilogue passes 32 rows of
 // a wave's tile at a time through LDS: by rows, and by columns for what is stored transposed.
 //

@@ -8,8 +8,8 @@
 //   the fp16 copy of X goes to LDS, column by column;                             barrier
 //   A = X X^T, a block on or above the diagonal a wave; without its diagonal it goes to LDS
 //   as fp16, the diagonal as fp32;                                                barrier
-//   B = b A + c A A likewise, into a place of its own;                            barrier
-//   X <- (a + diag(B)) X + (B - diag(B)) X.                                       barrier
+//   B = b A + c A A likewise, with a part of its diagonal, into a place of its own;  barrier
+//   X <- (a + the rest of the diagonal) X + B X.                                  barrier
 // Bound by the chain of a step (8.1 us at 128 x 512, 3.4 at 128 x 128, 1.7 at 64 x 64): four barriers, and between them LDS reads
 // that the few blocks of A and B leave to some of the waves (10 of 16 at 128 x 512).  32 of 128 x 512, five steps: 53 us;
 // 128 x 128 22; 64 x 1024 37.  X X^T's sum shared by the idle waves costs a barrier more: 59.9 us against 55.9.
@@ -180,18 +180,14 @@ __global__ __launch_bounds__(Cfg::NT) void small_kernel(SmallArgs p)
         asm volatile("" : "+v"(here));
         const int lr = here & 31, lk = here >> 5;
         auto col_of = [&](int j) { return 32 * (cb0 + j) + lr; };
-        // A block's values, fp16 and without the diagonal, to both of its places; its diagonal plus `more` to `d`.  B for
-        // an operand from registers has its columns in that operand's order.
-        auto put = [&](unsigned to, unsigned d, float more, int i, int j, const f32x16 &v, auto turned) __attribute__((always_inline)) {
+        // the place of a block's column in the order of an operand from registers
+        auto in_turn = [](int c) { return (c & 19) | ((c >> 2) & 1) << 3 | ((c >> 3) & 1) << 2; };
+        // A block's values, fp16 and without the diagonal, to both of its places.  B for an operand from registers has its
+        // columns in that operand's order.
+        auto put = [&](unsigned to, int i, int j, const f32x16 &v, auto turned) __attribute__((always_inline)) {
             constexpr bool TURNED = decltype(turned)::value;
-            const int col = TURNED ? (lr & 19) | ((lr >> 2) & 1) << 3 | ((lr >> 3) & 1) << 2 : lr;
+            const int col = TURNED ? in_turn(lr) : lr;
             const unsigned mine = to + (32 * j + lr) * AP + 2 * (32 * i + (TURNED ? 8 : 4) * lk), other = to + (32 * i + 4 * lk) * AP + 2 * (32 * j + col);
-            if (i == j) {   // (uniform)
-                float mid = 0.f;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) mid = r == diag ? v[r] : mid;
-                if (diag >= 0) *(lds_float *)(uintptr_t)(d + 4 * (32 * i + lr)) = mid + more;
-            }
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 half4 h = to_half(v, 4 * g);
@@ -249,7 +245,15 @@ __global__ __launch_bounds__(Cfg::NT) void small_kernel(SmallArgs p)
         if constexpr (!KEEP) __syncthreads();
 #pragma unroll
         for (int k = 0; k < MINE; ++k)
-            if (bi[k] < RF) put(ldsA, ldsDa, 0.f, bi[k], bj[k], blk[k], std::false_type{});
+            if (bi[k] < RF) {
+                if (bi[k] == bj[k]) {   // (uniform)
+                    float mid = 0.f;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) mid = r == diag ? blk[k][r] : mid;
+                    if (diag >= 0) *(lds_float *)(uintptr_t)(ldsDa + 4 * (32 * bi[k] + lr)) = mid;
+                }
+                put(ldsA, bi[k], bj[k], blk[k], std::false_type{});
+            }
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < MINE; ++k) {
@@ -262,6 +266,7 @@ __global__ __launch_bounds__(Cfg::NT) void small_kernel(SmallArgs p)
                 sq = mfma16<false>(*(const lds_half8 *)(uintptr_t)(at + 32 * i * AP), *(const lds_half8 *)(uintptr_t)(at + 32 * j * AP), sq);
             }
             const float dc = *(const lds_float *)(uintptr_t)(ldsDa + 4 * (32 * j + lr));
+            float others = 0.f;   // the diagonal's entry, in the lanes that have one
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const f32x4_t dr = *(const lds_f32x4 *)(uintptr_t)(ldsDa + 4 * (32 * i + 8 * g + 4 * lk));
@@ -272,12 +277,20 @@ __global__ __launch_bounds__(Cfg::NT) void small_kernel(SmallArgs p)
                     const float v = blk[k][r];
                     // A A = D D + D O + O D + O O
                     blk[k][r] = cb * v + cc * ((diagonal ? dc * v : (dr[e] + dc) * v) + sq[r]);
+                    others = diagonal ? sq[r] : others;
                 }
             }
-            put(ldsB, ldsDb, ca, i, j, blk[k], std::bool_constant<!KEEP>{});
+            put(ldsB, i, j, blk[k], std::bool_constant<!KEEP>{});
+            if (i == j && diag >= 0) {   // (B's place, after its zero)
+                const float b_ii = cb * dc + cc * (dc * dc + others);
+                const _Float16 mid = diagonal_of_copy(b_ii, dc, others);
+                const int at = KEEP ? lr : in_turn(lr);
+                *(lds_float *)(uintptr_t)(ldsDb + 4 * (32 * i + lr)) = ca + (b_ii - (float)mid);
+                *(lds_half *)(uintptr_t)(ldsB + (32 * i + lr) * AP + 2 * (32 * i + at)) = mid;
+            }
         }
         __syncthreads();
-        // X <- (a + diag(B)) X + (B - diag(B)) X
+        // X <- (a + the rest of B's diagonal) X + B X
         half8 xh[KEEP ? 1 : 2 * RF][CB];
         if constexpr (!KEEP)
             // the wave's columns: rows 16 s + 4 (lane / 32) .. + 3 and eight further

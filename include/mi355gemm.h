@@ -406,8 +406,11 @@ int gemm_grouped_e4m3_f32acc(int blockB, int groups, int R, int N, int K, float 
  *   coefficients: host memory, a, b, c of each of the `steps` (1 to 100) steps; read during the call.
  *   O           : bf16, M x N, ldo >= max(1,N), members strideO apart (at least a member).
  * M > N is computed from the other side (A = X^T X), which is the same X.  |G|_F is summed in 64 bits; G = 0 gives 0,
- * and an infinity or NaN in G makes its member NaN.  X is kept in fp32, the products are of fp16 copies (see
- * orthogonalise.hip): the result is within 1e-3 of its norm, 4e-3 where G is of rank one, before it is rounded to bf16.
+ * and an infinity or NaN in G makes its member NaN.  X is kept in fp32, the products are of fp16 copies, each value off by at most
+ * 2^-11 of itself (see orthogonalise.hip).  Before it is rounded to bf16 the result is off by at most 5e-3 of its norm with the usual
+ * five steps (3.4445, -4.7750, 2.0315), which amplify a rounding, and by at most 1e-3 with eight (1.875, -1.25, 0.375), which do not:
+ * whatever G's rank, however unequal or parallel its rows are.  Only where the copies' roundings agree (entries of one size, or no more
+ * than a few dozen that count) it can be 2e-2 and 2e-3.
  * fp16's range has to hold s^2, s sqrt(max(M,N)) and |b| s^2 + |c| s^4 for every singular value s on its way (to 1 and a
  * little above with the usual coefficients); what leaves it becomes infinite or NaN.
  * The workspace (orthogonalise_workspace bytes, 16-byte aligned) holds all members; 0 and NULL where one workgroup holds a member

@@ -380,6 +380,7 @@ int quant_e4m3_bf16(int transpose, int block, int M, int K, const uint16_t *X, i
  * Scales are any fp32 values; a product of two scales is formed first, and rounded as fp32 rounds it.
  * C is fp32, M x N.  A layer's output is x W^T with blocks of 128 of W; its input gradient is g W with W turned
  * (quant_e4m3_* with transpose, or the same values and scales transposed), its weight gradient g^T x with both turned and blockB = 1.
+ * The error is at most 1e-5 of |alpha| sum of |terms| + |beta C|, whatever K and the terms' signs are.
  * K <= 2^30; at most 2^23 - 1 tiles of 64 x 64 of C (2^35 elements).
  */
 int gemm_e4m3_f32acc(int blockB, int M, int N, int K, float alpha,

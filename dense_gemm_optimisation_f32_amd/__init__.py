@@ -610,13 +610,13 @@ def _members(one, batch, stride):
 
 
 def _here() -> int:
-    """The current device's index; -1 where there is none (the operands' own checks say so)."""
+    """The current device's index; -2, which no tensor has (host tensors have -1), where there is none: the operands' own checks say so."""
     if _device is None:
         _load_torch()
     try:
         return _device()
     except RuntimeError:
-        return -1
+        return -2
 
 
 def _at(device, x, name: str, dtype_name: str, need: int):

@@ -342,7 +342,7 @@ def _load_torch():
 
     _Tensor, _device, _raw_stream = torch.Tensor, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _DTYPES.update(float32=torch.float32, float16=torch.float16, bfloat16=torch.bfloat16, int32=torch.int32,
-                   float8_e4m3fn=torch.float8_e4m3fn)
+                   float8_e4m3fn=getattr(torch, "float8_e4m3fn", None))   # (None: a torch that has no such type)
     _torch = torch
     return torch
 

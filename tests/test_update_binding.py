@@ -51,3 +51,20 @@ def test_host_tensors_are_refused(monkeypatch, name, device):
     monkeypatch.setattr(dg, "_function", _Never)
     with pytest.raises(ValueError, match="CUDA"):
         CALLS[name]()
+
+
+def test_torch_without_8_bit_floats(monkeypatch):
+    """A torch that has no float8_e4m3fn: the operators of other types work as before, the 8-bit ones take raw addresses."""
+    monkeypatch.delattr(torch, "float8_e4m3fn")
+    for name in ("_torch", "_Tensor", "_device", "_raw_stream"):
+        monkeypatch.setattr(dg, name, None)
+    monkeypatch.setattr(dg, "_DTYPES", {})
+    x = torch.zeros(4, 4)
+    with pytest.raises(ValueError, match="CUDA"):        # (a host tensor; nothing about torch)
+        dg.moe_combine_f32(4, 1, 4, x, 4, 4, None, None, 0.0, x, 4, stream=0)
+    assert dg._DTYPES["float32"] is torch.float32
+    monkeypatch.setattr(dg, "_device", lambda: 0)
+    with pytest.raises(ValueError, match="CUDA|dtype"):
+        dg.quant_e4m3_f32(0, 1, 4, 4, 0x10000, 4, 16, x, 4, 16, 0x10000, 4, 4, stream=0)
+    with pytest.raises(dg.GemmError):                    # (block 7: the library's own refusal)
+        dg.quant_e4m3_f32(0, 7, 4, 4, 0x10000, 4, 16, 0x10000, 4, 16, 0x10000, 4, 4, stream=0)

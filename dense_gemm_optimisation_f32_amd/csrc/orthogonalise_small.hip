@@ -13,8 +13,8 @@
 // Bound by the chain of a step (8.1 us at 128 x 512, 3.4 at 128 x 128, 1.7 at 64 x 64): four barriers, and between them LDS reads
 // that the few blocks of A and B leave to some of the waves (10 of 16 at 128 x 512).  32 of 128 x 512, five steps: 53 us;
 // 128 x 128 22; 64 x 1024 37.  X X^T's sum shared by the idle waves costs a barrier more: 59.9 us against 55.9.
-// X's copy is the right operand of the last product too.  Where LDS does not hold it beside A and B (128 x 512, 64 x
-// 1024), they take its place, a wave owns all rows of its columns, and its own registers are that
+// X's copy is the right operand of the last product too.  Where LDS does not hold it beside A and B (more than 64 x 1024 or
+// 96 x 512), they take its place, a wave owns all rows of its columns, and its own registers are that
 // operand: eight rows of a lane's column are what a matrix-core op takes, in an order of rows that B's are
 // then read in too.
 #include "orthogonalise_internal.h"
@@ -58,6 +58,7 @@ struct SmallCfg {
     static constexpr int LDS = BODY + SMALL;
     static constexpr int BLOCKS = RF * (RF + 1) / 2, MINE = (BLOCKS + NW - 1) / NW;
     static_assert(LDS <= 160 * 1024 && (KEEP || WR == 1), "LDS");
+    static_assert(KEEP == (M < 128 || N < 512), "X's copy gives way to A and B at 128 x 512 alone");
 };
 
 // Four registers as fp16, two a conversion.

@@ -88,6 +88,43 @@ def test_groups(counts, N, K):
     assert float(((C.double() - ref) / ref).abs().max()) <= TOL
 
 
+@pytest.mark.parametrize("K", [65536, 65541, 98304 + 200])
+@pytest.mark.parametrize("beta", [0.0, 0.5])
+def test_groups_in_pieces(K, beta):
+    """128 x 128 tiles, whose K goes in pieces that add to C: beta counts once, rows without a group stay as they were, rows that A does
+    not hold are zero, and a captured call gives the same when it is replayed."""
+    G, R, N, T = 2, 2100, 2048, 50
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    A, SA, a = same(T, K, T, 1.0, 1.1, gen)
+    B, SB, b = same(G * N, K, G * N, 1.0, 1.3, gen)
+    rows = torch.randint(0, T, (R,), device="cuda", generator=gen, dtype=torch.int32)
+    rows[5], rows[1200] = T, -1
+    offsets = torch.tensor([0, 1100, 2000], dtype=torch.int32, device="cuda")
+    old = torch.rand(R, N, device="cuda", generator=gen) * K if beta else torch.full((R, N), float("nan"), device="cuda")
+    C = old.clone()
+
+    def call():
+        dg.gemm_grouped_e4m3_f32acc(1, G, R, N, K, 1.0, A, T, K, SA, T, rows, B, K, N * K, SB, G * N, N, offsets, beta, C, N)
+
+    call()
+    group = torch.cat([torch.zeros(1100, dtype=torch.long), torch.ones(900, dtype=torch.long)]).cuda()
+    held = ((rows >= 0) & (rows < T))[:2000, None]
+    ref = torch.where(held, K * a[rows.long().clamp(0, T - 1)][:2000, None] * b.view(G, N)[group], 0)
+    if beta:
+        ref = ref + beta * old[:2000].double()
+    assert torch.all((C[:2000].double() - ref).abs() <= TOL * ref)
+    assert torch.equal(C[2000:].view(torch.int32), old[2000:].view(torch.int32))
+    first = C.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(3):
+        C.copy_(old)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(C.view(torch.int32), first.view(torch.int32))
+
+
 @pytest.mark.parametrize("M,N,K", [(4, 5, 1 << 20), (64, 64, 262144), (512, 512, 262144), (2048, 2048, 65536), (2, 2, 8400000)])
 def test_infinite_scales(M, N, K):
     """An infinite scale makes its row infinite, whatever stood in the sum before it; two of either sign NaN; other rows are not touched."""

@@ -733,7 +733,7 @@ struct E4m3StreamCfg {
 // 16 RB rows; its waves take the slices of 128 k in turn, each through a ring of S
 // slots that only it loads and reads: no barrier until the end, S slices on their way per
 // wave.  The waves' results are added in wave order.  Needs what e4m3_dma_kernel needs.  16 x 4096 x 4096: 5.9 us with its launch;
-// 128 rows over 64 groups of 1024 x 2048: 19.2 us, 114 MB read at 5.9 TB/s (with 128 x 128 tiles 34); 16 x 4096 x 4001 8.3 us
+// 128 rows over 64 groups of 1024 x 2048: 19.7 us, 114 MB read at 5.8 TB/s (with 128 x 128 tiles 34); 16 x 4096 x 4001 8.3 us
 // (through registers 61).
 template <class Cfg, int BLOCKB>
 __global__ __launch_bounds__(Cfg::NT) void e4m3_stream_kernel(E4m3Args p)
@@ -1017,8 +1017,6 @@ bool aligned(const E4m3Problem &q)
 template <class Cfg>
 hipError_t launch_dma(const E4m3Problem &q, hipStream_t stream)
 {
-    if constexpr (!Cfg::LONG)
-        if (chain_of(q.K, Cfg::KG) > kChain) return launch_dma<typename Cfg::Long>(q, stream);
     if constexpr (!Cfg::SHIFT)
         if (!aligned(q)) return launch_dma<typename Cfg::Shifted>(q, stream);
     E4m3Args a = arguments(q);
@@ -1080,13 +1078,19 @@ using Stream32 = E4m3StreamCfg<2, 2, 4, 2>;
 using Stream16 = E4m3StreamCfg<1, 2, 4, 2>;
 constexpr TileTime kTime128 = {1.15, 2}, kTime64x128 = {0.63, 4}, kTime64 = {0.42, 1}, kTime32 = {0.22, 1};
 
+template <class Cfg>
+hipError_t launch_any_k(const E4m3Problem &q, hipStream_t stream)
+{
+    return chain_of(q.K, Cfg::KG) > kChain ? launch_dma<typename Cfg::Long>(q, stream) : launch_dma<Cfg>(q, stream);
+}
+
 // 128 x 128 tiles have no registers left for sums of twice 32 bits, so a longer K goes in pieces of kChain slices, each adding to C:
 // 4096 x 4096 x 65536 2.10 ms in two, 2.13 in one (with such sums in eight waves, half a tile each and one workgroup a CU, 2.46).  At most 16,
 // whose roundings in C then stay small beside those of a piece.
 hipError_t launch_tile128(E4m3Problem q, hipStream_t stream)
 {
     constexpr int PIECE = 128 * kChain;
-    if (q.K > 16 * PIECE) return launch_dma<Tile64x128>(q, stream);
+    if (q.K > 16 * PIECE) return launch_any_k<Tile64x128>(q, stream);
     const int K = q.K;
     for (int k0 = 0; k0 < K; k0 += PIECE) {
         q.K = K - k0 < PIECE ? K - k0 : PIECE;
@@ -1103,7 +1107,7 @@ hipError_t launch_tile128(E4m3Problem q, hipStream_t stream)
 hipError_t launch_tiles(const E4m3Problem &q, hipStream_t stream)
 {
     const double rows = (double)q.R / q.groups, slices = (q.K + 127) / 128;
-    // Up to 16 rows a group: streamed (64 groups, 128 rows, 1024 x 2048: 25.8 us, against 34 with 128x128 tiles; 512
+    // Up to 16 rows a group: streamed (64 groups, 128 rows, 1024 x 2048: 19.7 us, against 34 with 128x128 tiles; 512
     // rows 31.9 against 34.3 with the best tile; a plain 16 x 4096 x 4096 5.8 against 17).
     if (rows <= 16 && holds(q, Stream16::BM, Stream16::BN, Stream16::NT)) return launch_stream<Stream16>(q, stream);
     // Otherwise the tile whose rounds of 256 workgroups take the least time.  Groups part-fill half of their tiles,
@@ -1120,8 +1124,8 @@ hipError_t launch_tiles(const E4m3Problem &q, hipStream_t stream)
     // 7.4 us against 13, 512 x 512 x 4096 7.2 against 14; 64 groups of 47 rows 64 against 38)
     const double c32 = q.offsets ? 1e300 : time(32, 32, Stream32::NT, 512, kTime32);
     if (c32 < c64 && c32 < c64x128 && c32 < c128) return launch_stream<Stream32>(q, stream);
-    if (c64 <= c64x128 && c64 <= c128) return launch_dma<Tile64>(q, stream);
-    if (c64x128 < c128) return launch_dma<Tile64x128>(q, stream);
+    if (c64 <= c64x128 && c64 <= c128) return launch_any_k<Tile64>(q, stream);
+    if (c64x128 < c128) return launch_any_k<Tile64x128>(q, stream);
     return launch_tile128(q, stream);
 }
 

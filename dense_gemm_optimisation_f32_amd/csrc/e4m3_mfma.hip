@@ -1078,6 +1078,7 @@ using Stream32 = E4m3StreamCfg<2, 2, 4, 2>;
 using Stream16 = E4m3StreamCfg<1, 2, 4, 2>;
 constexpr TileTime kTime128 = {1.15, 2}, kTime64x128 = {0.63, 4}, kTime64 = {0.42, 1}, kTime32 = {0.22, 1};
 
+// Sums of more than kChain slices by the tile's long form: 1024 x 2048 x 131072 663 -> 686 us, 512 x 512 x 262144 263 -> 281.
 template <class Cfg>
 hipError_t launch_any_k(const E4m3Problem &q, hipStream_t stream)
 {
@@ -1085,8 +1086,8 @@ hipError_t launch_any_k(const E4m3Problem &q, hipStream_t stream)
 }
 
 // 128 x 128 tiles have no registers left for sums of twice 32 bits, so a longer K goes in pieces of kChain slices, each adding to C:
-// 4096 x 4096 x 65536 2.10 ms in two, 2.13 in one (with such sums in eight waves, half a tile each and one workgroup a CU, 2.46).  At most 16,
-// whose roundings in C then stay small beside those of a piece.
+// 4096 x 4096 x 65536 2.10 ms in two, 2.13 in one (with such sums in eight waves, half a tile each and one workgroup a CU, 2.46).  At
+// most 16, whose roundings in C then stay small beside those of a piece.
 hipError_t launch_tile128(E4m3Problem q, hipStream_t stream)
 {
     constexpr int PIECE = 128 * kChain;

@@ -17,8 +17,8 @@
 //   * The diagonal of B = b A + c A A is split: what goes with the rest of B in its fp16 copy, times X's copy, and what is left, in
 //     fp32, times fp32's X (diagonal_of_copy in orthogonalise_internal.h has the rule and its reason).
 // A model of this arithmetic against 64 bits, before the result is rounded to bf16 (which costs 1.7e-3): five steps of (3.4445, -4.775,
-// 2.0315) 1.4e-3 off for gradients of full rank, mostly below 3e-3 for those of low rank, of few or of unequal rows (4.4e-3 at most); eight of (1.875, -1.25,
-// 0.375), which bring back what is a little off, 2e-4 to 1e-3.  Where the copies' roundings all agree (entries of one size) the
+// 2.0315) 1.4e-3 off for gradients of full rank, mostly below 3e-3 for those of low rank, of few or of unequal rows (4.4e-3 at most);
+// eight of (1.875, -1.25, 0.375), which bring back what is a little off, 2e-4 to 1e-3.  Where the copies' roundings all agree (entries of one size) the
 // first steps, which amplify a relative error up to 10 times, are up to 1.2e-2 off.
 #include "orthogonalise_internal.h"
 #include "routed_internal.h"

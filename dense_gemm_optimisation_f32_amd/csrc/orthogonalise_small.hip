@@ -11,8 +11,8 @@
 //   B = b A + c A A likewise, with a part of its diagonal, into a place of its own;  barrier
 //   X <- (a + the rest of the diagonal) X + B X.                                  barrier
 // Bound by the chain of a step (8.5 us at 128 x 512, 3.4 at 128 x 128, 1.7 at 64 x 64): four barriers, and between them LDS reads
-// that the few blocks of A and B leave to some of the waves (10 of 16 at 128 x 512).  32 of 128 x 512, five steps: 55 us (53 with B's diagonal kept out of its copy);
-// 128 x 128 22; 64 x 1024 37.  X X^T's sum shared by the idle waves costs a barrier more: 59.9 us against 55.9.
+// that the few blocks of A and B leave to some of the waves (10 of 16 at 128 x 512).  32 of 128 x 512, five steps: 55 us (53 with
+// B's diagonal kept out of its copy); 128 x 128 22; 64 x 1024 37.  X X^T's sum shared by the idle waves costs a barrier more: 59.9 us against 55.9.
 // X's copy is the right operand of the last product too.  Where LDS does not hold it beside A and B (more than 64 x 1024 or
 // 96 x 512), they take its place, a wave owns all rows of its columns, and its own registers are that
 // operand: eight rows of a lane's column are what a matrix-core op takes, in an order of rows that B's are
